@@ -92,7 +92,8 @@ enum {
   SAGE_ERR_DEVICE_TIMEOUT = -12,/* a kernel gave up waiting on an internal barrier (see sage_device_error) */
   SAGE_ERR_ARG = -13,           /* another invalid argument (e.g. non-finite or non-positive sm_scale) */
   SAGE_ERR_TOO_LARGE = -14,     /* sizes exceed the library's index limits */
-  SAGE_ERR_DEVICE_SMEM = -15    /* a kernel's dynamic shared memory was not 1024-byte aligned; it did no work */
+  SAGE_ERR_DEVICE_SMEM = -15,   /* a kernel's dynamic shared memory was not 1024-byte aligned; it did no work */
+  SAGE_ERR_DEVICE_PAGE = -16    /* a page table, page list or length named tokens outside the cache */
 };
 
 /* dtype codes for sage_sageattn */
@@ -375,14 +376,132 @@ SAGE_API int sage_sageattn_host(const void* q_host, const void* k_host, const vo
                                 float sm_scale, int smooth_k, void* out_host, int n_groups, void* workspace_dev,
                                 size_t workspace_bytes, void* cuda_stream);
 
+/* ------------------------------------------------- 8-bit paged K/V cache -- */
+
+/* A cache of keys and values in 8 bits for sequences that grow (answering
+ * token by token, prompts taken in chunks) or are attended to by queries of
+ * another length (an encoder's states). It has num_pages pages of page_size
+ * tokens (a multiple of 32, at most 4096) of H key/value heads; each 32
+ * consecutive tokens of a head (a block) have one fp32 scale for their keys
+ * and one for their values: value = code * scale, codes in [-127, 127].
+ * All pointers are device pointers, 16-byte aligned, arrays contiguous,
+ * n = page_size / 32, D = 128 or 64:
+ *   k_codes : int8  [num_pages][H][n][D/64][32 tokens][64 channels]
+ *   v_codes : int8  [num_pages][H][n][D channels][32 positions]; token
+ *             8j + 2t + e of the block (j, t < 4, e < 2) is at position
+ *             8t + 2j + e
+ *   k_scale, v_scale : float [num_pages][H][n]
+ * A page table names each sequence's pages in order, so token i of sequence b
+ * lies in page table[b][i / page_size] at i % page_size. Pages may be shared
+ * by sequences that only read them.
+ * At most 2^20 pages (TOO_LARGE). */
+typedef struct sage_cache {
+  int8_t* k_codes_dev;
+  int8_t* v_codes_dev;
+  float* k_scale_dev;
+  float* v_scale_dev;
+  int64_t num_pages, page_size, H, D;
+} sage_cache;
+
+/* Page table of B sequences: int32 rows of max_pages entries, row_stride
+ * elements apart. Entries past a sequence's length are not read.
+ *
+ * What is in device memory (table entries, lengths, starts, counts, page
+ * lists) cannot be checked before the call returns. The kernels check it
+ * before they use it: a length or count that is negative or reaches past the
+ * table (or past T) is cut to what is there, a page number outside the cache
+ * is taken as a page without tokens, and the device error word is set
+ * (sage_device_error then reports SAGE_ERR_DEVICE_PAGE). */
+typedef struct sage_page_table {
+  const int32_t* table_dev;
+  int64_t row_stride;
+  int64_t max_pages;
+} sage_page_table;
+
+/* Bytes of one cache, each array starting on a 256-byte boundary in the order
+ * of sage_cache's fields. With base_dev (256-byte aligned, at least *bytes
+ * long), *cache receives the pointers carved from it and the sizes.
+ * Errors: SHAPE (also a page_size that is no positive multiple of 32),
+ * HEAD_DIM, TOO_LARGE, NULLPTR, ALIGN. */
+SAGE_API int sage_cache_size(int64_t num_pages, int64_t page_size, int64_t H, int64_t D, size_t* bytes,
+                             void* base_dev, sage_cache* cache);
+
+/* Writes new tokens into the cache: tokens 0 .. counts[b] - 1 of k and v
+ * (BF16 (B, T, H, D)) become tokens starts[b] .. starts[b] + counts[b] - 1 of
+ * sequence b. starts, counts: int32 [B]; counts NULL: T tokens each. Padding
+ * tokens (counts[b] and up) are not read.
+ * Per block and head, with a = max |x| over the new tokens in it and s the
+ * block's scale where older tokens of the sequence (before starts[b]) lie in
+ * it, else 0: the new scale is max(s, a / 127), new codes are
+ * rint(x / scale), and where the scale grew, older codes c become
+ * rint(c * (s / scale)); fp32, correctly rounded. A block whose new tokens
+ * hold an infinity or NaN gets the scale NaN, and every row that attends to it
+ * becomes NaN. Tokens behind the last new one in its block are lost (a
+ * sequence may be cut back and written on). The pages written must belong to
+ * one sequence of the call only: copy a shared page first
+ * (sage_cache_copy_pages).
+ * Softmax does not change when one vector is taken off all keys of a
+ * sequence, so a caller who knows a key mean per channel early may subtract
+ * it before the call, for finer codes.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, TOO_LARGE, ARCH, CUDA; on the
+ * device DEVICE_PAGE. */
+SAGE_API int sage_cache_append(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
+                               const int32_t* counts_dev, const sage_bf16_tensor* k, const sage_bf16_tensor* v,
+                               int64_t B, int64_t T, void* cuda_stream);
+
+/* Reads tokens starts[b] .. starts[b] + counts[b] - 1 of each sequence back as
+ * BF16(code * scale) into (B, T, H, D) outputs with element strides (b, s, h)
+ * and channel stride 1; rows counts[b] and up are left as they were. counts
+ * NULL: T tokens each. Errors: as sage_cache_append. */
+SAGE_API int sage_cache_read(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
+                             const int32_t* counts_dev, int64_t B, int64_t T, void* k_dev, int64_t kb, int64_t ks,
+                             int64_t kh, void* v_dev, int64_t vb, int64_t vs, int64_t vh, void* cuda_stream);
+
+/* Copies page src[i] to page dst[i] (codes and scales of all heads) for
+ * i < n; src, dst: int32 [n] in device memory. An entry with dst < 0 or
+ * dst = src stands for nothing. No page may be named twice as dst, nor both
+ * as dst and as src of another entry; src may repeat. Lists that break this,
+ * or name a page outside the cache, copy nothing and set the device error
+ * word (DEVICE_PAGE). At most 2^20 entries.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, TOO_LARGE, ARCH, CUDA. */
+SAGE_API int sage_cache_copy_pages(const sage_cache* cache, const int32_t* src_dev, const int32_t* dst_dev,
+                                   int64_t n, void* cuda_stream);
+
+/* Workspace bytes of sage_cache_attention for these sizes (they do not depend
+ * on the lengths). Errors: NULLPTR, SHAPE, HEAD_DIM, TOO_LARGE. */
+SAGE_API int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t D,
+                                                 size_t* bytes);
+
+/* Attention of queries to the cache: for row t < q_lengths[b] of sequence b
+ * and query head h, which reads key/value head h / (H / cache->H),
+ *   out = sum_j p_j v_j / sum_j p_j, p_j = exp(sm_scale q . k_j - max),
+ *   lse = ln sum_j exp(sm_scale q . k_j),
+ * over the tokens j < lengths[b] of the cache, or with is_causal those with
+ * j <= lengths[b] - q_lengths[b] + t: the queries are the sequence's last
+ * tokens, whose keys were appended before. A row that sees no token gets
+ * out = 0 and lse = -inf. Rows q_lengths[b] and up are left as they were.
+ * lengths, q_lengths: int32 [B]; q_lengths NULL: T each. q, out: BF16
+ * (B, T, H, D), H a multiple of cache->H; lse_dev: fp32 [B][H][T] or NULL.
+ * sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
+ * workspace_dev: sage_cache_attention_workspace_size bytes, 256-byte aligned,
+ * contents do not matter; not used by another call at the same time.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,
+ * CUDA; on the device DEVICE_PAGE. */
+SAGE_API int sage_cache_attention(const sage_cache* cache, const sage_page_table* pages, const int32_t* lengths_dev,
+                                  const int32_t* q_lengths_dev, const sage_bf16_tensor* q, int64_t B, int64_t T,
+                                  int64_t H, float sm_scale, int is_causal, void* out_dev, int64_t ob, int64_t os,
+                                  int64_t oh, float* lse_dev, void* workspace_dev, size_t workspace_bytes,
+                                  void* cuda_stream);
+
 /* ---------------------------------------------------------- diagnostics -- */
 
 /* Synchronizes cuda_stream, then reads and clears the current device's error
  * word. Kernels set it (and return early) when a bounded wait on an internal
  * barrier runs out, or, before any work, when their dynamic shared memory is
  * not 1024-byte aligned (the attention kernel uses all of it for aligned
- * operand tiles); they never trap. *code receives SAGE_OK,
- * SAGE_ERR_DEVICE_TIMEOUT or SAGE_ERR_DEVICE_SMEM. Returns SAGE_OK, NULLPTR
+ * operand tiles), or when a page number or length in device memory
+ * points outside the cache; they never trap. *code receives SAGE_OK,
+ * SAGE_ERR_DEVICE_TIMEOUT, SAGE_ERR_DEVICE_SMEM or SAGE_ERR_DEVICE_PAGE. Returns SAGE_OK, NULLPTR
  * or CUDA. */
 SAGE_API int sage_device_error(void* cuda_stream, int* code);
 

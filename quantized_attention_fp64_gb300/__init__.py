@@ -22,3 +22,12 @@ from .api import (  # noqa: F401
     sageattn_host,
     workspace_size,
 )
+from .cache import (  # noqa: F401
+    QuantizedCache,
+    alloc_cache,
+    cache_append,
+    cache_attention,
+    cache_attention_workspace_size,
+    cache_copy_pages,
+    cache_read,
+)

@@ -39,6 +39,17 @@ class SageattnArgs(ctypes.Structure):
                 ("cuda_stream", c_vp)]
 
 
+class Cache(ctypes.Structure):
+    """sage_cache"""
+    _fields_ = [("k_codes_dev", c_vp), ("v_codes_dev", c_vp), ("k_scale_dev", c_vp), ("v_scale_dev", c_vp),
+                ("num_pages", c_i64), ("page_size", c_i64), ("H", c_i64), ("D", c_i64)]
+
+
+class PageTable(ctypes.Structure):
+    """sage_page_table"""
+    _fields_ = [("table_dev", c_vp), ("row_stride", c_i64), ("max_pages", c_i64)]
+
+
 _SIGNATURES = {
     "sage_bundle_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p, c_vp, ctypes.POINTER(Quantized)]),
     "sage_quantize_scratch_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p]),
@@ -66,6 +77,16 @@ _SIGNATURES = {
     "sage_host_workspace_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, c_size_p]),
     "sage_sageattn_host": (c_int, [c_vp, c_vp, c_vp, I64x4, c_int, ctypes.c_char_p, c_int, ctypes.c_float, c_int, c_vp,
                                    c_int, c_vp, ctypes.c_size_t, c_vp]),
+    "sage_cache_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p, c_vp, ctypes.POINTER(Cache)]),
+    "sage_cache_append": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp,
+                                  ctypes.POINTER(Bf16Tensor), ctypes.POINTER(Bf16Tensor), c_i64, c_i64, c_vp]),
+    "sage_cache_read": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp, c_i64, c_i64, c_vp,
+                                c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp]),
+    "sage_cache_copy_pages": (c_int, [ctypes.POINTER(Cache), c_vp, c_vp, c_i64, c_vp]),
+    "sage_cache_attention_workspace_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_size_p]),
+    "sage_cache_attention": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp,
+                                     ctypes.POINTER(Bf16Tensor), c_i64, c_i64, c_i64, ctypes.c_float, c_int, c_vp,
+                                     c_i64, c_i64, c_i64, c_vp, c_vp, ctypes.c_size_t, c_vp]),
     "sage_device_error": (c_int, [c_vp, ctypes.POINTER(c_int)]),
     "sage_selftest_wait_timeout": (c_int, [c_vp]),
     "sage_strerror": (ctypes.c_char_p, [c_int]),

@@ -191,6 +191,13 @@ int* device_error_ptr() {
   return g_err_ptr[dev];
 }
 
+int device_error_word(int** word) {
+  int dev = 0;
+  const int rc = check_device(&dev);
+  if (rc == SAGE_OK) *word = g_err_ptr[dev];
+  return rc;
+}
+
 }  // namespace sage
 
 namespace sage {
@@ -604,7 +611,9 @@ int sage_device_error(void* cuda_stream, int* code) {
   if (cudaMemcpy(&v, g_err_ptr[dev], sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SAGE_ERR_CUDA;
   const int zero = 0;
   if (cudaMemcpy(g_err_ptr[dev], &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return SAGE_ERR_CUDA;
-  *code = v == 0 ? SAGE_OK : (v == kDevErrSmemAlign ? SAGE_ERR_DEVICE_SMEM : SAGE_ERR_DEVICE_TIMEOUT);
+  *code = v == 0 ? SAGE_OK
+                 : (v == kDevErrSmemAlign ? SAGE_ERR_DEVICE_SMEM
+                                          : (v == kDevErrPage ? SAGE_ERR_DEVICE_PAGE : SAGE_ERR_DEVICE_TIMEOUT));
   return SAGE_OK;
 }
 
@@ -633,6 +642,7 @@ const char* sage_strerror(int code) {
     case SAGE_ERR_ARG: return "invalid argument (sm_scale must be finite and positive)";
     case SAGE_ERR_TOO_LARGE: return "sizes exceed the library's limits";
     case SAGE_ERR_DEVICE_SMEM: return "a kernel found its shared memory window misaligned and did no work";
+    case SAGE_ERR_DEVICE_PAGE: return "a page table, page list or length named tokens outside the cache";
     default: return "unknown error code";
   }
 }

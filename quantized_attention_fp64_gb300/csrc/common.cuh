@@ -22,6 +22,8 @@ __host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return (a + b 
 // dynamic shared memory not 1024-byte aligned (it returns before any work).
 constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrSmemAlign = 2;
+// A page table, a page list or a length named tokens outside the cache.
+constexpr int kDevErrPage = 3;
 
 // One BF16 input: element (b, s, h, d) at p[b*sb + s*ss + h*sh + d].
 struct Bf16In {
@@ -74,6 +76,9 @@ cudaError_t launch_prologue(const Bf16In& q, const Bf16In& k, const Bf16In& v, i
 // Device address of the current device's error word (set up on first use),
 // or nullptr if the runtime call fails.
 int* device_error_ptr();
+// The same with its reason: SAGE_OK and *word set, or the SAGE_ERR_* code
+// (ARCH, CUDA) of the current device's checks.
+int device_error_word(int** word);
 size_t prologue_scratch_bytes(int64_t B, int64_t S, int64_t H, int64_t D);
 // Whether launch_prologue touches its scratch for this shape (the cluster
 // kernel of short sequences does not).
