@@ -353,7 +353,7 @@ def test_attention_peaked_rows(T):
     assert np.abs(f32(lse) - ref[1]).max() <= 2.0 ** -11
 
 
-@pytest.mark.parametrize("T", [1, 40, 140])
+@pytest.mark.parametrize("T", [1, 6, 13, 40, 140])
 def test_attention_nan_stays_with_the_rows_that_see_it(T):
     rng = np.random.default_rng(24)
     H, Hkv, D, page = 4, 2, 64, 64
