@@ -188,6 +188,9 @@ int sage_cache_attention(const sage_cache* cache, const sage_page_table* pages, 
       (rc = check_ints(lengths_dev, true)) != SAGE_OK || (rc = check_ints(q_lengths_dev, false)) != SAGE_OK ||
       (rc = check_in(q, &a.q)) != SAGE_OK || (rc = check_out(out_dev, ob, os, oh, &a.out)) != SAGE_OK)
     return rc;
+  // the call's blocks, all sequences and heads, are counted in 32 bits
+  const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;
+  if (B > 0 && a.c.H > 0 && seq_blocks > ((int64_t(1) << 31) - 1) / (B * a.c.H)) return SAGE_ERR_TOO_LARGE;
   if (lse_dev != nullptr && !aligned(lse_dev, 4)) return SAGE_ERR_ALIGN;
   if (!(std::isnan(sm_scale) || (std::isfinite(sm_scale) && sm_scale > 0.0f))) return SAGE_ERR_ARG;
   const size_t need = (B == 0 || T == 0 || H == 0) ? 0 : cache_attention_workspace_bytes(B, T, H, a.c.H, cache->D);

@@ -18,11 +18,12 @@
 // last; partial items leave their running maximum, sum and unnormalised output
 // in the workspace, two slots per CTA, and a second kernel joins them in the
 // order of the keys.
-// Warps. Each of a CTA's 8 warps takes every 8th block of the range through a
+// Warps. Each of a CTA's 4 warps takes every 4th block of the range through a
 // ring of its own: lane 0 copies a block's keys and values (contiguous in the
 // cache) into shared memory with bulk copies that complete on an mbarrier,
 // kStages blocks ahead, so loads never wait for another warp. The warps' parts
-// of an item are joined in shared memory where the item ends.
+// of an item are joined in shared memory where the item ends; two or three CTAs
+// share an SM, so that one streams while another joins.
 // Products. The item's rows (query tokens x heads that share the key/value
 // head) are the 16 rows of m16n8k16 products. Queries become fp16 times a power
 // of two per row (their largest value lies in [1, 4), so a bf16 value keeps its
@@ -41,9 +42,6 @@ namespace sage {
 namespace {
 
 constexpr int kRowThreads = 128;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 160;                  // one per SM
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr float kLazy = 8.0f;                   // p may reach 2^8 before the running maximum follows
@@ -51,55 +49,34 @@ constexpr float kLazy = 8.0f;                   // p may reach 2^8 before the ru
 // ---------------------------------------------------------------- the plan --
 
 struct Seq {
-  int64_t len, q_len;
+  int len, q_len;
 };
 
-__device__ __forceinline__ Seq load_seq(const CacheAttentionArgs& a, int64_t b, bool* bad) {
+__device__ __forceinline__ Seq load_seq(const CacheAttentionArgs& a, int b, bool* bad) {
   Seq s;
-  s.len = checked_length(a.lengths[b], table_capacity(a.pt.max_pages, a.c.blocks_per_page), bad);
-  s.q_len = a.q_lengths != nullptr ? checked_length(a.q_lengths[b], a.T, bad) : a.T;
+  s.len = static_cast<int>(checked_length(a.lengths[b], table_capacity(a.pt.max_pages, a.c.blocks_per_page), bad));
+  s.q_len = static_cast<int>(a.q_lengths != nullptr ? checked_length(a.q_lengths[b], a.T, bad) : a.T);
   return s;
 }
 
 // Units of one head of a sequence: its blocks, or one that is empty (a row
 // without keys still has an output). A sequence without queries has one, too.
-__device__ __forceinline__ int64_t seq_units(const Seq& s) {
-  const int64_t n = (s.len + kCacheBlock - 1) / kCacheBlock;
+// All units of a call together are fewer than 2^31 (checked on the host).
+__device__ __forceinline__ int seq_units(const Seq& s) {
+  const int n = (s.len + kCacheBlock - 1) / kCacheBlock;
   return (n == 0 || s.q_len == 0) ? 1 : n;
 }
 
-// Unit u of total W belongs to CTA owner(u); CTA c has [first(c), first(c + 1)).
+// CTA c of `ctas` has the units [first(c), first(c + 1)) of W, unit u belongs to owner(u).
 struct Split {
-  int64_t each, extra;  // W = each * ctas + extra: the first `extra` CTAs have one more
-  __device__ Split(int64_t W, int ctas) : each(W / ctas), extra(W % ctas) {}
-  __device__ int64_t first(int64_t c) const { return c * each + (c < extra ? c : extra); }
-  __device__ int64_t owner(int64_t u) const {
-    const int64_t head = extra * (each + 1);
+  int each, extra;  // W = each * ctas + extra: the first `extra` CTAs have one more
+  __device__ Split(int W, int ctas) : each(W / ctas), extra(W % ctas) {}
+  __device__ int first(int c) const { return c * each + (c < extra ? c : extra); }
+  __device__ int owner(int u) const {
+    const int head = extra * (each + 1);
     return u < head ? u / (each + 1) : extra + (u - head) / each;
   }
 };
-
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Sum of seq_units over sequences [0, n); every thread of the CTA gets it.
-// buf: kWarps values of shared memory.
-__device__ int64_t units_before(const CacheAttentionArgs& a, int64_t n, int64_t* buf) {
-  int64_t x = 0;
-  bool bad = false;
-  for (int64_t b = threadIdx.x; b < n; b += kThreads) x += seq_units(load_seq(a, b, &bad));
-  x = warp_sum(x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) x += buf[w];
-  return x;
-}
 
 // ------------------------------------------------------------- arithmetic --
 
@@ -107,6 +84,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
@@ -126,11 +109,24 @@ __device__ __forceinline__ void codes_to_half(uint32_t x, uint32_t& lo, uint32_t
   hi = *reinterpret_cast<const uint32_t*>(&rb);
 }
 
+// Four int8 codes to two pairs of fp16 code + 1152: the sum over the rows that
+// p weights takes 1152 sum p off again.
+constexpr float kBias = 1152.0f;
+__device__ __forceinline__ void codes_to_biased_half(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  x ^= 0x80808080u;
+  lo = __byte_perm(x, 0x64646464u, 0x4140);
+  hi = __byte_perm(x, 0x64646464u, 0x4342);
+}
+
+// d = a b + c, m16n8k16, fp16 with fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                         float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  mma16816(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int* dev_err) {
@@ -161,26 +157,35 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 // ------------------------------------------------------------------ decode --
 
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxSms = 160;
+
 template <int D, int MT>
 struct Dec {
+  // CTAs of an SM: what the accumulators' registers allow (168 or 255 a
+  // thread); stages: blocks in flight per warp, 192 KB of an SM's in all
+  static constexpr int kCtasPerSm = MT == 1 ? 3 : 2;
+  static constexpr int kStages = (MT == 1 ? 2 : 3) * (128 / D);
   static constexpr uint32_t kBlockBytes = kCacheBlock * D;     // keys or values of a block
-  static constexpr int kStages = D == 128 ? 3 : 5;             // blocks in flight per warp
   static constexpr uint32_t kRing = kWarps * kStages * 2 * kBlockBytes;
-  static constexpr uint32_t kOffMerge = kRing;                 // [warp][16 rows][64 channels] fp32
-  static constexpr uint32_t kOffMl = kOffMerge + kWarps * 16 * 64 * 4;  // [warp][16 MT rows] (m, l)
+  static constexpr uint32_t kOffMerge = kRing;                 // [warp][16 rows][32 channels] fp32
+  static constexpr uint32_t kOffMl = kOffMerge + kWarps * 16 * 32 * 4;  // [warp][16 MT rows] (m, l)
   static constexpr uint32_t kOffScale = kOffMl + kWarps * 16 * MT * 8;  // [warp][stage] (key, value) scale
   static constexpr uint32_t kOffValid = kOffScale + kWarps * kStages * 8;
   static constexpr uint32_t kOffBar = kOffValid + kWarps * kStages * 4;
-  static constexpr uint32_t kOffPlan = kOffBar + kWarps * kStages * 8;
-  static constexpr uint32_t kBytes = kOffPlan + 128;
+  static constexpr uint32_t kOffPlan = kOffBar + kWarps * kStages * 8;  // kWarps sums, then (b, unit in b)
+  static constexpr uint32_t kBytes = kOffPlan + (kWarps + 2) * 4;
+  static_assert(kCtasPerSm * (kBytes + 1024) <= 233472u && kOffBar % 8 == 0, "shared memory of one SM");
+  // workspace: a descriptor of each CTA's last item, then two slots per CTA
+  static constexpr size_t kDesc = size_t(kMaxSms) * kCtasPerSm * sizeof(int4);
   static constexpr size_t kSlot = size_t(16) * MT * (D + 2);   // floats of a partial item
-  static_assert(kBytes <= 232448u && kOffBar % 8 == 0 && kOffPlan % 8 == 0, "shared memory of one CTA");
+  static constexpr size_t kWorkspace = kDesc + size_t(kMaxSms) * kCtasPerSm * 2 * kSlot * 4;
 };
 
 // A position in the list of units.
 struct Cursor {
-  int64_t b, blk, units;  // sequence, block of the head, units of the head
-  int32_t h;
+  int b, h, blk, units;  // sequence, head, block of the head, units of the head
   Seq s;
 };
 
@@ -198,7 +203,7 @@ __device__ __forceinline__ void cursor_settle(const CacheAttentionArgs& a, Curso
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode_kernel(const CacheAttentionArgs a) {
   using L = Dec<D, MT>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -207,64 +212,69 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
   const int g = lane >> 2, t = lane & 3;
   if (threadIdx.x < kWarps * L::kStages) tc::mbar_init(sbase + L::kOffBar + 8 * threadIdx.x, 2);
   tc::fence_mbar_init();
-  __syncthreads();
   // the previous kernel of the stream may still run up to here
   tc::griddep_wait();
   tc::griddep_launch_dependents();
 
-  // this CTA's range of units and where it begins
-  int64_t* plan = reinterpret_cast<int64_t*>(smem + L::kOffPlan);  // kWarps values, then (b, unit of b's first head)
-  const int64_t W = units_before(a, a.B, plan) * a.c.H;
+  // this CTA's range of units and where it begins: each thread sums a run of
+  // sequences, a scan over the threads finds whose run the range begins in
+  int* plan = reinterpret_cast<int*>(smem + L::kOffPlan);
+  const int run = (static_cast<int>(a.B) + kThreads - 1) / kThreads;
+  const int b_lo = min(run * static_cast<int>(threadIdx.x), static_cast<int>(a.B));
+  const int b_hi = min(b_lo + run, static_cast<int>(a.B));
+  int mine = 0;
+  bool bad = false;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(load_seq(a, b, &bad));
+  if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) plan[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, W = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += plan[w];
+    W += plan[w];
+  }
+  W *= a.c.H;
   const Split split(W, static_cast<int>(gridDim.x));
-  const int64_t lo = split.first(blockIdx.x), hi = split.first(blockIdx.x + 1);
-  if (lo == hi) return;
-  for (int64_t base = 0, before = 0; base < a.B; base += kThreads) {
-    const int64_t b = base + threadIdx.x;
-    bool bad = false;
-    const int64_t mine = b < a.B ? seq_units(load_seq(a, b, &bad)) : 0;
-    if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+  const int lo = split.first(static_cast<int>(blockIdx.x)), hi = split.first(static_cast<int>(blockIdx.x) + 1);
+  before *= a.c.H;
+  if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
+    int b = b_lo;
+    for (;; ++b) {
+      const int u = seq_units(load_seq(a, b, &bad)) * a.c.H;
+      if (lo < before + u) break;
+      before += u;
     }
-    __syncthreads();
-    if (lane == 31) plan[warp] = incl;
-    __syncthreads();
-    int64_t start = before, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) start += plan[w];
-      all += plan[w];
-    }
-    start += incl - mine;  // units of one head before sequence b
-    if (b < a.B && start * a.c.H <= lo && lo < (start + mine) * a.c.H) {
-      plan[kWarps] = b;
-      plan[kWarps + 1] = lo - start * a.c.H;
-    }
-    before += all;
-    if (before * a.c.H > lo && blockIdx.x != 0) break;  // CTA 0 looks at every length once
+    plan[kWarps] = b;
+    plan[kWarps + 1] = lo - before;
   }
   __syncthreads();
-  Cursor seg;
-  {
-    bool bad = false;
-    seg.b = plan[kWarps];
-    seg.s = load_seq(a, seg.b, &bad);
-    seg.units = seq_units(seg.s);
-    seg.h = static_cast<int32_t>(plan[kWarps + 1] / seg.units);
-    seg.blk = plan[kWarps + 1] % seg.units;
+  int4* desc = static_cast<int4*>(a.workspace);
+  if (lo == hi) {
+    if (threadIdx.x == 0) desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
   }
-  const int64_t n_cta = hi - lo;
-  const int64_t n_mine = n_cta > warp ? (n_cta - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
+  Cursor seg;
+  seg.b = plan[kWarps];
+  seg.s = load_seq(a, seg.b, &bad);
+  seg.units = seq_units(seg.s);
+  seg.h = plan[kWarps + 1] / seg.units;
+  seg.blk = plan[kWarps + 1] - seg.h * seg.units;
+  const int n_cta = hi - lo;
+  const int n_mine = n_cta > warp ? (n_cta - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
 
   // the warp's next 32 blocks, one per lane: lane i of the window has blocks i, i + 32, ...
   Cursor ahead = seg;
-  ahead.blk += warp + static_cast<int64_t>(lane) * kWarps;
+  ahead.blk += warp + lane * kWarps;
   if (lane < n_mine) cursor_settle(a, ahead);
   int64_t window = -1;  // its block number in the cache, -1: no tokens
-  const auto fill_window = [&](int64_t k0) {
+  const auto fill_window = [&](int k0) {
     window = -1;
     if (k0 + lane < n_mine) {
       if (k0 > 0) {
@@ -272,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
         cursor_settle(a, ahead);
       }
       if (ahead.s.q_len > 0 && ahead.blk * kCacheBlock < ahead.s.len) {
-        const int64_t page = a.pt.table[ahead.b * a.pt.stride + ahead.blk / a.c.blocks_per_page];
+        const int pg = ahead.blk / a.c.blocks_per_page;
+        const int page = a.pt.table[ahead.b * a.pt.stride + pg];
         if (page_ok(page, a.c.num_pages))
-          window = block_slot(page, ahead.h, a.c.H, a.c.blocks_per_page,
-                              static_cast<int32_t>(ahead.blk % a.c.blocks_per_page));
+          window = block_slot(page, ahead.h, a.c.H, a.c.blocks_per_page, ahead.blk - pg * a.c.blocks_per_page);
         else
           atomicExch(a.dev_err, kDevErrPage);
       }
@@ -285,21 +295,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
   const uint32_t bars = sbase + L::kOffBar + static_cast<uint32_t>(warp) * L::kStages * 8;
   const uint32_t scales = sbase + L::kOffScale + static_cast<uint32_t>(warp) * L::kStages * 8;
   volatile int* valid = reinterpret_cast<volatile int*>(smem + L::kOffValid) + warp * L::kStages;
-  int64_t issued = 0;
+  int issued = 0;
+  uint32_t into = 0;  // stage of the next issue
   const auto issue = [&]() {  // whole warp
     if (issued >= n_mine) return;
     if ((issued & 31) == 0) fill_window(issued);
-    const int64_t slot = __shfl_sync(0xffffffffu, window, static_cast<int>(issued & 31));
+    const int64_t slot = __shfl_sync(0xffffffffu, window, issued & 31);
     if (lane == 0) {
-      const uint32_t s = static_cast<uint32_t>(issued % L::kStages);
-      const uint32_t bar = bars + 8 * s, dst = ring + s * 2 * L::kBlockBytes;
-      valid[s] = slot >= 0;
+      const uint32_t bar = bars + 8 * into, dst = ring + into * 2 * L::kBlockBytes;
+      valid[into] = slot >= 0;
       if (slot >= 0) {
         tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
         tc::bulk_load(dst, a.c.k + slot * L::kBlockBytes, L::kBlockBytes, bar);
         tc::bulk_load(dst + L::kBlockBytes, a.c.v + slot * L::kBlockBytes, L::kBlockBytes, bar);
-        cp_async4_only(scales + 8 * s, a.c.ks + slot);
-        cp_async4_only(scales + 8 * s + 4, a.c.vs + slot);
+        cp_async4_only(scales + 8 * into, a.c.ks + slot);
+        cp_async4_only(scales + 8 * into + 4, a.c.vs + slot);
         cp_async_arrive(bar);
       } else {
         tc::mbar_arrive(bar);
@@ -307,23 +317,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
       }
     }
     ++issued;
+    into = into + 1 == L::kStages ? 0 : into + 1;
   };
 #pragma unroll 1
   for (int s = 0; s < L::kStages; ++s) issue();
 
-  int64_t taken = 0;  // blocks of this warp done
+  int taken = 0;  // blocks of this warp done
+  uint32_t from = 0, parity = 0;  // stage and phase of the next one
   bool alive = true;
   const int G = a.H / a.c.H;
 #pragma unroll 1
-  for (int64_t at = 0; at < n_cta;) {
+  for (int at = 0; at < n_cta;) {
     // the segment: units [at, at + n) of the CTA, blocks [seg.blk, seg.blk + n) of one item
-    const int64_t n = min(seg.units - seg.blk, n_cta - at);
-    const int64_t R = seg.s.q_len * G;
-    const int64_t min_sees = a.causal ? seg.s.len - seg.s.q_len + 1 : seg.s.len;  // of the item's first token
+    const int n = min(seg.units - seg.blk, n_cta - at);
+    const int R = seg.s.q_len * G;
+    const int min_sees = a.causal ? seg.s.len - seg.s.q_len + 1 : seg.s.len;  // of the first token
     // queries: A fragments of the key products, rows g and g + 8 of each 16
     uint32_t qf[MT][kHalves][4][4];
     float f[MT][2];
-    int64_t sees[MT][2];
+    int sees[MT][2];  // keys that the row sees (a length fits 31 bits)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -332,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
         uint32_t w[kHalves][8];
         sees[mt][e] = 0;
         if (r < R) {
-          const int64_t tok = r / G;
+          const int tok = r / G;
           sees[mt][e] = a.causal ? seg.s.len - seg.s.q_len + 1 + tok : seg.s.len;
-          const uint16_t* p = a.q.p + seg.b * a.q.sb + tok * a.q.ss + (static_cast<int64_t>(seg.h) * G + r % G) * a.q.sh + 16 * t;
+          const uint16_t* p = a.q.p + seg.b * a.q.sb + tok * a.q.ss + (seg.h * G + r - tok * G) * a.q.sh + 16 * t;
 #pragma unroll
           for (int i = 0; i < kHalves; ++i) {
             *reinterpret_cast<uint4*>(w[i]) = *reinterpret_cast<const uint4*>(p + 64 * i);
@@ -366,64 +378,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
                 pack_half2(__uint_as_float(w[i][x] << 16) * down, __uint_as_float(w[i][x] & 0xFFFF0000u) * down);
       }
     }
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];
+    float2 o[MT][D / 8][2], l[MT][2];  // rows g and g + 8: channels 8x + 2t, + 1; sums of even and odd keys
+    float m[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) o[mt][x][0] = o[mt][x][1] = o[mt][x][2] = o[mt][x][3] = 0.0f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
-    }
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[mt][x][e] = make_float2(0.0f, 0.0f);
+        l[mt][e] = make_float2(0.0f, 0.0f);
+        m[mt][e] = -INFINITY;
+      }
     // this warp's blocks of the segment: CTA units that are warp mod 8
-    const int64_t first = at + (warp - at % kWarps + kWarps) % kWarps;
+    const int first = at + (warp - at % kWarps + kWarps) % kWarps;
 #pragma unroll 1
-    for (int64_t u = first; u < at + n && alive; u += kWarps) {
-      const uint32_t s = static_cast<uint32_t>(taken % L::kStages);
-      const uint32_t parity = static_cast<uint32_t>(taken / L::kStages) & 1u;
+    for (int u = first; u < at + n && alive; u += kWarps) {
+      const uint32_t s = from;
       alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * s, parity, a.dev_err));
       if (!alive) break;
       if (valid[s] != 0) {
         const uint8_t* kb = smem + (ring - sbase) + s * 2 * L::kBlockBytes;
         const uint8_t* vb = kb + L::kBlockBytes;
         const float2 sc = *reinterpret_cast<const float2*>(smem + (scales - sbase) + 8 * s);
-        const int64_t key0 = (seg.blk + (u - at)) * kCacheBlock;
-        const bool masked = key0 + kCacheBlock > min_sees;
+        const int key0 = (seg.blk + (u - at)) * kCacheBlock;
         float z[MT][4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < kHalves; ++i) {
+          uint32_t cw[4][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) z[mt][j][0] = z[mt][j][1] = z[mt][j][2] = z[mt][j][3] = 0.0f;
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(cw[j]) = *reinterpret_cast<const uint4*>(kb + i * 2048 + j * 512 + lane * 16);
 #pragma unroll
-          for (int i = 0; i < kHalves; ++i) {
-            const uint4 c = *reinterpret_cast<const uint4*>(kb + i * 2048 + j * 512 + lane * 16);
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int j = 0; j < 4; ++j) {
               uint32_t b0, b1;
-              codes_to_half(cw[x], b0, b1);
+              codes_to_half(cw[j][x], b0, b1);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816(z[mt][j], qf[mt][i][x], b0, b1);
+              for (int mt = 0; mt < MT; ++mt) {
+                if (i == 0 && x == 0) mma16816(z[mt][j], qf[mt][i][x], b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                else mma16816(z[mt][j], qf[mt][i][x], b0, b1);
+              }
             }
-          }
+        }
+        const bool masked = key0 + kCacheBlock > min_sees;
+        if (masked) {
+          // keys behind what the row sees: below every number here, and p = 0 below
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (key0 + 8 * j + 2 * t + (x & 1) >= sees[mt][x >> 1]) z[mt][j][x] = -INFINITY;
         }
         uint32_t pf[MT][2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float y = z[mt][j][x] * (f[mt][x >> 1] * sc.x);
-              if (masked && key0 + 8 * j + 2 * t + (x & 1) >= sees[mt][x >> 1]) y = -INFINITY;
-              z[mt][j][x] = y;
-              mx[x >> 1] = fmaxf(mx[x >> 1], y);
-            }
+          // logits are z * c with c >= 0, so the largest z gives the largest logit
+          float c[2], mx[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            c[e] = f[mt][e] * sc.x;
+            float y = max3(z[mt][0][2 * e], z[mt][0][2 * e + 1], z[mt][1][2 * e]);
+            y = max3(y, z[mt][1][2 * e + 1], z[mt][2][2 * e]);
+            y = max3(y, z[mt][2][2 * e + 1], z[mt][3][2 * e]);
+            y = fmaxf(y, z[mt][3][2 * e + 1]);
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            mx[e] = y == -INFINITY ? y : y * c[e];
           }
           if (__any_sync(0xffffffffu, mx[0] > m[mt][0] + kLazy || mx[1] > m[mt][1] + kLazy)) {
             float alpha[2];
@@ -432,52 +455,75 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
               const float up = fmaxf(m[mt][e], mx[e]);
               alpha[e] = up == -INFINITY ? 1.0f : ex2(m[mt][e] - up);
               m[mt][e] = up;
-              l[mt][e] *= alpha[e];
+              l[mt][e].x *= alpha[e];
+              l[mt][e].y *= alpha[e];
             }
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-              o[mt][x][0] *= alpha[0];
-              o[mt][x][1] *= alpha[0];
-              o[mt][x][2] *= alpha[1];
-              o[mt][x][3] *= alpha[1];
-            }
+            for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) o[mt][x][e] = __fmul2_rn(o[mt][x][e], make_float2(alpha[e], alpha[e]));
           }
           const float ref[2] = {m[mt][0] == -INFINITY ? 0.0f : m[mt][0], m[mt][1] == -INFINITY ? 0.0f : m[mt][1]};
+          float2 p[4][2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) z[mt][j][x] = ex2(z[mt][j][x] - ref[x >> 1]);
-            l[mt][0] += z[mt][j][0] + z[mt][j][1];
-            l[mt][1] += z[mt][j][2] + z[mt][j][3];
-            pf[mt][j >> 1][(j & 1) * 2] = pack_half2(z[mt][j][0], z[mt][j][1]);
-            pf[mt][j >> 1][(j & 1) * 2 + 1] = pack_half2(z[mt][j][2], z[mt][j][3]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 y = __ffma2_rn(make_float2(z[mt][j][2 * e], z[mt][j][2 * e + 1]), make_float2(c[e], c[e]),
+                                          make_float2(-ref[e], -ref[e]));
+              p[j][e] = make_float2(ex2(y.x), ex2(y.y));
+            }
+          if (masked) {
+            // a scale of 0 or NaN would make a hidden key's logit NaN
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (key0 + 8 * j + 2 * t >= sees[mt][e]) p[j][e].x = 0.0f;
+                if (key0 + 8 * j + 2 * t + 1 >= sees[mt][e]) p[j][e].y = 0.0f;
+              }
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              l[mt][e] = __fadd2_rn(l[mt][e], p[j][e]);
+              pf[mt][j >> 1][(j & 1) * 2 + e] = pack_half2(p[j][e].x, p[j][e].y);
+            }
         }
         // a block that a row does not reach adds nothing to it, whatever its scale is
-        float vs[MT][2];
+        float vs[MT][2], off[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          // what the values' bias adds: the sum of the rounded p, as a product with ones
+          float d[4];
+          mma16816(d, pf[mt][0], 0x3C003C00u, 0x3C003C00u, 0.0f, 0.0f, 0.0f, 0.0f);
+          mma16816(d, pf[mt][1], 0x3C003C00u, 0x3C003C00u);
+          off[mt][0] = -kBias * d[0];
+          off[mt][1] = -kBias * d[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) vs[mt][e] = key0 < sees[mt][e] ? sc.y : 0.0f;
+        }
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {
           const uint2 c = *reinterpret_cast<const uint2*>(vb + x * 256 + lane * 8);
           uint32_t b[4];
-          codes_to_half(c.x, b[0], b[1]);
-          codes_to_half(c.y, b[2], b[3]);
+          codes_to_biased_half(c.x, b[0], b[1]);
+          codes_to_biased_half(c.y, b[2], b[3]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(d, pf[mt][0], b[0], b[1]);
+            float d[4];
+            mma16816(d, pf[mt][0], b[0], b[1], off[mt][0], off[mt][0], off[mt][1], off[mt][1]);
             mma16816(d, pf[mt][1], b[2], b[3]);
-            o[mt][x][0] = fmaf(d[0], vs[mt][0], o[mt][x][0]);
-            o[mt][x][1] = fmaf(d[1], vs[mt][0], o[mt][x][1]);
-            o[mt][x][2] = fmaf(d[2], vs[mt][1], o[mt][x][2]);
-            o[mt][x][3] = fmaf(d[3], vs[mt][1], o[mt][x][3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              o[mt][x][e] = __ffma2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(vs[mt][e], vs[mt][e]), o[mt][x][e]);
           }
         }
       }
       ++taken;
+      from = from + 1 == L::kStages ? 0 : from + 1;
+      if (from == 0) parity ^= 1u;
       __syncwarp();  // every lane is done with the stage
       issue();
     }
@@ -488,62 +534,73 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
-        if (t == 0) ml[warp * 16 * MT + mt * 16 + e * 8 + g] = make_float2(m[mt][e], l[mt][e]);
+        float y = l[mt][e].x + l[mt][e].y;
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (t == 0) ml[warp * 16 * MT + mt * 16 + e * 8 + g] = make_float2(m[mt][e], y);
       }
     const bool whole = n == seg.units;
     const int which = at == 0 ? 0 : 1;  // a partial item is the range's first or its last
-    float* part = static_cast<float*>(a.workspace) + (static_cast<size_t>(blockIdx.x) * 2 + which) * L::kSlot;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + L::kDesc) +
+                  (static_cast<size_t>(blockIdx.x) * 2 + which) * L::kSlot;
+    if (at + n == n_cta && threadIdx.x == 0) {
+      // the last item, if it begins here and goes on in other CTAs: up to which one, and whose rows
+      const int rest = seg.units - seg.blk - n;
+      desc[blockIdx.x] = seg.blk == 0 && rest > 0 ? make_int4(split.owner(hi + rest - 1), seg.b, seg.h, which)
+                                                  : make_int4(-1, 0, 0, 0);
+    }
+    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (mt * 16 >= R) break;
+      const int row = threadIdx.x >> 3, c4 = threadIdx.x & 7;
+      const int r = mt * 16 + row;
+      float top = -INFINITY, sum = 0.0f, wt[kWarps];
 #pragma unroll
-      for (int half = 0; half < kHalves; ++half) {
-        // rows of 64 channels as 32 pairs, pair u of row r at u ^ 4 (r mod 4): no bank conflicts
-        float2* buf = reinterpret_cast<float2*>(smem + L::kOffMerge) + warp * 16 * 32;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 16 * MT + r].x);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = ml[w * 16 * MT + r];
+        wt[w] = ex2(x.x - (top == -INFINITY ? 0.0f : top));
+        sum = fmaf(x.y, wt[w], sum);
+      }
+      const int tok = r / G, head = seg.h * G + r - tok * G;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint16_t* dst = a.out.p + seg.b * a.out.sb + tok * a.out.ss + head * a.out.sh + 4 * c4;
+      if (r < R && c4 == 0) {
+        if (!whole) *reinterpret_cast<float2*>(part + 16 * MT * D + 2 * r) = make_float2(top, sum);
+        else if (a.lse != nullptr)
+          a.lse[(static_cast<int64_t>(seg.b) * a.H + head) * a.T + tok] =
+              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      }
+#pragma unroll
+      for (int cut = 0; cut < D / 32; ++cut) {
+        // 32 channels of a row as 16 pairs, pair u of row r at u ^ 4 (r mod 4): no bank conflicts
+        float2* buf = reinterpret_cast<float2*>(smem + L::kOffMerge);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
           const int u = (4 * x + t) ^ ((g & 3) * 4);
-          buf[g * 32 + u] = make_float2(o[mt][half * 8 + x][0], o[mt][half * 8 + x][1]);
-          buf[(g + 8) * 32 + u] = make_float2(o[mt][half * 8 + x][2], o[mt][half * 8 + x][3]);
+          buf[(warp * 16 + g) * 16 + u] = o[mt][cut * 4 + x][0];
+          buf[(warp * 16 + g + 8) * 16 + u] = o[mt][cut * 4 + x][1];
         }
         __syncthreads();
-        const int row = threadIdx.x >> 4, c4 = threadIdx.x & 15;
-        const int r = mt * 16 + row;
         if (r < R) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 16 * MT + r].x);
-          const float ref = top == -INFINITY ? 0.0f : top;
-          float sum = 0.0f;
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 x = ml[w * 16 * MT + r];
-            const float wt = ex2(x.x - ref);
-            const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float2*>(smem + L::kOffMerge) +
-                                                              (w * 16 + row) * 32 + ((2 * c4) ^ ((row & 3) * 4)));
-            sum = fmaf(x.y, wt, sum);
-            acc.x = fmaf(y.x, wt, acc.x);
-            acc.y = fmaf(y.y, wt, acc.y);
-            acc.z = fmaf(y.z, wt, acc.z);
-            acc.w = fmaf(y.w, wt, acc.w);
+            const float4 y = *reinterpret_cast<const float4*>(buf + (w * 16 + row) * 16 + ((2 * c4) ^ ((row & 3) * 4)));
+            acc.x = fmaf(y.x, wt[w], acc.x);
+            acc.y = fmaf(y.y, wt[w], acc.y);
+            acc.z = fmaf(y.z, wt[w], acc.z);
+            acc.w = fmaf(y.w, wt[w], acc.w);
           }
           if (whole) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int64_t tok = r / G, head = static_cast<int64_t>(seg.h) * G + r % G;
-            uint16_t* p = a.out.p + seg.b * a.out.sb + tok * a.out.ss + head * a.out.sh + half * 64 + 4 * c4;
             const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
             const __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(p) =
+            *reinterpret_cast<uint2*>(dst + cut * 32) =
                 make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
-            if (a.lse != nullptr && half == 0 && c4 == 0)
-              a.lse[(seg.b * a.H + head) * a.T + tok] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
           } else {
-            *reinterpret_cast<float4*>(part + static_cast<size_t>(r) * D + half * 64 + 4 * c4) = acc;
-            if (half == 0 && c4 == 0)
-              *reinterpret_cast<float2*>(part + static_cast<size_t>(16) * MT * D + 2 * r) = make_float2(top, sum);
+            *reinterpret_cast<float4*>(part + r * D + cut * 32 + 4 * c4) = acc;
           }
         }
         __syncthreads();
@@ -556,66 +613,101 @@ __global__ void __launch_bounds__(kThreads, 1) cache_decode_kernel(const CacheAt
   }
   if (!alive) {
     // copies in flight land before the CTA ends
-    for (; taken < issued; ++taken)
-      wait_bounded(bars + 8 * static_cast<uint32_t>(taken % L::kStages),
-                   static_cast<uint32_t>(taken / L::kStages) & 1u, a.dev_err);
+    for (; taken < issued; ++taken) {
+      wait_bounded(bars + 8 * from, parity, a.dev_err);
+      from = from + 1 == L::kStages ? 0 : from + 1;
+      if (from == 0) parity ^= 1u;
+    }
   }
 }
 
-// Joins the partial items: one CTA per (sequence, key/value head); a warp per row.
+// Joins the items that several CTAs share. Block (c, y) serves the item that
+// begins in CTA c and ends in a later one, two of its rows: of 8 warps, four
+// share a row, each with every 4th part.
+constexpr int kJoinWarps = 8, kJoinRows = 2, kJoinParts = kJoinWarps / kJoinRows;
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheAttentionArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttentionArgs a) {
   constexpr int kV = D / 32;  // channels per lane
   using L = Dec<D, MT>;
-  __shared__ int64_t buf[kWarps];
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float2 ml_s[kJoinWarps];
   tc::griddep_wait();
-  const int64_t b = blockIdx.y;
-  const int32_t h = static_cast<int32_t>(blockIdx.x);
-  const int64_t W = units_before(a, a.B, buf) * a.c.H;
-  const int64_t before = units_before(a, b, buf) * a.c.H;
-  bool bad = false;
-  const Seq s = load_seq(a, b, &bad);
-  const int64_t n = seq_units(s), u0 = before + h * n;
-  const Split split(W, ctas);
-  const int64_t c0 = split.owner(u0), c1 = split.owner(u0 + n - 1);
-  if (c0 == c1) return;  // one CTA had the whole item
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = static_cast<int>(blockIdx.x);
+  const int4 item = static_cast<const int4*>(a.workspace)[c0];  // last CTA, sequence, head, slot in the first CTA
+  if (item.x < 0) return;
   const int G = a.H / a.c.H;
-  const float* ws = static_cast<const float*>(a.workspace);
-  // CTA c0's part is its first one if its range begins with the item, else its last; the others' their first
-  const size_t slot0 = (static_cast<size_t>(c0) * 2 + (split.first(c0) < u0 ? 1 : 0)) * L::kSlot;
-  for (int64_t r = warp; r < s.q_len * G; r += kWarps) {
-    float top = -INFINITY;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) {
-      const float* p = ws + (c == c0 ? slot0 : static_cast<size_t>(c) * 2 * L::kSlot);
-      top = fmaxf(top, p[static_cast<size_t>(16) * MT * D + 2 * r]);
+  bool bad = false;
+  const int R = load_seq(a, item.y, &bad).q_len * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = static_cast<int>(blockIdx.y) * kJoinRows + warp / kJoinParts;
+  const float* ws = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + L::kDesc);
+  float top = -INFINITY, sum = 0.0f, acc[kV];
+#pragma unroll
+  for (int x = 0; x < kV; ++x) acc[x] = 0.0f;
+  if (r < R) {
+    // parts of this warp, four at a time: their loads do not wait for one another
+    for (int c = c0 + warp % kJoinParts; c <= item.x; c += 4 * kJoinParts) {
+      float2 x[4];
+      float y[4][kV];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ci = c + i * kJoinParts;
+        x[i] = make_float2(-INFINITY, 0.0f);
+        if (ci <= item.x) {
+          const float* p = ws + (static_cast<size_t>(ci) * 2 + (ci == c0 ? item.w : 0)) * L::kSlot;
+          x[i] = *reinterpret_cast<const float2*>(p + 16 * MT * D + 2 * r);
+          if constexpr (kV == 4) *reinterpret_cast<float4*>(y[i]) = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
+          else *reinterpret_cast<float2*>(y[i]) = *reinterpret_cast<const float2*>(p + r * D + 2 * lane);
+        } else {
+#pragma unroll
+          for (int v = 0; v < kV; ++v) y[i][v] = 0.0f;
+        }
+      }
+      const float up = fmaxf(max3(x[0].x, x[1].x, x[2].x), fmaxf(x[3].x, top));
+      const float ref = up == -INFINITY ? 0.0f : up, alpha = ex2(top - ref);
+      top = up;
+      sum *= alpha;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[v] *= alpha;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wt = ex2(x[i].x - ref);
+        sum = fmaf(x[i].y, wt, sum);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) acc[v] = fmaf(y[i][v], wt, acc[v]);
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, acc[kV];
-#pragma unroll
-    for (int x = 0; x < kV; ++x) acc[x] = 0.0f;
-#pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
-      const float* p = ws + (c == c0 ? slot0 : static_cast<size_t>(c) * 2 * L::kSlot);
-      const float2 x = *reinterpret_cast<const float2*>(p + static_cast<size_t>(16) * MT * D + 2 * r);
-      const float wt = ex2(x.x - ref);
-      sum = fmaf(x.y, wt, sum);
-#pragma unroll
-      for (int i = 0; i < kV; ++i) acc[i] = fmaf(p[r * D + kV * lane + i], wt, acc[i]);
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t tok = r / G, head = static_cast<int64_t>(h) * G + r % G;
-    uint16_t* p = a.out.p + b * a.out.sb + tok * a.out.ss + head * a.out.sh + kV * lane;
-#pragma unroll
-    for (int i = 0; i < kV; i += 2) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-      *reinterpret_cast<uint32_t*>(p + i) = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    if (a.lse != nullptr && lane == 0)
-      a.lse[(b * a.H + head) * a.T + tok] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = acc[v];
+  if (lane == 0) ml_s[warp] = make_float2(top, sum);
+  __syncthreads();
+  if (r >= R || warp % kJoinParts != 0) return;
+  float all = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kJoinParts; ++w) all = fmaxf(all, ml_s[warp + w].x);
+  const float ref = all == -INFINITY ? 0.0f : all;
+  sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc[v] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinParts; ++w) {
+    const float wt = ex2(ml_s[warp + w].x - ref);
+    sum = fmaf(ml_s[warp + w].y, wt, sum);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[v]);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int tok = r / G, head = item.z * G + r - tok * G;
+  uint16_t* p = a.out.p + item.y * a.out.sb + tok * a.out.ss + head * a.out.sh + kV * lane;
+#pragma unroll
+  for (int i = 0; i < kV; i += 2) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(p + i) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  if (a.lse != nullptr && lane == 0)
+    a.lse[(static_cast<int64_t>(item.y) * a.H + head) * a.T + tok] =
+        sum == 0.0f ? -INFINITY : (all + log2f(sum)) * kLn2;
 }
 
 // -------------------------------------------------------------- many rows --
@@ -681,42 +773,39 @@ __global__ void __launch_bounds__(kRowThreads) cache_attention_kernel(CacheAtten
     a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + t] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-int decode_ctas(const CacheAttentionArgs& a) {
-  // a CTA for every 8 blocks that the tables can name (one per warp), at most one per SM
-  const int64_t blocks = a.B * a.c.H * (table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock);
-  const int sms = sm_count_current();
-  const int64_t most = sms < kMaxCtas ? sms : kMaxCtas, want = div_up(blocks, kWarps);
-  return static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
-}
-
 template <int D, int MT>
 cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
   using L = Dec<D, MT>;
-  const int ctas = decode_ctas(a);
+  // a CTA for every 4 blocks that the tables can name (one per warp), at most what the SMs hold
+  const int64_t blocks = a.B * a.c.H * (table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock);
+  const int sms = sm_count_current() < kMaxSms ? sm_count_current() : kMaxSms;
+  const int64_t most = static_cast<int64_t>(sms) * L::kCtasPerSm, want = div_up(blocks, kWarps);
+  const unsigned ctas = static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most));
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(cache_decode_kernel<D, MT>), L::kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT>, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.c.H), static_cast<unsigned>(a.B));
+  if ((e = cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT>, a)) != cudaSuccess || ctas == 1) return e;
+  cfg.gridDim = dim3(ctas, static_cast<unsigned>(div_up(a.T * (a.H / a.c.H), kJoinRows)));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, MT>, a, ctas);
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, MT>, a);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace_bytes(int64_t, int64_t T, int64_t H, int64_t Hkv, int64_t D) {
   const int64_t rows = T * (H / Hkv);
-  if (rows <= 16) return size_t(kMaxCtas) * 2 * (D == 128 ? Dec<128, 1>::kSlot : Dec<64, 1>::kSlot) * 4;
-  if (rows <= 32) return size_t(kMaxCtas) * 2 * (D == 128 ? Dec<128, 2>::kSlot : Dec<64, 2>::kSlot) * 4;
+  if (rows <= 16) return D == 128 ? Dec<128, 1>::kWorkspace : Dec<64, 1>::kWorkspace;
+  if (rows <= 32) return D == 128 ? Dec<128, 2>::kWorkspace : Dec<64, 2>::kWorkspace;
   return 0;
 }
 
