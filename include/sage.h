@@ -403,20 +403,22 @@ typedef struct sage_cache {
   int64_t num_pages, page_size, H, D;
 } sage_cache;
 
-/* Page table of B sequences: int32 rows of max_pages entries, row_stride
- * elements apart. Entries past a sequence's length are not read.
+/* Page tables, here table_dev, table_stride, max_pages: int32 rows of
+ * max_pages entries, table_stride elements apart, one row for each sequence.
+ * Entries past a sequence's length are not read.
  *
  * What is in device memory (table entries, lengths, starts, counts, page
  * lists) cannot be checked before the call returns. The kernels check it
  * before they use it: a length or count that is negative or reaches past the
  * table (or past T) is cut to what is there, a page number outside the cache
  * is taken as a page without tokens, and the device error word is set
- * (sage_device_error then reports SAGE_ERR_DEVICE_PAGE). */
-typedef struct sage_page_table {
-  const int32_t* table_dev;
-  int64_t row_stride;
-  int64_t max_pages;
-} sage_page_table;
+ * (sage_device_error then reports SAGE_ERR_DEVICE_PAGE).
+ *
+ * The calls on tokens take their arguments in one struct, which is read before
+ * the call returns and not kept: a caller with many calls of one shape keeps a
+ * filled one and changes the pointers. Tensors are (B, T, heads, D) BF16 with
+ * element strides stride_b, stride_s, stride_h (multiples of 8) and channel
+ * stride 1, 16-byte aligned. */
 
 /* Bytes of one cache, each array starting on a 256-byte boundary in the order
  * of sage_cache's fields. With base_dev (256-byte aligned, at least *bytes
@@ -445,17 +447,35 @@ SAGE_API int sage_cache_size(int64_t num_pages, int64_t page_size, int64_t H, in
  * it before the call, for finer codes.
  * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, TOO_LARGE, ARCH, CUDA; on the
  * device DEVICE_PAGE. */
-SAGE_API int sage_cache_append(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
-                               const int32_t* counts_dev, const sage_bf16_tensor* k, const sage_bf16_tensor* v,
-                               int64_t B, int64_t T, void* cuda_stream);
+typedef struct sage_cache_append_args {
+  const sage_cache* cache;
+  const int32_t* table_dev;
+  int64_t table_stride, max_pages;
+  const int32_t* starts_dev;
+  const int32_t* counts_dev;
+  sage_bf16_tensor k, v;
+  int64_t B, T;
+  void* cuda_stream;
+} sage_cache_append_args;
+SAGE_API int sage_cache_append(const sage_cache_append_args* args);
 
 /* Reads tokens starts[b] .. starts[b] + counts[b] - 1 of each sequence back as
- * BF16(code * scale) into (B, T, H, D) outputs with element strides (b, s, h)
- * and channel stride 1; rows counts[b] and up are left as they were. counts
- * NULL: T tokens each. Errors: as sage_cache_append. */
-SAGE_API int sage_cache_read(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
-                             const int32_t* counts_dev, int64_t B, int64_t T, void* k_dev, int64_t kb, int64_t ks,
-                             int64_t kh, void* v_dev, int64_t vb, int64_t vs, int64_t vh, void* cuda_stream);
+ * BF16(code * scale) into (B, T, H, D) tensors; counts NULL: T tokens each.
+ * Rows counts[b] and up, and those of tokens on pages outside the cache, are
+ * left as they were, or with zero_rest != 0 set to 0.
+ * Errors: as sage_cache_append. */
+typedef struct sage_cache_read_args {
+  const sage_cache* cache;
+  const int32_t* table_dev;
+  int64_t table_stride, max_pages;
+  const int32_t* starts_dev;
+  const int32_t* counts_dev;
+  sage_bf16_tensor k_out, v_out;   /* written */
+  int64_t B, T;
+  int32_t zero_rest;
+  void* cuda_stream;
+} sage_cache_read_args;
+SAGE_API int sage_cache_read(const sage_cache_read_args* args);
 
 /* Copies page src[i] to page dst[i] (codes and scales of all heads) for
  * i < n; src, dst: int32 [n] in device memory. An entry with dst < 0 or
@@ -479,7 +499,8 @@ SAGE_API int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H
  * over the tokens j < lengths[b] of the cache, or with is_causal those with
  * j <= lengths[b] - q_lengths[b] + t: the queries are the sequence's last
  * tokens, whose keys were appended before. A row that sees no token gets
- * out = 0 and lse = -inf. Rows q_lengths[b] and up are left as they were.
+ * out = 0 and lse = -inf. Rows q_lengths[b] and up are left as they were, or
+ * with zero_rest != 0 set to out = 0 and lse = -inf.
  * lengths, q_lengths: int32 [B]; q_lengths NULL: T each. q, out: BF16
  * (B, T, H, D), H a multiple of cache->H; lse_dev: fp32 [B][H][T] or NULL.
  * sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
@@ -489,11 +510,24 @@ SAGE_API int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H
  * (TOO_LARGE). Scales are not negative (sage_cache_append writes none).
  * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,
  * CUDA; on the device DEVICE_PAGE. */
-SAGE_API int sage_cache_attention(const sage_cache* cache, const sage_page_table* pages, const int32_t* lengths_dev,
-                                  const int32_t* q_lengths_dev, const sage_bf16_tensor* q, int64_t B, int64_t T,
-                                  int64_t H, float sm_scale, int is_causal, void* out_dev, int64_t ob, int64_t os,
-                                  int64_t oh, float* lse_dev, void* workspace_dev, size_t workspace_bytes,
-                                  void* cuda_stream);
+typedef struct sage_cache_attention_args {
+  const sage_cache* cache;
+  const int32_t* table_dev;
+  int64_t table_stride, max_pages;
+  const int32_t* lengths_dev;
+  const int32_t* q_lengths_dev;
+  sage_bf16_tensor q;
+  sage_bf16_tensor out;            /* written */
+  int64_t B, T, H;
+  float sm_scale;
+  int32_t is_causal;
+  int32_t zero_rest;
+  float* lse_dev;
+  void* workspace_dev;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} sage_cache_attention_args;
+SAGE_API int sage_cache_attention(const sage_cache_attention_args* args);
 
 /* ---------------------------------------------------------- diagnostics -- */
 

@@ -45,9 +45,28 @@ class Cache(ctypes.Structure):
                 ("num_pages", c_i64), ("page_size", c_i64), ("H", c_i64), ("D", c_i64)]
 
 
-class PageTable(ctypes.Structure):
-    """sage_page_table"""
-    _fields_ = [("table_dev", c_vp), ("row_stride", c_i64), ("max_pages", c_i64)]
+_TABLE_FIELDS = [("cache", c_vp), ("table_dev", c_vp), ("table_stride", c_i64), ("max_pages", c_i64)]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """sage_cache_append_args"""
+    _fields_ = _TABLE_FIELDS + [("starts_dev", c_vp), ("counts_dev", c_vp), ("k", Bf16Tensor), ("v", Bf16Tensor),
+                                ("B", c_i64), ("T", c_i64), ("cuda_stream", c_vp)]
+
+
+class CacheReadArgs(ctypes.Structure):
+    """sage_cache_read_args"""
+    _fields_ = _TABLE_FIELDS + [("starts_dev", c_vp), ("counts_dev", c_vp), ("k_out", Bf16Tensor),
+                                ("v_out", Bf16Tensor), ("B", c_i64), ("T", c_i64), ("zero_rest", ctypes.c_int32),
+                                ("cuda_stream", c_vp)]
+
+
+class CacheAttentionArgs(ctypes.Structure):
+    """sage_cache_attention_args"""
+    _fields_ = _TABLE_FIELDS + [("lengths_dev", c_vp), ("q_lengths_dev", c_vp), ("q", Bf16Tensor), ("out", Bf16Tensor),
+                                ("B", c_i64), ("T", c_i64), ("H", c_i64), ("sm_scale", ctypes.c_float),
+                                ("is_causal", ctypes.c_int32), ("zero_rest", ctypes.c_int32), ("lse_dev", c_vp),
+                                ("workspace_dev", c_vp), ("workspace_bytes", ctypes.c_size_t), ("cuda_stream", c_vp)]
 
 
 _SIGNATURES = {
@@ -78,15 +97,11 @@ _SIGNATURES = {
     "sage_sageattn_host": (c_int, [c_vp, c_vp, c_vp, I64x4, c_int, ctypes.c_char_p, c_int, ctypes.c_float, c_int, c_vp,
                                    c_int, c_vp, ctypes.c_size_t, c_vp]),
     "sage_cache_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p, c_vp, ctypes.POINTER(Cache)]),
-    "sage_cache_append": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp,
-                                  ctypes.POINTER(Bf16Tensor), ctypes.POINTER(Bf16Tensor), c_i64, c_i64, c_vp]),
-    "sage_cache_read": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp, c_i64, c_i64, c_vp,
-                                c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp]),
-    "sage_cache_copy_pages": (c_int, [ctypes.POINTER(Cache), c_vp, c_vp, c_i64, c_vp]),
+    "sage_cache_append": (c_int, [ctypes.POINTER(CacheAppendArgs)]),
+    "sage_cache_read": (c_int, [ctypes.POINTER(CacheReadArgs)]),
+    "sage_cache_copy_pages": (c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
     "sage_cache_attention_workspace_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_size_p]),
-    "sage_cache_attention": (c_int, [ctypes.POINTER(Cache), ctypes.POINTER(PageTable), c_vp, c_vp,
-                                     ctypes.POINTER(Bf16Tensor), c_i64, c_i64, c_i64, ctypes.c_float, c_int, c_vp,
-                                     c_i64, c_i64, c_i64, c_vp, c_vp, ctypes.c_size_t, c_vp]),
+    "sage_cache_attention": (c_int, [ctypes.POINTER(CacheAttentionArgs)]),
     "sage_device_error": (c_int, [c_vp, ctypes.POINTER(c_int)]),
     "sage_selftest_wait_timeout": (c_int, [c_vp]),
     "sage_strerror": (ctypes.c_char_p, [c_int]),

@@ -23,7 +23,8 @@ from dataclasses import dataclass, field
 import torch
 
 from . import _lib
-from .api import (_LAYOUTS, SAGE_ERR_LAYOUT, SAGE_ERR_SHAPE, SageError, _check, _stream_handle, _workspace)
+from .api import (_LAYOUTS, SAGE_ERR_LAYOUT, SAGE_ERR_SHAPE, SageError, _check, _get_device, _stream_handle, _tls,
+                  _workspace)
 
 SAGE_ERR_DTYPE = -3
 SAGE_ERR_DEVICE_PAGE = -16
@@ -44,6 +45,8 @@ class QuantizedCache:
     H: int = field(init=False)
     D: int = field(init=False)
     c: _lib.Cache = field(init=False, repr=False)
+    address: int = field(init=False, repr=False)   # of c, which lives as long as the object
+    signature: tuple = field(init=False, repr=False)
 
     def __post_init__(self):
         ts = (self.k_codes, self.v_codes, self.k_scale, self.v_scale)
@@ -67,7 +70,9 @@ class QuantizedCache:
         _check(_lib.load().sage_cache_size(P, n * BLOCK, H, D, ctypes.byref(ctypes.c_size_t(0)), None, None))
         for name, value in (("num_pages", P), ("page_size", n * BLOCK), ("H", H), ("D", D)):
             object.__setattr__(self, name, value)
-        object.__setattr__(self, "c", _lib.Cache(*(t.data_ptr() for t in ts), P, n * BLOCK, H, D))
+        c = _lib.Cache(*(t.data_ptr() or 16 for t in ts), P, n * BLOCK, H, D)  # an empty array has no address
+        for name, value in (("c", c), ("address", ctypes.addressof(c)), ("signature", (P, n, H, D, self.k_codes.get_device()))):
+            object.__setattr__(self, name, value)
 
     @property
     def device(self) -> torch.device:
@@ -95,7 +100,7 @@ class _on:
         self.index, self.ctx = index, None
 
     def __enter__(self):
-        if self.index != torch.cuda.current_device():
+        if self.index != _get_device():
             self.ctx = torch.cuda.device(self.index)
             self.ctx.__enter__()
         return _stream_handle(self.index)
@@ -103,6 +108,29 @@ class _on:
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+
+# A call whose shapes, strides, types, devices and flags this thread has seen
+# before skips the checks: the thread keeps one filled argument struct for each
+# such signature and changes only the pointers (answering token by token, a
+# call's host work counts). Per thread, so that no other thread rewrites a struct
+# while the library reads it. Calls that give out or workspace go the full way.
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _kept(key):
+    calls = getattr(_tls, "cache_calls", None)
+    return None if calls is None else calls.get(key)
+
+
+def _keep(key, value):
+    calls = getattr(_tls, "cache_calls", None)
+    if calls is None or len(calls) > 256:
+        calls = _tls.cache_calls = {}
+    calls[key] = value
 
 
 def _ints(t, n: int | None, cache: QuantizedCache, what: str):
@@ -122,7 +150,8 @@ def _ints(t, n: int | None, cache: QuantizedCache, what: str):
     return t.data_ptr()
 
 
-def _table(t, B: int, cache: QuantizedCache) -> _lib.PageTable:
+def _table(t, B: int, cache: QuantizedCache):
+    """(address, row stride, entries of a row) of an int32 [B, max_pages] page table."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("page_table must be a torch tensor")
     if t.device != cache.k_codes.device:
@@ -135,11 +164,11 @@ def _table(t, B: int, cache: QuantizedCache) -> _lib.PageTable:
     if n > 1 and t.stride(1) != 1:
         raise SageError(SAGE_ERR_LAYOUT, "the page table's rows must be contiguous")
     # an empty table has no address: any aligned one does, it is not read
-    return _lib.PageTable(t.data_ptr() or cache.k_codes.data_ptr(), t.stride(0) if n else 0, n)
+    return t.data_ptr() or cache.address, t.stride(0) if n else 0, n
 
 
 def _tokens(t, cache: QuantizedCache, layout: str, what: str):
-    """(B, T, heads) and (pointer, strides) of a BF16 [B, T, heads, D] tensor (or [B, heads, T, D])."""
+    """(B, T, heads) and the C tensor of a BF16 [B, T, heads, D] tensor (or [B, heads, T, D])."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected torch tensors")
     if not t.is_cuda:
@@ -154,11 +183,9 @@ def _tokens(t, cache: QuantizedCache, layout: str, what: str):
     if st[3] != 1:
         raise SageError(SAGE_ERR_LAYOUT, "the channel stride must be 1")
     sh = t.shape
-    # an empty tensor has no address: it is not read
-    ptr = t.data_ptr() or cache.k_codes.data_ptr()
     if layout == "NHD":
-        return (sh[0], sh[1], sh[2]), (ptr, st[0], st[1], st[2])
-    return (sh[0], sh[2], sh[1]), (ptr, st[0], st[2], st[1])
+        return (sh[0], sh[1], sh[2]), _lib.Bf16Tensor(t.data_ptr(), st[0], st[1], st[2])
+    return (sh[0], sh[2], sh[1]), _lib.Bf16Tensor(t.data_ptr(), st[0], st[2], st[1])
 
 
 def _check_layout(layout: str):
@@ -178,6 +205,23 @@ def cache_append(cache: QuantizedCache, k, v, page_table, starts, counts=None, t
     with its tokens; older codes of the block are then rounded again. Tokens behind the
     last new one in its block are lost, so a sequence may be cut back and written on.
     The pages written must belong to one sequence only."""
+    try:
+        key = ("append", cache.signature, _meta(k), _meta(v), _meta(page_table), _meta(starts), _meta(counts), tensor_layout)
+        kept = _kept(key)
+    except (AttributeError, TypeError):
+        key = kept = None
+    if kept is not None and kept[2] == _get_device():
+        args, ref, index = kept
+        args.cache = cache.address
+        args.table_dev = page_table.data_ptr()
+        args.starts_dev = starts.data_ptr()
+        if counts is not None:
+            args.counts_dev = counts.data_ptr()
+        args.k.ptr_dev = k.data_ptr()
+        args.v.ptr_dev = v.data_ptr()
+        args.cuda_stream = _stream_handle(index)
+        _check(_lib.load().sage_cache_append(ref))
+        return
     _check_cache(cache)
     _check_layout(tensor_layout)
     (B, T, H), ki = _tokens(k, cache, tensor_layout, "k")
@@ -188,17 +232,42 @@ def cache_append(cache: QuantizedCache, k, v, page_table, starts, counts=None, t
     if starts is None:
         raise TypeError("starts must be a torch tensor")
     st, ct = _ints(starts, B, cache, "starts"), _ints(counts, B, cache, "counts")
-    if B == 0:
+    if k.numel() == 0:
         return
-    with _on(cache.k_codes.get_device()) as stream:
-        _check(_lib.load().sage_cache_append(cache.c, table, st, ct, _lib.Bf16Tensor(*ki), _lib.Bf16Tensor(*vi), B, T,
-                                             stream))
+    index = cache.k_codes.get_device()
+    args = _lib.CacheAppendArgs(cache.address, *table, st, ct, ki, vi, B, T)
+    with _on(index) as stream:
+        args.cuda_stream = stream
+        _check(_lib.load().sage_cache_append(ctypes.byref(args)))
+    if key is not None and table[2]:
+        _keep(key, (args, ctypes.byref(args), index))
 
 
 def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, tensor_layout: str = "NHD", out=None):
     """Reads tokens starts[b] .. starts[b] + counts[b] - 1 of each sequence back as BF16
     (sage_cache_read); counts None: T tokens each. Returns (k, v), each [B, T, H, D];
     rows counts[b] and up are 0, or left as they were in the tensors given as out."""
+    kept = key = None
+    if out is None:
+        try:
+            key = ("read", cache.signature, T, _meta(page_table), _meta(starts), _meta(counts), tensor_layout)
+            kept = _kept(key)
+        except (AttributeError, TypeError):
+            key = None
+    if kept is not None and kept[2] == _get_device():
+        args, ref, index, shape = kept
+        both = torch.empty(shape, dtype=torch.bfloat16, device=page_table.device)
+        args.cache = cache.address
+        args.table_dev = page_table.data_ptr()
+        args.starts_dev = starts.data_ptr()
+        if counts is not None:
+            args.counts_dev = counts.data_ptr()
+        k, v = both.unbind(0)
+        args.k_out.ptr_dev = k.data_ptr()
+        args.v_out.ptr_dev = v.data_ptr()
+        args.cuda_stream = _stream_handle(index)
+        _check(_lib.load().sage_cache_read(ref))
+        return k, v
     _check_cache(cache)
     _check_layout(tensor_layout)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
@@ -210,21 +279,24 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
     if starts is None:
         raise TypeError("starts must be a torch tensor")
     st, ct = _ints(starts, B, cache, "starts"), _ints(counts, B, cache, "counts")
-    device = cache.k_codes.device
+    shape = (2, B, T, cache.H, cache.D) if tensor_layout == "NHD" else (2, B, cache.H, T, cache.D)
+    zero_rest = out is None
     if out is None:
-        shape = (B, T, cache.H, cache.D) if tensor_layout == "NHD" else (B, cache.H, T, cache.D)
-        if counts is None:
-            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in (0, 1))
-        else:
-            out = tuple(torch.zeros((2,) + shape, dtype=torch.bfloat16, device=device))
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device).unbind(0)
     k, v = out
     ks, ko = _tokens(k, cache, tensor_layout, "out")
     vs, vo = _tokens(v, cache, tensor_layout, "out")
     if ks != (B, T, cache.H) or vs != ks:
         raise SageError(SAGE_ERR_SHAPE, "out must be two tensors [B, T, H, D]")
-    if B:
-        with _on(cache.k_codes.get_device()) as stream:
-            _check(_lib.load().sage_cache_read(cache.c, table, st, ct, B, T, *ko, *vo, stream))
+    if k.numel() == 0:
+        return k, v
+    index = cache.k_codes.get_device()
+    args = _lib.CacheReadArgs(cache.address, *table, st, ct, ko, vo, B, T, zero_rest)
+    with _on(index) as stream:
+        args.cuda_stream = stream
+        _check(_lib.load().sage_cache_read(ctypes.byref(args)))
+    if key is not None and table[2]:
+        _keep(key, (args, ctypes.byref(args), index, shape))
     return k, v
 
 
@@ -243,7 +315,18 @@ def cache_copy_pages(cache: QuantizedCache, src, dst) -> None:
     if n == 0:
         return
     with _on(cache.k_codes.get_device()) as stream:
-        _check(_lib.load().sage_cache_copy_pages(cache.c, s, d, n, stream))
+        _check(_lib.load().sage_cache_copy_pages(cache.address, s, d, n, stream))
+
+
+_NAN = float("nan")
+
+
+def _call_workspace(device, stream: int, need: int) -> torch.Tensor:
+    """The thread's workspace for its calls on this stream, or one from the captured graph's
+    memory pool: a replay may run beside other calls."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    return _workspace(device, stream, need)
 
 
 def cache_attention_workspace_size(B: int, T: int, H: int, H_kv: int, D: int = 128) -> int:
@@ -266,6 +349,39 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
     workspace: a uint8 tensor of cache_attention_workspace_size bytes that no other call
     uses at the same time; None: the library's own, one for each thread and stream (a
     captured graph gets its own from its memory pool)."""
+    kept = key = None
+    if out is None and workspace is None:
+        try:
+            key = ("attention", cache.signature, _meta(q), _meta(page_table), _meta(lengths), _meta(q_lengths),
+                   bool(is_causal), bool(return_lse), tensor_layout)
+            kept = _kept(key)
+        except (AttributeError, TypeError):
+            key = None
+    if kept is not None and kept[2] == _get_device():
+        args, ref, index, shape, lse_shape, need = kept
+        device = q.device
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        stream = _stream_handle(index)
+        args.cache = cache.address
+        args.table_dev = page_table.data_ptr()
+        args.lengths_dev = lengths.data_ptr()
+        if q_lengths is not None:
+            args.q_lengths_dev = q_lengths.data_ptr()
+        args.q.ptr_dev = q.data_ptr()
+        args.out.ptr_dev = out.data_ptr()
+        args.sm_scale = _NAN if sm_scale is None else float(sm_scale)
+        if need:
+            workspace = _call_workspace(device, stream, need)
+            args.workspace_dev = workspace.data_ptr()
+            args.workspace_bytes = need
+        args.cuda_stream = stream
+        if return_lse:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
+            args.lse_dev = lse.data_ptr()
+            _check(_lib.load().sage_cache_attention(ref))
+            return out, lse
+        _check(_lib.load().sage_cache_attention(ref))
+        return out
     _check_cache(cache)
     _check_layout(tensor_layout)
     (B, T, H), qi = _tokens(q, cache, tensor_layout, "q")
@@ -277,33 +393,41 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
         raise TypeError("lengths must be a torch tensor")
     lens, q_lens = _ints(lengths, B, cache, "lengths"), _ints(q_lengths, B, cache, "q_lengths")
     device = cache.k_codes.device
+    zero_rest = out is None
     if out is None:
-        make = torch.empty if q_lengths is None else torch.zeros
-        out = make(q.shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
     shape, oi = _tokens(out, cache, tensor_layout, "out")
     if shape != (B, T, H):
         raise SageError(SAGE_ERR_SHAPE, "out must have q's shape")
+    # with a given out, padding rows of the log-sum-exp are -inf all the same
     lse = None
     if return_lse:
-        if q_lengths is None:
+        if zero_rest or q_lengths is None:
             lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
         else:
             lse = torch.full((B, H, T), float("-inf"), dtype=torch.float32, device=device)
     if out.numel() == 0:
         return (out, lse) if return_lse else out
-    lib = _lib.load()
-    with _on(cache.k_codes.get_device()) as stream:
-        n = cache_attention_workspace_size(B, T, H, Hkv, cache.D)
-        if workspace is None and n:
-            if torch.cuda.is_current_stream_capturing():
-                workspace = torch.empty(n, dtype=torch.uint8, device=device)
-            else:
-                workspace = _workspace(device, stream, n)
-        elif workspace is not None and workspace.device != device:
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch tensor")
+        if workspace.device != device:
             raise ValueError("workspace must live on the cache's device")
-        _check(lib.sage_cache_attention(
-            cache.c, table, lens, q_lens, _lib.Bf16Tensor(*qi), B, T, H,
-            float("nan") if sm_scale is None else float(sm_scale), bool(is_causal), *oi,
-            lse.data_ptr() if return_lse else None, workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, stream))
+        if not workspace.is_contiguous():
+            raise SageError(SAGE_ERR_LAYOUT, "workspace must be contiguous")
+    index = cache.k_codes.get_device()
+    need = cache_attention_workspace_size(B, T, H, Hkv, cache.D)
+    args = _lib.CacheAttentionArgs(cache.address, *table, lens, q_lens, qi, oi, B, T, H,
+                                   _NAN if sm_scale is None else float(sm_scale), bool(is_causal), zero_rest,
+                                   lse.data_ptr() if return_lse else None)
+    with _on(index) as stream:
+        if workspace is None and need:
+            workspace = _call_workspace(device, stream, need)
+        if workspace is not None:
+            args.workspace_dev = workspace.data_ptr()
+            args.workspace_bytes = workspace.numel() * workspace.element_size()
+        args.cuda_stream = stream
+        _check(_lib.load().sage_cache_attention(ctypes.byref(args)))
+    if key is not None and table[2]:
+        _keep(key, (args, ctypes.byref(args), index, q.shape, (B, H, T), need))
     return (out, lse) if return_lse else out

@@ -91,6 +91,7 @@ struct CacheAttentionArgs {
   int64_t B, T;
   int32_t H;                 // query heads
   bool causal;
+  bool zero_rest;            // rows past q_lengths become 0 and -inf
   float sm_log2;             // sm_scale * log2(e)
   int* dev_err;
 };
@@ -100,8 +101,8 @@ cudaError_t launch_cache_append(const CacheView& c, int64_t D, const PageTable& 
                                 const int32_t* counts, const Bf16In& k, const Bf16In& v, int64_t B, int64_t T,
                                 int* dev_err, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
-                              const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T, int* dev_err,
-                              cudaStream_t stream);
+                              const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T,
+                              bool zero_rest, int* dev_err, cudaStream_t stream);
 cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t* src, const int32_t* dst, int64_t n,
                                     int* dev_err, cudaStream_t stream);
 size_t cache_attention_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t D);

@@ -43,11 +43,11 @@ int check_cache(const sage_cache* c, CacheView* view) {
   return SAGE_OK;
 }
 
-int check_table(const sage_page_table* t, PageTable* out) {
-  if (t == nullptr || t->table_dev == nullptr) return SAGE_ERR_NULLPTR;
-  if (!aligned(t->table_dev, 4)) return SAGE_ERR_ALIGN;
-  if (t->max_pages < 0 || t->row_stride < 0) return SAGE_ERR_SHAPE;
-  *out = PageTable{t->table_dev, t->row_stride, t->max_pages};
+int check_table(const int32_t* table, int64_t stride, int64_t max_pages, PageTable* out) {
+  if (table == nullptr) return SAGE_ERR_NULLPTR;
+  if (!aligned(table, 4)) return SAGE_ERR_ALIGN;
+  if (max_pages < 0 || stride < 0) return SAGE_ERR_SHAPE;
+  *out = PageTable{table, stride, max_pages};
   return SAGE_OK;
 }
 
@@ -56,19 +56,19 @@ int check_ints(const int32_t* p, bool needed) {
   return aligned(p, 4) ? SAGE_OK : SAGE_ERR_ALIGN;
 }
 
-int check_in(const sage_bf16_tensor* t, Bf16In* out) {
-  if (t == nullptr || t->ptr_dev == nullptr) return SAGE_ERR_NULLPTR;
-  if (!aligned(t->ptr_dev, 16) || !stride_ok(t->stride_b) || !stride_ok(t->stride_s) || !stride_ok(t->stride_h))
-    return SAGE_ERR_ALIGN;
-  *out = Bf16In{static_cast<const uint16_t*>(t->ptr_dev), t->stride_b, t->stride_s, t->stride_h};
-  return SAGE_OK;
+int check_tensor(const sage_bf16_tensor& t) {
+  if (t.ptr_dev == nullptr) return SAGE_ERR_NULLPTR;
+  return aligned(t.ptr_dev, 16) && stride_ok(t.stride_b) && stride_ok(t.stride_s) && stride_ok(t.stride_h)
+             ? SAGE_OK
+             : SAGE_ERR_ALIGN;
 }
 
-int check_out(void* p, int64_t ob, int64_t os, int64_t oh, Out* out) {
-  if (p == nullptr) return SAGE_ERR_NULLPTR;
-  if (!aligned(p, 16) || !stride_ok(ob) || !stride_ok(os) || !stride_ok(oh)) return SAGE_ERR_ALIGN;
-  *out = Out{static_cast<uint16_t*>(p), ob, os, oh};
-  return SAGE_OK;
+Bf16In to_in(const sage_bf16_tensor& t) {
+  return Bf16In{static_cast<const uint16_t*>(t.ptr_dev), t.stride_b, t.stride_s, t.stride_h};
+}
+
+Out to_out(const sage_bf16_tensor& t) {
+  return Out{static_cast<uint16_t*>(const_cast<void*>(t.ptr_dev)), t.stride_b, t.stride_s, t.stride_h};
 }
 
 int check_batch(int64_t B, int64_t T) {
@@ -114,42 +114,40 @@ int sage_cache_size(int64_t num_pages, int64_t page_size, int64_t H, int64_t D, 
   return SAGE_OK;
 }
 
-int sage_cache_append(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
-                      const int32_t* counts_dev, const sage_bf16_tensor* k, const sage_bf16_tensor* v, int64_t B,
-                      int64_t T, void* cuda_stream) {
+int sage_cache_append(const sage_cache_append_args* args) {
+  if (args == nullptr) return SAGE_ERR_NULLPTR;
   CacheView c;
   PageTable pt;
-  Bf16In ki, vi;
   int rc;
-  if ((rc = check_cache(cache, &c)) != SAGE_OK || (rc = check_batch(B, T)) != SAGE_OK ||
-      (rc = check_table(pages, &pt)) != SAGE_OK || (rc = check_ints(starts_dev, true)) != SAGE_OK ||
-      (rc = check_ints(counts_dev, false)) != SAGE_OK || (rc = check_in(k, &ki)) != SAGE_OK ||
-      (rc = check_in(v, &vi)) != SAGE_OK)
+  if ((rc = check_cache(args->cache, &c)) != SAGE_OK || (rc = check_batch(args->B, args->T)) != SAGE_OK ||
+      (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &pt)) != SAGE_OK ||
+      (rc = check_ints(args->starts_dev, true)) != SAGE_OK || (rc = check_ints(args->counts_dev, false)) != SAGE_OK ||
+      (rc = check_tensor(args->k)) != SAGE_OK || (rc = check_tensor(args->v)) != SAGE_OK)
     return rc;
   int* dev_err = nullptr;
   if ((rc = device_error_word(&dev_err)) != SAGE_OK) return rc;
-  if (B == 0 || T == 0 || c.H == 0) return SAGE_OK;
-  return cuda_status(launch_cache_append(c, cache->D, pt, starts_dev, counts_dev, ki, vi, B, T, dev_err,
-                                         static_cast<cudaStream_t>(cuda_stream)));
+  if (args->B == 0 || args->T == 0 || c.H == 0) return SAGE_OK;
+  return cuda_status(launch_cache_append(c, args->cache->D, pt, args->starts_dev, args->counts_dev, to_in(args->k),
+                                         to_in(args->v), args->B, args->T, dev_err,
+                                         static_cast<cudaStream_t>(args->cuda_stream)));
 }
 
-int sage_cache_read(const sage_cache* cache, const sage_page_table* pages, const int32_t* starts_dev,
-                    const int32_t* counts_dev, int64_t B, int64_t T, void* k_dev, int64_t kb, int64_t ks, int64_t kh,
-                    void* v_dev, int64_t vb, int64_t vs, int64_t vh, void* cuda_stream) {
+int sage_cache_read(const sage_cache_read_args* args) {
+  if (args == nullptr) return SAGE_ERR_NULLPTR;
   CacheView c;
   PageTable pt;
-  Out ko, vo;
   int rc;
-  if ((rc = check_cache(cache, &c)) != SAGE_OK || (rc = check_batch(B, T)) != SAGE_OK ||
-      (rc = check_table(pages, &pt)) != SAGE_OK || (rc = check_ints(starts_dev, true)) != SAGE_OK ||
-      (rc = check_ints(counts_dev, false)) != SAGE_OK || (rc = check_out(k_dev, kb, ks, kh, &ko)) != SAGE_OK ||
-      (rc = check_out(v_dev, vb, vs, vh, &vo)) != SAGE_OK)
+  if ((rc = check_cache(args->cache, &c)) != SAGE_OK || (rc = check_batch(args->B, args->T)) != SAGE_OK ||
+      (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &pt)) != SAGE_OK ||
+      (rc = check_ints(args->starts_dev, true)) != SAGE_OK || (rc = check_ints(args->counts_dev, false)) != SAGE_OK ||
+      (rc = check_tensor(args->k_out)) != SAGE_OK || (rc = check_tensor(args->v_out)) != SAGE_OK)
     return rc;
   int* dev_err = nullptr;
   if ((rc = device_error_word(&dev_err)) != SAGE_OK) return rc;
-  if (B == 0 || T == 0 || c.H == 0) return SAGE_OK;
-  return cuda_status(launch_cache_read(c, cache->D, pt, starts_dev, counts_dev, ko, vo, B, T, dev_err,
-                                       static_cast<cudaStream_t>(cuda_stream)));
+  if (args->B == 0 || args->T == 0 || c.H == 0) return SAGE_OK;
+  return cuda_status(launch_cache_read(c, args->cache->D, pt, args->starts_dev, args->counts_dev, to_out(args->k_out),
+                                       to_out(args->v_out), args->B, args->T, args->zero_rest != 0, dev_err,
+                                       static_cast<cudaStream_t>(args->cuda_stream)));
 }
 
 int sage_cache_copy_pages(const sage_cache* cache, const int32_t* src_dev, const int32_t* dst_dev, int64_t n,
@@ -177,41 +175,47 @@ int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H, int64_t
   return SAGE_OK;
 }
 
-int sage_cache_attention(const sage_cache* cache, const sage_page_table* pages, const int32_t* lengths_dev,
-                         const int32_t* q_lengths_dev, const sage_bf16_tensor* q, int64_t B, int64_t T, int64_t H,
-                         float sm_scale, int is_causal, void* out_dev, int64_t ob, int64_t os, int64_t oh,
-                         float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* cuda_stream) {
+int sage_cache_attention(const sage_cache_attention_args* args) {
+  if (args == nullptr) return SAGE_ERR_NULLPTR;
   CacheAttentionArgs a;
   int rc;
-  if ((rc = check_cache(cache, &a.c)) != SAGE_OK || (rc = check_batch(B, T)) != SAGE_OK ||
-      (rc = check_heads(H, a.c.H)) != SAGE_OK || (rc = check_table(pages, &a.pt)) != SAGE_OK ||
-      (rc = check_ints(lengths_dev, true)) != SAGE_OK || (rc = check_ints(q_lengths_dev, false)) != SAGE_OK ||
-      (rc = check_in(q, &a.q)) != SAGE_OK || (rc = check_out(out_dev, ob, os, oh, &a.out)) != SAGE_OK)
+  const int64_t B = args->B, T = args->T, H = args->H;
+  if ((rc = check_cache(args->cache, &a.c)) != SAGE_OK || (rc = check_batch(B, T)) != SAGE_OK ||
+      (rc = check_heads(H, a.c.H)) != SAGE_OK ||
+      (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &a.pt)) != SAGE_OK ||
+      (rc = check_ints(args->lengths_dev, true)) != SAGE_OK ||
+      (rc = check_ints(args->q_lengths_dev, false)) != SAGE_OK || (rc = check_tensor(args->q)) != SAGE_OK ||
+      (rc = check_tensor(args->out)) != SAGE_OK)
     return rc;
   // the call's blocks, all sequences and heads, are counted in 32 bits
   const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;
   if (B > 0 && a.c.H > 0 && seq_blocks > ((int64_t(1) << 31) - 1) / (B * a.c.H)) return SAGE_ERR_TOO_LARGE;
-  if (lse_dev != nullptr && !aligned(lse_dev, 4)) return SAGE_ERR_ALIGN;
-  if (!(std::isnan(sm_scale) || (std::isfinite(sm_scale) && sm_scale > 0.0f))) return SAGE_ERR_ARG;
-  const size_t need = (B == 0 || T == 0 || H == 0) ? 0 : cache_attention_workspace_bytes(B, T, H, a.c.H, cache->D);
+  if (args->lse_dev != nullptr && !aligned(args->lse_dev, 4)) return SAGE_ERR_ALIGN;
+  const float sm = args->sm_scale;
+  if (!(std::isnan(sm) || (std::isfinite(sm) && sm > 0.0f))) return SAGE_ERR_ARG;
+  const int64_t D = args->cache->D;
+  const size_t need = (B == 0 || T == 0 || H == 0) ? 0 : cache_attention_workspace_bytes(B, T, H, a.c.H, D);
   if (need > 0) {
-    if (workspace_dev == nullptr) return SAGE_ERR_NULLPTR;
-    if (!aligned(workspace_dev, 256)) return SAGE_ERR_ALIGN;
-    if (workspace_bytes < need) return SAGE_ERR_WORKSPACE;
+    if (args->workspace_dev == nullptr) return SAGE_ERR_NULLPTR;
+    if (!aligned(args->workspace_dev, 256)) return SAGE_ERR_ALIGN;
+    if (args->workspace_bytes < need) return SAGE_ERR_WORKSPACE;
   }
   if ((rc = device_error_word(&a.dev_err)) != SAGE_OK) return rc;
   if (B == 0 || T == 0 || H == 0) return SAGE_OK;
-  const double scale = std::isnan(sm_scale) ? 1.0 / std::sqrt(static_cast<double>(cache->D)) : sm_scale;
-  a.lengths = lengths_dev;
-  a.q_lengths = q_lengths_dev;
-  a.lse = lse_dev;
-  a.workspace = workspace_dev;
+  const double scale = std::isnan(sm) ? 1.0 / std::sqrt(static_cast<double>(D)) : sm;
+  a.lengths = args->lengths_dev;
+  a.q_lengths = args->q_lengths_dev;
+  a.q = to_in(args->q);
+  a.out = to_out(args->out);
+  a.lse = args->lse_dev;
+  a.workspace = args->workspace_dev;
   a.B = B;
   a.T = T;
   a.H = static_cast<int32_t>(H);
-  a.causal = is_causal != 0;
+  a.causal = args->is_causal != 0;
+  a.zero_rest = args->zero_rest != 0 && args->q_lengths_dev != nullptr;
   a.sm_log2 = static_cast<float>(scale * 1.4426950408889634);
-  return cuda_status(launch_cache_attention(a, cache->D, static_cast<cudaStream_t>(cuda_stream)));
+  return cuda_status(launch_cache_attention(a, D, static_cast<cudaStream_t>(args->cuda_stream)));
 }
 
 }  // extern "C"

@@ -539,6 +539,17 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         y += __shfl_xor_sync(0xffffffffu, y, 2);
         if (t == 0) ml[warp * 16 * MT + mt * 16 + e * 8 + g] = make_float2(m[mt][e], y);
       }
+    if (a.zero_rest && seg.blk == 0) {
+      // padding rows, by the CTA that has the item's first block
+      const int rest = (static_cast<int>(a.T) - seg.s.q_len) * G;
+      for (int x = threadIdx.x; x < rest * (D / 8); x += kThreads) {
+        const int r = R + x / (D / 8), tok = r / G, head = seg.h * G + r - tok * G;
+        *reinterpret_cast<uint4*>(a.out.p + seg.b * a.out.sb + tok * a.out.ss + head * a.out.sh + x % (D / 8) * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse != nullptr && x % (D / 8) == 0)
+          a.lse[(static_cast<int64_t>(seg.b) * a.H + head) * a.T + tok] = -INFINITY;
+      }
+    }
     const bool whole = n == seg.units;
     const int which = at == 0 ? 0 : 1;  // a partial item is the range's first or its last
     float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + L::kDesc) +
@@ -724,7 +735,13 @@ __global__ void __launch_bounds__(kRowThreads) cache_attention_kernel(CacheAtten
   const int64_t len = checked_length(a.lengths[b], table_capacity(a.pt.max_pages, a.c.blocks_per_page), &bad);
   const int64_t q_len = a.q_lengths != nullptr ? checked_length(a.q_lengths[b], a.T, &bad) : a.T;
   if (bad && i == 0) atomicExch(a.dev_err, kDevErrPage);
-  if (t >= q_len) return;
+  if (t >= q_len) {
+    if (a.zero_rest) {
+      if (i < D) a.out.p[b * a.out.sb + t * a.out.ss + h * a.out.sh + i] = 0;
+      if (a.lse != nullptr && i == 0) a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + t] = -INFINITY;
+    }
+    return;
+  }
   int64_t sees = a.causal ? len - q_len + t + 1 : len;
   if (sees < 0) sees = 0;
   const uint16_t* q = a.q.p + b * a.q.sb + t * a.q.ss + h * a.q.sh;

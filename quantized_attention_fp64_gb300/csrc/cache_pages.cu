@@ -183,13 +183,20 @@ __device__ __forceinline__ uint32_t to_bf16x2(float a, float b) {
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageTable pt, const int32_t* starts,
                                                               const int32_t* counts, Out k, Out v, int64_t T,
-                                                              int* dev_err) {
+                                                              bool zero_rest, int* dev_err) {
   constexpr int kCh = D / 4;
   __shared__ __align__(16) uint8_t vt[D * 36];
   const Span s = find_span(c, pt, starts, counts, T, dev_err);
-  if (s.slot < 0) return;
   const int half = threadIdx.x >> 7, i = threadIdx.x & 127;
   const int row = i >> 2, part = i & 3;
+  const Out& o = half ? v : k;
+  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + (s.t0 + row) * o.ss +
+                  static_cast<int64_t>(blockIdx.y) * o.sh + part * kCh;
+  if (zero_rest && row >= s.first && s.t0 + row < T && (row >= s.end || s.slot < 0)) {
+#pragma unroll
+    for (int q = 0; q < kCh / 8; ++q) reinterpret_cast<uint4*>(dst)[q] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (s.slot < 0) return;
   const float scale = (half ? c.vs : c.ks)[s.slot];
   const int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
   uint32_t codes[kCh / 4];
@@ -216,9 +223,6 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageT
       codes[q] = p[0] | (p[36] << 8) | (p[72] << 16) | (static_cast<uint32_t>(p[108]) << 24);
     }
   }
-  const Out& o = half ? v : k;
-  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + (s.t0 + row) * o.ss +
-                  static_cast<int64_t>(blockIdx.y) * o.sh + part * kCh;
   const int8_t* cb = reinterpret_cast<const int8_t*>(codes);
 #pragma unroll
   for (int q = 0; q < kCh / 8; ++q)
@@ -301,12 +305,12 @@ cudaError_t launch_cache_append(const CacheView& c, int64_t D, const PageTable& 
 }
 
 cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
-                              const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T, int* dev_err,
-                              cudaStream_t stream) {
+                              const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T,
+                              bool zero_rest, int* dev_err, cudaStream_t stream) {
   if (D == 128)
-    cache_read_kernel<128><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, dev_err);
+    cache_read_kernel<128><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, zero_rest, dev_err);
   else
-    cache_read_kernel<64><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, dev_err);
+    cache_read_kernel<64><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, zero_rest, dev_err);
   return cudaGetLastError();
 }
 

@@ -131,7 +131,7 @@ def _cache(**over):
 
 
 def _tab(ptr=0x50000, stride=4, n=4):
-    return _lib.PageTable(ptr, stride, n)
+    return ptr, stride, n
 
 
 BAD_CACHES = [(dict(D=96), HEAD_DIM), (dict(page=48), SHAPE), (dict(page=0), SHAPE), (dict(H=-1), SHAPE),
@@ -156,22 +156,27 @@ def test_cache_size(lib):
         assert lib.sage_cache_size(a["P"], a["page"], a["H"], a["D"], ctypes.byref(n), None, None) == code
 
 
+def _addr(struct):
+    return ctypes.cast(ctypes.pointer(struct), ctypes.c_void_p).value
+
+
 def _append(lib, cache=None, table=None, starts=0x60000, counts=None, k=None, v=None, B=2, T=4):
-    t = _lib.Bf16Tensor(0x70000, 1024, 256, 128)
-    return lib.sage_cache_append(cache or _cache(), table or _tab(), starts, counts, k or t, v or t, B, T, None)
+    t, cache = _lib.Bf16Tensor(0x70000, 1024, 256, 128), cache or _cache()
+    return lib.sage_cache_append(_lib.CacheAppendArgs(_addr(cache), *(table or _tab()), starts, counts, k or t, v or t, B, T,
+                                                      None))
 
 
 def _read(lib, cache=None, table=None, starts=0x60000, counts=None, k=None, v=None, B=2, T=4):
-    k, v = (x if x is not None else _lib.Bf16Tensor(0x70000, 1024, 256, 128) for x in (k, v))
-    return lib.sage_cache_read(cache or _cache(), table or _tab(), starts, counts, B, T, k.ptr_dev, k.stride_b,
-                               k.stride_s, k.stride_h, v.ptr_dev, v.stride_b, v.stride_s, v.stride_h, None)
+    t, cache = _lib.Bf16Tensor(0x70000, 1024, 256, 128), cache or _cache()
+    return lib.sage_cache_read(_lib.CacheReadArgs(_addr(cache), *(table or _tab()), starts, counts, k or t, v or t, B, T, 0,
+                                                  None))
 
 
 def _attend(lib, cache=None, table=None, starts=0x60000, counts=None, k=None, v=None, B=2, T=4, H=4, sm=0.1, lse=None,
             ws=0x90000, wsn=1 << 40):
-    k, v = (x if x is not None else _lib.Bf16Tensor(0x70000, 2048, 512, 128) for x in (k, v))
-    return lib.sage_cache_attention(cache or _cache(), table or _tab(), starts, counts, k, B, T, H, ctypes.c_float(sm), 1,
-                                    v.ptr_dev, v.stride_b, v.stride_s, v.stride_h, lse, ws, wsn, None)
+    t, cache = _lib.Bf16Tensor(0x70000, 2048, 512, 128), cache or _cache()
+    return lib.sage_cache_attention(_lib.CacheAttentionArgs(_addr(cache), *(table or _tab()), starts, counts, k or t, v or t,
+                                                            B, T, H, sm, 1, 0, lse, ws, wsn, None))
 
 
 @pytest.mark.parametrize("call", [_append, _read, _attend])
@@ -203,6 +208,10 @@ def test_refusals_of_attention(lib):
     for sm in (0.0, -1.0, math.inf):
         assert _attend(lib, sm=sm) == ARG
     assert _attend(lib, lse=0x80002) == ALIGN
+    # blocks of all sequences and heads are counted in 32 bits
+    assert _attend(lib, B=60000, table=_tab(n=1 << 20)) == TOO_LARGE
+    assert lib.sage_cache_attention(None) == NULLPTR and lib.sage_cache_append(None) == NULLPTR
+    assert lib.sage_cache_read(None) == NULLPTR
     n = ctypes.c_size_t(0)
     assert lib.sage_cache_attention_workspace_size(2, 4, 4, 2, 128, ctypes.byref(n)) == OK
     if n.value:
@@ -218,7 +227,8 @@ def test_refusals_of_attention(lib):
 
 def test_refusals_of_copy(lib):
     def copy(cache=None, src=0x50000, dst=0x60000, n=3):
-        return lib.sage_cache_copy_pages(cache or _cache(), src, dst, n, None)
+        cache = cache or _cache()
+        return lib.sage_cache_copy_pages(_addr(cache), src, dst, n, None)
 
     for over, code in BAD_CACHES:
         assert copy(cache=_cache(**over)) == code
@@ -232,7 +242,9 @@ def test_structs_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         pytest.skip("no host C compiler")
-    for struct, name in ((_lib.Cache, "sage_cache"), (_lib.PageTable, "sage_page_table")):
+    for struct, name in ((_lib.Cache, "sage_cache"), (_lib.CacheAppendArgs, "sage_cache_append_args"),
+                         (_lib.CacheReadArgs, "sage_cache_read_args"),
+                         (_lib.CacheAttentionArgs, "sage_cache_attention_args")):
         fields = [f[0] for f in struct._fields_]
         src = tmp_path / f"{name}.c"
         src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "sage.h"\nint main(void) {\n'
