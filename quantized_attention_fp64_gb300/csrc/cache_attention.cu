@@ -160,6 +160,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSms = 160;
+constexpr int kClusterBlocks = 8;  // blocks per warp up to which a cluster takes an item
 
 template <int D, int MT>
 struct Dec {
@@ -202,7 +203,55 @@ __device__ __forceinline__ void cursor_settle(const CacheAttentionArgs& a, Curso
   }
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The rows rank, rank + parts, ... of an item from the parts that the cluster's
+// CTAs hold at the start of their shared memory (as in a workspace slot).
 template <int D, int MT>
+__device__ __forceinline__ void join_cluster(const CacheAttentionArgs& a, uint32_t sbase, int rank, int parts, int b,
+                                             int h, int R) {
+  constexpr int kRows = kThreads / D;  // rows at a time, a thread per channel
+  const int G = a.H / a.c.H, ch = static_cast<int>(threadIdx.x) % D;
+  for (int r = rank + parts * (static_cast<int>(threadIdx.x) / D); r < R; r += parts * kRows) {
+    const uint32_t at = sbase + (r * D + ch) * 4, at_ml = sbase + (16 * MT * D + 2 * r) * 4;
+    float m[8], l[8], o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      m[c] = -INFINITY;
+      l[c] = o[c] = 0.0f;
+      if (c < parts) {
+        m[c] = ld_cluster_f32(tc::mapa_shared(at_ml, c));
+        l[c] = ld_cluster_f32(tc::mapa_shared(at_ml + 4, c));
+        o[c] = ld_cluster_f32(tc::mapa_shared(at, c));
+      }
+    }
+    float top = m[0];
+#pragma unroll
+    for (int c = 1; c < 8; ++c) top = fmaxf(top, m[c]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float wt = ex2(m[c] - ref);
+      sum = fmaf(l[c], wt, sum);
+      acc = fmaf(o[c], wt, acc);
+    }
+    const int tok = r / G, head = h * G + r - tok * G;
+    const __nv_bfloat16 v = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc / sum);
+    a.out.p[b * a.out.sb + tok * a.out.ss + head * a.out.sh + ch] = *reinterpret_cast<const uint16_t*>(&v);
+    if (a.lse != nullptr && ch == 0)
+      a.lse[(static_cast<int64_t>(b) * a.H + head) * a.T + tok] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+// kCluster: small calls. A cluster of CTAs has one item each, cut into equal
+// parts; the parts are joined through distributed shared memory and nothing
+// goes through the workspace.
+template <int D, int MT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode_kernel(const CacheAttentionArgs a) {
   using L = Dec<D, MT>;
   constexpr int kHalves = D / 64;
@@ -216,56 +265,75 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
   tc::griddep_wait();
   tc::griddep_launch_dependents();
 
-  // this CTA's range of units and where it begins: each thread sums a run of
-  // sequences, a scan over the threads finds whose run the range begins in
-  int* plan = reinterpret_cast<int*>(smem + L::kOffPlan);
-  const int run = (static_cast<int>(a.B) + kThreads - 1) / kThreads;
-  const int b_lo = min(run * static_cast<int>(threadIdx.x), static_cast<int>(a.B));
-  const int b_hi = min(b_lo + run, static_cast<int>(a.B));
-  int mine = 0;
-  bool bad = false;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(load_seq(a, b, &bad));
-  if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) plan[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, W = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += plan[w];
-    W += plan[w];
-  }
-  W *= a.c.H;
-  const Split split(W, static_cast<int>(gridDim.x));
-  const int lo = split.first(static_cast<int>(blockIdx.x)), hi = split.first(static_cast<int>(blockIdx.x) + 1);
-  before *= a.c.H;
-  if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
-    int b = b_lo;
-    for (;; ++b) {
-      const int u = seq_units(load_seq(a, b, &bad)) * a.c.H;
-      if (lo < before + u) break;
-      before += u;
-    }
-    plan[kWarps] = b;
-    plan[kWarps + 1] = lo - before;
-  }
-  __syncthreads();
-  int4* desc = static_cast<int4*>(a.workspace);
-  if (lo == hi) {
-    if (threadIdx.x == 0) desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
-  }
   Cursor seg;
-  seg.b = plan[kWarps];
-  seg.s = load_seq(a, seg.b, &bad);
-  seg.units = seq_units(seg.s);
-  seg.h = plan[kWarps + 1] / seg.units;
-  seg.blk = plan[kWarps + 1] - seg.h * seg.units;
+  int lo = 0, hi, rank = 0, parts = 1;
+  int4* desc = static_cast<int4*>(a.workspace);
+  Split split(0, 1);
+  bool bad = false;
+  if constexpr (kCluster) {
+    rank = static_cast<int>(tc::cluster_ctarank());
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(parts));
+    const int item = static_cast<int>(blockIdx.x) / parts;
+    seg.b = item / a.c.H;
+    seg.h = item - seg.b * a.c.H;
+    seg.s = load_seq(a, seg.b, &bad);
+    if (bad && rank == 0 && threadIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
+    seg.units = seq_units(seg.s);
+    split = Split(seg.units, parts);
+    lo = split.first(rank);
+    hi = split.first(rank + 1);
+    seg.blk = lo;
+    __syncthreads();  // the barriers are set up
+  } else {
+    // this CTA's range of units and where it begins: each thread sums a run of
+    // sequences, a scan over the threads finds whose run the range begins in
+    int* plan = reinterpret_cast<int*>(smem + L::kOffPlan);
+    const int run = (static_cast<int>(a.B) + kThreads - 1) / kThreads;
+    const int b_lo = min(run * static_cast<int>(threadIdx.x), static_cast<int>(a.B));
+    const int b_hi = min(b_lo + run, static_cast<int>(a.B));
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += seq_units(load_seq(a, b, &bad));
+    if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) plan[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, W = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += plan[w];
+      W += plan[w];
+    }
+    W *= a.c.H;
+    split = Split(W, static_cast<int>(gridDim.x));
+    lo = split.first(static_cast<int>(blockIdx.x));
+    hi = split.first(static_cast<int>(blockIdx.x) + 1);
+    before *= a.c.H;
+    if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
+      int b = b_lo;
+      for (;; ++b) {
+        const int u = seq_units(load_seq(a, b, &bad)) * a.c.H;
+        if (lo < before + u) break;
+        before += u;
+      }
+      plan[kWarps] = b;
+      plan[kWarps + 1] = lo - before;
+    }
+    __syncthreads();
+    if (lo == hi) {
+      if (threadIdx.x == 0) desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    seg.b = plan[kWarps];
+    seg.s = load_seq(a, seg.b, &bad);
+    seg.units = seq_units(seg.s);
+    seg.h = plan[kWarps + 1] / seg.units;
+    seg.blk = plan[kWarps + 1] - seg.h * seg.units;
+  }
   const int n_cta = hi - lo;
   const int n_mine = n_cta > warp ? (n_cta - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
 
@@ -327,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
   bool alive = true;
   const int G = a.H / a.c.H;
 #pragma unroll 1
-  for (int at = 0; at < n_cta;) {
+  for (int at = 0; at < n_cta || (kCluster && at == 0);) {
     // the segment: units [at, at + n) of the CTA, blocks [seg.blk, seg.blk + n) of one item
     const int n = min(seg.units - seg.blk, n_cta - at);
     const int R = seg.s.q_len * G;
@@ -550,11 +618,13 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
           a.lse[(static_cast<int64_t>(seg.b) * a.H + head) * a.T + tok] = -INFINITY;
       }
     }
-    const bool whole = n == seg.units;
+    const bool whole = kCluster ? parts == 1 : n == seg.units;
     const int which = at == 0 ? 0 : 1;  // a partial item is the range's first or its last
-    float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + L::kDesc) +
-                  (static_cast<size_t>(blockIdx.x) * 2 + which) * L::kSlot;
-    if (at + n == n_cta && threadIdx.x == 0) {
+    // a cluster's parts stay in shared memory, over the ring, whose blocks are used up
+    float* part = kCluster ? reinterpret_cast<float*>(smem)
+                           : reinterpret_cast<float*>(static_cast<char*>(a.workspace) + L::kDesc) +
+                                 (static_cast<size_t>(blockIdx.x) * 2 + which) * L::kSlot;
+    if (!kCluster && at + n == n_cta && threadIdx.x == 0) {
       // the last item, if it begins here and goes on in other CTAs: up to which one, and whose rows
       const int rest = seg.units - seg.blk - n;
       desc[blockIdx.x] = seg.blk == 0 && rest > 0 ? make_int4(split.owner(hi + rest - 1), seg.b, seg.h, which)
@@ -618,6 +688,18 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       }
     }
     if (R == 0) __syncthreads();
+    if constexpr (kCluster) {
+      if (parts > 1) {
+        tc::cluster_arrive_release();
+        tc::cluster_wait_acquire();
+        join_cluster<D, MT>(a, sbase, rank, parts, seg.b, seg.h, R);
+        __syncwarp();
+        // no CTA ends while another reads its shared memory
+        tc::cluster_arrive_release();
+        tc::cluster_wait_acquire();
+      }
+      break;
+    }
     at += n;
     seg.blk += n;
     if (at < n_cta) cursor_settle(a, seg);
@@ -793,24 +875,43 @@ __global__ void __launch_bounds__(kRowThreads) cache_attention_kernel(CacheAtten
 template <int D, int MT>
 cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
   using L = Dec<D, MT>;
-  // a CTA for every 4 blocks that the tables can name (one per warp), at most what the SMs hold
-  const int64_t blocks = a.B * a.c.H * (table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock);
+  const int64_t items = a.B * a.c.H;
+  const int64_t item_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock;
   const int sms = sm_count_current() < kMaxSms ? sm_count_current() : kMaxSms;
-  const int64_t most = static_cast<int64_t>(sms) * L::kCtasPerSm, want = div_up(blocks, kWarps);
-  const unsigned ctas = static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most));
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(cache_decode_kernel<D, MT>), L::kBytes);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  const int64_t most = static_cast<int64_t>(sms) * L::kCtasPerSm;
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT>, a)) != cudaSuccess || ctas == 1) return e;
+  cudaError_t e;
+  // one launch, a cluster per item, where the clusters fit the GPU at once and
+  // a warp gets few blocks
+  int parts = 1;
+  while (parts < 8 && parts * kWarps < item_blocks && items * parts * 2 <= most) parts *= 2;
+  if (items <= most && item_blocks <= parts * kWarps * kClusterBlocks) {
+    if ((e = set_smem_limit_once(reinterpret_cast<const void*>(cache_decode_kernel<D, MT, true>), L::kBytes)) !=
+        cudaSuccess)
+      return e;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(parts);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(items * parts));
+    return cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT, true>, a);
+  }
+  // else a CTA for every 4 blocks that the tables can name (one per warp), at most what the SMs hold
+  const int64_t want = div_up(items * item_blocks, kWarps);
+  const unsigned ctas = static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most));
+  if ((e = set_smem_limit_once(reinterpret_cast<const void*>(cache_decode_kernel<D, MT, false>), L::kBytes)) !=
+      cudaSuccess)
+    return e;
+  cfg.gridDim = dim3(ctas);
+  if ((e = cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT, false>, a)) != cudaSuccess || ctas == 1) return e;
   cfg.gridDim = dim3(ctas, static_cast<unsigned>(div_up(a.T * (a.H / a.c.H), kJoinRows)));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;

@@ -319,6 +319,14 @@ ATTENTION = [
     (8, 2, 128, 64, [3001], None, 40, True),
     (2, 1, 64, 64, [5000], None, 2, True),
     (4, 4, 128, 64, [20, 300], None, 300, True),                        # more queries than tokens
+    # calls whose blocks are cut evenly over the GPU, items shared by CTAs and CTAs by items
+    (14, 2, 128, 64, [9001, 10, 0, 4000], None, 1, True),
+    (4, 1, 64, 128, [10000, 33], [3, 2], 3, True),
+    (40, 2, 128, 64, [8500, 500], None, 1, False),
+    (9, 1, 64, 32, [8200, 1, 5], [2, 0, 3], 3, True),
+    (8, 4, 128, 64, [(37 * i) % 400 for i in range(130)], None, 1, True),
+    (8, 8, 64, 32, [(53 * i) % 300 for i in range(150)], [i % 3 for i in range(150)], 2, True),
+    (16, 4, 64, 64, [(91 * i) % 700 for i in range(140)], None, 5, True),
 ]
 
 
