@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "lib", "libsage.so")
 SOURCES = ["api.cu", "prologue.cu", "attention_simt.cu", "attention_tc.cu", "lse_term.cu",
-           "quantize_noalloc.cu", "tmap.cu", "cache_api.cu", "cache_pages.cu", "cache_attention.cu"]
+           "quantize_noalloc.cu", "tmap.cu", "cache_api.cu", "cache_pages.cu", "cache_attention.cu",
+           "cache_attention_tc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "sage.h")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

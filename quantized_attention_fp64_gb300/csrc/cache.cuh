@@ -106,6 +106,7 @@ cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt
 cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t* src, const int32_t* dst, int64_t n,
                                     int* dev_err, cudaStream_t stream);
 size_t cache_attention_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t D);
+cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream);
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream);
 
 }  // namespace sage

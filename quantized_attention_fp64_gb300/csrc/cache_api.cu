@@ -171,6 +171,7 @@ int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H, int64_t
   if (Hkv < 0) return SAGE_ERR_SHAPE;
   if ((rc = check_batch(B, T)) != SAGE_OK || (rc = check_heads(H, Hkv)) != SAGE_OK) return rc;
   if (D != 128 && D != 64) return SAGE_ERR_HEAD_DIM;
+  if (H > 0 && T > kMaxTokens / (H / Hkv)) return SAGE_ERR_TOO_LARGE;
   *bytes = (B == 0 || T == 0 || H == 0) ? 0 : cache_attention_workspace_bytes(B, T, H, Hkv, D);
   return SAGE_OK;
 }
@@ -190,6 +191,7 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
   // the call's blocks, all sequences and heads, are counted in 32 bits
   const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;
   if (B > 0 && a.c.H > 0 && seq_blocks > ((int64_t(1) << 31) - 1) / (B * a.c.H)) return SAGE_ERR_TOO_LARGE;
+  if (H > 0 && T > kMaxTokens / (H / a.c.H)) return SAGE_ERR_TOO_LARGE;  // rows of a key/value head, too
   if (args->lse_dev != nullptr && !aligned(args->lse_dev, 4)) return SAGE_ERR_ALIGN;
   const float sm = args->sm_scale;
   if (!(std::isnan(sm) || (std::isfinite(sm) && sm > 0.0f))) return SAGE_ERR_ARG;
