@@ -12,11 +12,13 @@
 //                 32-key block, 16 bytes per lane and load, the next tile's
 //                 loads in flight in registers), turn them into fp16 and store
 //                 them in the 128-byte-swizzled layout that the MMA reads
-// Per tile and step j: S = Q K_j^T (tcgen05 kind::f16, fp32 in TMEM); the
-// softmax reads S, writes p as fp16 over it, and O += P V_j reads P from TMEM.
-// S and P share their columns (S0, S1, O0, O1 take all 512 at D = 128), so a
-// tile's next QK waits for its PV; the two tiles take turns on the tensor
-// cores.
+// Per tile and step j (64 keys at D = 128, 128 at D = 64): S = Q K_j^T
+// (tcgen05 kind::f16, fp32 in TMEM); the softmax reads S into registers and
+// releases it, so the next step's QK runs under the exponentials; p goes to
+// TMEM as fp16, and O += P V_j reads it there (P in shared memory would double
+// what the products read from it). At D = 128 the 512 columns hold, per tile,
+// 128 of O, 64 of S and two P of 32, written in turns; at D = 64 64 of O, 128
+// of S and one P of 64.
 // Numbers. Queries become fp16 times a power of two per row (their largest
 // value in [1, 4)); key codes are exact in fp16. Values become
 // fp16(code * fp16(s_v / R)), R the largest value scale of the unit's blocks:
@@ -64,8 +66,8 @@ struct Smem {
 };
 constexpr int kBarQFull = 0, kBarKFull = kBarQFull + 2, kBarKEmpty = kBarKFull + kStages;
 constexpr int kBarVFull = kBarKEmpty + kStages, kBarVEmpty = kBarVFull + kStages;
-constexpr int kBarSFull = kBarVEmpty + kStages, kBarPFull = kBarSFull + 2, kBarPVDone = kBarPFull + 2;
-constexpr int kBarDrain = kBarPVDone + 2, kBarScale = kBarDrain + 2;
+constexpr int kBarSFull = kBarVEmpty + kStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
+constexpr int kBarPVDone = kBarPFull + 2, kBarDrain = kBarPVDone + 4, kBarScale = kBarDrain + 2;  // PVDone: [tile][P buffer]
 constexpr int kNumBars = kBarScale + kScaleSlots;
 template <int D>
 struct SmemTail {
@@ -78,9 +80,20 @@ struct SmemTail {
 };
 static_assert(SmemTail<128>::kBytes <= 232448u, "shared memory of one CTA");
 
-__host__ __device__ constexpr uint32_t col_s(int i) { return 128u * static_cast<uint32_t>(i); }
+// Steps of a tile and its TMEM columns.
 template <int D>
-__host__ __device__ constexpr uint32_t col_o(int i) { return 256u + static_cast<uint32_t>(D) * static_cast<uint32_t>(i); }
+struct Step {
+  static constexpr int kKeysPerStep = D == 128 ? 64 : 128;
+  static constexpr int kPer = kKeys / kKeysPerStep;    // steps per key tile
+  static constexpr int kP = D == 128 ? 2 : 1;          // buffers of P
+  static constexpr uint32_t kIdescQK = D == 128 ? tc::kIdescM128N64 : tc::kIdescM128N128;
+  __host__ __device__ static constexpr uint32_t col_o(int i) { return static_cast<uint32_t>(D * i); }
+  __host__ __device__ static constexpr uint32_t col_s(int i) { return static_cast<uint32_t>(2 * D + (256 - D) * i); }
+  __host__ __device__ static constexpr uint32_t col_p(int i, int buf) {
+    return col_s(i) + static_cast<uint32_t>(kKeysPerStep + buf * (kKeysPerStep / 2));
+  }
+  static_assert(col_p(1, kP - 1) + kKeysPerStep / 2 <= kTmemCols, "tensor memory");
+};
 
 struct Ctx {
   uint32_t bar0;
@@ -197,19 +210,21 @@ __device__ __forceinline__ Unit find_unit(const CacheAttentionArgs& a, int pairs
   return u;
 }
 
+// dk: the step's first key of the key tile
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     const uint32_t off = static_cast<uint32_t>(ks >> 2) * Smem<D>::kSub + static_cast<uint32_t>(ks & 3) * 32u;
-    tc::mma_f16_ss(d_tmem, desc_at(dq, off), desc_at(dk, off), tc::kIdescM128N128, ks > 0 ? 1u : 0u);
+    tc::mma_f16_ss(d_tmem, desc_at(dq, off), desc_at(dk, off), Step<D>::kIdescQK, ks > 0 ? 1u : 0u);
   }
 }
+// dv: the step's first 64 keys of the value tile
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t tp, uint64_t dv, bool acc) {
   constexpr uint32_t idesc = D == 128 ? tc::kIdescM128N128 : tc::kIdescM128N64;
 #pragma unroll
-  for (int ks = 0; ks < kKeys / 16; ++ks) {
+  for (int ks = 0; ks < Step<D>::kKeysPerStep / 16; ++ks) {
     const uint32_t off = static_cast<uint32_t>(ks >> 2) * Smem<D>::kSubV + static_cast<uint32_t>(ks & 3) * 32u;
     mma_f16_ts(d_tmem, tp + 8u * static_cast<uint32_t>(ks), desc_at(dv, off), idesc, (acc || ks > 0) ? 1u : 0u);
   }
@@ -265,7 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::mbar_init(cx.bar(kBarQFull + s), kRows);
       tc::mbar_init(cx.bar(kBarSFull + s), 1);
       tc::mbar_init(cx.bar(kBarPFull + s), kRows);
-      tc::mbar_init(cx.bar(kBarPVDone + s), 1);
+      tc::mbar_init(cx.bar(kBarSFree + s), kRows);
+      tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
+      tc::mbar_init(cx.bar(kBarPVDone + 2 * s + 1), 1);
       tc::mbar_init(cx.bar(kBarDrain + s), 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -292,42 +309,52 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       // ------------------------------------------------ MMA issuer of tile i --
       const int i = warp;
       const bool leader = elect_one();
-      const uint32_t d_s = tmem + col_s(i), d_o = tmem + col_o<D>(i);
+      using S = Step<D>;
+      const uint32_t d_s = tmem + S::col_s(i), d_o = tmem + S::col_o(i);
       const uint64_t dq = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dv0 = tc::sw128_desc(sbase + L::kOffV);
+      const int n = u.n[i] * S::kPer, n_all = u.n_max * S::kPer;  // steps of this tile, and of the CTA
       bool ok = i < u.tiles;
-      if (ok && u.n[i] > 0) ok = wait_bar_warp(cx, cx.bar(kBarQFull + i), 0);
-      for (int j = 0; ok && j < u.n_max; ++j) {
-        const uint32_t s = static_cast<uint32_t>(j) % kStages, ph = (static_cast<uint32_t>(j) / kStages) & 1u;
-        // S of this step lies over P of the last one: its PV has to be done
-        if (j > 0 && j <= u.n[i] &&
-            !(ok = wait_bar_warp(cx, cx.bar(kBarPVDone + i), static_cast<uint32_t>(j - 1) & 1u)))
-          break;
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarKFull + s), ph))) break;
-        tc::tc_fence_after();
-        if (leader) {
-          if (j < u.n[i]) {
-            issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTile));
-            tc::mma_commit(cx.bar(kBarSFull + i));
-            tc::mma_commit(cx.bar(kBarKEmpty + s));
-          } else {
+      if (ok && n > 0) ok = wait_bar_warp(cx, cx.bar(kBarQFull + i), 0);
+      for (int j = 0; ok && j <= n_all; ++j) {
+        if (j < n_all) {
+          // QK_j once its keys are there and the softmax has read S_{j-1}
+          const int tile = j / S::kPer, in = j % S::kPer;
+          const uint32_t s = static_cast<uint32_t>(tile) % kStages, ph = (static_cast<uint32_t>(tile) / kStages) & 1u;
+          if (in == 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarKFull + s), ph))) break;
+          if (j < n) {
+            if (j > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), static_cast<uint32_t>(j - 1) & 1u))) break;
+            tc::tc_fence_after();
+            if (leader) {
+              issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTile + static_cast<uint32_t>(in * S::kKeysPerStep) * 128u));
+              tc::mma_commit(cx.bar(kBarSFull + i));
+              if (in == S::kPer - 1) tc::mma_commit(cx.bar(kBarKEmpty + s));
+            }
+          } else if (leader && in == S::kPer - 1) {
             tc::mbar_arrive(cx.bar(kBarKEmpty + s));  // no row of this tile sees the keys
           }
+          __syncwarp();
         }
-        __syncwarp();
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarVFull + s), ph))) break;
-        if (j < u.n[i] && !(ok = wait_bar_warp(cx, cx.bar(kBarPFull + i), static_cast<uint32_t>(j) & 1u))) break;
-        tc::tc_fence_after();
-        if (leader) {
-          if (j < u.n[i]) {
-            issue_pv<D>(d_o, d_s, desc_at(dv0, s * L::kTileV), j > 0);
-            tc::mma_commit(cx.bar(kBarPVDone + i));
-            tc::mma_commit(cx.bar(kBarVEmpty + s));
-          } else {
+        if (j >= 1) {
+          // PV_{j-1} once its values and P_{j-1} are there
+          const int jj = j - 1, tile = jj / S::kPer, in = jj % S::kPer;
+          const uint32_t s = static_cast<uint32_t>(tile) % kStages, ph = (static_cast<uint32_t>(tile) / kStages) & 1u;
+          if (in == 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarVFull + s), ph))) break;
+          if (jj < n) {
+            if (!(ok = wait_bar_warp(cx, cx.bar(kBarPFull + i), static_cast<uint32_t>(jj) & 1u))) break;
+            tc::tc_fence_after();
+            if (leader) {
+              issue_pv<D>(d_o, tmem + S::col_p(i, jj % S::kP),
+                          desc_at(dv0, s * L::kTileV + static_cast<uint32_t>(in) * (S::kKeysPerStep / 64) * L::kSubV),
+                          jj > 0);
+              tc::mma_commit(cx.bar(kBarPVDone + 2 * i + jj % S::kP));
+              if (in == S::kPer - 1) tc::mma_commit(cx.bar(kBarVEmpty + s));
+            }
+          } else if (leader && in == S::kPer - 1) {
             tc::mbar_arrive(cx.bar(kBarVEmpty + s));
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       // all MMAs of this warp complete before TMEM is freed
       if (leader) tc::mma_commit(cx.bar(kBarDrain + i));
@@ -464,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     const int i = (warp - 4) >> 2, wq = warp & 3;
     const int r = u.row0 + i * kRows + wq * 32 + lane;  // this thread's row
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_addr + col_s(i), tO = tmem + lane_addr + col_o<D>(i);
+    using S = Step<D>;
+    const uint32_t tS = tmem + lane_addr + S::col_s(i), tO = tmem + lane_addr + S::col_o(i);
     const bool real = r < u.R;
     const int tok = r / u.G, head = u.h * u.G + r - tok * u.G;
     const int sees = real ? row_sees(a, u, r) : 0;
@@ -505,34 +533,59 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     // the smallest limit in the warp decides, for all its lanes, whether a tile is masked
     const int all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
     const float* scale_ring = reinterpret_cast<const float*>(smem + T::kOffScale);
-    for (int j = 0; ok && j < u.n[i]; ++j) {
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + j % kScaleSlots), static_cast<uint32_t>(j / kScaleSlots) & 1u))) break;
-      const float4 ks = *reinterpret_cast<const float4*>(scale_ring + (j % kScaleSlots) * 4);
+    constexpr int kB = S::kKeysPerStep / kCacheBlock;  // blocks of a step
+    const int n = u.n[i] * S::kPer;
+    float k4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // scales of the key tile
+    // waits for the PV of step x (its P buffer and O are then free)
+    const auto wait_pv = [&](int x) {
+      return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + x % S::kP), static_cast<uint32_t>(x / S::kP) & 1u);
+    };
+    for (int j = 0; ok && j < n; ++j) {
+      const int tile = j / S::kPer, in = j % S::kPer;
+      if (in == 0) {
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + tile % kScaleSlots), static_cast<uint32_t>(tile / kScaleSlots) & 1u)))
+          break;
+        const float4 ks = *reinterpret_cast<const float4*>(scale_ring + (tile % kScaleSlots) * 4);
+        k4[0] = ks.x;
+        k4[1] = ks.y;
+        k4[2] = ks.z;
+        k4[3] = ks.w;
+      }
       if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), static_cast<uint32_t>(j) & 1u))) break;
       tc::tc_fence_after();
-      const float k4[4] = {ks.x, ks.y, ks.z, ks.w};
-      const bool masked = (j + 1) * kKeys > all_see || ks.x < 0.0f || ks.y < 0.0f || ks.z < 0.0f || ks.w < 0.0f;
-      uint32_t sr[4][32];
+      uint32_t sr[kB][32];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
+      for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
       tc::tmem_wait_ld();
-      float cb[4];
-      int lim[4];  // tokens of each block that the row sees
+      tc::tc_fence_before();
+      tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
+      float cb[kB];
+      int lim[kB];  // tokens of each block that the row sees
+      bool masked = (j + 1) * S::kKeysPerStep > all_see;
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const float k = kB == 4 || in == 0 ? k4[b] : k4[(b + 2) & 3];
+        cb[b] = f * k;
+        lim[b] = k < 0.0f ? 0 : sees - j * S::kKeysPerStep - 32 * b;
+        masked |= k < 0.0f;
+      }
       float mt = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        cb[b] = f * k4[b];
-        lim[b] = k4[b] < 0.0f ? 0 : sees - j * kKeys - 32 * b;
+      for (int b = 0; b < kB; ++b) {
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
         }
-        float mb = __uint_as_float(sr[b][0]);
+        float m0 = __uint_as_float(sr[b][0]), m1 = __uint_as_float(sr[b][1]);
 #pragma unroll
-        for (int c = 1; c < 31; c += 2) mb = max3(mb, __uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1]));
-        mb = fmaxf(mb, __uint_as_float(sr[b][31]));
-        mt = fmaxf(mt, mb == -INFINITY ? mb : mb * cb[b]);
+        for (int c = 2; c < 30; c += 4) {
+          m0 = max3(m0, __uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1]));
+          m1 = max3(m1, __uint_as_float(sr[b][c + 2]), __uint_as_float(sr[b][c + 3]));
+        }
+        m0 = max3(m0, __uint_as_float(sr[b][30]), __uint_as_float(sr[b][31]));
+        m0 = fmaxf(m0, m1);
+        mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
       }
       if (__any_sync(0xffffffffu, mt > m + kLazy)) {
         const float up = fmaxf(m, mt);
@@ -540,6 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         m = up;
         l *= alpha;
         if (j > 0) {
+          if (!(ok = wait_pv(j - 1))) break;  // O is at rest
+          tc::tc_fence_after();
           const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -559,36 +614,38 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       const float ref = m == -INFINITY ? 0.0f : m;
       const float2 n2 = make_float2(-ref, -ref);
       float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
+      uint32_t pw[kB / 2][32];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pw[32];
+      for (int b = 0; b < kB; ++b) {
+        const float2 c2 = make_float2(cb[b], cb[b]);
 #pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2) {
-          const int b = 2 * half + b2;
-          const float2 c2 = make_float2(cb[b], cb[b]);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
-            float2 p = make_float2(ex2(y.x), ex2(y.y));
-            if (masked) {
-              if (value_token(c) >= lim[b]) p.x = 0.0f;
-              if (value_token(c + 1) >= lim[b]) p.y = 0.0f;
-            }
-            if (c & 2) sb = __fadd2_rn(sb, p);
-            else sa = __fadd2_rn(sa, p);
-            pw[16 * b2 + c / 2] = pack_half2(p.x, p.y);
+        for (int c = 0; c < 32; c += 2) {
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
+          float2 p = make_float2(ex2(y.x), ex2(y.y));
+          if (masked) {
+            if (value_token(c) >= lim[b]) p.x = 0.0f;
+            if (value_token(c + 1) >= lim[b]) p.y = 0.0f;
           }
+          if (c & 2) sb = __fadd2_rn(sb, p);
+          else sa = __fadd2_rn(sa, p);
+          pw[b / 2][16 * (b & 1) + c / 2] = pack_half2(p.x, p.y);
         }
-        tc::tmem_st32(tS + 32u * half, pw);
       }
       l += (sa.x + sa.y) + (sb.x + sb.y);
+      if (j >= S::kP) {
+        if (!(ok = wait_pv(j - S::kP))) break;  // the buffer's last PV has read it
+        tc::tc_fence_after();
+      }
+      const uint32_t tP = tmem + lane_addr + S::col_p(i, j % S::kP);
+#pragma unroll
+      for (int x = 0; x < kB / 2; ++x) tc::tmem_st32(tP + 32u * x, pw[x]);
       tc::tmem_wait_st();
       tc::tc_fence_before();
       tc::mbar_arrive(cx.bar(kBarPFull + i));
     }
     // epilogue
-    if (ok && u.n[i] > 0) {
-      ok = wait_bar_warp(cx, cx.bar(kBarPVDone + i), static_cast<uint32_t>(u.n[i] - 1) & 1u);
+    if (ok && n > 0) {
+      ok = wait_pv(n - 1);
       tc::tc_fence_after();
     }
     const float* tops = reinterpret_cast<const float*>(smem + T::kOffTop);
