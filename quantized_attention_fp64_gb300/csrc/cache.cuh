@@ -106,7 +106,16 @@ cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt
 cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t* src, const int32_t* dst, int64_t n,
                                     int* dev_err, cudaStream_t stream);
 size_t cache_attention_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hkv, int64_t D);
+// Many query rows (tensor cores), and its workspace.
 cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream);
+size_t cache_attention_tc_workspace_bytes(int64_t D);
+// Joins the parts that the `ctas` CTAs of either attention kernel left in the
+// workspace: one int4 per CTA (last CTA of the item that begins in this one and
+// goes on, or -1; sequence; 2 x head + slot of the first part; first row), then,
+// desc_bytes on, two slots per CTA of slot_rows rows of D floats and their
+// (maximum, sum). rows: the most rows of a part.
+cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_rows, int rows, int ctas,
+                              size_t desc_bytes, cudaStream_t stream);
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream);
 
 }  // namespace sage

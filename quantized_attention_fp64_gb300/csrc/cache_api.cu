@@ -189,9 +189,13 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
       (rc = check_tensor(args->out)) != SAGE_OK)
     return rc;
   // the call's blocks, all sequences and heads, are counted in 32 bits
+  // (once for every 256 query rows that share a key/value head)
   const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;
-  if (B > 0 && a.c.H > 0 && seq_blocks > ((int64_t(1) << 31) - 1) / (B * a.c.H)) return SAGE_ERR_TOO_LARGE;
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1;
   if (H > 0 && T > kMaxTokens / (H / a.c.H)) return SAGE_ERR_TOO_LARGE;  // rows of a key/value head, too
+  const int64_t pairs = H > 0 ? div_up(T * (H / a.c.H), 256) : 0;
+  if (B > 0 && pairs > 0 && (pairs > kMost / (B * a.c.H) || seq_blocks > kMost / (B * a.c.H * pairs)))
+    return SAGE_ERR_TOO_LARGE;
   if (args->lse_dev != nullptr && !aligned(args->lse_dev, 4)) return SAGE_ERR_ALIGN;
   const float sm = args->sm_scale;
   if (!(std::isnan(sm) || (std::isfinite(sm) && sm > 0.0f))) return SAGE_ERR_ARG;

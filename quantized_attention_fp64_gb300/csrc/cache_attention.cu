@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     if (!kCluster && at + n == n_cta && threadIdx.x == 0) {
       // the last item, if it begins here and goes on in other CTAs: up to which one, and whose rows
       const int rest = seg.units - seg.blk - n;
-      desc[blockIdx.x] = seg.blk == 0 && rest > 0 ? make_int4(split.owner(hi + rest - 1), seg.b, seg.h, which)
+      desc[blockIdx.x] = seg.blk == 0 && rest > 0 ? make_int4(split.owner(hi + rest - 1), seg.b, 2 * seg.h + which, 0)
                                                   : make_int4(-1, 0, 0, 0);
     }
     __syncthreads();
@@ -714,42 +714,47 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
 }
 
 // Joins the items that several CTAs share. Block (c, y) serves the item that
-// begins in CTA c and ends in a later one, two of its rows: of 8 warps, four
-// share a row, each with every 4th part.
-constexpr int kJoinWarps = 8, kJoinRows = 2, kJoinParts = kJoinWarps / kJoinRows;
-template <int D, int MT>
-__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttentionArgs a) {
+// begins in CTA c and ends in a later one, kJoinWarps / kShare of its rows:
+// kShare warps share a row, each with every kShare-th part.
+constexpr int kJoinWarps = 8;
+template <int D, int kShare>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttentionArgs a, int slot_rows,
+                                                                     size_t desc_bytes) {
   constexpr int kV = D / 32;  // channels per lane
-  using L = Dec<D, MT>;
   __shared__ float acc_s[kJoinWarps][D];
   __shared__ float2 ml_s[kJoinWarps];
   tc::griddep_wait();
   const int c0 = static_cast<int>(blockIdx.x);
-  const int4 item = static_cast<const int4*>(a.workspace)[c0];  // last CTA, sequence, head, slot in the first CTA
+  const int4 item = static_cast<const int4*>(a.workspace)[c0];
   if (item.x < 0) return;
   const int G = a.H / a.c.H;
   bool bad = false;
   const int R = load_seq(a, item.y, &bad).q_len * G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = static_cast<int>(blockIdx.y) * kJoinRows + warp / kJoinParts;
-  const float* ws = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + L::kDesc);
+  const int slot_row = static_cast<int>(blockIdx.y) * (kJoinWarps / kShare) + warp / kShare;
+  const int r = item.w + slot_row;
+  const bool real = slot_row < slot_rows && r < R;
+  const size_t slot = static_cast<size_t>(slot_rows) * (D + 2);
+  const float* ws = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + desc_bytes);
   float top = -INFINITY, sum = 0.0f, acc[kV];
 #pragma unroll
   for (int x = 0; x < kV; ++x) acc[x] = 0.0f;
-  if (r < R) {
+  if (real) {
     // parts of this warp, four at a time: their loads do not wait for one another
-    for (int c = c0 + warp % kJoinParts; c <= item.x; c += 4 * kJoinParts) {
+    for (int c = c0 + warp % kShare; c <= item.x; c += 4 * kShare) {
       float2 x[4];
       float y[4][kV];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int ci = c + i * kJoinParts;
+        const int ci = c + i * kShare;
         x[i] = make_float2(-INFINITY, 0.0f);
         if (ci <= item.x) {
-          const float* p = ws + (static_cast<size_t>(ci) * 2 + (ci == c0 ? item.w : 0)) * L::kSlot;
-          x[i] = *reinterpret_cast<const float2*>(p + 16 * MT * D + 2 * r);
-          if constexpr (kV == 4) *reinterpret_cast<float4*>(y[i]) = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
-          else *reinterpret_cast<float2*>(y[i]) = *reinterpret_cast<const float2*>(p + r * D + 2 * lane);
+          const float* p = ws + (static_cast<size_t>(ci) * 2 + (ci == c0 ? item.z & 1 : 0)) * slot;
+          x[i] = *reinterpret_cast<const float2*>(p + slot_rows * D + 2 * slot_row);
+          if constexpr (kV == 4)
+            *reinterpret_cast<float4*>(y[i]) = *reinterpret_cast<const float4*>(p + slot_row * D + 4 * lane);
+          else
+            *reinterpret_cast<float2*>(y[i]) = *reinterpret_cast<const float2*>(p + slot_row * D + 2 * lane);
         } else {
 #pragma unroll
           for (int v = 0; v < kV; ++v) y[i][v] = 0.0f;
@@ -770,27 +775,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
       }
     }
   }
+  if constexpr (kShare > 1) {
 #pragma unroll
-  for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = acc[v];
-  if (lane == 0) ml_s[warp] = make_float2(top, sum);
-  __syncthreads();
-  if (r >= R || warp % kJoinParts != 0) return;
-  float all = -INFINITY;
+    for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = acc[v];
+    if (lane == 0) ml_s[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (!real || warp % kShare != 0) return;
 #pragma unroll
-  for (int w = 0; w < kJoinParts; ++w) all = fmaxf(all, ml_s[warp + w].x);
-  const float ref = all == -INFINITY ? 0.0f : all;
-  sum = 0.0f;
+    for (int w = 0; w < kShare; ++w) top = fmaxf(top, ml_s[warp + w].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    sum = 0.0f;
 #pragma unroll
-  for (int v = 0; v < kV; ++v) acc[v] = 0.0f;
+    for (int v = 0; v < kV; ++v) acc[v] = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinParts; ++w) {
-    const float wt = ex2(ml_s[warp + w].x - ref);
-    sum = fmaf(ml_s[warp + w].y, wt, sum);
+    for (int w = 0; w < kShare; ++w) {
+      const float wt = ex2(ml_s[warp + w].x - ref);
+      sum = fmaf(ml_s[warp + w].y, wt, sum);
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[v]);
+      for (int v = 0; v < kV; ++v) acc[v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[v]);
+    }
+  } else if (!real) {
+    return;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int tok = r / G, head = item.z * G + r - tok * G;
+  const int tok = r / G, head = (item.z >> 1) * G + r - tok * G;
   uint16_t* p = a.out.p + item.y * a.out.sb + tok * a.out.ss + head * a.out.sh + kV * lane;
 #pragma unroll
   for (int i = 0; i < kV; i += 2) {
@@ -798,8 +806,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
     *reinterpret_cast<uint32_t*>(p + i) = *reinterpret_cast<const uint32_t*>(&v);
   }
   if (a.lse != nullptr && lane == 0)
-    a.lse[(static_cast<int64_t>(item.y) * a.H + head) * a.T + tok] =
-        sum == 0.0f ? -INFINITY : (all + log2f(sum)) * kLn2;
+    a.lse[(static_cast<int64_t>(item.y) * a.H + head) * a.T + tok] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int D, int MT>
@@ -842,19 +849,35 @@ cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
     return e;
   cfg.gridDim = dim3(ctas);
   if ((e = cudaLaunchKernelEx(&cfg, cache_decode_kernel<D, MT, false>, a)) != cudaSuccess || ctas == 1) return e;
-  cfg.gridDim = dim3(ctas, static_cast<unsigned>(div_up(a.T * (a.H / a.c.H), kJoinRows)));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D, MT>, a);
+  return launch_cache_join(a, D, 16 * MT, static_cast<int>(a.T * (a.H / a.c.H)), static_cast<int>(ctas), L::kDesc,
+                           stream);
 }
 
 }  // namespace
+
+cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_rows, int rows, int ctas,
+                              size_t desc_bytes, cudaStream_t stream) {
+  // few rows may have many parts, many rows have few
+  const int share = rows <= 32 ? 4 : 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(div_up(rows, kJoinWarps / share)));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto kernel = D == 128 ? (share == 4 ? cache_join_kernel<128, 4> : cache_join_kernel<128, 1>)
+                               : (share == 4 ? cache_join_kernel<64, 4> : cache_join_kernel<64, 1>);
+  return cudaLaunchKernelEx(&cfg, kernel, a, slot_rows, desc_bytes);
+}
 
 size_t cache_attention_workspace_bytes(int64_t, int64_t T, int64_t H, int64_t Hkv, int64_t D) {
   const int64_t rows = T * (H / Hkv);
   if (rows <= 16) return D == 128 ? Dec<128, 1>::kWorkspace : Dec<64, 1>::kWorkspace;
   if (rows <= 32) return D == 128 ? Dec<128, 2>::kWorkspace : Dec<64, 2>::kWorkspace;
-  return 0;
+  return cache_attention_tc_workspace_bytes(D);
 }
 
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream) {

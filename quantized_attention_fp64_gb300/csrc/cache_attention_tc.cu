@@ -3,28 +3,32 @@
 //
 // A work unit is one key/value head of one sequence and a pair of tiles of 128
 // query rows (query tokens x the heads that share the key/value head, token
-// major), so the codes of a key tile are converted once for 256 rows. One CTA
-// per unit, 16 warps:
+// major), so the codes of a key tile (64 keys) are converted once for 256 rows.
+// The key tiles of all units form one list (pair, head, tile) that is cut into
+// equal ranges, one per CTA and SM, whatever the lengths and the mask; a unit
+// that several CTAs share leaves its parts in the workspace (at most two per
+// CTA, as in cache_attention.cu), and a second kernel joins them. 16 warps:
 //   warps 0, 1    one MMA-issuing thread per query tile
 //   warp 2        TMEM allocation
 //   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
-//   warps 12-15   converters: read the int8 codes of 128 keys (a warp per
+//   warps 12-15   converters: read the int8 codes of a key tile (two warps per
 //                 32-key block, 16 bytes per lane and load, the next tile's
 //                 loads in flight in registers), turn them into fp16 and store
-//                 them in the 128-byte-swizzled layout that the MMA reads
-// Per tile and step j (64 keys at D = 128, 128 at D = 64): S = Q K_j^T
+//                 them in the 128-byte-swizzled layout that the MMA reads, four
+//                 tiles ahead (eight at D = 64); they also bring the queries
+//                 and run ahead into the next unit
+// Per query tile and key tile j: S = Q K_j^T
 // (tcgen05 kind::f16, fp32 in TMEM); the softmax reads S into registers and
 // releases it, so the next step's QK runs under the exponentials; p goes to
 // TMEM as fp16, and O += P V_j reads it there (P in shared memory would double
-// what the products read from it). At D = 128 the 512 columns hold, per tile,
-// 128 of O, 64 of S and two P of 32, written in turns; at D = 64 64 of O, 128
-// of S and one P of 64.
+// what the products read from it). The columns hold, per tile, D of O, 64 of S
+// and two P of 32, written in turns.
 // Numbers. Queries become fp16 times a power of two per row (their largest
 // value in [1, 4)); key codes are exact in fp16. Values become
-// fp16(code * fp16(s_v / R)), R the largest value scale of the unit's blocks:
-// two roundings of 2^-12 relative; p is rounded to fp16, 2^-12 relative. A block
-// whose scale is below 2^-14 R loses bits of that (its values are then held to
-// 2^-25 R absolutely).
+// fp16(code * fp16(s_v / R)), R the largest value scale of the part's blocks so
+// far, in steps of 32 key tiles (O is rescaled when it grows): two roundings of
+// 2^-12 relative; p is rounded to fp16, 2^-12 relative. A block whose scale is
+// below 2^-14 R loses bits of that (its values are then held to 2^-25 R).
 // The keys of a block stand in the order in which the values are stored
 // (value_position), so V^T needs no reordering on the way.
 //
@@ -41,80 +45,99 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kRows = 128;      // rows of a query tile
-constexpr int kKeys = 128;      // keys of a key tile
-constexpr int kStages = 2;      // key and value tiles in shared memory
-constexpr int kScaleSlots = 4;  // key tiles whose scales are kept
+constexpr int kKeys = 64;       // keys of a key tile
+constexpr int kMaxSms = 160;
+constexpr int kMinTiles = 8;    // key tiles that are worth a CTA of their own
+constexpr int kScaleSlots = 16; // key tiles whose scales are kept (more than the stages and the tiles in the MMA)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;   // p may reach 2^8 before the running maximum follows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kTmemCols = 512;
 
 // registers per thread of the control, converter and softmax warps
-constexpr uint32_t kRegCtl = 56, kRegConv = 104, kRegSoftmax = 176;
+constexpr uint32_t kRegCtl = 64, kRegConv = 112, kRegSoftmax = 168;
 static_assert(128 * (kRegCtl + kRegConv) + 256 * kRegSoftmax <= 65536, "register file of one SM");
 
 template <int D>
 struct Smem {
   static constexpr uint32_t kSub = 128 * 128;             // 64 channels of 128 rows, fp16
-  static constexpr uint32_t kTile = (D / 64) * kSub;      // a query or key tile
-  static constexpr uint32_t kSubV = D * 128;              // 64 keys of D channels, fp16
-  static constexpr uint32_t kTileV = 2 * kSubV;
-  static constexpr uint32_t kOffQ = 0;                    // 2 tiles
-  static constexpr uint32_t kOffK = kOffQ + 2 * kTile;
-  static constexpr uint32_t kOffV = kOffK + kStages * kTile;
-  static constexpr uint32_t kOffBar = kOffV + kStages * kTileV;
+  static constexpr uint32_t kTile = (D / 64) * kSub;      // a query tile
+  static constexpr uint32_t kSubK = kKeys * 128;          // 64 channels of a key tile
+  static constexpr uint32_t kTileKV = (D / 64) * kSubK;   // keys; values are D rows of 64 keys
+  static constexpr int kStages = D == 128 ? 4 : 8;        // key and value tiles
+  static constexpr int kQ = D == 128 ? 1 : 2;             // units whose queries are kept
+  static constexpr uint32_t kOffQ = 0;                    // [unit][2 tiles]
+  static constexpr uint32_t kOffK = kOffQ + kQ * 2 * kTile;
+  static constexpr uint32_t kOffV = kOffK + kStages * kTileKV;
+  static constexpr uint32_t kOffBar = kOffV + kStages * kTileKV;
 };
-constexpr int kBarQFull = 0, kBarKFull = kBarQFull + 2, kBarKEmpty = kBarKFull + kStages;
-constexpr int kBarVFull = kBarKEmpty + kStages, kBarVEmpty = kBarVFull + kStages;
-constexpr int kBarSFull = kBarVEmpty + kStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
-constexpr int kBarPVDone = kBarPFull + 2, kBarDrain = kBarPVDone + 4, kBarScale = kBarDrain + 2;  // PVDone: [tile][P buffer]
-constexpr int kNumBars = kBarScale + kScaleSlots;
+constexpr int kMaxStages = 8;
+constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarKFull = kBarQEmpty + 2, kBarKEmpty = kBarKFull + kMaxStages;
+constexpr int kBarVFull = kBarKEmpty + kMaxStages, kBarVEmpty = kBarVFull + kMaxStages;
+constexpr int kBarSFull = kBarVEmpty + kMaxStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
+constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarScale = kBarDrain + 2;  // PFull, PVDone: [tile][P buffer]
+constexpr int kBarTop = kBarScale + 2;
+constexpr int kNumBars = kBarTop + 1;
 template <int D>
 struct SmemTail {
   static constexpr uint32_t kOffTmem = Smem<D>::kOffBar + kNumBars * 8;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffTop = kOffAbort + 4;                    // [converter warp] largest value scale
-  static constexpr uint32_t kOffScale = (kOffTop + 16 + 15) / 16 * 16;  // [slot][block] key scales
-  static_assert(kOffScale % 16 == 0 && kOffTop % 4 == 0, "a slot is read as one float4");
-  static constexpr uint32_t kBytes = kOffScale + kScaleSlots * 16;
+  static constexpr uint32_t kOffTop = kOffAbort + 4;                    // [2][converter warp] largest value scale
+  static constexpr uint32_t kOffScale = (kOffTop + 32 + 15) / 16 * 16;  // [slot] two key scales, O's factor, R
+  static_assert(kOffScale % 16 == 0, "a slot is read as one float4");
+  static constexpr uint32_t kOffPlan = kOffScale + kScaleSlots * 16;    // 16 sums, then where the CTA's range begins and how the list is cut
+  static constexpr uint32_t kOffRow = kOffPlan + 24 * 4;                // [unit][256 rows] powers of two of the queries
+  // one unit more than of the queries themselves: those are free once the
+  // unit's last QK is done, when a softmax thread may still have to read its
+  // factor; an issuer goes on to the next unit only after the softmax did
+  static constexpr int kRowUnits = Smem<D>::kQ + 1;
+  static constexpr uint32_t kBytes = kOffRow + kRowUnits * 2 * kRows * 4;
+  // workspace: a descriptor of each CTA's last unit, then two slots per CTA
+  static constexpr size_t kDesc = size_t(kMaxSms) * sizeof(int4);
+  static constexpr size_t kSlot = size_t(2) * kRows * (D + 2);          // floats
+  static constexpr size_t kWorkspace = kDesc + size_t(kMaxSms) * 2 * kSlot * 4;
 };
 static_assert(SmemTail<128>::kBytes <= 232448u, "shared memory of one CTA");
 
-// Steps of a tile and its TMEM columns.
+constexpr int kP = 2;                    // buffers of P
+constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
+// TMEM columns of the query tiles
 template <int D>
-struct Step {
-  static constexpr int kKeysPerStep = D == 128 ? 64 : 128;
-  static constexpr int kPer = kKeys / kKeysPerStep;    // steps per key tile
-  static constexpr int kP = D == 128 ? 2 : 1;          // buffers of P
-  static constexpr uint32_t kIdescQK = D == 128 ? tc::kIdescM128N64 : tc::kIdescM128N128;
-  __host__ __device__ static constexpr uint32_t col_o(int i) { return static_cast<uint32_t>(D * i); }
-  __host__ __device__ static constexpr uint32_t col_s(int i) { return static_cast<uint32_t>(2 * D + (256 - D) * i); }
-  __host__ __device__ static constexpr uint32_t col_p(int i, int buf) {
-    return col_s(i) + static_cast<uint32_t>(kKeysPerStep + buf * (kKeysPerStep / 2));
-  }
-  static_assert(col_p(1, kP - 1) + kKeysPerStep / 2 <= kTmemCols, "tensor memory");
+struct Cols {
+  __host__ __device__ static constexpr uint32_t o(int i) { return static_cast<uint32_t>(D * i); }
+  __host__ __device__ static constexpr uint32_t s(int i) { return static_cast<uint32_t>(2 * D + 128 * i); }
+  __host__ __device__ static constexpr uint32_t p(int i, int buf) { return s(i) + 64u + 32u * static_cast<uint32_t>(buf); }
 };
 
+// Barriers and the abort flag by their shared-memory addresses: one register.
 struct Ctx {
-  uint32_t bar0;
-  volatile int* abort_flag;
-  int* dev_err;
+  uint32_t bar0, abort_at;
   __device__ uint32_t bar(int i) const { return bar0 + 8u * static_cast<uint32_t>(i); }
 };
+__device__ __forceinline__ uint32_t load_flag(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_flag(uint32_t addr, uint32_t v) {
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
+// Bounded wait: when it runs out it raises the abort flag, which ends every
+// other wait of the CTA; the error word is set at the CTA's end.
+template <bool kHeedAbort = true>
 __device__ __forceinline__ bool wait_bar(const Ctx& cx, uint32_t bar, uint32_t parity) {
   if (tc::mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if ((it & 127u) == 0) {
-      if (*cx.abort_flag) return false;
+      if (kHeedAbort && load_flag(cx.abort_at) != 0) return false;
       const uint64_t now = tc::global_timer_ns();
       if (t0 == 0) {
         t0 = now;
       } else if (now - t0 > kTimeoutNs) {
-        *cx.abort_flag = 1;
-        atomicExch(cx.dev_err, kDevErrTimeout);
+        store_flag(cx.abort_at, 1u);
         return false;
       }
     }
@@ -172,34 +195,36 @@ __device__ __forceinline__ void codes_to_half(uint32_t x, __half2& lo, __half2& 
   lo = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&bias));
   hi = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
 }
+__device__ __forceinline__ void store16(uint32_t addr, const uint32_t* o) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// The work of a CTA, the same in every thread.
+// A pair of query tiles of one key/value head.
 struct Unit {
   int b, h, len, q_len, R, G;
   int row0, tiles;  // first row, query tiles with rows
   int n[2], n_max;  // key tiles of each query tile
 };
 
-// Keys that a row sees (any row; a row past the last counts as the last).
+// Keys that a row sees (a row past the last counts as the last).
 __device__ __forceinline__ int row_sees(const CacheAttentionArgs& a, const Unit& u, int r) {
   if (!a.causal) return u.len;
   const int tok = min(r, u.R - 1) / u.G;
   return max(u.len - u.q_len + tok + 1, 0);
 }
 
-__device__ __forceinline__ Unit find_unit(const CacheAttentionArgs& a, int pairs, bool* bad) {
+// Entry e of the list of (sequence, pair), without its head.
+__device__ __forceinline__ Unit find_entry(const CacheAttentionArgs& a, int pairs, int e, bool* bad) {
   Unit u;
-  // the last rows of a causal chunk see the most keys: first
-  const int heads = static_cast<int>(a.B) * a.c.H;
-  const int pair = pairs - 1 - static_cast<int>(blockIdx.x) / heads, bh = static_cast<int>(blockIdx.x) % heads;
-  u.b = bh / a.c.H;
-  u.h = bh - u.b * a.c.H;
+  u.b = e / pairs;
+  u.h = 0;
   u.len = static_cast<int>(checked_length(a.lengths[u.b], table_capacity(a.pt.max_pages, a.c.blocks_per_page), bad));
   u.q_len = static_cast<int>(a.q_lengths != nullptr ? checked_length(a.q_lengths[u.b], a.T, bad) : a.T);
   u.G = a.H / a.c.H;
   u.R = u.q_len * u.G;
-  u.row0 = pair * 2 * kRows;
+  u.row0 = (e - u.b * pairs) * 2 * kRows;
   u.tiles = u.row0 >= u.R ? 0 : (u.row0 + kRows >= u.R ? 1 : 2);
   u.n_max = 0;
 #pragma unroll
@@ -210,41 +235,78 @@ __device__ __forceinline__ Unit find_unit(const CacheAttentionArgs& a, int pairs
   return u;
 }
 
-// dk: the step's first key of the key tile
+__device__ __forceinline__ int unit_size(const Unit& u) { return max(u.n_max, 1); }
+
+// A CTA's place in the list, at key tile t of head h of entry e, with `todo`
+// tiles left in its range. The part of the range that lies in this unit is
+// [t, t + n) of its key tiles; a unit that sees no key or has no rows counts as
+// one (its rows still have outputs). The unit is found anew where it is needed:
+// that costs less than the registers to keep it.
+struct Place {
+  int e, h, t, todo;
+};
+struct Part {
+  Unit u;
+  int n, size;
+};
+__device__ __forceinline__ Part part_at(const CacheAttentionArgs& a, int pairs, const Place& p) {
+  bool bad = false;
+  Part x;
+  x.u = find_entry(a, pairs, p.e, &bad);
+  x.u.h = p.h;
+  x.size = unit_size(x.u);
+  x.n = min(x.size - p.t, p.todo);
+  return x;
+}
+__device__ __forceinline__ Place first_place(const int* plan) { return Place{plan[16], plan[17], plan[18], plan[19]}; }
+// Past a part of n tiles.
+__device__ __forceinline__ void place_next(const CacheAttentionArgs& a, Place& p, int n) {
+  p.todo -= n;
+  p.t = 0;
+  if (++p.h == a.c.H) {
+    p.h = 0;
+    ++p.e;
+  }
+}
+// Key tiles of query tile i in the part.
+__device__ __forceinline__ int part_tiles(const Place& p, const Part& x, int i) {
+  return max(min(p.t + x.n, i == 0 ? x.u.n[0] : x.u.n[1]) - p.t, 0);
+}
+
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t off = static_cast<uint32_t>(ks >> 2) * Smem<D>::kSub + static_cast<uint32_t>(ks & 3) * 32u;
-    tc::mma_f16_ss(d_tmem, desc_at(dq, off), desc_at(dk, off), Step<D>::kIdescQK, ks > 0 ? 1u : 0u);
+    const uint32_t sub = static_cast<uint32_t>(ks >> 2), off = static_cast<uint32_t>(ks & 3) * 32u;
+    tc::mma_f16_ss(d_tmem, desc_at(dq, sub * Smem<D>::kSub + off), desc_at(dk, sub * Smem<D>::kSubK + off),
+                   tc::kIdescM128N64, ks > 0 ? 1u : 0u);
   }
 }
-// dv: the step's first 64 keys of the value tile
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t tp, uint64_t dv, bool acc) {
   constexpr uint32_t idesc = D == 128 ? tc::kIdescM128N128 : tc::kIdescM128N64;
 #pragma unroll
-  for (int ks = 0; ks < Step<D>::kKeysPerStep / 16; ++ks) {
-    const uint32_t off = static_cast<uint32_t>(ks >> 2) * Smem<D>::kSubV + static_cast<uint32_t>(ks & 3) * 32u;
-    mma_f16_ts(d_tmem, tp + 8u * static_cast<uint32_t>(ks), desc_at(dv, off), idesc, (acc || ks > 0) ? 1u : 0u);
-  }
+  for (int ks = 0; ks < kKeys / 16; ++ks)
+    mma_f16_ts(d_tmem, tp + 8u * static_cast<uint32_t>(ks), desc_at(dv, 32u * static_cast<uint32_t>(ks)), idesc,
+               (acc || ks > 0) ? 1u : 0u);
 }
 
-// The next 32 key tiles' blocks of a converter warp, one per lane.
+// A block of the cache as a converter lane keeps it.
 struct Window {
   int64_t slot;  // block number in the cache, -1: none
   float ks, vs;
 };
-__device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, const Unit& u, int blk, bool* bad) {
+__device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64_t row_of_table, int h, int len, int blk,
+                                              bool* bad) {
   Window w;
   w.slot = -1;
   w.ks = -1.0f;  // no tokens
   w.vs = 0.0f;
-  if (blk * kCacheBlock < u.len) {
+  if (blk * kCacheBlock < len) {
     const int pg = blk / a.c.blocks_per_page;
-    const int page = a.pt.table[u.b * a.pt.stride + pg];
+    const int page = a.pt.table[row_of_table + pg];
     if (page_ok(page, a.c.num_pages)) {
-      w.slot = block_slot(page, u.h, a.c.H, a.c.blocks_per_page, blk - pg * a.c.blocks_per_page);
+      w.slot = block_slot(page, h, a.c.H, a.c.blocks_per_page, blk - pg * a.c.blocks_per_page);
       w.ks = a.c.ks[w.slot];
       w.vs = a.c.vs[w.slot];
     } else {
@@ -258,6 +320,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const CacheAttentionArgs a, int pairs) {
   using L = Smem<D>;
   using T = SmemTail<D>;
+  using C = Cols<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((tc::smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicExch(a.dev_err, kDevErrSmemAlign);
@@ -267,41 +330,91 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ctx cx;
   cx.bar0 = sbase + L::kOffBar;
-  cx.abort_flag = reinterpret_cast<volatile int*>(smem + T::kOffAbort);
-  cx.dev_err = a.dev_err;
-  tc::griddep_wait();
-  bool bad = false;
-  const Unit u = find_unit(a, pairs, &bad);
+  cx.abort_at = sbase + T::kOffAbort;
   if (threadIdx.x == 0) {
-    if (bad) atomicExch(a.dev_err, kDevErrPage);
-    *cx.abort_flag = 0;
-    const uint32_t tiles = static_cast<uint32_t>(max(u.tiles, 1));
+    store_flag(cx.abort_at, 0u);
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(cx.bar(kBarQFull + s), kRows);
+      tc::mbar_init(cx.bar(kBarQFull + s), 128);
+      tc::mbar_init(cx.bar(kBarQEmpty + s), 2);
       tc::mbar_init(cx.bar(kBarSFull + s), 1);
-      tc::mbar_init(cx.bar(kBarPFull + s), kRows);
       tc::mbar_init(cx.bar(kBarSFree + s), kRows);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s), kRows);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), kRows);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s + 1), 1);
       tc::mbar_init(cx.bar(kBarDrain + s), 1);
+      tc::mbar_init(cx.bar(kBarScale + s), 1);
     }
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < L::kStages; ++s) {
       tc::mbar_init(cx.bar(kBarKFull + s), 128);
-      tc::mbar_init(cx.bar(kBarKEmpty + s), tiles);
+      tc::mbar_init(cx.bar(kBarKEmpty + s), 2);
       tc::mbar_init(cx.bar(kBarVFull + s), 128);
-      tc::mbar_init(cx.bar(kBarVEmpty + s), tiles);
+      tc::mbar_init(cx.bar(kBarVEmpty + s), 2);
     }
-    for (int s = 0; s < kScaleSlots; ++s) tc::mbar_init(cx.bar(kBarScale + s), 4);
+    tc::mbar_init(cx.bar(kBarTop), 4);
     tc::fence_mbar_init();
   }
   if (warp == 2) {
     tc::tmem_alloc(sbase + T::kOffTmem, kTmemCols);
     tc::tmem_relinquish();
   }
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+
+  // this CTA's range of the list: each thread sums a run of entries, a scan over
+  // the threads finds whose run the range begins in
+  int* plan = reinterpret_cast<int*>(smem + T::kOffPlan);
+  bool bad = false;
+  const int entries = static_cast<int>(a.B) * pairs, run = (entries + kThreads - 1) / kThreads;
+  const int e_lo = min(run * static_cast<int>(threadIdx.x), entries), e_hi = min(e_lo + run, entries);
+  int mine = 0;
+  for (int e = e_lo; e < e_hi; ++e) mine += unit_size(find_entry(a, pairs, e, &bad));
+  if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) plan[warp] = incl;
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + T::kOffTmem);
+  int before = incl - mine, W = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += plan[w];
+    W += plan[w];
+  }
+  W *= a.c.H;
+  before *= a.c.H;
+  const int units = entries * a.c.H;
+  // no more CTAs than units, unless each still gets kMinTiles key tiles
+  const int ctas = min(static_cast<int>(gridDim.x), max(units, W / kMinTiles));
+  const int each = W / ctas, extra = W - each * ctas, c = static_cast<int>(blockIdx.x);
+  const int lo = c < ctas ? c * each + min(c, extra) : 0, hi = c < ctas ? lo + each + (c < extra ? 1 : 0) : 0;
+  if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
+    int e = e_lo;
+    for (;; ++e) {
+      const int x = unit_size(find_entry(a, pairs, e, &bad)) * a.c.H;
+      if (lo < before + x) break;
+      before += x;
+    }
+    const int size = unit_size(find_entry(a, pairs, e, &bad)), h = (lo - before) / size;
+    plan[16] = e;
+    plan[17] = h;
+    plan[18] = lo - before - h * size;
+  }
+  if (threadIdx.x == 0) {
+    plan[19] = hi - lo;
+    plan[20] = hi;
+    plan[21] = each;
+    plan[22] = extra;
+    // what stands if a wait runs out, or without work
+    static_cast<int4*>(a.workspace)[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+  __syncthreads();
 
   if (warp < 4) {
     regs_dec<kRegCtl>();
@@ -309,178 +422,305 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       // ------------------------------------------------ MMA issuer of tile i --
       const int i = warp;
       const bool leader = elect_one();
-      using S = Step<D>;
-      const uint32_t d_s = tmem + S::col_s(i), d_o = tmem + S::col_o(i);
-      const uint64_t dq = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
+      const uint32_t d_s = tmem + C::s(i), d_o = tmem + C::o(i);
+      const uint64_t dq0 = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dv0 = tc::sw128_desc(sbase + L::kOffV);
-      const int n = u.n[i] * S::kPer, n_all = u.n_max * S::kPer;  // steps of this tile, and of the CTA
-      bool ok = i < u.tiles;
-      if (ok && n > 0) ok = wait_bar_warp(cx, cx.bar(kBarQFull + i), 0);
-      for (int j = 0; ok && j <= n_all; ++j) {
-        if (j < n_all) {
-          // QK_j once its keys are there and the softmax has read S_{j-1}
-          const int tile = j / S::kPer, in = j % S::kPer;
-          const uint32_t s = static_cast<uint32_t>(tile) % kStages, ph = (static_cast<uint32_t>(tile) / kStages) & 1u;
-          if (in == 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarKFull + s), ph))) break;
-          if (j < n) {
-            if (j > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), static_cast<uint32_t>(j - 1) & 1u))) break;
-            tc::tc_fence_after();
-            if (leader) {
-              issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTile + static_cast<uint32_t>(in * S::kKeysPerStep) * 128u));
-              tc::mma_commit(cx.bar(kBarSFull + i));
-              if (in == S::kPer - 1) tc::mma_commit(cx.bar(kBarKEmpty + s));
+      // key tiles (keys, values, those of this query tile) and parts so far
+      uint32_t k_cnt = 0, v_cnt = 0, steps = 0, q_cnt = 0;
+      bool ok = true;
+      Place p = first_place(plan);
+      while (ok && p.todo > 0) {
+        const Part x = part_at(a, pairs, p);
+        const int n = part_tiles(p, x, i);                                // of this query tile
+        const int n_all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));  // of the converters
+        place_next(a, p, x.n);
+        if (n_all == 0) continue;
+        const uint32_t qb = q_cnt % L::kQ;
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarQFull + static_cast<int>(qb)), (q_cnt / L::kQ) & 1u))) break;
+        ++q_cnt;
+        if (n == 0 && leader) tc::mbar_arrive(cx.bar(kBarQEmpty + static_cast<int>(qb)));
+        const uint64_t dq = desc_at(dq0, qb * 2u * L::kTile);
+        for (int j = 0; j <= n_all; ++j) {
+          if (j < n_all) {
+            // QK_j once its keys are there and the softmax has read S_{j-1}
+            const uint32_t s = k_cnt % L::kStages;
+            if (!(ok = wait_bar_warp(cx, cx.bar(kBarKFull + static_cast<int>(s)), (k_cnt / L::kStages) & 1u))) break;
+            ++k_cnt;
+            if (j < n) {
+              const uint32_t st = steps + static_cast<uint32_t>(j);
+              if (st > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), (st - 1u) & 1u))) break;
+              tc::tc_fence_after();
+              if (leader) {
+                // the tile's scales are there as well (and the softmax has read the last tile's)
+                tc::mbar_arrive(cx.bar(kBarScale + i));
+                issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTileKV));
+                tc::mma_commit(cx.bar(kBarSFull + i));
+                tc::mma_commit(cx.bar(kBarKEmpty + static_cast<int>(s)));
+                if (j == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
+              }
+            } else if (leader) {
+              tc::mbar_arrive(cx.bar(kBarKEmpty + static_cast<int>(s)));  // no row of this tile sees the keys
             }
-          } else if (leader && in == S::kPer - 1) {
-            tc::mbar_arrive(cx.bar(kBarKEmpty + s));  // no row of this tile sees the keys
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        if (j >= 1) {
-          // PV_{j-1} once its values and P_{j-1} are there
-          const int jj = j - 1, tile = jj / S::kPer, in = jj % S::kPer;
-          const uint32_t s = static_cast<uint32_t>(tile) % kStages, ph = (static_cast<uint32_t>(tile) / kStages) & 1u;
-          if (in == 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarVFull + s), ph))) break;
-          if (jj < n) {
-            if (!(ok = wait_bar_warp(cx, cx.bar(kBarPFull + i), static_cast<uint32_t>(jj) & 1u))) break;
-            tc::tc_fence_after();
-            if (leader) {
-              issue_pv<D>(d_o, tmem + S::col_p(i, jj % S::kP),
-                          desc_at(dv0, s * L::kTileV + static_cast<uint32_t>(in) * (S::kKeysPerStep / 64) * L::kSubV),
-                          jj > 0);
-              tc::mma_commit(cx.bar(kBarPVDone + 2 * i + jj % S::kP));
-              if (in == S::kPer - 1) tc::mma_commit(cx.bar(kBarVEmpty + s));
+          if (j >= 1) {
+            // PV_{j-1} once its values and P_{j-1} are there
+            const uint32_t s = v_cnt % L::kStages;
+            if (!(ok = wait_bar_warp(cx, cx.bar(kBarVFull + static_cast<int>(s)), (v_cnt / L::kStages) & 1u))) break;
+            ++v_cnt;
+            if (j - 1 < n) {
+              const uint32_t st = steps + static_cast<uint32_t>(j) - 1u;
+              // (a barrier per P buffer: the softmax may be two tiles ahead of this wait)
+              const int pb = static_cast<int>(st % kP);
+              if (!(ok = wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + pb), (st / kP) & 1u))) break;
+              tc::tc_fence_after();
+              if (leader) {
+                issue_pv<D>(d_o, tmem + C::p(i, pb), desc_at(dv0, s * L::kTileKV), j > 1);
+                tc::mma_commit(cx.bar(kBarPVDone + 2 * i + pb));
+                tc::mma_commit(cx.bar(kBarVEmpty + static_cast<int>(s)));
+              }
+            } else if (leader) {
+              tc::mbar_arrive(cx.bar(kBarVEmpty + static_cast<int>(s)));
             }
-          } else if (leader && in == S::kPer - 1) {
-            tc::mbar_arrive(cx.bar(kBarVEmpty + s));
+            __syncwarp();
           }
-          __syncwarp();
         }
+        steps += static_cast<uint32_t>(n);
       }
       // all MMAs of this warp complete before TMEM is freed
       if (leader) tc::mma_commit(cx.bar(kBarDrain + i));
       __syncwarp();
-      Ctx drain = cx;
-      volatile int no_abort = 0;
-      drain.abort_flag = &no_abort;
-      wait_bar(drain, cx.bar(kBarDrain + i), 0);
+      wait_bar<false>(cx, cx.bar(kBarDrain + i), 0);
     }
     __syncwarp();
   } else if (warp >= 12) {
     // ------------------------------------------------------------ converters --
     regs_dec<kRegConv>();
-    const int w = warp - 12;  // block of each key tile
-    // the largest value scale of the unit's blocks (NaN passes)
-    float top = 0.0f;
-    bool bad_page = false;
-    for (int t = lane; t < u.n_max; t += 32) top = fmaxf(top, load_window(a, u, t * 4 + w, &bad_page).vs);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float* tops = reinterpret_cast<float*>(smem + T::kOffTop);
-    if (lane == 0) tops[w] = top;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    const float inv_top = top > 0.0f ? 1.0f / top : 0.0f;
-    // Load x of the warp. Keys: tokens 8 (x mod 4) + lane / 4 of 64-channel half
-    // x / 4, channels 16 (lane mod 4) and up. Values: channel 16 x + v_ch,
-    // positions 16 (lane mod 2) and up, where v_ch is lane / 2 with its bits 1
-    // and 2 exchanged: the 8 lanes of a store phase then write channels c, c + 1,
-    // c + 4, c + 5, whose swizzled chunks are all different.
+    const int w = warp - 12, blk = w & 1, part2 = w >> 1;  // block of each key tile, half of its codes
+    // Load x of the warp, of kLoads. Keys: 8 tokens of one 64-channel half,
+    // channels 16 (lane mod 4) and up of token lane / 4. Values: 16 channels,
+    // positions 16 (lane mod 2) and up of channel v_ch, which is lane / 2 with
+    // its bits 1 and 2 exchanged: the 8 lanes of a store phase then write
+    // channels c, c + 1, c + 4, c + 5, whose swizzled chunks are all different.
+    constexpr int kLoads = D / 32;
     const int v_ch = ((lane >> 1) & 9) | ((lane >> 1) & 2) << 1 | ((lane >> 1) & 4) >> 1;
     const int v_at = 2 * v_ch + (lane & 1);
+    uint4 kr[kLoads], vr[kLoads];  // raw codes: 512 bytes per load of the warp
+    float* tops = reinterpret_cast<float*>(smem + T::kOffTop);
+    bool bad_page = false, ok = true;
+    // the tile that is fetched next: tile t of t_end of the unit at `p`
+    Place p = first_place(plan);
+    int t = 0, t_end = 0, n = 0, len = 0;
+    int64_t row_of_table = 0;
+    uint32_t windows = 0, parts = 0;
     Window win{-1, -1.0f, 0.0f};
-    uint4 kr[D / 16], vr[D / 16];  // raw codes of the block: 512 bytes per load of the warp
-    // window lane t holds key tile t mod 32; loads of a block that is not there read nothing
-    const auto fetch = [&](int j, const int8_t* base, int at, uint4 (&r)[D / 16]) {
-      const int64_t slot = __shfl_sync(0xffffffffu, win.slot, j & 31);
-      const uint4* p = reinterpret_cast<const uint4*>(base + slot * (kCacheBlock * D)) + at;
+    int64_t slot = -1;
+    float ks = 0.0f, vs = 0.0f, top = 0.0f, factor = 1.0f;
+    int in_window = 0, head = 0;
+    // R of the next 32 tiles: the largest value scale so far (NaN passes)
+    const auto open_window = [&](bool fresh) {
+      win = load_window(a, row_of_table, head, len, (t + lane) * kB + blk, &bad_page);
+      float x = t + lane < t_end ? fmaxf(win.vs, 0.0f) : 0.0f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) r[x] = slot >= 0 ? p[x * 32] : make_uint4(0u, 0u, 0u, 0u);
+      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      const float* buf = tops + 4 * (windows & 1u);
+      if (lane == 0) {
+        tops[4 * (windows & 1u) + w] = x;
+        tc::mbar_arrive(cx.bar(kBarTop));
+      }
+      if (!wait_bar_warp(cx, cx.bar(kBarTop), windows & 1u)) ok = false;
+      ++windows;
+      x = fmaxf(fmaxf(buf[0], buf[1]), fmaxf(buf[2], buf[3]));
+      factor = 1.0f;
+      if (fresh) {
+        top = x;
+      } else if (x > top) {
+        factor = top / x;
+        top = x;
+      }
+      in_window = 0;
     };
-    if (u.n_max > 0) {
-      win = load_window(a, u, lane * 4 + w, &bad_page);
-      fetch(0, a.c.k, lane, kr);
-      fetch(0, a.c.v, v_at, vr);
-    }
-    bool ok = true;
-    for (int j = 0; ok && j < u.n_max; ++j) {
-      const uint32_t s = static_cast<uint32_t>(j) % kStages, ph = (static_cast<uint32_t>(j) / kStages) & 1u;
-      const float ks = __shfl_sync(0xffffffffu, win.ks, j & 31);
-      const float vs = __shfl_sync(0xffffffffu, win.vs, j & 31);
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarKEmpty + s), ph ^ 1u))) break;
-      const uint32_t k_row = sbase + L::kOffK + s * L::kTile;
+    const auto pick = [&]() {
+      slot = __shfl_sync(0xffffffffu, win.slot, in_window);
+      ks = __shfl_sync(0xffffffffu, win.ks, in_window);
+      vs = __shfl_sync(0xffffffffu, win.vs, in_window);
+    };
+    // The queries of a unit to fp16, times a power of two per row, in the
+    // swizzled layout: four lanes share a row, 32 rows at a time.
+    const auto bring_queries = [&](const Unit& u) {
+      const uint32_t qb = parts % L::kQ;
+      if (!wait_bar_warp(cx, cx.bar(kBarQEmpty + static_cast<int>(qb)), ((parts / L::kQ) & 1u) ^ 1u)) {
+        ok = false;
+        return;
+      }
+      float* rows = reinterpret_cast<float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
+      ++parts;
+      const int g = lane >> 2, c4 = lane & 3;
+      const uint16_t* base = a.q.p + u.b * a.q.sb + c4 * 16;
+#pragma unroll 2
+      for (int it = 0; it < 8; ++it) {
+        const int rr = it * 32 + w * 8 + g, r = u.row0 + rr;
+        uint32_t x[D / 64][8];
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const int n = lane >> 2, row = w * 32 + 8 * (n >> 1) + 2 * (x & 3) + (n & 1);  // value_position of token 8x + n
-          const uint32_t cw[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint4 lo4 = make_uint4(0u, 0u, 0u, 0u), hi4 = lo4;
+          if (r < u.R) {
+            const int tok = r / u.G;
+            const uint4* src = reinterpret_cast<const uint4*>(base + tok * a.q.ss + (u.h * u.G + r - tok * u.G) * a.q.sh + hf * 64);
+            lo4 = src[0];
+            hi4 = src[1];
+          }
+          *reinterpret_cast<uint4*>(x[hf]) = lo4;
+          *reinterpret_cast<uint4*>(x[hf] + 4) = hi4;
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = max(amax, max(x[hf][e] & 0x7FFFu, (x[hf][e] >> 16) & 0x7FFFu));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        uint32_t ex = amax >> 7;
+        ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
+        const float down = __uint_as_float((254u - ex) << 23);
+        if (c4 == 0) rows[rr] = __uint_as_float(ex << 23);
+        const uint32_t at = sbase + L::kOffQ + (qb * 2u + static_cast<uint32_t>(rr >> 7)) * L::kTile +
+                            static_cast<uint32_t>(rr & 127) * 128u;
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf) {
           uint32_t o[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            __half2 lo, hi;
-            codes_to_half(cw[e], lo, hi);
-            o[2 * e] = bits(lo);
-            o[2 * e + 1] = bits(hi);
-          }
-          const uint32_t at = k_row + static_cast<uint32_t>(x >> 2) * L::kSub + static_cast<uint32_t>(row) * 128u;
-          const uint32_t c = static_cast<uint32_t>(lane & 3) * 2u, sw = static_cast<uint32_t>(row) & 7u;
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c ^ sw) << 4)), "r"(o[0]), "r"(o[1]),
-                       "r"(o[2]), "r"(o[3])
-                       : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c + 1u) ^ sw) << 4)), "r"(o[4]), "r"(o[5]),
-                       "r"(o[6]), "r"(o[7])
-                       : "memory");
+          for (int e = 0; e < 8; ++e)
+            o[e] = pack_half2(__uint_as_float(x[hf][e] << 16) * down, __uint_as_float(x[hf][e] & 0xFFFF0000u) * down);
+          const uint32_t ch = static_cast<uint32_t>(c4) * 2u, sw = static_cast<uint32_t>(rr) & 7u;
+          store16(at + static_cast<uint32_t>(hf) * L::kSub + ((ch ^ sw) << 4), o);
+          store16(at + static_cast<uint32_t>(hf) * L::kSub + (((ch + 1u) ^ sw) << 4), o + 4);
         }
-      if (lane == 0) {
-        // a value scale that is NaN makes the rows that see the block NaN through their logits
-        reinterpret_cast<float*>(smem + T::kOffScale)[(j % kScaleSlots) * 4 + w] = vs != vs ? vs : ks;
-        tc::mbar_arrive(cx.bar(kBarScale + j % kScaleSlots));
       }
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarKFull + s));
-      // the next tile's window and keys
-      if (j + 1 < u.n_max) {
-        if (((j + 1) & 31) == 0) win = load_window(a, u, (j + 1 + lane) * 4 + w, &bad_page);
-        fetch(j + 1, a.c.k, lane, kr);
+      tc::mbar_arrive(cx.bar(kBarQFull + static_cast<int>(qb)));
+    };
+    // opens the first unit from p on that has tiles; false at the end of the range
+    const auto open_part = [&]() {
+      while (p.todo > 0) {
+        const Part x = part_at(a, pairs, p);
+        n = x.n;
+        const int tiles = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
+        if (tiles > 0) {
+          t = p.t;
+          t_end = p.t + tiles;
+          len = x.u.len;
+          head = x.u.h;
+          row_of_table = x.u.b * a.pt.stride;
+          open_window(true);
+          pick();
+          if (ok) bring_queries(x.u);
+          return true;
+        }
+        place_next(a, p, n);
       }
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarVEmpty + s), ph ^ 1u))) break;
+      return false;
+    };
+    const auto advance = [&]() {
+      factor = 1.0f;
+      if (++t < t_end) {
+        if (++in_window == 32) open_window(false);
+        pick();
+        return true;
+      }
+      place_next(a, p, n);
+      return open_part();
+    };
+    const auto fetch = [&](const int8_t* base, int at, uint4 (&r)[kLoads]) {
+      const uint4* src = reinterpret_cast<const uint4*>(base + slot * (kCacheBlock * D)) + part2 * kLoads * 32 + at;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) r[x] = slot >= 0 ? src[x * 32] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    bool more = open_part();
+    if (more) {
+      fetch(a.c.k, lane, kr);
+      fetch(a.c.v, v_at, vr);
+    }
+    for (uint32_t cnt = 0; ok && more; ++cnt) {
+      const uint32_t s = cnt % L::kStages, ph = (cnt / L::kStages) & 1u;
+      if (!(ok = wait_bar_warp(cx, cx.bar(kBarKEmpty + static_cast<int>(s)), ph ^ 1u))) break;
+      const uint32_t k_row = sbase + L::kOffK + s * L::kTileKV;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) {
+        // eight tokens j8 of a 64-channel half: the warp's 4 of half part2, or (D = 64) its two of the block
+        const int j8 = D == 128 ? x : part2 * 2 + x, hf = D == 128 ? part2 : 0;
+        const int n8 = lane >> 2, row = blk * 32 + 8 * (n8 >> 1) + 2 * j8 + (n8 & 1);  // value_position of token 8 j8 + n8
+        const uint32_t cw[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          __half2 lo2, hi2;
+          codes_to_half(cw[e], lo2, hi2);
+          o[2 * e] = bits(lo2);
+          o[2 * e + 1] = bits(hi2);
+        }
+        const uint32_t at = k_row + static_cast<uint32_t>(hf) * L::kSubK + static_cast<uint32_t>(row) * 128u;
+        const uint32_t ch = static_cast<uint32_t>(lane & 3) * 2u, sw = static_cast<uint32_t>(row) & 7u;
+        store16(at + ((ch ^ sw) << 4), o);
+        store16(at + (((ch + 1u) ^ sw) << 4), o + 4);
+      }
+      if (lane == 0) {
+        float* ring = reinterpret_cast<float*>(smem + T::kOffScale) + (cnt % kScaleSlots) * 4;
+        // a value scale that is NaN makes the rows that see the block NaN through their logits
+        if (part2 == 0) ring[blk] = vs != vs ? vs : ks;
+        else ring[2 + blk] = blk == 0 ? factor : top;
+      }
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(cx.bar(kBarKFull + static_cast<int>(s)));
+      const float vs_now = vs, top_now = top;
+      // the next tile of the unit; the next unit only once this one's values are out
+      const bool last = t + 1 >= t_end;
+      if (!last) {
+        advance();
+        if (!ok) break;
+        fetch(a.c.k, lane, kr);
+      }
+      if (!(ok = wait_bar_warp(cx, cx.bar(kBarVEmpty + static_cast<int>(s)), ph ^ 1u))) break;
       // fp16(s_v / R) below 2^-14 would lose bits: the power of two comes off after the product then
-      float h = vs == vs ? vs * inv_top : 0.0f, shift = 1.0f;
+      float h = (vs_now == vs_now && top_now > 0.0f) ? vs_now / top_now : 0.0f, shift = 1.0f;
       if (h < 6.1035156e-05f) {
         h *= 16384.0f;
         shift = 6.1035156e-05f;
       }
       const __half2 h2 = __float2half2_rn(h), shift2 = __float2half2_rn(shift);
-      const uint32_t v_row = sbase + L::kOffV + s * L::kTileV + static_cast<uint32_t>(w >> 1) * L::kSubV;
+      const uint32_t v_row = sbase + L::kOffV + s * L::kTileKV;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const int ch = 16 * x + v_ch;
+      for (int x = 0; x < kLoads; ++x) {
+        const int ch = 16 * (part2 * kLoads + x) + v_ch;
         const uint32_t cw[4] = {vr[x].x, vr[x].y, vr[x].z, vr[x].w};
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          __half2 lo, hi;
-          codes_to_half(cw[e], lo, hi);
-          lo = __hmul2(lo, h2);
-          hi = __hmul2(hi, h2);
+          __half2 lo2, hi2;
+          codes_to_half(cw[e], lo2, hi2);
+          lo2 = __hmul2(lo2, h2);
+          hi2 = __hmul2(hi2, h2);
           if (shift != 1.0f) {
-            lo = __hmul2(lo, shift2);
-            hi = __hmul2(hi, shift2);
+            lo2 = __hmul2(lo2, shift2);
+            hi2 = __hmul2(hi2, shift2);
           }
-          o[2 * e] = bits(lo);
-          o[2 * e + 1] = bits(hi);
+          o[2 * e] = bits(lo2);
+          o[2 * e + 1] = bits(hi2);
         }
         const uint32_t at = v_row + static_cast<uint32_t>(ch) * 128u;
-        const uint32_t c = static_cast<uint32_t>(w & 1) * 4u + static_cast<uint32_t>(lane & 1) * 2u;
+        const uint32_t chunk = static_cast<uint32_t>(blk) * 4u + static_cast<uint32_t>(lane & 1) * 2u;
         const uint32_t sw = static_cast<uint32_t>(ch) & 7u;
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c ^ sw) << 4)), "r"(o[0]), "r"(o[1]),
-                     "r"(o[2]), "r"(o[3])
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c + 1u) ^ sw) << 4)), "r"(o[4]), "r"(o[5]),
-                     "r"(o[6]), "r"(o[7])
-                     : "memory");
+        store16(at + ((chunk ^ sw) << 4), o);
+        store16(at + (((chunk + 1u) ^ sw) << 4), o + 4);
       }
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarVFull + s));
-      if (j + 1 < u.n_max) fetch(j + 1, a.c.v, v_at, vr);
+      tc::mbar_arrive(cx.bar(kBarVFull + static_cast<int>(s)));
+      if (last) {
+        more = advance();
+        if (!ok) break;
+        if (more) fetch(a.c.k, lane, kr);
+      }
+      if (more) fetch(a.c.v, v_at, vr);
     }
     if (bad_page) atomicExch(a.dev_err, kDevErrPage);
     __syncwarp();
@@ -489,215 +729,225 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     // --------------------------------------------------------------- softmax --
     regs_inc<kRegSoftmax>();
     const int i = (warp - 4) >> 2, wq = warp & 3;
-    const int r = u.row0 + i * kRows + wq * 32 + lane;  // this thread's row
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    using S = Step<D>;
-    const uint32_t tS = tmem + lane_addr + S::col_s(i), tO = tmem + lane_addr + S::col_o(i);
-    const bool real = r < u.R;
-    const int tok = r / u.G, head = u.h * u.G + r - tok * u.G;
-    const int sees = real ? row_sees(a, u, r) : 0;
-    bool ok = i < u.tiles;
-    float m = -INFINITY, l = 0.0f, f = 0.0f;
-    if (ok && u.n[i] > 0) {
-      // the row's queries to fp16, times a power of two, in the swizzled layout
-      const uint32_t q_row = sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile + static_cast<uint32_t>(wq * 32 + lane) * 128u;
-      uint4 x[D / 8];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        x[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (real) x[c] = reinterpret_cast<const uint4*>(a.q.p + u.b * a.q.sb + tok * a.q.ss + head * a.q.sh)[c];
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = max(amax, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-      }
-      uint32_t ex = amax >> 7;
-      ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
-      const float down = __uint_as_float((254u - ex) << 23);
-      f = __uint_as_float(ex << 23) * a.sm_log2;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_half2(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xFFFF0000u) * down);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                         q_row + static_cast<uint32_t>(c >> 3) * L::kSub + (((c & 7) ^ (lane & 7)) << 4)),
-                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                     : "memory");
-      }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarQFull + i));
-    }
-    // the smallest limit in the warp decides, for all its lanes, whether a tile is masked
-    const int all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
-    const float* scale_ring = reinterpret_cast<const float*>(smem + T::kOffScale);
-    constexpr int kB = S::kKeysPerStep / kCacheBlock;  // blocks of a step
-    const int n = u.n[i] * S::kPer;
-    float k4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // scales of the key tile
+    const uint32_t tS = tmem + lane_addr + C::s(i), tO = tmem + lane_addr + C::o(i);
+    const float* ring = reinterpret_cast<const float*>(smem + T::kOffScale);
+    const int rr = i * kRows + wq * 32 + lane;  // this thread's row of a pair
+    bool ok = true;
+    uint32_t steps = 0, tile_cnt = 0, parts = 0;  // key tiles of this query tile; of the converters, and their units
     // waits for the PV of step x (its P buffer and O are then free)
-    const auto wait_pv = [&](int x) {
-      return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + x % S::kP), static_cast<uint32_t>(x / S::kP) & 1u);
+    const auto wait_pv = [&](uint32_t x) {
+      return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + static_cast<int>(x % kP)), (x / kP) & 1u);
     };
-    for (int j = 0; ok && j < n; ++j) {
-      const int tile = j / S::kPer, in = j % S::kPer;
-      if (in == 0) {
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + tile % kScaleSlots), static_cast<uint32_t>(tile / kScaleSlots) & 1u)))
-          break;
-        const float4 ks = *reinterpret_cast<const float4*>(scale_ring + (tile % kScaleSlots) * 4);
-        k4[0] = ks.x;
-        k4[1] = ks.y;
-        k4[2] = ks.z;
-        k4[3] = ks.w;
+    Place p = first_place(plan);
+    while (p.todo > 0) {
+      int n, all, sees;
+      bool real;
+      {
+        const Part x = part_at(a, pairs, p);
+        const int r = x.u.row0 + rr;
+        real = r < x.u.R;
+        sees = real ? row_sees(a, x.u, r) : 0;
+        n = part_tiles(p, x, i);
+        all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
       }
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), static_cast<uint32_t>(j) & 1u))) break;
-      tc::tc_fence_after();
-      uint32_t sr[kB][32];
+      float m = -INFINITY, l = 0.0f, f = 0.0f, top = 0.0f;
+      const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
+      // the smallest limit in the warp decides, for all its lanes, whether a step is masked
+      const int all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
+      for (int j = 0; ok && j < n; ++j) {
+        const uint32_t st = steps + static_cast<uint32_t>(j);
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + i), st & 1u))) break;
+        // two key scales, what O has to be multiplied with, R
+        const float4 sc = *reinterpret_cast<const float4*>(ring + ((tile_cnt + static_cast<uint32_t>(j)) % kScaleSlots) * 4);
+        if (j == 0) f = rows[rr] * a.sm_log2;
+        top = sc.w;
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), st & 1u))) break;
+        tc::tc_fence_after();
+        uint32_t sr[kB][32];
 #pragma unroll
-      for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
-      tc::tmem_wait_ld();
-      tc::tc_fence_before();
-      tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
-      float cb[kB];
-      int lim[kB];  // tokens of each block that the row sees
-      bool masked = (j + 1) * S::kKeysPerStep > all_see;
+        for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
+        const int key0 = (p.t + j) * kKeys;
+        float cb[kB];
+        int lim[kB];  // tokens of each block that the row sees
+        bool masked = key0 + kKeys > all_see;
 #pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        const float k = kB == 4 || in == 0 ? k4[b] : k4[(b + 2) & 3];
-        cb[b] = f * k;
-        lim[b] = k < 0.0f ? 0 : sees - j * S::kKeysPerStep - 32 * b;
-        masked |= k < 0.0f;
-      }
-      float mt = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
+        for (int b = 0; b < kB; ++b) {
+          const float k = b == 0 ? sc.x : sc.y;
+          cb[b] = f * k;
+          lim[b] = k < 0.0f ? 0 : sees - key0 - 32 * b;
+          masked |= k < 0.0f;
         }
-        float m0 = __uint_as_float(sr[b][0]), m1 = __uint_as_float(sr[b][1]);
+        float mt = -INFINITY;
 #pragma unroll
-        for (int c = 2; c < 30; c += 4) {
-          m0 = max3(m0, __uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1]));
-          m1 = max3(m1, __uint_as_float(sr[b][c + 2]), __uint_as_float(sr[b][c + 3]));
-        }
-        m0 = max3(m0, __uint_as_float(sr[b][30]), __uint_as_float(sr[b][31]));
-        m0 = fmaxf(m0, m1);
-        mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
-      }
-      if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-        const float up = fmaxf(m, mt);
-        const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
-        m = up;
-        l *= alpha;
-        if (j > 0) {
-          if (!(ok = wait_pv(j - 1))) break;  // O is at rest
-          tc::tc_fence_after();
-          const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + 32u * c, o);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), a2);
-              o[k] = __float_as_uint(y.x);
-              o[k + 1] = __float_as_uint(y.y);
-            }
-            tc::tmem_st32(tO + 32u * c, o);
-          }
-        }
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-      const float2 n2 = make_float2(-ref, -ref);
-      float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-      uint32_t pw[kB / 2][32];
-#pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        const float2 c2 = make_float2(cb[b], cb[b]);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
-          float2 p = make_float2(ex2(y.x), ex2(y.y));
+        for (int b = 0; b < kB; ++b) {
           if (masked) {
-            if (value_token(c) >= lim[b]) p.x = 0.0f;
-            if (value_token(c + 1) >= lim[b]) p.y = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
           }
-          if (c & 2) sb = __fadd2_rn(sb, p);
-          else sa = __fadd2_rn(sa, p);
-          pw[b / 2][16 * (b & 1) + c / 2] = pack_half2(p.x, p.y);
+          float m0 = __uint_as_float(sr[b][0]), m1 = __uint_as_float(sr[b][1]);
+#pragma unroll
+          for (int c = 2; c < 30; c += 4) {
+            m0 = max3(m0, __uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1]));
+            m1 = max3(m1, __uint_as_float(sr[b][c + 2]), __uint_as_float(sr[b][c + 3]));
+          }
+          m0 = max3(m0, __uint_as_float(sr[b][30]), __uint_as_float(sr[b][31]));
+          m0 = fmaxf(m0, m1);
+          mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
         }
+        if (__any_sync(0xffffffffu, mt > m + kLazy) || sc.z != 1.0f) {
+          const float up = fmaxf(m, mt);
+          const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
+          m = up;
+          l *= alpha;
+          if (j > 0) {
+            if (!(ok = wait_pv(st - 1u))) break;  // O is at rest
+            tc::tc_fence_after();
+            const float y = alpha * sc.z;
+            const float2 a2 = make_float2(y, y);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::tmem_ld32(tO + 32u * c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 y2 = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), a2);
+                o[k] = __float_as_uint(y2.x);
+                o[k + 1] = __float_as_uint(y2.y);
+              }
+              tc::tmem_st32(tO + 32u * c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        const float2 n2 = make_float2(-ref, -ref);
+        float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
+        uint32_t pw[32];
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const float2 c2 = make_float2(cb[b], cb[b]);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
+            float2 pp = make_float2(ex2(y.x), ex2(y.y));
+            if (masked) {
+              if (value_token(c) >= lim[b]) pp.x = 0.0f;
+              if (value_token(c + 1) >= lim[b]) pp.y = 0.0f;
+            }
+            if (c & 2) sb = __fadd2_rn(sb, pp);
+            else sa = __fadd2_rn(sa, pp);
+            pw[16 * b + c / 2] = pack_half2(pp.x, pp.y);
+          }
+        }
+        l += (sa.x + sa.y) + (sb.x + sb.y);
+        if (st >= kP) {
+          if (!(ok = wait_pv(st - kP))) break;  // the buffer's last PV has read it
+          tc::tc_fence_after();
+        }
+        const uint32_t tP = tmem + lane_addr + C::p(i, static_cast<int>(st % kP));
+        tc::tmem_st32(tP, pw);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)));
       }
-      l += (sa.x + sa.y) + (sb.x + sb.y);
-      if (j >= S::kP) {
-        if (!(ok = wait_pv(j - S::kP))) break;  // the buffer's last PV has read it
+      if (!ok) break;
+      steps += static_cast<uint32_t>(n);
+      tile_cnt += static_cast<uint32_t>(all);
+      parts += all > 0 ? 1u : 0u;
+
+      // the part's rows: to the output, or to the workspace
+      const Part x = part_at(a, pairs, p);
+      const Unit& u = x.u;
+      const int r = u.row0 + rr, tok = r / u.G, head = u.h * u.G + r - tok * u.G;
+      if (n > 0) {
+        if (!(ok = wait_pv(steps - 1u))) break;
         tc::tc_fence_after();
       }
-      const uint32_t tP = tmem + lane_addr + S::col_p(i, j % S::kP);
-#pragma unroll
-      for (int x = 0; x < kB / 2; ++x) tc::tmem_st32(tP + 32u * x, pw[x]);
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-      tc::mbar_arrive(cx.bar(kBarPFull + i));
-    }
-    // epilogue
-    if (ok && n > 0) {
-      ok = wait_pv(n - 1);
-      tc::tc_fence_after();
-    }
-    const float* tops = reinterpret_cast<const float*>(smem + T::kOffTop);
-    if (!real) l = 0.0f;
-    if (ok || i >= u.tiles) {
-      const bool empty = i >= u.tiles || u.n[i] == 0;
-      const bool pad = !real && a.zero_rest && r < static_cast<int>(a.T) * u.G;
-      const float top = empty ? 0.0f : fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-      const float inv = l == 0.0f ? 0.0f : top / l;
+      const bool whole = x.n == x.size;
+      const int which = p.todo == plan[19] ? 0 : 1;
+      if (p.todo == x.n && threadIdx.x == 128 && p.t == 0 && x.size > x.n) {
+        // the last unit begins here and goes on in other CTAs: up to which one, and whose rows
+        const int end = plan[20] + x.size - x.n - 1, each = plan[21], extra = plan[22], head_units = extra * (each + 1);
+        static_cast<int4*>(a.workspace)[blockIdx.x] =
+            make_int4(end < head_units ? end / (each + 1) : extra + (end - head_units) / each, u.b, 2 * u.h + which,
+                      u.row0);
+      }
+      const bool pad = !real && a.zero_rest && p.t == 0 && r < static_cast<int>(a.T) * u.G;
+      if (!real) l = 0.0f;
+      const bool none = n == 0 || !real;
+      const bool to_out = whole ? real || pad : pad;
+      float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + T::kDesc) +
+                    (static_cast<size_t>(blockIdx.x) * 2 + which) * T::kSlot;
+      // l = 0: no key was seen
+      const float scale = none || l == 0.0f ? 0.0f : (whole ? top / l : top);
       uint16_t* dst = a.out.p + u.b * a.out.sb + tok * a.out.ss + head * a.out.sh;
-      if (a.lse != nullptr && (real || pad))
+      if (to_out && a.lse != nullptr)
         a.lse[(static_cast<int64_t>(u.b) * a.H + head) * a.T + tok] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (!whole && real) *reinterpret_cast<float2*>(part + 2 * kRows * D + 2 * rr) = make_float2(m, l);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
-        if (!empty) {
-          tc::tmem_ld32(tO + 32u * c, o);
+        if (n > 0) {
+          tc::tmem_ld32(tO + 32u * cc, o);
           tc::tmem_wait_ld();
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+        for (int k = 0; k < 32; ++k)
+          o[k] = (none || l == 0.0f) ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
+        if (to_out) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = (empty || l == 0.0f) ? 0.0f : __uint_as_float(o[8 * k + 2 * e]) * inv;
-            const float y = (empty || l == 0.0f) ? 0.0f : __uint_as_float(o[8 * k + 2 * e + 1]) * inv;
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                             __uint_as_float(o[8 * k + 2 * e + 1]));
+              w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(dst + 32 * cc + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (real || pad) *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (real) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(part + rr * D + 32 * cc + 4 * k) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
+      tc::tc_fence_before();
+      place_next(a, p, x.n);
     }
-    tc::tc_fence_before();
     __syncwarp();
     regs_dec<kRegCtl>();
   }
   tc::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && load_flag(cx.abort_at) != 0) atomicExch(a.dev_err, kDevErrTimeout);
   if (warp == 2) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, kTmemCols);
+    tc::tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(smem + T::kOffTmem), kTmemCols);
   }
 }
 
 }  // namespace
 
+size_t cache_attention_tc_workspace_bytes(int64_t D) {
+  return D == 128 ? SmemTail<128>::kWorkspace : SmemTail<64>::kWorkspace;
+}
+
 cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream) {
   const int64_t rows = a.T * (a.H / a.c.H);
   const int64_t pairs = div_up(rows, 2 * kRows);
+  const int64_t tiles = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kKeys + 1;
   const int64_t units = pairs * a.B * a.c.H;
-  if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int sms = sm_count_current() < kMaxSms ? sm_count_current() : kMaxSms;
+  // what the tables can name bounds the work: no CTA without any
+  const int64_t want = units > tiles * units / kMinTiles ? units : tiles * units / kMinTiles;
+  const unsigned ctas = static_cast<unsigned>(want < sms ? want : sms);
   const auto kernel = D == 128 ? cache_attention_tc_kernel<128> : cache_attention_tc_kernel<64>;
   const int bytes = static_cast<int>(D == 128 ? SmemTail<128>::kBytes : SmemTail<64>::kBytes);
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes);
@@ -706,13 +956,15 @@ cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cu
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(pairs));
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(pairs))) != cudaSuccess || ctas == 1) return e;
+  return launch_cache_join(a, D, 2 * kRows, static_cast<int>(rows < 2 * kRows ? rows : 2 * kRows),
+                           static_cast<int>(ctas), D == 128 ? SmemTail<128>::kDesc : SmemTail<64>::kDesc, stream);
 }
 
 }  // namespace sage
