@@ -188,6 +188,7 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
       (rc = check_ints(args->q_lengths_dev, false)) != SAGE_OK || (rc = check_tensor(args->q)) != SAGE_OK ||
       (rc = check_tensor(args->out)) != SAGE_OK)
     return rc;
+  if (a.c.num_pages == 0) a.pt.max_pages = 0;  // without pages there are no tokens, whatever the table says
   // the call's blocks, all sequences and heads, are counted in 32 bits
   // (once for every 256 query rows that share a key/value head)
   const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;

@@ -24,11 +24,11 @@
 // what the products read from it). The columns hold, per tile, D of O, 64 of S
 // and two P of 32, written in turns.
 // Numbers. Queries become fp16 times a power of two per row (their largest
-// value in [1, 4)); key codes are exact in fp16. Values become
-// fp16(code * fp16(s_v / R)), R the largest value scale of the part's blocks so
-// far, in steps of 32 key tiles (O is rescaled when it grows): two roundings of
-// 2^-12 relative; p is rounded to fp16, 2^-12 relative. A block whose scale is
-// below 2^-14 R loses bits of that (its values are then held to 2^-25 R).
+// value in [1, 4)); key and value codes are exact in fp16. The value scales go
+// into the weights: with R the largest value scale of the part's blocks so far
+// (found for 32 key tiles at a time; O is rescaled when it grows), P holds
+// fp16(p s_v / R), a rounding of 2^-12 relative (where p s_v / R is below 2^-14,
+// of 2^-25), and the sum of p is taken in fp32, block by block, times R / s_v.
 // The keys of a block stand in the order in which the values are stored
 // (value_position), so V^T needs no reordering on the way.
 //
@@ -43,12 +43,14 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kConv = 4;        // converter warps
+constexpr int kThreads = 384 + 32 * kConv;
 constexpr int kRows = 128;      // rows of a query tile
 constexpr int kKeys = 64;       // keys of a key tile
 constexpr int kMaxSms = 160;
 constexpr int kMinTiles = 8;    // key tiles that are worth a CTA of their own
-constexpr int kScaleSlots = 16; // key tiles whose scales are kept (more than the stages and the tiles in the MMA)
+constexpr int kWindow = 32;     // key tiles whose pages and scales are looked up together
+constexpr int kWindows = 16;    // lookups that are kept (more than the stages and what lies between)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;   // p may reach 2^8 before the running maximum follows
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -56,7 +58,9 @@ constexpr uint32_t kTmemCols = 512;
 
 // registers per thread of the control, converter and softmax warps
 constexpr uint32_t kRegCtl = 64, kRegConv = 112, kRegSoftmax = 168;
-static_assert(128 * (kRegCtl + kRegConv) + 256 * kRegSoftmax <= 65536, "register file of one SM");
+constexpr uint32_t kRegLaunch = 65536 / kThreads / 8 * 8;
+static_assert(128 * kRegCtl + 32 * kConv * kRegConv + 256 * kRegSoftmax <= kThreads * kRegLaunch,
+              "registers that the CTA is launched with");
 
 template <int D>
 struct Smem {
@@ -72,21 +76,21 @@ struct Smem {
   static constexpr uint32_t kOffBar = kOffV + kStages * kTileKV;
 };
 constexpr int kMaxStages = 8;
-constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarKFull = kBarQEmpty + 2, kBarKEmpty = kBarKFull + kMaxStages;
-constexpr int kBarVFull = kBarKEmpty + kMaxStages, kBarVEmpty = kBarVFull + kMaxStages;
-constexpr int kBarSFull = kBarVEmpty + kMaxStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
+constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarFull = kBarQEmpty + 2, kBarEmpty = kBarFull + kMaxStages;
+constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
 constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarScale = kBarDrain + 2;  // PFull, PVDone: [tile][P buffer]
 constexpr int kBarTop = kBarScale + 2;
 constexpr int kNumBars = kBarTop + 1;
 template <int D>
 struct SmemTail {
-  static constexpr uint32_t kOffTmem = Smem<D>::kOffBar + kNumBars * 8;
-  static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffTop = kOffAbort + 4;                    // [2][converter warp] largest value scale
-  static constexpr uint32_t kOffScale = (kOffTop + 32 + 15) / 16 * 16;  // [slot] two key scales, O's factor, R
-  static_assert(kOffScale % 16 == 0, "a slot is read as one float4");
-  static constexpr uint32_t kOffPlan = kOffScale + kScaleSlots * 16;    // 16 sums, then where the CTA's range begins and how the list is cut
-  static constexpr uint32_t kOffRow = kOffPlan + 24 * 4;                // [unit][256 rows] powers of two of the queries
+  static constexpr uint32_t kOffAbort = Smem<D>::kOffBar + kNumBars * 8;  // as Ctx::abort_at has it
+  static constexpr uint32_t kOffTmem = kOffAbort + 4;
+  static constexpr uint32_t kOffTop = kOffTmem + 4;                    // [2][converter warp] largest value scale
+  static constexpr uint32_t kOffScale = (kOffTop + 2 * kConv * 4 + 15) / 16 * 16;  // [window][tile] two (key scale, log2(s_v / R))
+  static_assert(kOffScale % 16 == 0, "a tile's scales are read as one float4");
+  static constexpr uint32_t kOffTopOf = kOffScale + kWindows * kWindow * 16;      // [window] R, what O is rescaled with
+  static constexpr uint32_t kOffPlan = kOffTopOf + kWindows * 8;    // a sum per warp, then where the CTA's range begins and how the list is cut
+  static constexpr uint32_t kOffRow = kOffPlan + (kThreads / 32 + 8) * 4;                // [unit][256 rows] powers of two of the queries
   // one unit more than of the queries themselves: those are free once the
   // unit's last QK is done, when a softmax thread may still have to read its
   // factor; an issuer goes on to the next unit only after the softmax did
@@ -104,14 +108,22 @@ constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 // TMEM columns of the query tiles
 template <int D>
 struct Cols {
-  __host__ __device__ static constexpr uint32_t o(int i) { return static_cast<uint32_t>(D * i); }
-  __host__ __device__ static constexpr uint32_t s(int i) { return static_cast<uint32_t>(2 * D + 128 * i); }
+  __host__ __device__ static constexpr uint32_t o(int i) { return 128u * static_cast<uint32_t>(i); }
+  __host__ __device__ static constexpr uint32_t s(int i) { return 256u + 128u * static_cast<uint32_t>(i); }
   __host__ __device__ static constexpr uint32_t p(int i, int buf) { return s(i) + 64u + 32u * static_cast<uint32_t>(buf); }
 };
 
-// Barriers and the abort flag by their shared-memory addresses: one register.
+// One arrival for the warp, after what its lanes did (an arrival per lane would
+// be 32 atomics on one word).
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
+// Barriers and the abort flag by their shared-memory addresses.
 struct Ctx {
-  uint32_t bar0, abort_at;
+  uint32_t bar0;
+  __device__ uint32_t abort_at() const { return bar0 + 8u * kNumBars; }
   __device__ uint32_t bar(int i) const { return bar0 + 8u * static_cast<uint32_t>(i); }
 };
 __device__ __forceinline__ uint32_t load_flag(uint32_t addr) {
@@ -132,12 +144,12 @@ __device__ __forceinline__ bool wait_bar(const Ctx& cx, uint32_t bar, uint32_t p
   for (uint32_t it = 1;; ++it) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if ((it & 127u) == 0) {
-      if (kHeedAbort && load_flag(cx.abort_at) != 0) return false;
+      if (kHeedAbort && load_flag(cx.abort_at()) != 0) return false;
       const uint64_t now = tc::global_timer_ns();
       if (t0 == 0) {
         t0 = now;
       } else if (now - t0 > kTimeoutNs) {
-        store_flag(cx.abort_at, 1u);
+        store_flag(cx.abort_at(), 1u);
         return false;
       }
     }
@@ -184,6 +196,23 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 columns (as tc::tmem_ld32).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -258,7 +287,7 @@ __device__ __forceinline__ Part part_at(const CacheAttentionArgs& a, int pairs, 
   x.n = min(x.size - p.t, p.todo);
   return x;
 }
-__device__ __forceinline__ Place first_place(const int* plan) { return Place{plan[16], plan[17], plan[18], plan[19]}; }
+__device__ __forceinline__ Place first_place(const int* found) { return Place{found[0], found[1], found[2], found[3]}; }
 // Past a part of n tiles.
 __device__ __forceinline__ void place_next(const CacheAttentionArgs& a, Place& p, int n) {
   p.todo -= n;
@@ -291,24 +320,43 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t tp, uint64_t 
                (acc || ks > 0) ? 1u : 0u);
 }
 
-// A block of the cache as a converter lane keeps it.
+// 16 codes to fp16, into chunks c and c + 1 of a 128-byte row in the swizzled layout (sw: the row mod 8).
+__device__ __forceinline__ void store_codes(uint32_t row, uint32_t c, uint32_t sw, const uint4& codes) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    __half2 lo, hi;
+    codes_to_half(w[e], lo, hi);
+    o[2 * e] = bits(lo);
+    o[2 * e + 1] = bits(hi);
+  }
+  store16(row + ((c ^ sw) << 4), o);
+  store16(row + (((c + 1u) ^ sw) << 4), o + 4);
+}
+
+// A block of the cache as a converter lane keeps it. One that is not there
+// (bad page, or past the sequence) stands at the cache's start: its codes are
+// read and get the weight 0.
 struct Window {
-  int64_t slot;  // block number in the cache, -1: none
+  int64_t at;  // first byte in the codes
   float ks, vs;
 };
+template <int D>
 __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64_t row_of_table, int h, int len, int blk,
                                               bool* bad) {
   Window w;
-  w.slot = -1;
+  w.at = 0;
   w.ks = -1.0f;  // no tokens
   w.vs = 0.0f;
   if (blk * kCacheBlock < len) {
     const int pg = blk / a.c.blocks_per_page;
     const int page = a.pt.table[row_of_table + pg];
     if (page_ok(page, a.c.num_pages)) {
-      w.slot = block_slot(page, h, a.c.H, a.c.blocks_per_page, blk - pg * a.c.blocks_per_page);
-      w.ks = a.c.ks[w.slot];
-      w.vs = a.c.vs[w.slot];
+      const int64_t slot = block_slot(page, h, a.c.H, a.c.blocks_per_page, blk - pg * a.c.blocks_per_page);
+      w.at = slot * (kCacheBlock * D);
+      w.ks = a.c.ks[slot];
+      w.vs = a.c.vs[slot];
     } else {
       *bad = true;
     }
@@ -330,28 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ctx cx;
   cx.bar0 = sbase + L::kOffBar;
-  cx.abort_at = sbase + T::kOffAbort;
   if (threadIdx.x == 0) {
-    store_flag(cx.abort_at, 0u);
+    store_flag(cx.abort_at(), 0u);
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(cx.bar(kBarQFull + s), 128);
+      tc::mbar_init(cx.bar(kBarQFull + s), kConv);
       tc::mbar_init(cx.bar(kBarQEmpty + s), 2);
       tc::mbar_init(cx.bar(kBarSFull + s), 1);
-      tc::mbar_init(cx.bar(kBarSFree + s), kRows);
-      tc::mbar_init(cx.bar(kBarPFull + 2 * s), kRows);
-      tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), kRows);
+      tc::mbar_init(cx.bar(kBarSFree + s), 4);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s), 4);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), 4);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s + 1), 1);
       tc::mbar_init(cx.bar(kBarDrain + s), 1);
       tc::mbar_init(cx.bar(kBarScale + s), 1);
     }
     for (int s = 0; s < L::kStages; ++s) {
-      tc::mbar_init(cx.bar(kBarKFull + s), 128);
-      tc::mbar_init(cx.bar(kBarKEmpty + s), 2);
-      tc::mbar_init(cx.bar(kBarVFull + s), 128);
-      tc::mbar_init(cx.bar(kBarVEmpty + s), 2);
+      tc::mbar_init(cx.bar(kBarFull + s), kConv);
+      tc::mbar_init(cx.bar(kBarEmpty + s), 2);
     }
-    tc::mbar_init(cx.bar(kBarTop), 4);
+    tc::mbar_init(cx.bar(kBarTop), kConv);
     tc::fence_mbar_init();
   }
   if (warp == 2) {
@@ -364,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   // this CTA's range of the list: each thread sums a run of entries, a scan over
   // the threads finds whose run the range begins in
   int* plan = reinterpret_cast<int*>(smem + T::kOffPlan);
+  int* found = plan + kThreads / 32;  // entry, head, tile, tiles; end of the range; how the list is cut
   bool bad = false;
   const int entries = static_cast<int>(a.B) * pairs, run = (entries + kThreads - 1) / kThreads;
   const int e_lo = min(run * static_cast<int>(threadIdx.x), entries), e_hi = min(e_lo + run, entries);
@@ -402,15 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       before += x;
     }
     const int size = unit_size(find_entry(a, pairs, e, &bad)), h = (lo - before) / size;
-    plan[16] = e;
-    plan[17] = h;
-    plan[18] = lo - before - h * size;
+    found[0] = e;
+    found[1] = h;
+    found[2] = lo - before - h * size;
   }
   if (threadIdx.x == 0) {
-    plan[19] = hi - lo;
-    plan[20] = hi;
-    plan[21] = each;
-    plan[22] = extra;
+    found[3] = hi - lo;
+    found[4] = hi;
+    found[5] = each;
+    found[6] = extra;
     // what stands if a wait runs out, or without work
     static_cast<int4*>(a.workspace)[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
@@ -425,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       const uint32_t d_s = tmem + C::s(i), d_o = tmem + C::o(i);
       const uint64_t dq0 = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dv0 = tc::sw128_desc(sbase + L::kOffV);
-      // key tiles (keys, values, those of this query tile) and parts so far
-      uint32_t k_cnt = 0, v_cnt = 0, steps = 0, q_cnt = 0;
+      // key tiles (of the converters, of this query tile) and parts so far
+      uint32_t cnt = 0, steps = 0, q_cnt = 0;
       bool ok = true;
-      Place p = first_place(plan);
+      Place p = first_place(found);
       while (ok && p.todo > 0) {
         const Part x = part_at(a, pairs, p);
         const int n = part_tiles(p, x, i);                                // of this query tile
@@ -440,12 +486,38 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         ++q_cnt;
         if (n == 0 && leader) tc::mbar_arrive(cx.bar(kBarQEmpty + static_cast<int>(qb)));
         const uint64_t dq = desc_at(dq0, qb * 2u * L::kTile);
-        for (int j = 0; j <= n_all; ++j) {
+        // PV_j once P_j is there (its values came with its keys)
+        const auto pv = [&](int j) {
+          const int s = static_cast<int>((cnt + static_cast<uint32_t>(j)) % L::kStages);
+          if (j < n) {
+            const uint32_t st = steps + static_cast<uint32_t>(j);
+            // (a barrier per P buffer: the softmax may be two tiles ahead of this wait)
+            const int pb = static_cast<int>(st % kP);
+            if (!wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + pb), (st / kP) & 1u)) return false;
+            tc::tc_fence_after();
+            if (leader) {
+              issue_pv<D>(d_o, tmem + C::p(i, pb), desc_at(dv0, static_cast<uint32_t>(s) * L::kTileKV), j > 0);
+              tc::mma_commit(cx.bar(kBarPVDone + 2 * i + pb));
+              tc::mma_commit(cx.bar(kBarEmpty + s));
+            }
+          } else if (leader) {
+            tc::mbar_arrive(cx.bar(kBarEmpty + s));  // no row of this query tile sees the keys
+          }
+          __syncwarp();
+          return true;
+        };
+        for (int j = 0; ok && j <= n_all; ++j) {
+          bool pending = j > 0;
           if (j < n_all) {
+            const uint32_t at = cnt + static_cast<uint32_t>(j), s = at % L::kStages, ph = (at / L::kStages) & 1u;
+            const uint32_t full = cx.bar(kBarFull + static_cast<int>(s));
+            // keys that are late do not hold up the last tile's PV
+            if (pending && !__any_sync(0xffffffffu, tc::mbar_try_wait(full, ph))) {
+              if (!(ok = pv(j - 1))) break;
+              pending = false;
+            }
             // QK_j once its keys are there and the softmax has read S_{j-1}
-            const uint32_t s = k_cnt % L::kStages;
-            if (!(ok = wait_bar_warp(cx, cx.bar(kBarKFull + static_cast<int>(s)), (k_cnt / L::kStages) & 1u))) break;
-            ++k_cnt;
+            if (!(ok = wait_bar_warp(cx, full, ph))) break;
             if (j < n) {
               const uint32_t st = steps + static_cast<uint32_t>(j);
               if (st > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), (st - 1u) & 1u))) break;
@@ -455,36 +527,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
                 tc::mbar_arrive(cx.bar(kBarScale + i));
                 issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTileKV));
                 tc::mma_commit(cx.bar(kBarSFull + i));
-                tc::mma_commit(cx.bar(kBarKEmpty + static_cast<int>(s)));
                 if (j == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
               }
-            } else if (leader) {
-              tc::mbar_arrive(cx.bar(kBarKEmpty + static_cast<int>(s)));  // no row of this tile sees the keys
+              __syncwarp();
             }
-            __syncwarp();
           }
-          if (j >= 1) {
-            // PV_{j-1} once its values and P_{j-1} are there
-            const uint32_t s = v_cnt % L::kStages;
-            if (!(ok = wait_bar_warp(cx, cx.bar(kBarVFull + static_cast<int>(s)), (v_cnt / L::kStages) & 1u))) break;
-            ++v_cnt;
-            if (j - 1 < n) {
-              const uint32_t st = steps + static_cast<uint32_t>(j) - 1u;
-              // (a barrier per P buffer: the softmax may be two tiles ahead of this wait)
-              const int pb = static_cast<int>(st % kP);
-              if (!(ok = wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + pb), (st / kP) & 1u))) break;
-              tc::tc_fence_after();
-              if (leader) {
-                issue_pv<D>(d_o, tmem + C::p(i, pb), desc_at(dv0, s * L::kTileKV), j > 1);
-                tc::mma_commit(cx.bar(kBarPVDone + 2 * i + pb));
-                tc::mma_commit(cx.bar(kBarVEmpty + static_cast<int>(s)));
-              }
-            } else if (leader) {
-              tc::mbar_arrive(cx.bar(kBarVEmpty + static_cast<int>(s)));
-            }
-            __syncwarp();
-          }
+          if (pending && !(ok = pv(j - 1))) break;
         }
+        cnt += static_cast<uint32_t>(n_all);
         steps += static_cast<uint32_t>(n);
       }
       // all MMAs of this warp complete before TMEM is freed
@@ -496,57 +546,59 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   } else if (warp >= 12) {
     // ------------------------------------------------------------ converters --
     regs_dec<kRegConv>();
-    const int w = warp - 12, blk = w & 1, part2 = w >> 1;  // block of each key tile, half of its codes
+    const int w = warp - 12, blk = w & 1, share = w >> 1;  // block of each key tile, share of its codes
     // Load x of the warp, of kLoads. Keys: 8 tokens of one 64-channel half,
     // channels 16 (lane mod 4) and up of token lane / 4. Values: 16 channels,
     // positions 16 (lane mod 2) and up of channel v_ch, which is lane / 2 with
     // its bits 1 and 2 exchanged: the 8 lanes of a store phase then write
     // channels c, c + 1, c + 4, c + 5, whose swizzled chunks are all different.
-    constexpr int kLoads = D / 32;
+    constexpr int kLoads = 2 * D / 16 / kConv;
     const int v_ch = ((lane >> 1) & 9) | ((lane >> 1) & 2) << 1 | ((lane >> 1) & 4) >> 1;
     const int v_at = 2 * v_ch + (lane & 1);
     uint4 kr[kLoads], vr[kLoads];  // raw codes: 512 bytes per load of the warp
     float* tops = reinterpret_cast<float*>(smem + T::kOffTop);
     bool bad_page = false, ok = true;
     // the tile that is fetched next: tile t of t_end of the unit at `p`
-    Place p = first_place(plan);
+    Place p = first_place(found);
     int t = 0, t_end = 0, n = 0, len = 0;
     int64_t row_of_table = 0;
     uint32_t windows = 0, parts = 0;
-    Window win{-1, -1.0f, 0.0f};
-    int64_t slot = -1;
-    float ks = 0.0f, vs = 0.0f, top = 0.0f, factor = 1.0f;
+    Window win{0, -1.0f, 0.0f};
+    int64_t at = 0;  // the block's first byte in the codes
+    float top = 0.0f;
     int in_window = 0, head = 0;
     // R of the next 32 tiles: the largest value scale so far (NaN passes)
     const auto open_window = [&](bool fresh) {
-      win = load_window(a, row_of_table, head, len, (t + lane) * kB + blk, &bad_page);
+      win = load_window<D>(a, row_of_table, head, len, (t + lane) * kB + blk, &bad_page);
       float x = t + lane < t_end ? fmaxf(win.vs, 0.0f) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      const float* buf = tops + 4 * (windows & 1u);
+      const float* buf = tops + kConv * (windows & 1u);
       if (lane == 0) {
-        tops[4 * (windows & 1u) + w] = x;
+        tops[kConv * (windows & 1u) + w] = x;
         tc::mbar_arrive(cx.bar(kBarTop));
       }
       if (!wait_bar_warp(cx, cx.bar(kBarTop), windows & 1u)) ok = false;
-      ++windows;
-      x = fmaxf(fmaxf(buf[0], buf[1]), fmaxf(buf[2], buf[3]));
-      factor = 1.0f;
-      if (fresh) {
-        top = x;
-      } else if (x > top) {
-        factor = top / x;
-        top = x;
+#pragma unroll
+      for (int k = 0; k < kConv; ++k) x = fmaxf(x, buf[k]);
+      const float factor = fresh || !(x > top) ? 1.0f : top / x;
+      if (fresh || x > top) top = x;
+      // the softmax's view: key scales (negative: no tokens) and log2(s_v / R),
+      // which is held above -40, where a weight of it is 0 in fp16 (no value
+      // scale: the codes are 0 and any weight will do)
+      const uint32_t slot = windows % kWindows;
+      if (share == 0) {
+        float* row = reinterpret_cast<float*>(smem + T::kOffScale) + (slot * kWindow + lane) * 4 + blk;
+        row[0] = win.ks;
+        row[2] = win.vs == 0.0f ? 0.0f : (win.vs == win.vs ? fmaxf(log2f(win.vs / top), -40.0f) : win.vs);
       }
+      if (w == 0 && lane == 0) reinterpret_cast<float2*>(smem + T::kOffTopOf)[slot] = make_float2(top, factor);
+      ++windows;
       in_window = 0;
     };
-    const auto pick = [&]() {
-      slot = __shfl_sync(0xffffffffu, win.slot, in_window);
-      ks = __shfl_sync(0xffffffffu, win.ks, in_window);
-      vs = __shfl_sync(0xffffffffu, win.vs, in_window);
-    };
+    const auto pick = [&]() { at = __shfl_sync(0xffffffffu, win.at, in_window); };
     // The queries of a unit to fp16, times a power of two per row, in the
-    // swizzled layout: four lanes share a row, 32 rows at a time.
+    // swizzled layout: four lanes share a row, 8 rows of a warp at a time.
     const auto bring_queries = [&](const Unit& u) {
       const uint32_t qb = parts % L::kQ;
       if (!wait_bar_warp(cx, cx.bar(kBarQEmpty + static_cast<int>(qb)), ((parts / L::kQ) & 1u) ^ 1u)) {
@@ -557,48 +609,54 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       ++parts;
       const int g = lane >> 2, c4 = lane & 3;
       const uint16_t* base = a.q.p + u.b * a.q.sb + c4 * 16;
-#pragma unroll 2
-      for (int it = 0; it < 8; ++it) {
-        const int rr = it * 32 + w * 8 + g, r = u.row0 + rr;
-        uint32_t x[D / 64][8];
+      constexpr int kTimes = 2 * kRows / (8 * kConv), kAhead = 256 / D;  // rows per lane, of which so many load together
+#pragma unroll 1
+      for (int it0 = 0; it0 < kTimes; it0 += kAhead) {
+        uint4 x[kAhead][D / 32];
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          uint4 lo4 = make_uint4(0u, 0u, 0u, 0u), hi4 = lo4;
+        for (int y = 0; y < kAhead; ++y) {
+          const int r = u.row0 + ((it0 + y) * kConv + w) * 8 + g;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) x[y][e] = make_uint4(0u, 0u, 0u, 0u);
           if (r < u.R) {
             const int tok = r / u.G;
-            const uint4* src = reinterpret_cast<const uint4*>(base + tok * a.q.ss + (u.h * u.G + r - tok * u.G) * a.q.sh + hf * 64);
-            lo4 = src[0];
-            hi4 = src[1];
+            const uint4* src = reinterpret_cast<const uint4*>(base + tok * a.q.ss + (u.h * u.G + r - tok * u.G) * a.q.sh);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) x[y][e] = src[(e >> 1) * 8 + (e & 1)];
           }
-          *reinterpret_cast<uint4*>(x[hf]) = lo4;
-          *reinterpret_cast<uint4*>(x[hf] + 4) = hi4;
         }
-        uint32_t amax = 0;
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf)
+        for (int y = 0; y < kAhead; ++y) {
+          const int rr = ((it0 + y) * kConv + w) * 8 + g;
+          uint32_t amax = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = max(amax, max(x[hf][e] & 0x7FFFu, (x[hf][e] >> 16) & 0x7FFFu));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        uint32_t ex = amax >> 7;
-        ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
-        const float down = __uint_as_float((254u - ex) << 23);
-        if (c4 == 0) rows[rr] = __uint_as_float(ex << 23);
-        const uint32_t at = sbase + L::kOffQ + (qb * 2u + static_cast<uint32_t>(rr >> 7)) * L::kTile +
-                            static_cast<uint32_t>(rr & 127) * 128u;
+          for (int e = 0; e < D / 32; ++e) {
+            const uint32_t v[4] = {x[y][e].x, x[y][e].y, x[y][e].z, x[y][e].w};
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf) {
-          uint32_t o[8];
+            for (int k = 0; k < 4; ++k) amax = max(amax, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+          }
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          uint32_t ex = amax >> 7;
+          ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
+          const float down = __uint_as_float((254u - ex) << 23);
+          if (c4 == 0) rows[rr] = __uint_as_float(ex << 23);
+          const uint32_t to = sbase + L::kOffQ + (qb * 2u + static_cast<uint32_t>(rr >> 7)) * L::kTile +
+                              static_cast<uint32_t>(rr & 127) * 128u;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            o[e] = pack_half2(__uint_as_float(x[hf][e] << 16) * down, __uint_as_float(x[hf][e] & 0xFFFF0000u) * down);
-          const uint32_t ch = static_cast<uint32_t>(c4) * 2u, sw = static_cast<uint32_t>(rr) & 7u;
-          store16(at + static_cast<uint32_t>(hf) * L::kSub + ((ch ^ sw) << 4), o);
-          store16(at + static_cast<uint32_t>(hf) * L::kSub + (((ch + 1u) ^ sw) << 4), o + 4);
+          for (int e = 0; e < D / 32; ++e) {
+            const uint32_t v[4] = {x[y][e].x, x[y][e].y, x[y][e].z, x[y][e].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = pack_half2(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xFFFF0000u) * down);
+            const uint32_t ch = static_cast<uint32_t>(c4) * 2u + static_cast<uint32_t>(e & 1), sw = static_cast<uint32_t>(rr) & 7u;
+            store16(to + static_cast<uint32_t>(e >> 1) * L::kSub + ((ch ^ sw) << 4), o);
+          }
         }
       }
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarQFull + static_cast<int>(qb)));
+      arrive_warp(cx.bar(kBarQFull + static_cast<int>(qb)), lane);
     };
     // opens the first unit from p on that has tiles; false at the end of the range
     const auto open_part = [&]() {
@@ -622,19 +680,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       return false;
     };
     const auto advance = [&]() {
-      factor = 1.0f;
       if (++t < t_end) {
-        if (++in_window == 32) open_window(false);
+        if (++in_window == kWindow) open_window(false);
         pick();
         return true;
       }
       place_next(a, p, n);
       return open_part();
     };
-    const auto fetch = [&](const int8_t* base, int at, uint4 (&r)[kLoads]) {
-      const uint4* src = reinterpret_cast<const uint4*>(base + slot * (kCacheBlock * D)) + part2 * kLoads * 32 + at;
+    const auto fetch = [&](const int8_t* codes, int lane_at, uint4 (&r)[kLoads]) {
+      const uint4* src = reinterpret_cast<const uint4*>(codes + at) + share * kLoads * 32 + lane_at;
 #pragma unroll
-      for (int x = 0; x < kLoads; ++x) r[x] = slot >= 0 ? src[x * 32] : make_uint4(0u, 0u, 0u, 0u);
+      for (int x = 0; x < kLoads; ++x) r[x] = src[x * 32];
     };
     bool more = open_part();
     if (more) {
@@ -642,37 +699,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       fetch(a.c.v, v_at, vr);
     }
     for (uint32_t cnt = 0; ok && more; ++cnt) {
-      const uint32_t s = cnt % L::kStages, ph = (cnt / L::kStages) & 1u;
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarKEmpty + static_cast<int>(s)), ph ^ 1u))) break;
-      const uint32_t k_row = sbase + L::kOffK + s * L::kTileKV;
+      const uint32_t s = cnt % L::kStages;
+      if (!(ok = wait_bar_warp(cx, cx.bar(kBarEmpty + static_cast<int>(s)), ((cnt / L::kStages) & 1u) ^ 1u))) break;
+      const uint32_t k_row = sbase + L::kOffK + s * L::kTileKV, v_row = sbase + L::kOffV + s * L::kTileKV;
 #pragma unroll
       for (int x = 0; x < kLoads; ++x) {
-        // eight tokens j8 of a 64-channel half: the warp's 4 of half part2, or (D = 64) its two of the block
-        const int j8 = D == 128 ? x : part2 * 2 + x, hf = D == 128 ? part2 : 0;
+        const int at8 = share * kLoads + x, j8 = at8 & 3, hf = at8 >> 2;  // eight tokens of a 64-channel half
         const int n8 = lane >> 2, row = blk * 32 + 8 * (n8 >> 1) + 2 * j8 + (n8 & 1);  // value_position of token 8 j8 + n8
-        const uint32_t cw[4] = {kr[x].x, kr[x].y, kr[x].z, kr[x].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          __half2 lo2, hi2;
-          codes_to_half(cw[e], lo2, hi2);
-          o[2 * e] = bits(lo2);
-          o[2 * e + 1] = bits(hi2);
-        }
-        const uint32_t at = k_row + static_cast<uint32_t>(hf) * L::kSubK + static_cast<uint32_t>(row) * 128u;
-        const uint32_t ch = static_cast<uint32_t>(lane & 3) * 2u, sw = static_cast<uint32_t>(row) & 7u;
-        store16(at + ((ch ^ sw) << 4), o);
-        store16(at + (((ch + 1u) ^ sw) << 4), o + 4);
+        store_codes(k_row + static_cast<uint32_t>(hf) * L::kSubK + static_cast<uint32_t>(row) * 128u,
+                    static_cast<uint32_t>(lane & 3) * 2u, static_cast<uint32_t>(row) & 7u, kr[x]);
       }
-      if (lane == 0) {
-        float* ring = reinterpret_cast<float*>(smem + T::kOffScale) + (cnt % kScaleSlots) * 4;
-        // a value scale that is NaN makes the rows that see the block NaN through their logits
-        if (part2 == 0) ring[blk] = vs != vs ? vs : ks;
-        else ring[2 + blk] = blk == 0 ? factor : top;
-      }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarKFull + static_cast<int>(s)));
-      const float vs_now = vs, top_now = top;
       // the next tile of the unit; the next unit only once this one's values are out
       const bool last = t + 1 >= t_end;
       if (!last) {
@@ -680,47 +716,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         if (!ok) break;
         fetch(a.c.k, lane, kr);
       }
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarVEmpty + static_cast<int>(s)), ph ^ 1u))) break;
-      // fp16(s_v / R) below 2^-14 would lose bits: the power of two comes off after the product then
-      float h = (vs_now == vs_now && top_now > 0.0f) ? vs_now / top_now : 0.0f, shift = 1.0f;
-      if (h < 6.1035156e-05f) {
-        h *= 16384.0f;
-        shift = 6.1035156e-05f;
-      }
-      const __half2 h2 = __float2half2_rn(h), shift2 = __float2half2_rn(shift);
-      const uint32_t v_row = sbase + L::kOffV + s * L::kTileKV;
 #pragma unroll
       for (int x = 0; x < kLoads; ++x) {
-        const int ch = 16 * (part2 * kLoads + x) + v_ch;
-        const uint32_t cw[4] = {vr[x].x, vr[x].y, vr[x].z, vr[x].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          __half2 lo2, hi2;
-          codes_to_half(cw[e], lo2, hi2);
-          lo2 = __hmul2(lo2, h2);
-          hi2 = __hmul2(hi2, h2);
-          if (shift != 1.0f) {
-            lo2 = __hmul2(lo2, shift2);
-            hi2 = __hmul2(hi2, shift2);
-          }
-          o[2 * e] = bits(lo2);
-          o[2 * e + 1] = bits(hi2);
-        }
-        const uint32_t at = v_row + static_cast<uint32_t>(ch) * 128u;
-        const uint32_t chunk = static_cast<uint32_t>(blk) * 4u + static_cast<uint32_t>(lane & 1) * 2u;
-        const uint32_t sw = static_cast<uint32_t>(ch) & 7u;
-        store16(at + ((chunk ^ sw) << 4), o);
-        store16(at + (((chunk + 1u) ^ sw) << 4), o + 4);
+        const int ch = 16 * (share * kLoads + x) + v_ch;
+        store_codes(v_row + static_cast<uint32_t>(ch) * 128u,
+                    static_cast<uint32_t>(blk) * 4u + static_cast<uint32_t>(lane & 1) * 2u, static_cast<uint32_t>(ch) & 7u,
+                    vr[x]);
       }
+      if (!last) fetch(a.c.v, v_at, vr);
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(cx.bar(kBarVFull + static_cast<int>(s)));
+      arrive_warp(cx.bar(kBarFull + static_cast<int>(s)), lane);
       if (last) {
         more = advance();
         if (!ok) break;
-        if (more) fetch(a.c.k, lane, kr);
+        if (more) {
+          fetch(a.c.k, lane, kr);
+          fetch(a.c.v, v_at, vr);
+        }
       }
-      if (more) fetch(a.c.v, v_at, vr);
     }
     if (bad_page) atomicExch(a.dev_err, kDevErrPage);
     __syncwarp();
@@ -730,38 +743,42 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     regs_inc<kRegSoftmax>();
     const int i = (warp - 4) >> 2, wq = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_addr + C::s(i), tO = tmem + lane_addr + C::o(i);
-    const float* ring = reinterpret_cast<const float*>(smem + T::kOffScale);
+    const uint32_t tO = tmem + lane_addr + C::o(i), tS = tO + (C::s(0) - C::o(0));
+    const float4* scales = reinterpret_cast<const float4*>(smem + T::kOffScale);
+    const float2* tops = reinterpret_cast<const float2*>(smem + T::kOffTopOf);
     const int rr = i * kRows + wq * 32 + lane;  // this thread's row of a pair
     bool ok = true;
-    uint32_t steps = 0, tile_cnt = 0, parts = 0;  // key tiles of this query tile; of the converters, and their units
+    uint32_t steps = 0, windows = 0, parts = 0;  // key tiles of this query tile; the converters' windows and units
     // waits for the PV of step x (its P buffer and O are then free)
     const auto wait_pv = [&](uint32_t x) {
       return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + static_cast<int>(x % kP)), (x / kP) & 1u);
     };
-    Place p = first_place(plan);
+    Place p = first_place(found);
     while (p.todo > 0) {
-      int n, all, sees;
-      bool real;
+      int n, sees, all_see;
       {
         const Part x = part_at(a, pairs, p);
         const int r = x.u.row0 + rr;
-        real = r < x.u.R;
+        const bool real = r < x.u.R;
         sees = real ? row_sees(a, x.u, r) : 0;
+        // the smallest limit in the warp decides, for all its lanes, whether a tile is masked
+        all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
         n = part_tiles(p, x, i);
-        all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
       }
       float m = -INFINITY, l = 0.0f, f = 0.0f, top = 0.0f;
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
-      // the smallest limit in the warp decides, for all its lanes, whether a step is masked
-      const int all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t st = steps + static_cast<uint32_t>(j);
         if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + i), st & 1u))) break;
-        // two key scales, what O has to be multiplied with, R
-        const float4 sc = *reinterpret_cast<const float4*>(ring + ((tile_cnt + static_cast<uint32_t>(j)) % kScaleSlots) * 4);
-        if (j == 0) f = rows[rr] * a.sm_log2;
-        top = sc.w;
+        const uint32_t win = (windows + static_cast<uint32_t>(j) / kWindow) % kWindows;
+        const float4 sc = scales[win * kWindow + static_cast<uint32_t>(j) % kWindow];
+        const bool opens = j % kWindow == 0;
+        float factor = 1.0f;  // what O is rescaled with because R grew
+        if (opens) {
+          if (j == 0) f = rows[rr] * a.sm_log2;
+          top = tops[win].x;
+          factor = tops[win].y;
+        }
         if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), st & 1u))) break;
         tc::tc_fence_after();
         uint32_t sr[kB][32];
@@ -769,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
         tc::tmem_wait_ld();
         tc::tc_fence_before();
-        tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
+        arrive_warp(cx.bar(kBarSFree + i), lane);  // the next QK may overwrite S
         const int key0 = (p.t + j) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
@@ -799,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           m0 = fmaxf(m0, m1);
           mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
         }
-        if (__any_sync(0xffffffffu, mt > m + kLazy) || sc.z != 1.0f) {
+        if (__any_sync(0xffffffffu, mt > m + kLazy) || factor != 1.0f) {
           const float up = fmaxf(m, mt);
           const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
           m = up;
@@ -807,30 +824,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           if (j > 0) {
             if (!(ok = wait_pv(st - 1u))) break;  // O is at rest
             tc::tc_fence_after();
-            const float y = alpha * sc.z;
+            const float y = alpha * factor;
             const float2 a2 = make_float2(y, y);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + 32u * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16u * c, o);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) {
+              for (int k = 0; k < 16; k += 2) {
                 const float2 y2 = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), a2);
                 o[k] = __float_as_uint(y2.x);
                 o[k + 1] = __float_as_uint(y2.y);
               }
-              tc::tmem_st32(tO + 32u * c, o);
+              tmem_st16(tO + 16u * c, o);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        const float2 n2 = make_float2(-ref, -ref);
-        float2 sa = make_float2(0.0f, 0.0f), sb = make_float2(0.0f, 0.0f);
-        uint32_t pw[32];
+        if (st >= kP) {
+          if (!(ok = wait_pv(st - kP))) break;  // the buffer's last PV has read it
+          tc::tc_fence_after();
+        }
+        const uint32_t tP = tS + (C::p(0, 0) - C::s(0)) + (C::p(0, 1) - C::p(0, 0)) * (st % kP);
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          const float2 c2 = make_float2(cb[b], cb[b]);
+          // p s_v / R, whose sum over the block is taken back to that of p
+          uint32_t pw[16];
+          const float lh = b == 0 ? sc.z : sc.w;
+          const float2 c2 = make_float2(cb[b], cb[b]), n2 = make_float2(lh - ref, lh - ref);
+          float2 sa = make_float2(0.0f, 0.0f), sb = sa;
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
@@ -841,38 +864,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             }
             if (c & 2) sb = __fadd2_rn(sb, pp);
             else sa = __fadd2_rn(sa, pp);
-            pw[16 * b + c / 2] = pack_half2(pp.x, pp.y);
+            pw[c / 2] = pack_half2(pp.x, pp.y);
           }
+          tmem_st16(tP + 16u * b, pw);
+          // (a block that the row does not reach adds nothing, whatever its scale is)
+          l = fmaf((sa.x + sa.y) + (sb.x + sb.y), lim[b] > 0 ? ex2(-lh) : 0.0f, l);
         }
-        l += (sa.x + sa.y) + (sb.x + sb.y);
-        if (st >= kP) {
-          if (!(ok = wait_pv(st - kP))) break;  // the buffer's last PV has read it
-          tc::tc_fence_after();
-        }
-        const uint32_t tP = tmem + lane_addr + C::p(i, static_cast<int>(st % kP));
-        tc::tmem_st32(tP, pw);
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)));
+        arrive_warp(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)), lane);
       }
       if (!ok) break;
       steps += static_cast<uint32_t>(n);
-      tile_cnt += static_cast<uint32_t>(all);
-      parts += all > 0 ? 1u : 0u;
 
       // the part's rows: to the output, or to the workspace
       const Part x = part_at(a, pairs, p);
       const Unit& u = x.u;
+      const int all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
+      windows += static_cast<uint32_t>((all + kWindow - 1) / kWindow);
+      parts += all > 0 ? 1u : 0u;
       const int r = u.row0 + rr, tok = r / u.G, head = u.h * u.G + r - tok * u.G;
+      const bool real = r < u.R;
       if (n > 0) {
         if (!(ok = wait_pv(steps - 1u))) break;
         tc::tc_fence_after();
       }
       const bool whole = x.n == x.size;
-      const int which = p.todo == plan[19] ? 0 : 1;
+      const int which = p.todo == found[3] ? 0 : 1;
       if (p.todo == x.n && threadIdx.x == 128 && p.t == 0 && x.size > x.n) {
         // the last unit begins here and goes on in other CTAs: up to which one, and whose rows
-        const int end = plan[20] + x.size - x.n - 1, each = plan[21], extra = plan[22], head_units = extra * (each + 1);
+        const int end = found[4] + x.size - x.n - 1, each = found[5], extra = found[6], head_units = extra * (each + 1);
         static_cast<int4*>(a.workspace)[blockIdx.x] =
             make_int4(end < head_units ? end / (each + 1) : extra + (end - head_units) / each, u.b, 2 * u.h + which,
                       u.row0);
@@ -926,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && load_flag(cx.abort_at) != 0) atomicExch(a.dev_err, kDevErrTimeout);
+  if (threadIdx.x == 0 && load_flag(cx.abort_at()) != 0) atomicExch(a.dev_err, kDevErrTimeout);
   if (warp == 2) {
     tc::tc_fence_after();
     tc::tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(smem + T::kOffTmem), kTmemCols);
