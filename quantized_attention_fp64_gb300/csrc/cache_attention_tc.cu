@@ -78,8 +78,7 @@ struct Smem {
 constexpr int kMaxStages = 8;
 constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarFull = kBarQEmpty + 2, kBarEmpty = kBarFull + kMaxStages;
 constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
-constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarScale = kBarDrain + 2;  // PFull, PVDone: [tile][P buffer]
-constexpr int kBarTop = kBarScale + 2;
+constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarTop = kBarDrain + 2;  // PFull, PVDone: [tile][P buffer]
 constexpr int kNumBars = kBarTop + 1;
 template <int D>
 struct SmemTail {
@@ -383,14 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(cx.bar(kBarQFull + s), kConv);
       tc::mbar_init(cx.bar(kBarQEmpty + s), 2);
-      tc::mbar_init(cx.bar(kBarSFull + s), 1);
+      tc::mbar_init(cx.bar(kBarSFull + s), 2);
       tc::mbar_init(cx.bar(kBarSFree + s), 4);
       tc::mbar_init(cx.bar(kBarPFull + 2 * s), 4);
       tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), 4);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s + 1), 1);
       tc::mbar_init(cx.bar(kBarDrain + s), 1);
-      tc::mbar_init(cx.bar(kBarScale + s), 1);
     }
     for (int s = 0; s < L::kStages; ++s) {
       tc::mbar_init(cx.bar(kBarFull + s), kConv);
@@ -523,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
               if (st > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), (st - 1u) & 1u))) break;
               tc::tc_fence_after();
               if (leader) {
-                // the tile's scales are there as well (and the softmax has read the last tile's)
-                tc::mbar_arrive(cx.bar(kBarScale + i));
+                // S is there when the MMAs are done (this one and all before it); the plain
+                // arrival passes on what the converters wrote: scales, powers of two
+                tc::mbar_arrive(cx.bar(kBarSFull + i));
                 issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTileKV));
                 tc::mma_commit(cx.bar(kBarSFull + i));
                 if (j == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
@@ -769,7 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t st = steps + static_cast<uint32_t>(j);
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarScale + i), st & 1u))) break;
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), st & 1u))) break;
+        tc::tc_fence_after();
+        uint32_t sr[kB][32];
+#pragma unroll
+        for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
         const uint32_t win = (windows + static_cast<uint32_t>(j) / kWindow) % kWindows;
         const float4 sc = scales[win * kWindow + static_cast<uint32_t>(j) % kWindow];
         const bool opens = j % kWindow == 0;
@@ -779,11 +782,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           top = tops[win].x;
           factor = tops[win].y;
         }
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), st & 1u))) break;
-        tc::tc_fence_after();
-        uint32_t sr[kB][32];
-#pragma unroll
-        for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         arrive_warp(cx.bar(kBarSFree + i), lane);  // the next QK may overwrite S
@@ -842,10 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        if (st >= kP) {
-          if (!(ok = wait_pv(st - kP))) break;  // the buffer's last PV has read it
-          tc::tc_fence_after();
-        }
+        // the buffer's last PV, two tiles back, was issued before this tile's QK,
+        // so it was done when S was there
         const uint32_t tP = tS + (C::p(0, 0) - C::s(0)) + (C::p(0, 1) - C::p(0, 0)) * (st % kP);
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
