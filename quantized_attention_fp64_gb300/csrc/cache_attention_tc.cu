@@ -363,6 +363,27 @@ __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64
   return w;
 }
 
+// One block of a row: p s_v / R = 2^(s c + n) of its 32 scores, in fp16, and
+// their sum. kMasked: from token lim on they are 0, whatever s and c are.
+template <bool kMasked>
+__device__ __forceinline__ float exp_block(const uint32_t (&s)[32], float c, float n, int lim, uint32_t (&pw)[16]) {
+  const float2 c2 = make_float2(c, c), n2 = make_float2(n, n);
+  float2 sa = make_float2(0.0f, 0.0f), sb = sa;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, n2);
+    float2 p = make_float2(ex2(y.x), ex2(y.y));
+    if (kMasked) {
+      if (value_token(k) >= lim) p.x = 0.0f;
+      if (value_token(k + 1) >= lim) p.y = 0.0f;
+    }
+    if (k & 2) sb = __fadd2_rn(sb, p);
+    else sa = __fadd2_rn(sa, p);
+    pw[k / 2] = pack_half2(p.x, p.y);
+  }
+  return (sa.x + sa.y) + (sb.x + sb.y);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const CacheAttentionArgs a, int pairs) {
   using L = Smem<D>;
@@ -383,9 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::mbar_init(cx.bar(kBarQFull + s), kConv);
       tc::mbar_init(cx.bar(kBarQEmpty + s), 2);
       tc::mbar_init(cx.bar(kBarSFull + s), 2);
-      tc::mbar_init(cx.bar(kBarSFree + s), 4);
-      tc::mbar_init(cx.bar(kBarPFull + 2 * s), 4);
-      tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), 4);
+      tc::mbar_init(cx.bar(kBarSFree + s), kRows);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s), kRows);
+      tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), kRows);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s + 1), 1);
       tc::mbar_init(cx.bar(kBarDrain + s), 1);
@@ -784,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         }
         tc::tmem_wait_ld();
         tc::tc_fence_before();
-        arrive_warp(cx.bar(kBarSFree + i), lane);  // the next QK may overwrite S
+        tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
         const int key0 = (p.t + j) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
@@ -846,29 +867,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           // p s_v / R, whose sum over the block is taken back to that of p
+          // (a block that the row does not reach adds nothing, whatever its scale is)
           uint32_t pw[16];
           const float lh = b == 0 ? sc.z : sc.w;
-          const float2 c2 = make_float2(cb[b], cb[b]), n2 = make_float2(lh - ref, lh - ref);
-          float2 sa = make_float2(0.0f, 0.0f), sb = sa;
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[b][c]), __uint_as_float(sr[b][c + 1])), c2, n2);
-            float2 pp = make_float2(ex2(y.x), ex2(y.y));
-            if (masked) {
-              if (value_token(c) >= lim[b]) pp.x = 0.0f;
-              if (value_token(c + 1) >= lim[b]) pp.y = 0.0f;
-            }
-            if (c & 2) sb = __fadd2_rn(sb, pp);
-            else sa = __fadd2_rn(sa, pp);
-            pw[c / 2] = pack_half2(pp.x, pp.y);
+          float back = ex2(-lh), sum;
+          if (masked) {
+            sum = exp_block<true>(sr[b], cb[b], lh - ref, lim[b], pw);
+            if (lim[b] <= 0) back = 0.0f;
+          } else {
+            sum = exp_block<false>(sr[b], cb[b], lh - ref, 32, pw);
           }
           tmem_st16(tP + 16u * b, pw);
-          // (a block that the row does not reach adds nothing, whatever its scale is)
-          l = fmaf((sa.x + sa.y) + (sb.x + sb.y), lim[b] > 0 ? ex2(-lh) : 0.0f, l);
+          l = fmaf(sum, back, l);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        arrive_warp(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)), lane);
+        tc::mbar_arrive(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)));
       }
       if (!ok) break;
       steps += static_cast<uint32_t>(n);
