@@ -17,12 +17,12 @@
 //                 them in the 128-byte-swizzled layout that the MMA reads, four
 //                 tiles ahead (eight at D = 64); they also bring the queries
 //                 and run ahead into the next unit
-// Per query tile and key tile j: S = Q K_j^T
-// (tcgen05 kind::f16, fp32 in TMEM); the softmax reads S into registers and
-// releases it, so the next step's QK runs under the exponentials; p goes to
-// TMEM as fp16, and O += P V_j reads it there (P in shared memory would double
-// what the products read from it). The columns hold, per tile, D of O, 64 of S
-// and two P of 32, written in turns.
+// Per query tile and key tile j: S = Q K_j^T (tcgen05 kind::f16, fp32 in TMEM)
+// into one of two buffers; the softmax reads S into registers and writes p as
+// fp16 over it, and O += P V_j reads it there (P in shared memory would double
+// what the products read from it). QK_{j+1} fills the other buffer meanwhile,
+// and QK_{j+2} waits for PV_j. The columns hold, per query tile, D of O and two
+// times 64 of S.
 // Numbers. Queries become fp16 times a power of two per row (their largest
 // value in [1, 4)); key and value codes are exact in fp16. The value scales go
 // into the weights: with R the largest value scale of the part's blocks so far
@@ -57,7 +57,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kTmemCols = 512;
 
 // registers per thread of the control, converter and softmax warps
-constexpr uint32_t kRegCtl = 64, kRegConv = 112, kRegSoftmax = 168;
+constexpr uint32_t kRegCtl = 56, kRegConv = 104, kRegSoftmax = 176;
 constexpr uint32_t kRegLaunch = 65536 / kThreads / 8 * 8;
 static_assert(128 * kRegCtl + 32 * kConv * kRegConv + 256 * kRegSoftmax <= kThreads * kRegLaunch,
               "registers that the CTA is launched with");
@@ -77,8 +77,8 @@ struct Smem {
 };
 constexpr int kMaxStages = 8;
 constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarFull = kBarQEmpty + 2, kBarEmpty = kBarFull + kMaxStages;
-constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarSFree = kBarSFull + 2, kBarPFull = kBarSFree + 2;
-constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarTop = kBarDrain + 2;  // PFull, PVDone: [tile][P buffer]
+constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarPFull = kBarSFull + 4;
+constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarTop = kBarDrain + 2;  // SFull, PFull, PVDone: [tile][buffer]
 constexpr int kNumBars = kBarTop + 1;
 template <int D>
 struct SmemTail {
@@ -102,14 +102,15 @@ struct SmemTail {
 };
 static_assert(SmemTail<128>::kBytes <= 232448u, "shared memory of one CTA");
 
-constexpr int kP = 2;                    // buffers of P
+constexpr int kS = 2;                    // buffers of S and P
 constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 // TMEM columns of the query tiles
 template <int D>
 struct Cols {
   __host__ __device__ static constexpr uint32_t o(int i) { return 128u * static_cast<uint32_t>(i); }
-  __host__ __device__ static constexpr uint32_t s(int i) { return 256u + 128u * static_cast<uint32_t>(i); }
-  __host__ __device__ static constexpr uint32_t p(int i, int buf) { return s(i) + 64u + 32u * static_cast<uint32_t>(buf); }
+  __host__ __device__ static constexpr uint32_t s(int i, int buf) {
+    return 256u + 128u * static_cast<uint32_t>(i) + 64u * static_cast<uint32_t>(buf);
+  }
 };
 
 // One arrival for the warp, after what its lanes did (an arrival per lane would
@@ -403,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(cx.bar(kBarQFull + s), kConv);
       tc::mbar_init(cx.bar(kBarQEmpty + s), 2);
-      tc::mbar_init(cx.bar(kBarSFull + s), 2);
-      tc::mbar_init(cx.bar(kBarSFree + s), kRows);
+      tc::mbar_init(cx.bar(kBarSFull + 2 * s), 2);
+      tc::mbar_init(cx.bar(kBarSFull + 2 * s + 1), 2);
       tc::mbar_init(cx.bar(kBarPFull + 2 * s), kRows);
       tc::mbar_init(cx.bar(kBarPFull + 2 * s + 1), kRows);
       tc::mbar_init(cx.bar(kBarPVDone + 2 * s), 1);
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       // ------------------------------------------------ MMA issuer of tile i --
       const int i = warp;
       const bool leader = elect_one();
-      const uint32_t d_s = tmem + C::s(i), d_o = tmem + C::o(i);
+      const uint32_t d_o = tmem + C::o(i);
       const uint64_t dq0 = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dv0 = tc::sw128_desc(sbase + L::kOffV);
       // key tiles (of the converters, of this query tile) and parts so far
@@ -510,13 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           const int s = static_cast<int>((cnt + static_cast<uint32_t>(j)) % L::kStages);
           if (j < n) {
             const uint32_t st = steps + static_cast<uint32_t>(j);
-            // (a barrier per P buffer: the softmax may be two tiles ahead of this wait)
-            const int pb = static_cast<int>(st % kP);
-            if (!wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + pb), (st / kP) & 1u)) return false;
+            const int buf = static_cast<int>(st % kS);
+            if (!wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + buf), (st / kS) & 1u)) return false;
             tc::tc_fence_after();
             if (leader) {
-              issue_pv<D>(d_o, tmem + C::p(i, pb), desc_at(dv0, static_cast<uint32_t>(s) * L::kTileKV), j > 0);
-              tc::mma_commit(cx.bar(kBarPVDone + 2 * i + pb));
+              issue_pv<D>(d_o, tmem + C::s(i, buf), desc_at(dv0, static_cast<uint32_t>(s) * L::kTileKV), j > 0);
+              tc::mma_commit(cx.bar(kBarPVDone + 2 * i + buf));
               tc::mma_commit(cx.bar(kBarEmpty + s));
             }
           } else if (leader) {
@@ -535,18 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
               if (!(ok = pv(j - 1))) break;
               pending = false;
             }
-            // QK_j once its keys are there and the softmax has read S_{j-1}
+            // QK_j once its keys are there and PV_{j-2} has read P in its buffer
             if (!(ok = wait_bar_warp(cx, full, ph))) break;
             if (j < n) {
               const uint32_t st = steps + static_cast<uint32_t>(j);
-              if (st > 0 && !(ok = wait_bar_warp(cx, cx.bar(kBarSFree + i), (st - 1u) & 1u))) break;
+              const int buf = static_cast<int>(st % kS);
+              if (st >= kS && !(ok = wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + buf), (st / kS - 1u) & 1u))) break;
               tc::tc_fence_after();
               if (leader) {
-                // S is there when the MMAs are done (this one and all before it); the plain
-                // arrival passes on what the converters wrote: scales, powers of two
-                tc::mbar_arrive(cx.bar(kBarSFull + i));
-                issue_qk<D>(d_s, dq, desc_at(dk0, s * L::kTileKV));
-                tc::mma_commit(cx.bar(kBarSFull + i));
+                // S is there when the MMAs are done; the plain arrival passes on what the
+                // converters wrote: scales, powers of two
+                tc::mbar_arrive(cx.bar(kBarSFull + 2 * i + buf));
+                issue_qk<D>(tmem + C::s(i, buf), dq, desc_at(dk0, s * L::kTileKV));
+                tc::mma_commit(cx.bar(kBarSFull + 2 * i + buf));
                 if (j == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
               }
               __syncwarp();
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     regs_inc<kRegSoftmax>();
     const int i = (warp - 4) >> 2, wq = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tO = tmem + lane_addr + C::o(i), tS = tO + (C::s(0) - C::o(0));
+    const uint32_t tO = tmem + lane_addr + C::o(i);
     const float4* scales = reinterpret_cast<const float4*>(smem + T::kOffScale);
     const float2* tops = reinterpret_cast<const float2*>(smem + T::kOffTopOf);
     const int rr = i * kRows + wq * 32 + lane;  // this thread's row of a pair
@@ -771,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     uint32_t steps = 0, windows = 0, parts = 0;  // key tiles of this query tile; the converters' windows and units
     // waits for the PV of step x (its P buffer and O are then free)
     const auto wait_pv = [&](uint32_t x) {
-      return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + static_cast<int>(x % kP)), (x / kP) & 1u);
+      return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + static_cast<int>(x % kS)), (x / kS) & 1u);
     };
     Place p = first_place(found);
     while (p.todo > 0) {
@@ -789,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t st = steps + static_cast<uint32_t>(j);
-        if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + i), st & 1u))) break;
+        const uint32_t buf = st % kS, tS = tO + (C::s(0, 0) - C::o(0)) + (C::s(0, 1) - C::s(0, 0)) * buf;
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarSFull + 2 * i + static_cast<int>(buf)), (st / kS) & 1u))) break;
         tc::tc_fence_after();
         uint32_t sr[kB][32];
 #pragma unroll
@@ -804,8 +806,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           factor = tops[win].y;
         }
         tc::tmem_wait_ld();
-        tc::tc_fence_before();
-        tc::mbar_arrive(cx.bar(kBarSFree + i));  // the next QK may overwrite S
         const int key0 = (p.t + j) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
@@ -817,14 +817,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           lim[b] = k < 0.0f ? 0 : sees - key0 - 32 * b;
           masked |= k < 0.0f;
         }
-        float mt = -INFINITY;
+        if (masked) {
 #pragma unroll
-        for (int b = 0; b < kB; ++b) {
-          if (masked) {
+          for (int b = 0; b < kB; ++b)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
-          }
+        }
+        // p s_v / R, whose sum over a block is taken back to that of p. First
+        // with the running maximum as it is, next to the search for this
+        // tile's; that stands unless some row has grown by 2^8.
+        uint32_t pw[kB][16];
+        float sum[kB], mt = -INFINITY;
+        const bool plain = j > 0 && !masked && factor == 1.0f;
+        if (plain) {
+#pragma unroll
+          for (int b = 0; b < kB; ++b)
+            sum[b] = exp_block<false>(sr[b], cb[b], (b == 0 ? sc.z : sc.w) - (m == -INFINITY ? 0.0f : m), 32, pw[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
           float m0 = __uint_as_float(sr[b][0]), m1 = __uint_as_float(sr[b][1]);
 #pragma unroll
           for (int c = 2; c < 30; c += 4) {
@@ -835,7 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           m0 = fmaxf(m0, m1);
           mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
         }
-        if (__any_sync(0xffffffffu, mt > m + kLazy) || factor != 1.0f) {
+        const bool grew = __any_sync(0xffffffffu, mt > m + kLazy);
+        if (grew || factor != 1.0f) {
           const float up = fmaxf(m, mt);
           const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
           m = up;
@@ -860,29 +873,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
-        // the buffer's last PV, two tiles back, was issued before this tile's QK,
-        // so it was done when S was there
-        const uint32_t tP = tS + (C::p(0, 0) - C::s(0)) + (C::p(0, 1) - C::p(0, 0)) * (st % kP);
+        if (!plain || grew) {
+#pragma unroll
+          for (int b = 0; b < kB; ++b)
+            sum[b] = exp_block<true>(sr[b], cb[b], (b == 0 ? sc.z : sc.w) - (m == -INFINITY ? 0.0f : m), lim[b], pw[b]);
+        }
+        // P goes over this row's S, which is in registers
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          // p s_v / R, whose sum over the block is taken back to that of p
+          tmem_st16(tS + 16u * b, pw[b]);
           // (a block that the row does not reach adds nothing, whatever its scale is)
-          uint32_t pw[16];
-          const float lh = b == 0 ? sc.z : sc.w;
-          float back = ex2(-lh), sum;
-          if (masked) {
-            sum = exp_block<true>(sr[b], cb[b], lh - ref, lim[b], pw);
-            if (lim[b] <= 0) back = 0.0f;
-          } else {
-            sum = exp_block<false>(sr[b], cb[b], lh - ref, 32, pw);
-          }
-          tmem_st16(tP + 16u * b, pw);
-          l = fmaf(sum, back, l);
+          l = fmaf(sum[b], lim[b] > 0 ? ex2(-(b == 0 ? sc.z : sc.w)) : 0.0f, l);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(cx.bar(kBarPFull + 2 * i + static_cast<int>(st % kP)));
+        tc::mbar_arrive(cx.bar(kBarPFull + 2 * i + static_cast<int>(buf)));
       }
       if (!ok) break;
       steps += static_cast<uint32_t>(n);
