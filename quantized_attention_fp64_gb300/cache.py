@@ -256,13 +256,13 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
             key = None
     if kept is not None and kept[2] == _get_device():
         args, ref, index, shape = kept
-        both = torch.empty(shape, dtype=torch.bfloat16, device=page_table.device)
+        device = page_table.device
+        k, v = torch.empty(shape, dtype=torch.bfloat16, device=device), torch.empty(shape, dtype=torch.bfloat16, device=device)
         args.cache = cache.address
         args.table_dev = page_table.data_ptr()
         args.starts_dev = starts.data_ptr()
         if counts is not None:
             args.counts_dev = counts.data_ptr()
-        k, v = both.unbind(0)
         args.k_out.ptr_dev = k.data_ptr()
         args.v_out.ptr_dev = v.data_ptr()
         args.cuda_stream = _stream_handle(index)
@@ -279,10 +279,10 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
     if starts is None:
         raise TypeError("starts must be a torch tensor")
     st, ct = _ints(starts, B, cache, "starts"), _ints(counts, B, cache, "counts")
-    shape = (2, B, T, cache.H, cache.D) if tensor_layout == "NHD" else (2, B, cache.H, T, cache.D)
+    shape = (B, T, cache.H, cache.D) if tensor_layout == "NHD" else (B, cache.H, T, cache.D)
     zero_rest = out is None
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device).unbind(0)
+        out = [torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device) for _ in (0, 1)]
     k, v = out
     ks, ko = _tokens(k, cache, tensor_layout, "out")
     vs, vo = _tokens(v, cache, tensor_layout, "out")

@@ -16,6 +16,7 @@
 
 #include "cache.cuh"
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace sage {
 namespace {
@@ -70,40 +71,72 @@ __device__ Span find_span(const CacheView& c, const PageTable& pt, const int32_t
   return s;
 }
 
+// A token's D channels are D / 8 lanes wide, 16 bytes of BF16 and 8 codes a
+// lane, so 128 threads cover kRows tokens at a time and every access to global
+// memory is whole sectors. Value codes change between token rows and channel
+// rows in shared memory, four channels by eight positions to a thread.
+template <int D>
+struct Tile {
+  static constexpr int kLanes = D / 8;           // lanes of a token
+  static constexpr int kRows = 128 / kLanes;     // tokens at a time
+  static constexpr int kTimes = kCacheBlock / kRows;
+  static constexpr int kPitch = D + 16;          // bytes of a token row in shared memory: no bank conflicts
+  static constexpr int kQuads = D;               // units of 4 channels x 8 positions: D / 4 x 4
+};
+
+// Bytes 4 x 4: out[p] gets byte p of w0..w3.
+__device__ __forceinline__ void transpose4(const uint32_t (&w)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  out[0] = __byte_perm(a, b, 0x5410);
+  out[1] = __byte_perm(a, b, 0x7632);
+  out[2] = __byte_perm(c, d, 0x5410);
+  out[3] = __byte_perm(c, d, 0x7632);
+}
+
+__device__ __forceinline__ uint32_t shrink4(uint32_t w, float r) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o |= (static_cast<uint32_t>(static_cast<int>(rintf(static_cast<int8_t>(w >> (8 * e)) * r))) & 255u) << (8 * e);
+  return o;
+}
+
 // ------------------------------------------------------------------ append --
 // One CTA writes one block of one head: threads 0..127 its keys, 128..255 its
-// values. Four threads share a token, D / 4 channels each.
+// values.
 template <int D>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
                                                                 const int32_t* counts, Bf16In k, Bf16In v, int64_t T,
                                                                 int* dev_err) {
-  constexpr int kCh = D / 4;  // channels per thread
-  constexpr int kW = kCh / 2; // 32-bit words of them
-  // value codes of the block, transposed through shared memory: 36-byte rows
-  // so that the byte stores of one warp (8 tokens x 4 channel groups) spread
-  __shared__ __align__(16) uint8_t vt[D * 36];
+  using L = Tile<D>;
+  __shared__ __align__(16) uint8_t vt[kCacheBlock * L::kPitch];
   __shared__ uint32_t amax_w[8];
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
   const Span s = find_span(c, pt, starts, counts, T, dev_err);
   if (s.slot < 0) return;
   const int half = threadIdx.x >> 7, i = threadIdx.x & 127;
-  const int row = i >> 2, part = i & 3;  // token slot, channel group
-  const bool mine = row >= s.first && row < s.end;
+  const int ch = (i % L::kLanes) * 8, row0 = i / L::kLanes;
   const Bf16In& in = half ? v : k;
   float* scale_at = (half ? c.vs : c.ks) + s.slot;
   const float s_old = s.first > 0 ? *scale_at : 0.0f;
-  uint32_t w[kW];
+  const uint16_t* src = in.p + static_cast<int64_t>(blockIdx.z) * in.sb + static_cast<int64_t>(blockIdx.y) * in.sh + ch;
+  uint4 x[L::kTimes];
 #pragma unroll
-  for (int q = 0; q < kW; ++q) w[q] = 0u;
-  if (mine) {
-    const uint16_t* p = in.p + static_cast<int64_t>(blockIdx.z) * in.sb + (s.t0 + row) * in.ss +
-                        static_cast<int64_t>(blockIdx.y) * in.sh + part * kCh;
-#pragma unroll
-    for (int q = 0; q < kW / 4; ++q) reinterpret_cast<uint4*>(w)[q] = reinterpret_cast<const uint4*>(p)[q];
+  for (int q = 0; q < L::kTimes; ++q) {
+    const int row = q * L::kRows + row0;
+    x[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= s.first && row < s.end) x[q] = *reinterpret_cast<const uint4*>(src + (s.t0 + row) * in.ss);
   }
   // max |x| as bit patterns: those of infinities and NaN are the largest
   uint32_t a = 0;
 #pragma unroll
-  for (int q = 0; q < kW; ++q) a = max(a, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
+  for (int q = 0; q < L::kTimes; ++q) {
+    const uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a = max(a, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
   if ((threadIdx.x & 31) == 0) amax_w[threadIdx.x >> 5] = a;
@@ -117,66 +150,65 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, Pag
   const float shrink = (grew && usable) ? __fdiv_rn(s_old, s_new) : 0.0f;
   if (i == 0) *scale_at = s_new;
   int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
-  uint32_t codes[kCh / 4];
 #pragma unroll
-  for (int q = 0; q < kCh / 4; ++q) {
-    codes[q] = 0u;
-    if (mine && usable)
-      codes[q] = pack4(quantize_one(bf16_lo(w[2 * q]), s_new), quantize_one(bf16_hi(w[2 * q]), s_new),
-                       quantize_one(bf16_lo(w[2 * q + 1]), s_new), quantize_one(bf16_hi(w[2 * q + 1]), s_new));
-  }
-  if (half == 0) {
-    // keys: this thread's channels lie inside one 64-channel half
-    int8_t* p = block + (part * kCh / 64) * (kCacheBlock * 64) + row * 64 + (part * kCh) % 64;
-    if (row < s.first) {
-      if (grew) {
-#pragma unroll
-        for (int q = 0; q < kCh / 16; ++q) {
-          uint4 o = reinterpret_cast<uint4*>(p)[q];
-          int8_t* ob = reinterpret_cast<int8_t*>(&o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) ob[e] = static_cast<int8_t>(rintf(ob[e] * shrink));
-          reinterpret_cast<uint4*>(p)[q] = o;
-        }
+  for (int q = 0; q < L::kTimes; ++q) {
+    const int row = q * L::kRows + row0;
+    uint2 codes = make_uint2(0u, 0u);
+    if (usable && row >= s.first && row < s.end) {
+      codes.x = pack4(quantize_one(bf16_lo(x[q].x), s_new), quantize_one(bf16_hi(x[q].x), s_new),
+                      quantize_one(bf16_lo(x[q].y), s_new), quantize_one(bf16_hi(x[q].y), s_new));
+      codes.y = pack4(quantize_one(bf16_lo(x[q].z), s_new), quantize_one(bf16_hi(x[q].z), s_new),
+                      quantize_one(bf16_lo(x[q].w), s_new), quantize_one(bf16_hi(x[q].w), s_new));
+    }
+    if (half == 0) {
+      uint2* p = reinterpret_cast<uint2*>(block + (ch / 64) * (kCacheBlock * 64) + row * 64 + ch % 64);
+      if (row >= s.first) {
+        *p = codes;
+      } else if (grew) {
+        const uint2 was = *p;
+        *p = make_uint2(shrink4(was.x, shrink), shrink4(was.y, shrink));
       }
     } else {
-#pragma unroll
-      for (int q = 0; q < kCh / 16; ++q)
-        reinterpret_cast<uint4*>(p)[q] = make_uint4(codes[4 * q], codes[4 * q + 1], codes[4 * q + 2], codes[4 * q + 3]);
+      *reinterpret_cast<uint2*>(vt + row * L::kPitch + ch) = codes;
     }
-  } else {
-    const int pos = value_position(row);
-#pragma unroll
-    for (int e = 0; e < kCh; ++e) vt[(part * kCh + e) * 36 + pos] = static_cast<uint8_t>(codes[e / 4] >> (8 * (e % 4)));
   }
   __syncthreads();
-  if (half == 1) {
-    for (int ch = i; ch < D; ch += 128) {
-      uint32_t o[8];
+  if (half == 1 && i < L::kQuads) {
+    const int quad = i >> 2, g = i & 3;  // channels 4 quad .. + 3, positions 8 g .. + 7
+    uint32_t lo[4], hi[4], w[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = *reinterpret_cast<const uint32_t*>(vt + ch * 36 + 4 * q);
-      int8_t* p = block + ch * kCacheBlock;
+    for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(vt + value_token(8 * g + e) * L::kPitch + 4 * quad);
+    transpose4(w, lo);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = *reinterpret_cast<const uint32_t*>(vt + value_token(8 * g + 4 + e) * L::kPitch + 4 * quad);
+    transpose4(w, hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint2* p = reinterpret_cast<uint2*>(block + (4 * quad + e) * kCacheBlock + 8 * g);
+      uint2 o = make_uint2(lo[e], hi[e]);
       if (s.first > 0) {
         // older tokens' codes stay in the block
-        uint32_t was[8];
-        *reinterpret_cast<uint4*>(was) = reinterpret_cast<const uint4*>(p)[0];
-        *reinterpret_cast<uint4*>(was + 4) = reinterpret_cast<const uint4*>(p)[1];
-        int8_t* ob = reinterpret_cast<int8_t*>(o);
-        const int8_t* wb = reinterpret_cast<const int8_t*>(was);
+        uint2 was = *p;
+        if (grew) was = make_uint2(shrink4(was.x, shrink), shrink4(was.y, shrink));
+        uint32_t keep_lo = 0, keep_hi = 0;
 #pragma unroll
-        for (int e = 0; e < kCacheBlock; ++e)
-          if (value_token(e) < s.first) ob[e] = grew ? static_cast<int8_t>(rintf(wb[e] * shrink)) : wb[e];
+        for (int b = 0; b < 4; ++b) {
+          if (value_token(8 * g + b) < s.first) keep_lo |= 255u << (8 * b);
+          if (value_token(8 * g + 4 + b) < s.first) keep_hi |= 255u << (8 * b);
+        }
+        o = make_uint2((was.x & keep_lo) | (o.x & ~keep_lo), (was.y & keep_hi) | (o.y & ~keep_hi));
       }
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      *p = o;
     }
   }
 }
 
 // -------------------------------------------------------------------- read --
 
-__device__ __forceinline__ uint32_t to_bf16x2(float a, float b) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t codes, int at, float scale) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(static_cast<int8_t>(codes >> (8 * at)) * scale,
+                                                 static_cast<int8_t>(codes >> (8 * at + 8)) * scale);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -184,53 +216,59 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageTable pt, const int32_t* starts,
                                                               const int32_t* counts, Out k, Out v, int64_t T,
                                                               bool zero_rest, int* dev_err) {
-  constexpr int kCh = D / 4;
-  __shared__ __align__(16) uint8_t vt[D * 36];
+  using L = Tile<D>;
+  __shared__ __align__(16) uint8_t vt[kCacheBlock * L::kPitch];
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
   const Span s = find_span(c, pt, starts, counts, T, dev_err);
   const int half = threadIdx.x >> 7, i = threadIdx.x & 127;
-  const int row = i >> 2, part = i & 3;
+  const int ch = (i % L::kLanes) * 8, row0 = i / L::kLanes;
   const Out& o = half ? v : k;
-  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + (s.t0 + row) * o.ss +
-                  static_cast<int64_t>(blockIdx.y) * o.sh + part * kCh;
-  if (zero_rest && row >= s.first && s.t0 + row < T && (row >= s.end || s.slot < 0)) {
+  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + static_cast<int64_t>(blockIdx.y) * o.sh + ch;
+  if (zero_rest) {
 #pragma unroll
-    for (int q = 0; q < kCh / 8; ++q) reinterpret_cast<uint4*>(dst)[q] = make_uint4(0u, 0u, 0u, 0u);
+    for (int q = 0; q < L::kTimes; ++q) {
+      const int row = q * L::kRows + row0;
+      if (row >= s.first && s.t0 + row < T && (row >= s.end || s.slot < 0))
+        *reinterpret_cast<uint4*>(dst + (s.t0 + row) * o.ss) = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
   if (s.slot < 0) return;
   const float scale = (half ? c.vs : c.ks)[s.slot];
   const int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
-  uint32_t codes[kCh / 4];
-  if (half == 1) {
-    for (int ch = i; ch < D; ch += 128) {
-      uint32_t o[8];
-      *reinterpret_cast<uint4*>(o) = reinterpret_cast<const uint4*>(block + ch * kCacheBlock)[0];
-      *reinterpret_cast<uint4*>(o + 4) = reinterpret_cast<const uint4*>(block + ch * kCacheBlock)[1];
+  uint2 codes[L::kTimes];
+  if (half == 0) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) *reinterpret_cast<uint32_t*>(vt + ch * 36 + 4 * q) = o[q];
-    }
-  } else {
-    const int8_t* p = block + (part * kCh / 64) * (kCacheBlock * 64) + row * 64 + (part * kCh) % 64;
+    for (int q = 0; q < L::kTimes; ++q)
+      codes[q] = *reinterpret_cast<const uint2*>(block + (ch / 64) * (kCacheBlock * 64) + (q * L::kRows + row0) * 64 + ch % 64);
+  } else if (i < L::kQuads) {
+    const int quad = i >> 2, g = i & 3;
+    uint2 x[4];
 #pragma unroll
-    for (int q = 0; q < kCh / 16; ++q) reinterpret_cast<uint4*>(codes)[q] = reinterpret_cast<const uint4*>(p)[q];
+    for (int e = 0; e < 4; ++e)
+      x[e] = *reinterpret_cast<const uint2*>(block + (4 * quad + e) * kCacheBlock + 8 * g);
+    uint32_t w[4], t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = x[e].x;
+    transpose4(w, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(vt + value_token(8 * g + e) * L::kPitch + 4 * quad) = t[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = x[e].y;
+    transpose4(w, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<uint32_t*>(vt + value_token(8 * g + 4 + e) * L::kPitch + 4 * quad) = t[e];
   }
   __syncthreads();
-  if (row < s.first || row >= s.end) return;
-  if (half == 1) {
-    const int pos = value_position(row);
 #pragma unroll
-    for (int q = 0; q < kCh / 4; ++q) {
-      const uint8_t* p = vt + (part * kCh + 4 * q) * 36 + pos;
-      codes[q] = p[0] | (p[36] << 8) | (p[72] << 16) | (static_cast<uint32_t>(p[108]) << 24);
-    }
+  for (int q = 0; q < L::kTimes; ++q) {
+    const int row = q * L::kRows + row0;
+    if (row < s.first || row >= s.end) continue;
+    const uint2 w = half ? *reinterpret_cast<const uint2*>(vt + row * L::kPitch + ch) : codes[q];
+    *reinterpret_cast<uint4*>(dst + (s.t0 + row) * o.ss) =
+        make_uint4(to_bf16x2(w.x, 0, scale), to_bf16x2(w.x, 2, scale), to_bf16x2(w.y, 0, scale), to_bf16x2(w.y, 2, scale));
   }
-  const int8_t* cb = reinterpret_cast<const int8_t*>(codes);
-#pragma unroll
-  for (int q = 0; q < kCh / 8; ++q)
-    reinterpret_cast<uint4*>(dst)[q] =
-        make_uint4(to_bf16x2(cb[8 * q] * scale, cb[8 * q + 1] * scale),
-                   to_bf16x2(cb[8 * q + 2] * scale, cb[8 * q + 3] * scale),
-                   to_bf16x2(cb[8 * q + 4] * scale, cb[8 * q + 5] * scale),
-                   to_bf16x2(cb[8 * q + 6] * scale, cb[8 * q + 7] * scale));
 }
 
 // -------------------------------------------------------------------- copy --
@@ -247,6 +285,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, c
                                                                   int64_t n, int64_t codes_bytes, int64_t scales,
                                                                   int64_t chunks, int* dev_err) {
   extern __shared__ uint32_t taken[];
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
   const int64_t words = (c.num_pages + 31) / 32;
   for (int64_t i = threadIdx.x; i < words; i += kCopyThreads) taken[i] = 0u;
   __syncthreads();
@@ -278,12 +318,40 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, c
     const int64_t lo = chunk * kCopyChunk, hi = min(lo + kCopyChunk, codes_bytes);
     const uint4* from = reinterpret_cast<const uint4*>(base + s * codes_bytes);
     uint4* to = reinterpret_cast<uint4*>(base + d * codes_bytes);
-    for (int64_t q = lo / 16 + threadIdx.x; q < hi / 16; q += kCopyThreads) to[q] = from[q];
+    // a whole chunk is eight 16-byte pieces per thread, all in flight at once
+    uint4 x[kCopyChunk / 16 / kCopyThreads];
+#pragma unroll
+    for (int y = 0; y < kCopyChunk / 16 / kCopyThreads; ++y) {
+      const int64_t q = lo / 16 + threadIdx.x + y * kCopyThreads;
+      if (q < hi / 16) x[y] = from[q];
+    }
+#pragma unroll
+    for (int y = 0; y < kCopyChunk / 16 / kCopyThreads; ++y) {
+      const int64_t q = lo / 16 + threadIdx.x + y * kCopyThreads;
+      if (q < hi / 16) to[q] = x[y];
+    }
     if (chunk == 0) {
       float* sc = which ? c.vs : c.ks;
       for (int64_t q = threadIdx.x; q < scales; q += kCopyThreads) sc[d * scales + q] = sc[s * scales + q];
     }
   }
+}
+
+// Launched as a programmatic dependent: the grid may come up while the stream's
+// previous kernel still runs; it waits for it before it reads anything.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 dim3 span_grid(const CacheView& c, int64_t B, int64_t T) {
@@ -297,21 +365,15 @@ dim3 span_grid(const CacheView& c, int64_t B, int64_t T) {
 cudaError_t launch_cache_append(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
                                 const int32_t* counts, const Bf16In& k, const Bf16In& v, int64_t B, int64_t T,
                                 int* dev_err, cudaStream_t stream) {
-  if (D == 128)
-    cache_append_kernel<128><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, dev_err);
-  else
-    cache_append_kernel<64><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, dev_err);
-  return cudaGetLastError();
+  return launch(D == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, span_grid(c, B, T), kThreads, 0, stream, c,
+                pt, starts, counts, k, v, T, dev_err);
 }
 
 cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
                               const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T,
                               bool zero_rest, int* dev_err, cudaStream_t stream) {
-  if (D == 128)
-    cache_read_kernel<128><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, zero_rest, dev_err);
-  else
-    cache_read_kernel<64><<<span_grid(c, B, T), kThreads, 0, stream>>>(c, pt, starts, counts, k, v, T, zero_rest, dev_err);
-  return cudaGetLastError();
+  return launch(D == 128 ? cache_read_kernel<128> : cache_read_kernel<64>, span_grid(c, B, T), kThreads, 0, stream, c, pt,
+                starts, counts, k, v, T, zero_rest, dev_err);
 }
 
 cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t* src, const int32_t* dst, int64_t n,
@@ -323,9 +385,8 @@ cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(cache_copy_kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t work = n * 2 * chunks, most = int64_t(8) * sm_count_current();
-  cache_copy_kernel<<<static_cast<unsigned>(work < most ? work : most), kCopyThreads, smem, stream>>>(
-      c, src, dst, n, bytes, scales, chunks, dev_err);
-  return cudaGetLastError();
+  return launch(cache_copy_kernel, dim3(static_cast<unsigned>(work < most ? work : most)), kCopyThreads,
+                static_cast<size_t>(smem), stream, c, src, dst, n, bytes, scales, chunks, dev_err);
 }
 
 }  // namespace sage
