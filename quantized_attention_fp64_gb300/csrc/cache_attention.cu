@@ -19,7 +19,7 @@
 // in the workspace, two slots per CTA, and a second kernel joins them in the
 // order of the keys.
 // Warps. Each of a CTA's 4 warps takes every 4th block of the range through a
-// ring of its own: lane 0 copies a block's keys and values (contiguous in the
+// ring of its own: a lane copies a block's keys and values (contiguous in the
 // cache) into shared memory with bulk copies that complete on an mbarrier,
 // kStages blocks ahead, so loads never wait for another warp. The warps' parts
 // of an item are joined in shared memory where the item ends; two or three CTAs
@@ -145,15 +145,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int*
   }
 }
 
-// 4-byte asynchronous copy whose completion counts as one arrival on `bar`
-// (together with the thread's earlier ones).
-__device__ __forceinline__ void cp_async4_only(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // ------------------------------------------------------------------ decode --
 
 constexpr int kWarps = 4;
@@ -172,8 +163,7 @@ struct Dec {
   static constexpr uint32_t kOffMerge = kRing;                 // [warp][16 rows][32 channels] fp32
   static constexpr uint32_t kOffMl = kOffMerge + kWarps * 16 * 32 * 4;  // [warp][16 MT rows] (m, l)
   static constexpr uint32_t kOffScale = kOffMl + kWarps * 16 * MT * 8;  // [warp][stage] (key, value) scale
-  static constexpr uint32_t kOffValid = kOffScale + kWarps * kStages * 8;
-  static constexpr uint32_t kOffBar = kOffValid + kWarps * kStages * 4;
+  static constexpr uint32_t kOffBar = kOffScale + kWarps * kStages * 8;
   static constexpr uint32_t kOffPlan = kOffBar + kWarps * kStages * 8;  // kWarps sums, then (b, unit in b)
   static constexpr uint32_t kBytes = kOffPlan + (kWarps + 2) * 4;
   static_assert(kCtasPerSm * (kBytes + 1024) <= 233472u && kOffBar % 8 == 0, "shared memory of one SM");
@@ -258,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
   const uint32_t sbase = tc::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  if (threadIdx.x < kWarps * L::kStages) tc::mbar_init(sbase + L::kOffBar + 8 * threadIdx.x, 2);
+  if (threadIdx.x < kWarps * L::kStages) tc::mbar_init(sbase + L::kOffBar + 8 * threadIdx.x, 1);
   tc::fence_mbar_init();
   // the previous kernel of the stream may still run up to here
   tc::griddep_wait();
@@ -340,9 +330,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
   Cursor ahead = seg;
   ahead.blk += warp + lane * kWarps;
   if (lane < n_mine) cursor_settle(a, ahead);
-  int64_t window = -1;  // its block number in the cache, -1: no tokens
+  int64_t at_codes = -1;               // first byte in the codes, -1: no tokens
+  float2 at_scales = make_float2(-1.0f, 0.0f);  // key scale (-1: no tokens), value scale
   const auto fill_window = [&](int k0) {
-    window = -1;
+    at_codes = -1;
+    at_scales.x = -1.0f;
     if (k0 + lane < n_mine) {
       if (k0 > 0) {
         ahead.blk += 32 * kWarps;
@@ -351,35 +343,32 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       if (ahead.s.q_len > 0 && ahead.blk * kCacheBlock < ahead.s.len) {
         const int pg = ahead.blk / a.c.blocks_per_page;
         const int page = a.pt.table[ahead.b * a.pt.stride + pg];
-        if (page_ok(page, a.c.num_pages))
-          window = block_slot(page, ahead.h, a.c.H, a.c.blocks_per_page, ahead.blk - pg * a.c.blocks_per_page);
-        else
+        if (page_ok(page, a.c.num_pages)) {
+          const int64_t slot = block_slot(page, ahead.h, a.c.H, a.c.blocks_per_page, ahead.blk - pg * a.c.blocks_per_page);
+          at_codes = slot * L::kBlockBytes;
+          at_scales = make_float2(a.c.ks[slot], a.c.vs[slot]);
+        } else {
           atomicExch(a.dev_err, kDevErrPage);
+        }
       }
     }
   };
   const uint32_t ring = sbase + static_cast<uint32_t>(warp) * L::kStages * 2 * L::kBlockBytes;
   const uint32_t bars = sbase + L::kOffBar + static_cast<uint32_t>(warp) * L::kStages * 8;
-  const uint32_t scales = sbase + L::kOffScale + static_cast<uint32_t>(warp) * L::kStages * 8;
-  volatile int* valid = reinterpret_cast<volatile int*>(smem + L::kOffValid) + warp * L::kStages;
+  float2* scales = reinterpret_cast<float2*>(smem + L::kOffScale) + warp * L::kStages;
   int issued = 0;
   uint32_t into = 0;  // stage of the next issue
-  const auto issue = [&]() {  // whole warp
+  const auto issue = [&]() {  // whole warp; the lane that has the block sends for it
     if (issued >= n_mine) return;
     if ((issued & 31) == 0) fill_window(issued);
-    const int64_t slot = __shfl_sync(0xffffffffu, window, issued & 31);
-    if (lane == 0) {
+    if (lane == (issued & 31)) {
       const uint32_t bar = bars + 8 * into, dst = ring + into * 2 * L::kBlockBytes;
-      valid[into] = slot >= 0;
-      if (slot >= 0) {
+      scales[into] = at_scales;
+      if (at_codes >= 0) {
         tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
-        tc::bulk_load(dst, a.c.k + slot * L::kBlockBytes, L::kBlockBytes, bar);
-        tc::bulk_load(dst + L::kBlockBytes, a.c.v + slot * L::kBlockBytes, L::kBlockBytes, bar);
-        cp_async4_only(scales + 8 * into, a.c.ks + slot);
-        cp_async4_only(scales + 8 * into + 4, a.c.vs + slot);
-        cp_async_arrive(bar);
+        tc::bulk_load(dst, a.c.k + at_codes, L::kBlockBytes, bar);
+        tc::bulk_load(dst + L::kBlockBytes, a.c.v + at_codes, L::kBlockBytes, bar);
       } else {
-        tc::mbar_arrive(bar);
         tc::mbar_arrive(bar);
       }
     }
@@ -463,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       const uint32_t s = from;
       alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * s, parity, a.dev_err));
       if (!alive) break;
-      if (valid[s] != 0) {
+      const float2 sc = scales[s];
+      if (sc.x >= 0.0f || sc.x != sc.x) {
         const uint8_t* kb = smem + (ring - sbase) + s * 2 * L::kBlockBytes;
         const uint8_t* vb = kb + L::kBlockBytes;
-        const float2 sc = *reinterpret_cast<const float2*>(smem + (scales - sbase) + 8 * s);
         const int key0 = (seg.blk + (u - at)) * kCacheBlock;
         float z[MT][4][4];
 #pragma unroll
