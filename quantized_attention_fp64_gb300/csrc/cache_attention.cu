@@ -160,7 +160,8 @@ struct Dec {
   static constexpr int kStages = (MT == 1 ? 2 : 3) * (128 / D);
   static constexpr uint32_t kBlockBytes = kCacheBlock * D;     // keys or values of a block
   static constexpr uint32_t kRing = kWarps * kStages * 2 * kBlockBytes;
-  static constexpr uint32_t kOffMerge = kRing;                 // [warp][16 rows][32 channels] fp32
+  static constexpr uint32_t kOffMerge = kRing;                 // [warp][16 rows][32 channels] fp32, or the queries
+  static_assert(16 * MT * D * 2 <= kWarps * 16 * 32 * 4, "the queries fit");
   static constexpr uint32_t kOffMl = kOffMerge + kWarps * 16 * 32 * 4;  // [warp][16 MT rows] (m, l)
   static constexpr uint32_t kOffScale = kOffMl + kWarps * 16 * MT * 8;  // [warp][stage] (key, value) scale
   static constexpr uint32_t kOffBar = kOffScale + kWarps * kStages * 8;
@@ -388,7 +389,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     const int n = min(seg.units - seg.blk, n_cta - at);
     const int R = seg.s.q_len * G;
     const int min_sees = a.causal ? seg.s.len - seg.s.q_len + 1 : seg.s.len;  // of the first token
-    // queries: A fragments of the key products, rows g and g + 8 of each 16
+    // Queries: A fragments of the key products, rows g and g + 8 of each 16. All
+    // warps make them (each needs the rows' powers of two) and put a part of them
+    // into shared memory, where the joins' buffer lies idle: a lane's four
+    // registers of a product are one 16-byte load, and 32 registers stay free.
+    uint4* qs = reinterpret_cast<uint4*>(smem + L::kOffMerge) + lane;
     uint32_t qf[MT][kHalves][4][4];
     float f[MT][2];
     int sees[MT][2];  // keys that the row sees (a length fits 31 bits)
@@ -434,6 +439,15 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
                 pack_half2(__uint_as_float(w[i][x] << 16) * down, __uint_as_float(w[i][x] & 0xFFFF0000u) * down);
       }
     }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < kHalves; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x == warp)
+            qs[((mt * kHalves + i) * 4 + x) * 32] = make_uint4(qf[mt][i][x][0], qf[mt][i][x][1], qf[mt][i][x][2], qf[mt][i][x][3]);
+    __syncthreads();
     float2 o[MT][D / 8][2], l[MT][2];  // rows g and g + 8: channels 8x + 2t, + 1; sums of even and odd keys
     float m[MT][2];
 #pragma unroll
@@ -465,17 +479,21 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(cw[j]) = *reinterpret_cast<const uint4*>(kb + i * 2048 + j * 512 + lane * 16);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 4; ++x) {
+            uint32_t qa[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) *reinterpret_cast<uint4*>(qa[mt]) = qs[((mt * kHalves + i) * 4 + x) * 32];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t b0, b1;
               codes_to_half(cw[j][x], b0, b1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                if (i == 0 && x == 0) mma16816(z[mt][j], qf[mt][i][x], b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
-                else mma16816(z[mt][j], qf[mt][i][x], b0, b1);
+                if (i == 0 && x == 0) mma16816(z[mt][j], qa[mt], b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                else mma16816(z[mt][j], qa[mt], b0, b1);
               }
             }
+          }
         }
         const bool masked = key0 + kCacheBlock > min_sees;
         if (masked) {
