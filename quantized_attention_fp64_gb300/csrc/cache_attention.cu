@@ -364,14 +364,14 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     if ((issued & 31) == 0) fill_window(issued);
     if (lane == (issued & 31)) {
       const uint32_t bar = bars + 8 * into, dst = ring + into * 2 * L::kBlockBytes;
-      scales[into] = at_scales;
       if (at_codes >= 0) {
-        tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
+        // (the copies do not wait for the scales; the phase ends after the arrival)
         tc::bulk_load(dst, a.c.k + at_codes, L::kBlockBytes, bar);
         tc::bulk_load(dst + L::kBlockBytes, a.c.v + at_codes, L::kBlockBytes, bar);
-      } else {
-        tc::mbar_arrive(bar);
       }
+      scales[into] = at_scales;
+      if (at_codes >= 0) tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
+      else tc::mbar_arrive(bar);
     }
     ++issued;
     into = into + 1 == L::kStages ? 0 : into + 1;
@@ -865,7 +865,7 @@ cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
 cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_rows, int rows, int ctas,
                               size_t desc_bytes, cudaStream_t stream) {
   // few rows may have many parts, many rows have few
-  const int share = rows <= 32 ? 4 : 1;
+  const int share = rows <= 32 ? 8 : 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -875,8 +875,8 @@ cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_r
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = D == 128 ? (share == 4 ? cache_join_kernel<128, 4> : cache_join_kernel<128, 1>)
-                               : (share == 4 ? cache_join_kernel<64, 4> : cache_join_kernel<64, 1>);
+  const auto kernel = D == 128 ? (share > 1 ? cache_join_kernel<128, 8> : cache_join_kernel<128, 1>)
+                               : (share > 1 ? cache_join_kernel<64, 8> : cache_join_kernel<64, 1>);
   return cudaLaunchKernelEx(&cfg, kernel, a, slot_rows, desc_bytes);
 }
 
