@@ -165,8 +165,8 @@ struct Dec {
   static constexpr uint32_t kOffMl = kOffMerge + kWarps * 16 * 32 * 4;  // [warp][16 MT rows] (m, l)
   static constexpr uint32_t kOffScale = kOffMl + kWarps * 16 * MT * 8;  // [warp][stage] (key, value) scale
   static constexpr uint32_t kOffBar = kOffScale + kWarps * kStages * 8;
-  static constexpr uint32_t kOffPlan = kOffBar + kWarps * kStages * 8;  // kWarps sums, then (b, unit in b)
-  static constexpr uint32_t kBytes = kOffPlan + (kWarps + 2) * 4;
+  static constexpr uint32_t kOffPlan = kOffBar + kWarps * kStages * 8;  // kWarps sums, then where the range begins
+  static constexpr uint32_t kBytes = kOffPlan + (kWarps + 6) * 4;
   static_assert(kCtasPerSm * (kBytes + 1024) <= 233472u && kOffBar % 8 == 0, "shared memory of one SM");
   // workspace: a descriptor of each CTA's last item, then two slots per CTA
   static constexpr size_t kDesc = size_t(kMaxSms) * kCtasPerSm * sizeof(int4);
@@ -238,6 +238,25 @@ __device__ __forceinline__ void join_cluster(const CacheAttentionArgs& a, uint32
   }
 }
 
+// The queries of rows g and g + 8 of row tile mt of an item, this lane's channels; 0 past the last row.
+template <int D>
+__device__ __forceinline__ void load_queries(const CacheAttentionArgs& a, const Cursor& c, int mt, int g, int t,
+                                             uint4 (&raw)[2][D / 32]) {
+  const int G = a.H / a.c.H;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = mt * 16 + e * 8 + g;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) raw[e][x] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < c.s.q_len * G) {
+      const int tok = r / G;
+      const uint4* p = reinterpret_cast<const uint4*>(a.q.p + c.b * a.q.sb + tok * a.q.ss + (c.h * G + r - tok * G) * a.q.sh + 16 * t);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) raw[e][x] = p[(x >> 1) * 8 + (x & 1)];
+    }
+  }
+}
+
 // kCluster: small calls. A cluster of CTAs has one item each, cut into equal
 // parts; the parts are joined through distributed shared memory and nothing
 // goes through the workspace.
@@ -305,13 +324,21 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     before *= a.c.H;
     if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
       int b = b_lo;
+      Seq x;
+      int units;
       for (;; ++b) {
-        const int u = seq_units(load_seq(a, b, &bad)) * a.c.H;
-        if (lo < before + u) break;
-        before += u;
+        x = load_seq(a, b, &bad);
+        units = seq_units(x);
+        if (lo < before + units * a.c.H) break;
+        before += units * a.c.H;
       }
+      const int h = (lo - before) / units;
       plan[kWarps] = b;
-      plan[kWarps + 1] = lo - before;
+      plan[kWarps + 1] = h;
+      plan[kWarps + 2] = lo - before - h * units;
+      plan[kWarps + 3] = units;
+      plan[kWarps + 4] = x.len;
+      plan[kWarps + 5] = x.q_len;
     }
     __syncthreads();
     if (lo == hi) {
@@ -319,10 +346,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       return;
     }
     seg.b = plan[kWarps];
-    seg.s = load_seq(a, seg.b, &bad);
-    seg.units = seq_units(seg.s);
-    seg.h = plan[kWarps + 1] / seg.units;
-    seg.blk = plan[kWarps + 1] - seg.h * seg.units;
+    seg.h = plan[kWarps + 1];
+    seg.blk = plan[kWarps + 2];
+    seg.units = plan[kWarps + 3];
+    seg.s.len = plan[kWarps + 4];
+    seg.s.q_len = plan[kWarps + 5];
   }
   const int n_cta = hi - lo;
   const int n_mine = n_cta > warp ? (n_cta - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
@@ -376,8 +404,23 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     ++issued;
     into = into + 1 == L::kStages ? 0 : into + 1;
   };
-#pragma unroll 1
-  for (int s = 0; s < L::kStages; ++s) issue();
+  // the first copies: a lane each
+  if (n_mine > 0) {
+    fill_window(0);
+    issued = min(n_mine, L::kStages);
+    into = issued == L::kStages ? 0 : static_cast<uint32_t>(issued);
+    if (lane < issued) {
+      const uint32_t bar = bars + 8 * lane, dst = ring + lane * 2 * L::kBlockBytes;
+      if (at_codes >= 0) {
+        tc::bulk_load(dst, a.c.k + at_codes, L::kBlockBytes, bar);
+        tc::bulk_load(dst + L::kBlockBytes, a.c.v + at_codes, L::kBlockBytes, bar);
+      }
+      scales[lane] = at_scales;
+      if (at_codes >= 0) tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
+      else tc::mbar_arrive(bar);
+    }
+    __syncwarp();
+  }
 
   int taken = 0;  // blocks of this warp done
   uint32_t from = 0, parity = 0;  // stage and phase of the next one
@@ -394,36 +437,24 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     // into shared memory, where the joins' buffer lies idle: a lane's four
     // registers of a product are one 16-byte load, and 32 registers stay free.
     uint4* qs = reinterpret_cast<uint4*>(smem + L::kOffMerge) + lane;
-    uint32_t qf[MT][kHalves][4][4];
     float f[MT][2];
     int sees[MT][2];  // keys that the row sees (a length fits 31 bits)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      uint4 raw[2][D / 32];  // channels 64 i + 16 t and up
+      load_queries<D>(a, seg, mt, g, t, raw);
+      uint32_t qf[kHalves][4][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = mt * 16 + e * 8 + g;
-        uint32_t w[kHalves][8];
-        sees[mt][e] = 0;
-        if (r < R) {
-          const int tok = r / G;
-          sees[mt][e] = a.causal ? seg.s.len - seg.s.q_len + 1 + tok : seg.s.len;
-          const uint16_t* p = a.q.p + seg.b * a.q.sb + tok * a.q.ss + (seg.h * G + r - tok * G) * a.q.sh + 16 * t;
-#pragma unroll
-          for (int i = 0; i < kHalves; ++i) {
-            *reinterpret_cast<uint4*>(w[i]) = *reinterpret_cast<const uint4*>(p + 64 * i);
-            *reinterpret_cast<uint4*>(w[i] + 4) = *reinterpret_cast<const uint4*>(p + 64 * i + 8);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kHalves; ++i)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[i][x] = 0u;
-        }
+        sees[mt][e] = r >= R ? 0 : (a.causal ? seg.s.len - seg.s.q_len + 1 + r / G : seg.s.len);
         uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i)
+        for (int x = 0; x < D / 32; ++x) {
+          const uint32_t w[4] = {raw[e][x].x, raw[e][x].y, raw[e][x].z, raw[e][x].w};
 #pragma unroll
-          for (int x = 0; x < 8; ++x) amax = max(amax, max(w[i][x] & 0x7FFFu, (w[i][x] >> 16) & 0x7FFFu));
+          for (int y = 0; y < 4; ++y) amax = max(amax, max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+        }
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // the power of two below the largest value; infinities and NaN stay what they are
@@ -432,21 +463,21 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         const float down = __uint_as_float((254u - ex) << 23);
         f[mt][e] = __uint_as_float(ex << 23) * a.sm_log2;
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i)
+        for (int x = 0; x < D / 32; ++x) {
+          const uint32_t w[4] = {raw[e][x].x, raw[e][x].y, raw[e][x].z, raw[e][x].w};
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            qf[mt][i][x >> 1][(x & 1) * 2 + e] =
-                pack_half2(__uint_as_float(w[i][x] << 16) * down, __uint_as_float(w[i][x] & 0xFFFF0000u) * down);
+          for (int y = 0; y < 4; ++y)
+            qf[x >> 1][(x & 1) * 2 + (y >> 1)][(y & 1) * 2 + e] =
+                pack_half2(__uint_as_float(w[y] << 16) * down, __uint_as_float(w[y] & 0xFFFF0000u) * down);
+        }
       }
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < kHalves; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           if (x == warp)
-            qs[((mt * kHalves + i) * 4 + x) * 32] = make_uint4(qf[mt][i][x][0], qf[mt][i][x][1], qf[mt][i][x][2], qf[mt][i][x][3]);
+            qs[((mt * kHalves + i) * 4 + x) * 32] = make_uint4(qf[i][x][0], qf[i][x][1], qf[i][x][2], qf[i][x][3]);
+    }
     __syncthreads();
     float2 o[MT][D / 8][2], l[MT][2];  // rows g and g + 8: channels 8x + 2t, + 1; sums of even and odd keys
     float m[MT][2];
@@ -602,6 +633,15 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       issue();
     }
 
+    // the next item's queries are on their way to L1 during the join (its head
+    // is the next one of the sequence, unless that was the last)
+    if (!kCluster && at + n < n_cta && seg.h + 1 < a.c.H && threadIdx.x < R * (D / 64)) {
+      const int r = threadIdx.x / (D / 64), tok = r / G;
+      const uint16_t* p = a.q.p + seg.b * a.q.sb + tok * a.q.ss + ((seg.h + 1) * G + r - tok * G) * a.q.sh +
+                          64 * (threadIdx.x % (D / 64));
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+    }
+
     // join the warps' parts of the item
     float2* ml = reinterpret_cast<float2*>(smem + L::kOffMl);
 #pragma unroll
@@ -640,7 +680,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (mt * 16 >= R) break;
-      const int row = threadIdx.x >> 3, c4 = threadIdx.x & 7;
+      // 16 rows x 32 channels of each warp at a time, or where there are no more
+      // than 8 rows 8 x 64: pairs of channels, pair u of row r at u ^ 4 (r mod 4),
+      // which is free of bank conflicts
+      const bool few = R - mt * 16 <= 8;
+      const int row = few ? threadIdx.x >> 4 : threadIdx.x >> 3, c4 = few ? threadIdx.x & 15 : threadIdx.x & 7;
       const int r = mt * 16 + row;
       float top = -INFINITY, sum = 0.0f, wt[kWarps];
 #pragma unroll
@@ -660,37 +704,50 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
           a.lse[(static_cast<int64_t>(seg.b) * a.H + head) * a.T + tok] =
               sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
       }
+      float2* buf = reinterpret_cast<float2*>(smem + L::kOffMerge);
+      // sums the warps' channels 4 c4 .. + 3 of the row, `pitch` pairs a row and `rows` rows a warp, and puts them out
+      const auto gather = [&](int first, int rows, int pitch) {
+        if (r >= R) return;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int cut = 0; cut < D / 32; ++cut) {
-        // 32 channels of a row as 16 pairs, pair u of row r at u ^ 4 (r mod 4): no bank conflicts
-        float2* buf = reinterpret_cast<float2*>(smem + L::kOffMerge);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int u = (4 * x + t) ^ ((g & 3) * 4);
-          buf[(warp * 16 + g) * 16 + u] = o[mt][cut * 4 + x][0];
-          buf[(warp * 16 + g + 8) * 16 + u] = o[mt][cut * 4 + x][1];
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(buf + (w * rows + row) * pitch + ((2 * c4) ^ ((row & 3) * 4)));
+          acc.x = fmaf(y.x, wt[w], acc.x);
+          acc.y = fmaf(y.y, wt[w], acc.y);
+          acc.z = fmaf(y.z, wt[w], acc.z);
+          acc.w = fmaf(y.w, wt[w], acc.w);
         }
-        __syncthreads();
-        if (r < R) {
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(buf + (w * 16 + row) * 16 + ((2 * c4) ^ ((row & 3) * 4)));
-            acc.x = fmaf(y.x, wt[w], acc.x);
-            acc.y = fmaf(y.y, wt[w], acc.y);
-            acc.z = fmaf(y.z, wt[w], acc.z);
-            acc.w = fmaf(y.w, wt[w], acc.w);
-          }
-          if (whole) {
-            const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(dst + cut * 32) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
-          } else {
-            *reinterpret_cast<float4*>(part + r * D + cut * 32 + 4 * c4) = acc;
-          }
+        if (whole) {
+          const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+          const __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(dst + first) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+        } else {
+          *reinterpret_cast<float4*>(part + r * D + first + 4 * c4) = acc;
         }
-        __syncthreads();
+      };
+      if (few) {
+#pragma unroll
+        for (int cut = 0; cut < D / 64; ++cut) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) buf[(warp * 8 + g) * 32 + ((4 * x + t) ^ ((g & 3) * 4))] = o[mt][cut * 8 + x][0];
+          __syncthreads();
+          gather(cut * 64, 8, 32);
+          __syncthreads();
+        }
+      } else {
+#pragma unroll
+        for (int cut = 0; cut < D / 32; ++cut) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int u = (4 * x + t) ^ ((g & 3) * 4);
+            buf[(warp * 16 + g) * 16 + u] = o[mt][cut * 4 + x][0];
+            buf[(warp * 16 + g + 8) * 16 + u] = o[mt][cut * 4 + x][1];
+          }
+          __syncthreads();
+          gather(cut * 32, 16, 16);
+          __syncthreads();
+        }
       }
     }
     if (R == 0) __syncthreads();
