@@ -33,37 +33,94 @@ __device__ __forceinline__ int quantize_one(float x, float s) {
   return static_cast<int>(fminf(fmaxf(c, -127.0f), 127.0f));
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (a & 255) | ((b & 255) << 8) | ((c & 255) << 16) | (static_cast<uint32_t>(d) << 24);
+// Packed pairs of fp32.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float pair_lo(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float pair_hi(uint64_t p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Eight codes, rint(x / s) with the division correctly rounded, from eight
+// BF16 values. Instead of dividing eight times: with inv = 1 / s rounded once,
+// y = x * inv is within two steps of x / s, y + (x - y s) inv within one, and
+// the same correction of that is x / s correctly rounded (Markstein's theorem:
+// the residual of a quotient within one step is exact under a fused
+// multiply-add, and inv is correctly rounded). The theorem wants no residual
+// below the range: [kScaleLow, kScaleHigh] keeps it there; other scales divide.
+// Adding 1.5 * 2^23 leaves the rounded integer in the low byte.
+constexpr float kScaleLow = 0x1p-90f, kScaleHigh = 0x1p+100f;
+
+__device__ __forceinline__ uint2 quantize8(const uint4& x, float s, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m[8];
+  if (s >= kScaleLow && s <= kScaleHigh) {
+    const uint64_t magic = pair(12582912.0f, 12582912.0f), inv2 = pair(inv, inv), minus_s = pair(-s, -s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t v = pair(bf16_lo(w[e]), bf16_hi(w[e]));
+      uint64_t y = mul2(v, inv2);
+      y = fma2(fma2(y, minus_s, v), inv2, y);
+      y = fma2(fma2(y, minus_s, v), inv2, y);
+      y = add2(y, magic);
+      m[2 * e] = static_cast<uint32_t>(y);
+      m[2 * e + 1] = static_cast<uint32_t>(y >> 32);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[2 * e] = static_cast<uint32_t>(quantize_one(bf16_lo(w[e]), s));
+      m[2 * e + 1] = static_cast<uint32_t>(quantize_one(bf16_hi(w[e]), s));
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410));
 }
 
 // The block that blockIdx.x stands for in sequence blockIdx.z, and the tokens
 // of the call that fall into it.
 struct Span {
   int64_t slot;   // block number in the cache, -1: nothing to do
-  int64_t t0;     // the call's token in the block's slot 0 (negative: older tokens come first)
+  int t0;         // the call's token in the block's slot 0 (negative: older tokens come first)
   int first, end; // slots [first, end) hold the call's tokens
 };
 
-__device__ Span find_span(const CacheView& c, const PageTable& pt, const int32_t* starts, const int32_t* counts,
-                          int64_t T, int* dev_err) {
-  const int64_t b = blockIdx.z;
-  const int32_t h = static_cast<int32_t>(blockIdx.y);
+__device__ __forceinline__ Span find_span(const CacheView& c, const PageTable& pt, const int32_t* starts,
+                                          const int32_t* counts, int32_t T, int* dev_err) {
+  const int b = static_cast<int>(blockIdx.z);
   Span s;
   s.slot = -1;
   bool bad = false;
-  const int64_t capacity = table_capacity(pt.max_pages, c.blocks_per_page);
-  const int64_t start = checked_length(starts[b], capacity, &bad);
-  int64_t n = counts != nullptr ? checked_length(counts[b], T, &bad) : T;
-  n = checked_length(n, capacity - start, &bad);
-  const int64_t blk = start / kCacheBlock + blockIdx.x;
-  s.t0 = blk * kCacheBlock - start;
-  s.first = s.t0 < 0 ? static_cast<int>(-s.t0) : 0;
-  s.end = static_cast<int>(min(n - s.t0, static_cast<int64_t>(kCacheBlock)));
+  // lengths are 32-bit, and so is every number of tokens and blocks below
+  const int32_t capacity = static_cast<int32_t>(table_capacity(pt.max_pages, c.blocks_per_page));
+  const int32_t start = static_cast<int32_t>(checked_length(starts[b], capacity, &bad));
+  int32_t n = counts != nullptr ? static_cast<int32_t>(checked_length(counts[b], T, &bad)) : T;
+  n = static_cast<int32_t>(checked_length(n, capacity - start, &bad));
+  const uint32_t blk = static_cast<uint32_t>(start) / kCacheBlock + blockIdx.x;
+  s.t0 = static_cast<int>(blk * kCacheBlock - static_cast<uint32_t>(start));
+  s.first = s.t0 < 0 ? -s.t0 : 0;
+  s.end = min(n - s.t0, kCacheBlock);
   if (s.end > s.first) {
-    const int64_t page = pt.table[b * pt.stride + blk / c.blocks_per_page];
+    const uint32_t in_seq = blk / static_cast<uint32_t>(c.blocks_per_page);
+    const int64_t page = pt.table[b * pt.stride + in_seq];
     if (page_ok(page, c.num_pages))
-      s.slot = block_slot(page, h, c.H, c.blocks_per_page, static_cast<int32_t>(blk % c.blocks_per_page));
+      s.slot = block_slot(page, static_cast<int32_t>(blockIdx.y), c.H, c.blocks_per_page,
+                          static_cast<int32_t>(blk - in_seq * static_cast<uint32_t>(c.blocks_per_page)));
     else
       bad = true;
   }
@@ -104,10 +161,15 @@ __device__ __forceinline__ uint32_t shrink4(uint32_t w, float r) {
 
 // ------------------------------------------------------------------ append --
 // One CTA writes one block of one head: threads 0..127 its keys, 128..255 its
-// values.
+// values. A call of many tokens is bound by instructions more than by HBM: 70
+// us for 16 sequences of up to 4096 tokens, 8 heads of 128, where the bytes
+// alone take 45; with eight plain divisions a thread it was 118, and the
+// numbers of tokens and blocks in 64 bits cost another 14. Five CTAs to an SM
+// (48 registers): with six the same call is 1 us quicker, but 64 single tokens
+// take 0.7 us longer; with eight the registers spill (+3 us).
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
-                                                                const int32_t* counts, Bf16In k, Bf16In v, int64_t T,
+__global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
+                                                                const int32_t* counts, Bf16In k, Bf16In v, int32_t T,
                                                                 int* dev_err) {
   using L = Tile<D>;
   __shared__ __align__(16) uint8_t vt[kCacheBlock * L::kPitch];
@@ -121,13 +183,15 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, Pag
   const Bf16In& in = half ? v : k;
   float* scale_at = (half ? c.vs : c.ks) + s.slot;
   const float s_old = s.first > 0 ? *scale_at : 0.0f;
-  const uint16_t* src = in.p + static_cast<int64_t>(blockIdx.z) * in.sb + static_cast<int64_t>(blockIdx.y) * in.sh + ch;
+  const uint16_t* src = in.p + static_cast<int64_t>(blockIdx.z) * in.sb + static_cast<int64_t>(blockIdx.y) * in.sh + ch +
+                        (s.t0 + row0) * in.ss;
+  const int64_t step = L::kRows * in.ss;
   uint4 x[L::kTimes];
 #pragma unroll
   for (int q = 0; q < L::kTimes; ++q) {
     const int row = q * L::kRows + row0;
     x[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= s.first && row < s.end) x[q] = *reinterpret_cast<const uint4*>(src + (s.t0 + row) * in.ss);
+    if (row >= s.first && row < s.end) x[q] = *reinterpret_cast<const uint4*>(src + q * step);
   }
   // max |x| as bit patterns: those of infinities and NaN are the largest
   uint32_t a = 0;
@@ -135,10 +199,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, Pag
   for (int q = 0; q < L::kTimes; ++q) {
     const uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a = max(a, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+    for (int e = 0; e < 4; ++e) a = __vmaxu2(a, w[e] & 0x7FFF7FFFu);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  a = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
   if ((threadIdx.x & 31) == 0) amax_w[threadIdx.x >> 5] = a;
   __syncthreads();  // also: every thread has read s_old
   a = max(max(amax_w[half * 4], amax_w[half * 4 + 1]), max(amax_w[half * 4 + 2], amax_w[half * 4 + 3]));
@@ -149,17 +212,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, Pag
   const bool grew = s.first > 0 && !(s_new == s_old);
   const float shrink = (grew && usable) ? __fdiv_rn(s_old, s_new) : 0.0f;
   if (i == 0) *scale_at = s_new;
+  const float inv = __fdiv_rn(1.0f, s_new);
   int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
 #pragma unroll
   for (int q = 0; q < L::kTimes; ++q) {
     const int row = q * L::kRows + row0;
     uint2 codes = make_uint2(0u, 0u);
-    if (usable && row >= s.first && row < s.end) {
-      codes.x = pack4(quantize_one(bf16_lo(x[q].x), s_new), quantize_one(bf16_hi(x[q].x), s_new),
-                      quantize_one(bf16_lo(x[q].y), s_new), quantize_one(bf16_hi(x[q].y), s_new));
-      codes.y = pack4(quantize_one(bf16_lo(x[q].z), s_new), quantize_one(bf16_hi(x[q].z), s_new),
-                      quantize_one(bf16_lo(x[q].w), s_new), quantize_one(bf16_hi(x[q].w), s_new));
-    }
+    if (usable && row >= s.first && row < s.end) codes = quantize8(x[q], s_new, inv);
     if (half == 0) {
       uint2* p = reinterpret_cast<uint2*>(block + (ch / 64) * (kCacheBlock * 64) + row * 64 + ch % 64);
       if (row >= s.first) {
@@ -206,15 +265,24 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheView c, Pag
 
 // -------------------------------------------------------------------- read --
 
-__device__ __forceinline__ uint32_t to_bf16x2(uint32_t codes, int at, float scale) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(static_cast<int8_t>(codes >> (8 * at)) * scale,
-                                                 static_cast<int8_t>(codes >> (8 * at + 8)) * scale);
+// Two codes times the scale, rounded to BF16 once. u: the codes plus 128, as
+// unsigned bytes; a byte under the exponent of 2^23 is the fp32 2^23 + u, whose
+// difference with 2^23 + 128 is the code, exactly: two byte permutes and half
+// an instruction in place of a conversion at a quarter of the rate.
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t u, int at, uint64_t scale2) {
+  const uint64_t bias = pair(-8388736.0f, -8388736.0f);
+  const uint32_t lo = __byte_perm(u, 0x4B000000u, 0x7440 + at), hi = __byte_perm(u, 0x4B000000u, 0x7441 + at);
+  const uint64_t x = mul2(add2(static_cast<uint64_t>(hi) << 32 | lo, bias), scale2);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(pair_lo(x), pair_hi(x));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The same blocks the other way. 8 sequences of 8000 tokens, 8 heads of 128:
+// 61 us, 6.4 TB/s; with six CTAs to an SM in place of eight 65 us, and 68 with
+// conversions of integers and numbers of tokens in 64 bits.
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageTable pt, const int32_t* starts,
-                                                              const int32_t* counts, Out k, Out v, int64_t T,
+__global__ void __launch_bounds__(kThreads, 8) cache_read_kernel(CacheView c, PageTable pt, const int32_t* starts,
+                                                              const int32_t* counts, Out k, Out v, int32_t T,
                                                               bool zero_rest, int* dev_err) {
   using L = Tile<D>;
   __shared__ __align__(16) uint8_t vt[kCacheBlock * L::kPitch];
@@ -224,17 +292,20 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageT
   const int half = threadIdx.x >> 7, i = threadIdx.x & 127;
   const int ch = (i % L::kLanes) * 8, row0 = i / L::kLanes;
   const Out& o = half ? v : k;
-  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + static_cast<int64_t>(blockIdx.y) * o.sh + ch;
+  uint16_t* dst = o.p + static_cast<int64_t>(blockIdx.z) * o.sb + static_cast<int64_t>(blockIdx.y) * o.sh + ch +
+                  (s.t0 + row0) * o.ss;
+  const int64_t step = L::kRows * o.ss;
   if (zero_rest) {
 #pragma unroll
     for (int q = 0; q < L::kTimes; ++q) {
       const int row = q * L::kRows + row0;
       if (row >= s.first && s.t0 + row < T && (row >= s.end || s.slot < 0))
-        *reinterpret_cast<uint4*>(dst + (s.t0 + row) * o.ss) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + q * step) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (s.slot < 0) return;
   const float scale = (half ? c.vs : c.ks)[s.slot];
+  const uint64_t scale2 = pair(scale, scale);
   const int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
   uint2 codes[L::kTimes];
   if (half == 0) {
@@ -265,9 +336,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageT
   for (int q = 0; q < L::kTimes; ++q) {
     const int row = q * L::kRows + row0;
     if (row < s.first || row >= s.end) continue;
-    const uint2 w = half ? *reinterpret_cast<const uint2*>(vt + row * L::kPitch + ch) : codes[q];
-    *reinterpret_cast<uint4*>(dst + (s.t0 + row) * o.ss) =
-        make_uint4(to_bf16x2(w.x, 0, scale), to_bf16x2(w.x, 2, scale), to_bf16x2(w.y, 0, scale), to_bf16x2(w.y, 2, scale));
+    uint2 w = half ? *reinterpret_cast<const uint2*>(vt + row * L::kPitch + ch) : codes[q];
+    w.x ^= 0x80808080u;
+    w.y ^= 0x80808080u;
+    *reinterpret_cast<uint4*>(dst + q * step) =
+        make_uint4(to_bf16x2(w.x, 0, scale2), to_bf16x2(w.x, 2, scale2), to_bf16x2(w.y, 0, scale2),
+                   to_bf16x2(w.y, 2, scale2));
   }
 }
 
@@ -277,63 +351,115 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheView c, PageT
 // dst of one entry and src of another: the copies would depend on their order.
 // Every CTA checks the whole lists with one bit per page in shared memory
 // before it copies anything, so a list that breaks the rule, or names a page
-// that is not there, moves no byte and sets the device error word.
+// that is not there, moves no byte and sets the device error word. The first
+// bytes are on their way meanwhile. 2000 pages of 64 tokens, 8 heads of 128:
+// 102 us, 5.1 TB/s read and written; 16 such pages of 4 heads: 2.6 us. Chunks of
+// 32768 bytes take as long for many pages and 0.5 us more for few.
 constexpr int kCopyThreads = 256;
-constexpr int64_t kCopyChunk = 32768;  // bytes of codes that one CTA moves at a time
+constexpr int kCopyCtas = 4;           // per SM at a time
+constexpr int kCopyWaves = 4;          // grids of 4 to 24 CTAs per SM measure within 3%
+constexpr int kCopyChunk = 16384;      // bytes of codes that one CTA moves at a time
+constexpr int kCopyPieces = kCopyChunk / 16 / kCopyThreads;
+constexpr int kCheckAtOnce = 4;        // entries whose loads a thread has in flight
 
-__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, const int32_t* src, const int32_t* dst,
-                                                                  int64_t n, int64_t codes_bytes, int64_t scales,
-                                                                  int64_t chunks, int* dev_err) {
+struct CopyUnit {
+  const uint4* from;  // null: nothing to move
+  uint4* to;
+  int pieces;         // 16-byte pieces
+  int32_t s, d;       // pages
+  int which;          // 0 keys, 1 values
+  bool first;         // the page's first chunk: its scales go with it
+};
+
+__device__ __forceinline__ CopyUnit copy_unit(const CacheView& c, const int32_t* src, const int32_t* dst,
+                                              int64_t codes_bytes, int64_t chunks, int64_t u) {
+  const int64_t entry = u / (2 * chunks);
+  const int r = static_cast<int>(u - entry * 2 * chunks);
+  CopyUnit m;
+  m.s = src[entry];
+  m.d = dst[entry];
+  m.which = r >= chunks;
+  const int64_t lo = (r - (m.which ? chunks : 0)) * kCopyChunk;
+  m.first = lo == 0;
+  m.pieces = static_cast<int>(min(codes_bytes - lo, static_cast<int64_t>(kCopyChunk)) / 16);
+  int8_t* base = m.which ? c.v : c.k;
+  const bool moves = m.d >= 0 && m.d != m.s && page_ok(m.s, c.num_pages);
+  m.from = moves ? reinterpret_cast<const uint4*>(base + m.s * codes_bytes + lo) : nullptr;
+  m.to = reinterpret_cast<uint4*>(base + m.d * codes_bytes + lo);
+  return m;
+}
+
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) cache_copy_kernel(CacheView c, const int32_t* src,
+                                                                             const int32_t* dst, int64_t n,
+                                                                             int64_t codes_bytes, int64_t scales,
+                                                                             int64_t chunks, int* dev_err) {
   extern __shared__ uint32_t taken[];
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int64_t words = (c.num_pages + 31) / 32;
-  for (int64_t i = threadIdx.x; i < words; i += kCopyThreads) taken[i] = 0u;
+  const int64_t total = n * 2 * chunks;
+  uint4 x[kCopyPieces];
+  const auto fetch = [&](const CopyUnit& m) {
+#pragma unroll
+    for (int y = 0; y < kCopyPieces; ++y) {
+      const int q = threadIdx.x + y * kCopyThreads;
+      if (m.from != nullptr && q < m.pieces) x[y] = m.from[q];
+    }
+  };
+  // the first unit's bytes are on their way while the lists are checked
+  CopyUnit m = copy_unit(c, src, dst, codes_bytes, chunks, blockIdx.x);
+  fetch(m);
+  const int words = static_cast<int>((c.num_pages + 31) / 32);
+  for (int i = threadIdx.x; i < words; i += kCopyThreads) taken[i] = 0u;
   __syncthreads();
   bool bad = false;
-  for (int64_t i = threadIdx.x; i < n; i += kCopyThreads) {
-    const int32_t d = dst[i], s = src[i];
-    if (d < 0 || d == s) continue;
-    if (!page_ok(d, c.num_pages) || !page_ok(s, c.num_pages)) bad = true;
-    else if (atomicOr(&taken[d >> 5], 1u << (d & 31)) >> (d & 31) & 1u) bad = true;
+  for (int64_t i0 = threadIdx.x; i0 < n; i0 += kCheckAtOnce * kCopyThreads) {
+    int32_t d[kCheckAtOnce], s[kCheckAtOnce];
+#pragma unroll
+    for (int y = 0; y < kCheckAtOnce; ++y) {
+      const int64_t i = i0 + y * kCopyThreads;
+      d[y] = i < n ? dst[i] : -1;
+      s[y] = i < n ? src[i] : -1;
+    }
+#pragma unroll
+    for (int y = 0; y < kCheckAtOnce; ++y) {
+      if (d[y] < 0 || d[y] == s[y]) continue;
+      if (!page_ok(d[y], c.num_pages) || !page_ok(s[y], c.num_pages)) bad = true;
+      else if (atomicOr(&taken[d[y] >> 5], 1u << (d[y] & 31)) >> (d[y] & 31) & 1u) bad = true;
+    }
   }
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < n; i += kCopyThreads) {
-    const int32_t d = dst[i], s = src[i];
-    if (d >= 0 && d != s && page_ok(s, c.num_pages) && (taken[s >> 5] >> (s & 31) & 1u)) bad = true;
+  for (int64_t i0 = threadIdx.x; i0 < n; i0 += kCheckAtOnce * kCopyThreads) {
+    int32_t d[kCheckAtOnce], s[kCheckAtOnce];
+#pragma unroll
+    for (int y = 0; y < kCheckAtOnce; ++y) {
+      const int64_t i = i0 + y * kCopyThreads;
+      d[y] = i < n ? dst[i] : -1;
+      s[y] = i < n ? src[i] : -1;
+    }
+#pragma unroll
+    for (int y = 0; y < kCheckAtOnce; ++y)
+      if (d[y] >= 0 && d[y] != s[y] && page_ok(s[y], c.num_pages) && (taken[s[y] >> 5] >> (s[y] & 31) & 1u)) bad = true;
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) flag_pages(dev_err);
     return;
   }
-  // work: n entries x (keys, values) x chunks of a page's codes
-  const int64_t total = n * 2 * chunks;
-  for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-    const int64_t entry = u / (2 * chunks), r = u % (2 * chunks);
-    const int which = static_cast<int>(r / chunks);
-    const int64_t chunk = r % chunks;
-    const int32_t d = dst[entry], s = src[entry];
-    if (d < 0 || d == s) continue;
-    int8_t* base = which ? c.v : c.k;
-    const int64_t lo = chunk * kCopyChunk, hi = min(lo + kCopyChunk, codes_bytes);
-    const uint4* from = reinterpret_cast<const uint4*>(base + s * codes_bytes);
-    uint4* to = reinterpret_cast<uint4*>(base + d * codes_bytes);
-    // a whole chunk is eight 16-byte pieces per thread, all in flight at once
-    uint4 x[kCopyChunk / 16 / kCopyThreads];
+  for (int64_t u = blockIdx.x;;) {
+    if (m.from != nullptr) {
 #pragma unroll
-    for (int y = 0; y < kCopyChunk / 16 / kCopyThreads; ++y) {
-      const int64_t q = lo / 16 + threadIdx.x + y * kCopyThreads;
-      if (q < hi / 16) x[y] = from[q];
+      for (int y = 0; y < kCopyPieces; ++y) {
+        const int q = threadIdx.x + y * kCopyThreads;
+        if (q < m.pieces) m.to[q] = x[y];
+      }
+      if (m.first) {
+        float* sc = m.which ? c.vs : c.ks;
+        for (int64_t q = threadIdx.x; q < scales; q += kCopyThreads) sc[m.d * scales + q] = sc[m.s * scales + q];
+      }
     }
-#pragma unroll
-    for (int y = 0; y < kCopyChunk / 16 / kCopyThreads; ++y) {
-      const int64_t q = lo / 16 + threadIdx.x + y * kCopyThreads;
-      if (q < hi / 16) to[q] = x[y];
-    }
-    if (chunk == 0) {
-      float* sc = which ? c.vs : c.ks;
-      for (int64_t q = threadIdx.x; q < scales; q += kCopyThreads) sc[d * scales + q] = sc[s * scales + q];
-    }
+    u += gridDim.x;
+    if (u >= total) break;
+    m = copy_unit(c, src, dst, codes_bytes, chunks, u);
+    fetch(m);
   }
 }
 
@@ -366,14 +492,14 @@ cudaError_t launch_cache_append(const CacheView& c, int64_t D, const PageTable& 
                                 const int32_t* counts, const Bf16In& k, const Bf16In& v, int64_t B, int64_t T,
                                 int* dev_err, cudaStream_t stream) {
   return launch(D == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, span_grid(c, B, T), kThreads, 0, stream, c,
-                pt, starts, counts, k, v, T, dev_err);
+                pt, starts, counts, k, v, static_cast<int32_t>(T), dev_err);
 }
 
 cudaError_t launch_cache_read(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
                               const int32_t* counts, const Out& k, const Out& v, int64_t B, int64_t T,
                               bool zero_rest, int* dev_err, cudaStream_t stream) {
   return launch(D == 128 ? cache_read_kernel<128> : cache_read_kernel<64>, span_grid(c, B, T), kThreads, 0, stream, c, pt,
-                starts, counts, k, v, T, zero_rest, dev_err);
+                starts, counts, k, v, static_cast<int32_t>(T), zero_rest, dev_err);
 }
 
 cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t* src, const int32_t* dst, int64_t n,
@@ -384,7 +510,7 @@ cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t
   const int smem = static_cast<int>((c.num_pages + 31) / 32 * 4);
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(cache_copy_kernel), smem);
   if (e != cudaSuccess) return e;
-  const int64_t work = n * 2 * chunks, most = int64_t(8) * sm_count_current();
+  const int64_t work = n * 2 * chunks, most = int64_t(kCopyWaves) * kCopyCtas * sm_count_current();
   return launch(cache_copy_kernel, dim3(static_cast<unsigned>(work < most ? work : most)), kCopyThreads,
                 static_cast<size_t>(smem), stream, c, src, dst, n, bytes, scales, chunks, dev_err);
 }
