@@ -190,8 +190,9 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
     return rc;
   if (a.c.num_pages == 0) a.pt.max_pages = 0;  // without pages there are no tokens, whatever the table says
   // the call's blocks, all sequences and heads, are counted in 32 bits
-  // (once for every 256 query rows that share a key/value head)
-  const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 1;
+  // (once for every 256 query rows that share a key/value head, with 16 more
+  // for what beginning a unit counts)
+  const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 16;
   constexpr int64_t kMost = (int64_t(1) << 31) - 1;
   if (H > 0 && T > kMaxTokens / (H / a.c.H)) return SAGE_ERR_TOO_LARGE;  // rows of a key/value head, too
   const int64_t pairs = H > 0 ? div_up(T * (H / a.c.H), 256) : 0;

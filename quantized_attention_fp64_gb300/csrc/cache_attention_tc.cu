@@ -229,6 +229,13 @@ __device__ __forceinline__ void store16(uint32_t addr, const uint32_t* o) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                : "memory");
 }
+// A whole sector of global memory (32-byte aligned). A thread writes its own
+// row, so two halves would be two writes to L2: 110 -> 106 us there.
+__device__ __forceinline__ void store32(void* to, const uint32_t* o) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
+               "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // A pair of query tiles of one key/value head.
@@ -267,40 +274,52 @@ __device__ __forceinline__ Unit find_entry(const CacheAttentionArgs& a, int pair
 
 __device__ __forceinline__ int unit_size(const Unit& u) { return max(u.n_max, 1); }
 
-// A CTA's place in the list, at key tile t of head h of entry e, with `todo`
-// tiles left in its range. The part of the range that lies in this unit is
-// [t, t + n) of its key tiles; a unit that sees no key or has no rows counts as
-// one (its rows still have outputs). The unit is found anew where it is needed:
-// that costs less than the registers to keep it.
+// The list counts a unit's key tiles and, before them, kBegin more: what
+// beginning a unit and bringing its rows out costs (2 x 4097 rows of 16 heads
+// of 64 over up to 1500 keys: 106 us without, 96 with; between 3 and 11 both
+// head dimensions measure within 2%).
+template <int D>
+constexpr int kBegin = D == 128 ? 8 : 6;
+
+// A CTA's place in the list, `at` entries of the list into head h of entry e,
+// with `todo` left in its range. The part of the range that lies in this unit
+// is its next n, key tiles [t, t + tiles); a unit that sees no key or has no
+// rows counts as one tile (its rows still have outputs). A part without tiles
+// (the range ends where the unit begins) stands for nothing. The unit is found
+// anew where it is needed: that costs less than the registers to keep it.
 struct Place {
-  int e, h, t, todo;
+  int e, h, at, todo;
 };
 struct Part {
   Unit u;
-  int n, size;
+  int n;                // of the list
+  int t, tiles, size;   // key tiles: first of the part, of the part, of the unit
 };
+template <int D>
 __device__ __forceinline__ Part part_at(const CacheAttentionArgs& a, int pairs, const Place& p) {
   bool bad = false;
   Part x;
   x.u = find_entry(a, pairs, p.e, &bad);
   x.u.h = p.h;
   x.size = unit_size(x.u);
-  x.n = min(x.size - p.t, p.todo);
+  x.n = min(x.size + kBegin<D> - p.at, p.todo);
+  x.t = max(p.at - kBegin<D>, 0);
+  x.tiles = max(p.at + x.n - kBegin<D>, 0) - x.t;
   return x;
 }
 __device__ __forceinline__ Place first_place(const int* found) { return Place{found[0], found[1], found[2], found[3]}; }
 // Past a part of n tiles.
 __device__ __forceinline__ void place_next(const CacheAttentionArgs& a, Place& p, int n) {
   p.todo -= n;
-  p.t = 0;
+  p.at = 0;
   if (++p.h == a.c.H) {
     p.h = 0;
     ++p.e;
   }
 }
 // Key tiles of query tile i in the part.
-__device__ __forceinline__ int part_tiles(const Place& p, const Part& x, int i) {
-  return max(min(p.t + x.n, i == 0 ? x.u.n[0] : x.u.n[1]) - p.t, 0);
+__device__ __forceinline__ int part_tiles(const Part& x, int i) {
+  return max(min(x.t + x.tiles, i == 0 ? x.u.n[0] : x.u.n[1]) - x.t, 0);
 }
 
 template <int D>
@@ -435,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   const int entries = static_cast<int>(a.B) * pairs, run = (entries + kThreads - 1) / kThreads;
   const int e_lo = min(run * static_cast<int>(threadIdx.x), entries), e_hi = min(e_lo + run, entries);
   int mine = 0;
-  for (int e = e_lo; e < e_hi; ++e) mine += unit_size(find_entry(a, pairs, e, &bad));
+  for (int e = e_lo; e < e_hi; ++e) mine += unit_size(find_entry(a, pairs, e, &bad)) + kBegin<D>;
   if (bad && blockIdx.x == 0) atomicExch(a.dev_err, kDevErrPage);
   int incl = mine;
 #pragma unroll
@@ -458,17 +477,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   before *= a.c.H;
   const int units = entries * a.c.H;
   // no more CTAs than units, unless each still gets kMinTiles key tiles
-  const int ctas = min(static_cast<int>(gridDim.x), max(units, W / kMinTiles));
+  const int ctas = min(static_cast<int>(gridDim.x), max(units, (W - units * kBegin<D>) / kMinTiles));
   const int each = W / ctas, extra = W - each * ctas, c = static_cast<int>(blockIdx.x);
   const int lo = c < ctas ? c * each + min(c, extra) : 0, hi = c < ctas ? lo + each + (c < extra ? 1 : 0) : 0;
   if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
     int e = e_lo;
     for (;; ++e) {
-      const int x = unit_size(find_entry(a, pairs, e, &bad)) * a.c.H;
+      const int x = (unit_size(find_entry(a, pairs, e, &bad)) + kBegin<D>) * a.c.H;
       if (lo < before + x) break;
       before += x;
     }
-    const int size = unit_size(find_entry(a, pairs, e, &bad)), h = (lo - before) / size;
+    const int size = unit_size(find_entry(a, pairs, e, &bad)) + kBegin<D>, h = (lo - before) / size;
     found[0] = e;
     found[1] = h;
     found[2] = lo - before - h * size;
@@ -497,9 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       bool ok = true;
       Place p = first_place(found);
       while (ok && p.todo > 0) {
-        const Part x = part_at(a, pairs, p);
-        const int n = part_tiles(p, x, i);                                // of this query tile
-        const int n_all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));  // of the converters
+        const Part x = part_at<D>(a, pairs, p);
+        const int n = part_tiles(x, i);                                // of this query tile
+        const int n_all = max(part_tiles(x, 0), part_tiles(x, 1));  // of the converters
         place_next(a, p, x.n);
         if (n_all == 0) continue;
         const uint32_t qb = q_cnt % L::kQ;
@@ -680,21 +699,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::fence_proxy_async_smem();
       arrive_warp(cx.bar(kBarQFull + static_cast<int>(qb)), lane);
     };
+    const auto fetch = [&](const int8_t* codes, int lane_at, uint4 (&r)[kLoads]) {
+      const uint4* src = reinterpret_cast<const uint4*>(codes + at) + share * kLoads * 32 + lane_at;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) r[x] = src[x * 32];
+    };
     // opens the first unit from p on that has tiles; false at the end of the range
     const auto open_part = [&]() {
       while (p.todo > 0) {
-        const Part x = part_at(a, pairs, p);
+        const Part x = part_at<D>(a, pairs, p);
         n = x.n;
-        const int tiles = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
+        const int tiles = max(part_tiles(x, 0), part_tiles(x, 1));
         if (tiles > 0) {
-          t = p.t;
-          t_end = p.t + tiles;
+          t = x.t;
+          t_end = x.t + tiles;
           len = x.u.len;
           head = x.u.h;
           row_of_table = x.u.b * a.pt.stride;
           open_window(true);
           pick();
+          // on their way while the queries are brought
           if (ok) bring_queries(x.u);
+          fetch(a.c.k, lane, kr);
+          fetch(a.c.v, v_at, vr);
           return true;
         }
         place_next(a, p, n);
@@ -710,16 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       place_next(a, p, n);
       return open_part();
     };
-    const auto fetch = [&](const int8_t* codes, int lane_at, uint4 (&r)[kLoads]) {
-      const uint4* src = reinterpret_cast<const uint4*>(codes + at) + share * kLoads * 32 + lane_at;
-#pragma unroll
-      for (int x = 0; x < kLoads; ++x) r[x] = src[x * 32];
-    };
     bool more = open_part();
-    if (more) {
-      fetch(a.c.k, lane, kr);
-      fetch(a.c.v, v_at, vr);
-    }
     for (uint32_t cnt = 0; ok && more; ++cnt) {
       const uint32_t s = cnt % L::kStages;
       if (!(ok = wait_bar_warp(cx, cx.bar(kBarEmpty + static_cast<int>(s)), ((cnt / L::kStages) & 1u) ^ 1u))) break;
@@ -751,10 +769,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       if (last) {
         more = advance();
         if (!ok) break;
-        if (more) {
-          fetch(a.c.k, lane, kr);
-          fetch(a.c.v, v_at, vr);
-        }
       }
     }
     if (bad_page) atomicExch(a.dev_err, kDevErrPage);
@@ -779,13 +793,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     while (p.todo > 0) {
       int n, sees, all_see;
       {
-        const Part x = part_at(a, pairs, p);
+        const Part x = part_at<D>(a, pairs, p);
+        if (x.tiles == 0) {
+          place_next(a, p, x.n);
+          continue;
+        }
         const int r = x.u.row0 + rr;
         const bool real = r < x.u.R;
         sees = real ? row_sees(a, x.u, r) : 0;
         // the smallest limit in the warp decides, for all its lanes, whether a tile is masked
         all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
-        n = part_tiles(p, x, i);
+        n = part_tiles(x, i);
       }
       float m = -INFINITY, l = 0.0f, f = 0.0f, top = 0.0f;
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
@@ -807,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           factor = tops[win].y;
         }
         tc::tmem_wait_ld();
-        const int key0 = (p.t + j) * kKeys;
+        const int key0 = (max(p.at - kBegin<D>, 0) + j) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
         bool masked = key0 + kKeys > all_see;
@@ -898,9 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       steps += static_cast<uint32_t>(n);
 
       // the part's rows: to the output, or to the workspace
-      const Part x = part_at(a, pairs, p);
+      const Part x = part_at<D>(a, pairs, p);
       const Unit& u = x.u;
-      const int all = max(part_tiles(p, x, 0), part_tiles(p, x, 1));
+      const int all = max(part_tiles(x, 0), part_tiles(x, 1));
       windows += static_cast<uint32_t>((all + kWindow - 1) / kWindow);
       parts += all > 0 ? 1u : 0u;
       const int r = u.row0 + rr, tok = r / u.G, head = u.h * u.G + r - tok * u.G;
@@ -909,16 +927,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         if (!(ok = wait_pv(steps - 1u))) break;
         tc::tc_fence_after();
       }
-      const bool whole = x.n == x.size;
+      const bool whole = x.tiles == x.size;
       const int which = p.todo == found[3] ? 0 : 1;
-      if (p.todo == x.n && threadIdx.x == 128 && p.t == 0 && x.size > x.n) {
+      if (p.todo == x.n && threadIdx.x == 128 && x.t == 0 && !whole) {
         // the last unit begins here and goes on in other CTAs: up to which one, and whose rows
-        const int end = found[4] + x.size - x.n - 1, each = found[5], extra = found[6], head_units = extra * (each + 1);
+        const int end = found[4] + x.size - x.tiles - 1, each = found[5], extra = found[6], head_units = extra * (each + 1);
         static_cast<int4*>(a.workspace)[blockIdx.x] =
             make_int4(end < head_units ? end / (each + 1) : extra + (end - head_units) / each, u.b, 2 * u.h + which,
                       u.row0);
       }
-      const bool pad = !real && a.zero_rest && p.t == 0 && r < static_cast<int>(a.T) * u.G;
+      const bool pad = !real && a.zero_rest && x.t == 0 && r < static_cast<int>(a.T) * u.G;
       if (!real) l = 0.0f;
       const bool none = n == 0 || !real;
       const bool to_out = whole ? real || pad : pad;
@@ -926,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
                     (static_cast<size_t>(blockIdx.x) * 2 + which) * T::kSlot;
       // l = 0: no key was seen
       const float scale = none || l == 0.0f ? 0.0f : (whole ? top / l : top);
+      const bool wide = ((reinterpret_cast<uintptr_t>(a.out.p) | ((a.out.sb | a.out.ss | a.out.sh) << 1)) & 31) == 0;
       uint16_t* dst = a.out.p + u.b * a.out.sb + tok * a.out.ss + head * a.out.sh;
       if (to_out && a.lse != nullptr)
         a.lse[(static_cast<int64_t>(u.b) * a.H + head) * a.T + tok] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -942,21 +961,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           o[k] = (none || l == 0.0f) ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
         if (to_out) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                             __uint_as_float(o[8 * k + 2 * e + 1]));
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[16 * k + 2 * e]),
+                                                             __uint_as_float(o[16 * k + 2 * e + 1]));
               w[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            *reinterpret_cast<uint4*>(dst + 32 * cc + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+            uint16_t* to = dst + 32 * cc + 16 * k;
+            if (wide) {
+              store32(to, w);
+            } else {
+              *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         } else if (real) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(part + rr * D + 32 * cc + 4 * k) =
-                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) store32(part + rr * D + 32 * cc + 8 * k, o + 8 * k);
         }
       }
       tc::tc_fence_before();
