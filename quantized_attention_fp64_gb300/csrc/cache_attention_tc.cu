@@ -11,6 +11,7 @@
 //   warps 0, 1    one MMA-issuing thread per query tile
 //   warp 2        TMEM allocation
 //   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
+//   warp 3        where there is one query tile only (kOne, below): brings the codes
 //   warps 12-15   converters: read the int8 codes of a key tile (two warps per
 //                 32-key block, 16 bytes per lane and load, the next tile's
 //                 loads in flight in registers), turn them into fp16 and store
@@ -47,6 +48,7 @@ constexpr int kConv = 4;        // converter warps
 constexpr int kThreads = 384 + 32 * kConv;
 constexpr int kRows = 128;      // rows of a query tile
 constexpr int kKeys = 64;       // keys of a key tile
+constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 constexpr int kMaxSms = 160;
 constexpr int kMinTiles = 8;    // key tiles that are worth a CTA of their own
 constexpr int kWindow = 32;     // key tiles whose pages and scales are looked up together
@@ -63,27 +65,34 @@ constexpr uint32_t kRegLaunch = 65536 / kThreads / 8 * 8;
 static_assert(128 * kRegCtl + 32 * kConv * kRegConv + 256 * kRegSoftmax <= kThreads * kRegLaunch,
               "registers that the CTA is launched with");
 
-template <int D>
+template <int D, bool kOne>
 struct Smem {
   static constexpr uint32_t kSub = 128 * 128;             // 64 channels of 128 rows, fp16
   static constexpr uint32_t kTile = (D / 64) * kSub;      // a query tile
+  static constexpr int kQTiles = kOne ? 1 : 2;            // of a unit
   static constexpr uint32_t kSubK = kKeys * 128;          // 64 channels of a key tile
   static constexpr uint32_t kTileKV = (D / 64) * kSubK;   // keys; values are D rows of 64 keys
   static constexpr int kStages = D == 128 ? 4 : 8;        // key and value tiles
   static constexpr int kQ = D == 128 ? 1 : 2;             // units whose queries are kept
-  static constexpr uint32_t kOffQ = 0;                    // [unit][2 tiles]
-  static constexpr uint32_t kOffK = kOffQ + kQ * 2 * kTile;
+  // key and value tiles as codes, where they wait in shared memory
+  static constexpr int kRaw = !kOne ? 1 : (D == 128 ? 3 : 6);
+  static constexpr uint32_t kRawBlock = kCacheBlock * D;  // bytes of a block's keys or values
+  static constexpr uint32_t kOffQ = 0;                    // [unit][tile]
+  static constexpr uint32_t kOffK = kOffQ + kQ * kQTiles * kTile;
   static constexpr uint32_t kOffV = kOffK + kStages * kTileKV;
-  static constexpr uint32_t kOffBar = kOffV + kStages * kTileKV;
+  static constexpr uint32_t kOffRaw = kOffV + kStages * kTileKV;         // [stage] keys of the blocks, values of the blocks
+  static constexpr uint32_t kOffBar = kOffRaw + (kOne ? kRaw * 2 * kB * kRawBlock : 0);
 };
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8, kMaxRaw = 6;
 constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarFull = kBarQEmpty + 2, kBarEmpty = kBarFull + kMaxStages;
 constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarPFull = kBarSFull + 4;
 constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarTop = kBarDrain + 2;  // SFull, PFull, PVDone: [tile][buffer]
-constexpr int kNumBars = kBarTop + 1;
-template <int D>
+constexpr int kBarFold = kBarTop + 1;  // the second half of a folded part is in the workspace; it has been read
+constexpr int kBarRaw = kBarFold + 2, kBarRawFree = kBarRaw + kMaxRaw;
+constexpr int kNumBars = kBarRawFree + kMaxRaw;
+template <int D, bool kOne>
 struct SmemTail {
-  static constexpr uint32_t kOffAbort = Smem<D>::kOffBar + kNumBars * 8;  // as Ctx::abort_at has it
+  static constexpr uint32_t kOffAbort = Smem<D, kOne>::kOffBar + kNumBars * 8;  // as Ctx::abort_at has it
   static constexpr uint32_t kOffTmem = kOffAbort + 4;
   static constexpr uint32_t kOffTop = kOffTmem + 4;                    // [2][converter warp] largest value scale
   static constexpr uint32_t kOffScale = (kOffTop + 2 * kConv * 4 + 15) / 16 * 16;  // [window][tile] two (key scale, log2(s_v / R))
@@ -94,17 +103,21 @@ struct SmemTail {
   // one unit more than of the queries themselves: those are free once the
   // unit's last QK is done, when a softmax thread may still have to read its
   // factor; an issuer goes on to the next unit only after the softmax did
-  static constexpr int kRowUnits = Smem<D>::kQ + 1;
+  static constexpr int kRowUnits = Smem<D, kOne>::kQ + 1;
   static constexpr uint32_t kBytes = kOffRow + kRowUnits * 2 * kRows * 4;
   // workspace: a descriptor of each CTA's last unit, then two slots per CTA
   static constexpr size_t kDesc = size_t(kMaxSms) * sizeof(int4);
   static constexpr size_t kSlot = size_t(2) * kRows * (D + 2);          // floats
   static constexpr size_t kWorkspace = kDesc + size_t(kMaxSms) * 2 * kSlot * 4;
 };
-static_assert(SmemTail<128>::kBytes <= 232448u, "shared memory of one CTA");
+static_assert(SmemTail<128, false>::kBytes <= 232448u && SmemTail<128, true>::kBytes <= 232448u &&
+                  SmemTail<64, false>::kBytes <= 232448u && SmemTail<64, true>::kBytes <= 232448u,
+              "shared memory of one CTA");
+static_assert(SmemTail<128, true>::kWorkspace == SmemTail<128, false>::kWorkspace &&
+                  SmemTail<64, true>::kWorkspace == SmemTail<64, false>::kWorkspace,
+              "one workspace");
 
 constexpr int kS = 2;                    // buffers of S and P
-constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 // TMEM columns of the query tiles
 template <int D>
 struct Cols {
@@ -229,6 +242,11 @@ __device__ __forceinline__ void store16(uint32_t addr, const uint32_t* o) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                : "memory");
 }
+__device__ __forceinline__ uint4 load16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 // A whole sector of global memory (32-byte aligned). A thread writes its own
 // row, so two halves would be two writes to L2: 110 -> 106 us there.
 __device__ __forceinline__ void store32(void* to, const uint32_t* o) {
@@ -322,12 +340,26 @@ __device__ __forceinline__ int part_tiles(const Part& x, int i) {
   return max(min(x.t + x.tiles, i == 0 ? x.u.n[0] : x.u.n[1]) - x.t, 0);
 }
 
+// kOne (at most 128 query rows of a key/value head, so one query tile). A part
+// of kFold key tiles or more is folded: tile slot i takes its key tiles i,
+// i + 2, ..., both slots with the same queries, and slot 0 joins the two at the
+// part's end, through rows of the workspace that the part leaves free. Shorter
+// parts do not pay for the join. And warp 3 sends for the codes with bulk
+// copies, where the second query tile's room lets some wait in shared memory.
+// 40 rows over 14 x 20000 tokens, 8 heads of 128: 231 us as the form for more
+// rows does it, 241 with folding alone, 215 with the copies alone, 176 with
+// both; what bounds it is the conversion of the codes, which takes no less for
+// fewer rows (32 rows, without tensor memory: 149 us).
+constexpr int kFold = 8;
+static_assert(kWindow % 2 == 0, "a folded query tile begins a window at its own first tile of it");
+__device__ __forceinline__ bool folds(const Part& x) { return x.u.tiles == 1 && x.tiles >= kFold; }
+
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     const uint32_t sub = static_cast<uint32_t>(ks >> 2), off = static_cast<uint32_t>(ks & 3) * 32u;
-    tc::mma_f16_ss(d_tmem, desc_at(dq, sub * Smem<D>::kSub + off), desc_at(dk, sub * Smem<D>::kSubK + off),
+    tc::mma_f16_ss(d_tmem, desc_at(dq, sub * Smem<D, false>::kSub + off), desc_at(dk, sub * Smem<D, false>::kSubK + off),
                    tc::kIdescM128N64, ks > 0 ? 1u : 0u);
   }
 }
@@ -384,6 +416,12 @@ __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64
   return w;
 }
 
+// log2(s_v / R), held above -40, where a weight of it is 0 in fp16 (no value
+// scale: the codes are 0 and any weight will do).
+__device__ __forceinline__ float weight_of_scale(float vs, float top) {
+  return vs == 0.0f ? 0.0f : (vs == vs ? fmaxf(log2f(vs / top), -40.0f) : vs);
+}
+
 // One block of a row: p s_v / R = 2^(s c + n) of its 32 scores, in fp16, and
 // their sum. kMasked: from token lim on they are 0, whatever s and c are.
 template <bool kMasked>
@@ -405,10 +443,10 @@ __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], float c, flo
   return (sa.x + sa.y) + (sb.x + sb.y);
 }
 
-template <int D>
+template <int D, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const CacheAttentionArgs a, int pairs) {
-  using L = Smem<D>;
-  using T = SmemTail<D>;
+  using L = Smem<D, kOne>;
+  using T = SmemTail<D, kOne>;
   using C = Cols<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((tc::smem_u32(smem) & 1023u) != 0) {
@@ -437,6 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::mbar_init(cx.bar(kBarEmpty + s), 2);
     }
     tc::mbar_init(cx.bar(kBarTop), kConv);
+    for (int s = 0; s < L::kRaw; ++s) {
+      tc::mbar_init(cx.bar(kBarRaw + s), 1);
+      tc::mbar_init(cx.bar(kBarRawFree + s), kConv);
+    }
+    tc::mbar_init(cx.bar(kBarFold), kRows);
+    tc::mbar_init(cx.bar(kBarFold + 1), kRows);
     tc::fence_mbar_init();
   }
   if (warp == 2) {
@@ -509,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       const int i = warp;
       const bool leader = elect_one();
       const uint32_t d_o = tmem + C::o(i);
-      const uint64_t dq0 = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(i) * L::kTile);
+      const uint64_t dq0 = tc::sw128_desc(sbase + L::kOffQ);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dv0 = tc::sw128_desc(sbase + L::kOffV);
       // key tiles (of the converters, of this query tile) and parts so far
       uint32_t cnt = 0, steps = 0, q_cnt = 0;
@@ -517,25 +561,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       Place p = first_place(found);
       while (ok && p.todo > 0) {
         const Part x = part_at<D>(a, pairs, p);
-        const int n = part_tiles(x, i);                                // of this query tile
         const int n_all = max(part_tiles(x, 0), part_tiles(x, 1));  // of the converters
+        const int fold = kOne && folds(x) ? 1 : 0;
+        const int n = fold ? (n_all + 1 - i) >> 1 : part_tiles(x, i);  // of this query tile
+        const auto mine = [&](int j) { return fold ? (j & 1) == i : j < n; };
         place_next(a, p, x.n);
         if (n_all == 0) continue;
         const uint32_t qb = q_cnt % L::kQ;
         if (!(ok = wait_bar_warp(cx, cx.bar(kBarQFull + static_cast<int>(qb)), (q_cnt / L::kQ) & 1u))) break;
         ++q_cnt;
         if (n == 0 && leader) tc::mbar_arrive(cx.bar(kBarQEmpty + static_cast<int>(qb)));
-        const uint64_t dq = desc_at(dq0, qb * 2u * L::kTile);
+        const uint64_t dq = desc_at(dq0, (qb * L::kQTiles + (kOne ? 0u : static_cast<uint32_t>(i))) * L::kTile);
         // PV_j once P_j is there (its values came with its keys)
         const auto pv = [&](int j) {
           const int s = static_cast<int>((cnt + static_cast<uint32_t>(j)) % L::kStages);
-          if (j < n) {
-            const uint32_t st = steps + static_cast<uint32_t>(j);
+          if (mine(j)) {
+            const uint32_t st = steps + static_cast<uint32_t>(j >> fold);
             const int buf = static_cast<int>(st % kS);
             if (!wait_bar_warp(cx, cx.bar(kBarPFull + 2 * i + buf), (st / kS) & 1u)) return false;
             tc::tc_fence_after();
             if (leader) {
-              issue_pv<D>(d_o, tmem + C::s(i, buf), desc_at(dv0, static_cast<uint32_t>(s) * L::kTileKV), j > 0);
+              issue_pv<D>(d_o, tmem + C::s(i, buf), desc_at(dv0, static_cast<uint32_t>(s) * L::kTileKV), j > fold);
               tc::mma_commit(cx.bar(kBarPVDone + 2 * i + buf));
               tc::mma_commit(cx.bar(kBarEmpty + s));
             }
@@ -545,20 +591,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           __syncwarp();
           return true;
         };
-        for (int j = 0; ok && j <= n_all; ++j) {
-          bool pending = j > 0;
+        // PV_j follows this query tile's next QK
+        for (int j = 0; ok && j <= n_all + fold; ++j) {
+          bool pending = j > fold;
           if (j < n_all) {
             const uint32_t at = cnt + static_cast<uint32_t>(j), s = at % L::kStages, ph = (at / L::kStages) & 1u;
             const uint32_t full = cx.bar(kBarFull + static_cast<int>(s));
             // keys that are late do not hold up the last tile's PV
             if (pending && !__any_sync(0xffffffffu, tc::mbar_try_wait(full, ph))) {
-              if (!(ok = pv(j - 1))) break;
+              if (!(ok = pv(j - 1 - fold))) break;
               pending = false;
             }
             // QK_j once its keys are there and PV_{j-2} has read P in its buffer
             if (!(ok = wait_bar_warp(cx, full, ph))) break;
-            if (j < n) {
-              const uint32_t st = steps + static_cast<uint32_t>(j);
+            if (mine(j)) {
+              const uint32_t st = steps + static_cast<uint32_t>(j >> fold);
               const int buf = static_cast<int>(st % kS);
               if (st >= kS && !(ok = wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + buf), (st / kS - 1u) & 1u))) break;
               tc::tc_fence_after();
@@ -568,12 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
                 tc::mbar_arrive(cx.bar(kBarSFull + 2 * i + buf));
                 issue_qk<D>(tmem + C::s(i, buf), dq, desc_at(dk0, s * L::kTileKV));
                 tc::mma_commit(cx.bar(kBarSFull + 2 * i + buf));
-                if (j == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
+                if ((j >> fold) == n - 1) tc::mma_commit(cx.bar(kBarQEmpty + static_cast<int>(qb)));
               }
               __syncwarp();
             }
           }
-          if (pending && !(ok = pv(j - 1))) break;
+          if (pending && !(ok = pv(j - 1 - fold))) break;
         }
         cnt += static_cast<uint32_t>(n_all);
         steps += static_cast<uint32_t>(n);
@@ -582,6 +629,56 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       if (leader) tc::mma_commit(cx.bar(kBarDrain + i));
       __syncwarp();
       wait_bar<false>(cx, cx.bar(kBarDrain + i), 0);
+    } else if (kOne && warp == 3) {
+      // ----------------------------------------------------- codes in advance --
+      // Looks 32 key tiles up at a time, two blocks a lane, and sends for them
+      // with bulk copies, kRaw tiles ahead of the converters.
+      uint32_t sent = 0, windows = 0;
+      bool ok = true, bad_page = false;
+      Place p = first_place(found);
+      while (ok && p.todo > 0) {
+        const Part x = part_at<D>(a, pairs, p);
+        place_next(a, p, x.n);
+        const int tiles = part_tiles(x, 0);
+        float top = 0.0f;
+        Window win[kB];
+        for (int j = 0; ok && j < tiles; ++j, ++sent) {
+          if (j % kWindow == 0) {
+            float most = 0.0f;
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+              win[b] = load_window<D>(a, x.u.b * a.pt.stride, x.u.h, x.u.len, (x.t + j + lane) * kB + b, &bad_page);
+              if (j + lane < tiles) most = fmaxf(most, win[b].vs);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float factor = j == 0 || !(most > top) ? 1.0f : top / most;
+            if (j == 0 || most > top) top = most;
+            float n[kB];
+#pragma unroll
+            for (int b = 0; b < kB; ++b) n[b] = weight_of_scale(win[b].vs, top);
+            const uint32_t slot = windows % kWindows;
+            reinterpret_cast<float4*>(smem + T::kOffScale)[slot * kWindow + lane] =
+                make_float4(win[0].ks, win[1].ks, n[0], n[1]);
+            if (lane == 0) reinterpret_cast<float2*>(smem + T::kOffTopOf)[slot] = make_float2(top, factor);
+            ++windows;
+          }
+          const int64_t at0 = __shfl_sync(0xffffffffu, win[0].at, j % kWindow);
+          const int64_t at1 = __shfl_sync(0xffffffffu, win[1].at, j % kWindow);
+          const uint32_t r = sent % L::kRaw;
+          const uint32_t bar = cx.bar(kBarRaw + static_cast<int>(r));
+          if (!(ok = wait_bar_warp(cx, cx.bar(kBarRawFree + static_cast<int>(r)), ((sent / L::kRaw) & 1u) ^ 1u))) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar, 2 * kB * L::kRawBlock);
+          __syncwarp();
+          if (lane < 2 * kB)  // keys of block 0, 1, values of block 0, 1
+            tc::bulk_load(sbase + L::kOffRaw + (r * 2 * kB + static_cast<uint32_t>(lane)) * L::kRawBlock,
+                          (lane < kB ? a.c.k : a.c.v) + ((lane & 1) ? at1 : at0), L::kRawBlock, bar);
+        }
+      }
+      if (bad_page) atomicExch(a.dev_err, kDevErrPage);
+      // copies in flight land before the CTA ends (some are left where a wait ran out)
+      for (uint32_t k = sent < L::kRaw ? 0u : sent - L::kRaw; k < sent; ++k)
+        wait_bar<false>(cx, cx.bar(kBarRaw + static_cast<int>(k % L::kRaw)), (k / L::kRaw) & 1u);
     }
     __syncwarp();
   } else if (warp >= 12) {
@@ -596,7 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     constexpr int kLoads = 2 * D / 16 / kConv;
     const int v_ch = ((lane >> 1) & 9) | ((lane >> 1) & 2) << 1 | ((lane >> 1) & 4) >> 1;
     const int v_at = 2 * v_ch + (lane & 1);
-    uint4 kr[kLoads], vr[kLoads];  // raw codes: 512 bytes per load of the warp
     float* tops = reinterpret_cast<float*>(smem + T::kOffTop);
     bool bad_page = false, ok = true;
     // the tile that is fetched next: tile t of t_end of the unit at `p`
@@ -624,14 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       for (int k = 0; k < kConv; ++k) x = fmaxf(x, buf[k]);
       const float factor = fresh || !(x > top) ? 1.0f : top / x;
       if (fresh || x > top) top = x;
-      // the softmax's view: key scales (negative: no tokens) and log2(s_v / R),
-      // which is held above -40, where a weight of it is 0 in fp16 (no value
-      // scale: the codes are 0 and any weight will do)
+      // the softmax's view: key scales (negative: no tokens) and log2(s_v / R)
       const uint32_t slot = windows % kWindows;
       if (share == 0) {
         float* row = reinterpret_cast<float*>(smem + T::kOffScale) + (slot * kWindow + lane) * 4 + blk;
         row[0] = win.ks;
-        row[2] = win.vs == 0.0f ? 0.0f : (win.vs == win.vs ? fmaxf(log2f(win.vs / top), -40.0f) : win.vs);
+        row[2] = weight_of_scale(win.vs, top);
       }
       if (w == 0 && lane == 0) reinterpret_cast<float2*>(smem + T::kOffTopOf)[slot] = make_float2(top, factor);
       ++windows;
@@ -650,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       ++parts;
       const int g = lane >> 2, c4 = lane & 3;
       const uint16_t* base = a.q.p + u.b * a.q.sb + c4 * 16;
-      constexpr int kTimes = 2 * kRows / (8 * kConv), kAhead = 256 / D;  // rows per lane, of which so many load together
+      constexpr int kTimes = L::kQTiles * kRows / (8 * kConv), kAhead = 256 / D;  // rows per lane, of which so many load together
 #pragma unroll 1
       for (int it0 = 0; it0 < kTimes; it0 += kAhead) {
         uint4 x[kAhead][D / 32];
@@ -682,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);
           const float down = __uint_as_float((254u - ex) << 23);
           if (c4 == 0) rows[rr] = __uint_as_float(ex << 23);
-          const uint32_t to = sbase + L::kOffQ + (qb * 2u + static_cast<uint32_t>(rr >> 7)) * L::kTile +
+          const uint32_t to = sbase + L::kOffQ + (qb * L::kQTiles + static_cast<uint32_t>(rr >> 7)) * L::kTile +
                               static_cast<uint32_t>(rr & 127) * 128u;
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) {
@@ -699,10 +793,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::fence_proxy_async_smem();
       arrive_warp(cx.bar(kBarQFull + static_cast<int>(qb)), lane);
     };
-    const auto fetch = [&](const int8_t* codes, int lane_at, uint4 (&r)[kLoads]) {
-      const uint4* src = reinterpret_cast<const uint4*>(codes + at) + share * kLoads * 32 + lane_at;
+    // the warp's share of a tile's codes, into stage s
+    const auto put_keys = [&](uint32_t s, const uint4 (&kr)[kLoads]) {
+      const uint32_t k_row = sbase + L::kOffK + s * L::kTileKV;
 #pragma unroll
-      for (int x = 0; x < kLoads; ++x) r[x] = src[x * 32];
+      for (int x = 0; x < kLoads; ++x) {
+        const int at8 = share * kLoads + x, j8 = at8 & 3, hf = at8 >> 2;  // eight tokens of a 64-channel half
+        const int n8 = lane >> 2, row = blk * 32 + 8 * (n8 >> 1) + 2 * j8 + (n8 & 1);  // value_position of token 8 j8 + n8
+        store_codes(k_row + static_cast<uint32_t>(hf) * L::kSubK + static_cast<uint32_t>(row) * 128u,
+                    static_cast<uint32_t>(lane & 3) * 2u, static_cast<uint32_t>(row) & 7u, kr[x]);
+      }
+    };
+    const auto put_values = [&](uint32_t s, const uint4 (&vr)[kLoads]) {
+      const uint32_t v_row = sbase + L::kOffV + s * L::kTileKV;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) {
+        const int ch = 16 * (share * kLoads + x) + v_ch;
+        store_codes(v_row + static_cast<uint32_t>(ch) * 128u,
+                    static_cast<uint32_t>(blk) * 4u + static_cast<uint32_t>(lane & 1) * 2u, static_cast<uint32_t>(ch) & 7u,
+                    vr[x]);
+      }
     };
     // opens the first unit from p on that has tiles; false at the end of the range
     const auto open_part = [&]() {
@@ -719,9 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           open_window(true);
           pick();
           // on their way while the queries are brought
-          if (ok) bring_queries(x.u);
-          fetch(a.c.k, lane, kr);
-          fetch(a.c.v, v_at, vr);
+          if (!kOne && ok) bring_queries(x.u);
           return true;
         }
         place_next(a, p, n);
@@ -737,38 +845,69 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       place_next(a, p, n);
       return open_part();
     };
-    bool more = open_part();
-    for (uint32_t cnt = 0; ok && more; ++cnt) {
-      const uint32_t s = cnt % L::kStages;
-      if (!(ok = wait_bar_warp(cx, cx.bar(kBarEmpty + static_cast<int>(s)), ((cnt / L::kStages) & 1u) ^ 1u))) break;
-      const uint32_t k_row = sbase + L::kOffK + s * L::kTileKV, v_row = sbase + L::kOffV + s * L::kTileKV;
+    if constexpr (kOne) {
+      // warp 3 brings the codes: they wait in shared memory
+      Place q = first_place(found);
+      uint32_t cnt = 0;
+      while (ok && q.todo > 0) {
+        const Part x = part_at<D>(a, pairs, q);
+        place_next(a, q, x.n);
+        const int tiles = part_tiles(x, 0);
+        if (tiles > 0) bring_queries(x.u);
+        for (int j = 0; ok && j < tiles; ++j, ++cnt) {
+          const uint32_t s = cnt % L::kStages, r = cnt % L::kRaw;
+          if (!(ok = wait_bar_warp(cx, cx.bar(kBarRaw + static_cast<int>(r)), (cnt / L::kRaw) & 1u))) break;
+          uint4 kr[kLoads], vr[kLoads];
+          const uint32_t from = sbase + L::kOffRaw + (r * 2 * kB + static_cast<uint32_t>(blk)) * L::kRawBlock +
+                                static_cast<uint32_t>(share * kLoads) * 512u;
 #pragma unroll
-      for (int x = 0; x < kLoads; ++x) {
-        const int at8 = share * kLoads + x, j8 = at8 & 3, hf = at8 >> 2;  // eight tokens of a 64-channel half
-        const int n8 = lane >> 2, row = blk * 32 + 8 * (n8 >> 1) + 2 * j8 + (n8 & 1);  // value_position of token 8 j8 + n8
-        store_codes(k_row + static_cast<uint32_t>(hf) * L::kSubK + static_cast<uint32_t>(row) * 128u,
-                    static_cast<uint32_t>(lane & 3) * 2u, static_cast<uint32_t>(row) & 7u, kr[x]);
+          for (int y = 0; y < kLoads; ++y) {
+            kr[y] = load16(from + static_cast<uint32_t>(y * 32 + lane) * 16u);
+            vr[y] = load16(from + kB * L::kRawBlock + static_cast<uint32_t>(y * 32 + v_at) * 16u);
+          }
+          arrive_warp(cx.bar(kBarRawFree + static_cast<int>(r)), lane);
+          if (!(ok = wait_bar_warp(cx, cx.bar(kBarEmpty + static_cast<int>(s)), ((cnt / L::kStages) & 1u) ^ 1u))) break;
+          put_keys(s, kr);
+          put_values(s, vr);
+          tc::fence_proxy_async_smem();
+          arrive_warp(cx.bar(kBarFull + static_cast<int>(s)), lane);
+        }
       }
-      // the next tile of the unit; the next unit only once this one's values are out
-      const bool last = t + 1 >= t_end;
-      if (!last) {
-        advance();
-        if (!ok) break;
+    } else {
+      uint4 kr[kLoads], vr[kLoads];  // raw codes: 512 bytes per load of the warp
+      const auto fetch = [&](const int8_t* codes, int lane_at, uint4 (&r)[kLoads]) {
+        const uint4* src = reinterpret_cast<const uint4*>(codes + at) + share * kLoads * 32 + lane_at;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) r[x] = src[x * 32];
+      };
+      bool more = open_part();
+      if (more) {
         fetch(a.c.k, lane, kr);
+        fetch(a.c.v, v_at, vr);
       }
-#pragma unroll
-      for (int x = 0; x < kLoads; ++x) {
-        const int ch = 16 * (share * kLoads + x) + v_ch;
-        store_codes(v_row + static_cast<uint32_t>(ch) * 128u,
-                    static_cast<uint32_t>(blk) * 4u + static_cast<uint32_t>(lane & 1) * 2u, static_cast<uint32_t>(ch) & 7u,
-                    vr[x]);
-      }
-      if (!last) fetch(a.c.v, v_at, vr);
-      tc::fence_proxy_async_smem();
-      arrive_warp(cx.bar(kBarFull + static_cast<int>(s)), lane);
-      if (last) {
-        more = advance();
-        if (!ok) break;
+      for (uint32_t cnt = 0; ok && more; ++cnt) {
+        const uint32_t s = cnt % L::kStages;
+        if (!(ok = wait_bar_warp(cx, cx.bar(kBarEmpty + static_cast<int>(s)), ((cnt / L::kStages) & 1u) ^ 1u))) break;
+        put_keys(s, kr);
+        // the next tile of the unit; the next unit only once this one's values are out
+        const bool last = t + 1 >= t_end;
+        if (!last) {
+          advance();
+          if (!ok) break;
+          fetch(a.c.k, lane, kr);
+        }
+        put_values(s, vr);
+        if (!last) fetch(a.c.v, v_at, vr);
+        tc::fence_proxy_async_smem();
+        arrive_warp(cx.bar(kBarFull + static_cast<int>(s)), lane);
+        if (last) {
+          more = advance();
+          if (!ok) break;
+          if (more) {
+            fetch(a.c.k, lane, kr);
+            fetch(a.c.v, v_at, vr);
+          }
+        }
       }
     }
     if (bad_page) atomicExch(a.dev_err, kDevErrPage);
@@ -785,25 +924,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     const int rr = i * kRows + wq * 32 + lane;  // this thread's row of a pair
     bool ok = true;
     uint32_t steps = 0, windows = 0, parts = 0;  // key tiles of this query tile; the converters' windows and units
+    uint32_t folded = 0;  // folded parts
     // waits for the PV of step x (its P buffer and O are then free)
     const auto wait_pv = [&](uint32_t x) {
       return wait_bar_warp(cx, cx.bar(kBarPVDone + 2 * i + static_cast<int>(x % kS)), (x / kS) & 1u);
     };
     Place p = first_place(found);
     while (p.todo > 0) {
-      int n, sees, all_see;
+      int n, sees, all_see, fold;
       {
         const Part x = part_at<D>(a, pairs, p);
         if (x.tiles == 0) {
           place_next(a, p, x.n);
           continue;
         }
-        const int r = x.u.row0 + rr;
+        fold = kOne && folds(x) ? 1 : 0;
+        const int r = x.u.row0 + (fold ? rr & (kRows - 1) : rr);
         const bool real = r < x.u.R;
         sees = real ? row_sees(a, x.u, r) : 0;
         // the smallest limit in the warp decides, for all its lanes, whether a tile is masked
         all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
-        n = part_tiles(x, i);
+        n = fold ? (part_tiles(x, 0) + 1 - i) >> 1 : part_tiles(x, i);
       }
       float m = -INFINITY, l = 0.0f, f = 0.0f, top = 0.0f;
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
@@ -815,17 +956,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         uint32_t sr[kB][32];
 #pragma unroll
         for (int b = 0; b < kB; ++b) tc::tmem_ld32(tS + 32u * b, sr[b]);
-        const uint32_t win = (windows + static_cast<uint32_t>(j) / kWindow) % kWindows;
-        const float4 sc = scales[win * kWindow + static_cast<uint32_t>(j) % kWindow];
-        const bool opens = j % kWindow == 0;
+        const int jj = fold ? 2 * j + i : j;  // key tile of the part
+        const uint32_t win = (windows + static_cast<uint32_t>(jj) / kWindow) % kWindows;
+        const float4 sc = scales[win * kWindow + static_cast<uint32_t>(jj) % kWindow];
+        const bool opens = (jj & ~fold) % kWindow == 0;
         float factor = 1.0f;  // what O is rescaled with because R grew
         if (opens) {
-          if (j == 0) f = rows[rr] * a.sm_log2;
+          if (j == 0) f = rows[fold ? rr & (kRows - 1) : rr] * a.sm_log2;
           top = tops[win].x;
           factor = tops[win].y;
         }
         tc::tmem_wait_ld();
-        const int key0 = (max(p.at - kBegin<D>, 0) + j) * kKeys;
+        const int key0 = (max(p.at - kBegin<D>, 0) + jj) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
         bool masked = key0 + kKeys > all_see;
@@ -937,20 +1079,56 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
                       u.row0);
       }
       const bool pad = !real && a.zero_rest && x.t == 0 && r < static_cast<int>(a.T) * u.G;
-      if (!real) l = 0.0f;
-      const bool none = n == 0 || !real;
       const bool to_out = whole ? real || pad : pad;
       float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + T::kDesc) +
                     (static_cast<size_t>(blockIdx.x) * 2 + which) * T::kSlot;
+      float2 other = make_float2(-INFINITY, 0.0f);  // the second half's maximum and sum
+      float s_own = 1.0f, s_other = 0.0f;
+      if (fold) {
+        // slot 1's half through the rows of the workspace that the part leaves free
+        float* half = part + (kRows + (rr & (kRows - 1))) * D;
+        float2* half_ml = reinterpret_cast<float2*>(part + 2 * kRows * D + 2 * (kRows + (rr & (kRows - 1))));
+        if (i == 1) {
+          if (!(ok = wait_bar_warp(cx, cx.bar(kBarFold + 1), (folded & 1u) ^ 1u))) break;
+          *half_ml = make_float2(m, l);
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + 32u * cc, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[k]) * top);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) store32(half + 32 * cc + 8 * k, o + 8 * k);
+          }
+          __threadfence_block();
+          tc::mbar_arrive(cx.bar(kBarFold));
+        } else {
+          if (!(ok = wait_bar_warp(cx, cx.bar(kBarFold), folded & 1u))) break;
+          other = __ldcg(half_ml);
+          if (other.y != 0.0f) {
+            const float up = fmaxf(m, other.x);
+            s_own = l == 0.0f ? 0.0f : ex2(m - up);
+            s_other = ex2(other.x - up);
+            l = l * s_own + other.y * s_other;
+            m = up;
+          }
+        }
+        ++folded;
+      }
+      if (!real) l = s_other = 0.0f;
+      const bool none = n == 0 || !real;
       // l = 0: no key was seen
-      const float scale = none || l == 0.0f ? 0.0f : (whole ? top / l : top);
+      const float scale = none || l == 0.0f || s_own == 0.0f ? 0.0f : (whole ? top / l : top) * s_own;
+      if (s_other != 0.0f && whole) s_other /= l;
       const bool wide = ((reinterpret_cast<uintptr_t>(a.out.p) | ((a.out.sb | a.out.ss | a.out.sh) << 1)) & 31) == 0;
       uint16_t* dst = a.out.p + u.b * a.out.sb + tok * a.out.ss + head * a.out.sh;
       if (to_out && a.lse != nullptr)
         a.lse[(static_cast<int64_t>(u.b) * a.H + head) * a.T + tok] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (!whole && real) *reinterpret_cast<float2*>(part + 2 * kRows * D + 2 * rr) = make_float2(m, l);
+      const int chunks = __any_sync(0xffffffffu, real || to_out) ? D / 32 : 0;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int cc = 0; cc < chunks; ++cc) {
         uint32_t o[32];
         if (n > 0) {
           tc::tmem_ld32(tO + 32u * cc, o);
@@ -958,7 +1136,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          o[k] = (none || l == 0.0f) ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
+          o[k] = (none || l == 0.0f || s_own == 0.0f) ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
+        if (s_other != 0.0f) {
+          const float4* half = reinterpret_cast<const float4*>(part + (kRows + rr) * D + 32 * cc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 y = __ldcg(half + k);
+            o[4 * k] = __float_as_uint(fmaf(y.x, s_other, __uint_as_float(o[4 * k])));
+            o[4 * k + 1] = __float_as_uint(fmaf(y.y, s_other, __uint_as_float(o[4 * k + 1])));
+            o[4 * k + 2] = __float_as_uint(fmaf(y.z, s_other, __uint_as_float(o[4 * k + 2])));
+            o[4 * k + 3] = __float_as_uint(fmaf(y.w, s_other, __uint_as_float(o[4 * k + 3])));
+          }
+        }
         if (to_out) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -982,6 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           for (int k = 0; k < 4; ++k) store32(part + rr * D + 32 * cc + 8 * k, o + 8 * k);
         }
       }
+      if (fold && i == 0) tc::mbar_arrive(cx.bar(kBarFold + 1));
       tc::tc_fence_before();
       place_next(a, p, x.n);
     }
@@ -1000,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
 }  // namespace
 
 size_t cache_attention_tc_workspace_bytes(int64_t D) {
-  return D == 128 ? SmemTail<128>::kWorkspace : SmemTail<64>::kWorkspace;
+  return D == 128 ? SmemTail<128, false>::kWorkspace : SmemTail<64, false>::kWorkspace;
 }
 
 cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream) {
@@ -1012,8 +1202,11 @@ cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cu
   // what the tables can name bounds the work: no CTA without any
   const int64_t want = units > tiles * units / kMinTiles ? units : tiles * units / kMinTiles;
   const unsigned ctas = static_cast<unsigned>(want < sms ? want : sms);
-  const auto kernel = D == 128 ? cache_attention_tc_kernel<128> : cache_attention_tc_kernel<64>;
-  const int bytes = static_cast<int>(D == 128 ? SmemTail<128>::kBytes : SmemTail<64>::kBytes);
+  const bool one = rows <= kRows;
+  const auto kernel = D == 128 ? (one ? cache_attention_tc_kernel<128, true> : cache_attention_tc_kernel<128, false>)
+                               : (one ? cache_attention_tc_kernel<64, true> : cache_attention_tc_kernel<64, false>);
+  const int bytes = static_cast<int>(D == 128 ? (one ? SmemTail<128, true>::kBytes : SmemTail<128, false>::kBytes)
+                                              : (one ? SmemTail<64, true>::kBytes : SmemTail<64, false>::kBytes));
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1028,7 +1221,7 @@ cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cu
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, a, static_cast<int>(pairs))) != cudaSuccess || ctas == 1) return e;
   return launch_cache_join(a, D, 2 * kRows, static_cast<int>(rows < 2 * kRows ? rows : 2 * kRows),
-                           static_cast<int>(ctas), D == 128 ? SmemTail<128>::kDesc : SmemTail<64>::kDesc, stream);
+                           static_cast<int>(ctas), D == 128 ? SmemTail<128, false>::kDesc : SmemTail<64, false>::kDesc, stream);
 }
 
 }  // namespace sage

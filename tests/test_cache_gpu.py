@@ -335,6 +335,56 @@ def test_attention(H, Hkv, D, page, lengths, q_lengths, T, causal):
     attend(np.random.default_rng(21), H, Hkv, D, page, lengths, q_lengths, T, causal)
 
 
+FOLDED = [
+    # 33 to 128 rows of a key/value head over long and short sequences: parts whose key tiles two
+    # warpgroups share, whole items and items cut over CTAs, odd numbers of tiles, rows that see none
+    (8, 1, 128, 64, [1200, 3000, 1025], None, 8, True),
+    (8, 1, 64, 32, [1200, 3000, 1025], None, 8, True),
+    (4, 4, 64, 32, [5000, 1100], [100, 33], 100, False),
+    (16, 2, 128, 64, [2048] * 40, None, 5, True),
+    (4, 1, 128, 32, [9000], [40], 64, True),
+    (12, 2, 64, 64, [1500, 20], None, 50, True),
+    (5, 1, 128, 128, [511, 512, 513, 575, 577, 0, 1], [25, 24, 0, 1, 25, 25, 25], 25, False),
+    (8, 8, 64, 64, [(97 * i) % 1500 for i in range(30)], [(7 * i) % 41 for i in range(30)], 40, True),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,D,page,lengths,q_lengths,T,causal", FOLDED)
+def test_attention_one_query_tile(H, Hkv, D, page, lengths, q_lengths, T, causal):
+    attend(np.random.default_rng(31), H, Hkv, D, page, lengths, q_lengths, T, causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_one_query_tile_nan_and_bad_pages(D):
+    """A NaN scale reaches the rows that see it only; a page that is not there counts as one without tokens."""
+    rng = np.random.default_rng(32)
+    H, Hkv, page, n, T = 8, 1, 64, 2100, 9
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    q = bf16(rng, 1, T, H, D)
+    clean = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=True)
+    pg, blk = c.at(table[0], n - 1)  # tokens 2080 .. 2099: rows t see up to 2091 + t
+    for s in (c.k_scale, c.v_scale):
+        was = s[pg, 0, blk]
+        s[pg, 0, blk] = np.nan
+        out = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=True)
+        assert torch.isnan(out.float()).all()
+        s[pg, 0, blk] = was
+    early = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=True, q_lengths=ints([T]))
+    assert torch.equal(early, clean)
+    bad = table.copy()
+    bad[0, 3] = 2 ** 30
+    out, lse = sage.cache_attention(q, upload(c), ints(bad), ints([n]), is_causal=True, return_lse=True)
+    assert sage.device_error() == DEVICE_PAGE
+    c.k_scale[table[0, 3]] = 0.0  # the definition without these 64 tokens: their weight taken out by hand
+    o, l, w = oc.attention(c, f32(q), table, [n], [T], True, 1 / math.sqrt(D))
+    c.v_scale[table[0, 3]] = 0.0
+    o, _, w = oc.attention(c, f32(q), table, [n], [T], True, 1 / math.sqrt(D))
+    part = 1.0 - 64.0 / np.exp(l)  # keys of scale 0 have the logit 0: 64 ones in the sum
+    part = np.moveaxis(part, 1, 2)[..., None]
+    close(out, lse, o / part, l + np.log(part[..., 0].transpose(0, 2, 1)), w / part)
+
+
 @pytest.mark.parametrize("case", [2, 7, 10, 11])
 def test_attention_hnd_and_scale(case):
     H, Hkv, D, page, lengths, q_lengths, T, causal = ATTENTION[case]
