@@ -179,6 +179,31 @@ def test_append_odd_values():
     assert gpu.k_scale[3] == np.float32(1) / np.float32(127)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_quotients_at_and_next_to_ties(D):
+    """Scales that are powers of two make every half a tie; others put quotients next to one. All sizes of scale."""
+    rng = np.random.default_rng(14)
+    powers = [-133, -126, -98, -91, -90, -89, -40, -1, 0, 1, 50, 99, 100, 101, 119]
+    n = len(powers) * 64
+    table, P = make_table(rng, [n], 64)
+    c = oc.Cache(P, 2, D, 64)
+    gpu = upload(c)
+    x = np.empty((1, n, 2, D))
+    for i, e in enumerate(powers):
+        # a block whose scale is 2^e, halves up to 127; then one whose scale is 2^e times 128..255 / 127 / 128
+        halves = rng.integers(-254, 255, (32, 2, D)) / 2.0
+        halves[0, :, 0] = 127
+        x[0, 64 * i:64 * i + 32] = np.ldexp(halves, e)
+        m = np.ldexp(rng.integers(128, 256, (32, 2, D)).astype(float), rng.integers(-9, 0, (32, 2, D)))
+        m[0, :, 0] = 255 - i
+        x[0, 64 * i + 32:64 * i + 64] = np.ldexp(m * rng.choice([-1, 1], m.shape), e)
+    k = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()
+    v = -k.flip(1).contiguous()
+    oc.append(c, f32(k), f32(v), table, [0], [n])
+    sage.cache_append(gpu, k, v, ints(table), ints([0]))
+    same_tokens(gpu, c, table, [n])
+
+
 def test_append_strided_inputs_and_untouched_rest():
     rng = np.random.default_rng(12)
     H, D, page = 2, 128, 64
@@ -319,6 +344,8 @@ ATTENTION = [
     (8, 2, 128, 64, [3001], None, 40, True),
     (2, 1, 64, 64, [5000], None, 2, True),
     (4, 4, 128, 64, [20, 300], None, 300, True),                        # more queries than tokens
+    (2, 2, 64, 32, [(61 * i) % 500 for i in range(90)], [(37 * i) % 291 for i in range(90)], 290, True),
+    (3, 1, 128, 64, [1500, 40, 0, 2300], [190, 10, 190, 0], 190, False),
     # calls whose blocks are cut evenly over the GPU, items shared by CTAs and CTAs by items
     (14, 2, 128, 64, [9001, 10, 0, 4000], None, 1, True),
     (4, 1, 64, 128, [10000, 33], [3, 2], 3, True),
@@ -346,6 +373,7 @@ FOLDED = [
     (12, 2, 64, 64, [1500, 20], None, 50, True),
     (5, 1, 128, 128, [511, 512, 513, 575, 577, 0, 1], [25, 24, 0, 1, 25, 25, 25], 25, False),
     (8, 8, 64, 64, [(97 * i) % 1500 for i in range(30)], [(7 * i) % 41 for i in range(30)], 40, True),
+    (4, 1, 128, 32, [(61 * i) % 900 for i in range(200)], [(5 * i) % 18 for i in range(200)], 17, True),
 ]
 
 
@@ -679,6 +707,57 @@ def test_graph_replay_with_moving_lengths():
         same_tokens(gpu, c, table, [s + 1 for s in starts])
         n0.add_(1)
         n1.add_(1)
+
+
+@pytest.mark.parametrize("T", [1, 12, 80])
+def test_two_graphs_replayed_at_once(T):
+    """Each captured call keeps a workspace of its own: replays on two streams do not disturb one another."""
+    rng = np.random.default_rng(35)
+    B, H, Hkv, D, page = 2, 8, 2, 128, 64
+    lengths = [5000, 3000]
+    table, P = make_table(rng, lengths, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    gpu, t, n = upload(c), ints(table), ints(lengths)
+    qs = [bf16(rng, B, T, H, D) for _ in (0, 1)]
+    alone = [sage.cache_attention(q, gpu, t, n, is_causal=True) for q in qs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(sage.cache_attention(q, gpu, t, n, is_causal=True))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], alone[0]) and torch.equal(outs[1], alone[1])
+
+
+@pytest.mark.parametrize("T", [1, 12, 80, 300])
+def test_page_table_rows_of_a_wider_tensor(T):
+    rng = np.random.default_rng(36)
+    lengths = [400, 301, 0]
+    table, P = make_table(rng, lengths, 32)
+    c = random_cache(rng, P, 2, 64, 32)
+    gpu = upload(c)
+    wide = torch.full((3, table.shape[1] + 9), 2 ** 30, dtype=torch.int32, device="cuda")
+    view = wide[:, 4:4 + table.shape[1]]
+    view.copy_(ints(table))
+    q = bf16(rng, 3, T, 4, 64)
+    for a, b in zip(sage.cache_attention(q, gpu, view, ints(lengths), return_lse=True),
+                    sage.cache_attention(q, gpu, ints(table), ints(lengths), return_lse=True)):
+        assert torch.equal(a, b)
+    k, v = sage.cache_read(gpu, view, ints([3, 3, 0]), 290, counts=ints([290, 290, 0]))
+    for b in (0, 1):
+        for got, want in zip((k, v), c.tokens(table[b], 3, 293)):
+            assert torch.equal(got[b].cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16))
+    kk, vv = bf16(rng, 3, 1, 2, 64), bf16(rng, 3, 1, 2, 64)
+    oc.append(c, f32(kk), f32(vv), table, [399, 300, 0], [1, 1, 0])
+    sage.cache_append(gpu, kk, vv, view, ints([399, 300, 0]), counts=ints([1, 1, 0]))
+    same_tokens(gpu, c, table, [400, 301, 0])
 
 
 def test_two_streams_at_once():
