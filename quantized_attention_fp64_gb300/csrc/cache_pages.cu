@@ -167,8 +167,12 @@ __device__ __forceinline__ uint32_t shrink4(uint32_t w, float r) {
 // numbers of tokens and blocks in 64 bits cost another 14. Five CTAs to an SM
 // (48 registers): with six the same call is 1 us quicker, but 64 single tokens
 // take 0.7 us longer; with eight the registers spill (+3 us).
-template <int D>
-__global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
+// kFew: calls of at most a block's tokens, whose time is that of loads that
+// wait for one another. The older tokens' codes, should the scale grow, are
+// asked for before that is known: 64 single tokens, appended and read back,
+// 10.1 -> 9.2 us; in a call of many tokens the registers cost 2 us of 70.
+template <int D, bool kFew>
+__global__ void __launch_bounds__(kThreads, kFew ? 4 : 5) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
                                                                 const int32_t* counts, Bf16In k, Bf16In v, int32_t T,
                                                                 int* dev_err) {
   using L = Tile<D>;
@@ -193,6 +197,20 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, 
     x[q] = make_uint4(0u, 0u, 0u, 0u);
     if (row >= s.first && row < s.end) x[q] = *reinterpret_cast<const uint4*>(src + q * step);
   }
+  int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
+  const int quad = i >> 2, g = i & 3;  // values: channels 4 quad .. + 3, positions 8 g .. + 7
+  // codes of the block's older tokens: of the keys of row e * kRows + row0, of the values of channel 4 quad + e
+  const auto older = [&](int e) {
+    return *reinterpret_cast<const uint2*>(
+        half ? block + (4 * quad + e) * kCacheBlock + 8 * g
+             : block + (ch / 64) * (kCacheBlock * 64) + (e * L::kRows + row0) * 64 + ch % 64);
+  };
+  uint2 was[4];
+  if (kFew && s.first > 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (half ? i < L::kQuads : e < L::kTimes && e * L::kRows + row0 < s.first) was[e] = older(e);
+  }
   // max |x| as bit patterns: those of infinities and NaN are the largest
   uint32_t a = 0;
 #pragma unroll
@@ -213,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, 
   const float shrink = (grew && usable) ? __fdiv_rn(s_old, s_new) : 0.0f;
   if (i == 0) *scale_at = s_new;
   const float inv = __fdiv_rn(1.0f, s_new);
-  int8_t* block = (half ? c.v : c.k) + s.slot * (kCacheBlock * D);
 #pragma unroll
   for (int q = 0; q < L::kTimes; ++q) {
     const int row = q * L::kRows + row0;
@@ -224,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, 
       if (row >= s.first) {
         *p = codes;
       } else if (grew) {
-        const uint2 was = *p;
-        *p = make_uint2(shrink4(was.x, shrink), shrink4(was.y, shrink));
+        const uint2 old = kFew ? was[q] : older(q);
+        *p = make_uint2(shrink4(old.x, shrink), shrink4(old.y, shrink));
       }
     } else {
       *reinterpret_cast<uint2*>(vt + row * L::kPitch + ch) = codes;
@@ -233,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, 
   }
   __syncthreads();
   if (half == 1 && i < L::kQuads) {
-    const int quad = i >> 2, g = i & 3;  // channels 4 quad .. + 3, positions 8 g .. + 7
     uint32_t lo[4], hi[4], w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(vt + value_token(8 * g + e) * L::kPitch + 4 * quad);
@@ -248,15 +264,15 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(CacheView c, 
       uint2 o = make_uint2(lo[e], hi[e]);
       if (s.first > 0) {
         // older tokens' codes stay in the block
-        uint2 was = *p;
-        if (grew) was = make_uint2(shrink4(was.x, shrink), shrink4(was.y, shrink));
+        uint2 old = kFew ? was[e] : older(e);
+        if (grew) old = make_uint2(shrink4(old.x, shrink), shrink4(old.y, shrink));
         uint32_t keep_lo = 0, keep_hi = 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           if (value_token(8 * g + b) < s.first) keep_lo |= 255u << (8 * b);
           if (value_token(8 * g + 4 + b) < s.first) keep_hi |= 255u << (8 * b);
         }
-        o = make_uint2((was.x & keep_lo) | (o.x & ~keep_lo), (was.y & keep_hi) | (o.y & ~keep_hi));
+        o = make_uint2((old.x & keep_lo) | (o.x & ~keep_lo), (old.y & keep_hi) | (o.y & ~keep_hi));
       }
       *p = o;
     }
@@ -491,7 +507,10 @@ dim3 span_grid(const CacheView& c, int64_t B, int64_t T) {
 cudaError_t launch_cache_append(const CacheView& c, int64_t D, const PageTable& pt, const int32_t* starts,
                                 const int32_t* counts, const Bf16In& k, const Bf16In& v, int64_t B, int64_t T,
                                 int* dev_err, cudaStream_t stream) {
-  return launch(D == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, span_grid(c, B, T), kThreads, 0, stream, c,
+  const bool few = T <= kCacheBlock;
+  const auto kernel = D == 128 ? (few ? cache_append_kernel<128, true> : cache_append_kernel<128, false>)
+                               : (few ? cache_append_kernel<64, true> : cache_append_kernel<64, false>);
+  return launch(kernel, span_grid(c, B, T), kThreads, 0, stream, c,
                 pt, starts, counts, k, v, static_cast<int32_t>(T), dev_err);
 }
 
