@@ -32,6 +32,13 @@ SAGE_ERR_DEVICE_PAGE = -16
 BLOCK = 32  # tokens that share a scale
 
 
+_signatures: dict = {}
+
+
+def _signature(*sizes) -> int:
+    return _signatures.setdefault(sizes, len(_signatures))
+
+
 @dataclass(frozen=True, eq=False)
 class QuantizedCache:
     """The cache's four arrays (see sage_cache): one object for all sequences of a layer."""
@@ -46,7 +53,7 @@ class QuantizedCache:
     D: int = field(init=False)
     c: _lib.Cache = field(init=False, repr=False)
     address: int = field(init=False, repr=False)   # of c, which lives as long as the object
-    signature: tuple = field(init=False, repr=False)
+    signature: int = field(init=False, repr=False) # the same for caches of the same sizes on one device
 
     def __post_init__(self):
         ts = (self.k_codes, self.v_codes, self.k_scale, self.v_scale)
@@ -71,7 +78,7 @@ class QuantizedCache:
         for name, value in (("num_pages", P), ("page_size", n * BLOCK), ("H", H), ("D", D)):
             object.__setattr__(self, name, value)
         c = _lib.Cache(*(t.data_ptr() or 16 for t in ts), P, n * BLOCK, H, D)  # an empty array has no address
-        for name, value in (("c", c), ("address", ctypes.addressof(c)), ("signature", (P, n, H, D, self.k_codes.get_device()))):
+        for name, value in (("c", c), ("address", ctypes.addressof(c)), ("signature", _signature(P, n, H, D, self.k_codes.get_device()))):
             object.__setattr__(self, name, value)
 
     @property
@@ -113,23 +120,26 @@ class _on:
 # A call whose shapes, strides, types, devices and flags this thread has seen
 # before skips the checks: the thread keeps one filled argument struct for each
 # such signature and changes only the pointers (answering token by token, a
-# call's host work counts). Per thread, so that no other thread rewrites a struct
-# while the library reads it. Calls that give out or workspace go the full way.
+# call's host work counts; the signatures are written out flat for the same
+# reason). Per thread, so that no other thread rewrites a struct while the
+# library reads it. Calls that give out or workspace go the full way.
 
 
 def _meta(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-def _kept(key):
+def _kept_calls() -> dict:
     calls = getattr(_tls, "cache_calls", None)
-    return None if calls is None else calls.get(key)
+    if calls is None:
+        calls = _tls.cache_calls = {}
+    return calls
 
 
 def _keep(key, value):
-    calls = getattr(_tls, "cache_calls", None)
-    if calls is None or len(calls) > 256:
-        calls = _tls.cache_calls = {}
+    calls = _kept_calls()
+    if len(calls) > 256:
+        calls.clear()
     calls[key] = value
 
 
@@ -206,21 +216,25 @@ def cache_append(cache: QuantizedCache, k, v, page_table, starts, counts=None, t
     last new one in its block are lost, so a sequence may be cut back and written on.
     The pages written must belong to one sequence only."""
     try:
-        key = ("append", cache.signature, _meta(k), _meta(v), _meta(page_table), _meta(starts), _meta(counts), tensor_layout)
-        kept = _kept(key)
+        key = ("append", cache.signature, tensor_layout, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(),
+               v.dtype, v.get_device(), page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
+               starts.shape, starts.stride(), starts.dtype, starts.get_device(), _meta(counts))
+        kept = _kept_calls().get(key)
     except (AttributeError, TypeError):
         key = kept = None
-    if kept is not None and kept[2] == _get_device():
-        args, ref, index = kept
+    if kept is not None and kept[0] == _get_device():
+        index, fn, ref, args, ki, vi = kept
         args.cache = cache.address
         args.table_dev = page_table.data_ptr()
         args.starts_dev = starts.data_ptr()
         if counts is not None:
             args.counts_dev = counts.data_ptr()
-        args.k.ptr_dev = k.data_ptr()
-        args.v.ptr_dev = v.data_ptr()
+        ki.ptr_dev = k.data_ptr()
+        vi.ptr_dev = v.data_ptr()
         args.cuda_stream = _stream_handle(index)
-        _check(_lib.load().sage_cache_append(ref))
+        rc = fn(ref)
+        if rc:
+            _check(rc)
         return
     _check_cache(cache)
     _check_layout(tensor_layout)
@@ -240,7 +254,7 @@ def cache_append(cache: QuantizedCache, k, v, page_table, starts, counts=None, t
         args.cuda_stream = stream
         _check(_lib.load().sage_cache_append(ctypes.byref(args)))
     if key is not None and table[2]:
-        _keep(key, (args, ctypes.byref(args), index))
+        _keep(key, (index, _lib.load().sage_cache_append, ctypes.byref(args), args, args.k, args.v))
 
 
 def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, tensor_layout: str = "NHD", out=None):
@@ -250,23 +264,26 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
     kept = key = None
     if out is None:
         try:
-            key = ("read", cache.signature, T, _meta(page_table), _meta(starts), _meta(counts), tensor_layout)
-            kept = _kept(key)
+            key = ("read", cache.signature, tensor_layout, T, page_table.shape, page_table.stride(), page_table.dtype,
+                   page_table.get_device(), starts.shape, starts.stride(), starts.dtype, starts.get_device(), _meta(counts))
+            kept = _kept_calls().get(key)
         except (AttributeError, TypeError):
             key = None
-    if kept is not None and kept[2] == _get_device():
-        args, ref, index, shape = kept
-        device = page_table.device
-        k, v = torch.empty(shape, dtype=torch.bfloat16, device=device), torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if kept is not None and kept[0] == _get_device():
+        index, fn, ref, args, ko, vo, shape = kept
+        k = torch.empty(shape, dtype=torch.bfloat16, device=page_table.device)
+        v = torch.empty_like(k)
         args.cache = cache.address
         args.table_dev = page_table.data_ptr()
         args.starts_dev = starts.data_ptr()
         if counts is not None:
             args.counts_dev = counts.data_ptr()
-        args.k_out.ptr_dev = k.data_ptr()
-        args.v_out.ptr_dev = v.data_ptr()
+        ko.ptr_dev = k.data_ptr()
+        vo.ptr_dev = v.data_ptr()
         args.cuda_stream = _stream_handle(index)
-        _check(_lib.load().sage_cache_read(ref))
+        rc = fn(ref)
+        if rc:
+            _check(rc)
         return k, v
     _check_cache(cache)
     _check_layout(tensor_layout)
@@ -296,7 +313,7 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
         args.cuda_stream = stream
         _check(_lib.load().sage_cache_read(ctypes.byref(args)))
     if key is not None and table[2]:
-        _keep(key, (args, ctypes.byref(args), index, shape))
+        _keep(key, (index, _lib.load().sage_cache_read, ctypes.byref(args), args, args.k_out, args.v_out, shape))
     return k, v
 
 
@@ -352,13 +369,15 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
     kept = key = None
     if out is None and workspace is None:
         try:
-            key = ("attention", cache.signature, _meta(q), _meta(page_table), _meta(lengths), _meta(q_lengths),
-                   bool(is_causal), bool(return_lse), tensor_layout)
-            kept = _kept(key)
+            key = ("attention", cache.signature, tensor_layout, bool(is_causal), bool(return_lse), q.shape, q.stride(),
+                   q.dtype, q.get_device(), page_table.shape, page_table.stride(), page_table.dtype,
+                   page_table.get_device(), lengths.shape, lengths.stride(), lengths.dtype, lengths.get_device(),
+                   _meta(q_lengths))
+            kept = _kept_calls().get(key)
         except (AttributeError, TypeError):
             key = None
-    if kept is not None and kept[2] == _get_device():
-        args, ref, index, shape, lse_shape, need = kept
+    if kept is not None and kept[0] == _get_device():
+        index, fn, ref, args, qi, oi, shape, lse_shape, need = kept
         device = q.device
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)
         stream = _stream_handle(index)
@@ -367,21 +386,21 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
         args.lengths_dev = lengths.data_ptr()
         if q_lengths is not None:
             args.q_lengths_dev = q_lengths.data_ptr()
-        args.q.ptr_dev = q.data_ptr()
-        args.out.ptr_dev = out.data_ptr()
+        qi.ptr_dev = q.data_ptr()
+        oi.ptr_dev = out.data_ptr()
         args.sm_scale = _NAN if sm_scale is None else float(sm_scale)
         if need:
             workspace = _call_workspace(device, stream, need)
             args.workspace_dev = workspace.data_ptr()
-            args.workspace_bytes = need
         args.cuda_stream = stream
+        lse = None
         if return_lse:
             lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
             args.lse_dev = lse.data_ptr()
-            _check(_lib.load().sage_cache_attention(ref))
-            return out, lse
-        _check(_lib.load().sage_cache_attention(ref))
-        return out
+        rc = fn(ref)
+        if rc:
+            _check(rc)
+        return (out, lse) if return_lse else out
     _check_cache(cache)
     _check_layout(tensor_layout)
     (B, T, H), qi = _tokens(q, cache, tensor_layout, "q")
@@ -429,5 +448,8 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
         args.cuda_stream = stream
         _check(_lib.load().sage_cache_attention(ctypes.byref(args)))
     if key is not None and table[2]:
-        _keep(key, (args, ctypes.byref(args), index, q.shape, (B, H, T), need))
+        if need:
+            args.workspace_bytes = need
+        _keep(key, (index, _lib.load().sage_cache_attention, ctypes.byref(args), args, args.q, args.out, q.shape, (B, H, T),
+                    need))
     return (out, lse) if return_lse else out
