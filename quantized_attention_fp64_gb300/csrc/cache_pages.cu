@@ -367,63 +367,91 @@ __global__ void __launch_bounds__(kThreads, 8) cache_read_kernel(CacheView c, Pa
 // dst of one entry and src of another: the copies would depend on their order.
 // Every CTA checks the whole lists with one bit per page in shared memory
 // before it copies anything, so a list that breaks the rule, or names a page
-// that is not there, moves no byte and sets the device error word. The first
-// bytes are on their way meanwhile. 2000 pages of 64 tokens, 8 heads of 128:
-// 102 us, 5.1 TB/s read and written; 16 such pages of 4 heads: 2.6 us. Chunks of
-// 32768 bytes take as long for many pages and 0.5 us more for few.
-constexpr int kCopyThreads = 256;
-constexpr int kCopyCtas = 4;           // per SM at a time
-constexpr int kCopyWaves = 4;          // grids of 4 to 24 CTAs per SM measure within 3%
-constexpr int kCopyChunk = 16384;      // bytes of codes that one CTA moves at a time
-constexpr int kCopyPieces = kCopyChunk / 16 / kCopyThreads;
-constexpr int kCheckAtOnce = 4;        // entries whose loads a thread has in flight
+// that is not there, moves no byte and sets the device error word.
+// Each warp moves its chunks through shared memory with bulk copies, one after
+// the other; kCopyWarps of them in flight per SM are what HBM needs, and no
+// register holds a byte of them. The first is on its way while the lists are
+// checked. 2000 pages of 64 tokens, 8 heads of 128: 87 us, 6.0 TB/s read and
+// written (102 us through registers, with 64 KB in flight per SM); 16 pages of 4
+// heads: 3.1 us (2.7). 6 warps of 32768 bytes, 12 of 16384 and 24 of 8192
+// measure 88, 86 and 91.
+constexpr int kCopyWarps = 8;
+constexpr int kCopyThreads = 32 * kCopyWarps;
+constexpr int kCopyChunk = 16384;        // bytes of codes that a warp moves at a time
+constexpr int kCopySmall = 4096;       // where there are fewer of them than warps, or no room
+constexpr int kCopyBits = 227 * 1024 - 256 - kCopyWarps * kCopyChunk;
+static_assert(kCopyWarps * kCopySmall + (1 << 17) <= 227 * 1024 - 256, "a bit for each of 2^20 pages");
+constexpr int kCheckAtOnce = 8;        // entries whose loads a thread has in flight
+constexpr uint64_t kCopyTimeoutNs = 2000000000ull;
 
 struct CopyUnit {
-  const uint4* from;  // null: nothing to move
-  uint4* to;
-  int pieces;         // 16-byte pieces
-  int32_t s, d;       // pages
-  int which;          // 0 keys, 1 values
-  bool first;         // the page's first chunk: its scales go with it
+  const int8_t* from;  // null: nothing to move
+  int8_t* to;
+  uint32_t bytes;
+  int32_t s, d;        // pages
+  int which;           // 0 keys, 1 values
+  bool first;          // the page's first chunk: its scales go with it
 };
 
 __device__ __forceinline__ CopyUnit copy_unit(const CacheView& c, const int32_t* src, const int32_t* dst,
-                                              int64_t codes_bytes, int64_t chunks, int64_t u) {
+                                              int64_t codes_bytes, int chunk, int64_t chunks, int64_t u) {
   const int64_t entry = u / (2 * chunks);
-  const int r = static_cast<int>(u - entry * 2 * chunks);
+  const int64_t r = u - entry * 2 * chunks;
   CopyUnit m;
   m.s = src[entry];
   m.d = dst[entry];
   m.which = r >= chunks;
-  const int64_t lo = (r - (m.which ? chunks : 0)) * kCopyChunk;
+  const int64_t lo = (r - (m.which ? chunks : 0)) * chunk;
   m.first = lo == 0;
-  m.pieces = static_cast<int>(min(codes_bytes - lo, static_cast<int64_t>(kCopyChunk)) / 16);
+  m.bytes = static_cast<uint32_t>(min(codes_bytes - lo, static_cast<int64_t>(chunk)));
   int8_t* base = m.which ? c.v : c.k;
   const bool moves = m.d >= 0 && m.d != m.s && page_ok(m.s, c.num_pages);
-  m.from = moves ? reinterpret_cast<const uint4*>(base + m.s * codes_bytes + lo) : nullptr;
-  m.to = reinterpret_cast<uint4*>(base + m.d * codes_bytes + lo);
+  m.from = moves ? base + m.s * codes_bytes + lo : nullptr;
+  m.to = base + m.d * codes_bytes + lo;
   return m;
 }
 
-__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) cache_copy_kernel(CacheView c, const int32_t* src,
-                                                                             const int32_t* dst, int64_t n,
-                                                                             int64_t codes_bytes, int64_t scales,
-                                                                             int64_t chunks, int* dev_err) {
-  extern __shared__ uint32_t taken[];
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(CacheView c, const int32_t* src, const int32_t* dst,
+                                                                  int64_t n, int64_t codes_bytes, int64_t scales,
+                                                                  int chunk, int64_t chunks, int* dev_err) {
+  extern __shared__ __align__(128) uint8_t buffers[];  // a chunk per warp, then a bit per page
+  __shared__ uint64_t landed[kCopyWarps];
+  uint32_t* taken = reinterpret_cast<uint32_t*>(buffers + kCopyWarps * chunk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar = tc::smem_u32(&landed[warp]), buffer = tc::smem_u32(buffers) + static_cast<uint32_t>(warp * chunk);
+  if (lane == 0) {
+    tc::mbar_init(bar, 1);
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int64_t total = n * 2 * chunks;
-  uint4 x[kCopyPieces];
+  const int64_t total = n * 2 * chunks, step = static_cast<int64_t>(gridDim.x) * kCopyWarps;
+  int64_t u = blockIdx.x + static_cast<int64_t>(warp) * gridDim.x;
   const auto fetch = [&](const CopyUnit& m) {
-#pragma unroll
-    for (int y = 0; y < kCopyPieces; ++y) {
-      const int q = threadIdx.x + y * kCopyThreads;
-      if (m.from != nullptr && q < m.pieces) x[y] = m.from[q];
-    }
+    if (lane != 0 || m.from == nullptr) return;
+    tc::fence_proxy_async_global();  // earlier kernels wrote the page
+    tc::mbar_arrive_expect_tx(bar, m.bytes);
+    tc::bulk_load(buffer, m.from, m.bytes, bar);
   };
-  // the first unit's bytes are on their way while the lists are checked
-  CopyUnit m = copy_unit(c, src, dst, codes_bytes, chunks, blockIdx.x);
-  fetch(m);
+  uint32_t phase = 0;
+  const auto wait = [&]() {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !tc::mbar_try_wait(bar, phase & 1u); ++it) {
+      if ((it & 127u) != 0) continue;
+      const uint64_t now = tc::global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kCopyTimeoutNs) return false;
+    }
+    ++phase;
+    return true;
+  };
+  CopyUnit m;
+  m.from = nullptr;
+  if (u < total) {
+    m = copy_unit(c, src, dst, codes_bytes, chunk, chunks, u);
+    fetch(m);
+  }
   const int words = static_cast<int>((c.num_pages + 31) / 32);
   for (int i = threadIdx.x; i < words; i += kCopyThreads) taken[i] = 0u;
   __syncthreads();
@@ -458,25 +486,38 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) cache_copy_kernel(Cac
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) flag_pages(dev_err);
-    return;
+    if (m.from != nullptr && !wait() && lane == 0) atomicExch(dev_err, kDevErrTimeout);
+    return;  // with no copy in flight
   }
-  for (int64_t u = blockIdx.x;;) {
+  while (u < total) {
+    // where the next chunk is, looked up under this one's copy
+    CopyUnit next;
+    next.from = nullptr;
+    if (u + step < total) next = copy_unit(c, src, dst, codes_bytes, chunk, chunks, u + step);
     if (m.from != nullptr) {
-#pragma unroll
-      for (int y = 0; y < kCopyPieces; ++y) {
-        const int q = threadIdx.x + y * kCopyThreads;
-        if (q < m.pieces) m.to[q] = x[y];
-      }
       if (m.first) {
         float* sc = m.which ? c.vs : c.ks;
-        for (int64_t q = threadIdx.x; q < scales; q += kCopyThreads) sc[m.d * scales + q] = sc[m.s * scales + q];
+        for (int64_t q = lane; q < scales; q += 32) sc[m.d * scales + q] = sc[m.s * scales + q];
       }
+      if (!wait()) {
+        if (lane == 0) atomicExch(dev_err, kDevErrTimeout);
+        break;
+      }
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         reinterpret_cast<uint64_t>(m.to)),
+                     "r"(buffer), "r"(m.bytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the buffer has been read
+      }
+      __syncwarp();
     }
-    u += gridDim.x;
-    if (u >= total) break;
-    m = copy_unit(c, src, dst, codes_bytes, chunks, u);
+    u += step;
+    m = next;
     fetch(m);
   }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Launched as a programmatic dependent: the grid may come up while the stream's
@@ -525,13 +566,16 @@ cudaError_t launch_cache_copy_pages(const CacheView& c, int64_t D, const int32_t
                                     int* dev_err, cudaStream_t stream) {
   const int64_t scales = static_cast<int64_t>(c.H) * c.blocks_per_page;
   const int64_t bytes = scales * kCacheBlock * D;
-  const int64_t chunks = div_up(bytes, kCopyChunk);
-  const int smem = static_cast<int>((c.num_pages + 31) / 32 * 4);
+  const int64_t warps = static_cast<int64_t>(sm_count_current()) * kCopyWarps;
+  const int bits = static_cast<int>((c.num_pages + 31) / 32 * 4);
+  const int chunk = n * 2 * div_up(bytes, kCopyChunk) < warps || bits > kCopyBits ? kCopySmall : kCopyChunk;
+  const int64_t chunks = div_up(bytes, chunk);
+  const int smem = kCopyWarps * chunk + bits;
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(cache_copy_kernel), smem);
   if (e != cudaSuccess) return e;
-  const int64_t work = n * 2 * chunks, most = int64_t(kCopyWaves) * kCopyCtas * sm_count_current();
+  const int64_t work = n * 2 * chunks, most = sm_count_current();
   return launch(cache_copy_kernel, dim3(static_cast<unsigned>(work < most ? work : most)), kCopyThreads,
-                static_cast<size_t>(smem), stream, c, src, dst, n, bytes, scales, chunks, dev_err);
+                static_cast<size_t>(smem), stream, c, src, dst, n, bytes, scales, chunk, chunks, dev_err);
 }
 
 }  // namespace sage

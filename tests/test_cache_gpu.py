@@ -275,6 +275,34 @@ def test_copy_pages(H, D, page, P):
         assert np.array_equal(t.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("H,D,page,P,n", [
+    (3, 128, 96, 900, 400),          # chunks that end inside a page, several to a warp
+    (7, 64, 32, 6000, 2900), (1, 64, 32, 1 << 20, 5000),
+    (8, 128, 4096, 12, 5),
+])
+def test_copy_many_pages(H, D, page, P, n):
+    """Sources and targets in no order; every other page keeps its bytes."""
+    gpu = sage.alloc_cache(P, H, "cuda", D=D, page_size=page)
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    gpu.k_codes.view(torch.int32).random_(generator=gen)
+    gpu.v_codes.view(torch.int32).random_(generator=gen)
+    gpu.k_scale.uniform_(generator=gen)
+    gpu.v_scale.uniform_(generator=gen)
+    order = torch.randperm(P, device="cuda", generator=gen).int()
+    src, dst = order[:n].clone(), order[n:2 * n].clone()
+    src[1::7] = src[0]                 # one page to many
+    dst[5::11] = -1                    # and entries that stand for nothing
+    src[3], dst[3] = order[-1], order[-1]
+    live = (dst >= 0) & (dst != src)
+    take = torch.arange(P, device="cuda")
+    take[dst[live].long()] = src[live].long()
+    arrays = (gpu.k_codes, gpu.v_codes, gpu.k_scale, gpu.v_scale)
+    want = [t[take] for t in arrays]
+    sage.cache_copy_pages(gpu, src, dst)
+    for t, w in zip(arrays, want):
+        assert torch.equal(t, w)
+
+
 @pytest.mark.parametrize("src,dst", [
     ([0, 1], [5, 5]), ([0, 5], [5, 6]), ([0, 99], [5, 6]), ([0, -1], [5, 6]), ([0, 1], [5, 8]),
     ([0, 1], [5, 2 ** 31 - 1]), ([0, -2 ** 31], [5, 7]),
