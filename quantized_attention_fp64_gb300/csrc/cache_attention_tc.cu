@@ -34,6 +34,15 @@
 // (value_position), so V^T needs no reordering on the way.
 //
 // Every wait on an mbarrier is bounded, as in attention_tc.cu.
+// Measured (GB300): a causal chunk of 2000 tokens over 16001, 32 heads on 8 of
+// 128: 402 us, 1223 TFLOP/s, 64% of cuBLAS's bf16 rate; the tensor pipe is busy
+// 71% of the cycles (QK with 64 keys is bound by shared memory, which reads Q
+// again for every key tile), and the chain of a key tile's softmax takes the
+// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 96 us, 446
+// TFLOP/s, of which the softmax's chain is 1300 cycles per 64 keys and beginning
+// and ending a unit 4 us of every 20. What was slower: key tiles of 128 without a
+// second buffer of S; S and P apart (404 us); four softmax warpgroups, and eight
+// converter warps (both spill); waiting for keys and P by polling (410).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,7 +59,7 @@ constexpr int kRows = 128;      // rows of a query tile
 constexpr int kKeys = 64;       // keys of a key tile
 constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 constexpr int kMaxSms = 160;
-constexpr int kMinTiles = 8;    // key tiles that are worth a CTA of their own
+constexpr int kMinTiles = 2;    // key tiles that are worth a CTA of their own (64 rows over 1000 tokens, 4 heads: 16 us; with 8, 23)
 constexpr int kWindow = 32;     // key tiles whose pages and scales are looked up together
 constexpr int kWindows = 16;    // lookups that are kept (more than the stages and what lies between)
 constexpr float kLn2 = 0.6931471805599453f;
