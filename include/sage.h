@@ -506,8 +506,8 @@ SAGE_API int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H
  * sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * workspace_dev: sage_cache_attention_workspace_size bytes, 256-byte aligned,
  * contents do not matter; not used by another call at the same time.
- * B * cache->H * (32-token blocks a table row can name), times every started
- * 256 of the T * H / cache->H rows of a key/value head, is below 2^31
+ * B * cache->H * (32-token blocks a table row can name + 16), times every
+ * started 256 of the T * H / cache->H rows of a key/value head, is below 2^31
  * (TOO_LARGE). Scales are not negative (sage_cache_append writes none).
  * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,
  * CUDA; on the device DEVICE_PAGE. */

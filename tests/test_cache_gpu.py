@@ -5,8 +5,10 @@ held to a bound that is derived, not fitted. With A = sum_j p_j |v_j| / sum_j p_
 (in float64), an output differs from the float64 formula on the same codes by at
 most
   2^-8 |o|    the rounding of the output to bf16 (half a step),
-  2^-11 A     the rounding of p to fp16 for the tensor cores,
-  2^-10 A     values scaled to fp16 (the scale's and the product's rounding),
+  2^-11 A     the rounding of p (with many rows: of p times the value scale) to fp16
+              for the tensor cores,
+  2^-10 A     the value scales: their logarithm and what is raised from it, or their
+              product with a fp32 sum (a bound; both err by less),
   2^-12 A     logits: D products accumulated in fp32 err by at most
               (D + 3) 2^-24 sum |q_d k_d| sm_scale < 2^-13.5 here (sum |q k| sm_scale < 10),
               which p and the sum of p each take once,
