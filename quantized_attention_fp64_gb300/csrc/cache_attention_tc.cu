@@ -26,10 +26,13 @@
 // times 64 of S.
 // Numbers. Queries become fp16 times a power of two per row (their largest
 // value in [1, 4)); key and value codes are exact in fp16. The value scales go
-// into the weights: with R the largest value scale of the part's blocks so far
-// (found for 32 key tiles at a time; O is rescaled when it grows), P holds
-// fp16(p s_v / R), a rounding of 2^-12 relative (where p s_v / R is below 2^-14,
-// of 2^-25), and the sum of p is taken in fp32, block by block, times R / s_v.
+// into the weights: with m a row's running maximum of z + log2 s_v (z: the
+// logits times log2 e), P holds fp16(2^(z + log2 s_v - m)), a rounding of 2^-11
+// of the weight (where it is below 2^-14 of the largest, of 2^-25 of that),
+// O = sum P vcode, and the sum of 2^(z - m) is taken in fp32, block by block,
+// from the weights before they are rounded, over s_v. So what a row does not
+// see, whatever its scale, does not touch it. A value scale below 2^-90 counts
+// as 2^-90 here, or the sum would leave fp32.
 // The keys of a block stand in the order in which the values are stored
 // (value_position), so V^T needs no reordering on the way.
 //
@@ -63,8 +66,8 @@ constexpr int kMinTiles = 2;    // key tiles that are worth a CTA of their own (
 constexpr int kWindow = 32;     // key tiles whose pages and scales are looked up together
 constexpr int kWindows = 16;    // lookups that are kept (more than the stages and what lies between)
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 6.0f;     // where the maximum is looked for: p may reach 2^6 before the running one follows
-constexpr float kMost = 4096.0f;  // elsewhere: the sum of a block's p s_v / R may (then some p s_v / R is above 2^7)
+constexpr float kLazy = 6.0f;     // where the maximum is looked for: a weight may reach 2^6 before the running one follows
+constexpr float kMost = 4096.0f;  // elsewhere: the sum of a block's weights may (then some weight is above 2^7)
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kTmemCols = 512;
 
@@ -95,19 +98,19 @@ struct Smem {
 constexpr int kMaxStages = 8, kMaxRaw = 6;
 constexpr int kBarQFull = 0, kBarQEmpty = 2, kBarFull = kBarQEmpty + 2, kBarEmpty = kBarFull + kMaxStages;
 constexpr int kBarSFull = kBarEmpty + kMaxStages, kBarPFull = kBarSFull + 4;
-constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4, kBarTop = kBarDrain + 2;  // SFull, PFull, PVDone: [tile][buffer]
-constexpr int kBarFold = kBarTop + 1;  // the second half of a folded part is in the workspace; it has been read
+constexpr int kBarPVDone = kBarPFull + 4, kBarDrain = kBarPVDone + 4;  // SFull, PFull, PVDone: [tile][buffer]
+constexpr int kBarFold = kBarDrain + 2;  // the second half of a folded part is in the workspace; it has been read
 constexpr int kBarRaw = kBarFold + 2, kBarRawFree = kBarRaw + kMaxRaw;
 constexpr int kNumBars = kBarRawFree + kMaxRaw;
 template <int D, bool kOne>
 struct SmemTail {
   static constexpr uint32_t kOffAbort = Smem<D, kOne>::kOffBar + kNumBars * 8;  // as Ctx::abort_at has it
   static constexpr uint32_t kOffTmem = kOffAbort + 4;
-  static constexpr uint32_t kOffTop = kOffTmem + 4;                    // [2][converter warp] largest value scale
-  static constexpr uint32_t kOffScale = (kOffTop + 2 * kConv * 4 + 15) / 16 * 16;  // [window][tile] two (key scale, log2(s_v / R))
+  // [window][tile] two key scales, two log2 s_v
+  static constexpr uint32_t kOffScale = (kOffTmem + 4 + 15) / 16 * 16;
   static_assert(kOffScale % 16 == 0, "a tile's scales are read as one float4");
-  static constexpr uint32_t kOffTopOf = kOffScale + kWindows * kWindow * 16;      // [window] R, what O is rescaled with
-  static constexpr uint32_t kOffPlan = kOffTopOf + kWindows * 8;    // a sum per warp, then where the CTA's range begins and how the list is cut
+  // a sum per warp, then where the CTA's range begins and how the list is cut
+  static constexpr uint32_t kOffPlan = kOffScale + kWindows * kWindow * 16;
   static constexpr uint32_t kOffRow = kOffPlan + (kThreads / 32 + 8) * 4;                // [unit][256 rows] powers of two of the queries
   // one unit more than of the queries themselves: those are free once the
   // unit's last QK is done, when a softmax thread may still have to read its
@@ -425,13 +428,10 @@ __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64
   return w;
 }
 
-// log2(s_v / R), held above -40, where a weight of it is 0 in fp16 (no value
-// scale: the codes are 0 and any weight will do).
-__device__ __forceinline__ float weight_of_scale(float vs, float top) {
-  return vs == 0.0f ? 0.0f : (vs == vs ? fmaxf(log2f(vs / top), -40.0f) : vs);
-}
+// log2 of a value scale (0: the codes are 0, and any weight will do).
+__device__ __forceinline__ float log_scale(float vs) { return vs == vs ? fmaxf(__log2f(vs), -90.0f) : vs; }
 
-// One block of a row: p s_v / R = 2^(s c + n) of its 32 scores, in fp16, and
+// One block of a row: the weights 2^(s c + n) of its 32 scores, in fp16, and
 // their sum. kMasked: from token lim on they are 0, whatever s and c are.
 template <bool kMasked>
 __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], float c, float n, int lim, uint32_t (&pw)[16]) {
@@ -483,7 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       tc::mbar_init(cx.bar(kBarFull + s), kConv);
       tc::mbar_init(cx.bar(kBarEmpty + s), 2);
     }
-    tc::mbar_init(cx.bar(kBarTop), kConv);
     for (int s = 0; s < L::kRaw; ++s) {
       tc::mbar_init(cx.bar(kBarRaw + s), 1);
       tc::mbar_init(cx.bar(kBarRawFree + s), kConv);
@@ -649,27 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         const Part x = part_at<D>(a, pairs, p);
         place_next(a, p, x.n);
         const int tiles = part_tiles(x, 0);
-        float top = 0.0f;
         Window win[kB];
         for (int j = 0; ok && j < tiles; ++j, ++sent) {
           if (j % kWindow == 0) {
-            float most = 0.0f;
 #pragma unroll
-            for (int b = 0; b < kB; ++b) {
+            for (int b = 0; b < kB; ++b)
               win[b] = load_window<D>(a, x.u.b * a.pt.stride, x.u.h, x.u.len, (x.t + j + lane) * kB + b, &bad_page);
-              if (j + lane < tiles) most = fmaxf(most, win[b].vs);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const float factor = j == 0 || !(most > top) ? 1.0f : top / most;
-            if (j == 0 || most > top) top = most;
-            float n[kB];
-#pragma unroll
-            for (int b = 0; b < kB; ++b) n[b] = weight_of_scale(win[b].vs, top);
-            const uint32_t slot = windows % kWindows;
-            reinterpret_cast<float4*>(smem + T::kOffScale)[slot * kWindow + lane] =
-                make_float4(win[0].ks, win[1].ks, n[0], n[1]);
-            if (lane == 0) reinterpret_cast<float2*>(smem + T::kOffTopOf)[slot] = make_float2(top, factor);
+            reinterpret_cast<float4*>(smem + T::kOffScale)[windows % kWindows * kWindow + lane] =
+                make_float4(win[0].ks, win[1].ks, log_scale(win[0].vs), log_scale(win[1].vs));
             ++windows;
           }
           const int64_t at0 = __shfl_sync(0xffffffffu, win[0].at, j % kWindow);
@@ -702,7 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     constexpr int kLoads = 2 * D / 16 / kConv;
     const int v_ch = ((lane >> 1) & 9) | ((lane >> 1) & 2) << 1 | ((lane >> 1) & 4) >> 1;
     const int v_at = 2 * v_ch + (lane & 1);
-    float* tops = reinterpret_cast<float*>(smem + T::kOffTop);
     bool bad_page = false, ok = true;
     // the tile that is fetched next: tile t of t_end of the unit at `p`
     Place p = first_place(found);
@@ -711,32 +696,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     uint32_t windows = 0, parts = 0;
     Window win{0, -1.0f, 0.0f};
     int64_t at = 0;  // the block's first byte in the codes
-    float top = 0.0f;
     int in_window = 0, head = 0;
-    // R of the next 32 tiles: the largest value scale so far (NaN passes)
-    const auto open_window = [&](bool fresh) {
+    // looks the next 32 tiles up; the softmax's view: key scales (negative: no tokens) and log2 s_v
+    const auto open_window = [&]() {
       win = load_window<D>(a, row_of_table, head, len, (t + lane) * kB + blk, &bad_page);
-      float x = t + lane < t_end ? fmaxf(win.vs, 0.0f) : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      const float* buf = tops + kConv * (windows & 1u);
-      if (lane == 0) {
-        tops[kConv * (windows & 1u) + w] = x;
-        tc::mbar_arrive(cx.bar(kBarTop));
-      }
-      if (!wait_bar_warp(cx, cx.bar(kBarTop), windows & 1u)) ok = false;
-#pragma unroll
-      for (int k = 0; k < kConv; ++k) x = fmaxf(x, buf[k]);
-      const float factor = fresh || !(x > top) ? 1.0f : top / x;
-      if (fresh || x > top) top = x;
-      // the softmax's view: key scales (negative: no tokens) and log2(s_v / R)
-      const uint32_t slot = windows % kWindows;
-      if (share == 0) {
-        float* row = reinterpret_cast<float*>(smem + T::kOffScale) + (slot * kWindow + lane) * 4 + blk;
-        row[0] = win.ks;
-        row[2] = weight_of_scale(win.vs, top);
-      }
-      if (w == 0 && lane == 0) reinterpret_cast<float2*>(smem + T::kOffTopOf)[slot] = make_float2(top, factor);
+      reinterpret_cast<float*>(smem + T::kOffScale)[(windows % kWindows * kWindow + lane) * 4 + 2 * share + blk] =
+          share == 0 ? win.ks : log_scale(win.vs);
       ++windows;
       in_window = 0;
     };
@@ -835,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           len = x.u.len;
           head = x.u.h;
           row_of_table = x.u.b * a.pt.stride;
-          open_window(true);
+          open_window();
           pick();
           // on their way while the queries are brought
           if (!kOne && ok) bring_queries(x.u);
@@ -847,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     };
     const auto advance = [&]() {
       if (++t < t_end) {
-        if (++in_window == kWindow) open_window(false);
+        if (++in_window == kWindow) open_window();
         pick();
         return true;
       }
@@ -929,7 +894,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tO = tmem + lane_addr + C::o(i);
     const float4* scales = reinterpret_cast<const float4*>(smem + T::kOffScale);
-    const float2* tops = reinterpret_cast<const float2*>(smem + T::kOffTopOf);
     const int rr = i * kRows + wq * 32 + lane;  // this thread's row of a pair
     bool ok = true;
     uint32_t steps = 0, windows = 0, parts = 0;  // key tiles of this query tile; the converters' windows and units
@@ -955,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         all_see = __reduce_min_sync(0xffffffffu, real ? sees : 0x7fffffff);
         n = fold ? (part_tiles(x, 0) + 1 - i) >> 1 : part_tiles(x, i);
       }
-      float m = -INFINITY, l = 0.0f, f = 0.0f, top = 0.0f;
+      float m = -INFINITY, l = 0.0f, f = 0.0f;
       const float* rows = reinterpret_cast<const float*>(smem + T::kOffRow) + (parts % T::kRowUnits) * 2 * kRows;
       for (int j = 0; ok && j < n; ++j) {
         const uint32_t st = steps + static_cast<uint32_t>(j);
@@ -968,13 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         const int jj = fold ? 2 * j + i : j;  // key tile of the part
         const uint32_t win = (windows + static_cast<uint32_t>(jj) / kWindow) % kWindows;
         const float4 sc = scales[win * kWindow + static_cast<uint32_t>(jj) % kWindow];
-        const bool opens = (jj & ~fold) % kWindow == 0;
-        float factor = 1.0f;  // what O is rescaled with because R grew
-        if (opens) {
-          if (j == 0) f = rows[fold ? rr & (kRows - 1) : rr] * a.sm_log2;
-          top = tops[win].x;
-          factor = tops[win].y;
-        }
+        if (j == 0) f = rows[fold ? rr & (kRows - 1) : rr] * a.sm_log2;
         tc::tmem_wait_ld();
         const int key0 = (max(p.at - kBegin<D>, 0) + jj) * kKeys;
         float cb[kB];
@@ -994,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             for (int c = 0; c < 32; ++c)
               if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
         }
-        // p s_v / R, whose sum over a block is taken back to that of p. First
+        // The weights, whose sum over a block is taken back to that of p. First
         // with the running maximum as it is; that stands unless some row's sum
         // shows a weight above 2^7 (or a row has seen no key yet). The search
         // for the maximum, 34 instructions on a busy pipe, is left to the tiles
@@ -1003,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         // without.
         uint32_t pw[kB][16];
         float sum[kB];
-        const bool plain = j > 0 && !masked && factor == 1.0f;
+        const bool plain = j > 0 && !masked;
         if (plain) {
 #pragma unroll
           for (int b = 0; b < kB; ++b)
@@ -1021,9 +979,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             }
             m0 = max3(m0, __uint_as_float(sr[b][30]), __uint_as_float(sr[b][31]));
             m0 = fmaxf(m0, m1);
-            mt = fmaxf(mt, m0 == -INFINITY ? m0 : m0 * cb[b]);
+            mt = fmaxf(mt, m0 == -INFINITY ? m0 : fmaf(m0, cb[b], b == 0 ? sc.z : sc.w));
           }
-          if (__any_sync(0xffffffffu, mt > m + kLazy) || factor != 1.0f) {
+          if (__any_sync(0xffffffffu, mt > m + kLazy)) {
             const float up = fmaxf(m, mt);
             const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
             m = up;
@@ -1031,8 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             if (j > 0) {
               if (!(ok = wait_pv(st - 1u))) break;  // O is at rest
               tc::tc_fence_after();
-              const float y = alpha * factor;
-              const float2 a2 = make_float2(y, y);
+              const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
@@ -1106,8 +1063,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             tc::tmem_ld32(tO + 32u * cc, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[k]) * top);
-#pragma unroll
             for (int k = 0; k < 4; ++k) store32(half + 32 * cc + 8 * k, o + 8 * k);
           }
           __threadfence_block();
@@ -1128,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
       if (!real) l = s_other = 0.0f;
       const bool none = n == 0 || !real;
       // l = 0: no key was seen
-      const float scale = none || l == 0.0f || s_own == 0.0f ? 0.0f : (whole ? top / l : top) * s_own;
+      const float scale = none || l == 0.0f || s_own == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f) * s_own;
       if (s_other != 0.0f && whole) s_other /= l;
       const bool wide = ((reinterpret_cast<uintptr_t>(a.out.p) | ((a.out.sb | a.out.ss | a.out.sh) << 1)) & 31) == 0;
       uint16_t* dst = a.out.p + u.b * a.out.sb + tok * a.out.ss + head * a.out.sh;

@@ -322,9 +322,9 @@ def test_copy_refuses_whole_lists(src, dst):
 # ---------------------------------------------------------------- attention --
 
 
-def close(out, lse, ref_o, ref_lse, weight):
+def close(out, lse, ref_o, ref_lse, weight, extra=0.0):
     o = f32(out).astype(np.float64)
-    tol = 2.0 ** -8 * np.abs(ref_o) + 2.0 ** -9 * weight + 1e-30
+    tol = 2.0 ** -8 * np.abs(ref_o) + 2.0 ** -9 * weight + 1e-30 + extra
     bad = ~(np.abs(o - ref_o) <= tol)
     assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4].tolist(), float(np.nanmax(np.abs(o - ref_o) / tol)))
     if lse is not None:
@@ -489,6 +489,67 @@ def test_attention_nan_stays_with_the_rows_that_see_it(T):
     assert torch.equal(out[1, :, 2:], clean[1, :, 2:])
     if first > 0:
         assert torch.equal(out[1, :first, :2], clean[1, :first, :2])
+
+
+def lost_weights(c, q, table, lengths, q_lengths, sm):
+    """What fp16 weights that hold the value scales may lose, [B, T, H, 1] float64. With many rows the
+    weights p_j s_j are scaled so that the largest is at least 1, and one below 2^-14 is rounded to a
+    multiple of 2^-24: by at most 2^-25 of the largest. Codes are at most 127, so over n keys the sum
+    errs by at most 127 n 2^-25 max_j p_j s_j / sum_j p_j."""
+    B, T, H, _ = q.shape
+    lost = np.zeros((B, T, H, 1))
+    for b in range(B):
+        n = int(lengths[b])
+        k, _ = c.tokens(table[b], 0, n)
+        s = np.stack([c.v_scale[c.at(table[b], pos)[0], :, c.at(table[b], pos)[1]] for pos in range(n)]).astype(np.float64)
+        sees = np.clip(n - q_lengths[b] + 1 + np.arange(T), 0, n)
+        for h in range(H):
+            z = q[b, :, h].astype(np.float64) @ k[:, h // (H // c.H)].T * sm
+            z[np.arange(n)[None, :] >= sees[:, None]] = -np.inf
+            p = np.exp(z - z.max(1, keepdims=True))
+            lost[b, :, h, 0] = 127 * n * 2.0 ** -25 * (p * s[:, h // (H // c.H)]).max(1) / p.sum(1)
+    return lost
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 6, 40, 200])
+def test_attention_value_scales_far_apart(T, D):
+    """Small values next to huge ones: what a row does not see, or gives no weight, costs it no precision."""
+    rng = np.random.default_rng(27)
+    H, Hkv, page = 4, 2, 64
+    n = 900 + T
+    table, P = make_table(rng, [n, n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    for pos in range(0, n, 32):
+        for b, e in ((0, 1e-6 if pos < 900 else 1e6), (1, 10.0 ** ((pos // 32 * 5) % 13 - 6))):
+            pg, blk = c.at(table[b], pos)
+            c.v_scale[pg, :, blk] *= e
+    q = bf16(rng, 2, T, H, D)
+    sm = 1 / math.sqrt(D)
+    for lengths in ([n, n], [900, 900]):  # and without the huge tokens of sequence 0
+        out, lse = sage.cache_attention(q, upload(c), ints(table), ints(lengths), is_causal=True, return_lse=True)
+        extra = lost_weights(c, f32(q), table, lengths, [T, T], sm) if T * H // Hkv > 32 else 0.0
+        close(out, lse, *oc.attention(c, f32(q), table, lengths, [T, T], True, sm), extra)
+
+
+def test_attention_unseen_tokens_do_not_matter():
+    """Rows of a chunk before a block of huge values, in the same call and the same key tiles."""
+    rng = np.random.default_rng(28)
+    H, Hkv, D, page, n, T = 4, 1, 128, 64, 640, 300
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    q = bf16(rng, 1, T, H, D)
+    as_before = c.v_scale.copy()
+    for pos in range(480, n, 32):
+        pg, blk = c.at(table[0], pos)
+        c.v_scale[pg, :, blk] *= 1e7
+    out, lse = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=True, return_lse=True)
+    ref = oc.attention(c, f32(q), table, [n], [T], True, 1 / math.sqrt(D))
+    # rows t < 140 see the keys up to 339 + t, none of them huge
+    close(out, lse, *ref, lost_weights(c, f32(q), table, [n], [T], 1 / math.sqrt(D)))
+    c.v_scale[:] = as_before
+    small = oc.attention(c, f32(q), table, [n], [T], True, 1 / math.sqrt(D))
+    assert np.array_equal(small[0][:, :140], ref[0][:, :140])
 
 
 @pytest.mark.parametrize("T", [1, 6, 140])
