@@ -28,9 +28,14 @@
 // head) are the 16 rows of m16n8k16 products. Queries become fp16 times a power
 // of two per row (their largest value lies in [1, 4), so a bf16 value keeps its
 // 8 bits down to 2^-16 of it, and errs by 2^-25 of it below), key codes are
-// exact in fp16, sums are fp32. p is rounded to fp16 (2^-11 relative) and
-// multiplied with the exact codes of the values; the block's value scale
-// multiplies the fp32 products.
+// exact in fp16, sums are fp32. The value scale of a block goes into its
+// weights: with m a row's running maximum of z + log2 s_v (z: the logits times
+// log2 e), the weights 2^(z + log2 s_v - m) are rounded to fp16 (by 2^-11 of
+// themselves, or of what is below 2^-14 of the largest by 2^-25 of that) and
+// multiplied with the exact codes; the sum of 2^(z - m) is taken in fp32, block
+// by block, from the weights before they are rounded, over s_v. So a key of
+// little weight and large values keeps its share. A value scale below 2^-90
+// counts as 2^-90, or that sum would leave fp32.
 // Measured (GB300, head dimension 128): one token each of 64 sequences of 900 to
 // 8192, 32 heads on 8: 105 us, 5.7 TB/s of 6.8; two of about 131000 tokens, 28
 // heads on 4: 51 us, 4.9 TB/s (the start, the uneven ends of the CTAs and the
@@ -48,7 +53,7 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
-constexpr float kLazy = 8.0f;                   // p may reach 2^8 before the running maximum follows
+constexpr float kLazy = 8.0f;                   // a weight may reach 2^8 before the running maximum follows
 
 // ---------------------------------------------------------------- the plan --
 
@@ -149,6 +154,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int*
     }
   }
 }
+
+// log2 of a value scale (0: the codes are 0, and any weight will do).
+__device__ __forceinline__ float log_scale(float vs) { return vs == vs ? fmaxf(__log2f(vs), -90.0f) : vs; }
 
 // ------------------------------------------------------------------ decode --
 
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         tc::bulk_load(dst, a.c.k + at_codes, L::kBlockBytes, bar);
         tc::bulk_load(dst + L::kBlockBytes, a.c.v + at_codes, L::kBlockBytes, bar);
       }
-      scales[into] = at_scales;
+      scales[into] = make_float2(at_scales.x, log_scale(at_scales.y));
       if (at_codes >= 0) tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
       else tc::mbar_arrive(bar);
     }
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         tc::bulk_load(dst, a.c.k + at_codes, L::kBlockBytes, bar);
         tc::bulk_load(dst + L::kBlockBytes, a.c.v + at_codes, L::kBlockBytes, bar);
       }
-      scales[lane] = at_scales;
+      scales[lane] = make_float2(at_scales.x, log_scale(at_scales.y));
       if (at_codes >= 0) tc::mbar_arrive_expect_tx(bar, 2 * L::kBlockBytes);
       else tc::mbar_arrive(bar);
     }
@@ -484,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
             qs[((mt * kHalves + i) * 4 + x) * 32] = make_uint4(qf[i][x][0], qf[i][x][1], qf[i][x][2], qf[i][x][3]);
     }
     __syncthreads();
-    float2 o[MT][D / 8][2], l[MT][2];  // rows g and g + 8: channels 8x + 2t, + 1; sums of even and odd keys
+    float2 o[MT][D / 8][2];  // rows g and g + 8: channels 8x + 2t, + 1
+    float l[MT][2];          // and the sum of this lane's keys
     float m[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) o[mt][x][e] = make_float2(0.0f, 0.0f);
-        l[mt][e] = make_float2(0.0f, 0.0f);
+        l[mt][e] = 0.0f;
         m[mt][e] = -INFINITY;
       }
     // this warp's blocks of the segment: CTA units that are warp mod 8
@@ -543,9 +552,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
                 if (key0 + 8 * j + 2 * t + (x & 1) >= sees[mt][x >> 1]) z[mt][j][x] = -INFINITY;
         }
         uint32_t pf[MT][2][4];
+        // a number in any case: where the scale is NaN so are the weights of the rows that see the block
+        const float unscale = ex2(-fmaxf(sc.y, -90.0f));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          // logits are z * c with c >= 0, so the largest z gives the largest logit
+          // logits are z * c with c >= 0, so the largest z gives the largest of a block
           float c[2], mx[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
             y = fmaxf(y, z[mt][3][2 * e + 1]);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            mx[e] = y == -INFINITY ? y : y * c[e];
+            mx[e] = y == -INFINITY ? y : fmaf(y, c[e], sc.y);
           }
           if (__any_sync(0xffffffffu, mx[0] > m[mt][0] + kLazy || mx[1] > m[mt][1] + kLazy)) {
             float alpha[2];
@@ -565,22 +576,22 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
               const float up = fmaxf(m[mt][e], mx[e]);
               alpha[e] = up == -INFINITY ? 1.0f : ex2(m[mt][e] - up);
               m[mt][e] = up;
-              l[mt][e].x *= alpha[e];
-              l[mt][e].y *= alpha[e];
+              l[mt][e] *= alpha[e];
             }
 #pragma unroll
             for (int x = 0; x < D / 8; ++x)
 #pragma unroll
               for (int e = 0; e < 2; ++e) o[mt][x][e] = __fmul2_rn(o[mt][x][e], make_float2(alpha[e], alpha[e]));
           }
-          const float ref[2] = {m[mt][0] == -INFINITY ? 0.0f : m[mt][0], m[mt][1] == -INFINITY ? 0.0f : m[mt][1]};
+          const float add[2] = {sc.y - (m[mt][0] == -INFINITY ? 0.0f : m[mt][0]),
+                                sc.y - (m[mt][1] == -INFINITY ? 0.0f : m[mt][1])};
           float2 p[4][2];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float2 y = __ffma2_rn(make_float2(z[mt][j][2 * e], z[mt][j][2 * e + 1]), make_float2(c[e], c[e]),
-                                          make_float2(-ref[e], -ref[e]));
+                                          make_float2(add[e], add[e]));
               p[j][e] = make_float2(ex2(y.x), ex2(y.y));
             }
           if (masked) {
@@ -593,16 +604,18 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
                 if (key0 + 8 * j + 2 * t + 1 >= sees[mt][e]) p[j][e].y = 0.0f;
               }
           }
+          float2 sum[2] = {p[0][0], p[0][1]};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              l[mt][e] = __fadd2_rn(l[mt][e], p[j][e]);
+              if (j > 0) sum[e] = __fadd2_rn(sum[e], p[j][e]);
               pf[mt][j >> 1][(j & 1) * 2 + e] = pack_half2(p[j][e].x, p[j][e].y);
             }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[mt][e] = fmaf(sum[e].x + sum[e].y, unscale, l[mt][e]);
         }
-        // a block that a row does not reach adds nothing to it, whatever its scale is
-        float vs[MT][2], off[MT][2];
+        float off[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           // what the values' bias adds: the sum of the rounded p, as a product with ones
@@ -611,8 +624,6 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
           mma16816(d, pf[mt][1], 0x3C003C00u, 0x3C003C00u);
           off[mt][0] = -kBias * d[0];
           off[mt][1] = -kBias * d[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) vs[mt][e] = key0 < sees[mt][e] ? sc.y : 0.0f;
         }
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {
@@ -627,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
             mma16816(d, pf[mt][1], b[2], b[3]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              o[mt][x][e] = __ffma2_rn(make_float2(d[2 * e], d[2 * e + 1]), make_float2(vs[mt][e], vs[mt][e]), o[mt][x][e]);
+              o[mt][x][e] = __fadd2_rn(o[mt][x][e], make_float2(d[2 * e], d[2 * e + 1]));
           }
         }
       }
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float y = l[mt][e].x + l[mt][e].y;
+        float y = l[mt][e];
         y += __shfl_xor_sync(0xffffffffu, y, 1);
         y += __shfl_xor_sync(0xffffffffu, y, 2);
         if (t == 0) ml[warp * 16 * MT + mt * 16 + e * 8 + g] = make_float2(m[mt][e], y);

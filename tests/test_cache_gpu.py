@@ -5,10 +5,9 @@ held to a bound that is derived, not fitted. With A = sum_j p_j |v_j| / sum_j p_
 (in float64), an output differs from the float64 formula on the same codes by at
 most
   2^-8 |o|    the rounding of the output to bf16 (half a step),
-  2^-11 A     the rounding of p (with many rows: of p times the value scale) to fp16
-              for the tensor cores,
-  2^-10 A     the value scales: their logarithm and what is raised from it, or their
-              product with a fp32 sum (a bound; both err by less),
+  2^-11 A     the rounding of p times the value scale to fp16 for the tensor cores,
+  2^-10 A     the value scales: their logarithm and what is raised from it (a bound;
+              they err by less),
   2^-12 A     logits: D products accumulated in fp32 err by at most
               (D + 3) 2^-24 sum |q_d k_d| sm_scale < 2^-13.5 here (sum |q k| sm_scale < 10),
               which p and the sum of p each take once,
@@ -492,7 +491,7 @@ def test_attention_nan_stays_with_the_rows_that_see_it(T):
 
 
 def lost_weights(c, q, table, lengths, q_lengths, sm):
-    """What fp16 weights that hold the value scales may lose, [B, T, H, 1] float64. With many rows the
+    """What fp16 weights that hold the value scales may lose, [B, T, H, 1] float64. The
     weights p_j s_j are scaled so that the largest is at least 1, and one below 2^-14 is rounded to a
     multiple of 2^-24: by at most 2^-25 of the largest. Codes are at most 127, so over n keys the sum
     errs by at most 127 n 2^-25 max_j p_j s_j / sum_j p_j."""
@@ -528,8 +527,32 @@ def test_attention_value_scales_far_apart(T, D):
     sm = 1 / math.sqrt(D)
     for lengths in ([n, n], [900, 900]):  # and without the huge tokens of sequence 0
         out, lse = sage.cache_attention(q, upload(c), ints(table), ints(lengths), is_causal=True, return_lse=True)
-        extra = lost_weights(c, f32(q), table, lengths, [T, T], sm) if T * H // Hkv > 32 else 0.0
+        extra = lost_weights(c, f32(q), table, lengths, [T, T], sm)
         close(out, lse, *oc.attention(c, f32(q), table, lengths, [T, T], True, sm), extra)
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_attention_little_weight_large_values(T):
+    """The tokens that the rows give 2^-22 of the weight hold values 2^22 times larger."""
+    rng = np.random.default_rng(29)
+    H, Hkv, D, page, n = 2, 1, 64, 64, 6144
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    q = np.ones((1, T, H, D), np.float32)
+    c.k_codes[:] = np.sign(c.k_codes) + (c.k_codes == 0)
+    for pos in range(0, n, 32):
+        pg, blk = c.at(table[0], pos)
+        k, v = (x.copy() for x in c.block_codes(pg, blk))
+        low = pos // 128 % 2 == 1  # every other block of each warp that takes every fourth
+        # keys whose product with the queries is 64 s_k or -64 s_k, give or take one channel
+        k[:] = -1 if low else 1
+        k[np.arange(k.shape[0]), :, np.arange(k.shape[0]) % D] *= -1
+        c.set_block_codes(pg, blk, k, v)
+        c.k_scale[pg, :, blk] = 15.38 / 124  # logits of 7.69 and -7.69: weights of 3.5 steps of fp16 below its normal numbers
+        c.v_scale[pg, :, blk] = 2.0 ** 22 / 40 if low else 1.0 / 40
+    out, lse = sage.cache_attention(torch.from_numpy(q).to(torch.bfloat16).cuda(), upload(c), ints(table), ints([n]),
+                                    return_lse=True, sm_scale=1.0)
+    close(out, lse, *oc.attention(c, q, table, [n], [T], False, 1.0))
 
 
 def test_attention_unseen_tokens_do_not_matter():
