@@ -966,8 +966,8 @@ size_t cache_attention_workspace_bytes(int64_t, int64_t T, int64_t H, int64_t Hk
 }
 
 // By the rows of a key/value head (14 x 20000 tokens, 8 heads of 128, us): up to
-// 16 one row tile, 98 (8 rows) and 104 (16); up to 32 two, 149; more on the tcgen05
-// tensor cores, 176 (40 rows) to 186 (128) and 257 (256). Its 128-row tiles take
+// 16 one row tile, 98 (8 rows) and 104 (16); up to 32 two, 148; more on the tcgen05
+// tensor cores, 169 (40 rows) to 180 (128) and 257 (256). Its 128-row tiles take
 // as long for 20 rows as for 40, and four row tiles have no registers.
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream) {
   const int64_t rows = a.T * (a.H / a.c.H);

@@ -58,12 +58,20 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 // Eight codes, rint(x / s) with the division correctly rounded, from eight
 // BF16 values. Instead of dividing eight times: with inv = 1 / s rounded once,
-// y = x * inv is within two steps of x / s, y + (x - y s) inv within one, and
-// the same correction of that is x / s correctly rounded (Markstein's theorem:
-// the residual of a quotient within one step is exact under a fused
-// multiply-add, and inv is correctly rounded). The theorem wants no residual
-// below the range: [kScaleLow, kScaleHigh] keeps it there; other scales divide.
-// Adding 1.5 * 2^23 leaves the rounded integer in the low byte.
+// y = x * inv is within 2^-23 of x / s (relative), and y + (x - y s) inv rounds
+// a number within 2^-46 of it; the same once more is x / s correctly rounded
+// (Markstein's theorem: inv is correctly rounded, and the residual of a quotient
+// within one step is exact under a fused multiply-add).
+// Once is enough for the code unless s, a 24-bit integer times a power of two,
+// is within 7 of a multiple of 2^17: codes turn at h = H / 2 plus or minus half
+// a step of fp32 there (H odd, below 2^8), that is at (H 2^t +- 1) / 2^(t + 1),
+// t >= 17. For x = X 2^a (X < 2^8) and s = S 2^b to fall within 2^-46 of that,
+// |X 2^n - (H 2^t +- 1) S| < 2^-46 2^49 = 8 with X 2^n above 2^47, so a multiple
+// of 2^39, hence S within 7 of a multiple of 2^t. (All scales of a block's
+// values are one, so this is asked once.)
+// The theorem wants no residual below the range: [kScaleLow, kScaleHigh] keeps
+// it there; other scales divide. Adding 1.5 * 2^23 leaves the rounded integer in
+// the low byte.
 constexpr float kScaleLow = 0x1p-90f, kScaleHigh = 0x1p+100f;
 
 __device__ __forceinline__ uint2 quantize8(const uint4& x, float s, float inv) {
@@ -71,15 +79,23 @@ __device__ __forceinline__ uint2 quantize8(const uint4& x, float s, float inv) {
   uint32_t m[8];
   if (s >= kScaleLow && s <= kScaleHigh) {
     const uint64_t magic = pair(12582912.0f, 12582912.0f), inv2 = pair(inv, inv), minus_s = pair(-s, -s);
+    uint64_t y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint64_t v = pair(bf16_lo(w[e]), bf16_hi(w[e]));
-      uint64_t y = mul2(v, inv2);
-      y = fma2(fma2(y, minus_s, v), inv2, y);
-      y = fma2(fma2(y, minus_s, v), inv2, y);
-      y = add2(y, magic);
-      m[2 * e] = static_cast<uint32_t>(y);
-      m[2 * e + 1] = static_cast<uint32_t>(y >> 32);
+      y[e] = mul2(v, inv2);
+      y[e] = fma2(fma2(y[e], minus_s, v), inv2, y[e]);
+    }
+    if (((__float_as_uint(s) + 32u) & 0xFFFFu) < 64u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = fma2(fma2(y[e], minus_s, pair(bf16_lo(w[e]), bf16_hi(w[e]))), inv2, y[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = add2(y[e], magic);
+      m[2 * e] = static_cast<uint32_t>(y[e]);
+      m[2 * e + 1] = static_cast<uint32_t>(y[e] >> 32);
     }
   } else {
 #pragma unroll
@@ -161,7 +177,7 @@ __device__ __forceinline__ uint32_t shrink4(uint32_t w, float r) {
 
 // ------------------------------------------------------------------ append --
 // One CTA writes one block of one head: threads 0..127 its keys, 128..255 its
-// values. A call of many tokens is bound by instructions more than by HBM: 70
+// values. A call of many tokens is bound by instructions more than by HBM: 69
 // us for 16 sequences of up to 4096 tokens, 8 heads of 128, where the bytes
 // alone take 45; with eight plain divisions a thread it was 118, and the
 // numbers of tokens and blocks in 64 bits cost another 14. Five CTAs to an SM
@@ -170,7 +186,7 @@ __device__ __forceinline__ uint32_t shrink4(uint32_t w, float r) {
 // kFew: calls of at most a block's tokens, whose time is that of loads that
 // wait for one another. The older tokens' codes, should the scale grow, are
 // asked for before that is known: 64 single tokens, appended and read back,
-// 10.1 -> 9.2 us; in a call of many tokens the registers cost 2 us of 70.
+// 10.1 -> 9.2 us; in a call of many tokens the registers cost 2 us of 69.
 template <int D, bool kFew>
 __global__ void __launch_bounds__(kThreads, kFew ? 4 : 5) cache_append_kernel(CacheView c, PageTable pt, const int32_t* starts,
                                                                 const int32_t* counts, Bf16In k, Bf16In v, int32_t T,

@@ -203,6 +203,22 @@ def test_append_quotients_at_and_next_to_ties(D):
     oc.append(c, f32(k), f32(v), table, [0], [n])
     sage.cache_append(gpu, k, v, ints(table), ints([0]))
     same_tokens(gpu, c, table, [n])
+    # scales that a block already has, next to those where quotients come nearest to a turn: older
+    # tokens keep the scale, and the new values' quotients by it are halves give or take a step of fp32
+    scales = np.array([1 - 2.0 ** -24, 1 + 2.0 ** -23, 3 - 2.0 ** -22, 3 * (1 + 2.0 ** -23), 2 - 2.0 ** -20, 1 + 33 * 2.0 ** -23,
+                       5 + 2.0 ** -21, 1 + 2.0 ** -18, 1 - 2.0 ** -19, 7 * (1 - 2.0 ** -22)], np.float32)
+    c.k_scale[table[0, :5]] = c.v_scale[table[0, :5]] = scales.reshape(5, 1, 2)
+    gpu.k_scale.copy_(torch.from_numpy(c.k_scale))
+    gpu.v_scale.copy_(torch.from_numpy(c.v_scale))
+    for i in range(10):
+        s = float(scales[i])
+        x = np.ldexp(rng.integers(1, 256, (1, 31, 2, D)).astype(float), rng.integers(-3, 2, (1, 31, 2, D)))
+        x = np.minimum(x, np.floor(100 * s)) * rng.choice([-1, 1], x.shape)
+        k = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()
+        v = k.flip(3).contiguous()
+        oc.append(c, f32(k), f32(v), table, [32 * i + 1], [31])
+        sage.cache_append(gpu, k, v, ints(table), ints([32 * i + 1]))
+    same_tokens(gpu, c, table, [320])
 
 
 def test_append_strided_inputs_and_untouched_rest():
