@@ -11,7 +11,10 @@ most
   2^-12 A     logits: D products accumulated in fp32 err by at most
               (D + 3) 2^-24 sum |q_d k_d| sm_scale < 2^-13.5 here (sum |q k| sm_scale < 10),
               which p and the sum of p each take once,
-together below 2^-8 |o| + 2^-9 A. The log-sum-exp errs by the logits' 2^-13.5 and
+together below 2^-8 |o| + 2^-9 A. (Up to 32 rows of a key/value head the products
+are of the codes plus 1152, whose share is taken off again: four roundings of 2^-23
+of 1152 sum p s_v at most, below 2^-12 A where the codes are not nearly all 0; there
+2^-10 of the largest scale bounds it, see the test of empty channels.) The log-sum-exp errs by the logits' 2^-13.5 and
 some roundings of numbers below 16 (2^-20 each): 2^-13 in all.
 """
 
@@ -569,6 +572,21 @@ def test_attention_little_weight_large_values(T):
     out, lse = sage.cache_attention(torch.from_numpy(q).to(torch.bfloat16).cuda(), upload(c), ints(table), ints([n]),
                                     return_lse=True, sm_scale=1.0)
     close(out, lse, *oc.attention(c, q, table, [n], [T], False, 1.0))
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 8, 40])
+def test_attention_empty_channels(T):
+    """Channels whose codes are all 0, as in a padded head dimension."""
+    rng = np.random.default_rng(30)
+    H, Hkv, D, page, n = 8, 1, 128, 64, 3000
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    c.v_codes[:, :, :, 96:] = 0
+    q = bf16(rng, 1, T, H, D)
+    out = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=True)
+    ref = oc.attention(c, f32(q), table, [n], [T], True, 1 / math.sqrt(D))
+    close(out[..., :96], None, *(x[..., :96] if x.ndim == 4 else x for x in ref))
+    assert out[..., 96:].abs().max().item() <= 2.0 ** -10 * c.v_scale.max()
 
 
 def test_attention_unseen_tokens_do_not_matter():
