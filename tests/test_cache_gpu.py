@@ -394,6 +394,11 @@ ATTENTION = [
     (4, 4, 128, 64, [20, 300], None, 300, True),                        # more queries than tokens
     (2, 2, 64, 32, [(61 * i) % 500 for i in range(90)], [(37 * i) % 291 for i in range(90)], 290, True),
     (3, 1, 128, 64, [1500, 40, 0, 2300], [190, 10, 190, 0], 190, False),
+    # more sequences than threads in a CTA
+    (2, 1, 64, 32, [(7 * i) % 90 for i in range(1500)], None, 1, True),
+    (5, 1, 64, 32, [(7 * i) % 90 for i in range(1300)], [i % 5 for i in range(1300)], 4, True),
+    (4, 1, 64, 32, [(11 * i) % 120 for i in range(700)], [i % 41 for i in range(700)], 40, False),
+    (2, 2, 64, 32, [(11 * i) % 120 for i in range(600)], [(3 * i) % 131 for i in range(600)], 130, True),
     # calls whose blocks are cut evenly over the GPU, items shared by CTAs and CTAs by items
     (14, 2, 128, 64, [9001, 10, 0, 4000], None, 1, True),
     (4, 1, 64, 128, [10000, 33], [3, 2], 3, True),
@@ -572,6 +577,30 @@ def test_attention_little_weight_large_values(T):
     out, lse = sage.cache_attention(torch.from_numpy(q).to(torch.bfloat16).cuda(), upload(c), ints(table), ints([n]),
                                     return_lse=True, sm_scale=1.0)
     close(out, lse, *oc.attention(c, q, table, [n], [T], False, 1.0))
+
+
+@pytest.mark.parametrize("e", [-100, -30, 60, 110])
+@pytest.mark.parametrize("T", [1, 20, 150])
+def test_attention_queries_of_any_size(T, e):
+    """Queries times 2^e and sm_scale times 2^-e: the same logits, and fp16 holds neither."""
+    rng = np.random.default_rng(37)
+    H, Hkv, D, page, n = 2, 2, 64, 64, 500
+    table, P = make_table(rng, [n], page)
+    gpu = upload(random_cache(rng, P, Hkv, D, page))
+    q = bf16(rng, 1, T, H, D)
+    a = sage.cache_attention(q, gpu, ints(table), ints([n]), is_causal=True, sm_scale=0.125, return_lse=True)
+    b = sage.cache_attention((q.double() * 2.0 ** e).to(torch.bfloat16), gpu, ints(table), ints([n]), is_causal=True,
+                             sm_scale=0.125 * 2.0 ** -e, return_lse=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("T", [1, 3, 9, 100])
+def test_attention_fresh_cache(T):
+    """Tokens of scale 0 (as a cleared cache holds them) are keys and values of 0."""
+    gpu = sage.alloc_cache(20, 2, "cuda", D=128, page_size=32)
+    q = bf16(np.random.default_rng(38), 1, T, 8, 128)
+    out, lse = sage.cache_attention(q, gpu, ints([list(range(20))]), ints([600]), return_lse=True)
+    assert (out == 0).all() and (lse - math.log(600)).abs().max().item() <= 2.0 ** -13
 
 
 @pytest.mark.parametrize("T", [1, 2, 4, 8, 40])
