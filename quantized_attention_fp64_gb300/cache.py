@@ -18,13 +18,13 @@ page number outside the cache counts as a page without tokens, and
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass, field
 
 import torch
 
 from . import _lib
-from .api import (_LAYOUTS, SAGE_ERR_LAYOUT, SAGE_ERR_SHAPE, SageError, _check, _get_device, _stream_handle, _tls,
-                  _workspace)
+from .api import (_LAYOUTS, SAGE_ERR_LAYOUT, SAGE_ERR_SHAPE, SageError, _check, _get_device, _stream_handle, _workspace)
 
 SAGE_ERR_DTYPE = -3
 SAGE_ERR_DEVICE_PAGE = -16
@@ -129,15 +129,16 @@ def _meta(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
-def _kept_calls() -> dict:
-    calls = getattr(_tls, "cache_calls", None)
-    if calls is None:
-        calls = _tls.cache_calls = {}
-    return calls
+class _Kept(threading.local):
+    def __init__(self):  # once in each thread
+        self.calls = {}
+
+
+_kept = _Kept()
 
 
 def _keep(key, value):
-    calls = _kept_calls()
+    calls = _kept.calls
     if len(calls) > 256:
         calls.clear()
     calls[key] = value
@@ -219,7 +220,7 @@ def cache_append(cache: QuantizedCache, k, v, page_table, starts, counts=None, t
         key = ("append", cache.signature, tensor_layout, k.shape, k.stride(), k.dtype, k.get_device(), v.shape, v.stride(),
                v.dtype, v.get_device(), page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device(),
                starts.shape, starts.stride(), starts.dtype, starts.get_device(), _meta(counts))
-        kept = _kept_calls().get(key)
+        kept = _kept.calls.get(key)
     except (AttributeError, TypeError):
         key = kept = None
     if kept is not None and kept[0] == _get_device():
@@ -266,7 +267,7 @@ def cache_read(cache: QuantizedCache, page_table, starts, T: int, counts=None, t
         try:
             key = ("read", cache.signature, tensor_layout, T, page_table.shape, page_table.stride(), page_table.dtype,
                    page_table.get_device(), starts.shape, starts.stride(), starts.dtype, starts.get_device(), _meta(counts))
-            kept = _kept_calls().get(key)
+            kept = _kept.calls.get(key)
         except (AttributeError, TypeError):
             key = None
     if kept is not None and kept[0] == _get_device():
@@ -373,13 +374,13 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
                    q.dtype, q.get_device(), page_table.shape, page_table.stride(), page_table.dtype,
                    page_table.get_device(), lengths.shape, lengths.stride(), lengths.dtype, lengths.get_device(),
                    _meta(q_lengths))
-            kept = _kept_calls().get(key)
+            kept = _kept.calls.get(key)
         except (AttributeError, TypeError):
             key = None
     if kept is not None and kept[0] == _get_device():
         index, fn, ref, args, qi, oi, shape, lse_shape, need = kept
         device = q.device
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty_like(q) if shape is None else torch.empty(shape, dtype=torch.bfloat16, device=device)
         stream = _stream_handle(index)
         args.cache = cache.address
         args.table_dev = page_table.data_ptr()
@@ -450,6 +451,6 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
     if key is not None and table[2]:
         if need:
             args.workspace_bytes = need
-        _keep(key, (index, _lib.load().sage_cache_attention, ctypes.byref(args), args, args.q, args.out, q.shape, (B, H, T),
-                    need))
+        _keep(key, (index, _lib.load().sage_cache_attention, ctypes.byref(args), args, args.q, args.out,
+                    None if q.is_contiguous() else q.shape, (B, H, T), need))
     return (out, lse) if return_lse else out
