@@ -794,9 +794,12 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
 }
 
 // Joins the items that several CTAs share. Block (c, y) serves the item that
-// begins in CTA c and ends in a later one, kJoinWarps / kShare of its rows:
-// kShare warps share a row, each with every kShare-th part.
+// begins in CTA c and ends in a later one. kShare warps share a row, each with
+// every kShare-th part; or a warp has kJoinRows rows, whose loads do not wait for
+// one another.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 2;
+__host__ __device__ constexpr int join_rows(int share) { return share > 1 ? kJoinWarps / share : kJoinWarps * kJoinRows; }
 template <int D, int kShare>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttentionArgs a, int slot_rows,
                                                                      size_t desc_bytes) {
@@ -811,82 +814,96 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
   bool bad = false;
   const int R = load_seq(a, item.y, &bad).q_len * G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot_row = static_cast<int>(blockIdx.y) * (kJoinWarps / kShare) + warp / kShare;
-  const int r = item.w + slot_row;
-  const bool real = slot_row < slot_rows && r < R;
+  constexpr int kRows = kShare > 1 ? 1 : kJoinRows, kAhead = kShare > 1 ? 4 : 2;  // rows of a warp, parts in flight
+  const int row0 = static_cast<int>(blockIdx.y) * join_rows(kShare) + warp / kShare * kRows;
   const size_t slot = static_cast<size_t>(slot_rows) * (D + 2);
   const float* ws = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) + desc_bytes);
-  float top = -INFINITY, sum = 0.0f, acc[kV];
+  float top[kRows], sum[kRows], acc[kRows][kV];
+  bool real[kRows];
 #pragma unroll
-  for (int x = 0; x < kV; ++x) acc[x] = 0.0f;
-  if (real) {
-    // parts of this warp, four at a time: their loads do not wait for one another
-    for (int c = c0 + warp % kShare; c <= item.x; c += 4 * kShare) {
-      float2 x[4];
-      float y[4][kV];
+  for (int y = 0; y < kRows; ++y) {
+    real[y] = row0 + y < slot_rows && item.w + row0 + y < R;
+    top[y] = -INFINITY;
+    sum[y] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ci = c + i * kShare;
-        x[i] = make_float2(-INFINITY, 0.0f);
-        if (ci <= item.x) {
-          const float* p = ws + (static_cast<size_t>(ci) * 2 + (ci == c0 ? item.z & 1 : 0)) * slot;
-          x[i] = *reinterpret_cast<const float2*>(p + slot_rows * D + 2 * slot_row);
-          if constexpr (kV == 4)
-            *reinterpret_cast<float4*>(y[i]) = *reinterpret_cast<const float4*>(p + slot_row * D + 4 * lane);
-          else
-            *reinterpret_cast<float2*>(y[i]) = *reinterpret_cast<const float2*>(p + slot_row * D + 2 * lane);
-        } else {
+    for (int v = 0; v < kV; ++v) acc[y][v] = 0.0f;
+  }
+  if (real[0]) {
+    for (int c = c0 + warp % kShare; c <= item.x; c += kAhead * kShare) {
+      float2 x[kRows][kAhead];
+      float z[kRows][kAhead][kV];
 #pragma unroll
-          for (int v = 0; v < kV; ++v) y[i][v] = 0.0f;
+      for (int y = 0; y < kRows; ++y)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int ci = c + i * kShare;
+          x[y][i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) z[y][i][v] = 0.0f;
+          if (ci <= item.x && real[y]) {
+            const float* p = ws + (static_cast<size_t>(ci) * 2 + (ci == c0 ? item.z & 1 : 0)) * slot;
+            x[y][i] = *reinterpret_cast<const float2*>(p + slot_rows * D + 2 * (row0 + y));
+            if constexpr (kV == 4)
+              *reinterpret_cast<float4*>(z[y][i]) = *reinterpret_cast<const float4*>(p + (row0 + y) * D + 4 * lane);
+            else
+              *reinterpret_cast<float2*>(z[y][i]) = *reinterpret_cast<const float2*>(p + (row0 + y) * D + 2 * lane);
+          }
         }
-      }
-      const float up = fmaxf(max3(x[0].x, x[1].x, x[2].x), fmaxf(x[3].x, top));
-      const float ref = up == -INFINITY ? 0.0f : up, alpha = ex2(top - ref);
-      top = up;
-      sum *= alpha;
 #pragma unroll
-      for (int v = 0; v < kV; ++v) acc[v] *= alpha;
+      for (int y = 0; y < kRows; ++y) {
+        float up = top[y];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float wt = ex2(x[i].x - ref);
-        sum = fmaf(x[i].y, wt, sum);
+        for (int i = 0; i < kAhead; ++i) up = fmaxf(up, x[y][i].x);
+        const float ref = up == -INFINITY ? 0.0f : up, alpha = ex2(top[y] - ref);
+        top[y] = up;
+        sum[y] *= alpha;
 #pragma unroll
-        for (int v = 0; v < kV; ++v) acc[v] = fmaf(y[i][v], wt, acc[v]);
+        for (int v = 0; v < kV; ++v) acc[y][v] *= alpha;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const float wt = ex2(x[y][i].x - ref);
+          sum[y] = fmaf(x[y][i].y, wt, sum[y]);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) acc[y][v] = fmaf(z[y][i][v], wt, acc[y][v]);
+        }
       }
     }
   }
   if constexpr (kShare > 1) {
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = acc[v];
-    if (lane == 0) ml_s[warp] = make_float2(top, sum);
+    for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = acc[0][v];
+    if (lane == 0) ml_s[warp] = make_float2(top[0], sum[0]);
     __syncthreads();
-    if (!real || warp % kShare != 0) return;
+    if (!real[0] || warp % kShare != 0) return;
 #pragma unroll
-    for (int w = 0; w < kShare; ++w) top = fmaxf(top, ml_s[warp + w].x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    sum = 0.0f;
+    for (int w = 0; w < kShare; ++w) top[0] = fmaxf(top[0], ml_s[warp + w].x);
+    const float ref = top[0] == -INFINITY ? 0.0f : top[0];
+    sum[0] = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = 0.0f;
+    for (int v = 0; v < kV; ++v) acc[0][v] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kShare; ++w) {
       const float wt = ex2(ml_s[warp + w].x - ref);
-      sum = fmaf(ml_s[warp + w].y, wt, sum);
+      sum[0] = fmaf(ml_s[warp + w].y, wt, sum[0]);
 #pragma unroll
-      for (int v = 0; v < kV; ++v) acc[v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[v]);
+      for (int v = 0; v < kV; ++v) acc[0][v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[0][v]);
     }
-  } else if (!real) {
-    return;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int tok = r / G, head = (item.z >> 1) * G + r - tok * G;
-  uint16_t* p = a.out.p + item.y * a.out.sb + tok * a.out.ss + head * a.out.sh + kV * lane;
 #pragma unroll
-  for (int i = 0; i < kV; i += 2) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-    *reinterpret_cast<uint32_t*>(p + i) = *reinterpret_cast<const uint32_t*>(&v);
+  for (int y = 0; y < kRows; ++y) {
+    if (!real[y]) break;
+    const float inv = sum[y] == 0.0f ? 0.0f : 1.0f / sum[y];
+    const int r = item.w + row0 + y, tok = r / G, head = (item.z >> 1) * G + r - tok * G;
+    uint16_t* p = a.out.p + item.y * a.out.sb + tok * a.out.ss + head * a.out.sh + kV * lane;
+#pragma unroll
+    for (int v = 0; v < kV; v += 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[y][v] * inv, acc[y][v + 1] * inv);
+      *reinterpret_cast<uint32_t*>(p + v) = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (a.lse != nullptr && lane == 0)
+      a.lse[(static_cast<int64_t>(item.y) * a.H + head) * a.T + tok] =
+          sum[y] == 0.0f ? -INFINITY : (top[y] + log2f(sum[y])) * kLn2;
   }
-  if (a.lse != nullptr && lane == 0)
-    a.lse[(static_cast<int64_t>(item.y) * a.H + head) * a.T + tok] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int D, int MT>
@@ -943,15 +960,17 @@ cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_rows, int rows, int ctas,
                               size_t desc_bytes, cudaStream_t stream) {
-  // few rows may have many parts, which 8 warps of a row share (a sequence of
-  // 131071 tokens, 28 heads on 4: 35 us, 60 with a warp per row); many rows have
-  // few (300 x 4 rows a head over 4000 tokens: 40 us, 64 with 8 warps per row)
-  const int share = rows <= 32 ? 8 : 1;
+  const int64_t items = a.B * a.c.H * div_up(a.T * (a.H / a.c.H), slot_rows);
+  // 8 warps to a row where an item has many parts (a sequence of 131071 tokens, 28
+  // heads on 4: 35 us, 60 with a warp per row; 64 rows over 20000 tokens 27 and
+  // 30), a warp per row where it has few (300 x 4 rows a head over 4000 tokens: 40
+  // us, 64 with 8 warps per row)
+  const int share = ctas > 8 * items ? 8 : 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(div_up(rows, kJoinWarps / share)));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(div_up(rows, join_rows(share))));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
