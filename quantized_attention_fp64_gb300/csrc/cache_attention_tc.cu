@@ -38,10 +38,10 @@
 //
 // Every wait on an mbarrier is bounded, as in attention_tc.cu.
 // Measured (GB300): a causal chunk of 2000 tokens over 16001, 32 heads on 8 of
-// 128: 397 us, 1240 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
+// 128: 396 us, 1242 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
 // 71% of the cycles (QK with 64 keys is bound by shared memory, which reads Q
 // again for every key tile), and the chain of a key tile's softmax takes the
-// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 93 us, 461
+// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 92 us, 467
 // TFLOP/s, of which the softmax's chain is 1300 cycles per 64 keys and beginning
 // and ending a unit 4 us of every 20. What was slower: key tiles of 128 without a
 // second buffer of S; S and P apart (404 us); four softmax warpgroups, and eight
