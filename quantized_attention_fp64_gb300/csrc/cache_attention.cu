@@ -960,12 +960,13 @@ cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_rows, int rows, int ctas,
                               size_t desc_bytes, cudaStream_t stream) {
+  // 8 warps to a row where an item has many parts and not too many rows (a
+  // sequence of 131071 tokens, 28 heads on 4: 35 us, 60 with a warp per row; 64 rows
+  // a head over 20000 tokens 27 and 32, 128 rows 35 and 37), else a warp (300 x 4
+  // rows over 4000 tokens, few parts: 40 us, 64 with 8 warps per row; 256 rows over
+  // 20000, many parts: 39 and 45)
   const int64_t items = a.B * a.c.H * div_up(a.T * (a.H / a.c.H), slot_rows);
-  // 8 warps to a row where an item has many parts (a sequence of 131071 tokens, 28
-  // heads on 4: 35 us, 60 with a warp per row; 64 rows over 20000 tokens 27 and
-  // 30), a warp per row where it has few (300 x 4 rows a head over 4000 tokens: 40
-  // us, 64 with 8 warps per row)
-  const int share = ctas > 8 * items ? 8 : 1;
+  const int share = ctas > 8 * items && rows <= 128 ? 8 : 1;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
