@@ -49,6 +49,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+
 #include "cache.cuh"
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -62,7 +64,14 @@ constexpr int kRows = 128;      // rows of a query tile
 constexpr int kKeys = 64;       // keys of a key tile
 constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 constexpr int kMaxSms = 160;
-constexpr int kMinTiles = 2;    // key tiles that are worth a CTA of their own (64 rows over 1000 tokens, 4 heads: 16 us; with 8, 23)
+// Key tiles that are worth a CTA of their own: with n to a unit and p CTAs the
+// tiles cost n / p and the join p, so p goes as the root of n (64 rows over 5000
+// tokens, 4 heads, 20 us, 22 with two tiles each; 256 rows 27 and 34; over 1000 tokens
+// 22, 21 with two and 26 with six).
+__host__ __device__ inline int least_tiles(int64_t n) {
+  const int least = static_cast<int>(sqrtf(0.4f * static_cast<float>(n)) + 0.5f);
+  return least > 2 ? least : 2;
+}
 constexpr int kWindow = 32;     // key tiles whose pages and scales are looked up together
 constexpr int kWindows = 16;    // lookups that are kept (more than the stages and what lies between)
 constexpr float kLn2 = 0.6931471805599453f;
@@ -528,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
   W *= a.c.H;
   before *= a.c.H;
   const int units = entries * a.c.H;
-  // no more CTAs than units, unless each still gets kMinTiles key tiles
-  const int ctas = min(static_cast<int>(gridDim.x), max(units, (W - units * kBegin<D>) / kMinTiles));
+  // no more CTAs than units, unless each still gets a few key tiles
+  const int tiles = W - units * kBegin<D>;
+  const int ctas = min(static_cast<int>(gridDim.x), max(units, tiles / least_tiles(tiles / units)));
   const int each = W / ctas, extra = W - each * ctas, c = static_cast<int>(blockIdx.x);
   const int lo = c < ctas ? c * each + min(c, extra) : 0, hi = c < ctas ? lo + each + (c < extra ? 1 : 0) : 0;
   if (lo < hi && before <= lo && lo < before + mine * a.c.H) {
@@ -1164,7 +1174,7 @@ cudaError_t launch_cache_attention_tc(const CacheAttentionArgs& a, int64_t D, cu
   const int64_t units = pairs * a.B * a.c.H;
   const int sms = sm_count_current() < kMaxSms ? sm_count_current() : kMaxSms;
   // what the tables can name bounds the work: no CTA without any
-  const int64_t want = units > tiles * units / kMinTiles ? units : tiles * units / kMinTiles;
+  const int64_t most = tiles * units / least_tiles(tiles), want = units > most ? units : most;
   const unsigned ctas = static_cast<unsigned>(want < sms ? want : sms);
   const bool one = rows <= kRows;
   const auto kernel = D == 128 ? (one ? cache_attention_tc_kernel<128, true> : cache_attention_tc_kernel<128, false>)
