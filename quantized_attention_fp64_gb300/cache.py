@@ -32,11 +32,11 @@ SAGE_ERR_DEVICE_PAGE = -16
 BLOCK = 32  # tokens that share a scale
 
 
-_signatures: dict = {}
-
-
-def _signature(*sizes) -> int:
-    return _signatures.setdefault(sizes, len(_signatures))
+def _signature(*sizes) -> tuple:
+    """What stands for a cache in the keys of kept calls, which are not checked again: all its
+    sizes and its device. The sizes themselves: a number given out for them would have to be
+    the same for all threads, whoever asks first."""
+    return sizes
 
 
 @dataclass(frozen=True, eq=False)
@@ -53,7 +53,7 @@ class QuantizedCache:
     D: int = field(init=False)
     c: _lib.Cache = field(init=False, repr=False)
     address: int = field(init=False, repr=False)   # of c, which lives as long as the object
-    signature: int = field(init=False, repr=False) # the same for caches of the same sizes on one device
+    signature: tuple = field(init=False, repr=False)  # the same for caches of the same sizes on one device
 
     def __post_init__(self):
         ts = (self.k_codes, self.v_codes, self.k_scale, self.v_scale)

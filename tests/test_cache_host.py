@@ -7,6 +7,8 @@ import ctypes
 import math
 import shutil
 import subprocess
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -14,7 +16,7 @@ import torch
 
 from oracle import cache as oc
 from oracle.sage_oracle import bf16_round
-from quantized_attention_fp64_gb300 import _build, _lib, alloc_cache, cache_append, cache_attention, cache_read
+from quantized_attention_fp64_gb300 import _build, _lib, alloc_cache, cache, cache_append, cache_attention, cache_read
 from quantized_attention_fp64_gb300.api import SageError
 
 OK, DTYPE, HEAD_DIM, SHAPE, LAYOUT, ALIGN, NULLPTR, WORKSPACE = 0, -3, -4, -5, -6, -7, -8, -9
@@ -268,3 +270,50 @@ def test_python_binding_rejects_host_tensors_and_bad_sizes(lib):
               lambda: cache_attention(x, None, None, None)):
         with pytest.raises(TypeError):
             f()
+
+
+# ------------------------------------------------- the keys of kept calls --
+
+
+def test_signatures_of_caches_made_in_between():
+    """A second cache is made while the first one's signature is being looked up."""
+    inner = []
+
+    class Size(int):
+        def __hash__(self):
+            if not inner:
+                inner.append(None)
+                inner[0] = cache._signature(8, 2, 2, 64, 0)
+            return super().__hash__()
+
+    outer = cache._signature(Size(16), 4, 1, 128, 0)
+    hash(outer)
+    assert inner[0] is not None and outer != inner[0]
+
+
+def test_signatures_from_many_threads():
+    """One signature for each combination of sizes, whoever asks first."""
+    n_threads, rounds = 8, 400
+    found = [dict() for _ in range(n_threads)]
+    go = threading.Barrier(n_threads)
+    was = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+
+    def work(i):
+        for r in range(rounds):
+            go.wait(60)
+            for j in range(4):
+                sizes = (1000 + r, 1 + (i + j) % 4, 2, 128, 0)
+                found[i][sizes] = cache._signature(*sizes)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(n_threads)]
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(was)
+    for f in found[1:]:
+        assert f == found[0]
+    assert len(set(found[0].values())) == len(found[0])
