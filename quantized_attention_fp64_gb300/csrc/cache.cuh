@@ -73,6 +73,19 @@ __host__ __device__ inline int64_t block_slot(int64_t page, int32_t h, int32_t H
   return (page * H + h) * blocks_per_page + blk;
 }
 
+// The tensor-core attention goes by tiles of 64 keys and looks 32 tiles up at a
+// time, past a sequence's end too. Lengths end at 2^31 - 32, where sums of a
+// length or a key's number with what a tile holds leave 32 bits: none is formed.
+constexpr int kTileKeys = 64;
+// Key tiles of a row that sees `sees` keys.
+__host__ __device__ inline int key_tiles(int sees) { return sees / kTileKeys + (sees % kTileKeys != 0 ? 1 : 0); }
+// Whether block `blk` of a sequence of `len` tokens holds any.
+__host__ __device__ inline bool block_has_tokens(int blk, int len) {
+  return blk < len / kCacheBlock + (len % kCacheBlock != 0 ? 1 : 0);
+}
+// Whether the tile whose first key is `key0` has a key that a row which sees `sees` keys does not.
+__host__ __device__ inline bool tile_hides_keys(int key0, int sees) { return sees - key0 < kTileKeys; }
+
 // Position of token `i` (0..31) of a block in a row of the values.
 __host__ __device__ inline int value_position(int i) { return ((i >> 1) & 3) * 8 + (i >> 3) * 2 + (i & 1); }
 // The token at position `p` of a row of the values.

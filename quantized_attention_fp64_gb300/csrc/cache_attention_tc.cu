@@ -61,7 +61,7 @@ namespace {
 constexpr int kConv = 4;        // converter warps
 constexpr int kThreads = 384 + 32 * kConv;
 constexpr int kRows = 128;      // rows of a query tile
-constexpr int kKeys = 64;       // keys of a key tile
+constexpr int kKeys = kTileKeys; // keys of a key tile
 constexpr int kB = kKeys / kCacheBlock;  // blocks of a key tile
 constexpr int kMaxSms = 160;
 // Key tiles that are worth a CTA of their own: with n to a unit and p CTAs the
@@ -305,7 +305,7 @@ __device__ __forceinline__ Unit find_entry(const CacheAttentionArgs& a, int pair
   u.n_max = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    u.n[i] = i < u.tiles ? (row_sees(a, u, u.row0 + i * kRows + kRows - 1) + kKeys - 1) / kKeys : 0;
+    u.n[i] = i < u.tiles ? key_tiles(row_sees(a, u, u.row0 + i * kRows + kRows - 1)) : 0;
     u.n_max = max(u.n_max, u.n[i]);
   }
   return u;
@@ -422,7 +422,7 @@ __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64
   w.at = 0;
   w.ks = -1.0f;  // no tokens
   w.vs = 0.0f;
-  if (blk * kCacheBlock < len) {
+  if (block_has_tokens(blk, len)) {
     const int pg = blk / a.c.blocks_per_page;
     const int page = a.pt.table[row_of_table + pg];
     if (page_ok(page, a.c.num_pages)) {
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         const int key0 = (max(p.at - kBegin<D>, 0) + jj) * kKeys;
         float cb[kB];
         int lim[kB];  // tokens of each block that the row sees
-        bool masked = key0 + kKeys > all_see;
+        bool masked = tile_hides_keys(key0, all_see);
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
           const float k = b == 0 ? sc.x : sc.y;

@@ -317,3 +317,42 @@ def test_signatures_from_many_threads():
     for f in found[1:]:
         assert f == found[0]
     assert len(set(found[0].values())) == len(found[0])
+
+
+# ----------------------------------------- key tiles of the longest sequences --
+
+
+@pytest.fixture(scope="module")
+def tiles_host(tmp_path_factory):
+    exe = tmp_path_factory.mktemp("cache") / "tiles"
+    src = str(_build.ROOT) + "/tests/helpers/cache_tiles_host.cu"
+    subprocess.run([_build.nvcc_path(), "-std=c++17", src, "-o", str(exe)], check=True, capture_output=True)
+
+    def ask(name, *args):
+        lines = "".join(f"{name} {' '.join(map(str, a))}\n" for a in args)
+        r = subprocess.run([str(exe)], input=lines, capture_output=True, text=True, check=True)
+        return [int(x) for x in r.stdout.split()]
+
+    return ask
+
+
+LONGEST = 2 ** 31 - 32
+LENGTHS = [0, 1, 31, 32, 33, 63, 64, 65, 2 ** 30, LONGEST - 4097, LONGEST - 2048, LONGEST - 64, LONGEST - 33, LONGEST - 32,
+           LONGEST - 31, LONGEST - 1, LONGEST]
+
+
+def test_key_tiles_up_to_the_longest_sequence(tiles_host):
+    assert tiles_host("tiles", *[(n,) for n in LENGTHS]) == [-(-n // 64) for n in LENGTHS]
+
+
+def test_look_ahead_ends_with_the_sequence(tiles_host):
+    """Every block that a window of 32 tiles may look up: from any tile of the sequence to 31 tiles behind it."""
+    asked = [(2 * t + i, n) for n in LENGTHS for t in {0, max(-(-n // 64) - 1, 0)} for i in range(64)]
+    assert tiles_host("tokens", *asked) == [int(32 * blk < n) for blk, n in asked]
+
+
+def test_tiles_with_hidden_keys(tiles_host):
+    """From the first to the last tile, for rows that see all, some and none of it, and for no row at all."""
+    asked = [(64 * t, n) for m in LENGTHS for t in {0, max(-(-m // 64) - 1, 0)}
+             for n in {max(m - 1, 0), m, 0, 64 * t, 64 * t + 63, 64 * t + 64, 2 ** 31 - 1} if n < 2 ** 31]
+    assert tiles_host("hides", *asked) == [int(key0 + 64 > n) for key0, n in asked]
