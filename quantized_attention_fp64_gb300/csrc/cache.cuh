@@ -91,6 +91,38 @@ __host__ __device__ inline int value_position(int i) { return ((i >> 1) & 3) * 8
 // The token at position `p` of a row of the values.
 __host__ __device__ inline int value_token(int p) { return ((p >> 1) & 3) * 8 + (p >> 3) * 2 + (p & 1); }
 
+// Value scales in the weights. Both attention kernels put a block's value scale
+// into its weights: with y = z + log2 s_v (z: a logit times log2 e) and m about
+// the largest y of the row, w = 2^(y - m) multiplies the codes, and the sum of
+// 2^(z - m) is that of w over s_v. In m a scale counts as 2^kLogScaleMin at least
+// (a scale of 0 everywhere: its codes are 0), so no 2^(z - m) is above
+// 2^(8 - kLogScaleMin). Scales are at most 2^121, so a row's sum is 2^-121 at least.
+// A weight that fp32 does not hold (below 2^-126) takes its part of the sum with
+// it, although next to larger value scales that part may be all of the sum. Parts
+// below 2^-45 of the sum do not matter. So while a row has met no scale above
+// 2^kLogPlainMax (its sum is 2^-kLogPlainMax at least then), a block whose scale is
+// 2^kLogPlainMin or more has a weight of 2^-96, 30 bits above what is lost, or does
+// not matter. In other blocks ("odd") the sum is taken apart from the weights, of
+// 2^(z - its largest in the block). Sums are taken to another maximum in two steps
+// (rescale()), since the factor may leave fp32 where the sum does not.
+constexpr float kLogScaleMin = -90.0f;
+constexpr float kLogPlainMin = -31.0f, kLogPlainMax = 20.0f;
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// log2 of a value scale.
+__device__ __forceinline__ float log_scale(float vs) { return vs == 0.0f ? kLogScaleMin : __log2f(vs); }
+
+// The factor from maximum m to `up` is the square of this.
+__device__ __forceinline__ float half_step(float m, float up) { return ex2(0.5f * (m - up)); }
+__device__ __forceinline__ float rescale(float l, float half) { return l * half * half; }
+#endif
+
 // Arguments of an attention call on the cache (checked on the host).
 struct CacheAttentionArgs {
   CacheView c;

@@ -33,9 +33,9 @@
 // log2 e), the weights 2^(z + log2 s_v - m) are rounded to fp16 (by 2^-11 of
 // themselves, or of what is below 2^-14 of the largest by 2^-25 of that) and
 // multiplied with the exact codes; the sum of 2^(z - m) is taken in fp32, block
-// by block, from the weights before they are rounded, over s_v. So a key of
-// little weight and large values keeps its share. A value scale below 2^-90
-// counts as 2^-90, or that sum would leave fp32.
+// by block, from the weights before they are rounded, over s_v (or apart from
+// them, see cache.cuh). So a key of little weight and large values keeps its
+// share, and one of small values its part of the sum.
 // Measured (GB300, head dimension 128): one token each of 64 sequences of 900 to
 // 8192, 32 heads on 8: 105 us, 5.7 TB/s of 6.8; two of about 131000 tokens, 28
 // heads on 4: 51 us, 4.9 TB/s (the start, the uneven ends of the CTAs and the
@@ -43,6 +43,8 @@
 // Ranges cut two to four times finer than what the SMs hold are slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -88,12 +90,6 @@ struct Split {
 };
 
 // ------------------------------------------------------------- arithmetic --
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -154,9 +150,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, int*
     }
   }
 }
-
-// log2 of a value scale (0: the codes are 0, and any weight will do).
-__device__ __forceinline__ float log_scale(float vs) { return vs == vs ? fmaxf(__log2f(vs), -90.0f) : vs; }
 
 // ------------------------------------------------------------------ decode --
 
@@ -239,9 +232,9 @@ __device__ __forceinline__ void join_cluster(const CacheAttentionArgs& a, uint32
     float sum = 0.0f, acc = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const float wt = ex2(m[c] - ref);
-      sum = fmaf(l[c], wt, sum);
-      acc = fmaf(o[c], wt, acc);
+      const float half = half_step(m[c], ref);
+      sum += rescale(l[c], half);
+      acc = fmaf(o[c], half * half, acc);
     }
     const int tok = r / G, head = h * G + r - tok * G;
     const __nv_bfloat16 v = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc / sum);
@@ -494,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
     __syncthreads();
     float2 o[MT][D / 8][2];  // rows g and g + 8: channels 8x + 2t, + 1
     float l[MT][2];          // and the sum of this lane's keys
+    bool large = false;      // a value scale above 2^kLogPlainMax has been met
     float m[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -504,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         l[mt][e] = 0.0f;
         m[mt][e] = -INFINITY;
       }
-    // this warp's blocks of the segment: CTA units that are warp mod 8
+    // this warp's blocks of the segment: CTA units that are warp mod kWarps
     const int first = at + (warp - at % kWarps + kWarps) % kWarps;
 #pragma unroll 1
     for (int u = first; u < at + n && alive; u += kWarps) {
@@ -512,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
       alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * s, parity, a.dev_err));
       if (!alive) break;
       const float2 sc = scales[s];
-      if (sc.x >= 0.0f || sc.x != sc.x) {
+      // one block of keys; `odd` takes its part of the sums apart from the weights
+      const auto block = [&](auto odd) {
         const uint8_t* kb = smem + (ring - sbase) + s * 2 * L::kBlockBytes;
         const uint8_t* vb = kb + L::kBlockBytes;
         const int key0 = (seg.blk + (u - at)) * kCacheBlock;
@@ -553,11 +548,11 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
         }
         uint32_t pf[MT][2][4];
         // a number in any case: where the scale is NaN so are the weights of the rows that see the block
-        const float unscale = ex2(-fmaxf(sc.y, -90.0f));
+        const float log_min = fmaxf(sc.y, kLogScaleMin), unscale = ex2(-log_min);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           // logits are z * c with c >= 0, so the largest z gives the largest of a block
-          float c[2], mx[2];
+          float c[2], zm[2], mx[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             c[e] = f[mt][e] * sc.x;
@@ -566,22 +561,35 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
             y = max3(y, z[mt][2][2 * e + 1], z[mt][3][2 * e]);
             y = fmaxf(y, z[mt][3][2 * e + 1]);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            mx[e] = y == -INFINITY ? y : fmaf(y, c[e], sc.y);
+            zm[e] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            mx[e] = zm[e] == -INFINITY ? -INFINITY : fmaf(zm[e], c[e], log_min);
           }
           if (__any_sync(0xffffffffu, mx[0] > m[mt][0] + kLazy || mx[1] > m[mt][1] + kLazy)) {
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float up = fmaxf(m[mt][e], mx[e]);
-              alpha[e] = up == -INFINITY ? 1.0f : ex2(m[mt][e] - up);
+              const float up = fmaxf(m[mt][e], mx[e]), half = up == -INFINITY ? 1.0f : half_step(m[mt][e], up);
+              alpha[e] = half * half;
               m[mt][e] = up;
-              l[mt][e] *= alpha[e];
+              l[mt][e] = rescale(l[mt][e], half);
             }
 #pragma unroll
             for (int x = 0; x < D / 8; ++x)
 #pragma unroll
               for (int e = 0; e < 2; ++e) o[mt][x][e] = __fmul2_rn(o[mt][x][e], make_float2(alpha[e], alpha[e]));
+          }
+          if constexpr (decltype(odd)::value) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float top = zm[e] * c[e];
+              float part = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  if (key0 + 8 * j + 2 * t + x < sees[mt][e]) part += ex2(fmaf(z[mt][j][2 * e + x], c[e], -top));
+              if (zm[e] != -INFINITY) l[mt][e] += rescale(part, half_step(top, m[mt][e]));
+            }
           }
           const float add[2] = {sc.y - (m[mt][0] == -INFINITY ? 0.0f : m[mt][0]),
                                 sc.y - (m[mt][1] == -INFINITY ? 0.0f : m[mt][1])};
@@ -613,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
               pf[mt][j >> 1][(j & 1) * 2 + e] = pack_half2(p[j][e].x, p[j][e].y);
             }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l[mt][e] = fmaf(sum[e].x + sum[e].y, unscale, l[mt][e]);
+          for (int e = 0; e < 2; ++e)
+            if (!decltype(odd)::value) l[mt][e] = fmaf(sum[e].x + sum[e].y, unscale, l[mt][e]);
         }
         float off[MT][2];
 #pragma unroll
@@ -641,6 +650,12 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
               o[mt][x][e] = __fadd2_rn(o[mt][x][e], make_float2(d[2 * e], d[2 * e + 1]));
           }
         }
+      };
+      if (sc.x >= 0.0f || sc.x != sc.x) {
+        large |= sc.y > kLogPlainMax;
+        // (the same for all lanes)
+        if (__builtin_expect(!large && !(sc.y < kLogPlainMin), 1)) block(std::false_type{});
+        else block(std::true_type{});
       }
       ++taken;
       from = from + 1 == L::kStages ? 0 : from + 1;
@@ -708,8 +723,9 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 x = ml[w * 16 * MT + r];
-        wt[w] = ex2(x.x - (top == -INFINITY ? 0.0f : top));
-        sum = fmaf(x.y, wt[w], sum);
+        const float half = half_step(x.x, top == -INFINITY ? 0.0f : top);
+        wt[w] = half * half;
+        sum += rescale(x.y, half);
       }
       const int tok = r / G, head = seg.h * G + r - tok * G;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -854,15 +870,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
         float up = top[y];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) up = fmaxf(up, x[y][i].x);
-        const float ref = up == -INFINITY ? 0.0f : up, alpha = ex2(top[y] - ref);
+        const float ref = up == -INFINITY ? 0.0f : up, step = half_step(top[y], ref), alpha = step * step;
         top[y] = up;
-        sum[y] *= alpha;
+        sum[y] = rescale(sum[y], step);
 #pragma unroll
         for (int v = 0; v < kV; ++v) acc[y][v] *= alpha;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          const float wt = ex2(x[y][i].x - ref);
-          sum[y] = fmaf(x[y][i].y, wt, sum[y]);
+          const float half = half_step(x[y][i].x, ref), wt = half * half;
+          sum[y] += rescale(x[y][i].y, half);
 #pragma unroll
           for (int v = 0; v < kV; ++v) acc[y][v] = fmaf(z[y][i][v], wt, acc[y][v]);
         }
@@ -883,8 +899,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
     for (int v = 0; v < kV; ++v) acc[0][v] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kShare; ++w) {
-      const float wt = ex2(ml_s[warp + w].x - ref);
-      sum[0] = fmaf(ml_s[warp + w].y, wt, sum[0]);
+      const float half = half_step(ml_s[warp + w].x, ref), wt = half * half;
+      sum[0] += rescale(ml_s[warp + w].y, half);
 #pragma unroll
       for (int v = 0; v < kV; ++v) acc[0][v] = fmaf(acc_s[warp + w][kV * lane + v], wt, acc[0][v]);
     }

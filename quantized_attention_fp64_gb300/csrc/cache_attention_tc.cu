@@ -30,9 +30,8 @@
 // logits times log2 e), P holds fp16(2^(z + log2 s_v - m)), a rounding of 2^-11
 // of the weight (where it is below 2^-14 of the largest, of 2^-25 of that),
 // O = sum P vcode, and the sum of 2^(z - m) is taken in fp32, block by block,
-// from the weights before they are rounded, over s_v. So what a row does not
-// see, whatever its scale, does not touch it. A value scale below 2^-90 counts
-// as 2^-90 here, or the sum would leave fp32.
+// from the weights before they are rounded, over s_v (or apart from them, see
+// cache.cuh). So what a row does not see, whatever its scale, does not touch it.
 // The keys of a block stand in the order in which the values are stored
 // (value_position), so V^T needs no reordering on the way.
 //
@@ -195,11 +194,6 @@ __device__ __forceinline__ bool wait_bar_warp(const Ctx& cx, uint32_t bar, uint3
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -415,12 +409,26 @@ struct Window {
   int64_t at;  // first byte in the codes
   float ks, vs;
 };
+// The key scale as the softmax reads it, of the block that the lane looked up for
+// its tile: the sign bit is set where the tile is not a plain one, because a block
+// has no tokens, or an odd value scale, or follows a large one of the part (*large:
+// in an earlier window).
+constexpr float kNoTokens = -INFINITY;
+__device__ __forceinline__ bool marked(float ks) { return __float_as_int(ks) < 0; }
+__device__ __forceinline__ float mark(const Window& w, int lane, bool* large) {
+  const float lv = log_scale(w.vs);
+  const uint32_t above = __ballot_sync(0xffffffffu, lv > kLogPlainMax);
+  const bool odd = *large || lv < kLogPlainMin || (above << (31 - lane)) != 0u;  // of the lanes up to this one
+  *large |= above != 0u;
+  if (w.ks < 0.0f) return kNoTokens;
+  return odd ? -fabsf(w.ks) : fabsf(w.ks);
+}
 template <int D>
 __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64_t row_of_table, int h, int len, int blk,
                                               bool* bad) {
   Window w;
   w.at = 0;
-  w.ks = -1.0f;  // no tokens
+  w.ks = kNoTokens;
   w.vs = 0.0f;
   if (block_has_tokens(blk, len)) {
     const int pg = blk / a.c.blocks_per_page;
@@ -436,9 +444,6 @@ __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64
   }
   return w;
 }
-
-// log2 of a value scale (0: the codes are 0, and any weight will do).
-__device__ __forceinline__ float log_scale(float vs) { return vs == vs ? fmaxf(__log2f(vs), -90.0f) : vs; }
 
 // One block of a row: the weights 2^(s c + n) of its 32 scores, in fp16, and
 // their sum. kMasked: from token lim on they are 0, whatever s and c are.
@@ -459,6 +464,23 @@ __device__ __forceinline__ float exp_block(const uint32_t (&s)[32], float c, flo
     pw[k / 2] = pack_half2(p.x, p.y);
   }
   return (sa.x + sa.y) + (sb.x + sb.y);
+}
+
+// What 16 keys (positions 16 h and up of a block, h = 0 or 1) of which the row sees
+// those of the block's first lim tokens add to its sum, apart from their weights:
+// 2^(s c - m), with s from tensor memory.
+__device__ __forceinline__ float part_of_sum(uint32_t taddr, int h, float c, float m, int lim) {
+  uint32_t s[16];
+  tmem_ld16(taddr, s);
+  tc::tmem_wait_ld();
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (value_token(k) + 4 * h < lim) top = fmaxf(top, __uint_as_float(s[k]) * c);
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (value_token(k) + 4 * h < lim) sum += ex2(fmaf(__uint_as_float(s[k]), c, -top));
+  return sum == 0.0f ? 0.0f : rescale(sum, half_step(top, m));
 }
 
 template <int D, bool kOne>
@@ -659,13 +681,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         place_next(a, p, x.n);
         const int tiles = part_tiles(x, 0);
         Window win[kB];
+        bool large[kB] = {};
         for (int j = 0; ok && j < tiles; ++j, ++sent) {
           if (j % kWindow == 0) {
 #pragma unroll
             for (int b = 0; b < kB; ++b)
               win[b] = load_window<D>(a, x.u.b * a.pt.stride, x.u.h, x.u.len, (x.t + j + lane) * kB + b, &bad_page);
+            const float k0 = mark(win[0], lane, &large[0]), k1 = mark(win[1], lane, &large[1]);
             reinterpret_cast<float4*>(smem + T::kOffScale)[windows % kWindows * kWindow + lane] =
-                make_float4(win[0].ks, win[1].ks, log_scale(win[0].vs), log_scale(win[1].vs));
+                make_float4(k0, k1, log_scale(win[0].vs), log_scale(win[1].vs));
             ++windows;
           }
           const int64_t at0 = __shfl_sync(0xffffffffu, win[0].at, j % kWindow);
@@ -704,14 +728,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
     int t = 0, t_end = 0, n = 0, len = 0;
     int64_t row_of_table = 0;
     uint32_t windows = 0, parts = 0;
-    Window win{0, -1.0f, 0.0f};
+    Window win{0, kNoTokens, 0.0f};
     int64_t at = 0;  // the block's first byte in the codes
     int in_window = 0, head = 0;
-    // looks the next 32 tiles up; the softmax's view: key scales (negative: no tokens) and log2 s_v
+    bool large = false;  // a large value scale in the part's earlier windows
+    // looks the next 32 tiles up; the softmax's view: key scales, marked, and log2 s_v
     const auto open_window = [&]() {
       win = load_window<D>(a, row_of_table, head, len, (t + lane) * kB + blk, &bad_page);
+      const float ks = mark(win, lane, &large);
       reinterpret_cast<float*>(smem + T::kOffScale)[(windows % kWindows * kWindow + lane) * 4 + 2 * share + blk] =
-          share == 0 ? win.ks : log_scale(win.vs);
+          share == 0 ? ks : log_scale(win.vs);
       ++windows;
       in_window = 0;
     };
@@ -810,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           len = x.u.len;
           head = x.u.h;
           row_of_table = x.u.b * a.pt.stride;
+          large = false;
           open_window();
           pick();
           // on their way while the queries are brought
@@ -952,15 +979,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         for (int b = 0; b < kB; ++b) {
           const float k = b == 0 ? sc.x : sc.y;
           cb[b] = f * k;
-          lim[b] = k < 0.0f ? 0 : sees - key0 - 32 * b;
-          masked |= k < 0.0f;
+          lim[b] = k == kNoTokens ? 0 : sees - key0 - 32 * b;
+          masked |= marked(k);
         }
         if (masked) {
 #pragma unroll
-          for (int b = 0; b < kB; ++b)
+          for (int b = 0; b < kB; ++b) {
+            cb[b] = f * fabsf(b == 0 ? sc.x : sc.y);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (value_token(c) >= lim[b]) sr[b][c] = 0xFF800000u;
+          }
         }
         // The weights, whose sum over a block is taken back to that of p. First
         // with the running maximum as it is; that stands unless some row's sum
@@ -989,13 +1018,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
             }
             m0 = max3(m0, __uint_as_float(sr[b][30]), __uint_as_float(sr[b][31]));
             m0 = fmaxf(m0, m1);
-            mt = fmaxf(mt, m0 == -INFINITY ? m0 : fmaf(m0, cb[b], b == 0 ? sc.z : sc.w));
+            mt = fmaxf(mt, m0 == -INFINITY ? m0 : fmaf(m0, cb[b], fmaxf(b == 0 ? sc.z : sc.w, kLogScaleMin)));
           }
           if (__any_sync(0xffffffffu, mt > m + kLazy)) {
             const float up = fmaxf(m, mt);
-            const float alpha = up == -INFINITY ? 1.0f : ex2(m - up);
+            const float half = up == -INFINITY ? 1.0f : half_step(m, up), alpha = half * half;
             m = up;
-            l *= alpha;
+            l = rescale(l, half);
             if (j > 0) {
               if (!(ok = wait_pv(st - 1u))) break;  // O is at rest
               tc::tc_fence_after();
@@ -1015,9 +1044,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
               }
             }
           }
+          const bool odd = (marked(sc.x) && sc.x != kNoTokens) || (marked(sc.y) && sc.y != kNoTokens);  // (of the warp)
+          if (odd) {
+#pragma unroll 1
+            for (int q = 0; q < 2 * kB; ++q)
+              l += part_of_sum(tS + 16u * q, q & 1, q < 2 ? cb[0] : cb[1], m, q < 2 ? lim[0] : lim[1]);
+          }
 #pragma unroll
-          for (int b = 0; b < kB; ++b)
+          for (int b = 0; b < kB; ++b) {
             sum[b] = exp_block<true>(sr[b], cb[b], (b == 0 ? sc.z : sc.w) - (m == -INFINITY ? 0.0f : m), lim[b], pw[b]);
+            if (odd) lim[b] = 0;  // l has the block's part
+          }
         }
         // P goes over this row's S, which is in registers
 #pragma unroll
@@ -1082,9 +1119,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
           other = __ldcg(half_ml);
           if (other.y != 0.0f) {
             const float up = fmaxf(m, other.x);
-            s_own = l == 0.0f ? 0.0f : ex2(m - up);
-            s_other = ex2(other.x - up);
-            l = l * s_own + other.y * s_other;
+            const float own = l == 0.0f ? 0.0f : half_step(m, up), its = half_step(other.x, up);
+            s_own = own * own;
+            s_other = its * its;
+            l = rescale(l, own) + rescale(other.y, its);
             m = up;
           }
         }

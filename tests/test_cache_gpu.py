@@ -955,3 +955,88 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert torch.equal(o, alone[i % len(qs)])
+
+
+# ------------------------------------------- value scales of the whole range --
+#
+# Scales from 0 and 2^-120 to 2^120 next to one another. The bound is that of the module with two
+# parts more: lost_weights() with no scale below 2^-90 (the weights are relative to the largest of
+# p_j max(s_j, 2^-90)); and the logarithms, numbers below 2^8 here: six roundings of 2^-17 on the
+# way to a weight or to the log-sum-exp, 2^-14 in all, which the 2^-10 A for the value scales holds,
+# and with which the log-sum-exp's 2^-13 stays below 2^-12.
+
+
+def scale_case(rng, Hkv, D, page, n, exponents):
+    """A cache of one sequence whose blocks' value scales take the exponents in turn (None: 0)."""
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    for i, pos in enumerate(range(0, n, 32)):
+        pg, blk = c.at(table[0], pos)
+        e = exponents[i % len(exponents)]
+        if e is None:
+            k, v = (x.copy() for x in c.block_codes(pg, blk))
+            c.set_block_codes(pg, blk, k, np.zeros_like(v))
+            c.v_scale[pg, :, blk] = 0.0
+        else:
+            c.v_scale[pg, :, blk] = np.float32(1.3 * 2.0 ** e)
+    return table, c
+
+
+def check_scales(rng, c, table, n, T, H, D, causal):
+    q = bf16(rng, 1, T, H, D)
+    sm = 1 / math.sqrt(D)
+    out, lse = sage.cache_attention(q, upload(c), ints(table), ints([n]), is_causal=causal, return_lse=True)
+    ref_o, ref_lse, weight = oc.attention(c, f32(q), table, [n], [T], causal, sm)
+    floor = c.v_scale.copy()
+    c.v_scale[:] = np.maximum(c.v_scale, np.float32(2.0 ** -90))
+    lost = lost_weights(c, f32(q), table, [n], [T], sm)
+    c.v_scale[:] = floor
+    o = f32(out).astype(np.float64)
+    tol = 2.0 ** -8 * np.abs(ref_o) + 2.0 ** -9 * weight + lost
+    bad = ~(np.abs(o - ref_o) <= tol)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4].tolist(), o[bad][:4], ref_o[bad][:4])
+    err = np.abs(f32(lse).astype(np.float64) - ref_lse)
+    assert err.max() <= 2.0 ** -12, err.max()
+
+
+SCALES = [
+    [None, 40],                    # blocks of zeros beside large values
+    [100, 40, None],               # the largest seen first
+    [-60, 70, -60, -60],
+    [-120, 119, 0],
+    [-100, -95],                   # small values alone
+    [-88, None, 2, 120],
+]
+
+
+@pytest.mark.parametrize("exponents", SCALES)
+@pytest.mark.parametrize("n,T,H,Hkv,D", [
+    (300, 1, 4, 2, 128), (300, 20, 2, 2, 64), (5000, 2, 4, 1, 128), (9000, 5, 4, 1, 64),
+    (700, 40, 2, 2, 64), (3000, 40, 4, 2, 128), (700, 300, 2, 2, 64), (1500, 300, 1, 1, 128),
+])
+def test_attention_value_scales_of_the_whole_range(n, T, H, Hkv, D, exponents):
+    rng = np.random.default_rng(41)
+    table, c = scale_case(rng, Hkv, D, 64, n, exponents)
+    check_scales(rng, c, table, n, T, H, D, False)
+    check_scales(rng, c, table, n, T, H, D, True)
+
+
+@pytest.mark.parametrize("n,T,H,Hkv,D", [(300, 1, 4, 2, 128), (9000, 5, 4, 1, 64), (3000, 40, 4, 2, 128), (1500, 300, 1, 1, 64)])
+def test_attention_large_values_met_last(n, T, H, Hkv, D):
+    """All but the last blocks are zeros or small; what they hold of the sum is joined across warps and CTAs."""
+    rng = np.random.default_rng(42)
+    blocks = -(-n // 32)
+    for head, tail in (([None], 110), ([-80], 115), ([-119], 60)):
+        table, c = scale_case(rng, Hkv, D, 32, n, head * (blocks - 2) + [tail, tail])
+        check_scales(rng, c, table, n, T, H, D, False)
+
+
+@pytest.mark.parametrize("n,T,H,Hkv,D", [(300, 1, 4, 2, 128), (9000, 5, 4, 1, 64), (6000, 40, 4, 2, 128), (4600, 300, 1, 1, 128),
+                                         (4600, 300, 1, 1, 64)])
+def test_attention_large_values_met_first(n, T, H, Hkv, D):
+    """Ordinary, small and no values behind large ones, over more tiles than are looked up at a time."""
+    rng = np.random.default_rng(43)
+    blocks = -(-n // 32)
+    for head, tail in ((119, [0]), (119, [19]), (30, [-70]), (21, [-31, -32]), (110, [None])):
+        table, c = scale_case(rng, Hkv, D, 32, n, [head, head] + tail * blocks)
+        check_scales(rng, c, table, n, T, H, D, True)
