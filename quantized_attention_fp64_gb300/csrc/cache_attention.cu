@@ -114,15 +114,6 @@ __device__ __forceinline__ void codes_to_half(uint32_t x, uint32_t& lo, uint32_t
   hi = *reinterpret_cast<const uint32_t*>(&rb);
 }
 
-// Four int8 codes to two pairs of fp16 code + 1152: the sum over the rows that
-// p weights takes 1152 sum p off again.
-constexpr float kBias = 1152.0f;
-__device__ __forceinline__ void codes_to_biased_half(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  x ^= 0x80808080u;
-  lo = __byte_perm(x, 0x64646464u, 0x4140);
-  hi = __byte_perm(x, 0x64646464u, 0x4342);
-}
-
 // d = a b + c, m16n8k16, fp16 with fp32 sums
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
                                          float c1, float c2, float c3) {
@@ -624,26 +615,16 @@ __global__ void __launch_bounds__(kThreads, Dec<D, MT>::kCtasPerSm) cache_decode
           for (int e = 0; e < 2; ++e)
             if (!decltype(odd)::value) l[mt][e] = fmaf(sum[e].x + sum[e].y, unscale, l[mt][e]);
         }
-        float off[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          // what the values' bias adds: the sum of the rounded p, as a product with ones
-          float d[4];
-          mma16816(d, pf[mt][0], 0x3C003C00u, 0x3C003C00u, 0.0f, 0.0f, 0.0f, 0.0f);
-          mma16816(d, pf[mt][1], 0x3C003C00u, 0x3C003C00u);
-          off[mt][0] = -kBias * d[0];
-          off[mt][1] = -kBias * d[2];
-        }
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {
           const uint2 c = *reinterpret_cast<const uint2*>(vb + x * 256 + lane * 8);
           uint32_t b[4];
-          codes_to_biased_half(c.x, b[0], b[1]);
-          codes_to_biased_half(c.y, b[2], b[3]);
+          codes_to_half(c.x, b[0], b[1]);
+          codes_to_half(c.y, b[2], b[3]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float d[4];
-            mma16816(d, pf[mt][0], b[0], b[1], off[mt][0], off[mt][0], off[mt][1], off[mt][1]);
+            mma16816(d, pf[mt][0], b[0], b[1], 0.0f, 0.0f, 0.0f, 0.0f);
             mma16816(d, pf[mt][1], b[2], b[3]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
