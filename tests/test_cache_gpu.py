@@ -1060,3 +1060,46 @@ def test_attention_empty_and_sparse_channels_exactly(n, T, D):
     one[D // 2] = 1.0 / (127 * n)
     close(out, lse, *ref, lost_weights(c, f32(q), table, [n], [T], 1 / math.sqrt(D)) * one)
     assert (out[..., D // 2 + 1:] == 0).all() and (out[..., D // 2] != 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hkv,n", [(1, 1, 20050), (1, 1, 20114), (40, 4, 1100), (40, 4, 1164)])
+def test_attention_nan_in_folded_parts(B, Hkv, n, D):
+    """33 to 128 rows over parts that both halves of a CTA share: a block of NaN at the end of the
+    sequence, in a key tile of the one half or the other, reaches the rows that see it and no others."""
+    rng = np.random.default_rng(45)
+    G, page, T = 4, 64, 30
+    lengths = [n] * B
+    table, P = make_table(rng, lengths, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    gpu = upload(c)
+    q, t, lens = bf16(rng, B, T, G * Hkv, D), ints(table), ints(lengths)
+    clean, clean_lse = sage.cache_attention(q, gpu, t, lens, is_causal=True, return_lse=True)
+    pg, blk = c.at(table[0], n - 1)
+    seen = (n - 1) // 32 * 32 - (n - T)          # the first row that sees a token of the last block
+    assert 0 < seen < T
+    head = Hkv - 1                               # of sequence 0
+    mine = slice(head * G, head * G + G)
+    for scale in (gpu.k_scale, gpu.v_scale):
+        was = scale[pg, head, blk].clone()
+        scale[pg, head, blk] = float("nan")
+        out, lse = sage.cache_attention(q, gpu, t, lens, is_causal=True, return_lse=True)
+        scale[pg, head, blk] = was
+        assert torch.isnan(out[0, seen:, mine].float()).all()
+        assert torch.equal(out[0, :seen, mine], clean[0, :seen, mine])
+        assert torch.equal(lse[0, mine, :seen], clean_lse[0, mine, :seen])
+        out[0, :, mine] = clean[0, :, mine]
+        assert torch.equal(out, clean)
+    # in a block that all rows see, behind a value scale that makes the tiles odd ones
+    for pos in (64, 640):
+        pg1, blk1 = c.at(table[0], pos)
+        pg2, blk2 = c.at(table[0], pos + 64)
+        gpu.v_scale[pg1, head, blk1] *= 2.0 ** 30
+        for scale in (gpu.k_scale, gpu.v_scale):
+            was = scale[pg2, head, blk2].clone()
+            scale[pg2, head, blk2] = float("nan")
+            out = sage.cache_attention(q, gpu, t, lens, is_causal=True)
+            scale[pg2, head, blk2] = was
+            assert torch.isnan(out[0, :, mine].float()).all()
+            out[0, :, mine] = clean[0, :, mine]
+            assert torch.equal(out, clean)
