@@ -508,7 +508,18 @@ SAGE_API int sage_cache_attention_workspace_size(int64_t B, int64_t T, int64_t H
  * contents do not matter; not used by another call at the same time.
  * B * cache->H * (32-token blocks a table row can name + 16), times every
  * started 256 of the T * H / cache->H rows of a key/value head, is below 2^31
- * (TOO_LARGE). Scales are not negative (sage_cache_append writes none).
+ * (TOO_LARGE). Scales are 0, or positive and at most 2^121, or NaN
+ * (sage_cache_append writes no others).
+ * Numbers: codes enter the products exactly, all sums are fp32. Queries enter
+ * as fp16 times a power of two per row: exact down to 2^-16 of the row's
+ * largest, off by up to 2^-25 of it below. Weights p_j times their value scale
+ * are rounded to fp16: by 2^-11 of themselves, and below 2^-14 of the row's
+ * largest by 2^-25 of that (in which scales below 2^-90 count as 2^-90).
+ * The lengths are on the device, so a call is planned for max_pages: small
+ * calls are quicker with a table, or the first columns of one, that is not much
+ * wider than the sequences are long (one of 1000 tokens: 7.1 us, with rows for
+ * 131072 tokens 10.3). The workspace holds 4 to 43 MB, by head dimension and
+ * rows of a key/value head.
  * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,
  * CUDA; on the device DEVICE_PAGE. */
 typedef struct sage_cache_attention_args {

@@ -39,7 +39,10 @@
 // Measured (GB300, head dimension 128): one token each of 64 sequences of 900 to
 // 8192, 32 heads on 8: 105 us, 5.7 TB/s of 6.8; two of about 131000 tokens, 28
 // heads on 4: 51 us, 4.9 TB/s (the start, the uneven ends of the CTAs and the
-// join take 10 us there); one of 1000: 6.2 us, a chain of dependent loads.
+// join take 10 us there); one of 1000: 6.6 us, a chain of dependent loads. 17 to
+// 32 rows of a head over 14 x 20000 tokens: 137 us, 4.2 TB/s; no pipe is full
+// there (issue slots 41%, tensor 47%, HBM 53%): with two warps to a scheduler the
+// latencies of a warp's own instructions add up.
 // Ranges cut two to four times finer than what the SMs hold are slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -925,6 +928,9 @@ cudaError_t launch_decode(const CacheAttentionArgs& a, cudaStream_t stream) {
   // and the second kernel, 6.7 so; one of 4000 11.7 and 9.9; 16 x 5 drafts over
   // 4001 tokens of 4 heads of 64 26 and 19. With more blocks a warp the clusters,
   // at most 8 CTAs an item, leave SMs idle that the list's even ranges use.
+  // (The blocks are those that the tables can name, since the lengths are on the
+  // device: a table for 131072 tokens sends 1000 through the list, 10.3 us where
+  // rows of their own length take 7.1.)
   // Clusters leave some places of the SMs empty, so nine tenths are given out:
   // 16 sequences of 1000 tokens, 4 heads of 64, 7.6 us, 12.2 where all are and
   // some clusters wait; 4001 tokens 12.5 with 6 CTAs an item, 14.9 with 4
@@ -986,8 +992,8 @@ size_t cache_attention_workspace_bytes(int64_t, int64_t T, int64_t H, int64_t Hk
 }
 
 // By the rows of a key/value head (14 x 20000 tokens, 8 heads of 128, us): up to
-// 16 one row tile, 98 (8 rows) and 104 (16); up to 32 two, 148; more on the tcgen05
-// tensor cores, 169 (40 rows) to 180 (128) and 257 (256). Its 128-row tiles take
+// 16 one row tile, 98 (8 rows) and 100 (16); up to 32 two, 137; more on the tcgen05
+// tensor cores, 171 (40 rows) to 181 (128) and 254 (256). Its 128-row tiles take
 // as long for 20 rows as for 40, and four row tiles have no registers.
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream) {
   const int64_t rows = a.T * (a.H / a.c.H);

@@ -37,10 +37,10 @@
 //
 // Every wait on an mbarrier is bounded, as in attention_tc.cu.
 // Measured (GB300): a causal chunk of 2000 tokens over 16001, 32 heads on 8 of
-// 128: 396 us, 1242 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
+// 128: 395 us, 1246 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
 // 71% of the cycles (QK with 64 keys is bound by shared memory, which reads Q
 // again for every key tile), and the chain of a key tile's softmax takes the
-// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 92 us, 467
+// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 95 us, 449
 // TFLOP/s, of which the softmax's chain is 1300 cycles per 64 keys and beginning
 // and ending a unit 4 us of every 20. What was slower: key tiles of 128 without a
 // second buffer of S; S and P apart (404 us); four softmax warpgroups, and eight
@@ -363,8 +363,8 @@ __device__ __forceinline__ int part_tiles(const Part& x, int i) {
 // copies, where the second query tile's room lets some wait in shared memory.
 // 40 rows over 14 x 20000 tokens, 8 heads of 128: 231 us as the form for more
 // rows does it, 241 with folding alone, 215 with the copies alone, 176 with
-// both (now 169); what bounds it is the conversion of the codes, which takes no
-// less for fewer rows (32 rows, without tensor memory: 148 us).
+// both (now 171); what bounds it is the conversion of the codes, which takes no
+// less for fewer rows (32 rows, without tensor memory: 137 us).
 constexpr int kFold = 8;
 static_assert(kWindow % 2 == 0, "a folded query tile begins a window at its own first tile of it");
 __device__ __forceinline__ bool folds(const Part& x) { return x.u.tiles == 1 && x.tiles >= kFold; }
