@@ -37,10 +37,10 @@
 //
 // Every wait on an mbarrier is bounded, as in attention_tc.cu.
 // Measured (GB300): a causal chunk of 2000 tokens over 16001, 32 heads on 8 of
-// 128: 395 us, 1246 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
+// 128: 396 us, 1240 TFLOP/s, 65% of cuBLAS's bf16 rate; the tensor pipe is busy
 // 71% of the cycles (QK with 64 keys is bound by shared memory, which reads Q
 // again for every key tile), and the chain of a key tile's softmax takes the
-// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 95 us, 449
+// rest. 2 x 4097 queries over up to 1500 states, 16 heads of 64: 96 us, 446
 // TFLOP/s, of which the softmax's chain is 1300 cycles per 64 keys and beginning
 // and ending a unit 4 us of every 20. What was slower: key tiles of 128 without a
 // second buffer of S; S and P apart (404 us); four softmax warpgroups, and eight
@@ -410,18 +410,22 @@ struct Window {
   float ks, vs;
 };
 // The key scale as the softmax reads it, of the block that the lane looked up for
-// its tile: the sign bit is set where the tile is not a plain one, because a block
-// has no tokens, or an odd value scale, or follows a large one of the part (*large:
-// in an earlier window).
-constexpr float kNoTokens = -INFINITY;
+// its tile: below 0 (its sign bit is set) where the tile is not a plain one. That is
+// because the block has no tokens, because its value scale is an odd one, or because
+// it follows a large one in its half of the part's tiles (*large: in an earlier
+// window). The other block of the tile may be the only one that has tokens, so one
+// that has none says whether it follows a large one, too.
+constexpr float kNoTokens = -INFINITY, kNoTokensOdd = -3e38f;  // (no scale is as large)
 __device__ __forceinline__ bool marked(float ks) { return __float_as_int(ks) < 0; }
+__device__ __forceinline__ bool has_tokens(float ks) { return !(ks <= kNoTokensOdd); }
+__device__ __forceinline__ bool marked_odd(float ks) { return marked(ks) && ks != kNoTokens; }
 __device__ __forceinline__ float mark(const Window& w, int lane, bool* large) {
   const float lv = log_scale(w.vs);
   const uint32_t above = __ballot_sync(0xffffffffu, lv > kLogPlainMax);
-  const bool odd = *large || lv < kLogPlainMin || (above << (31 - lane)) != 0u;  // of the lanes up to this one
+  const bool follows = *large || (above << (31 - lane)) != 0u;  // (or is one)
   *large |= above != 0u;
-  if (w.ks < 0.0f) return kNoTokens;
-  return odd ? -fabsf(w.ks) : fabsf(w.ks);
+  if (w.ks < 0.0f) return follows ? kNoTokensOdd : kNoTokens;
+  return follows || lv < kLogPlainMin ? -fabsf(w.ks) : fabsf(w.ks);
 }
 template <int D>
 __device__ __forceinline__ Window load_window(const CacheAttentionArgs& a, int64_t row_of_table, int h, int len, int blk,
@@ -979,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
         for (int b = 0; b < kB; ++b) {
           const float k = b == 0 ? sc.x : sc.y;
           cb[b] = f * k;
-          lim[b] = k == kNoTokens ? 0 : sees - key0 - 32 * b;
+          lim[b] = !has_tokens(k) ? 0 : sees - key0 - 32 * b;
           masked |= marked(k);
         }
         if (masked) {
@@ -1044,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_tc_kernel(const C
               }
             }
           }
-          const bool odd = (marked(sc.x) && sc.x != kNoTokens) || (marked(sc.y) && sc.y != kNoTokens);  // (of the warp)
+          const bool odd = marked_odd(sc.x) || marked_odd(sc.y);  // (the same for the warp)
           if (odd) {
 #pragma unroll 1
             for (int q = 0; q < 2 * kB; ++q)

@@ -1041,6 +1041,17 @@ def test_attention_large_values_met_first(n, T, H, Hkv, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,T,H,Hkv", [(660, 1, 4, 2), (660, 20, 1, 1), (660, 40, 2, 1), (660, 300, 1, 1), (5140, 300, 2, 1)])
+def test_attention_large_values_beside_the_last_block(n, T, H, Hkv, D):
+    """Every other block's values are large; the last block, alone in its key tile, is none of them."""
+    rng = np.random.default_rng(46)
+    for exponents in ([-30, 110], [-10, 119], [0, 100]):
+        table, c = scale_case(rng, Hkv, D, 64, n, exponents)
+        check_scales(rng, c, table, n, T, H, D, False)
+        check_scales(rng, c, table, n, T, H, D, True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,T", [(3000, 1), (3000, 2), (3000, 8), (40, 1), (300, 3), (3000, 40)])
 def test_attention_empty_and_sparse_channels_exactly(n, T, D):
     """Channels without codes come out as 0, and one code of 1 among many keys as what it is: the bound
