@@ -17,6 +17,7 @@ some roundings of numbers below 16 (2^-20 each): 2^-13 in all.
 """
 
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -933,6 +934,46 @@ def test_page_table_rows_of_a_wider_tensor(T):
     oc.append(c, f32(kk), f32(vv), table, [399, 300, 0], [1, 1, 0])
     sage.cache_append(gpu, kk, vv, view, ints([399, 300, 0]), counts=ints([1, 1, 0]))
     same_tokens(gpu, c, table, [400, 301, 0])
+
+
+def test_threads_with_caches_of_their_own():
+    """Caches of different sizes, made and used by threads at the same time, each on a stream of its own."""
+    n_threads = 4
+    go, found = threading.Barrier(n_threads), [None] * n_threads
+
+    def work(i):
+        try:
+            rng = np.random.default_rng(50 + i)
+            H, D, page, n = 1 + i, (64, 128)[i % 2], 32 * (1 + i // 2), 100 + 40 * i
+            table, P = make_table(rng, [n], page)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                k, v, q = bf16(rng, 1, n, H, D), bf16(rng, 1, n, H, D), bf16(rng, 1, 3, 4 * H, D)
+                t, zero, lens = ints(table), ints([0]), ints([n])
+                go.wait(60)
+                for _ in range(20):
+                    gpu = sage.alloc_cache(P, H, "cuda", D=D, page_size=page)
+                    sage.cache_append(gpu, k, v, t, zero)
+                    out, lse = sage.cache_attention(q, gpu, t, lens, is_causal=True, return_lse=True)
+                    kk, vv = sage.cache_read(gpu, t, zero, n)
+                stream.synchronize()
+                c = oc.Cache(P, H, D, page)
+                oc.append(c, f32(k), f32(v), table, [0], [n])
+                same_tokens(gpu, c, table, [n])
+                for got, want in zip((kk, vv), c.tokens(table[0], 0, n)):
+                    assert torch.equal(got[0].cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16))
+                close(out, lse, *oc.attention(c, f32(q), table, [n], [3], True, 1 / math.sqrt(D)))
+            found[i] = "right"
+        except BaseException as e:  # a thread's failure is the test's
+            found[i] = e
+            go.abort()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(n_threads)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert found == ["right"] * n_threads, found
 
 
 def test_two_streams_at_once():
