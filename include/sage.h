@@ -93,7 +93,8 @@ enum {
   SAGE_ERR_ARG = -13,           /* another invalid argument (e.g. non-finite or non-positive sm_scale) */
   SAGE_ERR_TOO_LARGE = -14,     /* sizes exceed the library's index limits */
   SAGE_ERR_DEVICE_SMEM = -15,   /* a kernel's dynamic shared memory was not 1024-byte aligned; it did no work */
-  SAGE_ERR_DEVICE_PAGE = -16    /* a page table, page list or length named tokens outside the cache */
+  SAGE_ERR_DEVICE_PAGE = -16,   /* a page table, page list or length named tokens outside the cache */
+  SAGE_ERR_DEVICE_OFFSETS = -17 /* the offsets of packed sequences decrease or leave the tensor */
 };
 
 /* dtype codes for sage_sageattn */
@@ -541,6 +542,176 @@ typedef struct sage_cache_attention_args {
 } sage_cache_attention_args;
 SAGE_API int sage_cache_attention(const sage_cache_attention_args* args);
 
+/* Adds the attention weights that the cache's tokens get from a step's queries
+ * to running scores, by which an eviction (sage_cache_evict) may go:
+ *   scores[b][hkv][j] += sum over t < q_lengths[b] and the H / cache->H heads h
+ *                        of hkv of exp(sm_scale q[b][t][h] . k_j - lse[b][h][t])
+ * for the tokens j < lengths[b] that row t sees, which are those of
+ * sage_cache_attention (is_causal, lengths and q_lengths as there); lse is what
+ * that call gave. A row whose lse is -inf (it saw no token) adds nothing.
+ * scores: fp32, element (b, hkv, j) at scores_dev + b * scores_stride_b +
+ * hkv * scores_stride_h + j, j < scores_size; tokens at scores_size and up get
+ * none. Scores of tokens that no row sees are left as they were. Every score is
+ * summed in one fixed order, so results repeat bit for bit.
+ * Numbers: codes and queries enter exactly, sums are fp32.
+ * A NaN in a key's scale makes that key's score NaN, a NaN in lse those of the
+ * keys that its row sees.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, TOO_LARGE (limits of
+ * sage_cache_attention), ARCH, CUDA; on the device DEVICE_PAGE. */
+typedef struct sage_cache_add_weights_args {
+  const sage_cache* cache;
+  const int32_t* table_dev;
+  int64_t table_stride, max_pages;
+  const int32_t* lengths_dev;
+  const int32_t* q_lengths_dev;
+  sage_bf16_tensor q;
+  int64_t B, T, H;
+  float sm_scale;
+  int32_t is_causal;
+  const float* lse_dev;            /* [B][H][T] */
+  float* scores_dev;               /* read and written */
+  int64_t scores_stride_b, scores_stride_h, scores_size;
+  void* cuda_stream;
+} sage_cache_add_weights_args;
+SAGE_API int sage_cache_add_weights(const sage_cache_add_weights_args* args);
+
+/* Cuts sequences back to `keep` tokens each, every head to its own: the last
+ * `recent` tokens stay, and of the others those keep - recent with the largest
+ * scores (of equal ones the earlier; -0 and 0 are equal; a NaN is below
+ * everything). A sequence of at most keep tokens keeps them all. Kept tokens
+ * move together in their order: the i-th becomes token i of the sequence in the
+ * pages that out_table names.
+ *   lengths_out[b]   = min(lengths[b], keep), int32
+ *   kept[b][h][i]    = where token i came from, i < lengths_out[b]; -1 behind,
+ *                      up to kept_size entries: int32 [B][H][kept_size],
+ *                      kept_size >= min(keep, scores_size)
+ *   scores_out[b][h][i] = its score; 0 behind, up to scores_size: fp32
+ *                      [B][H][scores_size]
+ * A new block's scale is the largest of its tokens' old ones, and codes c become
+ * rint(c * (s / scale)), fp32, correctly rounded, as when a block grows
+ * (sage_cache_append); slots of the last block behind the last token are 0. A NaN
+ * among a block's scales makes the new one NaN.
+ * lengths that reach past the table or past scores_size are cut, and the device
+ * error word is set. A token on a page outside the cache is taken as 0 with
+ * scale 0; what would go to a page outside the cache is lost.
+ * out_table: int32 rows of out_max_pages entries; it may be the table itself
+ * (the sequence is cut back in place), else its pages must not be among the
+ * ones read, nor be named twice. Pages behind a new length are not written.
+ * Pages read may be shared by sequences unless they are written.
+ * lengths_out, kept and scores_out must not overlap lengths and scores.
+ * workspace_dev: sage_cache_evict_workspace_size bytes, 256-byte aligned,
+ * contents do not matter; not used by another call at the same time.
+ * Errors: NULLPTR, SHAPE (also keep < 0, recent < 0, recent > keep, kept_size),
+ * HEAD_DIM, ALIGN, WORKSPACE, TOO_LARGE, ARCH, CUDA; on the device DEVICE_PAGE. */
+typedef struct sage_cache_evict_args {
+  const sage_cache* cache;
+  const int32_t* table_dev;
+  int64_t table_stride, max_pages;
+  const int32_t* out_table_dev;
+  int64_t out_table_stride, out_max_pages;
+  const int32_t* lengths_dev;
+  const float* scores_dev;
+  int64_t scores_stride_b, scores_stride_h, scores_size;
+  int64_t B, keep, recent;
+  int32_t* lengths_out_dev;
+  int32_t* kept_dev;
+  int64_t kept_size;
+  float* scores_out_dev;
+  void* workspace_dev;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} sage_cache_evict_args;
+SAGE_API int sage_cache_evict(const sage_cache_evict_args* args);
+
+/* Workspace bytes of sage_cache_evict. Errors: NULLPTR, SHAPE, HEAD_DIM,
+ * TOO_LARGE. */
+SAGE_API int sage_cache_evict_workspace_size(int64_t B, int64_t H, int64_t D, int64_t keep, int64_t scores_size,
+                                             size_t* bytes);
+
+/* ----------------------------------------------- prompts of language models -- */
+
+/* Rotary positions. Channels 0 .. rotary_dim - 1 of a head are rotary_dim / 2
+ * pairs, (i, i + rotary_dim / 2) or with interleaved != 0 (2i, 2i + 1); the pair
+ * (a, b) of a token at position p becomes
+ *   magnitude * (a cos - b sin, b cos + a sin) of the angle p * inv_freq[i],
+ * with inverse != 0 that of -p * inv_freq[i] (the transpose up to the magnitude's
+ * square: the gradient; and the way back). Channels from rotary_dim on are copied.
+ * q, k (and their outputs): BF16 (B, T, H, D) and (B, T, Hkv, D), D = 64 or 128,
+ * rotary_dim a positive multiple of 16 up to D; Hkv = 0: no k. An output may be
+ * its input itself; otherwise they must not overlap. positions: int32, element
+ * (b, t) at positions_dev + b * positions_stride_b + t * positions_stride_t
+ * (strides of 0 and negative positions are taken).
+ * turns_dev: rotary_dim / 2 frequencies as sage_rotary_turns makes them, in
+ * device memory: the part of a full turn that a position adds, in 2^-64 turns, so
+ * that the angle of any 32-bit position is reduced without error. Cosine and sine
+ * err by up to 2^-20 before the rounding to BF16.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG (rotary_dim, magnitude not finite),
+ * TOO_LARGE, ARCH, CUDA. */
+typedef struct sage_rotary_args {
+  sage_bf16_tensor q, k;           /* read */
+  sage_bf16_tensor q_out, k_out;   /* written */
+  int64_t B, T, H, Hkv, D, rotary_dim;
+  const uint64_t* turns_dev;
+  const int32_t* positions_dev;
+  int64_t positions_stride_b, positions_stride_t;
+  float magnitude;
+  int32_t interleaved;
+  int32_t inverse;
+  void* cuda_stream;
+} sage_rotary_args;
+SAGE_API int sage_rotary(const sage_rotary_args* args);
+
+/* turns[i] = inv_freq[i] / (2 pi), without its whole part, in units of 2^-64
+ * (host memory, no device needed): inv_freq in radians for each position.
+ * Errors: NULLPTR, SHAPE (n < 0), ARG (a frequency that is not finite). */
+SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turns);
+
+/* Attention over whole prompts of different lengths, packed one behind the
+ * other: rows offsets[b] .. offsets[b + 1] - 1 of q (N, H, D) are sequence b's
+ * queries, rows kv_offsets[b] .. kv_offsets[b + 1] - 1 of k and v (M, Hkv, D) its
+ * keys and values (kv_offsets NULL: offsets). Query head h reads key/value head
+ * h / (H / Hkv). With n queries and m keys, row t of the sequence sees its keys j
+ * with j <= m - n + t when is_causal != 0 (the queries are the last of the m
+ * tokens; rows with m - n + t < 0 see none), else all m:
+ *   out = sum_j p_j v_j / sum_j p_j, p_j = exp(sm_scale q . k_j - max),
+ *   lse = ln sum_j exp(sm_scale q . k_j), fp32, element (h, row) at
+ *   lse_dev + h * N + row (NULL: not asked for).
+ * A row that sees no key gets out = 0 and lse = -inf. Rows that belong to no
+ * sequence (in front of offsets[0], from offsets[B] on) are left as they were, or
+ * with zero_rest != 0 set to 0 and -inf.
+ * offsets, kv_offsets: int32 [B + 1] in device memory, not decreasing, within the
+ * tensors. Offsets that break this are cut to what is there, the device error
+ * word is set, and rows of out and lse hold anything.
+ * q, k, v, out: BF16, stride_b is not used; D = 128 or 64; out must not overlap
+ * the inputs. sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
+ * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16
+ * (by 2^-9 of themselves) for the product with v, their sum is taken in fp32
+ * before that.
+ * workspace_dev: sage_prompt_attention_workspace_size bytes, 256-byte aligned,
+ * contents do not matter; not used by another call at the same time.
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH, CUDA;
+ * on the device DEVICE_OFFSETS. */
+typedef struct sage_prompt_attention_args {
+  sage_bf16_tensor q, k, v;
+  sage_bf16_tensor out;            /* written */
+  int64_t N, M, H, Hkv, D, B;
+  const int32_t* offsets_dev;
+  const int32_t* kv_offsets_dev;
+  float sm_scale;
+  int32_t is_causal;
+  int32_t zero_rest;
+  float* lse_dev;
+  void* workspace_dev;
+  size_t workspace_bytes;
+  void* cuda_stream;
+} sage_prompt_attention_args;
+SAGE_API int sage_prompt_attention(const sage_prompt_attention_args* args);
+
+/* Workspace bytes of sage_prompt_attention for these sizes. Errors: NULLPTR,
+ * SHAPE, HEAD_DIM, TOO_LARGE. */
+SAGE_API int sage_prompt_attention_workspace_size(int64_t N, int64_t M, int64_t H, int64_t Hkv, int64_t D, int64_t B,
+                                                  size_t* bytes);
+
 /* ---------------------------------------------------------- diagnostics -- */
 
 /* Synchronizes cuda_stream, then reads and clears the current device's error
@@ -548,9 +719,10 @@ SAGE_API int sage_cache_attention(const sage_cache_attention_args* args);
  * barrier runs out, or, before any work, when their dynamic shared memory is
  * not 1024-byte aligned (the attention kernel uses all of it for aligned
  * operand tiles), or when a page number or length in device memory
- * points outside the cache; they never trap. *code receives SAGE_OK,
- * SAGE_ERR_DEVICE_TIMEOUT, SAGE_ERR_DEVICE_SMEM or SAGE_ERR_DEVICE_PAGE. Returns SAGE_OK, NULLPTR
- * or CUDA. */
+ * points outside the cache, or when the offsets of packed sequences decrease or
+ * leave the tensor; they never trap. *code receives SAGE_OK,
+ * SAGE_ERR_DEVICE_TIMEOUT, SAGE_ERR_DEVICE_SMEM, SAGE_ERR_DEVICE_PAGE or
+ * SAGE_ERR_DEVICE_OFFSETS. Returns SAGE_OK, NULLPTR or CUDA. */
 SAGE_API int sage_device_error(void* cuda_stream, int* code);
 
 /* Test support for the bounded waits: enqueues on cuda_stream one kernel

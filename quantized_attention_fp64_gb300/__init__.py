@@ -25,9 +25,14 @@ from .api import (  # noqa: F401
 from .cache import (  # noqa: F401
     QuantizedCache,
     alloc_cache,
+    cache_add_weights,
     cache_append,
     cache_attention,
     cache_attention_workspace_size,
     cache_copy_pages,
+    cache_evict,
+    cache_evict_workspace_size,
     cache_read,
 )
+from .prompt import prompt_attention, prompt_attention_workspace_size  # noqa: F401
+from .rotary import RotaryTable, rotary, rotary_inv_freq, rotary_table  # noqa: F401

@@ -69,6 +69,43 @@ class CacheAttentionArgs(ctypes.Structure):
                                 ("workspace_dev", c_vp), ("workspace_bytes", ctypes.c_size_t), ("cuda_stream", c_vp)]
 
 
+_SCORES_FIELDS = [("scores_stride_b", c_i64), ("scores_stride_h", c_i64), ("scores_size", c_i64)]
+
+
+class CacheAddWeightsArgs(ctypes.Structure):
+    """sage_cache_add_weights_args"""
+    _fields_ = _TABLE_FIELDS + [("lengths_dev", c_vp), ("q_lengths_dev", c_vp), ("q", Bf16Tensor), ("B", c_i64),
+                                ("T", c_i64), ("H", c_i64), ("sm_scale", ctypes.c_float), ("is_causal", ctypes.c_int32),
+                                ("lse_dev", c_vp), ("scores_dev", c_vp)] + _SCORES_FIELDS + [("cuda_stream", c_vp)]
+
+
+class CacheEvictArgs(ctypes.Structure):
+    """sage_cache_evict_args"""
+    _fields_ = _TABLE_FIELDS + [("out_table_dev", c_vp), ("out_table_stride", c_i64), ("out_max_pages", c_i64),
+                                ("lengths_dev", c_vp), ("scores_dev", c_vp)] + _SCORES_FIELDS + [
+        ("B", c_i64), ("keep", c_i64), ("recent", c_i64), ("lengths_out_dev", c_vp), ("kept_dev", c_vp),
+        ("kept_size", c_i64), ("scores_out_dev", c_vp), ("workspace_dev", c_vp), ("workspace_bytes", ctypes.c_size_t),
+        ("cuda_stream", c_vp)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """sage_rotary_args"""
+    _fields_ = [("q", Bf16Tensor), ("k", Bf16Tensor), ("q_out", Bf16Tensor), ("k_out", Bf16Tensor), ("B", c_i64),
+                ("T", c_i64), ("H", c_i64), ("Hkv", c_i64), ("D", c_i64), ("rotary_dim", c_i64), ("turns_dev", c_vp),
+                ("positions_dev", c_vp), ("positions_stride_b", c_i64), ("positions_stride_t", c_i64),
+                ("magnitude", ctypes.c_float), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("cuda_stream", c_vp)]
+
+
+class PromptAttentionArgs(ctypes.Structure):
+    """sage_prompt_attention_args"""
+    _fields_ = [("q", Bf16Tensor), ("k", Bf16Tensor), ("v", Bf16Tensor), ("out", Bf16Tensor), ("N", c_i64), ("M", c_i64),
+                ("H", c_i64), ("Hkv", c_i64), ("D", c_i64), ("B", c_i64), ("offsets_dev", c_vp),
+                ("kv_offsets_dev", c_vp), ("sm_scale", ctypes.c_float), ("is_causal", ctypes.c_int32),
+                ("zero_rest", ctypes.c_int32), ("lse_dev", c_vp), ("workspace_dev", c_vp),
+                ("workspace_bytes", ctypes.c_size_t), ("cuda_stream", c_vp)]
+
+
 _SIGNATURES = {
     "sage_bundle_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p, c_vp, ctypes.POINTER(Quantized)]),
     "sage_quantize_scratch_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_size_p]),
@@ -102,6 +139,13 @@ _SIGNATURES = {
     "sage_cache_copy_pages": (c_int, [c_vp, c_vp, c_vp, c_i64, c_vp]),
     "sage_cache_attention_workspace_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_size_p]),
     "sage_cache_attention": (c_int, [ctypes.POINTER(CacheAttentionArgs)]),
+    "sage_cache_add_weights": (c_int, [ctypes.POINTER(CacheAddWeightsArgs)]),
+    "sage_cache_evict": (c_int, [ctypes.POINTER(CacheEvictArgs)]),
+    "sage_cache_evict_workspace_size": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_size_p]),
+    "sage_rotary": (c_int, [ctypes.POINTER(RotaryArgs)]),
+    "sage_rotary_turns": (c_int, [ctypes.POINTER(ctypes.c_double), c_i64, ctypes.POINTER(ctypes.c_uint64)]),
+    "sage_prompt_attention": (c_int, [ctypes.POINTER(PromptAttentionArgs)]),
+    "sage_prompt_attention_workspace_size": (c_int, [c_i64] * 6 + [c_size_p]),
     "sage_device_error": (c_int, [c_vp, ctypes.POINTER(c_int)]),
     "sage_selftest_wait_timeout": (c_int, [c_vp]),
     "sage_strerror": (ctypes.c_char_p, [c_int]),

@@ -459,3 +459,135 @@ def cache_attention(q, cache: QuantizedCache, page_table, lengths, q_lengths=Non
         _keep(key, (index, _lib.load().sage_cache_attention, ctypes.byref(args), args, args.q, args.out,
                     None if q.is_contiguous() else q.shape, (B, H, T), need))
     return (out, lse) if return_lse else out
+
+
+def _scores(t, B: int, cache: QuantizedCache):
+    """(address, stride_b, stride_h, tokens) of an fp32 [B, H, tokens] tensor of scores."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("scores must be a torch tensor")
+    if t.device != cache.k_codes.device:
+        raise ValueError("scores must live on the cache's device")
+    if t.dtype != torch.float32:
+        raise SageError(SAGE_ERR_DTYPE, "scores must be float32")
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != cache.H:
+        raise SageError(SAGE_ERR_SHAPE, "scores must be [B, H, tokens] with the cache's heads")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise SageError(SAGE_ERR_LAYOUT, "a head's scores must be contiguous")
+    return t.data_ptr() or 16, t.stride(0), t.stride(1), t.shape[2]
+
+
+def cache_add_weights(scores, q, cache: QuantizedCache, page_table, lengths, lse, q_lengths=None, is_causal: bool = False,
+                      sm_scale=None, tensor_layout: str = "NHD"):
+    """Adds to scores (fp32 [B, cache.H, tokens]) the attention weights that the cache's tokens get from a step's
+    queries (sage_cache_add_weights): scores[b, h, j] += the sum of exp(sm_scale q . k_j - lse) over the rows of q that
+    see token j and the query heads that read head h. Arguments as in cache_attention, whose lse ([B, H, T]) it takes.
+    Tokens that scores has no place for are left out. Returns scores. cache_evict may go by them."""
+    kept = key = None
+    try:
+        key = ("weights", cache.signature, tensor_layout, bool(is_causal), scores.shape, scores.stride(), scores.dtype,
+               scores.get_device(), q.shape, q.stride(), q.dtype, q.get_device(), page_table.shape, page_table.stride(),
+               page_table.dtype, page_table.get_device(), lengths.shape, lengths.stride(), lengths.dtype,
+               lengths.get_device(), lse.shape, lse.stride(), lse.dtype, lse.get_device(), _meta(q_lengths))
+        kept = _kept.calls.get(key)
+    except (AttributeError, TypeError):
+        key = None
+    if kept is not None and kept[0] == _get_device():
+        index, fn, ref, args, qi = kept
+        args.cache = cache.address
+        args.table_dev = page_table.data_ptr()
+        args.lengths_dev = lengths.data_ptr()
+        if q_lengths is not None:
+            args.q_lengths_dev = q_lengths.data_ptr()
+        qi.ptr_dev = q.data_ptr()
+        args.lse_dev = lse.data_ptr()
+        args.scores_dev = scores.data_ptr()
+        args.sm_scale = _NAN if sm_scale is None else float(sm_scale)
+        args.cuda_stream = _stream_handle(index)
+        rc = fn(ref)
+        if rc:
+            _check(rc)
+        return scores
+    _check_cache(cache)
+    _check_layout(tensor_layout)
+    (B, T, H), qi = _tokens(q, cache, tensor_layout, "q")
+    if H % cache.H if cache.H else H:
+        raise SageError(SAGE_ERR_SHAPE, "the query heads must be a multiple of the cache's heads")
+    table = _table(page_table, B, cache)
+    if lengths is None or lse is None:
+        raise TypeError("lengths and lse must be torch tensors")
+    lens, q_lens = _ints(lengths, B, cache, "lengths"), _ints(q_lengths, B, cache, "q_lengths")
+    at, sb, sh, n = _scores(scores, B, cache)
+    if not isinstance(lse, torch.Tensor):
+        raise TypeError("lse must be a torch tensor")
+    if lse.device != cache.k_codes.device:
+        raise ValueError("lse must live on the cache's device")
+    if lse.dtype != torch.float32:
+        raise SageError(SAGE_ERR_DTYPE, "lse must be float32")
+    if tuple(lse.shape) != (B, H, T):
+        raise SageError(SAGE_ERR_SHAPE, "lse must be [B, H, T]")
+    if not lse.is_contiguous():
+        raise SageError(SAGE_ERR_LAYOUT, "lse must be contiguous")
+    if q.numel() == 0 or scores.numel() == 0:
+        return scores
+    index = cache.k_codes.get_device()
+    args = _lib.CacheAddWeightsArgs(cache.address, *table, lens, q_lens, qi, B, T, H,
+                                    _NAN if sm_scale is None else float(sm_scale), bool(is_causal), lse.data_ptr(), at,
+                                    sb, sh, n)
+    with _on(index) as stream:
+        args.cuda_stream = stream
+        _check(_lib.load().sage_cache_add_weights(ctypes.byref(args)))
+    if key is not None and table[2]:
+        _keep(key, (index, _lib.load().sage_cache_add_weights, ctypes.byref(args), args, args.q))
+    return scores
+
+
+def cache_evict_workspace_size(B: int, H: int, D: int, keep: int, tokens: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().sage_cache_evict_workspace_size(B, H, D, keep, tokens, ctypes.byref(n)))
+    return n.value
+
+
+def cache_evict(cache: QuantizedCache, page_table, lengths, scores, keep: int, recent: int = 0, out_table=None,
+                workspace=None):
+    """Cuts sequences back to keep tokens each, every head to its own (sage_cache_evict): the last ``recent`` stay, and
+    of the others those keep - recent with the largest scores ([B, cache.H, tokens], see cache_add_weights; of equal ones
+    the earlier). Kept tokens move together, in order, into the pages that out_table names (None: page_table, in place;
+    else pages that are not read, each named once). Returns (lengths, kept, scores), all new: int32 [B], the new
+    lengths; int32 [B, H, min(keep, tokens)], where each kept token came from, -1 behind the last; and the kept tokens'
+    scores in the shape of scores, 0 behind the last. Pages behind a new length may be given to others.
+
+    workspace: a uint8 tensor of cache_evict_workspace_size bytes that no other call uses at the same time; None: the
+    library's own, one for each thread and stream (a captured graph gets its own from its memory pool)."""
+    _check_cache(cache)
+    B = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else -1
+    lens = _ints(lengths, B if lengths is not None else None, cache, "lengths")
+    if lens is None and lengths is None:
+        raise TypeError("lengths must be a torch tensor")
+    table = _table(page_table, B, cache)
+    to = table if out_table is None else _table(out_table, B, cache)
+    at, sb, sh, n = _scores(scores, B, cache)
+    keep, recent = int(keep), int(recent)
+    need = cache_evict_workspace_size(B, cache.H, cache.D, keep, n)  # refuses sizes, too
+    device = cache.k_codes.device
+    most = min(keep, n)
+    new_lengths = torch.empty(B, dtype=torch.int32, device=device)
+    kept = torch.empty((B, cache.H, most), dtype=torch.int32, device=device)
+    new_scores = torch.empty((B, cache.H, n), dtype=torch.float32, device=device)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch tensor")
+        if workspace.device != device:
+            raise ValueError("workspace must live on the cache's device")
+        if not workspace.is_contiguous():
+            raise SageError(SAGE_ERR_LAYOUT, "workspace must be contiguous")
+    args = _lib.CacheEvictArgs(cache.address, *table, *to, lens or 16, at, sb, sh, n, B, keep, recent,
+                               new_lengths.data_ptr() or 16, kept.data_ptr() or 16, most, new_scores.data_ptr() or 16)
+    with _on(cache.k_codes.get_device()) as stream:
+        if workspace is None and need:
+            workspace = _call_workspace(device, stream, need)
+        if workspace is not None:
+            args.workspace_dev = workspace.data_ptr()
+            args.workspace_bytes = workspace.numel() * workspace.element_size()
+        args.cuda_stream = stream
+        _check(_lib.load().sage_cache_evict(ctypes.byref(args)))
+    return new_lengths, kept, new_scores

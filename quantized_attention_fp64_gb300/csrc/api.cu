@@ -611,9 +611,13 @@ int sage_device_error(void* cuda_stream, int* code) {
   if (cudaMemcpy(&v, g_err_ptr[dev], sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return SAGE_ERR_CUDA;
   const int zero = 0;
   if (cudaMemcpy(g_err_ptr[dev], &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return SAGE_ERR_CUDA;
-  *code = v == 0 ? SAGE_OK
-                 : (v == kDevErrSmemAlign ? SAGE_ERR_DEVICE_SMEM
-                                          : (v == kDevErrPage ? SAGE_ERR_DEVICE_PAGE : SAGE_ERR_DEVICE_TIMEOUT));
+  switch (v) {
+    case 0: *code = SAGE_OK; break;
+    case kDevErrSmemAlign: *code = SAGE_ERR_DEVICE_SMEM; break;
+    case kDevErrPage: *code = SAGE_ERR_DEVICE_PAGE; break;
+    case kDevErrOffsets: *code = SAGE_ERR_DEVICE_OFFSETS; break;
+    default: *code = SAGE_ERR_DEVICE_TIMEOUT;
+  }
   return SAGE_OK;
 }
 
@@ -643,6 +647,7 @@ const char* sage_strerror(int code) {
     case SAGE_ERR_TOO_LARGE: return "sizes exceed the library's limits";
     case SAGE_ERR_DEVICE_SMEM: return "a kernel found its shared memory window misaligned and did no work";
     case SAGE_ERR_DEVICE_PAGE: return "a page table, page list or length named tokens outside the cache";
+    case SAGE_ERR_DEVICE_OFFSETS: return "offsets of packed sequences decrease or leave the tensor";
     default: return "unknown error code";
   }
 }

@@ -163,4 +163,42 @@ cudaError_t launch_cache_join(const CacheAttentionArgs& a, int64_t D, int slot_r
                               size_t desc_bytes, cudaStream_t stream);
 cudaError_t launch_cache_attention(const CacheAttentionArgs& a, int64_t D, cudaStream_t stream);
 
+// Arguments of adding the weights of a step's queries to scores (checked on the host).
+struct CacheWeightsArgs {
+  CacheView c;
+  PageTable pt;
+  const int32_t* lengths;    // [B] tokens in the cache
+  const int32_t* q_lengths;  // [B] query tokens, or null: T each
+  Bf16In q;
+  const float* lse;          // [B][H][T]
+  float* scores;             // element (b, hkv, j) at b * scores_b + hkv * scores_h + j, j < scores_n
+  int64_t scores_b, scores_h, scores_n;
+  int64_t B, T;
+  int32_t H;                 // query heads
+  bool causal;
+  float sm_log2;             // sm_scale * log2(e)
+  int* dev_err;
+};
+cudaError_t launch_cache_weights(const CacheWeightsArgs& a, int64_t D, cudaStream_t stream);
+
+// Arguments of an eviction (checked on the host).
+struct CacheEvictArgs {
+  CacheView c;
+  PageTable from, to;
+  const int32_t* lengths;    // [B]
+  const float* scores;       // element (b, h, j) at b * scores_b + h * scores_h + j, j < scores_n
+  int64_t scores_b, scores_h;
+  int32_t scores_n;
+  int64_t B;
+  int32_t keep, recent;      // keep <= scores_n
+  int32_t* lengths_out;      // [B]
+  int32_t* kept;             // [B][H][kept_n]
+  int32_t kept_n;
+  float* scores_out;         // [B][H][scores_n]
+  void* workspace;
+  int* dev_err;
+};
+cudaError_t launch_cache_evict(const CacheEvictArgs& a, int64_t D, cudaStream_t stream);
+size_t cache_evict_workspace_bytes(int64_t B, int64_t H, int64_t D, int64_t keep);
+
 }  // namespace sage

@@ -6,6 +6,7 @@
 
 #include "../../include/sage.h"
 #include "cache.cuh"
+#include "checks.cuh"
 
 namespace sage {
 namespace {
@@ -14,11 +15,6 @@ constexpr int64_t kMaxPages = int64_t(1) << 20;  // the page lists' check keeps 
 constexpr int64_t kMaxPageSize = 4096;
 constexpr int64_t kMaxDim = 65535;               // sequences and heads are grid dimensions
 constexpr int64_t kMaxTokens = int64_t(1) << 30; // tokens of one call
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool stride_ok(int64_t s) { return s % 8 == 0; }
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA; }
 
 int check_cache_sizes(int64_t num_pages, int64_t page_size, int64_t H, int64_t D) {
   if (num_pages < 0 || page_size < 0 || H < 0 || D < 0) return SAGE_ERR_SHAPE;
@@ -51,26 +47,6 @@ int check_table(const int32_t* table, int64_t stride, int64_t max_pages, PageTab
   return SAGE_OK;
 }
 
-int check_ints(const int32_t* p, bool needed) {
-  if (p == nullptr) return needed ? SAGE_ERR_NULLPTR : SAGE_OK;
-  return aligned(p, 4) ? SAGE_OK : SAGE_ERR_ALIGN;
-}
-
-int check_tensor(const sage_bf16_tensor& t) {
-  if (t.ptr_dev == nullptr) return SAGE_ERR_NULLPTR;
-  return aligned(t.ptr_dev, 16) && stride_ok(t.stride_b) && stride_ok(t.stride_s) && stride_ok(t.stride_h)
-             ? SAGE_OK
-             : SAGE_ERR_ALIGN;
-}
-
-Bf16In to_in(const sage_bf16_tensor& t) {
-  return Bf16In{static_cast<const uint16_t*>(t.ptr_dev), t.stride_b, t.stride_s, t.stride_h};
-}
-
-Out to_out(const sage_bf16_tensor& t) {
-  return Out{static_cast<uint16_t*>(const_cast<void*>(t.ptr_dev)), t.stride_b, t.stride_s, t.stride_h};
-}
-
 int check_batch(int64_t B, int64_t T) {
   if (B < 0 || T < 0) return SAGE_ERR_SHAPE;
   if (B > kMaxDim || T > kMaxTokens) return SAGE_ERR_TOO_LARGE;
@@ -80,6 +56,19 @@ int check_batch(int64_t B, int64_t T) {
 int check_heads(int64_t H, int64_t Hkv) {
   if (H < 0 || (Hkv == 0 ? H != 0 : H % Hkv != 0)) return SAGE_ERR_SHAPE;
   return H > kMaxDim ? SAGE_ERR_TOO_LARGE : SAGE_OK;
+}
+
+// A call's blocks, all sequences and heads, are counted in 32 bits (once for
+// every 256 query rows that share a key/value head, with 16 more for what
+// beginning a unit counts).
+int check_units(const CacheView& c, const PageTable& pt, int64_t B, int64_t T, int64_t H) {
+  const int64_t seq_blocks = table_capacity(pt.max_pages, c.blocks_per_page) / kCacheBlock + 16;
+  constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+  if (H > 0 && T > kMaxTokens / (H / c.H)) return SAGE_ERR_TOO_LARGE;  // rows of a key/value head, too
+  const int64_t pairs = H > 0 ? div_up(T * (H / c.H), 256) : 0;
+  if (B > 0 && pairs > 0 && (pairs > kMost / (B * c.H) || seq_blocks > kMost / (B * c.H * pairs)))
+    return SAGE_ERR_TOO_LARGE;
+  return SAGE_OK;
 }
 
 }  // namespace
@@ -189,18 +178,9 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
       (rc = check_tensor(args->out)) != SAGE_OK)
     return rc;
   if (a.c.num_pages == 0) a.pt.max_pages = 0;  // without pages there are no tokens, whatever the table says
-  // the call's blocks, all sequences and heads, are counted in 32 bits
-  // (once for every 256 query rows that share a key/value head, with 16 more
-  // for what beginning a unit counts)
-  const int64_t seq_blocks = table_capacity(a.pt.max_pages, a.c.blocks_per_page) / kCacheBlock + 16;
-  constexpr int64_t kMost = (int64_t(1) << 31) - 1;
-  if (H > 0 && T > kMaxTokens / (H / a.c.H)) return SAGE_ERR_TOO_LARGE;  // rows of a key/value head, too
-  const int64_t pairs = H > 0 ? div_up(T * (H / a.c.H), 256) : 0;
-  if (B > 0 && pairs > 0 && (pairs > kMost / (B * a.c.H) || seq_blocks > kMost / (B * a.c.H * pairs)))
-    return SAGE_ERR_TOO_LARGE;
+  if ((rc = check_units(a.c, a.pt, B, T, H)) != SAGE_OK) return rc;
   if (args->lse_dev != nullptr && !aligned(args->lse_dev, 4)) return SAGE_ERR_ALIGN;
-  const float sm = args->sm_scale;
-  if (!(std::isnan(sm) || (std::isfinite(sm) && sm > 0.0f))) return SAGE_ERR_ARG;
+  if (!scale_ok(args->sm_scale)) return SAGE_ERR_ARG;
   const int64_t D = args->cache->D;
   const size_t need = (B == 0 || T == 0 || H == 0) ? 0 : cache_attention_workspace_bytes(B, T, H, a.c.H, D);
   if (need > 0) {
@@ -210,7 +190,6 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
   }
   if ((rc = device_error_word(&a.dev_err)) != SAGE_OK) return rc;
   if (B == 0 || T == 0 || H == 0) return SAGE_OK;
-  const double scale = std::isnan(sm) ? 1.0 / std::sqrt(static_cast<double>(D)) : sm;
   a.lengths = args->lengths_dev;
   a.q_lengths = args->q_lengths_dev;
   a.q = to_in(args->q);
@@ -222,8 +201,94 @@ int sage_cache_attention(const sage_cache_attention_args* args) {
   a.H = static_cast<int32_t>(H);
   a.causal = args->is_causal != 0;
   a.zero_rest = args->zero_rest != 0 && args->q_lengths_dev != nullptr;
-  a.sm_log2 = static_cast<float>(scale * 1.4426950408889634);
+  a.sm_log2 = scale_log2(args->sm_scale, D);
   return cuda_status(launch_cache_attention(a, D, static_cast<cudaStream_t>(args->cuda_stream)));
+}
+
+int sage_cache_add_weights(const sage_cache_add_weights_args* args) {
+  if (args == nullptr) return SAGE_ERR_NULLPTR;
+  CacheWeightsArgs a;
+  int rc;
+  const int64_t B = args->B, T = args->T, H = args->H;
+  if ((rc = check_cache(args->cache, &a.c)) != SAGE_OK || (rc = check_batch(B, T)) != SAGE_OK ||
+      (rc = check_heads(H, a.c.H)) != SAGE_OK ||
+      (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &a.pt)) != SAGE_OK ||
+      (rc = check_ints(args->lengths_dev, true)) != SAGE_OK ||
+      (rc = check_ints(args->q_lengths_dev, false)) != SAGE_OK || (rc = check_tensor(args->q)) != SAGE_OK ||
+      (rc = check_floats(args->lse_dev, true)) != SAGE_OK || (rc = check_floats(args->scores_dev, true)) != SAGE_OK)
+    return rc;
+  if (args->scores_size < 0) return SAGE_ERR_SHAPE;
+  if (a.c.num_pages == 0) a.pt.max_pages = 0;
+  if ((rc = check_units(a.c, a.pt, B, T, H)) != SAGE_OK) return rc;
+  if (!scale_ok(args->sm_scale)) return SAGE_ERR_ARG;
+  if ((rc = device_error_word(&a.dev_err)) != SAGE_OK) return rc;
+  if (B == 0 || T == 0 || H == 0 || a.pt.max_pages == 0) return SAGE_OK;
+  const int64_t D = args->cache->D;
+  a.lengths = args->lengths_dev;
+  a.q_lengths = args->q_lengths_dev;
+  a.q = to_in(args->q);
+  a.lse = args->lse_dev;
+  a.scores = args->scores_dev;
+  a.scores_b = args->scores_stride_b;
+  a.scores_h = args->scores_stride_h;
+  a.scores_n = args->scores_size;
+  a.B = B;
+  a.T = T;
+  a.H = static_cast<int32_t>(H);
+  a.causal = args->is_causal != 0;
+  a.sm_log2 = scale_log2(args->sm_scale, D);
+  return cuda_status(launch_cache_weights(a, D, static_cast<cudaStream_t>(args->cuda_stream)));
+}
+
+int sage_cache_evict_workspace_size(int64_t B, int64_t H, int64_t D, int64_t keep, int64_t scores_size,
+                                    size_t* bytes) {
+  if (bytes == nullptr) return SAGE_ERR_NULLPTR;
+  if (B < 0 || H < 0 || keep < 0 || scores_size < 0) return SAGE_ERR_SHAPE;
+  if (D != 128 && D != 64) return SAGE_ERR_HEAD_DIM;
+  if (B > kMaxDim || H > kMaxDim) return SAGE_ERR_TOO_LARGE;
+  *bytes = cache_evict_workspace_bytes(B, H, D, keep < scores_size ? keep : scores_size);
+  return SAGE_OK;
+}
+
+int sage_cache_evict(const sage_cache_evict_args* args) {
+  if (args == nullptr) return SAGE_ERR_NULLPTR;
+  CacheEvictArgs a;
+  int rc;
+  if ((rc = check_cache(args->cache, &a.c)) != SAGE_OK || (rc = check_batch(args->B, 0)) != SAGE_OK ||
+      (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &a.from)) != SAGE_OK ||
+      (rc = check_table(args->out_table_dev, args->out_table_stride, args->out_max_pages, &a.to)) != SAGE_OK ||
+      (rc = check_ints(args->lengths_dev, true)) != SAGE_OK ||
+      (rc = check_ints(args->lengths_out_dev, true)) != SAGE_OK || (rc = check_ints(args->kept_dev, true)) != SAGE_OK ||
+      (rc = check_floats(args->scores_dev, true)) != SAGE_OK ||
+      (rc = check_floats(args->scores_out_dev, true)) != SAGE_OK)
+    return rc;
+  const int64_t S = args->scores_size, keep = args->keep < S ? args->keep : S;
+  if (S < 0 || args->keep < 0 || args->recent < 0 || args->recent > args->keep || args->kept_size < keep)
+    return SAGE_ERR_SHAPE;
+  if (S > kMaxTokens || args->kept_size > kMaxTokens) return SAGE_ERR_TOO_LARGE;
+  const size_t need = cache_evict_workspace_bytes(args->B, a.c.H, args->cache->D, keep);
+  if (need > 0) {
+    if (args->workspace_dev == nullptr) return SAGE_ERR_NULLPTR;
+    if (!aligned(args->workspace_dev, 256)) return SAGE_ERR_ALIGN;
+    if (args->workspace_bytes < need) return SAGE_ERR_WORKSPACE;
+  }
+  if ((rc = device_error_word(&a.dev_err)) != SAGE_OK) return rc;
+  if (args->B == 0) return SAGE_OK;
+  if (a.c.num_pages == 0) a.from.max_pages = 0;
+  a.lengths = args->lengths_dev;
+  a.scores = args->scores_dev;
+  a.scores_b = args->scores_stride_b;
+  a.scores_h = args->scores_stride_h;
+  a.scores_n = static_cast<int32_t>(S);
+  a.B = args->B;
+  a.keep = static_cast<int32_t>(keep);
+  a.recent = static_cast<int32_t>(args->recent < keep ? args->recent : keep);
+  a.lengths_out = args->lengths_out_dev;
+  a.kept = args->kept_dev;
+  a.kept_n = static_cast<int32_t>(args->kept_size);
+  a.scores_out = args->scores_out_dev;
+  a.workspace = args->workspace_dev;
+  return cuda_status(launch_cache_evict(a, args->cache->D, static_cast<cudaStream_t>(args->cuda_stream)));
 }
 
 }  // extern "C"

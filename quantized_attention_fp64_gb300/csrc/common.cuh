@@ -24,6 +24,8 @@ constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrSmemAlign = 2;
 // A page table, a page list or a length named tokens outside the cache.
 constexpr int kDevErrPage = 3;
+// Offsets of packed sequences decrease or leave the tensor.
+constexpr int kDevErrOffsets = 4;
 
 // One BF16 input: element (b, s, h, d) at p[b*sb + s*ss + h*sh + d].
 struct Bf16In {
