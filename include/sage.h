@@ -680,8 +680,8 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * sequence (in front of offsets[0], from offsets[B] on) are left as they were, or
  * with zero_rest != 0 set to 0 and -inf.
  * offsets, kv_offsets: int32 [B + 1] in device memory, not decreasing, within the
- * tensors. Offsets that break this are cut to what is there, the device error
- * word is set, and rows of out and lse hold anything.
+ * tensors. With offsets that break this no row belongs to a sequence, and the
+ * device error word is set.
  * q, k, v, out: BF16, stride_b is not used; D = 128 or 64; out must not overlap
  * the inputs. sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16

@@ -35,15 +35,4 @@ struct PromptArgs {
 cudaError_t launch_prompt_attention(const PromptArgs& a, int64_t D, cudaStream_t stream);
 size_t prompt_attention_workspace_bytes(int64_t N, int64_t M, int64_t H, int64_t Hkv, int64_t D, int64_t B);
 
-// Rows [lo, hi) that offsets[b], offsets[b + 1] name in a tensor of n rows, cut
-// to what is there; *bad is set when they had to be cut.
-__host__ __device__ inline void packed_rows(int64_t lo, int64_t hi, int64_t n, bool* bad, int32_t* first,
-                                            int32_t* end) {
-  int64_t a = lo < 0 ? 0 : (lo > n ? n : lo), e = hi > n ? n : hi;
-  if (e < a) e = a;
-  if (a != lo || e != hi) *bad = true;
-  *first = static_cast<int32_t>(a);
-  *end = static_cast<int32_t>(e);
-}
-
 }  // namespace sage

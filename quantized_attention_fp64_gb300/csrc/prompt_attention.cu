@@ -1,78 +1,691 @@
-// Attention over packed prompts: a warp has one query row of one head and takes
-// the keys one after another, with the running maximum and sum of the softmax.
-#include <cuda_bf16.h>
+// Attention over packed prompts on the sm_103a tensor cores (tcgen05, TMA, TMEM).
+//
+//   out_t = sum_j p_tj v_j / sum_j p_tj,  p_tj = 2^(c (q_t . k_j - m_t)),  c = sm_scale log2 e
+// over the keys that row t sees: all m of its sequence, or with the causal mask
+// the first m - n + t + 1 (n queries). Both products are BF16 with fp32 sums; P
+// is rounded to BF16, l_t = sum_j p_tj is taken in fp32 before that.
+//
+// A unit of work is one head of 256 consecutive query rows of a sequence: two
+// tiles of 128 rows that share the key tiles (128 keys) that pass through shared
+// memory. A first kernel lists the row blocks of all sequences, those with the
+// most key tiles first; the CTAs, one for each SM, take the units in that order
+// forth and back (0 1 .. 151, 151 .. 1 0, ...), so that each gets about the same
+// work whatever the lengths are. Roles of the 12 warps:
+//   warp 0      TMA: the unit's queries, and a ring of key and value tiles in turn
+//   warps 1, 2  TMEM allocation; the products of query tile 0, 1 (one thread issues)
+//   warp 3      makes value tiles ready that hold keys which some row does not see
+//   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
+// TMEM holds S0, S1, O0, O1: all 512 columns at D = 128. The softmax reads S of a
+// key tile into registers and writes P over it, from where the product with V
+// reads it; that product and the next S = Q K^T are issued together when P is
+// there, so the tensor pipe works on one query tile while the other's softmax runs.
+// The maximum m_t that the exponentials go by follows only when the true one has
+// grown by 2^8: O is rescaled then, a few times at the beginning of a row, and
+// P and l stay within 2^8 of their usual range (no bit is lost in floating point).
+//
+// What a row does not see must not touch it, whatever stands there: its P is 0,
+// but 0 times an infinity or a NaN of V would be a NaN. In the tiles that hold
+// keys which some row of the unit does not see (the diagonal, the sequence's end)
+// warp 3 clears the rows behind the sequence's end and every infinity and NaN,
+// and tells the softmax warps, which then add those values to the rows that do
+// see them (a row's P of a key it sees is positive).
+//
+// Every wait on an mbarrier is bounded; when one runs out the kernel sets the
+// device error word, tells the other roles to stop, lets its copies and products
+// drain, frees its TMEM and returns.
+#include <cuda.h>
 
 #include "launch.cuh"
 #include "prompt.cuh"
-#include "tc_ptx.cuh"
+#include "tc_kernel.cuh"
 
 namespace sage {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kRows = 256;      // query rows of a unit
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8
 
-__device__ __forceinline__ float value(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+// A block of query rows, as the first kernel lists it.
+struct alignas(16) Block {
+  int32_t q0, rows;   // first row of the tensor, rows (1 .. 256)
+  int32_t kv0, keys;  // first key row, keys of the sequence
+  int32_t sees;       // keys that the block's row 0 sees with the causal mask, before it is cut to 0 .. keys
+  int32_t pad[3];
+};
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) prompt_attention_kernel(const PromptArgs a) {
-  constexpr int C = D / 32;
-  tc::griddep_wait();
+struct Header {
+  int32_t blocks;            // entries of the list
+  int32_t rest_lo, rest_hi;  // rows [0, rest_lo) and [rest_hi, N) belong to no sequence
+};
+constexpr size_t kHeaderBytes = 256;
+
+__host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B + 1; }
+
+// Keys that row r of a block sees.
+template <bool kCausal>
+__device__ __forceinline__ int32_t sees(const Block& b, int32_t r) {
+  return kCausal ? max(0, min(b.sees + r, b.keys)) : b.keys;
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t keys) { return keys / kKeys + (keys % kKeys != 0 ? 1 : 0); }
+// Key tiles of query tile i of a block.
+template <bool kCausal>
+__device__ __forceinline__ int32_t key_tiles(const Block& b, int i) {
+  return b.rows <= 128 * i ? 0 : tiles_of(sees<kCausal>(b, min(128 * i + 127, b.rows - 1)));
+}
+
+// ------------------------------------------------------------------ planning --
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+
+// Lists the row blocks of all sequences by their key tiles, the most first (in
+// 1024 classes). Offsets that decrease or leave the tensors: no block, all rows
+// are rest.
+template <bool kCausal>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offsets, const int32_t* kv_offsets, int32_t B,
+                                                            int32_t N, int32_t M, Header* header, Block* list,
+                                                            int* dev_err) {
+  __shared__ int32_t count[kBins];
+  __shared__ int32_t most;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  count[tid] = 0;
+  if (tid == 0) most = 0;
   tc::griddep_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int h = static_cast<int>(blockIdx.y);
-  if (row >= a.N) return;
-  int32_t first = 0, end = 0, kv_first = 0, kv_end = 0;
-  bool bad = false, found = false;
-  for (int b = 0; b < a.B && !found; ++b) {
-    packed_rows(a.offsets[b], a.offsets[b + 1], a.N, &bad, &first, &end);
-    packed_rows(a.kv_offsets[b], a.kv_offsets[b + 1], a.M, &bad, &kv_first, &kv_end);
-    found = row >= first && row < end;
+  tc::griddep_wait();
+  bool bad = false;
+  for (int32_t b = tid; b <= B; b += kPlanThreads) {
+    const int32_t o = offsets[b], k = kv_offsets[b];
+    bad |= o < 0 || o > N || k < 0 || k > M || (b > 0 && (offsets[b - 1] > o || kv_offsets[b - 1] > k));
   }
-  if (bad && lane == 0) atomicExch(a.dev_err, kDevErrOffsets);
-  uint16_t* out = a.out.p + row * a.out.ss + h * a.out.sh;
-  float* lse = a.lse != nullptr ? a.lse + h * a.N + row : nullptr;
-  if (!found) {
-    if (!a.zero_rest) return;
-    for (int c = 0; c < C; ++c) out[lane * C + c] = 0;
-    if (lse != nullptr && lane == 0) *lse = -INFINITY;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      *header = Header{0, 0, 0};
+      atomicExch(dev_err, kDevErrOffsets);
+    }
     return;
   }
-  const int64_t keys = kv_end - kv_first, last = a.causal ? keys - (end - row) : keys - 1;
-  const int hk = h / (a.H / a.Hkv);
-  float q[C], o[C], m = -INFINITY, l = 0.0f;
-  for (int c = 0; c < C; ++c) {
-    q[c] = value(a.q.p[row * a.q.ss + h * a.q.sh + lane * C + c]) * a.sm_log2;
-    o[c] = 0.0f;
+  const auto block_of = [&](int32_t b, int32_t p) {
+    const int32_t q0 = offsets[b], n = offsets[b + 1] - q0, kv0 = kv_offsets[b], m = kv_offsets[b + 1] - kv0;
+    Block e;
+    e.q0 = q0 + p * kRows;
+    e.rows = min(kRows, n - p * kRows);
+    e.kv0 = kv0;
+    e.keys = m;
+    e.sees = m - n + p * kRows + 1;
+    return e;
+  };
+  const auto blocks_of = [&](int32_t b) { return (offsets[b + 1] - offsets[b] + kRows - 1) / kRows; };
+  const auto cost = [&](const Block& e) { return max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1)); };
+  for (int32_t b = tid; b < B; b += kPlanThreads) {
+    const int32_t n = blocks_of(b);
+    if (n > 0) atomicMax(&most, cost(block_of(b, n - 1)));
   }
-  for (int64_t j = 0; j <= last; ++j) {
-    const uint16_t* k = a.k.p + (kv_first + j) * a.k.ss + hk * a.k.sh + lane * C;
-    const uint16_t* v = a.v.p + (kv_first + j) * a.v.ss + hk * a.v.sh + lane * C;
-    float z = 0.0f;
-    for (int c = 0; c < C; ++c) z = fmaf(q[c], value(k[c]), z);
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    const float up = fmaxf(m, z);
-    const float alpha = exp2f(m - up), p = exp2f(z - up);
-    m = up;
-    l = l * alpha + p;
-    for (int c = 0; c < C; ++c) o[c] = fmaf(p, value(v[c]), o[c] * alpha);
+  __syncthreads();
+  const int64_t top = max(most, 1);
+  const auto bin = [&](const Block& e) { return kBins - 1 - static_cast<int>(cost(e) * int64_t(kBins - 1) / top); };
+  for (int32_t b = warp; b < B; b += kPlanThreads / 32)
+    for (int32_t p = lane, n = blocks_of(b); p < n; p += 32) atomicAdd(&count[bin(block_of(b, p))], 1);
+  __syncthreads();
+  // where each class begins: a sum over the classes before it
+  const int32_t own = count[tid];
+  int32_t sum = own;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, sum, s);
+    if (lane >= s) sum += x;
   }
-  for (int c = 0; c < C; ++c) {
-    const __nv_bfloat16 r = __float2bfloat16_rn(last >= 0 ? o[c] / l : 0.0f);
-    out[lane * C + c] = *reinterpret_cast<const uint16_t*>(&r);
+  __shared__ int32_t warps[32];
+  if (lane == 31) warps[warp] = sum;
+  __syncthreads();
+  int32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += warps[w];
+  count[tid] = before + sum - own;
+  if (tid == kPlanThreads - 1) *header = Header{before + sum, offsets[0], offsets[B]};
+  __syncthreads();
+  for (int32_t b = warp; b < B; b += kPlanThreads / 32)
+    for (int32_t p = lane, n = blocks_of(b); p < n; p += 32) {
+      const Block e = block_of(b, p);
+      list[atomicAdd(&count[bin(e)], 1)] = e;
+    }
+}
+
+// ----------------------------------------------------------------- attention --
+
+template <int D>
+struct Smem {
+  static constexpr uint32_t kSub = 128 * 128;          // 64 channels of 128 rows
+  static constexpr uint32_t kTile = 128 * D * 2;       // 128 rows
+  static constexpr int kStages = D == 128 ? 5 : 10;    // key and value tiles in the ring
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr uint32_t kOffBar = kOffRing + kStages * kTile;
+  // barriers
+  static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kDrain = 12;
+  static constexpr int kRaw = 14, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
+  static constexpr int kFull = kFix + kFixes, kEmpty = kFull + kStages, kBars = kEmpty + kStages;
+  static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
+  static constexpr uint32_t kOffAbort = kOffTmem + 4;
+  static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
+  static constexpr uint32_t kBytes = kOffBad + 4 * kFixes;
+};
+static_assert(Smem<128>::kBytes <= 232448u && Smem<64>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
+
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t col_s(int i) { return 128u * static_cast<uint32_t>(i); }
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int i) { return 256u + static_cast<uint32_t>(D) * static_cast<uint32_t>(i); }
+
+constexpr uint32_t kCtlRegs = 88, kSoftmaxRegs = 208;
+static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs <= kThreads * 168, "registers of one CTA");
+
+struct Params {
+  const Header* header;
+  const Block* list;
+  Out out;
+  const uint16_t* v;
+  int64_t v_ss, v_sh;
+  float* lse;
+  int64_t N;
+  int32_t H, group;     // query heads, and those that share a key/value head
+  bool zero_rest;
+  float scale;          // c
+  int* dev_err;
+};
+
+// The CTA's i-th unit (the list's blocks times the heads, heads innermost), or -1.
+__device__ __forceinline__ int32_t unit_at(int32_t i, int32_t units) {
+  const int32_t g = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
+  if (i > (units - 1) / g) return -1;
+  const int32_t u = i * g + ((i & 1) ? g - 1 - c : c);
+  return u < units ? u : -1;
+}
+
+__device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
+  const int4* p = reinterpret_cast<const int4*>(list + e);
+  const int4 a = p[0];
+  Block b;
+  b.q0 = a.x;
+  b.rows = a.y;
+  b.kv0 = a.z;
+  b.keys = a.w;
+  b.sees = list[e].sees;
+  return b;
+}
+
+// Infinities and NaN of the BF16 pair in each word: the sign bits of the result.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; }
+
+// One key tile of the softmax for the thread's query row: S into registers, the
+// maximum, P over S. lim: keys of the tile that the row sees (kMask: fewer than
+// all for some row). Returns whether the rows of the warp go by a new maximum,
+// and the factor alpha for O.
+template <int D, bool kMask>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float c, int lim, bool first, float& m,
+                                             float& neg, float& l) {
+  uint32_t s[4][32];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) tc::tmem_ld32(tS + 32u * b, s[b]);
+  tc::tmem_wait_ld();
+  if (kMask) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (32 * b + k >= lim) s[b][k] = 0xFF800000u;  // -inf
   }
-  if (lse != nullptr && lane == 0) *lse = last >= 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+  float mx[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    mx[b] = __uint_as_float(s[b][0]);
+#pragma unroll
+    for (int k = 1; k < 31; k += 2) mx[b] = tc::max3(mx[b], __uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1]));
+    mx[b] = fmaxf(mx[b], __uint_as_float(s[b][31]));
+  }
+  const float up = fmaxf(tc::max3(mx[0], mx[1], mx[2]), mx[3]);
+  // (up - m) c > 8; with m = -inf whenever the row has seen a key
+  if (__any_sync(0xffffffffu, fmaf(up, c, neg) > kGrowth || (m == -INFINITY && up != -INFINITY))) {
+    const float m_new = fmaxf(m, up);
+    const float neg_new = m_new == -INFINITY ? 0.0f : -m_new * c;
+    if (!first) {
+      // a row that had seen nothing has O = 0 and l = 0
+      const float alpha = m == -INFINITY ? 0.0f : tc::exp2_approx(neg_new - neg);
+      l *= alpha;
+      const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        tc::tmem_ld32(tO + 32u * x, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float2 r = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), a2);
+          o[k] = __float_as_uint(r.x);
+          o[k + 1] = __float_as_uint(r.y);
+        }
+        tc::tmem_st32(tO + 32u * x, o);
+      }
+    }
+    m = m_new;
+    neg = neg_new;
+  }
+  const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+  float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    uint32_t p[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1])), c2, n2);
+      const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[b][k + 2]), __uint_as_float(s[b][k + 3])), c2, n2);
+      const float2 p01 = make_float2(tc::exp2_approx(x01.x), tc::exp2_approx(x01.y));
+      const float2 p23 = make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y));
+      sa = __fadd2_rn(sa, p01);
+      sb = __fadd2_rn(sb, p23);
+      p[k / 2] = tc::bf16x2(p01.x, p01.y);
+      p[k / 2 + 1] = tc::bf16x2(p23.x, p23.y);
+    }
+    tc::tmem_st16(tS + 16u * b, p);
+  }
+  l += (sa.x + sa.y) + (sb.x + sb.y);
+  tc::tmem_wait_st();
+}
+
+template <int D, bool kCausal>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const Params prm) {
+  using L = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((tc::smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicExch(prm.dev_err, kDevErrSmemAlign);
+    return;
+  }
+  const uint32_t sbase = tc::smem_u32(smem);
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), prm.dev_err};
+  volatile int32_t* bad_units = reinterpret_cast<volatile int32_t*>(smem + L::kOffBad);
+  if (threadIdx.x == 0) {
+    *w.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(w.bar(L::kQFull + i), 1);
+      tc::mbar_init(w.bar(L::kQEmpty + i), 1);
+      tc::mbar_init(w.bar(L::kSFull + i), 1);
+      tc::mbar_init(w.bar(L::kPFull + i), 128);
+      tc::mbar_init(w.bar(L::kOFull + i), 1);
+      tc::mbar_init(w.bar(L::kOEmpty + i), 128);
+      tc::mbar_init(w.bar(L::kDrain + i), 1);
+    }
+    for (int i = 0; i < 2 * kFixes; ++i) tc::mbar_init(w.bar(L::kRaw + i), 1);
+    for (int i = 0; i < L::kStages; ++i) {
+      tc::mbar_init(w.bar(L::kFull + i), 1);
+      tc::mbar_init(w.bar(L::kEmpty + i), 2);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(sbase + L::kOffTmem, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int32_t units = prm.header->blocks * prm.H;
+
+  if (warp < 4) {
+    tc::regs_dec<kCtlRegs>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- copies --
+      if (lane == 0) {
+        uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
+        int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
+        bool ok = true;
+        for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
+          const Block e = load_block(prm.list, u / prm.H);
+          const int32_t h = u % prm.H, hk = h / prm.group;
+          const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
+          const auto queries = [&](int t) {
+            if (!(ok = wait_bar(w, w.bar(L::kQEmpty + t), (q_cnt[t] & 1u) ^ 1u))) return;
+            ++q_cnt[t];
+            tc::mbar_arrive_expect_tx(w.bar(L::kQFull + t), L::kTile);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, h, e.q0 + 128 * t,
+                              w.bar(L::kQFull + t));
+          };
+          const int32_t masked = sees<kCausal>(e, 0) / kKeys;  // value tiles from here on pass through warp 3
+          const auto tile = [&](const void* map, int32_t j, bool through) {
+            const uint32_t st = at % L::kStages;
+            if (!(ok = wait_bar(w, w.bar(L::kEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) return;
+            ++at;
+            raw[st] = through ? static_cast<int32_t>(fixes % (2 * kFixes)) : -1;
+            const uint32_t full = w.bar(through ? L::kRaw + static_cast<int>(fixes++ % kFixes) : L::kFull + static_cast<int>(st));
+            tc::mbar_arrive_expect_tx(full, L::kTile);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tc::tma_load_3d(sbase + L::kOffRing + st * L::kTile + x * L::kSub, map, 64 * x, hk, e.kv0 + j * kKeys, full);
+          };
+          // the first tile's queries and keys before the second's
+          if (n0 > 0) queries(0);
+          for (int32_t j = 0; ok && j < n; ++j) {
+            tile(&tm_k, j, false);
+            if (j == 0 && ok && n1 > 0) queries(1);
+            if (ok) tile(&tm_v, j, j >= masked);
+          }
+        }
+        if (!ok) {
+          // every copy that this thread issued lands before the CTA exits
+          const tc::Waits d = w.draining();
+          for (int t = 0; t < 2; ++t)
+            if (q_cnt[t] > 0) wait_bar(d, w.bar(L::kQFull + t), (q_cnt[t] - 1) & 1u);
+          for (uint32_t p = at < L::kStages ? 0 : at - L::kStages; p < at; ++p) {
+            const int32_t f = raw[p % L::kStages];
+            if (f < 0) wait_bar(d, w.bar(L::kFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
+            else wait_bar(d, w.bar(L::kRaw + f % kFixes), static_cast<uint32_t>(f / kFixes) & 1u);
+          }
+        }
+      }
+    } else if (warp <= 2) {
+      // ------------------------------------------------ products of tile t --
+      const int t = warp - 1;
+      const bool leader = tc::elect_one();
+      const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o<D>(t);
+      const uint64_t dq = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(t) * L::kTile);
+      const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffRing), dv0 = tc::sw128_mn_desc(sbase + L::kOffRing, L::kSub);
+      uint32_t base = 0, q_cnt = 0, p_cnt = 0, done = 0;  // ring position of the unit's first tile; queries, P, units with keys so far
+      const auto full = [&](uint32_t p) {
+        return wait_bar_warp(w, w.bar(L::kFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
+      };
+      const auto empty = [&](uint32_t p) { return w.bar(L::kEmpty + static_cast<int>(p % L::kStages)); };
+      const auto product_s = [&](uint32_t p) {
+        const uint64_t dk = tc::desc_at(dk0, (p % L::kStages) * L::kTile);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = static_cast<uint32_t>(ks >> 2) * L::kSub + static_cast<uint32_t>(ks & 3) * 32u;
+          tc::mma_f16_ss(d_s, tc::desc_at(dq, off), tc::desc_at(dk, off), tc::IdescBf16<kKeys>::value, ks > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(w.bar(L::kSFull + t));
+        tc::mma_commit(empty(p));
+      };
+      bool ok = true;
+      for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
+        const Block e = load_block(prm.list, u / prm.H);
+        const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
+        if (own > 0) {
+          if (!(ok = wait_bar_warp(w, w.bar(L::kQFull + t), q_cnt & 1u)) || !(ok = full(base))) break;
+          tc::tc_fence_after();
+          if (leader) {
+            product_s(base);
+            if (own == 1) tc::mma_commit(w.bar(L::kQEmpty + t));
+          }
+          __syncwarp();
+        }
+        for (int32_t j = 0; j < n; ++j) {
+          const uint32_t pk = base + 2u * static_cast<uint32_t>(j), pv = pk + 1u;
+          if (!(ok = full(pv))) break;
+          // the softmax warps are through with the unit before: its O, and what warp 3 has told them
+          if (j == 0 && !(ok = wait_bar_warp(w, w.bar(L::kOEmpty + t), (done & 1u) ^ 1u))) break;
+          if (j < own) {
+            if (!(ok = wait_bar_warp(w, w.bar(L::kPFull + t), p_cnt & 1u))) break;
+            ++p_cnt;
+            if (j + 1 < own && !(ok = full(pk + 2u))) break;
+            tc::tc_fence_after();
+            if (leader) {
+              const uint64_t dv = tc::desc_at(dv0, (pv % L::kStages) * L::kTile);
+#pragma unroll
+              for (int ks = 0; ks < kKeys / 16; ++ks)
+                tc::mma_f16_ts(d_o, d_s + 8u * ks, tc::desc_at(dv, 2048u * ks), tc::IdescBf16<D, true>::value,
+                               (j > 0 || ks > 0) ? 1u : 0u);
+              tc::mma_commit(empty(pv));
+              if (j + 1 < own) {
+                product_s(pk + 2u);
+                if (j + 2 == own) tc::mma_commit(w.bar(L::kQEmpty + t));
+              } else {
+                tc::mma_commit(w.bar(L::kOFull + t));
+              }
+            }
+          } else {
+            // a key tile that only the other query tile sees
+            if (!(ok = full(pk))) break;
+            if (leader) {
+              tc::mbar_arrive(empty(pk));
+              tc::mbar_arrive(empty(pv));
+              if (own == 0 && j == 0) tc::mbar_arrive(w.bar(L::kOFull + t));
+            }
+          }
+          __syncwarp();
+        }
+        if (own > 0) ++q_cnt;
+        if (n > 0) ++done;
+        base += 2u * static_cast<uint32_t>(n);
+      }
+      // all products are done before TMEM is freed
+      if (leader) tc::mma_commit(w.bar(L::kDrain + t));
+      __syncwarp();
+      wait_bar(w.draining(), w.bar(L::kDrain + t), 0);
+    } else {
+      // ---------------------------------------- value tiles with hidden keys --
+      uint32_t base = 0, fixes = 0, done = 0;
+      bool ok = true;
+      for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
+        const Block e = load_block(prm.list, u / prm.H);
+        const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
+        bool bad = false;
+        for (int32_t j = sees<kCausal>(e, 0) / kKeys; j < n; ++j) {
+          const uint32_t p = base + 2u * static_cast<uint32_t>(j) + 1u;
+          if (!(ok = wait_bar_warp(w, w.bar(L::kRaw + static_cast<int>(fixes % kFixes)), (fixes / kFixes) & 1u))) break;
+          uint8_t* tile = smem + L::kOffRing + (p % L::kStages) * L::kTile;
+          const int32_t there = min(kKeys, e.keys - j * kKeys);
+          // rows of 128 bytes: row r of the 64 channels x at r * 128 + x * kSub
+          for (int x = 0; x < D / 64; ++x) {
+            uint4* chunk = reinterpret_cast<uint4*>(tile + x * L::kSub);
+            if (kCausal) {
+#pragma unroll 4
+              for (int q = lane; q < there * 8; q += 32) {
+                const uint4 v = chunk[q];
+                if ((not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) & 0x80008000u) {
+                  bad = true;
+                  uint32_t o[4] = {v.x, v.y, v.z, v.w};
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t f = not_finite(o[k]) & 0x80008000u;
+                    if (f & 0x8000u) o[k] &= 0xFFFF0000u;
+                    if (f & 0x80000000u) o[k] &= 0x0000FFFFu;
+                  }
+                  chunk[q] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+              }
+            }
+            for (int q = there * 8 + lane; q < kKeys * 8; q += 32) chunk[q] = make_uint4(0, 0, 0, 0);
+          }
+          bad = __any_sync(0xffffffffu, bad);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bad_units[done % kFixes] = bad ? 1 : 0;
+            tc::mbar_arrive(w.bar(L::kFix + static_cast<int>(fixes % kFixes)));
+            tc::mbar_arrive(w.bar(L::kFull + static_cast<int>(p % L::kStages)));
+          }
+          __syncwarp();
+          ++fixes;
+        }
+        base += 2u * static_cast<uint32_t>(n);
+        if (n > 0) ++done;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------------- softmax --
+    tc::regs_inc<kSoftmaxRegs>();
+    const int t = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + col_s(t), tO = tmem + lanes + col_o<D>(t);
+    uint32_t s_cnt = 0, fixes = 0, done = 0;
+    if (prm.zero_rest) {
+      const int32_t lo = prm.header->rest_lo, hi = prm.header->rest_hi;
+      const int64_t rest = lo + (prm.N - hi), chunks = rest * prm.H * (D / 8);
+      const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+      for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x - 128); x < chunks; x += step) {
+        const int64_t c = x % (D / 8), h = x / (D / 8) % prm.H, at = x / (D / 8) / prm.H;
+        const int64_t r = at < lo ? at : hi + (at - lo);
+        *reinterpret_cast<uint4*>(prm.out.p + r * prm.out.ss + h * prm.out.sh + 8 * c) = make_uint4(0, 0, 0, 0);
+        if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
+      }
+    }
+    bool ok = true;
+    for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
+      const Block e = load_block(prm.list, u / prm.H);
+      const int32_t h = u % prm.H;
+      const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
+      const int32_t r = 128 * t + row, mine = sees<kCausal>(e, r), all = sees<kCausal>(e, 128 * t) / kKeys;
+      float m = -INFINITY, neg = 0.0f, l = 0.0f;
+      for (int32_t j = 0; j < own; ++j) {
+        if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
+        ++s_cnt;
+        tc::tc_fence_after();
+        if (j < all)
+          softmax_tile<D, false>(tS, tO, prm.scale, kKeys, j == 0, m, neg, l);
+        else
+          softmax_tile<D, true>(tS, tO, prm.scale, mine - j * kKeys, j == 0, m, neg, l);
+        tc::tc_fence_before();
+        tc::mbar_arrive(w.bar(L::kPFull + t));
+      }
+      if (!ok) break;
+      // infinities and NaN that warp 3 has cleared
+      bool bad = false;
+      if (kCausal) {
+        const int32_t masked = sees<kCausal>(e, 0) / kKeys;
+        if (n > masked) {
+          fixes += static_cast<uint32_t>(n - masked);
+          if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>((fixes - 1) % kFixes)), ((fixes - 1) / kFixes) & 1u)))
+            break;
+          bad = own > 0 && bad_units[done % kFixes] != 0;
+        }
+      }
+      if (n > 0) {
+        if (!(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
+        ++done;
+        tc::tc_fence_after();
+      }
+      const bool valid = r < e.rows;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (valid && prm.lse != nullptr)
+        prm.lse[static_cast<int64_t>(h) * prm.N + e.q0 + r] = l == 0.0f ? -INFINITY : (log2f(l) - neg) * kLn2;
+      uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + h * prm.out.sh;
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        if (own > 0) {
+          tc::tmem_ld32(tO + 32u * x, o);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (x == D / 32 - 1 && n > 0) {
+          tc::tc_fence_before();
+          tc::mbar_arrive(w.bar(L::kOEmpty + t));
+        }
+        if (kCausal && bad) {
+          const int32_t first = sees<kCausal>(e, 0) / kKeys * kKeys;
+          for (int32_t k = first; k < mine; ++k) {
+            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + h / prm.group * prm.v_sh + 32 * x;
+            for (int y = 0; y < 32; ++y) {
+              const uint32_t b = v[y];
+              if ((b & 0x7F80u) == 0x7F80u) {
+                // an index known at compile time keeps o in registers
+#pragma unroll
+                for (int z = 0; z < 32; ++z)
+                  if (z == y) o[z] = __float_as_uint(__uint_as_float(o[z]) + __uint_as_float(b << 16));
+              }
+            }
+          }
+        }
+        if (valid) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pk[k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * x + 8 * q) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+      }
+    }
+    tc::regs_dec<kCtlRegs>();
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Rows of one head of a packed tensor: boxes of 64 channels x 128 rows, 128-byte swizzle.
+bool make_map(CUtensorMap* map, const Bf16In& x, int64_t rows, int64_t heads, int64_t D) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows)};
+  // (strides of one head or row are not used; the driver wants valid ones)
+  const uint64_t strides[2] = {static_cast<uint64_t>(heads > 1 ? x.sh : D) * 2, static_cast<uint64_t>(rows > 1 ? x.ss : D) * 2};
+  const uint32_t box[3] = {64, 1, 128};
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D>
+cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
+  const int64_t rows = a.M > 0 ? a.M : 1;  // a tensor without rows is not read
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, a.q, a.N, a.H, D) || !make_map(&tk, a.k, rows, a.Hkv, D) || !make_map(&tv, a.v, rows, a.Hkv, D))
+    return cudaErrorInvalidValue;
+  Header* header = static_cast<Header*>(a.workspace);
+  Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
+  cudaError_t e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPlanThreads, 0, stream,
+                                   a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N), static_cast<int32_t>(a.M),
+                                   header, list, a.dev_err);
+  if (e != cudaSuccess) return e;
+  Params p;
+  p.header = header;
+  p.list = list;
+  p.out = a.out;
+  p.v = a.v.p;
+  p.v_ss = a.v.ss;
+  p.v_sh = a.v.sh;
+  p.lse = a.lse;
+  p.N = a.N;
+  p.H = a.H;
+  p.group = a.H / a.Hkv;
+  p.zero_rest = a.zero_rest;
+  p.scale = a.sm_log2;
+  p.dev_err = a.dev_err;
+  const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;
+  const int bytes = static_cast<int>(Smem<D>::kBytes);
+  if ((e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes)) != cudaSuccess) return e;
+  const int64_t units = most_blocks(a.N, a.B) * a.H, sms = sm_count_current();
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads,
+                          static_cast<size_t>(bytes), stream, tq, tk, tv, p);
 }
 
 }  // namespace
 
-size_t prompt_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t prompt_attention_workspace_bytes(int64_t N, int64_t, int64_t, int64_t, int64_t, int64_t B) {
+  return (kHeaderBytes + static_cast<size_t>(most_blocks(N, B)) * sizeof(Block) + 255) / 256 * 256;
+}
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int64_t D, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(div_up(a.N, kThreads / 32)), static_cast<unsigned>(a.H));
-  return launch_dependent(D == 128 ? prompt_attention_kernel<128> : prompt_attention_kernel<64>, grid, kThreads, 0,
-                          stream, a);
+  return D == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
 }
 
 }  // namespace sage

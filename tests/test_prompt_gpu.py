@@ -1,0 +1,353 @@
+"""Attention over packed prompts on the GPU against the formula in float64.
+
+Outputs are held to a bound that is derived, not fitted. With A = sum_j p_j |v_j| / sum_j p_j (in float64),
+an output differs from the formula by at most
+  2^-8 |o|    its rounding to bf16 (half a step), where |o| itself may be off by the rest,
+  2^-8 A      the rounding of the weights to bf16 (half a step),
+  2^-12 A     logits: D products of bf16, exact in fp32, whose sum errs by at most D 2^-23 sum |q k| sm_scale
+              < 128 2^-23 12 < 2^-12.4 as an absolute error of the logit here, once in p and once in the sum of p,
+              together below 2^-11 A; and exponentials (2^-22) and the fp32 sums of p (at most m 2^-24 < 2^-12),
+together below 2^-8 |o| + (2^-8 + 2^-10) A + a little of the product of both, for which 2^-8 |o| becomes
+2^-8 (|o| + A / 64). The log-sum-exp errs by the logits' 2^-12.4, the sum's 2^-12 and roundings of numbers below
+32 (2^-19 each): 2^-11 in all.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_attention_fp64_gb300 as sage
+from quantized_attention_fp64_gb300.api import SageError
+
+pytestmark = pytest.mark.gpu
+
+DEVICE_OFFSETS = -17
+
+
+@pytest.fixture(autouse=True)
+def _library(sage_lib):
+    torch.cuda.synchronize()
+    sage.device_error()
+    yield
+    torch.cuda.synchronize()
+    assert sage.device_error() == 0  # a test that expects one has read and cleared it
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bf16(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def ends(sizes):
+    return [0] + np.cumsum(sizes).tolist()
+
+
+def formula(q, k, v, rows, keys, causal, sm):
+    """(o, lse, A) in float64 of sequences with these rows and keys; rows of no sequence are 0 and -inf."""
+    N, H, D = q.shape
+    G = H // k.shape[1]
+    o = torch.zeros((N, H, D), dtype=torch.float64, device="cuda")
+    a = torch.zeros_like(o)
+    lse = torch.full((H, N), -math.inf, dtype=torch.float64, device="cuda")
+    qd, kd, vd = q.double(), k.double(), v.double()
+    at = kv = 0
+    for n, m in zip(rows, keys):
+        if n and m:
+            x = qd[at:at + n].permute(1, 0, 2)
+            kk, vv = (t[kv:kv + m].permute(1, 0, 2).repeat_interleave(G, 0) for t in (kd, vd))
+            z = x @ kk.transpose(1, 2) * sm
+            if causal:
+                hidden = torch.arange(m, device="cuda") > torch.arange(n, device="cuda")[:, None] + (m - n)
+                z = torch.where(hidden, -math.inf, z)
+            top = z.amax(-1, keepdim=True)
+            p = torch.where(torch.isinf(top) & (top < 0), 0.0, torch.exp(z - top))
+            l = p.sum(-1, keepdim=True)
+            # 0 weights times what a row does not see count as 0
+            none = l == 0
+            pn = p / torch.where(none, 1.0, l)
+            o[at:at + n] = (pn @ vv).permute(1, 0, 2)
+            a[at:at + n] = (pn @ vv.abs()).permute(1, 0, 2)
+            lse[:, at:at + n] = torch.where(none, -math.inf, top + torch.log(l))[..., 0]
+        at, kv = at + n, kv + m
+    return o, lse, a
+
+
+def close(out, lse, ref):
+    o, l, a = ref
+    err = (out.double() - o).abs()
+    bound = (o.abs() + a / 64) * 2.0 ** -8 + a * (2.0 ** -8 + 2.0 ** -10) + 1e-30
+    worst = (err / bound).max().item() if err.numel() else 0.0
+    assert not torch.isnan(out).any() and worst <= 1.0, worst
+    if lse is not None:
+        there = torch.isfinite(l)
+        assert torch.equal(there, torch.isfinite(lse)) and (lse[~there] == -math.inf).all()
+        assert not there.any() or (lse.double() - l)[there].abs().max() <= 2.0 ** -11
+
+
+# rows of each sequence, keys of each (None: the same), query heads, key/value heads, head dimension, causal
+CASES = [
+    ([1], None, 1, 1, 128, True),
+    ([1, 1, 1], None, 4, 2, 64, True),
+    ([2, 127, 128, 129], None, 2, 1, 128, True),
+    ([255, 256, 257], None, 2, 2, 64, True),
+    ([0, 5, 0, 0, 300, 0], None, 4, 4, 128, True),
+    ([513, 1, 700], None, 7, 1, 128, True),
+    ([1000, 17], None, 5, 5, 64, False),
+    ([128, 384, 33], None, 8, 2, 128, False),
+    ([1, 7, 130], [400, 7, 131], 4, 1, 128, True),     # a prompt that goes on: more keys than rows
+    ([300, 40, 3], [100, 0, 1], 2, 1, 128, True),      # rows that see no key
+    ([300, 260], [0, 5], 2, 2, 64, True),
+    ([9, 0, 200], [1000, 50, 0], 6, 2, 64, False),
+    ([1] * 70 + [129] * 5, None, 3, 1, 128, True),     # more sequences than a warp has lanes
+    ([2500], None, 2, 1, 128, True),
+    ([1900, 2100], None, 1, 1, 64, True),
+    ([40, 4000], [4100, 4001], 2, 1, 128, False),
+]
+
+
+def inputs(seed, rows, keys, H, Hkv, D, spare=0):
+    g = gen(seed)
+    q, k, v = bf16(g, sum(rows) + spare, H, D), bf16(g, sum(keys) + spare, Hkv, D), bf16(g, sum(keys) + spare, Hkv, D)
+    return q, k, v
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_prompt_attention(case):
+    rows, keys, H, Hkv, D, causal = CASES[case]
+    same, keys = keys is None, keys or rows
+    q, k, v = inputs(case, rows, keys, H, Hkv, D)
+    out, lse = sage.prompt_attention(q, k, v, ints(ends(rows)), kv_offsets=None if same else ints(ends(keys)),
+                                     is_causal=causal, return_lse=True)
+    close(out, lse, formula(q, k, v, rows, keys, causal, 1 / math.sqrt(D)))
+    again = sage.prompt_attention(q, k, v, ints(ends(rows)), kv_offsets=None if same else ints(ends(keys)), is_causal=causal)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_layouts_strides_and_scale(D, causal):
+    rows, H, Hkv = [140, 3, 260], 4, 2
+    N = sum(rows)
+    g = gen(50)
+    fused = bf16(g, N, H + 2 * Hkv, D + 8)          # queries, keys and values of one projection, rows wider than a head
+    q, k, v = fused[:, :H, :D], fused[:, H:H + Hkv, :D], fused[:, H + Hkv:, :D]
+    ref = formula(q, k, v, rows, rows, causal, 0.2)
+    out, lse = sage.prompt_attention(q, k, v, ints(ends(rows)), is_causal=causal, sm_scale=0.2, return_lse=True)
+    close(out, lse, ref)
+    hnd = [t.transpose(0, 1).contiguous() for t in (q, k, v)]
+    out, lse = sage.prompt_attention(*hnd, ints(ends(rows)), is_causal=causal, sm_scale=0.2, return_lse=True, tensor_layout="HND")
+    close(out.transpose(0, 1), lse, ref)
+    wide = torch.full((N, H, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    sage.prompt_attention(q, k, v, ints(ends(rows)), is_causal=causal, sm_scale=0.2, out=wide[:, :, D:])
+    close(wide[:, :, D:], None, ref)
+    assert (wide[:, :, :D] == 7.0).all()
+
+
+def test_one_key_head_shared_without_copies():
+    rows = [200, 100]
+    g = gen(51)
+    q, k, v = bf16(g, 300, 4, 128), bf16(g, 300, 1, 128), bf16(g, 300, 1, 128)
+    out = sage.prompt_attention(q, k, v, ints(ends(rows)))
+    close(out, None, formula(q, k, v, rows, rows, True, 1 / math.sqrt(128)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rest_rows(D):
+    rows, spare = [70, 0, 200], 45
+    q, k, v = inputs(60, rows, rows, 3, 1, D, spare)
+    off = ints([20 + x for x in ends(rows)])        # rows in front of the first sequence, and behind the last
+    for t in (q, k, v):
+        t[:20] = math.nan
+        t[290:] = math.inf
+    ref = formula(q[20:290], k[20:290], v[20:290], rows, rows, True, 1 / math.sqrt(D))
+    out, lse = sage.prompt_attention(q, k, v, off, return_lse=True)
+    close(out[20:290], lse[:, 20:290], ref)
+    rest = torch.cat([torch.arange(20), torch.arange(290, 270 + spare)]).cuda()
+    assert (out[rest] == 0).all() and (lse[:, rest] == -math.inf).all()
+    given = torch.full_like(q, 3.0)
+    out, lse = sage.prompt_attention(q, k, v, off, return_lse=True, out=given)
+    assert out is given and (given[rest] == 3.0).all() and (lse[:, rest] == -math.inf).all()
+    close(given[20:290], lse[:, 20:290], ref)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_what_a_row_does_not_see_does_not_touch_it(what, D):
+    rows, H, Hkv = [200, 129, 513], 2, 1
+    q, k, v = inputs(70, rows, rows, H, Hkv, D)
+    ref = formula(q, k, v, rows, rows, True, 1 / math.sqrt(D))
+    # a later token's key and value, in the same key tile as earlier rows and in later tiles
+    k2, v2 = k.clone(), v.clone()
+    spots = [150, 199, 200 + 128, 329 + 130, 329 + 512]
+    for s in spots:
+        k2[s], v2[s, 0, 5:9] = what, what
+    out, lse = sage.prompt_attention(q, k2, v2, ints(ends(rows)), return_lse=True)
+    at = 0
+    for n, first in zip(rows, (150, 328, 459)):
+        close(out[at:first], lse[:, at:first], [r[at:first] if r.dim() == 3 and r.shape[0] == sum(rows) else r[:, at:first] for r in ref])
+        at += n
+    if math.isnan(what):
+        assert torch.isnan(lse[:, 150:200]).all() and torch.isnan(lse[:, 328]).all() and torch.isnan(lse[:, 459:]).all()
+        assert torch.isnan(out[150:200]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,past", [([300, 77], [0, 0]), ([60, 400], [200, 61])])
+def test_infinite_values_reach_the_rows_that_see_them(rows, past, D):
+    keys = [n + p for n, p in zip(rows, past)]
+    H, Hkv = 4, 2
+    q, k, v = inputs(71, rows, keys, H, Hkv, D)
+    ref = formula(q, k, v, rows, keys, True, 1 / math.sqrt(D))
+    v2 = v.clone()
+    marks = [(0, 3, 0, math.inf), (0, keys[0] - 30, 1, -math.inf), (0, keys[0] - 1, D - 1, math.nan), (1, keys[1] // 2, 33, math.inf),
+             (1, keys[1] - 20, 33, -math.inf), (1, keys[1] - 2, 7, math.inf)]
+    start = ends(keys)
+    for b, j, c, x in marks:
+        v2[start[b] + j, :, c] = x
+    out = sage.prompt_attention(q, k, v2, ints(ends(rows)), kv_offsets=ints(ends(keys)))
+    want = ref[0].clone()
+    at = 0
+    for b, n in enumerate(rows):
+        for t in range(n):
+            for bb, j, c, x in marks:
+                if bb == b and j <= past[b] + t:
+                    want[at + t, :, c] += x
+        at += n
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out[odd & ~torch.isnan(want)].double(), want[odd & ~torch.isnan(want)])
+    err = (out.double() - ref[0]).abs()
+    bound = (ref[0].abs() + ref[2] / 64) * 2.0 ** -8 + ref[2] * (2.0 ** -8 + 2.0 ** -10)
+    # the marked value itself is no longer part of the other channels' sums, and theirs are as before
+    assert (err[~odd] <= bound[~odd]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_growing_and_falling_logits(D):
+    # the running maximum has to follow, early and late, by little and by much
+    n = 700
+    g = gen(72)
+    q, k, v = (bf16(g, n, 2, D) for _ in range(3))
+    for shape in (torch.linspace(-3, 3, n), torch.linspace(3, -3, n), torch.sin(torch.arange(n) / 9.0) * 3):
+        kk = (k.float() * 0.1 + q.mean(0) + shape.cuda()[:, None, None]).to(torch.bfloat16)
+        qq = (q.float() * 0.1 + 1.0).to(torch.bfloat16)
+        sm = 1 / math.sqrt(D) / 2
+        ref = formula(qq, kk, v, [n], [n], True, sm)
+        assert (qq.float().abs().amax() * kk.float().abs().amax() * D * sm) < 120
+        out, lse = sage.prompt_attention(qq, kk, v, ints([0, n]), sm_scale=sm, return_lse=True)
+        # sum |q k| sm_scale is up to 60 here, five times the bound's: logits err by up to 2^-10
+        o, l, a = ref
+        assert ((out.double() - o).abs() <= (o.abs() + a / 64) * 2.0 ** -8 + a * (2.0 ** -8 + 2.0 ** -8)).all()
+        assert ((lse.double() - l).abs() <= 2.0 ** -9).all()
+
+
+def test_peaked_rows_take_one_value():
+    n, D = 300, 128
+    g = gen(73)
+    v = bf16(g, n, 1, D)
+    k = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[torch.arange(n), 0, torch.arange(n) % D] = 16.0
+    q = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    pick = torch.arange(n) // 3
+    q[torch.arange(n), 0, pick % D] = 64.0
+    out = sage.prompt_attention(q, k, v, ints([0, n]), is_causal=True)
+    only = pick < D  # keys pick and pick + D, ... have the same logit; rows that see the first alone copy its value
+    rows = torch.nonzero(only & (torch.arange(n) < D))[:, 0]
+    assert torch.equal(out[rows], v[pick[rows]])
+
+
+@pytest.mark.parametrize("off,kv", [
+    ([0, 50, 40, 100], None), ([-1, 50, 100], None), ([0, 50, 101], None), ([0, 2 ** 31 - 1, 100], None),
+    ([0, 50, 100], [0, 60, 50]), ([0, 50, 100], [0, 50, 90]), ([0, 50, 100], [-5, 50, 80])])
+def test_bad_offsets_are_flagged(off, kv):
+    g = gen(80)
+    q, k, v = bf16(g, 100, 2, 64), bf16(g, 80 if kv else 100, 1, 64), bf16(g, 80 if kv else 100, 1, 64)
+    out, lse = sage.prompt_attention(q, k, v, ints(off), kv_offsets=ints(kv) if kv else None, return_lse=True)
+    torch.cuda.synchronize()
+    assert sage.device_error() == DEVICE_OFFSETS
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_empty_calls():
+    g = gen(81)
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert sage.prompt_attention(e, e, e, ints([0])).shape == (0, 2, 64)
+    assert sage.prompt_attention(e, e, e, ints([0, 0, 0])).shape == (0, 2, 64)
+    q = bf16(g, 5, 2, 64)
+    out, lse = sage.prompt_attention(q, e, e, ints([0, 5]), kv_offsets=ints([0, 0]), return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    out, lse = sage.prompt_attention(q, q, q, ints([0]), return_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_refusals():
+    g = gen(82)
+    q, k, v = bf16(g, 10, 4, 64), bf16(g, 10, 2, 64), bf16(g, 10, 2, 64)
+    off = ints([0, 10])
+    bad = [
+        (dict(q=q.half()), -3), (dict(offsets=off.long()), -3), (dict(q=q[0]), -5), (dict(k=k[:9]), -5),
+        (dict(q=q[:, :3]), -5), (dict(k=k[..., :32], v=v[..., :32]), -5), (dict(offsets=ints([[0, 10]])), -5),
+        (dict(offsets=ints([])), -5), (dict(kv_offsets=ints([0, 5, 10])), -5), (dict(tensor_layout="BHND"), -6),
+        (dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), -6), (dict(sm_scale=0.0), -13),
+        (dict(sm_scale=math.inf), -13), (dict(offsets=ints([0, 1, 10, 2])[::2]), -6),
+        (dict(q=bf16(g, 10, 4, 32), k=bf16(g, 10, 2, 32), v=bf16(g, 10, 2, 32)), -4),
+        (dict(q=bf16(g, 10, 4, 65)[..., 1:], k=k), -7), (dict(out=bf16(g, 10, 2, 64)), -5),
+        (dict(workspace=torch.empty(10, dtype=torch.uint8, device="cuda")), -9),
+    ]
+    for change, code in bad:
+        with pytest.raises(SageError) as err:
+            sage.prompt_attention(**{**dict(q=q, k=k, v=v, offsets=off), **change})
+        assert err.value.code == code, (change, err.value)
+    with pytest.raises(ValueError):
+        sage.prompt_attention(q.cpu(), k, v, off)
+    with pytest.raises(ValueError):
+        sage.prompt_attention(q, k, v, off.cpu())
+    with pytest.raises(TypeError):
+        sage.prompt_attention(q, k, None, off)
+
+
+def test_graph_replay_with_other_offsets():
+    N, H, Hkv, D = 600, 4, 2, 128
+    q, k, v = inputs(90, [N], [N], H, Hkv, D)
+    off = ints([0, 100, 350, 600])
+    sage.prompt_attention(q, k, v, off)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out, lse = sage.prompt_attention(q, k, v, off, return_lse=True)
+    for e in ([0, 100, 350, 600], [0, 0, 599, 600], [0, 256, 512, 520]):
+        off.copy_(ints(e))
+        graph.replay()
+        torch.cuda.synchronize()
+        rows = np.diff(e).tolist()
+        close(out[:e[-1]], lse[:, :e[-1]], formula(q[:e[-1]], k, v, rows, rows, True, 1 / math.sqrt(D)))
+
+
+def test_two_streams_at_once():
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    rows = [[900, 30], [100] * 9, [1500]]
+    data = [inputs(91 + i, r, r, 4, 1, 128) for i, r in enumerate(rows)]
+    refs = [formula(*d, r, r, True, 1 / math.sqrt(128)) for d, r in zip(data, rows)]
+    torch.cuda.synchronize()
+    outs = [[] for _ in rows]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(sage.prompt_attention(*data[i], ints(ends(rows[i])), return_lse=True))
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, refs):
+        for out, lse in got:
+            close(out, lse, ref)
