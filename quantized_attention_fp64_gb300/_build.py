@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "lib", "libsage.so")
 SOURCES = ["api.cu", "prologue.cu", "attention_simt.cu", "attention_tc.cu", "lse_term.cu",
            "quantize_noalloc.cu", "tmap.cu", "cache_api.cu", "cache_pages.cu", "cache_attention.cu",
-           "cache_attention_tc.cu", "cache_weights.cu", "cache_evict.cu", "prompt_api.cu", "prompt_attention.cu",
+           "cache_attention_tc.cu", "cache_weights.cu", "cache_weights_tc.cu", "cache_evict.cu", "prompt_api.cu", "prompt_attention.cu",
            "rotary.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "sage.h")]

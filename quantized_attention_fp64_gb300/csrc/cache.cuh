@@ -180,6 +180,8 @@ struct CacheWeightsArgs {
   int* dev_err;
 };
 cudaError_t launch_cache_weights(const CacheWeightsArgs& a, int64_t D, cudaStream_t stream);
+// Many query rows (tensor cores).
+cudaError_t launch_cache_weights_tc(const CacheWeightsArgs& a, int64_t D, cudaStream_t stream);
 
 // Arguments of an eviction (checked on the host).
 struct CacheEvictArgs {

@@ -1,0 +1,476 @@
+"""Attention weights of cached tokens and eviction by them, on the GPU against the oracle.
+
+A weight w = exp(z - lse) is held to what fp32 can do: the logit's D products (exact in fp32) and their sum err by at
+most D 2^-23 sm_scale |q| |k| (Cauchy), its scale and the log-sum-exp in base 2 by 2^-22 (|z| + |lse|), the
+exponential by 2^-21 in all. Sums of R weights err by R 2^-24 of the sum at most, adding to the old score by half a
+step. Selected tokens, moved codes and scales have to be equal.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_attention_fp64_gb300 as sage
+from oracle import cache as oc
+from quantized_attention_fp64_gb300.api import SageError
+from test_cache_gpu import (ATTENTION, DEVICE_PAGE, _library, bf16, dev, f32, ints, make_table, poison_unused,  # noqa: F401
+                            random_cache, upload)
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(c, q, table, lengths, q_lengths, lse, causal, sm, S):
+    """(sums, bounds) of the weights, float64 [B, H, S]."""
+    B, T, H, D = q.shape
+    G = H // c.H
+    total, bound = np.zeros((2, B, c.H, S))
+    for b in range(B):
+        n, r = int(lengths[b]), int(q_lengths[b])
+        k, _ = c.tokens(table[b], 0, n)
+        sees = np.clip(n - r + 1 + np.arange(r), 0, n) if causal else np.full(r, n)
+        for h in range(H):
+            z = q[b, :r, h].astype(np.float64) @ k[:, h // G].T * sm
+            l = lse[b, h, :r].astype(np.float64)[:, None]
+            hidden = (np.arange(n)[None, :] >= sees[:, None]) | np.isinf(l)
+            w = np.where(hidden, 0.0, np.exp(np.where(hidden, 0.0, z - np.where(np.isinf(l), 0.0, l))))
+            size = np.linalg.norm(q[b, :r, h].astype(np.float64), axis=1)[:, None] * np.linalg.norm(k[:, h // G], axis=1)[None, :]
+            err = D * 2.0 ** -23 * sm * size + 2.0 ** -22 * (np.abs(z) + np.where(np.isinf(l), 0.0, np.abs(l))) + 2.0 ** -21
+            m = min(n, S)
+            total[b, h // G, :m] += w.sum(0)[:m]
+            bound[b, h // G, :m] += (w * err).sum(0)[:m] + r * 2.0 ** -24 * w.sum(0)[:m]
+    return total, bound * 1.01
+
+
+def add(rng, H, Hkv, D, page, lengths, q_lengths, T, causal, layout="NHD", sm=None, S=None):
+    B = len(lengths)
+    table, P = make_table(rng, lengths, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    poison_unused(c, table, lengths)
+    q = bf16(rng, B, T, H, D)
+    scale = 1 / math.sqrt(D) if sm is None else sm
+    ql = [T] * B if q_lengths is None else q_lengths
+    for b, r in enumerate(ql):
+        q[b, r:] = math.nan  # padding may hold anything
+    gpu = upload(c)
+    S = max(lengths + [1]) + 5 if S is None else S
+    wide = torch.from_numpy(rng.random((B, Hkv, S + 3)).astype(np.float32)).cuda()
+    scores = wide[:, :, 1:S + 1]
+    before = f32(scores).astype(np.float64)
+    qq = q if layout == "NHD" else q.transpose(1, 2).contiguous()
+    kw = dict(q_lengths=None if q_lengths is None else ints(q_lengths), is_causal=causal, sm_scale=sm, tensor_layout=layout)
+    _, lse = sage.cache_attention(qq, gpu, ints(table), ints(lengths), return_lse=True, **kw)
+    edges = wide[:, :, 0].clone(), wide[:, :, S + 1:].clone()
+    got = sage.cache_add_weights(scores, qq, gpu, ints(table), ints(lengths), lse, **kw)
+    assert got is scores and torch.equal(edges[0], wide[:, :, 0]) and torch.equal(edges[1], wide[:, :, S + 1:])
+    total, bound = weights(c, f32(q), table, lengths, ql, f32(lse), causal, scale, S)
+    after = f32(scores).astype(np.float64)
+    tol = bound + 2.0 ** -24 * np.abs(after)
+    bad = ~(np.abs(after - before - total) <= tol)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4].tolist(), float(np.nanmax((np.abs(after - before - total) / (tol + 1e-30)))))
+    for b, n in enumerate(lengths):
+        assert (after[b, :, min(n, S):] == before[b, :, min(n, S):]).all()
+    # the same again, bit for bit
+    again = torch.from_numpy(before.astype(np.float32)).cuda()
+    sage.cache_add_weights(again, qq, gpu, ints(table), ints(lengths), lse, **kw)
+    assert torch.equal(again, scores)
+
+
+WEIGHTS = ATTENTION + [
+    (7, 1, 128, 64, [500], None, 33, True),                   # 7 heads do not divide a tile's 128 rows
+    (12, 1, 64, 64, [500, 129, 1], [40, 3, 1], 40, True),
+    (130, 1, 64, 64, [200, 40], None, 3, True),               # more heads in a group than a tile has rows
+    (4, 4, 128, 128, [129], None, 128, True),
+    (2, 1, 128, 64, [128 * 5], None, 640, True),
+    (8, 1, 128, 64, [20000], None, 20, True),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WEIGHTS)))
+def test_weights(case):
+    add(np.random.default_rng(100 + case), *WEIGHTS[case])
+
+
+@pytest.mark.parametrize("T", [1, 5, 60])
+def test_weights_layout_scale_and_short_scores(T):
+    add(np.random.default_rng(7), 8, 2, 128, 64, [300, 77], None, T, True, layout="HND")
+    add(np.random.default_rng(8), 8, 2, 64, 64, [300, 77], None, T, False, sm=0.3)
+    add(np.random.default_rng(9), 8, 2, 64, 64, [300, 77, 10], None, T, True, S=130)
+    add(np.random.default_rng(10), 2, 2, 128, 32, [300, 77, 0], None, T, True, S=1)
+
+
+@pytest.mark.parametrize("T", [2, 50])
+def test_weights_sum_to_the_rows(T):
+    """All rows' weights add up to their number: each row's are a softmax."""
+    rng = np.random.default_rng(11)
+    lengths, H, Hkv, D = [1000, 333], 8, 2, 128
+    table, P = make_table(rng, lengths, 64)
+    gpu = upload(random_cache(rng, P, Hkv, D, 64))
+    q = bf16(rng, 2, T, H, D)
+    _, lse = sage.cache_attention(q, gpu, ints(table), ints(lengths), is_causal=True, return_lse=True)
+    scores = torch.zeros((2, Hkv, 1000), device="cuda")
+    sage.cache_add_weights(scores, q, gpu, ints(table), ints(lengths), lse, is_causal=True)
+    want = T * H // Hkv
+    assert ((scores.double().sum(-1) - want).abs() <= want * 2.0 ** -11).all()  # the log-sum-exp errs by up to 2^-13
+
+
+@pytest.mark.parametrize("T", [1, 7, 50])
+def test_weights_nan_stays_with_what_it_touches(T):
+    rng = np.random.default_rng(12)
+    lengths, H, Hkv, D, page = [200, 150], 4, 2, 128, 64
+    table, P = make_table(rng, lengths, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    c.k_scale[table[0][1], 1, 0] = np.nan  # tokens 64 .. 95 of sequence 0, head 1
+    gpu = upload(c)
+    q = bf16(rng, 2, T, H, D)
+    lse = torch.full((2, H, T), 3.0, device="cuda")
+    lse[1, 0, T - 1] = math.nan           # the last row of head 0 (key/value head 0) sees all tokens of sequence 1
+    lse[1, 3] = -math.inf                 # rows that saw nothing
+    scores = torch.zeros((2, Hkv, 200), device="cuda")
+    sage.cache_add_weights(scores, q, gpu, ints(table), ints(lengths), lse, is_causal=True)
+    odd = torch.isnan(scores)
+    want = torch.zeros_like(odd)
+    want[0, 1, 64:96] = True
+    want[1, 0, :150] = True
+    assert torch.equal(odd, want)
+
+
+@pytest.mark.parametrize("T", [1, 50])
+def test_weights_bad_pages_and_lengths_are_flagged(T):
+    rng = np.random.default_rng(13)
+    lengths, H, Hkv, D, page = [256, 256], 4, 2, 64, 64
+    table, P = make_table(rng, lengths, page)
+    gpu = upload(random_cache(rng, P, Hkv, D, page))
+    q = bf16(rng, 2, T, H, D)
+    lse = torch.full((2, H, T), 5.0, device="cuda")
+    ref = sage.cache_add_weights(torch.zeros((2, Hkv, 256), device="cuda"), q, gpu, ints(table), ints(lengths), lse)
+    assert sage.device_error() == 0
+    broken = table.copy()
+    broken[0, 1] = P
+    got = sage.cache_add_weights(torch.zeros((2, Hkv, 256), device="cuda"), q, gpu, ints(broken), ints(lengths), lse)
+    assert sage.device_error() == DEVICE_PAGE
+    want = ref.clone()
+    want[0, :, 64:128] = 0
+    assert torch.equal(got, want)
+    for change in (dict(lengths=ints([300, -1])), dict(q_lengths=ints([T + 1, 0])), dict(q_lengths=ints([-1, 0]))):
+        args = {**dict(lengths=ints(lengths)), **change}
+        sage.cache_add_weights(torch.zeros((2, Hkv, 256), device="cuda"), q, gpu, ints(table), args["lengths"], lse,
+                               q_lengths=args.get("q_lengths"))
+        assert sage.device_error() == DEVICE_PAGE
+
+
+def test_weights_refusals_and_empty_calls():
+    rng = np.random.default_rng(14)
+    table, P = make_table(rng, [40], 64)
+    gpu = upload(random_cache(rng, P, 2, 64, 64))
+    q, lse = bf16(rng, 1, 3, 4, 64), torch.zeros((1, 4, 3), device="cuda")
+    scores = torch.zeros((1, 2, 40), device="cuda")
+    good = dict(scores=scores, q=q, cache=gpu, page_table=ints(table), lengths=ints([40]), lse=lse)
+    for change, code in [
+        (dict(scores=scores.half()), -3), (dict(scores=scores[0]), -5), (dict(scores=scores[:, :1]), -5),
+        (dict(scores=torch.zeros((1, 2, 80), device="cuda")[:, :, ::2]), -6), (dict(q=q.float()), -3), (dict(q=q[:, :, :3]), -5),
+        (dict(lse=lse.double()), -3), (dict(lse=lse[:, :, :2]), -5), (dict(lse=lse.transpose(1, 2).contiguous().transpose(1, 2)), -6),
+        (dict(lengths=ints([40, 1])), -5), (dict(lengths=torch.tensor([40], device="cuda")), -3), (dict(sm_scale=-1.0), -13),
+        (dict(tensor_layout="x"), -6), (dict(q=bf16(rng, 1, 3, 4, 128)), -5)]:
+        with pytest.raises(SageError) as err:
+            sage.cache_add_weights(**{**good, **change})
+        assert err.value.code == code, change
+    with pytest.raises(TypeError):
+        sage.cache_add_weights(**{**good, "lse": None})
+    with pytest.raises(ValueError):
+        sage.cache_add_weights(**{**good, "lse": lse.cpu()})
+    empty = sage.cache_add_weights(scores[:, :, :0], q, gpu, ints(table), ints([40]), lse)
+    assert empty.shape == (1, 2, 0)
+    sage.cache_add_weights(scores, q[:, :0], gpu, ints(table), ints([40]), lse[:, :, :0])
+    sage.cache_add_weights(scores, q, gpu, ints(table)[:, :0], ints([0]), lse)
+    assert (scores == 0).all()
+
+
+# ------------------------------------------------------------------ eviction --
+
+
+def select(x, n, keep, recent):
+    """The tokens that stay, in order."""
+    stay = min(n, keep)
+    last = min(recent, stay)
+    y = x[:n - last].astype(np.float64)
+    y = np.where(np.isnan(y), -np.inf, y)
+    nan_last = np.isnan(x[:n - last])
+    order = np.lexsort((np.arange(n - last), nan_last, -y))  # by score, NaN behind -inf, then by place
+    return sorted(order[:stay - last].tolist()) + list(range(n - last, n))
+
+
+def evict(c: oc.Cache, table, lengths, scores, keep, recent, out_table):
+    """The oracle's eviction: changes c; returns lengths, kept and scores."""
+    B, H, S = scores.shape
+    new, K = np.zeros(B, np.int64), min(keep, S)
+    kept, moved = np.full((B, H, K), -1), np.zeros((B, H, S), np.float32)
+    old = [x.copy() for x in (c.k_codes, c.v_codes, c.k_scale, c.v_scale)]
+    src = oc.Cache.__new__(oc.Cache)
+    src.page_size, src.H, src.D = c.page_size, c.H, c.D
+    src.k_codes, src.v_codes, src.k_scale, src.v_scale = old
+    for b in range(B):
+        n = int(lengths[b])
+        for h in range(H):
+            ids = select(scores[b, h], n, keep, recent)
+            new[b] = m = len(ids)
+            kept[b, h, :m], moved[b, h, :m] = ids, scores[b, h, ids]
+            for i0 in range(0, m, 32):
+                part = ids[i0:i0 + 32]
+                at = [src.at(table[b], i) for i in part]
+                page, blk = c.at(out_table[b], i0)
+                both = [list(x) for x in c.block_codes(page, blk)]
+                for which, scales in enumerate((src.k_scale, src.v_scale)):
+                    s = np.array([scales[p, h, q] for p, q in at], np.float32)
+                    top = np.float32(np.nan) if np.isnan(s).any() else s.max()
+                    codes = np.zeros((32, c.D), np.int8)
+                    for i, ((p, q), t) in enumerate(zip(at, part)):
+                        if top > 0:
+                            codes[i] = np.rint(src.block_codes(p, q)[which][t % 32, h].astype(np.float32) * (s[i] / top))
+                    whole = np.array(both[which])
+                    whole[:, h] = codes
+                    both[which] = whole
+                    (c.k_scale, c.v_scale)[which][page, h, blk] = top
+                c.set_block_codes(page, blk, *[np.array(x) for x in both])
+    return new, kept, moved
+
+
+def same_cache(gpu, c):
+    for x, y in ((gpu.k_codes, c.k_codes), (gpu.v_codes, c.v_codes)):
+        bad = np.argwhere(x.cpu().numpy() != y)
+        assert not len(bad), (len(bad), bad[:3].tolist())
+    for x, y in ((gpu.k_scale, c.k_scale), (gpu.v_scale, c.v_scale)):
+        x = x.cpu().numpy()
+        assert np.array_equal(np.isnan(x), np.isnan(y)) and np.array_equal(x[~np.isnan(x)], y[~np.isnan(y)])
+
+
+def some_scores(rng, B, H, S):
+    """A few large ones, many equal ones (zeros among them), some negative."""
+    x = np.exp(rng.standard_normal((B, H, S)) * 2).astype(np.float32)
+    x[rng.random(x.shape) < 0.3] = 0.0
+    x[rng.random(x.shape) < 0.1] = -0.0
+    x[rng.random(x.shape) < 0.2] = 1.5
+    x[rng.random(x.shape) < 0.05] *= -1
+    return x
+
+
+EVICTIONS = [
+    # H, D, page, lengths, keep, recent
+    (1, 128, 32, [40], 20, 5),
+    (2, 64, 64, [1], 1, 0),
+    (2, 64, 64, [5, 0, 3], 0, 0),
+    (2, 128, 64, [100, 31, 64, 65], 64, 64),
+    (3, 64, 32, [333, 12, 0, 290], 96, 0),
+    (2, 128, 96, [500, 499, 1000], 333, 32),
+    (1, 64, 128, [3000], 2999, 1),
+    (1, 128, 64, [2500], 100, 0),
+    (4, 64, 64, [700, 1500], 800, 799),
+    (1, 64, 64, [9000], 1, 0),
+    (2, 128, 64, [9000, 40], 4100, 77),
+    (1, 64, 32, [(7 * i) % 90 for i in range(200)], 40, 3),
+]
+
+
+@pytest.mark.parametrize("place", ["in place", "other pages"])
+@pytest.mark.parametrize("case", range(len(EVICTIONS)))
+def test_evict(case, place):
+    H, D, page, lengths, keep, recent = EVICTIONS[case]
+    rng = np.random.default_rng(200 + case)
+    B, S = len(lengths), max(lengths + [1]) + 3
+    out_lengths = [min(n, keep) for n in lengths]
+    both, P = make_table(rng, lengths + out_lengths, page)
+    table, out_table = both[:B], both[B:]
+    c = random_cache(rng, P, H, D, page)
+    poison_unused(c, both, lengths + out_lengths)
+    scores = some_scores(rng, B, H, S)
+    scores[:, :, ::7] = np.where(rng.random(scores[:, :, ::7].shape) < 0.1, np.nan, scores[:, :, ::7])
+    gpu = upload(c)
+    old = dev(scores)
+    new, kept, moved = sage.cache_evict(gpu, ints(table), ints(lengths), old, keep, recent=recent,
+                                        out_table=None if place == "in place" else ints(out_table))
+    want = evict(c, table, lengths, scores, keep, recent, table if place == "in place" else out_table)
+    assert np.array_equal(new.cpu().numpy(), want[0])
+    assert np.array_equal(kept.cpu().numpy(), want[1])
+    assert np.array_equal(moved.cpu().numpy(), want[2], equal_nan=True)
+    assert np.array_equal(old.cpu().numpy(), scores, equal_nan=True)
+    same_cache(gpu, c)
+
+
+def test_evict_scores_of_all_kinds():
+    n, keep = 700, 200
+    rng = np.random.default_rng(220)
+    kinds = [np.zeros(n), np.full(n, -np.inf), np.full(n, np.nan), np.where(np.arange(n) % 3 == 0, np.nan, -np.inf),
+             np.arange(n), -np.arange(n), np.where(np.arange(n) % 2, 0.0, -0.0), np.full(n, np.inf),
+             rng.standard_normal(n) * 1e-40, rng.integers(0, 3, n), np.float32(1) + rng.integers(0, 4, n) * np.float32(2.0 ** -23),
+             np.where(np.arange(n) > 650, 1.0, 0.0)]
+    scores = np.stack(kinds).astype(np.float32)[:, None]
+    B = len(kinds)
+    table, P = make_table(rng, [n] * B, 64)
+    for recent in (0, 50):
+        gpu = upload(random_cache(rng, P, 1, 64, 64))
+        _, kept, moved = sage.cache_evict(gpu, ints(table), ints([n] * B), dev(scores), keep, recent=recent)
+        for b in range(B):
+            assert kept[b, 0].tolist() == select(scores[b, 0], n, keep, recent), (b, recent)
+            assert np.array_equal(moved[b, 0, :keep].cpu().numpy(), scores[b, 0][kept[b, 0].tolist()], equal_nan=True)
+
+
+def test_evict_long_sequences():
+    rng = np.random.default_rng(221)
+    n, H, D, page, keep, recent = 70001, 2, 64, 128, 30011, 1000
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, H, D, page)
+    scores = some_scores(rng, 1, H, n)
+    gpu = upload(c)
+    _, kept, _ = sage.cache_evict(gpu, ints(table), ints([n]), dev(scores), keep, recent=recent)
+    want = evict(c, table, [n], scores, keep, recent, table)
+    assert np.array_equal(kept.cpu().numpy(), want[1])
+    same_cache(gpu, c)
+
+
+def test_evict_scales_of_zero_and_nan():
+    rng = np.random.default_rng(222)
+    n, H, D, page, keep = 400, 2, 128, 64, 150
+    table, P = make_table(rng, [n], page)
+    c = random_cache(rng, P, H, D, page)
+    c.k_scale[table[0][0]], c.v_scale[table[0][1]] = 0.0, 0.0
+    c.k_scale[table[0][2], 0, 1], c.v_scale[table[0][4], 1, 0] = np.nan, np.nan
+    c.k_scale[table[0][5]] = 1e-42
+    scores = some_scores(rng, 1, H, n)
+    gpu = upload(c)
+    sage.cache_evict(gpu, ints(table), ints([n]), dev(scores), keep, recent=10)
+    evict(c, table, [n], scores, keep, 10, table)
+    same_cache(gpu, c)
+
+
+def test_evict_bad_pages_and_lengths_are_flagged():
+    rng = np.random.default_rng(223)
+    H, D, page, keep = 2, 64, 64, 70
+    table, P = make_table(rng, [300, 128], page)
+    c = random_cache(rng, P, H, D, page)
+    scores = some_scores(rng, 2, H, 300)
+    gpu = upload(c)
+    broken = table.copy()
+    broken[1, 1] = P + 7
+    out, _ = make_table(rng, [70, 70], page, spare=P)
+    out[0, :2], out[1, :2] = (P - 1, P), (P - 2, -1)   # the second page of each is outside the cache
+    new, kept, _ = sage.cache_evict(gpu, ints(broken), ints([300, 128]), dev(scores), keep, out_table=ints(out))
+    assert sage.device_error() == DEVICE_PAGE
+    assert new.tolist() == [70, 70]
+    assert kept[0, 0].tolist() == select(scores[0, 0], 300, keep, 0)
+    for lengths in ([301, 5], [-3, 5], [2 ** 31 - 1, 5]):
+        new, _, _ = sage.cache_evict(upload(c), ints(table), ints(lengths), dev(scores), keep)
+        assert sage.device_error() == DEVICE_PAGE
+        assert new.tolist() == [0 if lengths[0] < 0 else 70, 5]
+
+
+def test_evict_refusals_and_empty_calls():
+    rng = np.random.default_rng(224)
+    table, P = make_table(rng, [40, 10], 64)
+    c = random_cache(rng, P, 2, 64, 64)
+    gpu = upload(c)
+    scores = torch.zeros((2, 2, 40), device="cuda")
+    good = dict(cache=gpu, page_table=ints(table), lengths=ints([40, 10]), scores=scores, keep=20, recent=3)
+    for change, code in [
+        (dict(keep=-1), -5), (dict(recent=-1), -5), (dict(recent=21), -5), (dict(scores=scores[:1]), -5), (dict(scores=scores.int()), -3),
+        (dict(lengths=ints([40])), -5), (dict(lengths=ints([[40, 10]])), -5), (dict(lengths=torch.tensor([40, 10], device="cuda")), -3),
+        (dict(out_table=ints(table)[:1]), -5), (dict(out_table=ints(table).long()), -3)]:
+        with pytest.raises(SageError) as err:
+            sage.cache_evict(**{**good, **change})
+        assert err.value.code == code, change
+    with pytest.raises(TypeError):
+        sage.cache_evict(**{**good, "lengths": None})
+    same_cache(gpu, c)
+    new, kept, moved = sage.cache_evict(**{**good, "keep": 0, "recent": 0})
+    assert new.tolist() == [0, 0] and kept.shape == (2, 2, 0) and (moved == 0).all()
+    new, kept, moved = sage.cache_evict(gpu, ints(table)[:0], ints([]), scores[:0], 5)
+    assert new.shape == (0,) and kept.shape == (0, 2, 5) and moved.shape == (0, 2, 40)
+    new, kept, moved = sage.cache_evict(**{**good, "keep": 1000})     # nothing to cut
+    assert new.tolist() == [40, 10] and kept.shape == (2, 2, 40) and kept[1, 0].tolist() == list(range(10)) + [-1] * 30
+
+
+def test_evicted_sequences_go_on():
+    """A run of the operators as a program makes it: attention, weights, eviction, new tokens, attention again."""
+    rng = np.random.default_rng(225)
+    B, H, Hkv, D, page, keep, recent = 2, 4, 2, 128, 64, 160, 16
+    lengths = [300, 190]
+    table, P = make_table(rng, [n + 40 for n in lengths], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    gpu = upload(c)
+    tab, lens = ints(table), ints(lengths)
+    scores = torch.zeros((B, Hkv, 400), device="cuda")
+    for step in range(3):
+        q = bf16(rng, B, 1, H, D)
+        _, lse = sage.cache_attention(q, gpu, tab, lens, is_causal=True, return_lse=True)
+        sage.cache_add_weights(scores, q, gpu, tab, lens, lse, is_causal=True)
+    lens, kept, scores = sage.cache_evict(gpu, tab, lens, scores, keep, recent=recent)
+    before = scores.clone()
+    evict_lengths = lens.tolist()
+    assert evict_lengths == [keep, keep]
+    # the oracle's cache goes the same way, by the kernel's choice
+    old = [x.copy() for x in (c.k_codes, c.v_codes, c.k_scale, c.v_scale)]
+    src = oc.Cache.__new__(oc.Cache)
+    src.page_size, src.H, src.D = page, Hkv, D
+    src.k_codes, src.v_codes, src.k_scale, src.v_scale = old
+    k, v = bf16(rng, B, 1, Hkv, D), bf16(rng, B, 1, Hkv, D)
+    sage.cache_append(gpu, k, v, tab, lens)
+    lens += 1
+    q = bf16(rng, B, 1, H, D)
+    out, lse = sage.cache_attention(q, gpu, tab, lens, is_causal=True, return_lse=True)
+    sage.cache_add_weights(scores, q, gpu, tab, lens, lse, is_causal=True)
+    # read back, the sequences are the kept tokens (within half a step of their block's scale) and the new one
+    kk, vv = sage.cache_read(gpu, tab, torch.zeros_like(lens), keep + 1, counts=lens)
+    for b in range(B):
+        ks, vs = src.tokens(table[b], 0, lengths[b])
+        for h in range(Hkv):
+            ids = kept[b, h].cpu().numpy()
+            for got, was, scale in ((kk, ks, src.k_scale), (vv, vs, src.v_scale)):
+                diff = np.abs(f32(got[b, :keep, h]) - was[ids, h])
+                assert diff.max() <= scale.max() * 0.51 + 2.0 ** -8 * np.abs(was).max()
+        assert np.abs(f32(kk[b, keep]) - f32(k[b, 0])).max() <= 0.1
+    o, l, a = oc.attention_rows(f32(q[0, 0]), f32(kk[0, :, 0]).astype(np.float64), f32(vv[0, :, 0]).astype(np.float64),
+                                [keep + 1] * H, 1 / math.sqrt(D))
+    # tokens read back are rounded to bf16: 2^-8 of a logit's |q||k|, which is below 50 here with random signs
+    assert np.abs(f32(lse[0, :2, 0]) - l[:2]).max() <= 0.05
+    grown = (scores - before).sum(-1)
+    assert ((grown - H // Hkv).abs() <= 0.01).all()
+
+
+def test_scores_graph_replay():
+    rng = np.random.default_rng(226)
+    B, H, Hkv, D, page, keep = 2, 4, 2, 64, 32, 90
+    table, P = make_table(rng, [400, 400], page)
+    c = random_cache(rng, P, Hkv, D, page)
+    gpu = upload(c)
+    tab, lens = ints(table), ints([100, 200])
+    q = bf16(rng, B, 1, H, D)
+    start = torch.from_numpy(some_scores(rng, B, Hkv, 400)).cuda()
+    scores = start.clone()
+    lse = torch.full((B, H, 1), 4.0, device="cuda")
+
+    def step():
+        sage.cache_add_weights(scores, q, gpu, tab, lens, lse, is_causal=True)
+        return sage.cache_evict(gpu, tab, lens, scores, keep, recent=7)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            new, kept, moved = step()
+    for lengths in ([100, 200], [390, 5], [0, 91]):
+        for x, y in zip((gpu.k_codes, gpu.v_codes, gpu.k_scale, gpu.v_scale), (c.k_codes, c.v_codes, c.k_scale, c.v_scale)):
+            x.copy_(dev(y))
+        lens.copy_(ints(lengths))
+        scores.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        x = scores.cpu().numpy()
+        cc = oc.Cache.__new__(oc.Cache)
+        cc.page_size, cc.H, cc.D = page, Hkv, D
+        cc.k_codes, cc.v_codes, cc.k_scale, cc.v_scale = (t.copy() for t in (c.k_codes, c.v_codes, c.k_scale, c.v_scale))
+        want = evict(cc, table, lengths, x, keep, 7, table)
+        assert np.array_equal(new.cpu().numpy(), want[0]) and np.array_equal(kept.cpu().numpy(), want[1])
+        assert np.array_equal(moved.cpu().numpy(), want[2])
+        same_cache(gpu, cc)
