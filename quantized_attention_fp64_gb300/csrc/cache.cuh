@@ -201,6 +201,6 @@ struct CacheEvictArgs {
   int* dev_err;
 };
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, int64_t D, cudaStream_t stream);
-size_t cache_evict_workspace_bytes(int64_t B, int64_t H, int64_t D, int64_t keep);
+size_t cache_evict_workspace_bytes(int64_t B, int64_t H, int64_t keep, int64_t scores_n);
 
 }  // namespace sage

@@ -246,7 +246,8 @@ int sage_cache_evict_workspace_size(int64_t B, int64_t H, int64_t D, int64_t kee
   if (B < 0 || H < 0 || keep < 0 || scores_size < 0) return SAGE_ERR_SHAPE;
   if (D != 128 && D != 64) return SAGE_ERR_HEAD_DIM;
   if (B > kMaxDim || H > kMaxDim) return SAGE_ERR_TOO_LARGE;
-  *bytes = cache_evict_workspace_bytes(B, H, D, keep < scores_size ? keep : scores_size);
+  if (scores_size > kMaxTokens) return SAGE_ERR_TOO_LARGE;
+  *bytes = cache_evict_workspace_bytes(B, H, keep < scores_size ? keep : scores_size, scores_size);
   return SAGE_OK;
 }
 
@@ -266,7 +267,9 @@ int sage_cache_evict(const sage_cache_evict_args* args) {
   if (S < 0 || args->keep < 0 || args->recent < 0 || args->recent > args->keep || args->kept_size < keep)
     return SAGE_ERR_SHAPE;
   if (S > kMaxTokens || args->kept_size > kMaxTokens) return SAGE_ERR_TOO_LARGE;
-  const size_t need = cache_evict_workspace_bytes(args->B, a.c.H, args->cache->D, keep);
+  // blocks of all heads, keys and values, are numbered in 32 bits
+  if (args->B > 0 && a.c.H > 0 && div_up(keep, kCacheBlock) > (int64_t(1) << 30) / (args->B * a.c.H)) return SAGE_ERR_TOO_LARGE;
+  const size_t need = cache_evict_workspace_bytes(args->B, a.c.H, keep, S);
   if (need > 0) {
     if (args->workspace_dev == nullptr) return SAGE_ERR_NULLPTR;
     if (!aligned(args->workspace_dev, 256)) return SAGE_ERR_ALIGN;
