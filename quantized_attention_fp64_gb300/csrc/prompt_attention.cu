@@ -61,7 +61,10 @@ struct Header {
   int32_t blocks;            // entries of the list
   int32_t rest_lo, rest_hi;  // rows [0, rest_lo) and [rest_hi, N) belong to no sequence
 };
-constexpr size_t kHeaderBytes = 256;
+// Behind it a word of each scanning block of the first kernel: whether it has met
+// an infinity or a NaN. Then the list.
+constexpr size_t kOddAt = 64, kHeaderBytes = 4096;
+constexpr int kMostScans = 960;
 
 __host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B + 1; }
 
@@ -81,13 +84,78 @@ __device__ __forceinline__ int32_t key_tiles(const Block& b, int i) {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
+constexpr int kScanRows = 64;
 
-// Lists the row blocks of all sequences by their key tiles, the most first (in
-// 1024 classes). Offsets that decrease or leave the tensors: no block, all rows
-// are rest.
+// acc stays (0, 0) as long as no BF16 of the pairs is an infinity or a NaN.
+__device__ __forceinline__ uint32_t collect(uint32_t pair, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(pair), "r"(0u), "r"(acc));
+  return d;
+}
+// Those are the sign bits of this.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+
+struct Scan {
+  const uint16_t* v;
+  int64_t v_ss, v_sh;
+  int32_t heads, lanes;  // of a row: lanes = D / 8 chunks of 16 bytes
+  uint32_t* odd;
+};
+
+// Looks for infinities and NaN among the values that share a key tile with a key
+// that some row does not see: those of the sequences' own tokens (causal), and
+// the 127 rows behind a sequence's end.
+template <bool kCausal>
+__device__ __forceinline__ void scan_values(const int32_t* offsets, const int32_t* kv_offsets, int32_t B, int32_t M,
+                                            const Scan& sc) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int32_t lo = max(kv_offsets[0], 0), hi = static_cast<int32_t>(min(int64_t(M), int64_t(kv_offsets[B]) + kKeys - 1));
+  const bool all = kCausal && offsets == kv_offsets;
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
+  const int32_t chunks = kScanRows * sc.heads * sc.lanes;
+  for (int64_t r0 = lo + int64_t(blockIdx.x - 1) * kScanRows; r0 < hi; r0 += int64_t(gridDim.x - 1) * kScanRows) {
+    const int32_t r1 = static_cast<int32_t>(min(int64_t(hi), r0 + kScanRows));
+    if (!all) {
+      // the last sequence that begins at or before the rows' end; it and the one before may reach them
+      int32_t a = 0, z = B;
+      while (z - a > 1) {
+        const int32_t mid = (a + z) / 2;
+        if (kv_offsets[mid] < r1) a = mid;
+        else z = mid;
+      }
+      bool need = false;
+      for (int32_t b = a; b >= 0 && !need; --b) {
+        const int32_t end = kv_offsets[b + 1], own = kCausal ? offsets[b + 1] - offsets[b] : 0;
+        const int64_t first = int64_t(end) - own - kKeys;  // (the tile of the first own token begins at most so early)
+        need = r1 > first && r0 < int64_t(end) + kKeys;
+        if (int64_t(kv_offsets[b]) + kKeys < r0) break;    // sequences before end too early
+      }
+      if (!need) continue;
+    }
+#pragma unroll 4
+    for (int32_t x = tid; x < chunks; x += kPlanThreads) {
+      const int32_t c = x % sc.lanes, h = x / sc.lanes % sc.heads;
+      const int64_t r = r0 + x / sc.lanes / sc.heads;
+      if (r < r1) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sc.v + r * sc.v_ss + h * sc.v_sh + 8 * c);
+        acc[0] = collect(v.x, acc[0]);
+        acc[1] = collect(v.y, acc[1]);
+        acc[2] = collect(v.z, acc[2]);
+        acc[3] = collect(v.w, acc[3]);
+      }
+    }
+  }
+  const bool odd = not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]);
+  const bool any = __syncthreads_or(odd);
+  if (tid == 0) sc.odd[blockIdx.x - 1] = any ? 1u : 0u;
+}
+
+// Block 0 lists the row blocks of all sequences by their key tiles, the most first
+// (in 1024 classes); the others look the values over. Offsets that decrease or
+// leave the tensors: no block, all rows are rest.
 template <bool kCausal>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offsets, const int32_t* kv_offsets, int32_t B,
-                                                            int32_t N, int32_t M, Header* header, Block* list,
+                                                            int32_t N, int32_t M, Header* header, Block* list, const Scan sc,
                                                             int* dev_err) {
   __shared__ int32_t count[kBins];
   __shared__ int32_t most;
@@ -102,10 +170,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
     bad |= o < 0 || o > N || k < 0 || k > M || (b > 0 && (offsets[b - 1] > o || kv_offsets[b - 1] > k));
   }
   if (__syncthreads_or(bad)) {
-    if (tid == 0) {
+    if (tid == 0 && blockIdx.x == 0) {
       *header = Header{0, 0, 0};
       atomicExch(dev_err, kDevErrOffsets);
     }
+    return;  // (without units nothing asks for the scan)
+  }
+  if (blockIdx.x > 0) {
+    scan_values<kCausal>(offsets, kv_offsets, B, M, sc);
     return;
   }
   const auto block_of = [&](int32_t b, int32_t p) {
@@ -165,7 +237,8 @@ struct Smem {
   static constexpr uint32_t kOffBar = kOffRing + kStages * kTile;
   // barriers
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kDrain = 12;
-  static constexpr int kRaw = 14, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
+  static constexpr int kSFree = 14, kPFree = 16;         // P apart from S
+  static constexpr int kRaw = 18, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
   static constexpr int kFull = kFix + kFixes, kEmpty = kFull + kStages, kBars = kEmpty + kStages;
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
@@ -178,12 +251,20 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int i) { return 128u * static_cast<uint32_t>(i); }
 template <int D>
 __device__ __forceinline__ uint32_t col_o(int i) { return 256u + static_cast<uint32_t>(D) * static_cast<uint32_t>(i); }
+// At D = 64 there are columns left for P beside S: the next S = Q K^T then runs
+// under this one's exponentials. At D = 128 P takes the place of S.
+template <int D>
+constexpr bool kApart = D == 64;
+template <int D>
+__device__ __forceinline__ uint32_t col_p(int i) { return kApart<D> ? 384u + 64u * static_cast<uint32_t>(i) : col_s(i); }
 
-constexpr uint32_t kCtlRegs = 88, kSoftmaxRegs = 208;
+constexpr uint32_t kCtlRegs = 72, kSoftmaxRegs = 216;
 static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs <= kThreads * 168, "registers of one CTA");
 
 struct Params {
   const Header* header;
+  const uint32_t* odd;
+  int scans;            // words of it
   const Block* list;
   Out out;
   const uint16_t* v;
@@ -216,21 +297,47 @@ __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
   return b;
 }
 
-// Infinities and NaN of the BF16 pair in each word: the sign bits of the result.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; }
+// The CTA's units one after another; the next one's block is brought to L1 a unit ahead.
+struct Units {
+  const Block* list;
+  int32_t heads, units, i, u;
+  __device__ __forceinline__ Units(const Block* l, int32_t H, int32_t n) : list(l), heads(H), units(n), i(0) {
+    u = unit_at(0, units);
+    ahead();
+  }
+  __device__ __forceinline__ bool valid() const { return u >= 0; }
+  __device__ __forceinline__ int32_t head() const { return u % heads; }
+  __device__ __forceinline__ Block block() const { return load_block(list, u / heads); }
+  __device__ __forceinline__ int32_t next() const { return unit_at(i + 1, units); }
+  __device__ __forceinline__ void ahead() const {
+    const int32_t n = u >= 0 ? next() : -1;
+    if (n >= 0) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + n / heads));
+  }
+  __device__ __forceinline__ void advance() {
+    u = next();
+    ++i;
+    ahead();
+  }
+};
 
-// One key tile of the softmax for the thread's query row: S into registers, the
-// maximum, P over S. lim: keys of the tile that the row sees (kMask: fewer than
-// all for some row). Returns whether the rows of the warp go by a new maximum,
-// and the factor alpha for O.
-template <int D, bool kMask>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float c, int lim, bool first, float& m,
-                                             float& neg, float& l) {
+// One key tile of the softmax for the thread's query row of tile t: S into
+// registers, the maximum, P. lim: keys of the tile that the row sees. pv: products
+// with V of the query tile before this one. (One copy of the code for tiles with
+// and without hidden keys, and everything that runs once in a unit in small loops:
+// code that has not run for a while comes from far, 5000 cycles a time as it was.)
+template <int D>
+__device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t tS, uint32_t tP, uint32_t tO, float c,
+                                             int lim, bool first, uint32_t pv, float& m, float& neg, float& l) {
+  using L = Smem<D>;
   uint32_t s[4][32];
 #pragma unroll
   for (int b = 0; b < 4; ++b) tc::tmem_ld32(tS + 32u * b, s[b]);
   tc::tmem_wait_ld();
-  if (kMask) {
+  if (kApart<D>) {
+    tc::tc_fence_before();
+    tc::mbar_arrive(w.bar(L::kSFree + t));
+  }
+  if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -246,6 +353,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float c, 
     mx[b] = fmaxf(mx[b], __uint_as_float(s[b][31]));
   }
   const float up = fmaxf(tc::max3(mx[0], mx[1], mx[2]), mx[3]);
+  if (kApart<D> && pv > 0) {
+    // the product before this one is done with P, and with O
+    if (!tc::wait_bar_warp(w, w.bar(L::kPFree + t), (pv - 1) & 1u)) return false;
+    tc::tc_fence_after();
+  }
   // (up - m) c > 8; with m = -inf whenever the row has seen a key
   if (__any_sync(0xffffffffu, fmaf(up, c, neg) > kGrowth || (m == -INFINITY && up != -INFINITY))) {
     const float m_new = fmaxf(m, up);
@@ -256,17 +368,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float c, 
       l *= alpha;
       const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        tc::tmem_ld32(tO + 32u * x, o);
+      for (int x = 0; x < D / 16; ++x) {
+        uint32_t o[16];
+        tc::tmem_ld16(tO + 16u * x, o);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
+        for (int k = 0; k < 16; k += 2) {
           const float2 r = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), a2);
           o[k] = __float_as_uint(r.x);
           o[k + 1] = __float_as_uint(r.y);
         }
-        tc::tmem_st32(tO + 32u * x, o);
+        tc::tmem_st16(tO + 16u * x, o);
       }
     }
     m = m_new;
@@ -288,10 +400,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float c, 
       p[k / 2] = tc::bf16x2(p01.x, p01.y);
       p[k / 2 + 1] = tc::bf16x2(p23.x, p23.y);
     }
-    tc::tmem_st16(tS + 16u * b, p);
+    tc::tmem_st16(tP + 16u * b, p);
   }
   l += (sa.x + sa.y) + (sb.x + sb.y);
   tc::tmem_wait_st();
+  tc::tc_fence_before();
+  tc::mbar_arrive(w.bar(L::kPFull + t));
+  return true;
 }
 
 template <int D, bool kCausal>
@@ -318,6 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(w.bar(L::kOFull + i), 1);
       tc::mbar_init(w.bar(L::kOEmpty + i), 128);
       tc::mbar_init(w.bar(L::kDrain + i), 1);
+      tc::mbar_init(w.bar(L::kSFree + i), 128);
+      tc::mbar_init(w.bar(L::kPFree + i), 1);
     }
     for (int i = 0; i < 2 * kFixes; ++i) tc::mbar_init(w.bar(L::kRaw + i), 1);
     for (int i = 0; i < L::kStages; ++i) {
@@ -342,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   const int32_t units = prm.header->blocks * prm.H;
+  // value tiles with hidden keys pass through warp 3
+  bool met = false;
+  for (int i = static_cast<int>(threadIdx.x); i < prm.scans; i += kThreads) met |= prm.odd[i] != 0;
+  const bool odd = __syncthreads_or(met);
 
   if (warp < 4) {
     tc::regs_dec<kCtlRegs>();
@@ -351,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
         int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
         bool ok = true;
-        for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
-          const Block e = load_block(prm.list, u / prm.H);
-          const int32_t h = u % prm.H, hk = h / prm.group;
+        for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
+          const Block e = it.block();
+          const int32_t h = it.head(), hk = h / prm.group;
           const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
           const auto queries = [&](int t) {
             if (!(ok = wait_bar(w, w.bar(L::kQEmpty + t), (q_cnt[t] & 1u) ^ 1u))) return;
@@ -364,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, h, e.q0 + 128 * t,
                               w.bar(L::kQFull + t));
           };
-          const int32_t masked = sees<kCausal>(e, 0) / kKeys;  // value tiles from here on pass through warp 3
+          const int32_t masked = odd ? sees<kCausal>(e, 0) / kKeys : n;  // value tiles from here on pass through warp 3
           const auto tile = [&](const void* map, int32_t j, bool through) {
             const uint32_t st = at % L::kStages;
             if (!(ok = wait_bar(w, w.bar(L::kEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) return;
@@ -376,12 +497,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < D / 64; ++x)
               tc::tma_load_3d(sbase + L::kOffRing + st * L::kTile + x * L::kSub, map, 64 * x, hk, e.kv0 + j * kKeys, full);
           };
-          // the first tile's queries and keys before the second's
-          if (n0 > 0) queries(0);
+          // the first keys and values come before the queries, for which the unit
+          // before has to be through with its own
           for (int32_t j = 0; ok && j < n; ++j) {
             tile(&tm_k, j, false);
-            if (j == 0 && ok && n1 > 0) queries(1);
             if (ok) tile(&tm_v, j, j >= masked);
+            if (j == 0) {
+              if (ok && n0 > 0) queries(0);
+              if (ok && n1 > 0) queries(1);
+              // the next unit's queries on their way to L2
+              const int32_t next = it.next();
+              if (next >= 0) {
+                const Block f = load_block(prm.list, next / prm.H);
+                for (int t = 0; t < 2 && f.rows > 128 * t; ++t)
+#pragma unroll
+                  for (int x = 0; x < D / 64; ++x) tc::tma_prefetch_3d(&tm_q, 64 * x, next % prm.H, f.q0 + 128 * t);
+              }
+            }
           }
         }
         if (!ok) {
@@ -400,15 +532,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ products of tile t --
       const int t = warp - 1;
       const bool leader = tc::elect_one();
-      const uint32_t d_s = tmem + col_s(t), d_o = tmem + col_o<D>(t);
+      const uint32_t d_s = tmem + col_s(t), d_p = tmem + col_p<D>(t), d_o = tmem + col_o<D>(t);
       const uint64_t dq = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(t) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffRing), dv0 = tc::sw128_mn_desc(sbase + L::kOffRing, L::kSub);
-      uint32_t base = 0, q_cnt = 0, p_cnt = 0, done = 0;  // ring position of the unit's first tile; queries, P, units with keys so far
+      // ring position of the unit's first tile; queries, S, P, units with keys so far
+      uint32_t base = 0, q_cnt = 0, s_cnt = 0, p_cnt = 0, done = 0;
+      bool ok = true;
       const auto full = [&](uint32_t p) {
         return wait_bar_warp(w, w.bar(L::kFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
       };
       const auto empty = [&](uint32_t p) { return w.bar(L::kEmpty + static_cast<int>(p % L::kStages)); };
-      const auto product_s = [&](uint32_t p) {
+      // S of the key tile at ring position p, the unit's last one if `last`
+      const auto wait_s = [&](uint32_t p) {
+        if (!full(p)) return false;
+        if (kApart<D> && s_cnt > 0 && !wait_bar_warp(w, w.bar(L::kSFree + t), (s_cnt - 1) & 1u)) return false;
+        ++s_cnt;
+        return true;
+      };
+      const auto product_s = [&](uint32_t p, bool last) {
         const uint64_t dk = tc::desc_at(dk0, (p % L::kStages) * L::kTile);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -417,43 +558,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::mma_commit(w.bar(L::kSFull + t));
         tc::mma_commit(empty(p));
+        if (last) tc::mma_commit(w.bar(L::kQEmpty + t));
       };
-      bool ok = true;
-      for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
-        const Block e = load_block(prm.list, u / prm.H);
+      for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
+        const Block e = it.block();
         const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
         if (own > 0) {
-          if (!(ok = wait_bar_warp(w, w.bar(L::kQFull + t), q_cnt & 1u)) || !(ok = full(base))) break;
+          if (!(ok = wait_bar_warp(w, w.bar(L::kQFull + t), q_cnt & 1u)) || !(ok = wait_s(base))) break;
+          ++q_cnt;
           tc::tc_fence_after();
-          if (leader) {
-            product_s(base);
-            if (own == 1) tc::mma_commit(w.bar(L::kQEmpty + t));
-          }
+          if (leader) product_s(base, own == 1);
           __syncwarp();
         }
         for (int32_t j = 0; j < n; ++j) {
           const uint32_t pk = base + 2u * static_cast<uint32_t>(j), pv = pk + 1u;
+          const bool more = j + 1 < own;
+          if (kApart<D> && more) {
+            if (!(ok = wait_s(pk + 2u))) break;
+            tc::tc_fence_after();
+            if (leader) product_s(pk + 2u, j + 2 == own);
+            __syncwarp();
+          }
           if (!(ok = full(pv))) break;
           // the softmax warps are through with the unit before: its O, and what warp 3 has told them
           if (j == 0 && !(ok = wait_bar_warp(w, w.bar(L::kOEmpty + t), (done & 1u) ^ 1u))) break;
           if (j < own) {
+            if (!kApart<D> && more && !(ok = wait_s(pk + 2u))) break;
+            // the keys' part of the tile, in steps of 16
+            const int steps = min(kKeys, e.keys - j * kKeys + 15) / 16;
+            const uint64_t dv = tc::desc_at(dv0, (pv % L::kStages) * L::kTile);
             if (!(ok = wait_bar_warp(w, w.bar(L::kPFull + t), p_cnt & 1u))) break;
             ++p_cnt;
-            if (j + 1 < own && !(ok = full(pk + 2u))) break;
             tc::tc_fence_after();
             if (leader) {
-              const uint64_t dv = tc::desc_at(dv0, (pv % L::kStages) * L::kTile);
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks)
-                tc::mma_f16_ts(d_o, d_s + 8u * ks, tc::desc_at(dv, 2048u * ks), tc::IdescBf16<D, true>::value,
-                               (j > 0 || ks > 0) ? 1u : 0u);
+                if (ks < steps)
+                  tc::mma_f16_ts(d_o, d_p + 8u * ks, tc::desc_at(dv, 2048u * ks), tc::IdescBf16<D, true>::value,
+                                 (j > 0 || ks > 0) ? 1u : 0u);
+              if (!kApart<D> && more) product_s(pk + 2u, j + 2 == own);
               tc::mma_commit(empty(pv));
-              if (j + 1 < own) {
-                product_s(pk + 2u);
-                if (j + 2 == own) tc::mma_commit(w.bar(L::kQEmpty + t));
-              } else {
-                tc::mma_commit(w.bar(L::kOFull + t));
-              }
+              if (kApart<D>) tc::mma_commit(w.bar(L::kPFree + t));
+              if (!more) tc::mma_commit(w.bar(L::kOFull + t));
             }
           } else {
             // a key tile that only the other query tile sees
@@ -466,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (own > 0) ++q_cnt;
         if (n > 0) ++done;
         base += 2u * static_cast<uint32_t>(n);
       }
@@ -478,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------- value tiles with hidden keys --
       uint32_t base = 0, fixes = 0, done = 0;
       bool ok = true;
-      for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
-        const Block e = load_block(prm.list, u / prm.H);
+      for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
+        const Block e = it.block();
         const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
         bool bad = false;
-        for (int32_t j = sees<kCausal>(e, 0) / kKeys; j < n; ++j) {
+        for (int32_t j = odd ? sees<kCausal>(e, 0) / kKeys : n; j < n; ++j) {
           const uint32_t p = base + 2u * static_cast<uint32_t>(j) + 1u;
           if (!(ok = wait_bar_warp(w, w.bar(L::kRaw + static_cast<int>(fixes % kFixes)), (fixes / kFixes) & 1u))) break;
           uint8_t* tile = smem + L::kOffRing + (p % L::kStages) * L::kTile;
@@ -491,24 +636,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < D / 64; ++x) {
             uint4* chunk = reinterpret_cast<uint4*>(tile + x * L::kSub);
             if (kCausal) {
-#pragma unroll 4
+              uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
               for (int q = lane; q < there * 8; q += 32) {
                 const uint4 v = chunk[q];
-                if ((not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) & 0x80008000u) {
-                  bad = true;
-                  uint32_t o[4] = {v.x, v.y, v.z, v.w};
+                acc[0] = collect(v.x, acc[0]);
+                acc[1] = collect(v.y, acc[1]);
+                acc[2] = collect(v.z, acc[2]);
+                acc[3] = collect(v.w, acc[3]);
+              }
+              if (__any_sync(0xffffffffu, not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]))) {
+                bad = true;
+#pragma unroll 1
+                for (int q = lane; q < there * 8; q += 32) {
+                  uint32_t* o = reinterpret_cast<uint32_t*>(chunk + q);
+#pragma unroll 1
                   for (int k = 0; k < 4; ++k) {
-                    const uint32_t f = not_finite(o[k]) & 0x80008000u;
+                    const uint32_t f = not_finite(o[k]);
                     if (f & 0x8000u) o[k] &= 0xFFFF0000u;
                     if (f & 0x80000000u) o[k] &= 0x0000FFFFu;
                   }
-                  chunk[q] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
               }
             }
             for (int q = there * 8 + lane; q < kKeys * 8; q += 32) chunk[q] = make_uint4(0, 0, 0, 0);
           }
-          bad = __any_sync(0xffffffffu, bad);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -530,8 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + col_s(t), tO = tmem + lanes + col_o<D>(t);
-    uint32_t s_cnt = 0, fixes = 0, done = 0;
+    const uint32_t tS = tmem + lanes + col_s(t), tP = tmem + lanes + col_p<D>(t), tO = tmem + lanes + col_o<D>(t);
     if (prm.zero_rest) {
       const int32_t lo = prm.header->rest_lo, hi = prm.header->rest_hi;
       const int64_t rest = lo + (prm.N - hi), chunks = rest * prm.H * (D / 8);
@@ -543,85 +694,126 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
       }
     }
-    bool ok = true;
-    for (int32_t i = 0, u; ok && (u = unit_at(i, units)) >= 0; ++i) {
-      const Block e = load_block(prm.list, u / prm.H);
-      const int32_t h = u % prm.H;
-      const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
-      const int32_t r = 128 * t + row, mine = sees<kCausal>(e, r), all = sees<kCausal>(e, 128 * t) / kKeys;
-      float m = -INFINITY, neg = 0.0f, l = 0.0f;
-      for (int32_t j = 0; j < own; ++j) {
-        if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
-        ++s_cnt;
-        tc::tc_fence_after();
-        if (j < all)
-          softmax_tile<D, false>(tS, tO, prm.scale, kKeys, j == 0, m, neg, l);
-        else
-          softmax_tile<D, true>(tS, tO, prm.scale, mine - j * kKeys, j == 0, m, neg, l);
-        tc::tc_fence_before();
-        tc::mbar_arrive(w.bar(L::kPFull + t));
-      }
-      if (!ok) break;
+    // A unit is finished (O read, scaled and stored) when the next one's first P is
+    // on its way: the products then have something to do meanwhile.
+    struct Last {
+      Block e = {};
+      int32_t h, own, n, masked;
+      uint32_t fixes;  // value tiles from warp 3 up to the unit's end
+      float neg, l;
+    } last;
+    last.n = 0;
+    uint32_t s_cnt = 0, fixes = 0, done = 0;
+    const auto finish = [&]() {
+      if (last.n == 0) return true;
+      const Block& e = last.e;
       // infinities and NaN that warp 3 has cleared
       bool bad = false;
-      if (kCausal) {
-        const int32_t masked = sees<kCausal>(e, 0) / kKeys;
-        if (n > masked) {
-          fixes += static_cast<uint32_t>(n - masked);
-          if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>((fixes - 1) % kFixes)), ((fixes - 1) / kFixes) & 1u)))
-            break;
-          bad = own > 0 && bad_units[done % kFixes] != 0;
-        }
+      if (kCausal && odd && last.own > 0 && last.n > last.masked) {
+        const uint32_t f = last.fixes - 1;
+        if (!wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(f % kFixes)), (f / kFixes) & 1u)) return false;
+        bad = bad_units[done % kFixes] != 0;
       }
-      if (n > 0) {
-        if (!(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
-        ++done;
-        tc::tc_fence_after();
-      }
-      const bool valid = r < e.rows;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      if (valid && prm.lse != nullptr)
-        prm.lse[static_cast<int64_t>(h) * prm.N + e.q0 + r] = l == 0.0f ? -INFINITY : (log2f(l) - neg) * kLn2;
-      uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + h * prm.out.sh;
+      if (!wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u)) return false;
+      ++done;
+      tc::tc_fence_after();
+      const int32_t r = 128 * t + row;
+      const float inv = last.l == 0.0f ? 0.0f : 1.0f / last.l;
+      if (prm.lse != nullptr && r < e.rows)
+        prm.lse[static_cast<int64_t>(last.h) * prm.N + e.q0 + r] = last.l == 0.0f ? -INFINITY : (log2f(last.l) - last.neg) * kLn2;
+      // Four lanes exchange their rows' chunks of 16 bytes, so that a store covers 64
+      // bytes of 8 rows instead of 16 of 32: chunk 4 x + q of row j of the four goes
+      // from lane j to lane q (two exchanges, with the neighbour and the next pair).
+      uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r - (lane & 3)) * prm.out.ss + last.h * prm.out.sh;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
-        if (own > 0) {
-          tc::tmem_ld32(tO + 32u * x, o);
-          tc::tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (x == D / 32 - 1 && n > 0) {
+        tc::tmem_ld32(tO + 32u * x, o);
+        tc::tmem_wait_ld();
+        if (x == D / 32 - 1) {
           tc::tc_fence_before();
           tc::mbar_arrive(w.bar(L::kOEmpty + t));
         }
-        if (kCausal && bad) {
-          const int32_t first = sees<kCausal>(e, 0) / kKeys * kKeys;
-          for (int32_t k = first; k < mine; ++k) {
-            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + h / prm.group * prm.v_sh + 32 * x;
-            for (int y = 0; y < 32; ++y) {
-              const uint32_t b = v[y];
-              if ((b & 0x7F80u) == 0x7F80u) {
-                // an index known at compile time keeps o in registers
+        uint32_t c[4][4];
 #pragma unroll
-                for (int z = 0; z < 32; ++z)
-                  if (z == y) o[z] = __float_as_uint(__uint_as_float(o[z]) + __uint_as_float(b << 16));
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            c[q][k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
+            if (last.own == 0) c[q][k] = 0u;  // (O is not this unit's)
+          }
+#pragma unroll
+        for (int s = 1; s <= 2; s *= 2) {
+          const bool upper = (lane & s) != 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((q & s) == 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? c[q][k] : c[q + s][k], s);
+                if (upper) c[q][k] = got;
+                else c[q + s][k] = got;
               }
             }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r - (lane & 3) + j < e.rows)
+            *reinterpret_cast<uint4*>(dst + j * prm.out.ss + 32 * x + 8 * (lane & 3)) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+      }
+      last.n = 0;
+      if (kCausal && bad) {
+        __syncwarp();  // the row's values were stored by all four lanes
+        dst += (lane & 3) * prm.out.ss;
+        const int32_t mine = r < e.rows ? sees<kCausal>(e, r) : 0;
+#pragma unroll 1
+        for (int32_t k = last.masked * kKeys; k < mine; ++k) {
+          const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + last.h / prm.group * prm.v_sh;
+#pragma unroll 1
+          for (int y = 0; y < D; ++y) {
+            const uint32_t b = v[y];
+            if ((b & 0x7F80u) == 0x7F80u)
+              dst[y] = static_cast<uint16_t>(
+                  tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + __uint_as_float(b << 16), 0.0f));
           }
         }
-        if (valid) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pk[k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * x + 8 * q) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
+      }
+      return true;
+    };
+    bool ok = true;
+    for (Units it(prm.list, prm.H, units); ok; it.advance()) {
+      // (behind the last unit: nothing but to finish it)
+      Block e = {};
+      if (it.valid()) e = it.block();
+      else e.rows = 0;
+      const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
+      const int32_t r = 128 * t + row, mine = sees<kCausal>(e, r);
+      float m = -INFINITY, neg = 0.0f, l = 0.0f;
+      for (int32_t j = 0; ok && j < max(own, 1); ++j) {
+        if (j < own) {
+          if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
+          tc::tc_fence_after();
+          ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == 0, s_cnt, m, neg, l);
+          ++s_cnt;
         }
+        if (ok && j == 0) ok = finish();
+      }
+      if (!ok || !it.valid()) break;
+      last.e = e;
+      last.h = it.head();
+      last.own = own;
+      last.n = n;
+      last.masked = sees<kCausal>(e, 0) / kKeys;
+      if (odd && n > last.masked) fixes += static_cast<uint32_t>(n - last.masked);
+      last.fixes = fixes;
+      last.neg = neg;
+      last.l = l;
+      if (n == 0 && r < e.rows) {
+        // no row of the unit sees a key
+        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + last.h * prm.out.sh;
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(0, 0, 0, 0);
+        if (prm.lse != nullptr) prm.lse[static_cast<int64_t>(last.h) * prm.N + e.q0 + r] = -INFINITY;
       }
     }
     tc::regs_dec<kCtlRegs>();
@@ -651,13 +843,19 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   if (!make_map(&tq, a.q, a.N, a.H, D) || !make_map(&tk, a.k, rows, a.Hkv, D) || !make_map(&tv, a.v, rows, a.Hkv, D))
     return cudaErrorInvalidValue;
   Header* header = static_cast<Header*>(a.workspace);
+  uint32_t* odd = reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kOddAt);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
-  cudaError_t e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPlanThreads, 0, stream,
-                                   a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N), static_cast<int32_t>(a.M),
-                                   header, list, a.dev_err);
+  const int64_t sms = sm_count_current(), rows64 = div_up(a.M, kScanRows), fit = 2 * sms < kMostScans ? 2 * sms : kMostScans;
+  const int scans = static_cast<int>(rows64 < fit ? rows64 : fit);
+  const Scan sc{a.v.p, a.v.ss, a.v.sh, a.Hkv, D / 8, odd};
+  cudaError_t e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(static_cast<unsigned>(1 + scans)),
+                                   kPlanThreads, 0, stream, a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
+                                   static_cast<int32_t>(a.M), header, list, sc, a.dev_err);
   if (e != cudaSuccess) return e;
   Params p;
   p.header = header;
+  p.odd = odd;
+  p.scans = scans;
   p.list = list;
   p.out = a.out;
   p.v = a.v.p;
@@ -673,7 +871,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;
   const int bytes = static_cast<int>(Smem<D>::kBytes);
   if ((e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes)) != cudaSuccess) return e;
-  const int64_t units = most_blocks(a.N, a.B) * a.H, sms = sm_count_current();
+  const int64_t units = most_blocks(a.N, a.B) * a.H;
   return launch_dependent(kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads,
                           static_cast<size_t>(bytes), stream, tq, tk, tv, p);
 }
