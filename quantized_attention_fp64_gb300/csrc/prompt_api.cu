@@ -22,7 +22,7 @@ int check_prompt_sizes(int64_t N, int64_t M, int64_t H, int64_t Hkv, int64_t D, 
   if (Hkv == 0 ? H != 0 : H % Hkv != 0) return SAGE_ERR_SHAPE;
   if (N > kMaxTokens || M > kMaxTokens || H > kMaxDim || B > kMaxDim) return SAGE_ERR_TOO_LARGE;
   // units of 128 rows of a head are counted in 32 bits
-  if (H > 0 && N / 128 + B + 1 > ((int64_t(1) << 31) - 1) / H) return SAGE_ERR_TOO_LARGE;
+  if (H > 0 && N / 128 + B + 1 > (int64_t(1) << 30) / H) return SAGE_ERR_TOO_LARGE;
   return SAGE_OK;
 }
 

@@ -10,11 +10,12 @@
 // memory. A first kernel lists the row blocks of all sequences, those with the
 // most key tiles first; the CTAs, one for each SM, take the units in that order
 // forth and back (0 1 .. 151, 151 .. 1 0, ...), so that each gets about the same
-// work whatever the lengths are. Roles of the 12 warps:
+// work whatever the lengths are. Roles of the 16 warps:
 //   warp 0      TMA: the unit's queries, and a ring of key and value tiles in turn
 //   warps 1, 2  TMEM allocation; the products of query tile 0, 1 (one thread issues)
 //   warp 3      makes value tiles ready that hold keys which some row does not see
 //   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
+//   warps 12-15 output: O of either tile, scaled and stored
 // TMEM holds S0, S1, O0, O1: all 512 columns at D = 128. The softmax reads S of a
 // key tile into registers and writes P over it, from where the product with V
 // reads it; that product and the next S = Q K^T are issued together when P is
@@ -42,7 +43,7 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
@@ -73,7 +74,8 @@ template <bool kCausal>
 __device__ __forceinline__ int32_t sees(const Block& b, int32_t r) {
   return kCausal ? max(0, min(b.sees + r, b.keys)) : b.keys;
 }
-__device__ __forceinline__ int32_t tiles_of(int32_t keys) { return keys / kKeys + (keys % kKeys != 0 ? 1 : 0); }
+__device__ __forceinline__ int32_t tiles_of(int32_t keys) { return (keys + kKeys - 1) >> 7; }  // (keys are at most 2^30)
+static_assert(kKeys == 128, "key tiles are counted by shifts");
 // Key tiles of query tile i of a block.
 template <bool kCausal>
 __device__ __forceinline__ int32_t key_tiles(const Block& b, int i) {
@@ -238,12 +240,14 @@ struct Smem {
   // barriers
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kDrain = 12;
   static constexpr int kSFree = 14, kPFree = 16;         // P apart from S
-  static constexpr int kRaw = 18, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
-  static constexpr int kFull = kFix + kFixes, kEmpty = kFull + kStages, kBars = kEmpty + kStages;
+  static constexpr int kStat = 18;                       // a tile's sums and maxima are there
+  static constexpr int kRaw = 20, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
+  static constexpr int kFull = kFix + kFixes, kEmpty = kFull + kStages, kTurn = kEmpty + kStages, kBars = kTurn + 2;
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
-  static constexpr uint32_t kBytes = kOffBad + 4 * kFixes;
+  static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m
+  static constexpr uint32_t kBytes = kOffStat + 2 * 128 * 8;
 };
 static_assert(Smem<128>::kBytes <= 232448u && Smem<64>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
 
@@ -258,10 +262,26 @@ constexpr bool kApart = D == 64;
 template <int D>
 __device__ __forceinline__ uint32_t col_p(int i) { return kApart<D> ? 384u + 64u * static_cast<uint32_t>(i) : col_s(i); }
 
-constexpr uint32_t kCtlRegs = 72, kSoftmaxRegs = 216;
-static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs <= kThreads * 168, "registers of one CTA");
+constexpr uint32_t kCtlRegs = 72, kSoftmaxRegs = 184, kOutRegs = 72;  // 512 threads launched at 128
+static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 128, "registers of one CTA");
+static_assert(kOutRegs == kCtlRegs, "every warp runs the teardown with the control budget");
+
+// u / d for u below 2^31, by a multiplication.
+struct Divisor {
+  int32_t d;
+  uint32_t mul;
+  int shift;
+  explicit Divisor(int32_t x) : d(x), mul(0), shift(0) {
+    while ((int64_t(1) << shift) < x) ++shift;  // 2^shift >= d
+    if (x > 1) mul = static_cast<uint32_t>((uint64_t(1) << (31 + shift)) / static_cast<uint64_t>(x) + 1), --shift;
+  }
+  __device__ __forceinline__ int32_t of(int32_t u) const {
+    return d == 1 ? u : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(u), mul) >> shift);
+  }
+};
 
 struct Params {
+  Divisor H, group;     // query heads, and those that share a key/value head
   const Header* header;
   const uint32_t* odd;
   int scans;            // words of it
@@ -271,19 +291,10 @@ struct Params {
   int64_t v_ss, v_sh;
   float* lse;
   int64_t N;
-  int32_t H, group;     // query heads, and those that share a key/value head
   bool zero_rest;
   float scale;          // c
   int* dev_err;
 };
-
-// The CTA's i-th unit (the list's blocks times the heads, heads innermost), or -1.
-__device__ __forceinline__ int32_t unit_at(int32_t i, int32_t units) {
-  const int32_t g = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
-  if (i > (units - 1) / g) return -1;
-  const int32_t u = i * g + ((i & 1) ? g - 1 - c : c);
-  return u < units ? u : -1;
-}
 
 __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
   const int4* p = reinterpret_cast<const int4*>(list + e);
@@ -298,25 +309,35 @@ __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
 }
 
 // The CTA's units one after another; the next one's block is brought to L1 a unit ahead.
+// Unit u is one of the list's blocks and a head, heads innermost; the CTAs take
+// them in that order forth and back.
 struct Units {
-  const Block* list;
-  int32_t heads, units, i, u;
-  __device__ __forceinline__ Units(const Block* l, int32_t H, int32_t n) : list(l), heads(H), units(n), i(0) {
-    u = unit_at(0, units);
-    ahead();
+  const Params& prm;
+  int32_t units, u, step, other;
+  Block e;
+  int32_t h;
+  __device__ __forceinline__ Units(const Params& p, int32_t n) : prm(p), units(n) {
+    const int32_t g = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
+    u = c;
+    step = 2 * (g - 1 - c) + 1;
+    other = 2 * c + 1;
+    load();
   }
-  __device__ __forceinline__ bool valid() const { return u >= 0; }
-  __device__ __forceinline__ int32_t head() const { return u % heads; }
-  __device__ __forceinline__ Block block() const { return load_block(list, u / heads); }
-  __device__ __forceinline__ int32_t next() const { return unit_at(i + 1, units); }
-  __device__ __forceinline__ void ahead() const {
-    const int32_t n = u >= 0 ? next() : -1;
-    if (n >= 0) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + n / heads));
+  __device__ __forceinline__ bool valid() const { return u < units; }
+  __device__ __forceinline__ void load() {
+    if (u >= units) return;
+    const int32_t b = prm.H.of(u);
+    e = load_block(prm.list, b);
+    h = u - b * prm.H.d;
+    const int32_t next = u + step;
+    if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(prm.list + prm.H.of(next)));
   }
   __device__ __forceinline__ void advance() {
-    u = next();
-    ++i;
-    ahead();
+    u += step;
+    const int32_t s = step;
+    step = other;
+    other = s;
+    load();
   }
 };
 
@@ -354,7 +375,6 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
   }
   const float up = fmaxf(tc::max3(mx[0], mx[1], mx[2]), mx[3]);
   if (kApart<D> && pv > 0) {
-    // the product before this one is done with P, and with O
     if (!tc::wait_bar_warp(w, w.bar(L::kPFree + t), (pv - 1) & 1u)) return false;
     tc::tc_fence_after();
   }
@@ -386,9 +406,9 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
   }
   const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
   float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
+  uint32_t p[4][16];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    uint32_t p[16];
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1])), c2, n2);
@@ -397,10 +417,10 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
       const float2 p23 = make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y));
       sa = __fadd2_rn(sa, p01);
       sb = __fadd2_rn(sb, p23);
-      p[k / 2] = tc::bf16x2(p01.x, p01.y);
-      p[k / 2 + 1] = tc::bf16x2(p23.x, p23.y);
+      p[b][k / 2] = tc::bf16x2(p01.x, p01.y);
+      p[b][k / 2 + 1] = tc::bf16x2(p23.x, p23.y);
     }
-    tc::tmem_st16(tP + 16u * b, p);
+    tc::tmem_st16(tP + 16u * b, p[b]);
   }
   l += (sa.x + sa.y) + (sb.x + sb.y);
   tc::tmem_wait_st();
@@ -435,7 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(w.bar(L::kDrain + i), 1);
       tc::mbar_init(w.bar(L::kSFree + i), 128);
       tc::mbar_init(w.bar(L::kPFree + i), 1);
+      tc::mbar_init(w.bar(L::kStat + i), 128);
     }
+    for (int i = 0; i < 2; ++i) tc::mbar_init(w.bar(L::kTurn + i), 1);
     for (int i = 0; i < 2 * kFixes; ++i) tc::mbar_init(w.bar(L::kRaw + i), 1);
     for (int i = 0; i < L::kStages; ++i) {
       tc::mbar_init(w.bar(L::kFull + i), 1);
@@ -458,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int32_t units = prm.header->blocks * prm.H;
+  const int32_t units = prm.header->blocks * prm.H.d;
   // value tiles with hidden keys pass through warp 3
   bool met = false;
   for (int i = static_cast<int>(threadIdx.x); i < prm.scans; i += kThreads) met |= prm.odd[i] != 0;
@@ -472,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
         int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
         bool ok = true;
-        for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
-          const Block e = it.block();
-          const int32_t h = it.head(), hk = h / prm.group;
+        for (Units it(prm, units); ok && it.valid(); it.advance()) {
+          const Block& e = it.e;
+          const int32_t h = it.h, hk = prm.group.of(h);
           const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
           const auto queries = [&](int t) {
             if (!(ok = wait_bar(w, w.bar(L::kQEmpty + t), (q_cnt[t] & 1u) ^ 1u))) return;
@@ -485,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, h, e.q0 + 128 * t,
                               w.bar(L::kQFull + t));
           };
-          const int32_t masked = odd ? sees<kCausal>(e, 0) / kKeys : n;  // value tiles from here on pass through warp 3
+          const int32_t masked = odd ? sees<kCausal>(e, 0) >> 7 : n;  // value tiles from here on pass through warp 3
           const auto tile = [&](const void* map, int32_t j, bool through) {
             const uint32_t st = at % L::kStages;
             if (!(ok = wait_bar(w, w.bar(L::kEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) return;
@@ -506,12 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ok && n0 > 0) queries(0);
               if (ok && n1 > 0) queries(1);
               // the next unit's queries on their way to L2
-              const int32_t next = it.next();
-              if (next >= 0) {
-                const Block f = load_block(prm.list, next / prm.H);
+              const int32_t next = it.u + it.step;
+              if (next < units) {
+                const int32_t b = prm.H.of(next);
+                const Block f = load_block(prm.list, b);
                 for (int t = 0; t < 2 && f.rows > 128 * t; ++t)
 #pragma unroll
-                  for (int x = 0; x < D / 64; ++x) tc::tma_prefetch_3d(&tm_q, 64 * x, next % prm.H, f.q0 + 128 * t);
+                  for (int x = 0; x < D / 64; ++x) tc::tma_prefetch_3d(&tm_q, 64 * x, next - b * prm.H.d, f.q0 + 128 * t);
               }
             }
           }
@@ -530,19 +553,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp <= 2) {
       // ------------------------------------------------ products of tile t --
+      // The two query tiles' products take turns: issued side by side, they share the
+      // tensor pipe and end together, and then both softmaxes run at once and the pipe
+      // stands still. Tile 1's product with value tile j (and S of the next key tile)
+      // comes after tile 0's with j, and that with j + 1 after it. A tile says that a
+      // turn is over only where the other asks for it (tile 1 has as many key tiles as
+      // tile 0, or one more, or none at all), so no phase of the barriers is skipped.
       const int t = warp - 1;
       const bool leader = tc::elect_one();
       const uint32_t d_s = tmem + col_s(t), d_p = tmem + col_p<D>(t), d_o = tmem + col_o<D>(t);
       const uint64_t dq = tc::sw128_desc(sbase + L::kOffQ + static_cast<uint32_t>(t) * L::kTile);
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffRing), dv0 = tc::sw128_mn_desc(sbase + L::kOffRing, L::kSub);
-      // ring position of the unit's first tile; queries, S, P, units with keys so far
-      uint32_t base = 0, q_cnt = 0, s_cnt = 0, p_cnt = 0, done = 0;
-      bool ok = true;
+      // ring position of the unit's first tile; queries, S, P, units with keys, the other tile's turns so far
+      uint32_t base = 0, q_cnt = 0, s_cnt = 0, p_cnt = 0, done = 0, turns = 0;
       const auto full = [&](uint32_t p) {
         return wait_bar_warp(w, w.bar(L::kFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
       };
       const auto empty = [&](uint32_t p) { return w.bar(L::kEmpty + static_cast<int>(p % L::kStages)); };
-      // S of the key tile at ring position p, the unit's last one if `last`
+      // S of the key tile at ring position p
       const auto wait_s = [&](uint32_t p) {
         if (!full(p)) return false;
         if (kApart<D> && s_cnt > 0 && !wait_bar_warp(w, w.bar(L::kSFree + t), (s_cnt - 1) & 1u)) return false;
@@ -560,9 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_commit(empty(p));
         if (last) tc::mma_commit(w.bar(L::kQEmpty + t));
       };
-      for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
-        const Block e = it.block();
-        const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
+      bool ok = true;
+      for (Units it(prm, units); ok && it.valid(); it.advance()) {
+        const Block& e = it.e;
+        const int32_t own = key_tiles<kCausal>(e, t), theirs = key_tiles<kCausal>(e, 1 - t), n = max(own, theirs);
         if (own > 0) {
           if (!(ok = wait_bar_warp(w, w.bar(L::kQFull + t), q_cnt & 1u)) || !(ok = wait_s(base))) break;
           ++q_cnt;
@@ -580,15 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (!(ok = full(pv))) break;
-          // the softmax warps are through with the unit before: its O, and what warp 3 has told them
+          // the output warps are through with the unit before
           if (j == 0 && !(ok = wait_bar_warp(w, w.bar(L::kOEmpty + t), (done & 1u) ^ 1u))) break;
           if (j < own) {
             if (!kApart<D> && more && !(ok = wait_s(pk + 2u))) break;
             // the keys' part of the tile, in steps of 16
-            const int steps = min(kKeys, e.keys - j * kKeys + 15) / 16;
+            const int steps = (min(kKeys, e.keys - j * kKeys) + 15) >> 4;
             const uint64_t dv = tc::desc_at(dv0, (pv % L::kStages) * L::kTile);
             if (!(ok = wait_bar_warp(w, w.bar(L::kPFull + t), p_cnt & 1u))) break;
             ++p_cnt;
+            if (theirs > 0 && (t == 0 ? j > 0 : j < theirs)) {
+              if (!(ok = wait_bar_warp(w, w.bar(L::kTurn + 1 - t), turns & 1u))) break;
+              ++turns;
+            }
             tc::tc_fence_after();
             if (leader) {
 #pragma unroll
@@ -599,6 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!kApart<D> && more) product_s(pk + 2u, j + 2 == own);
               tc::mma_commit(empty(pv));
               if (kApart<D>) tc::mma_commit(w.bar(L::kPFree + t));
+              if (t == 0 ? theirs > 0 : j + 1 < theirs) {
+                if (kApart<D>) tc::mbar_arrive(w.bar(L::kTurn + t));  // issued
+                else tc::mma_commit(w.bar(L::kTurn + t));             // done
+              }
               if (!more) tc::mma_commit(w.bar(L::kOFull + t));
             }
           } else {
@@ -623,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------- value tiles with hidden keys --
       uint32_t base = 0, fixes = 0, done = 0;
       bool ok = true;
-      for (Units it(prm.list, prm.H, units); ok && it.valid(); it.advance()) {
-        const Block e = it.block();
+      for (Units it(prm, units); ok && it.valid(); it.advance()) {
+        const Block& e = it.e;
         const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
         bool bad = false;
-        for (int32_t j = odd ? sees<kCausal>(e, 0) / kKeys : n; j < n; ++j) {
+        for (int32_t j = odd ? sees<kCausal>(e, 0) >> 7 : n; j < n; ++j) {
           const uint32_t p = base + 2u * static_cast<uint32_t>(j) + 1u;
           if (!(ok = wait_bar_warp(w, w.bar(L::kRaw + static_cast<int>(fixes % kFixes)), (fixes / kFixes) & 1u))) break;
           uint8_t* tile = smem + L::kOffRing + (p % L::kStages) * L::kTile;
@@ -676,145 +713,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 12) {
     // ----------------------------------------------------------------- softmax --
     tc::regs_inc<kSoftmaxRegs>();
     const int t = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + col_s(t), tP = tmem + lanes + col_p<D>(t), tO = tmem + lanes + col_o<D>(t);
+    uint32_t s_cnt = 0, done = 0;
+    float2* stat = reinterpret_cast<float2*>(smem + L::kOffStat) + 128 * t + row;
+    bool ok = true;
+    for (Units it(prm, units); ok && it.valid(); it.advance()) {
+      const Block& e = it.e;
+      const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
+      const int32_t mine = sees<kCausal>(e, 128 * t + row);
+      float m = -INFINITY, neg = 0.0f, l = 0.0f;
+      for (int32_t j = 0; j < own; ++j) {
+        if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
+        tc::tc_fence_after();
+        if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == 0, s_cnt, m, neg, l))) break;
+        ++s_cnt;
+      }
+      if (ok && own > 0) {
+        // the unit before has been stored
+        if (!(ok = wait_bar_warp(w, w.bar(L::kOEmpty + t), (done & 1u) ^ 1u))) break;
+        *stat = make_float2(l, neg);
+        tc::mbar_arrive(w.bar(L::kStat + t));
+      }
+      if (n > 0) ++done;
+    }
+    tc::regs_dec<kCtlRegs>();
+  } else {
+    // ------------------------------------------------------------------ output --
+    // O is read, scaled and stored by warps of its own: the softmax goes on with the
+    // next unit.
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    tc::regs_dec<kOutRegs>();
     if (prm.zero_rest) {
       const int32_t lo = prm.header->rest_lo, hi = prm.header->rest_hi;
-      const int64_t rest = lo + (prm.N - hi), chunks = rest * prm.H * (D / 8);
-      const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-      for (int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x - 128); x < chunks; x += step) {
-        const int64_t c = x % (D / 8), h = x / (D / 8) % prm.H, at = x / (D / 8) / prm.H;
-        const int64_t r = at < lo ? at : hi + (at - lo);
+      // a row's head at a time for D / 8 threads
+      const int at = static_cast<int>(threadIdx.x) - 384, c = at % (D / 8);
+      const int64_t rest = lo + (prm.N - hi), items = rest * prm.H.d, step = static_cast<int64_t>(gridDim.x) * (128 / (D / 8));
+      for (int64_t x = static_cast<int64_t>(blockIdx.x) * (128 / (D / 8)) + at / (D / 8); x < items; x += step) {
+        const int64_t i = x / prm.H.d, h = x - i * prm.H.d, r = i < lo ? i : hi + (i - lo);
         *reinterpret_cast<uint4*>(prm.out.p + r * prm.out.ss + h * prm.out.sh + 8 * c) = make_uint4(0, 0, 0, 0);
         if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
       }
     }
-    // A unit is finished (O read, scaled and stored) when the next one's first P is
-    // on its way: the products then have something to do meanwhile.
-    struct Last {
-      Block e = {};
-      int32_t h, own, n, masked;
-      uint32_t fixes;  // value tiles from warp 3 up to the unit's end
-      float neg, l;
-    } last;
-    last.n = 0;
-    uint32_t s_cnt = 0, fixes = 0, done = 0;
-    const auto finish = [&]() {
-      if (last.n == 0) return true;
-      const Block& e = last.e;
-      // infinities and NaN that warp 3 has cleared
-      bool bad = false;
-      if (kCausal && odd && last.own > 0 && last.n > last.masked) {
-        const uint32_t f = last.fixes - 1;
-        if (!wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(f % kFixes)), (f / kFixes) & 1u)) return false;
-        bad = bad_units[done % kFixes] != 0;
+    uint32_t fixes = 0, done = 0, stats[2] = {0, 0};
+    bool ok = true;
+    for (Units it(prm, units); ok && it.valid(); it.advance()) {
+      const Block& e = it.e;
+      const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
+      const int32_t masked = sees<kCausal>(e, 0) >> 7;
+      bool bad = false;  // the unit has infinities or NaN that warp 3 has cleared
+      if (odd && n > masked) {
+        fixes += static_cast<uint32_t>(n - masked);
+        const uint32_t f = fixes - 1;
+        if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(f % kFixes)), (f / kFixes) & 1u))) break;
+        bad = kCausal && bad_units[done % kFixes] != 0;
       }
-      if (!wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u)) return false;
-      ++done;
-      tc::tc_fence_after();
-      const int32_t r = 128 * t + row;
-      const float inv = last.l == 0.0f ? 0.0f : 1.0f / last.l;
-      if (prm.lse != nullptr && r < e.rows)
-        prm.lse[static_cast<int64_t>(last.h) * prm.N + e.q0 + r] = last.l == 0.0f ? -INFINITY : (log2f(last.l) - last.neg) * kLn2;
-      // Four lanes exchange their rows' chunks of 16 bytes, so that a store covers 64
-      // bytes of 8 rows instead of 16 of 32: chunk 4 x + q of row j of the four goes
-      // from lane j to lane q (two exchanges, with the neighbour and the next pair).
-      uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r - (lane & 3)) * prm.out.ss + last.h * prm.out.sh;
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        tc::tmem_ld32(tO + 32u * x, o);
-        tc::tmem_wait_ld();
-        if (x == D / 32 - 1) {
-          tc::tc_fence_before();
-          tc::mbar_arrive(w.bar(L::kOEmpty + t));
+      for (int t = 0; t < 2; ++t) {
+        const int32_t own = t == 0 ? n0 : n1, r = 128 * t + row;
+        float2 st = make_float2(0.0f, 0.0f);
+        if (own > 0) {
+          uint32_t& c = stats[t];
+          if (!(ok = wait_bar_warp(w, w.bar(L::kStat + t), c & 1u))) break;
+          ++c;
+          st = reinterpret_cast<const float2*>(smem + L::kOffStat)[r];
         }
-        uint32_t c[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            c[q][k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
-            if (last.own == 0) c[q][k] = 0u;  // (O is not this unit's)
+        if (n > 0 && !(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
+        tc::tc_fence_after();
+        const float inv = st.x == 0.0f ? 0.0f : 1.0f / st.x;
+        if (prm.lse != nullptr && r < e.rows)
+          prm.lse[static_cast<int64_t>(it.h) * prm.N + e.q0 + r] = st.x == 0.0f ? -INFINITY : (log2f(st.x) - st.y) * kLn2;
+        // Four lanes exchange their rows' chunks of 16 bytes, so that a store covers 64
+        // bytes of 8 rows instead of 16 of 32: chunk 4 x + q of row j of the four goes
+        // from lane j to lane q (two exchanges, with the neighbour and the next pair).
+        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r - (lane & 3)) * prm.out.ss + it.h * prm.out.sh;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          tc::tmem_ld32(tmem + lanes + col_o<D>(t) + 32u * static_cast<uint32_t>(x), o);
+          tc::tmem_wait_ld();
+          if (x == D / 32 - 1 && n > 0) {
+            tc::tc_fence_before();
+            tc::mbar_arrive(w.bar(L::kOEmpty + t));
           }
-#pragma unroll
-        for (int s = 1; s <= 2; s *= 2) {
-          const bool upper = (lane & s) != 0;
+          uint32_t c[4][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if ((q & s) == 0) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? c[q][k] : c[q + s][k], s);
-                if (upper) c[q][k] = got;
-                else c[q + s][k] = got;
-              }
+            for (int k = 0; k < 4; ++k) {
+              c[q][k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
+              if (own == 0) c[q][k] = 0u;  // (O is not this unit's)
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (r - (lane & 3) + j < e.rows)
-            *reinterpret_cast<uint4*>(dst + j * prm.out.ss + 32 * x + 8 * (lane & 3)) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
-      }
-      last.n = 0;
-      if (kCausal && bad) {
-        __syncwarp();  // the row's values were stored by all four lanes
-        dst += (lane & 3) * prm.out.ss;
-        const int32_t mine = r < e.rows ? sees<kCausal>(e, r) : 0;
+          for (int s = 1; s <= 2; s *= 2) {
+            const bool upper = (lane & s) != 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if ((q & s) == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? c[q][k] : c[q + s][k], s);
+                  if (upper) c[q][k] = got;
+                  else c[q + s][k] = got;
+                }
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (r - (lane & 3) + j < e.rows)
+              *reinterpret_cast<uint4*>(dst + j * prm.out.ss + 32 * x + 8 * (lane & 3)) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+        }
+        if (kCausal && bad) {
+          __syncwarp();  // the row's values were stored by all four lanes
+          dst += (lane & 3) * prm.out.ss;
+          const int32_t mine = r < e.rows ? sees<kCausal>(e, r) : 0;
 #pragma unroll 1
-        for (int32_t k = last.masked * kKeys; k < mine; ++k) {
-          const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + last.h / prm.group * prm.v_sh;
+          for (int32_t k = masked * kKeys; k < mine; ++k) {
+            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + prm.group.of(it.h) * prm.v_sh;
 #pragma unroll 1
-          for (int y = 0; y < D; ++y) {
-            const uint32_t b = v[y];
-            if ((b & 0x7F80u) == 0x7F80u)
-              dst[y] = static_cast<uint16_t>(
-                  tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + __uint_as_float(b << 16), 0.0f));
+            for (int y = 0; y < D; ++y) {
+              const uint32_t b = v[y];
+              if ((b & 0x7F80u) == 0x7F80u)
+                dst[y] = static_cast<uint16_t>(
+                    tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + __uint_as_float(b << 16), 0.0f));
+            }
           }
         }
       }
-      return true;
-    };
-    bool ok = true;
-    for (Units it(prm.list, prm.H, units); ok; it.advance()) {
-      // (behind the last unit: nothing but to finish it)
-      Block e = {};
-      if (it.valid()) e = it.block();
-      else e.rows = 0;
-      const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
-      const int32_t r = 128 * t + row, mine = sees<kCausal>(e, r);
-      float m = -INFINITY, neg = 0.0f, l = 0.0f;
-      for (int32_t j = 0; ok && j < max(own, 1); ++j) {
-        if (j < own) {
-          if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
-          tc::tc_fence_after();
-          ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == 0, s_cnt, m, neg, l);
-          ++s_cnt;
-        }
-        if (ok && j == 0) ok = finish();
-      }
-      if (!ok || !it.valid()) break;
-      last.e = e;
-      last.h = it.head();
-      last.own = own;
-      last.n = n;
-      last.masked = sees<kCausal>(e, 0) / kKeys;
-      if (odd && n > last.masked) fixes += static_cast<uint32_t>(n - last.masked);
-      last.fixes = fixes;
-      last.neg = neg;
-      last.l = l;
-      if (n == 0 && r < e.rows) {
-        // no row of the unit sees a key
-        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + last.h * prm.out.sh;
-#pragma unroll
-        for (int q = 0; q < D / 8; ++q) *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(0, 0, 0, 0);
-        if (prm.lse != nullptr) prm.lse[static_cast<int64_t>(last.h) * prm.N + e.q0 + r] = -INFINITY;
-      }
+      if (n > 0) ++done;
     }
     tc::regs_dec<kCtlRegs>();
   }
@@ -852,7 +884,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
                                    kPlanThreads, 0, stream, a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
                                    static_cast<int32_t>(a.M), header, list, sc, a.dev_err);
   if (e != cudaSuccess) return e;
-  Params p;
+  Params p{Divisor(a.H), Divisor(a.H / a.Hkv)};
   p.header = header;
   p.odd = odd;
   p.scans = scans;
@@ -863,8 +895,6 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.v_sh = a.v.sh;
   p.lse = a.lse;
   p.N = a.N;
-  p.H = a.H;
-  p.group = a.H / a.Hkv;
   p.zero_rest = a.zero_rest;
   p.scale = a.sm_log2;
   p.dev_err = a.dev_err;
