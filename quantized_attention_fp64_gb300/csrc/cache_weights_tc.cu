@@ -39,18 +39,22 @@ struct Smem {
   static constexpr uint32_t kSub = 128 * 128;        // 64 channels of 128 rows
   static constexpr uint32_t kTileBytes = 128 * D * 2;
   static constexpr int kStages = 3;                  // query tiles
+  static constexpr int kLse = 4;                     // log-sum-exps of query tiles
   static constexpr uint32_t kOffK = 0;               // two pairs of key tiles
   static constexpr uint32_t kOffQ = 4 * kTileBytes;
   static constexpr uint32_t kOffLse = kOffQ + kStages * kTileBytes;   // [stage][128] -log2(e) lse
-  static constexpr uint32_t kOffScale = kOffLse + kStages * 512;      // [pair][8 blocks]
+  static constexpr uint32_t kOffScale = kOffLse + kLse * 512;         // [pair][8 blocks]
   static constexpr uint32_t kOffThere = kOffScale + 2 * 32;           // [pair][8 blocks]: on a page of the cache
-  static constexpr uint32_t kOffOdd = kOffThere + 2 * 32;             // [stage]: rows that are none
-  static constexpr uint32_t kOffBar = (kOffOdd + 4 * kStages + 7) / 8 * 8;
+  static constexpr uint32_t kOffOdd = kOffThere + 2 * 32;             // [lse]: rows that are none
+  static constexpr uint32_t kOffBar = (kOffOdd + 4 * kLse + 7) / 8 * 8;
   static constexpr int kQFull = 0, kQEmpty = kQFull + kStages, kKFull = kQEmpty + kStages, kKEmpty = kKFull + 2;
-  static constexpr int kSFull = kKEmpty + 2, kSFree = kSFull + 4, kDrain = kSFree + 4, kBars = kDrain + 1;
+  static constexpr int kSFull = kKEmpty + 2, kSFree = kSFull + 4, kDrain = kSFree + 4;
+  static constexpr int kLFull = kDrain + 1, kLEmpty = kLFull + kLse, kJoinFull = kLEmpty + kLse, kJoinFree = kJoinFull + 1;
+  static constexpr int kBars = kJoinFree + 1;
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kBytes = kOffAbort + 4;
+  static constexpr uint32_t kOffJoin = (kOffAbort + 4 + 15) / 16 * 16;  // [128] sums of the second half of the warps
+  static constexpr uint32_t kBytes = kOffJoin + 512;
 };
 static_assert(Smem<128>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
 
@@ -149,41 +153,50 @@ struct Walk {
   }
 };
 
-// One query tile for the thread's key: the sum of 2^(S scale + lse') over its rows.
-// kMask: of those that see the key only (row's token t sees it when t >= since).
-template <bool kMask>
-__device__ __forceinline__ float sum_tile(const uint32_t (&s)[4][32], float scale, const float* lse, int32_t since,
-                                          int32_t t0, const Params& prm, int32_t head0, int32_t rows) {
+// 64 rows of a query tile for the thread's key: the sum of 2^(S scale + lse').
+__device__ __forceinline__ float sum_rows(const uint32_t (&s)[2][32], float scale, const float* lse) {
   float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
   const float2 c2 = make_float2(scale, scale);
-  int32_t t = t0, g = head0;
 #pragma unroll
-  for (int b = 0; b < 4; ++b)
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float4 l = *reinterpret_cast<const float4*>(lse + 32 * b + k);
       const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1])), c2, make_float2(l.x, l.y));
       const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[b][k + 2]), __uint_as_float(s[b][k + 3])), c2, make_float2(l.z, l.w));
-      float2 p01 = make_float2(tc::exp2_approx(x01.x), tc::exp2_approx(x01.y));
-      float2 p23 = make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y));
-      if (kMask) {
-        // rows of the tile: heads head0 .. head0 + prm.heads - 1 of the group, token by token
-        const float ls[4] = {l.x, l.y, l.z, l.w};
-        float* p[4] = {&p01.x, &p01.y, &p23.x, &p23.y};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (a row's lse' of infinity: there is no such row, or it saw nothing)
-          if (t < since || t >= rows || ls[e] == INFINITY) *p[e] = 0.0f;
-          if (++g == head0 + prm.heads) {
-            g = head0;
-            ++t;
-          }
-        }
-      }
-      sa = __fadd2_rn(sa, p01);
-      sb = __fadd2_rn(sb, p23);
+      sa = __fadd2_rn(sa, make_float2(tc::exp2_approx(x01.x), tc::exp2_approx(x01.y)));
+      sb = __fadd2_rn(sb, make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y)));
     }
   return (sa.x + sa.y) + (sb.x + sb.y);
+}
+
+// S of rows that do not count becomes minus infinity in TMEM, so that their weights
+// are 0: those of tokens before `since` or from `rows` on, and those whose lse' is
+// that too (S may be a NaN). Rows of the tile: `heads` heads, token by token.
+__device__ __forceinline__ void hide_rows(uint32_t tS, const float* lse, int32_t since, int32_t t, int32_t heads,
+                                          int32_t rows) {
+  int32_t g = 0;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    uint32_t s[32];
+    tc::tmem_ld32(tS + 32u * static_cast<uint32_t>(b), s);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 l = *reinterpret_cast<const float4*>(lse + 32 * b + k);
+      const float ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool out = (t < since) | (t >= rows) | (ls[e] == -INFINITY);
+        s[k + e] = out ? 0xFF800000u : s[k + e];
+        const bool wrap = ++g == heads;
+        g = wrap ? 0 : g;
+        t += wrap ? 1 : 0;
+      }
+    }
+    tc::tmem_st32(tS + 32u * static_cast<uint32_t>(b), s);
+  }
+  tc::tmem_wait_st();
 }
 
 // Four codes to two BF16 pairs: 128 + the low seven bits, less 128 or (negative) 256.
@@ -215,8 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *w.abort_flag = 0;
     for (int i = 0; i < L::kStages; ++i) {
-      tc::mbar_init(w.bar(L::kQFull + i), 2);   // the copies, the log-sum-exps
-      tc::mbar_init(w.bar(L::kQEmpty + i), 9);  // the products, eight warps
+      tc::mbar_init(w.bar(L::kQFull + i), 1);
+      tc::mbar_init(w.bar(L::kQEmpty + i), 1);
+    }
+    for (int i = 0; i < L::kLse; ++i) {
+      tc::mbar_init(w.bar(L::kLFull + i), 1);
+      tc::mbar_init(w.bar(L::kLEmpty + i), 8);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(w.bar(L::kKFull + i), 128);
@@ -227,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(w.bar(L::kSFree + i), 4);
     }
     tc::mbar_init(w.bar(L::kDrain), 1);
+    tc::mbar_init(w.bar(L::kJoinFull), 4);
+    tc::mbar_init(w.bar(L::kJoinFree), 4);
     tc::fence_mbar_init();
   }
   const int32_t rows_there = prm.heads * prm.tokens;  // rows that a query tile's copy fills
@@ -270,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               k.h * prm.group + i % prm.splits * prm.heads, i / prm.splits * prm.tokens, k.b, full);
           }
         if (!ok) {
-          // copies land before the CTA exits (the other arrival may be missing: bounded)
+          // copies land before the CTA exits
           const tc::Waits d = w.draining();
           for (uint32_t p = at < L::kStages ? 0 : at - L::kStages; p < at; ++p)
             tc::wait_bar(d, w.bar(L::kQFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
@@ -284,18 +303,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk k;
       for (k.begin(a); ok && k.left > 0; k.next(a), ++unit) {
         if (!(ok = tc::wait_bar_warp(w, w.bar(L::kKFull + static_cast<int>(unit & 1u)), (unit >> 1) & 1u))) break;
+        const uint32_t at0 = at;
         for (int32_t i = k.first(prm), n = k.end(prm); i < n; ++i, ++at) {
           const uint32_t st = at % L::kStages;
           if (!(ok = tc::wait_bar_warp(w, w.bar(L::kQFull + static_cast<int>(st)), (at / L::kStages) & 1u))) break;
+          const int alone = static_cast<int>(at - at0) & 1;  // one key tile: query tiles in turn to either half of the warps
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= k.n) continue;
+            if (k.n == 1 && x != alone) continue;
             const int buf = 2 * x + static_cast<int>(s_cnt[x] & 1u);
             if (!(ok = tc::wait_bar_warp(w, w.bar(L::kSFree + buf), ((s_cnt[x] >> 1) & 1u) ^ 1u))) break;
             ++s_cnt[x];
             tc::tc_fence_after();
             if (leader) {
-              const uint64_t dk = tc::desc_at(dk0, (2u * (unit & 1u) + static_cast<uint32_t>(x)) * L::kTileBytes);
+              const uint64_t dk = tc::desc_at(dk0, (2u * (unit & 1u) + (k.n == 1 ? 0u : static_cast<uint32_t>(x))) * L::kTileBytes);
               const uint64_t dq = tc::desc_at(dq0, st * L::kTileBytes);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
@@ -320,30 +341,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::wait_bar(w.draining(), w.bar(L::kDrain), 0);
     } else if (warp == 2) {
       // ------------------------------------------------------ log-sum-exps --
+      // (those of the next tile are on their way while this one's are written)
       uint32_t at = 0;
+      int32_t t_off[4], g_off[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 32 * e + lane;
+        t_off[e] = r < rows_there ? r / prm.heads : 1 << 30;
+        g_off[e] = r % prm.heads;
+      }
+      const auto fetch = [&](const Walk& k, int32_t i, float (&x)[4], bool (&zero)[4]) {
+        const int32_t q = prm.splits == 1 ? i : i / prm.splits, g0 = (i - q * prm.splits) * prm.heads, t0 = q * prm.tokens;
+        const float* lse = a.lse + (static_cast<int64_t>(k.b) * a.H + k.h * prm.group) * a.T;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t t = t0 + t_off[e], g = g0 + g_off[e];
+          x[e] = t_off[e] < (1 << 30) && t < k.rows && g < prm.group ? lse[static_cast<int64_t>(g) * a.T + t] : -INFINITY;
+          // (rows that no copy fills, or that lie behind the last token, have S = 0)
+          zero[e] = t_off[e] == 1 << 30 || t >= a.T;
+        }
+      };
       Walk k;
-      for (k.begin(a); ok && k.left > 0; k.next(a))
-        for (int32_t i = k.first(prm), n = k.end(prm); i < n; ++i, ++at) {
-          const uint32_t st = at % L::kStages;
-          const int32_t t0 = i / prm.splits * prm.tokens, g0 = i % prm.splits * prm.heads;
+      for (k.begin(a); ok && k.left > 0; k.next(a)) {
+        const int32_t first = k.first(prm), n = k.end(prm);
+        float x[4];
+        bool zero[4];
+        if (first < n) fetch(k, first, x, zero);
+        for (int32_t i = first; i < n; ++i, ++at) {
+          const uint32_t st = at % L::kLse;
           float l[4];
           bool odd = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 32 * e + lane, t = t0 + r / prm.heads, g = g0 + r % prm.heads;
-            const bool there = r < rows_there && t < k.rows && g < prm.group;
-            const float x = there ? a.lse[(static_cast<int64_t>(k.b) * a.H + k.h * prm.group + g) * a.T + t] : -INFINITY;
-            odd |= x == -INFINITY;
-            l[e] = -x * kLog2e;
+            odd |= x[e] == -INFINITY && !zero[e];
+            l[e] = x[e] == -INFINITY ? -INFINITY : -x[e] * kLog2e;
           }
+          if (i + 1 < n) fetch(k, i + 1, x, zero);
           odd = __any_sync(0xffffffffu, odd);
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kQEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) break;
+          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kLEmpty + static_cast<int>(st)), ((at / L::kLse) & 1u) ^ 1u))) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) lse_ring[st * kTile + 32 * e + lane] = l[e];
           if (lane == 0) odd_ring[st] = odd ? 1 : 0;
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(w.bar(L::kQFull + static_cast<int>(st)));
+          if (lane == 0) tc::mbar_arrive(w.bar(L::kLFull + static_cast<int>(st)));
         }
+      }
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -352,47 +394,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256u * static_cast<uint32_t>(x);
-    uint32_t at = 0, unit = 0, s_cnt = 0;
+    uint32_t at = 0, unit = 0, s_cnt = 0, joins = 0;
     Walk k;
     for (k.begin(a); ok && k.left > 0; k.next(a), ++unit) {
       if (!(ok = tc::wait_bar_warp(w, w.bar(L::kKFull + static_cast<int>(unit & 1u)), (unit >> 1) & 1u))) break;
-      const int blk = 4 * x + (row >> 5);
-      const float scale = scale_ring[8 * (unit & 1u) + blk];
+      const bool alone = k.n == 1;       // one key tile: this half takes every second query tile
+      const int tile = alone ? 0 : x, blk = 4 * tile + (row >> 5);
+      // A scale of 0 or NaN counts as the smallest number, so that what is hidden
+      // (minus infinity) stays that; NaN comes back when the sum is there.
+      float scale = scale_ring[8 * (unit & 1u) + blk];
+      const bool odd_scale = scale != scale;
+      if (odd_scale || scale == 0.0f) scale = 0x1p-126f;
       const bool there = there_ring[8 * (unit & 1u) + blk] != 0;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(w.bar(L::kKEmpty + static_cast<int>(unit & 1u)));
-      const int32_t j0 = (k.tile + x) * kTile, j = j0 + row;
+      const int32_t j0 = (k.tile + tile) * kTile, j = j0 + row;
       const int32_t since = a.causal ? j - (k.len - k.rows) : 0;                    // the first row token that sees the key
       const int32_t all_since = a.causal ? j0 + kTile - 1 - (k.len - k.rows) : 0;   // and all keys of the tile
+      const int32_t first = k.first(prm), n = k.end(prm), step = alone ? 2 : 1;
       float sum = 0.0f;
-      const bool mine = x < k.n;
-      for (int32_t i = k.first(prm), n = k.end(prm); i < n; ++i, ++at) {
-        const uint32_t st = at % L::kStages;
-        if (!(ok = tc::wait_bar_warp(w, w.bar(L::kQFull + static_cast<int>(st)), (at / L::kStages) & 1u))) break;
-        if (mine) {
-          const int buf = static_cast<int>(s_cnt & 1u);
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kSFull + 2 * x + buf), (s_cnt >> 1) & 1u))) break;
-          ++s_cnt;
-          tc::tc_fence_after();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) tc::tmem_ld32(tS + 128u * static_cast<uint32_t>(buf) + 32u * b, s[b]);
-          tc::tmem_wait_ld();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(w.bar(L::kSFree + 2 * x + buf));
-          const int32_t t0 = i / prm.splits * prm.tokens;
-          const float* lse = lse_ring + st * kTile;
-          if (t0 >= all_since && odd_ring[st] == 0)
-            sum += sum_tile<false>(s, scale, lse, since, t0, prm, 0, k.rows);
-          else
-            sum += sum_tile<true>(s, scale, lse, since, t0, prm, 0, k.rows);
+      // S is read 64 columns at a time, the next ones under this one's exponentials
+      uint32_t s0[2][32], s1[2][32];
+      const auto fetch = [&](uint32_t (&s)[2][32], uint32_t half) {
+        const uint32_t at_col = tS + 128u * (s_cnt & 1u) + 64u * half;
+        tc::tmem_ld32(at_col, s[0]);
+        tc::tmem_ld32(at_col + 32u, s[1]);
+      };
+      int32_t i = first;
+      const auto pass = [&](int32_t until) {  // log-sum-exps of query tiles that the other half takes
+        for (; i < until; ++i, ++at) {
+          const uint32_t st = at % L::kLse;
+          if (!tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(st)), (at / L::kLse) & 1u)) return false;
+          if (lane == 0) tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(st)));
         }
+        return true;
+      };
+      int32_t mine = first + (alone ? x : 0);
+      if (!(ok = pass(min(mine, n)))) break;
+      // S of the next query tile: log-sum-exps and S are there, what does not count is hidden
+      const auto begin = [&]() {
+        const uint32_t st = at % L::kLse;
+        if (!tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(st)), (at / L::kLse) & 1u)) return false;
+        if (!tc::wait_bar_warp(w, w.bar(L::kSFull + 2 * x + static_cast<int>(s_cnt & 1u)), (s_cnt >> 1) & 1u)) return false;
+        tc::tc_fence_after();
+        const int32_t t0 = (prm.splits == 1 ? mine : mine / prm.splits) * prm.tokens;
+        if (t0 < all_since || odd_ring[st] != 0)
+          hide_rows(tS + 128u * (s_cnt & 1u), lse_ring + st * kTile, since, t0, prm.heads, k.rows);
+        fetch(s0, 0);
+        return true;
+      };
+      if (mine < n && !(ok = begin())) break;
+      while (mine < n) {
+        const uint32_t st = at % L::kLse;
+        const float* lse = lse_ring + st * kTile;
+        tc::tmem_wait_ld();
+        fetch(s1, 1);
+        float part = sum_rows(s0, scale, lse);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(w.bar(L::kQEmpty + static_cast<int>(st)));
+        if (lane == 0) tc::mbar_arrive(w.bar(L::kSFree + 2 * x + static_cast<int>(s_cnt & 1u)));
+        ++s_cnt;
+        ++i, ++at;
+        mine += step;
+        if (!(ok = pass(min(mine, n)))) break;
+        if (mine < n && !(ok = begin())) break;
+        part += sum_rows(s1, scale, lse + 64);
+        sum += part;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(st)));
       }
       if (!ok) break;
-      if (mine && there && j < k.shown) {
+      if (alone) {
+        // both halves' sums, always in this order
+        volatile float* join = reinterpret_cast<volatile float*>(smem + L::kOffJoin);
+        if (x == 1) {
+          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kJoinFree), (joins & 1u) ^ 1u))) break;
+          join[row] = sum;
+        } else {
+          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kJoinFull), joins & 1u))) break;
+          sum += join[row];
+        }
+        ++joins;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(w.bar(x == 1 ? L::kJoinFull : L::kJoinFree));
+      }
+      if (odd_scale && sum != 0.0f) sum = __uint_as_float(0x7FC00000u);
+      if ((x == 0 || !alone) && there && j < k.shown) {
         float* p = a.scores + k.b * a.scores_b + k.h * a.scores_h + j;
         *p += sum;
       }
