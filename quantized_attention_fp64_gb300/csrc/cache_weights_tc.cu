@@ -29,7 +29,7 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kTile = 128;        // keys of a tile, and query rows of one
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kTmemCols = 512;
@@ -48,19 +48,17 @@ struct Smem {
   static constexpr uint32_t kOffOdd = kOffThere + 2 * 32;             // [lse]: rows that are none
   static constexpr uint32_t kOffBar = (kOffOdd + 4 * kLse + 7) / 8 * 8;
   static constexpr int kQFull = 0, kQEmpty = kQFull + kStages, kKFull = kQEmpty + kStages, kKEmpty = kKFull + 2;
-  static constexpr int kSFull = kKEmpty + 2, kSFree = kSFull + 4, kDrain = kSFree + 4;
-  static constexpr int kLFull = kDrain + 1, kLEmpty = kLFull + kLse, kJoinFull = kLEmpty + kLse, kJoinFree = kJoinFull + 1;
-  static constexpr int kBars = kJoinFree + 1;
+  static constexpr int kSFull = kKEmpty + 2, kSFree = kSFull + 4, kDrain = kSFree + 4, kJoin = kDrain + 2;
+  static constexpr int kLFull = kJoin + 12, kLEmpty = kLFull + kLse, kBars = kLEmpty + kLse;
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffJoin = (kOffAbort + 4 + 15) / 16 * 16;  // [128] sums of the second half of the warps
-  static constexpr uint32_t kBytes = kOffJoin + 512;
+  static constexpr uint32_t kBytes = kOffAbort + 4;
 };
 static_assert(Smem<128>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
 
-// Registers: 512 threads launched at 128.
-constexpr uint32_t kCtlRegs = 72, kSumRegs = 176, kKeyRegs = 88;
-static_assert(128 * kCtlRegs + 256 * kSumRegs + 128 * kKeyRegs <= 512 * 128, "registers of one CTA");
+// Registers: 768 threads launched at 80.
+constexpr uint32_t kCtlRegs = 56, kSumRegs = 80, kKeyRegs = 104;
+static_assert(kSumRegs == 80 && 128 * kCtlRegs + 512 * kSumRegs + 128 * kKeyRegs <= kThreads * 80, "registers of one CTA");
 
 struct Params {
   CacheWeightsArgs a;
@@ -153,20 +151,18 @@ struct Walk {
   }
 };
 
-// 64 rows of a query tile for the thread's key: the sum of 2^(S scale + lse').
-__device__ __forceinline__ float sum_rows(const uint32_t (&s)[2][32], float scale, const float* lse) {
+// 32 rows of a query tile for the thread's key: the sum of 2^(S scale + lse').
+__device__ __forceinline__ float sum_rows(const uint32_t (&s)[32], float scale, const float* lse) {
   float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
   const float2 c2 = make_float2(scale, scale);
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 l = *reinterpret_cast<const float4*>(lse + 32 * b + k);
-      const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1])), c2, make_float2(l.x, l.y));
-      const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[b][k + 2]), __uint_as_float(s[b][k + 3])), c2, make_float2(l.z, l.w));
-      sa = __fadd2_rn(sa, make_float2(tc::exp2_approx(x01.x), tc::exp2_approx(x01.y)));
-      sb = __fadd2_rn(sb, make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y)));
-    }
+  for (int k = 0; k < 32; k += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(lse + k);
+    const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, make_float2(l.x, l.y));
+    const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, make_float2(l.z, l.w));
+    sa = __fadd2_rn(sa, make_float2(tc::exp2_approx(x01.x), tc::exp2_approx(x01.y)));
+    sb = __fadd2_rn(sb, make_float2(tc::exp2_approx(x23.x), tc::exp2_approx(x23.y)));
+  }
   return (sa.x + sa.y) + (sb.x + sb.y);
 }
 
@@ -199,6 +195,12 @@ __device__ __forceinline__ void hide_rows(uint32_t tS, const float* lse, int32_t
   tc::tmem_wait_st();
 }
 
+// Which of the four groups of sum warps (and S) takes the q-th query tile of a unit
+// with n key tiles, key tile x: two of them share a key tile, or four the only one.
+__device__ __forceinline__ int group_of(int n, int x, uint32_t q) {
+  return n == 1 ? static_cast<int>(q & 3u) : 2 * x + static_cast<int>(q & 1u);
+}
+
 // Four codes to two BF16 pairs: 128 + the low seven bits, less 128 or (negative) 256.
 __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t low = w & 0x7F7F7F7Fu, sign = w & 0x80808080u;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *w.abort_flag = 0;
     for (int i = 0; i < L::kStages; ++i) {
       tc::mbar_init(w.bar(L::kQFull + i), 1);
-      tc::mbar_init(w.bar(L::kQEmpty + i), 1);
+      tc::mbar_init(w.bar(L::kQEmpty + i), 2);
     }
     for (int i = 0; i < L::kLse; ++i) {
       tc::mbar_init(w.bar(L::kLFull + i), 1);
@@ -237,15 +239,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(w.bar(L::kKFull + i), 128);
-      tc::mbar_init(w.bar(L::kKEmpty + i), 9);
+      tc::mbar_init(w.bar(L::kKEmpty + i), 18);  // both issuers, 16 warps
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(w.bar(L::kSFull + i), 1);
       tc::mbar_init(w.bar(L::kSFree + i), 4);
     }
     tc::mbar_init(w.bar(L::kDrain), 1);
-    tc::mbar_init(w.bar(L::kJoinFull), 4);
-    tc::mbar_init(w.bar(L::kJoinFree), 4);
+    tc::mbar_init(w.bar(L::kDrain + 1), 1);
+    for (int i = 0; i < 12; ++i) tc::mbar_init(w.bar(L::kJoin + i), 4);
     tc::fence_mbar_init();
   }
   const int32_t rows_there = prm.heads * prm.tokens;  // rows that a query tile's copy fills
@@ -295,28 +297,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::wait_bar(d, w.bar(L::kQFull + static_cast<int>(p % L::kStages)), (p / L::kStages) & 1u);
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
       // ------------------------------------------------------------- products --
+      // One warp for the first two groups of sum warps, one for the others: a single one
+      // is not done with its waits in a product's time.
+      const int x = warp >> 1;
       const bool leader = tc::elect_one();
       const uint64_t dk0 = tc::sw128_desc(sbase + L::kOffK), dq0 = tc::sw128_desc(sbase + L::kOffQ);
-      uint32_t at = 0, unit = 0, s_cnt[2] = {0, 0};
+      uint32_t at = 0, unit = 0, freed = 0;  // freed: a bit for each S, its phase
       Walk k;
       for (k.begin(a); ok && k.left > 0; k.next(a), ++unit) {
         if (!(ok = tc::wait_bar_warp(w, w.bar(L::kKFull + static_cast<int>(unit & 1u)), (unit >> 1) & 1u))) break;
         const uint32_t at0 = at;
         for (int32_t i = k.first(prm), n = k.end(prm); i < n; ++i, ++at) {
-          const uint32_t st = at % L::kStages;
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kQFull + static_cast<int>(st)), (at / L::kStages) & 1u))) break;
-          const int alone = static_cast<int>(at - at0) & 1;  // one key tile: query tiles in turn to either half of the warps
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (k.n == 1 && x != alone) continue;
-            const int buf = 2 * x + static_cast<int>(s_cnt[x] & 1u);
-            if (!(ok = tc::wait_bar_warp(w, w.bar(L::kSFree + buf), ((s_cnt[x] >> 1) & 1u) ^ 1u))) break;
-            ++s_cnt[x];
+          const uint32_t st = at % L::kStages, ls = at % L::kLse;
+          // (the log-sum-exps as well: who waits for S then finds them, and misses no phase of theirs)
+          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(ls)), (at / L::kLse) & 1u)) ||
+              !(ok = tc::wait_bar_warp(w, w.bar(L::kQFull + static_cast<int>(st)), (at / L::kStages) & 1u)))
+            break;
+          if (k.n == 2 || (((at - at0) >> 1) & 1u) == static_cast<uint32_t>(x)) {
+            const int tile = k.n == 2 ? x : 0, buf = group_of(k.n, tile, at - at0);
+            if (!(ok = tc::wait_bar_warp(w, w.bar(L::kSFree + buf), ((freed >> buf) & 1u) ^ 1u))) break;
+            freed ^= 1u << buf;
             tc::tc_fence_after();
             if (leader) {
-              const uint64_t dk = tc::desc_at(dk0, (2u * (unit & 1u) + (k.n == 1 ? 0u : static_cast<uint32_t>(x))) * L::kTileBytes);
+              const uint64_t dk = tc::desc_at(dk0, (2u * (unit & 1u) + static_cast<uint32_t>(tile)) * L::kTileBytes);
               const uint64_t dq = tc::desc_at(dq0, st * L::kTileBytes);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
@@ -326,9 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc::mma_commit(w.bar(L::kSFull + buf));
             }
-            __syncwarp();
           }
-          if (!ok) break;
           if (leader) tc::mma_commit(w.bar(L::kQEmpty + static_cast<int>(st)));
           __syncwarp();
         }
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) tc::mma_commit(w.bar(L::kKEmpty + static_cast<int>(unit & 1u)));
         __syncwarp();
       }
-      if (leader) tc::mma_commit(w.bar(L::kDrain));
+      if (leader) tc::mma_commit(w.bar(L::kDrain + x));
       __syncwarp();
-      tc::wait_bar(w.draining(), w.bar(L::kDrain), 0);
+      tc::wait_bar(w.draining(), w.bar(L::kDrain + x), 0);
     } else if (warp == 2) {
       // ------------------------------------------------------ log-sum-exps --
       // (those of the next tile are on their way while this one's are written)
@@ -388,18 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 12) {
+  } else if (warp >= 8) {
     // --------------------------------------------------------------------- sums --
-    tc::regs_inc<kSumRegs>();
-    const int x = (warp - 4) >> 2;
+    const int group = (warp - 8) >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256u * static_cast<uint32_t>(x);
-    uint32_t at = 0, unit = 0, s_cnt = 0, joins = 0;
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128u * static_cast<uint32_t>(group);
+    uint32_t at = 0, unit = 0, s_cnt = 0;
     Walk k;
     for (k.begin(a); ok && k.left > 0; k.next(a), ++unit) {
       if (!(ok = tc::wait_bar_warp(w, w.bar(L::kKFull + static_cast<int>(unit & 1u)), (unit >> 1) & 1u))) break;
-      const bool alone = k.n == 1;       // one key tile: this half takes every second query tile
-      const int tile = alone ? 0 : x, blk = 4 * tile + (row >> 5);
+      const bool alone = k.n == 1;  // one key tile for all four groups
+      const int tile = alone ? 0 : group >> 1, blk = 4 * tile + (row >> 5);
       // A scale of 0 or NaN counts as the smallest number, so that what is hidden
       // (minus infinity) stays that; NaN comes back when the sum is there.
       float scale = scale_ring[8 * (unit & 1u) + blk];
@@ -411,84 +413,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t j0 = (k.tile + tile) * kTile, j = j0 + row;
       const int32_t since = a.causal ? j - (k.len - k.rows) : 0;                    // the first row token that sees the key
       const int32_t all_since = a.causal ? j0 + kTile - 1 - (k.len - k.rows) : 0;   // and all keys of the tile
-      const int32_t first = k.first(prm), n = k.end(prm), step = alone ? 2 : 1;
+      const int32_t first = k.first(prm), n = k.end(prm), step = alone ? 4 : 2;
       float sum = 0.0f;
-      // S is read 64 columns at a time, the next ones under this one's exponentials
-      uint32_t s0[2][32], s1[2][32];
-      const auto fetch = [&](uint32_t (&s)[2][32], uint32_t half) {
-        const uint32_t at_col = tS + 128u * (s_cnt & 1u) + 64u * half;
-        tc::tmem_ld32(at_col, s[0]);
-        tc::tmem_ld32(at_col + 32u, s[1]);
-      };
-      int32_t i = first;
-      const auto pass = [&](int32_t until) {  // log-sum-exps of query tiles that the other half takes
-        for (; i < until; ++i, ++at) {
-          const uint32_t st = at % L::kLse;
-          if (!tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(st)), (at / L::kLse) & 1u)) return false;
-          if (lane == 0) tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(st)));
-        }
-        return true;
-      };
-      int32_t mine = first + (alone ? x : 0);
-      if (!(ok = pass(min(mine, n)))) break;
-      // S of the next query tile: log-sum-exps and S are there, what does not count is hidden
-      const auto begin = [&]() {
-        const uint32_t st = at % L::kLse;
-        if (!tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(st)), (at / L::kLse) & 1u)) return false;
-        if (!tc::wait_bar_warp(w, w.bar(L::kSFull + 2 * x + static_cast<int>(s_cnt & 1u)), (s_cnt >> 1) & 1u)) return false;
+      for (int32_t q = alone ? group : group & 1; q < n - first; q += step) {
+        const uint32_t ls = (at + static_cast<uint32_t>(q)) % L::kLse, phase = (at + static_cast<uint32_t>(q)) / L::kLse;
+        if (!(ok = tc::wait_bar_warp(w, w.bar(L::kSFull + group), s_cnt & 1u)) ||
+            !(ok = tc::wait_bar_warp(w, w.bar(L::kLFull + static_cast<int>(ls)), phase & 1u)))
+          break;
+        ++s_cnt;
         tc::tc_fence_after();
-        const int32_t t0 = (prm.splits == 1 ? mine : mine / prm.splits) * prm.tokens;
-        if (t0 < all_since || odd_ring[st] != 0)
-          hide_rows(tS + 128u * (s_cnt & 1u), lse_ring + st * kTile, since, t0, prm.heads, k.rows);
-        fetch(s0, 0);
-        return true;
-      };
-      if (mine < n && !(ok = begin())) break;
-      while (mine < n) {
-        const uint32_t st = at % L::kLse;
-        const float* lse = lse_ring + st * kTile;
+        const float* lse = lse_ring + ls * kTile;
+        const int32_t t0 = (prm.splits == 1 ? first + q : (first + q) / prm.splits) * prm.tokens;
+        if (t0 < all_since || odd_ring[ls] != 0) hide_rows(tS, lse, since, t0, prm.heads, k.rows);
+        // S is read 32 columns at a time, the next ones under this one's exponentials;
+        // it is free for the next query tile when half of them are done
+        uint32_t s0[32], s1[32];
+        tc::tmem_ld32(tS, s0);
         tc::tmem_wait_ld();
-        fetch(s1, 1);
+        tc::tmem_ld32(tS + 32u, s1);
         float part = sum_rows(s0, scale, lse);
+        tc::tmem_wait_ld();
+        tc::tmem_ld32(tS + 64u, s0);
+        part += sum_rows(s1, scale, lse + 32);
+        tc::tmem_ld32(tS + 96u, s1);
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(w.bar(L::kSFree + 2 * x + static_cast<int>(s_cnt & 1u)));
-        ++s_cnt;
-        ++i, ++at;
-        mine += step;
-        if (!(ok = pass(min(mine, n)))) break;
-        if (mine < n && !(ok = begin())) break;
-        part += sum_rows(s1, scale, lse + 64);
+        if (lane == 0) tc::mbar_arrive(w.bar(L::kSFree + group));
+        part += sum_rows(s0, scale, lse + 64);
+        part += sum_rows(s1, scale, lse + 96);
         sum += part;
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(st)));
+        if (lane == 0) {
+          // eight arrivals: two groups of four warps, or one that arrives twice
+          tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(ls)));
+          if (alone) tc::mbar_arrive(w.bar(L::kLEmpty + static_cast<int>(ls)));
+        }
       }
       if (!ok) break;
-      if (alone) {
-        // both halves' sums, always in this order
-        volatile float* join = reinterpret_cast<volatile float*>(smem + L::kOffJoin);
-        if (x == 1) {
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kJoinFree), (joins & 1u) ^ 1u))) break;
-          join[row] = sum;
-        } else {
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kJoinFull), joins & 1u))) break;
-          sum += join[row];
-        }
-        ++joins;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(w.bar(x == 1 ? L::kJoinFull : L::kJoinFree));
-      }
+      at += static_cast<uint32_t>(max(n - first, 0));
       if (odd_scale && sum != 0.0f) sum = __uint_as_float(0x7FC00000u);
-      if ((x == 0 || !alone) && there && j < k.shown) {
-        float* p = a.scores + k.b * a.scores_b + k.h * a.scores_h + j;
-        *p += sum;
+      // The groups add their sums one after another, so that they always come in this
+      // order. (Four barriers for each, unit by unit: a group may be three units ahead of
+      // the next one, which has to begin a unit before the keys of the one after the
+      // next are brought.)
+      const int turn = 4 * group + static_cast<int>(unit & 3u);
+      if (group > 0 && !(ok = tc::wait_bar_warp(w, w.bar(L::kJoin + turn - 4), (unit >> 2) & 1u))) break;
+      if (there && j < k.shown && !(sum == 0.0f)) {
+        volatile float* p = a.scores + k.b * a.scores_b + k.h * a.scores_h + j;
+        *p = *p + sum;
       }
+      __syncwarp();
+      if (lane == 0 && group < 3) tc::mbar_arrive(w.bar(L::kJoin + turn));
     }
     tc::regs_dec<kCtlRegs>();
   } else {
     // --------------------------------------------------------------------- keys --
-    tc::regs_dec<kKeyRegs>();
+    tc::regs_inc<kKeyRegs>();
     const int g = lane >> 2, t4 = lane & 3;
     uint32_t unit = 0;
     bool bad = false;
@@ -498,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = tc::wait_bar_warp(w, w.bar(L::kKEmpty + static_cast<int>(buf)), ((unit >> 1) & 1u) ^ 1u))) break;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int local = 2 * (warp - 12) + y;             // block of the pair
+        const int local = 2 * (warp - 4) + y;             // block of the pair
         const int32_t blk = k.tile * 4 + local;
         if (local >= 4 * k.n) continue;
         int64_t slot = -1;
@@ -540,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // lengths that had to be cut
-  if (blockIdx.x == 0 && warp == 3) {
+  if (blockIdx.x == 0 && warp == 2) {
     bool bad = false;
     const int32_t capacity = static_cast<int32_t>(table_capacity(a.pt.max_pages, a.c.blocks_per_page));
     for (int b = lane; b < a.B; b += 32) {
