@@ -28,10 +28,13 @@ namespace sage {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kMoveWarps = 8;
+constexpr int kMoveWarps = 4;
 constexpr int kStaged = 48 * 1024;  // scores of a head that shared memory holds
 
-// Integers in the order of the scores.
+// Integers in the order of the scores, and back (-0 comes back as 0).
+__device__ __forceinline__ float score_of(uint32_t u) {
+  return __uint_as_float(u == 0u ? 0x7FC00000u : u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
 __device__ __forceinline__ uint32_t order_of(float x) {
   uint32_t u = __float_as_uint(x);
   if (x != x) return 0u;
@@ -113,9 +116,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const CacheEvictArgs a
   int32_t* before = work.before + head * (work.old_blocks + 1);
   if (in_place)
     for (int32_t i = tid; i < 2 * work.new_blocks; i += kThreads) work.read[head * 2 * work.new_blocks + i] = 0;
-  if (kStage && open) {
-#pragma unroll 4
-    for (int32_t i = tid; i < decided; i += kThreads) keys[i] = order_of(x[i]);
+  if (kStage) {
+#pragma unroll 8
+    for (int32_t i = tid; i < len; i += kThreads) keys[i] = order_of(x[i]);
     // (each thread reads back what it wrote, until the barriers below)
   }
   const auto key = [&](int32_t i) { return kStage ? keys[i] : order_of(x[i]); };
@@ -176,14 +179,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const CacheEvictArgs a
   }
   if (lane == 0) sums[0][warp] = sure, sums[1][warp] = same;
   __syncthreads();
-  uint32_t place = 0, equal = 0;
-  for (int w = 0; w < warp; ++w) {
-    place += sums[0][w] + min(left - min(left, equal), sums[1][w]);
-    equal += sums[1][w];
+  // (of the equal ones before this warp's part, `left` at most stay)
+  uint32_t place = lane < warp ? sums[0][lane] : 0u, equal = lane < warp ? sums[1][lane] : 0u;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    place += __shfl_xor_sync(0xffffffffu, place, s);
+    equal += __shfl_xor_sync(0xffffffffu, equal, s);
   }
+  place += min(left, equal);
   for (int32_t i0 = lo; i0 < hi; i0 += 32) {
     const int32_t i = i0 + lane;
-    const uint32_t u = open && i < decided ? key(i) : 0u;
+    const uint32_t u = i < hi ? key(i) : 0u;
     const bool s = i < hi && (!open || i >= decided || (need > 0 && u > known));
     const bool e = i < hi && !s && need > 0 && u == known;
     const uint32_t equals = __ballot_sync(0xffffffffu, e);
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const CacheEvictArgs a
     if (stays) {
       const uint32_t at = place + __popc(stay_mask & ((1u << lane) - 1u));
       kept[at] = i;
-      moved[at] = x[i];
+      moved[at] = score_of(u);
     }
     place += __popc(stay_mask);
     equal += __popc(equals);
@@ -232,7 +238,7 @@ __device__ __forceinline__ void store_release(uint32_t* p, uint32_t v) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CacheEvictArgs a, const Work work, bool in_place) {
+__global__ void __launch_bounds__(kMoveWarps * 32, 8) move_kernel(const CacheEvictArgs a, const Work work, bool in_place) {
   constexpr int kRows = D / 32;    // channels of a lane
   constexpr int kPitch = 36;       // bytes of a channel's row in shared memory: no bank conflicts
   __shared__ __align__(16) uint8_t tile[kMoveWarps][D * kPitch];
@@ -244,14 +250,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CacheEvictA
     if (threadIdx.x == 0) ticket = atomicAdd(work.ticket, 1u);
     __syncthreads();
   }
-  // units: block by block of all heads, keys and values
-  const int64_t heads = a.B * a.c.H;
-  const int64_t unit = static_cast<int64_t>(in_place ? ticket : blockIdx.x) * kMoveWarps + warp;
-  if (unit >= heads * 2 * work.new_blocks) return;
-  const bool values = (unit & 1) != 0;
-  const int64_t head = unit / 2 % heads;
-  const int32_t m = static_cast<int32_t>(unit / 2 / heads);
-  const int b = static_cast<int>(head / a.c.H), h = static_cast<int>(head % a.c.H);
+  // units: block by block of all heads, keys and values (counted in 32 bits)
+  const uint32_t heads = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.c.H);
+  const uint32_t unit = (in_place ? ticket : blockIdx.x) * kMoveWarps + static_cast<uint32_t>(warp);
+  if (unit >= heads * 2u * static_cast<uint32_t>(work.new_blocks)) return;
+  const bool values = (unit & 1u) != 0;
+  const uint32_t block = unit / 2u / heads, of_block = unit / 2u - block * heads;
+  const int32_t m = static_cast<int32_t>(block);
+  const int b = static_cast<int>(of_block / static_cast<uint32_t>(a.c.H)), h = static_cast<int>(of_block) - b * a.c.H;
+  const int64_t head = of_block;
   bool bad = false;
   const int32_t len = length_of(a, b, &bad), stay = min(len, a.keep);
   bad = false;
@@ -347,50 +354,64 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CacheEvictA
     if (lane == 0) a.c.ks[to] = top;
     return;
   }
-  // values: lane has channels lane, lane + 32, ...
+  // values: the old blocks on their way to L2, a line for each lane
+  const uint32_t all = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+  for (uint32_t rest = all; rest != 0;) {
+    const int64_t s = __shfl_sync(0xffffffffu, slot, __ffs(rest) - 1);
+    rest &= ~__ballot_sync(0xffffffffu, slot == s);
+    if (s >= 0 && lane * 128 < D * kCacheBlock)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + s * (D * kCacheBlock) + lane * 128));
+  }
+  // lane has channels lane, lane + 32, ...
   uint8_t* rows = tile[warp] + lane * kPitch;
 #pragma unroll
   for (int y = 0; y < kRows; ++y)
 #pragma unroll
     for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(rows + y * 32 * kPitch + 4 * e) = 0u;
   uint32_t w[kRows][8];
-  int64_t have = -1;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int64_t s = __shfl_sync(0xffffffffu, slot, i);
-    const int from = value_position(__shfl_sync(0xffffffffu, src, i) % kCacheBlock), at = value_position(i);
+  // where a lane's token stands in its old block's rows (low byte), and goes to
+  const int places = value_position(src & (kCacheBlock - 1)) | value_position(lane) << 8;
+  uint32_t left = all;
+  while (left != 0) {
+    // the tokens of one old block
+    const int64_t s = __shfl_sync(0xffffffffu, slot, __ffs(left) - 1);
+    uint32_t here = __ballot_sync(0xffffffffu, slot == s) & left;
+    left &= ~here;
     if (s < 0) continue;
-    if (s != have) {
-      have = s;
-      const int8_t* p = a.c.v + (s * D + lane) * kCacheBlock;
+    const int8_t* p = a.c.v + (s * D + lane) * kCacheBlock;
 #pragma unroll
-      for (int y = 0; y < kRows; ++y) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p + y * 32 * kCacheBlock);
-        const uint4 v = *reinterpret_cast<const uint4*>(p + y * 32 * kCacheBlock + 16);
-        w[y][0] = u.x, w[y][1] = u.y, w[y][2] = u.z, w[y][3] = u.w;
-        w[y][4] = v.x, w[y][5] = v.y, w[y][6] = v.z, w[y][7] = v.w;
-      }
+    for (int y = 0; y < kRows; ++y) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p + y * 32 * kCacheBlock);
+      const uint4 v = *reinterpret_cast<const uint4*>(p + y * 32 * kCacheBlock + 16);
+      w[y][0] = u.x, w[y][1] = u.y, w[y][2] = u.z, w[y][3] = u.w;
+      w[y][4] = v.x, w[y][5] = v.y, w[y][6] = v.z, w[y][7] = v.w;
     }
-    uint32_t word[kRows];
-    switch (from >> 2) {  // the same for the whole warp
+#pragma unroll 1
+    while (here != 0) {
+      const int at = __shfl_sync(0xffffffffu, places, __ffs(here) - 1);
+      here &= here - 1u;
+      uint32_t word[kRows];
+      switch ((at >> 2) & 7) {  // the same for the whole warp
 #define SAGE_PICK(e)                                            \
   case e:                                                       \
     _Pragma("unroll") for (int y = 0; y < kRows; ++y) word[y] = w[y][e]; \
     break;
-      SAGE_PICK(0)
-      SAGE_PICK(1)
-      SAGE_PICK(2)
-      SAGE_PICK(3)
-      SAGE_PICK(4)
-      SAGE_PICK(5)
-      SAGE_PICK(6)
-      default:
+        SAGE_PICK(0)
+        SAGE_PICK(1)
+        SAGE_PICK(2)
+        SAGE_PICK(3)
+        SAGE_PICK(4)
+        SAGE_PICK(5)
+        SAGE_PICK(6)
+        default:
 #pragma unroll
-        for (int y = 0; y < kRows; ++y) word[y] = w[y][7];
+          for (int y = 0; y < kRows; ++y) word[y] = w[y][7];
 #undef SAGE_PICK
-    }
+      }
+      uint8_t* to_byte = rows + (at >> 8);
 #pragma unroll
-    for (int y = 0; y < kRows; ++y) rows[y * 32 * kPitch + at] = static_cast<uint8_t>(word[y] >> (8 * (from & 3)));
+      for (int y = 0; y < kRows; ++y) to_byte[y * 32 * kPitch] = static_cast<uint8_t>(word[y] >> (8 * (at & 3)));
+    }
   }
   have_read();
   // ratios in the order of the positions

@@ -425,8 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* lse = lse_ring + ls * kTile;
         const int32_t t0 = (prm.splits == 1 ? first + q : (first + q) / prm.splits) * prm.tokens;
         if (t0 < all_since || odd_ring[ls] != 0) hide_rows(tS, lse, since, t0, prm.heads, k.rows);
-        // S is read 32 columns at a time, the next ones under this one's exponentials;
-        // it is free for the next query tile when half of them are done
+        // S is read 32 columns at a time, the next ones under this one's exponentials
         uint32_t s0[32], s1[32];
         tc::tmem_ld32(tS, s0);
         tc::tmem_wait_ld();
@@ -435,12 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         tc::tmem_ld32(tS + 64u, s0);
         part += sum_rows(s1, scale, lse + 32);
+        tc::tmem_wait_ld();
         tc::tmem_ld32(tS + 96u, s1);
+        part += sum_rows(s0, scale, lse + 64);
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(w.bar(L::kSFree + group));
-        part += sum_rows(s0, scale, lse + 64);
         part += sum_rows(s1, scale, lse + 96);
         sum += part;
         __syncwarp();
