@@ -67,7 +67,7 @@ struct Header {
 constexpr size_t kOddAt = 64, kHeaderBytes = 4096;
 constexpr int kMostScans = 960;
 
-__host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B + 1; }
+__host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B; }
 
 // Keys that row r of a block sees.
 template <bool kCausal>
@@ -83,6 +83,24 @@ __device__ __forceinline__ int32_t key_tiles(const Block& b, int i) {
 }
 
 // ------------------------------------------------------------------ planning --
+
+__device__ __forceinline__ bool bad_offsets(const int32_t* offsets, const int32_t* kv_offsets, int32_t b, int32_t N,
+                                            int32_t M) {
+  const int32_t o = offsets[b], k = kv_offsets[b];
+  return o < 0 || o > N || k < 0 || k > M || (b > 0 && (offsets[b - 1] > o || kv_offsets[b - 1] > k));
+}
+
+// The p-th row block of sequence b.
+__device__ __forceinline__ Block row_block(const int32_t* offsets, const int32_t* kv_offsets, int32_t b, int32_t p) {
+  const int32_t q0 = offsets[b], n = offsets[b + 1] - q0, kv0 = kv_offsets[b], m = kv_offsets[b + 1] - kv0;
+  Block e = {};
+  e.q0 = q0 + p * kRows;
+  e.rows = min(kRows, n - p * kRows);
+  e.kv0 = kv0;
+  e.keys = m;
+  e.sees = m - n + p * kRows + 1;
+  return e;
+}
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
@@ -114,7 +132,10 @@ __device__ __forceinline__ void scan_values(const int32_t* offsets, const int32_
   const int32_t lo = max(kv_offsets[0], 0), hi = static_cast<int32_t>(min(int64_t(M), int64_t(kv_offsets[B]) + kKeys - 1));
   const bool all = kCausal && offsets == kv_offsets;
   uint32_t acc[4] = {0u, 0u, 0u, 0u};
-  const int32_t chunks = kScanRows * sc.heads * sc.lanes;
+  // a row's chunks of 16 bytes to as many threads, or all threads to a row
+  const int lane_bits = __ffs(sc.lanes) - 1;
+  const int32_t row_chunks = sc.heads * sc.lanes, row_threads = min(row_chunks, kPlanThreads);
+  const int32_t rows_at_once = kPlanThreads / row_threads;
   for (int64_t r0 = lo + int64_t(blockIdx.x - 1) * kScanRows; r0 < hi; r0 += int64_t(gridDim.x - 1) * kScanRows) {
     const int32_t r1 = static_cast<int32_t>(min(int64_t(hi), r0 + kScanRows));
     if (!all) {
@@ -134,12 +155,11 @@ __device__ __forceinline__ void scan_values(const int32_t* offsets, const int32_
       }
       if (!need) continue;
     }
-#pragma unroll 4
-    for (int32_t x = tid; x < chunks; x += kPlanThreads) {
-      const int32_t c = x % sc.lanes, h = x / sc.lanes % sc.heads;
-      const int64_t r = r0 + x / sc.lanes / sc.heads;
-      if (r < r1) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sc.v + r * sc.v_ss + h * sc.v_sh + 8 * c);
+    for (int32_t c = tid % row_threads; c < row_chunks; c += row_threads) {
+      const uint16_t* p = sc.v + (c >> lane_bits) * sc.v_sh + 8 * (c & (sc.lanes - 1));
+#pragma unroll 8
+      for (int64_t r = r0 + tid / row_threads; r < r1 && tid < rows_at_once * row_threads; r += rows_at_once) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + r * sc.v_ss);
         acc[0] = collect(v.x, acc[0]);
         acc[1] = collect(v.y, acc[1]);
         acc[2] = collect(v.z, acc[2]);
@@ -167,10 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   bool bad = false;
-  for (int32_t b = tid; b <= B; b += kPlanThreads) {
-    const int32_t o = offsets[b], k = kv_offsets[b];
-    bad |= o < 0 || o > N || k < 0 || k > M || (b > 0 && (offsets[b - 1] > o || kv_offsets[b - 1] > k));
-  }
+  for (int32_t b = tid; b <= B; b += kPlanThreads) bad |= bad_offsets(offsets, kv_offsets, b, N, M);
   if (__syncthreads_or(bad)) {
     if (tid == 0 && blockIdx.x == 0) {
       *header = Header{0, 0, 0};
@@ -182,16 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
     scan_values<kCausal>(offsets, kv_offsets, B, M, sc);
     return;
   }
-  const auto block_of = [&](int32_t b, int32_t p) {
-    const int32_t q0 = offsets[b], n = offsets[b + 1] - q0, kv0 = kv_offsets[b], m = kv_offsets[b + 1] - kv0;
-    Block e;
-    e.q0 = q0 + p * kRows;
-    e.rows = min(kRows, n - p * kRows);
-    e.kv0 = kv0;
-    e.keys = m;
-    e.sees = m - n + p * kRows + 1;
-    return e;
-  };
+  const auto block_of = [&](int32_t b, int32_t p) { return row_block(offsets, kv_offsets, b, p); };
   const auto blocks_of = [&](int32_t b) { return (offsets[b + 1] - offsets[b] + kRows - 1) / kRows; };
   const auto cost = [&](const Block& e) { return max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1)); };
   for (int32_t b = tid; b < B; b += kPlanThreads) {
@@ -247,7 +255,8 @@ struct Smem {
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
   static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m
-  static constexpr uint32_t kBytes = kOffStat + 2 * 128 * 8;
+  static constexpr uint32_t kOffBlock = (kOffStat + 2 * 128 * 8 + 15) / 16 * 16;  // the CTA's block, and the header, without a list
+  static constexpr uint32_t kBytes = kOffBlock + sizeof(Block) + 16;
 };
 static_assert(Smem<128>::kBytes <= 232448u && Smem<64>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
 
@@ -285,7 +294,9 @@ struct Params {
   const Header* header;
   const uint32_t* odd;
   int scans;            // words of it
-  const Block* list;
+  const Block* list;    // null: no list, a unit for each CTA
+  const int32_t *offsets, *kv_offsets;
+  int32_t B, M;
   Out out;
   const uint16_t* v;
   int64_t v_ss, v_sh;
@@ -313,10 +324,11 @@ __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
 // them in that order forth and back.
 struct Units {
   const Params& prm;
+  const Block* list;
   int32_t units, u, step, other;
   Block e;
   int32_t h;
-  __device__ __forceinline__ Units(const Params& p, int32_t n) : prm(p), units(n) {
+  __device__ __forceinline__ Units(const Params& p, const Block* l, int32_t n) : prm(p), list(l), units(n) {
     const int32_t g = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
     u = c;
     step = 2 * (g - 1 - c) + 1;
@@ -327,10 +339,10 @@ struct Units {
   __device__ __forceinline__ void load() {
     if (u >= units) return;
     const int32_t b = prm.H.of(u);
-    e = load_block(prm.list, b);
+    e = load_block(list, b);
     h = u - b * prm.H.d;
     const int32_t next = u + step;
-    if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(prm.list + prm.H.of(next)));
+    if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + prm.H.of(next)));
   }
   __device__ __forceinline__ void advance() {
     u += step;
@@ -480,11 +492,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int32_t units = prm.header->blocks * prm.H.d;
-  // value tiles with hidden keys pass through warp 3
-  bool met = false;
-  for (int i = static_cast<int>(threadIdx.x); i < prm.scans; i += kThreads) met |= prm.odd[i] != 0;
-  const bool odd = __syncthreads_or(met);
+  // Few units: no list is made beforehand, each CTA looks its own up; value tiles
+  // with hidden keys then always pass through warp 3.
+  Block* own_block = reinterpret_cast<Block*>(smem + L::kOffBlock);
+  Header* own_header = reinterpret_cast<Header*>(own_block + 1);
+  const bool direct = prm.list == nullptr;
+  bool met = direct;
+  if (direct) {
+    if (warp == 0) {
+      const int32_t N = static_cast<int32_t>(prm.N), B = prm.B;
+      bool bad = false;
+      for (int32_t b = lane; b <= B; b += 32) bad |= bad_offsets(prm.offsets, prm.kv_offsets, b, N, prm.M);
+      bad = __any_sync(0xffffffffu, bad);
+      if (bad && lane == 0 && blockIdx.x == 0) atomicExch(prm.dev_err, kDevErrOffsets);
+      if (lane == 0) *own_header = bad ? Header{0, 0, 0} : Header{0, prm.offsets[0], prm.offsets[B]};
+      __syncwarp();
+      int32_t before = 0;
+      const int32_t mine = prm.H.of(static_cast<int32_t>(blockIdx.x));
+      for (int32_t b0 = 0; !bad && b0 < B && before <= mine; b0 += 32) {
+        const int32_t b = b0 + lane, n = b < B ? (prm.offsets[b + 1] - prm.offsets[b] + kRows - 1) / kRows : 0;
+        int32_t sum = n;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const int32_t x = __shfl_up_sync(0xffffffffu, sum, s);
+          if (lane >= s) sum += x;
+        }
+        const int32_t p = mine - (before + sum - n);
+        if (p >= 0 && p < n) {
+          *own_block = row_block(prm.offsets, prm.kv_offsets, b, p);
+          own_header->blocks = 1;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
+  } else {
+    for (int i = static_cast<int>(threadIdx.x); i < prm.scans; i += kThreads) met |= prm.odd[i] != 0;
+  }
+  const bool odd = __syncthreads_or(met);  // value tiles with hidden keys pass through warp 3
+  const Block* list = direct ? own_block - prm.H.of(static_cast<int32_t>(blockIdx.x)) : prm.list;
+  const Header* header = direct ? own_header : prm.header;
+  const int32_t units = direct ? (header->blocks != 0 ? static_cast<int32_t>(blockIdx.x) + 1 : 0) : header->blocks * prm.H.d;
 
   if (warp < 4) {
     tc::regs_dec<kCtlRegs>();
@@ -494,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
         int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
         bool ok = true;
-        for (Units it(prm, units); ok && it.valid(); it.advance()) {
+        for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
           const Block& e = it.e;
           const int32_t h = it.h, hk = prm.group.of(h);
           const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
@@ -531,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int32_t next = it.u + it.step;
               if (next < units) {
                 const int32_t b = prm.H.of(next);
-                const Block f = load_block(prm.list, b);
+                const Block f = load_block(list, b);
                 for (int t = 0; t < 2 && f.rows > 128 * t; ++t)
 #pragma unroll
                   for (int x = 0; x < D / 64; ++x) tc::tma_prefetch_3d(&tm_q, 64 * x, next - b * prm.H.d, f.q0 + 128 * t);
@@ -589,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) tc::mma_commit(w.bar(L::kQEmpty + t));
       };
       bool ok = true;
-      for (Units it(prm, units); ok && it.valid(); it.advance()) {
+      for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
         const Block& e = it.e;
         const int32_t own = key_tiles<kCausal>(e, t), theirs = key_tiles<kCausal>(e, 1 - t), n = max(own, theirs);
         if (own > 0) {
@@ -660,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------- value tiles with hidden keys --
       uint32_t base = 0, fixes = 0, done = 0;
       bool ok = true;
-      for (Units it(prm, units); ok && it.valid(); it.advance()) {
+      for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
         const Block& e = it.e;
         const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
         bool bad = false;
@@ -723,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_cnt = 0, done = 0;
     float2* stat = reinterpret_cast<float2*>(smem + L::kOffStat) + 128 * t + row;
     bool ok = true;
-    for (Units it(prm, units); ok && it.valid(); it.advance()) {
+    for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
       const int32_t mine = sees<kCausal>(e, 128 * t + row);
@@ -751,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     tc::regs_dec<kOutRegs>();
     if (prm.zero_rest) {
-      const int32_t lo = prm.header->rest_lo, hi = prm.header->rest_hi;
+      const int32_t lo = header->rest_lo, hi = header->rest_hi;
       // a row's head at a time for D / 8 threads
       const int at = static_cast<int>(threadIdx.x) - 384, c = at % (D / 8);
       const int64_t rest = lo + (prm.N - hi), items = rest * prm.H.d, step = static_cast<int64_t>(gridDim.x) * (128 / (D / 8));
@@ -763,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     uint32_t fixes = 0, done = 0, stats[2] = {0, 0};
     bool ok = true;
-    for (Units it(prm, units); ok && it.valid(); it.advance()) {
+    for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
       const int32_t masked = sees<kCausal>(e, 0) >> 7;
@@ -877,18 +924,31 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   Header* header = static_cast<Header*>(a.workspace);
   uint32_t* odd = reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kOddAt);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
-  const int64_t sms = sm_count_current(), rows64 = div_up(a.M, kScanRows), fit = 2 * sms < kMostScans ? 2 * sms : kMostScans;
-  const int scans = static_cast<int>(rows64 < fit ? rows64 : fit);
-  const Scan sc{a.v.p, a.v.ss, a.v.sh, a.Hkv, D / 8, odd};
-  cudaError_t e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(static_cast<unsigned>(1 + scans)),
-                                   kPlanThreads, 0, stream, a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
-                                   static_cast<int32_t>(a.M), header, list, sc, a.dev_err);
-  if (e != cudaSuccess) return e;
+  const int64_t units = most_blocks(a.N, a.B) * a.H, sms = sm_count_current();
+  // A unit for each CTA at most: no first kernel, which costs more than its list and
+  // its look at the values save then. 100 tokens, 28 heads (28 units): 8.8 us instead
+  // of 11.3; 1230 tokens (140 units): 24.4 us instead of 28.1.
+  const bool direct = units <= sms;
+  int scans = 0;
+  cudaError_t e;
+  if (!direct) {
+    const int64_t rows64 = div_up(a.M, kScanRows), fit = 2 * sms < kMostScans ? 2 * sms : kMostScans;
+    scans = static_cast<int>(rows64 < fit ? rows64 : fit);
+    const Scan sc{a.v.p, a.v.ss, a.v.sh, a.Hkv, D / 8, odd};
+    e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(static_cast<unsigned>(1 + scans)),
+                         kPlanThreads, 0, stream, a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
+                         static_cast<int32_t>(a.M), header, list, sc, a.dev_err);
+    if (e != cudaSuccess) return e;
+  }
   Params p{Divisor(a.H), Divisor(a.H / a.Hkv)};
   p.header = header;
   p.odd = odd;
   p.scans = scans;
-  p.list = list;
+  p.list = direct ? nullptr : list;
+  p.offsets = a.offsets;
+  p.kv_offsets = a.kv_offsets;
+  p.B = a.B;
+  p.M = static_cast<int32_t>(a.M);
   p.out = a.out;
   p.v = a.v.p;
   p.v_ss = a.v.ss;
@@ -901,8 +961,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;
   const int bytes = static_cast<int>(Smem<D>::kBytes);
   if ((e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes)) != cudaSuccess) return e;
-  const int64_t units = most_blocks(a.N, a.B) * a.H;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads,
+  const int64_t grid = units < 1 ? 1 : units < sms ? units : sms;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads,
                           static_cast<size_t>(bytes), stream, tq, tk, tv, p);
 }
 
