@@ -83,7 +83,7 @@ enum {
   SAGE_ERR_DTYPE = -3,          /* an input or output is not BF16 */
   SAGE_ERR_HEAD_DIM = -4,       /* D != 128 (D = 64 is also taken by the bundle entries and sage_sageattn_ex) */
   SAGE_ERR_SHAPE = -5,          /* Q, K, V shapes differ, or a size is negative */
-  SAGE_ERR_LAYOUT = -6,         /* tensor_layout is neither "NHD" nor "HND", or channel stride != 1 */
+  SAGE_ERR_LAYOUT = -6,         /* tensor_layout is neither "NHD" nor "HND", channel stride != 1, or strides that a call refuses */
   SAGE_ERR_ALIGN = -7,          /* a base pointer is not 16-byte aligned, or a stride is not a multiple of 8 elements */
   SAGE_ERR_NULLPTR = -8,        /* a required pointer is NULL */
   SAGE_ERR_WORKSPACE = -9,      /* workspace or scratch smaller than required */
@@ -552,11 +552,12 @@ SAGE_API int sage_cache_attention(const sage_cache_attention_args* args);
  * scores: fp32, element (b, hkv, j) at scores_dev + b * scores_stride_b +
  * hkv * scores_stride_h + j, j < scores_size; tokens at scores_size and up get
  * none. Scores of tokens that no row sees are left as they were. Every score is
- * summed in one fixed order, so results repeat bit for bit.
+ * summed in one fixed order, so results repeat bit for bit. The rows of scores
+ * must not overlap, and q's strides must be positive (LAYOUT).
  * Numbers: codes and queries enter exactly, sums are fp32.
  * A NaN in a key's scale makes that key's score NaN, a NaN in lse those of the
  * keys that its row sees.
- * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, TOO_LARGE (limits of
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, LAYOUT, ALIGN, ARG, TOO_LARGE (limits of
  * sage_cache_attention), ARCH, CUDA; on the device DEVICE_PAGE. */
 typedef struct sage_cache_add_weights_args {
   const sage_cache* cache;
@@ -682,15 +683,15 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * offsets, kv_offsets: int32 [B + 1] in device memory, not decreasing, within the
  * tensors. With offsets that break this no row belongs to a sequence, and the
  * device error word is set.
- * q, k, v, out: BF16, stride_b is not used; D = 128 or 64; out must not overlap
- * the inputs. sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
+ * q, k, v, out: BF16, stride_b is not used, the other strides of q, k and v must
+ * be positive (LAYOUT); D = 128 or 64; out must not overlap the inputs. sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16
  * (by 2^-9 of themselves) for the product with v, their sum is taken in fp32
  * before that.
  * workspace_dev: sage_prompt_attention_workspace_size bytes, 256-byte aligned,
  * contents do not matter; not used by another call at the same time.
- * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH, CUDA;
- * on the device DEVICE_OFFSETS. */
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, LAYOUT, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,
+ * CUDA; on the device DEVICE_OFFSETS. */
 typedef struct sage_prompt_attention_args {
   sage_bf16_tensor q, k, v;
   sage_bf16_tensor out;            /* written */

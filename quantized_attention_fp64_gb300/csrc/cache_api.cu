@@ -214,10 +214,12 @@ int sage_cache_add_weights(const sage_cache_add_weights_args* args) {
       (rc = check_heads(H, a.c.H)) != SAGE_OK ||
       (rc = check_table(args->table_dev, args->table_stride, args->max_pages, &a.pt)) != SAGE_OK ||
       (rc = check_ints(args->lengths_dev, true)) != SAGE_OK ||
-      (rc = check_ints(args->q_lengths_dev, false)) != SAGE_OK || (rc = check_tensor(args->q)) != SAGE_OK ||
-      (rc = check_floats(args->lse_dev, true)) != SAGE_OK || (rc = check_floats(args->scores_dev, true)) != SAGE_OK)
+      (rc = check_ints(args->q_lengths_dev, false)) != SAGE_OK ||
+      (rc = check_mapped(args->q, B, T, H)) != SAGE_OK || (rc = check_floats(args->lse_dev, true)) != SAGE_OK ||
+      (rc = check_floats(args->scores_dev, true)) != SAGE_OK)
     return rc;
   if (args->scores_size < 0) return SAGE_ERR_SHAPE;
+  if (!rows_apart(B, args->scores_stride_b, a.c.H, args->scores_stride_h, args->scores_size)) return SAGE_ERR_LAYOUT;
   if (a.c.num_pages == 0) a.pt.max_pages = 0;
   if ((rc = check_units(a.c, a.pt, B, T, H)) != SAGE_OK) return rc;
   if (!scale_ok(args->sm_scale)) return SAGE_ERR_ARG;

@@ -31,6 +31,35 @@ inline int check_tensor(const sage_bf16_tensor& t) {
              : SAGE_ERR_ALIGN;
 }
 
+// Tensors that a tensor map describes: the strides of dimensions with more than
+// one entry are positive and below 2^40 bytes (an expanded dimension has stride 0).
+inline bool mapped_stride_ok(int64_t n, int64_t s) { return n <= 1 || (s > 0 && s < int64_t(1) << 39); }
+inline int check_mapped(const sage_bf16_tensor& t, int64_t B, int64_t S, int64_t H) {
+  const int rc = check_tensor(t);
+  if (rc != SAGE_OK) return rc;
+  return mapped_stride_ok(B, t.stride_b) && mapped_stride_ok(S, t.stride_s) && mapped_stride_ok(H, t.stride_h)
+             ? SAGE_OK
+             : SAGE_ERR_LAYOUT;
+}
+
+// Rows of n entries, B by H of them, that are written: none may overlap another
+// (strides in entries, either one the larger).
+inline bool rows_apart(int64_t B, int64_t stride_b, int64_t H, int64_t stride_h, int64_t n) {
+  int64_t sb = stride_b < 0 ? -stride_b : stride_b, sh = stride_h < 0 ? -stride_h : stride_h;
+  if (n <= 0 || B <= 0 || H <= 0 || (B == 1 && H == 1)) return true;
+  if (B == 1) return sh >= n;
+  if (H == 1) return sb >= n;
+  if (sb < sh) {
+    int64_t x = sb;
+    sb = sh;
+    sh = x;
+    x = B;
+    B = H;
+    H = x;
+  }
+  return sh >= n && sb - n >= 0 && (sb - n) / sh >= H - 1;
+}
+
 inline Bf16In to_in(const sage_bf16_tensor& t) {
   return Bf16In{static_cast<const uint16_t*>(t.ptr_dev), t.stride_b, t.stride_s, t.stride_h};
 }

@@ -102,8 +102,9 @@ int sage_prompt_attention(const sage_prompt_attention_args* args) {
   if (args == nullptr) return SAGE_ERR_NULLPTR;
   int rc;
   const int64_t N = args->N, M = args->M, H = args->H, D = args->D, B = args->B;
-  if ((rc = check_prompt_sizes(N, M, H, args->Hkv, D, B)) != SAGE_OK || (rc = check_tensor(args->q)) != SAGE_OK ||
-      (rc = check_tensor(args->k)) != SAGE_OK || (rc = check_tensor(args->v)) != SAGE_OK ||
+  if ((rc = check_prompt_sizes(N, M, H, args->Hkv, D, B)) != SAGE_OK || (rc = check_mapped(args->q, 1, N, H)) != SAGE_OK ||
+      (rc = check_mapped(args->k, 1, M, args->Hkv)) != SAGE_OK ||
+      (rc = check_mapped(args->v, 1, M, args->Hkv)) != SAGE_OK ||
       (rc = check_tensor(args->out)) != SAGE_OK || (rc = check_ints(args->offsets_dev, true)) != SAGE_OK ||
       (rc = check_ints(args->kv_offsets_dev, false)) != SAGE_OK || (rc = check_floats(args->lse_dev, false)) != SAGE_OK)
     return rc;

@@ -474,3 +474,135 @@ def test_scores_graph_replay():
         assert np.array_equal(new.cpu().numpy(), want[0]) and np.array_equal(kept.cpu().numpy(), want[1])
         assert np.array_equal(moved.cpu().numpy(), want[2])
         same_cache(gpu, cc)
+
+
+@pytest.mark.parametrize("T", [1, 50])
+def test_weights_refuse_rows_that_overlap(T):
+    rng = np.random.default_rng(227)
+    table, P = make_table(rng, [100, 90], 64)
+    gpu = upload(random_cache(rng, P, 2, 64, 64))
+    q, lse = bf16(rng, 2, T, 4, 64), torch.zeros((2, 4, T), device="cuda")
+    row = torch.zeros((1, 1, 100), device="cuda")
+    args = (ints(table), ints([100, 90]), lse)
+    for scores in (row.expand(2, 2, 100), torch.zeros((2, 1, 100), device="cuda").expand(2, 2, 100),
+                   torch.zeros(500, device="cuda").as_strided((2, 2, 100), (150, 100, 1))):
+        with pytest.raises(SageError) as e:
+            sage.cache_add_weights(scores, q, gpu, *args)
+        assert e.value.code == -6 and (scores == 0).all()
+    scores = torch.zeros((2, 2, 100), device="cuda")
+    for x in (q[:1].expand(2, T, 4, 64), q[:, :, :1].expand(2, T, 4, 64)):
+        with pytest.raises(SageError) as e:
+            sage.cache_add_weights(scores, x, gpu, *args)
+        assert e.value.code == -6
+    # rows apart in the other order
+    turned = torch.zeros((2, 2, 100), device="cuda").transpose(0, 1)
+    sage.cache_add_weights(turned, q, gpu, *args)
+    sage.cache_add_weights(scores, q, gpu, *args)
+    assert torch.equal(turned, scores) and (scores > 0).any()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_scores_graphs_replayed_at_once(T):
+    """Two graphs of weights and eviction on caches of their own replay on two streams."""
+    rng = np.random.default_rng(228)
+    B, H, Hkv, D, page, keep = 3, 8, 2, 128, 64, 700
+    runs = []
+    for lengths in ([2000, 900, 1500], [800, 3000, 10]):
+        table, P = make_table(rng, [n + page for n in lengths], page)
+        c = random_cache(rng, P, Hkv, D, page)
+        q = bf16(rng, B, T, H, D)
+        runs.append((c, upload(c), ints(table), ints(lengths), q, torch.full((B, H, T), 5.0, device="cuda"),
+                     torch.zeros((B, Hkv, 3000), device="cuda")))
+
+    def step(r):
+        sage.cache_add_weights(r[6], r[4], r[1], r[2], r[3], r[5])
+        return sage.cache_evict(r[1], r[2], r[3], r[6], keep, recent=100)
+
+    def restore(r):
+        for x, y in zip((r[1].k_codes, r[1].v_codes, r[1].k_scale, r[1].v_scale),
+                        (r[0].k_codes, r[0].v_codes, r[0].k_scale, r[0].v_scale)):
+            x.copy_(dev(y))
+        r[6].zero_()
+
+    want = []
+    for r in runs:
+        res = step(r)
+        want.append([x.clone() for x in res] + [r[6].clone(), r[1].k_codes.clone(), r[1].v_codes.clone()])
+        restore(r)
+    streams, graphs, got = [torch.cuda.Stream() for _ in runs], [], []
+    torch.cuda.synchronize()
+    for s, r in zip(streams, runs):
+        with torch.cuda.stream(s):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                got.append(step(r))
+            graphs.append(g)
+    for _ in range(4):
+        for r in runs:
+            restore(r)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for r, res, w in zip(runs, got, want):
+            for x, y in zip(list(res) + [r[6], r[1].k_codes, r[1].v_codes], w):
+                assert torch.equal(x, y)
+
+
+def test_a_serving_run():
+    """The operators together: packed prompts are turned and attended, go into the cache, are cut back by their
+    weights, and tokens are generated behind them at their own positions."""
+    from test_cache_gpu import close as close_cached
+    from test_prompt_gpu import close as close_prompt, ends, formula
+
+    rng = np.random.default_rng(229)
+    rows, H, Hkv, D, page, keep, recent, new = [70, 1, 300, 0, 129], 8, 2, 128, 64, 96, 16, 3
+    B, N, T = len(rows), sum(rows), max(rows)
+    table, P = make_table(rng, [n + new for n in rows], page)
+    gpu = sage.alloc_cache(P, Hkv, "cuda", D, page)
+    tab, lens, off = ints(table), ints(rows), ints(ends(rows))
+    freqs = sage.rotary_table(D, base=500000.0, scaling="yarn", factor=4.0, original_length=1024, device="cuda")
+    q, k, v = bf16(rng, N + 5, H, D), bf16(rng, N + 5, Hkv, D), bf16(rng, N + 5, Hkv, D)
+    pos = torch.cat([torch.arange(n) for n in rows + [5]]).to(torch.int32).cuda()
+    q, k = sage.rotary(q, k, pos, freqs)
+    sm = 1 / math.sqrt(D) / freqs.magnitude ** 2
+    out, lse = sage.prompt_attention(q, k, v, off, sm_scale=sm, return_lse=True)
+    close_prompt(out[:N], lse[:, :N], formula(q[:N], k[:N], v[:N], rows, rows, True, sm))
+    assert (out[N:] == 0).all()
+
+    # into the cache, and what the prompts' rows gave each token
+    def padded(x):
+        y = torch.zeros((B, T) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+        for b in range(B):
+            y[b, :rows[b]] = x[ends(rows)[b]:ends(rows)[b + 1]]
+        return y
+
+    sage.cache_append(gpu, padded(k), padded(v), tab, torch.zeros_like(lens), counts=lens)
+    qp = padded(q)
+    _, lse = sage.cache_attention(qp, gpu, tab, lens, q_lengths=lens, is_causal=True, sm_scale=sm, return_lse=True)
+    scores = torch.zeros((B, Hkv, T + new), device="cuda")
+    sage.cache_add_weights(scores, qp, gpu, tab, lens, lse, q_lengths=lens, is_causal=True, sm_scale=sm)
+    total = torch.tensor(rows, device="cuda", dtype=torch.float64)[:, None] * (H // Hkv)
+    assert ((scores.double().sum(-1) - total).abs() <= total * 2.0 ** -11).all()
+    lens, kept, scores = sage.cache_evict(gpu, tab, lens, scores, keep, recent=recent)
+    assert lens.tolist() == [min(n, keep) for n in rows]
+    assert kept[2, :, keep - recent:].tolist() == [list(range(rows[2] - recent, rows[2]))] * Hkv
+
+    # new tokens, whose positions go on where the prompts ended
+    for t in range(new):
+        q, k, v = bf16(rng, B, 1, H, D), bf16(rng, B, 1, Hkv, D), bf16(rng, B, 1, Hkv, D)
+        q, k = sage.rotary(q, k, ints([[n + t] for n in rows]), freqs)
+        sage.cache_append(gpu, k, v, tab, lens)
+        lens = lens + 1
+        out, lse = sage.cache_attention(q, gpu, tab, lens, is_causal=True, sm_scale=sm, return_lse=True)
+        c = oc.Cache.__new__(oc.Cache)
+        c.page_size, c.H, c.D = page, Hkv, D
+        c.k_codes, c.v_codes = gpu.k_codes.cpu().numpy(), gpu.v_codes.cpu().numpy()
+        c.k_scale, c.v_scale = gpu.k_scale.cpu().numpy(), gpu.v_scale.cpu().numpy()
+        close_cached(out, lse, *oc.attention(c, f32(q), table, lens.tolist(), [1] * B, True, sm))
+        before = scores.clone()
+        sage.cache_add_weights(scores, q, gpu, tab, lens, lse, is_causal=True, sm_scale=sm)
+        total, bound = weights(c, f32(q), table, lens.tolist(), [1] * B, f32(lse), True, sm, T + new)
+        x = (scores.double() - before.double()).cpu().numpy()
+        assert (np.abs(x - total) <= bound + f32(scores).astype(np.float64) * 2.0 ** -24 + 1e-30).all()

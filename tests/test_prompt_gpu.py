@@ -351,3 +351,140 @@ def test_two_streams_at_once():
     for got, ref in zip(outs, refs):
         for out, lse in got:
             close(out, lse, ref)
+
+
+# ------------------------------------------------ calls with a list of units --
+# Calls of more units than there are SMs make a list of them first and look the values over. With every query head
+# repeated until there are as many, they give the bits of the calls without.
+
+
+def repeated(q, k, v, off, kv=None, **kw):
+    """The same call with each query head `r` times, which has over 300 units; returns it and r."""
+    r = -(-304 // q.shape[1])
+    out, lse = sage.prompt_attention(q.repeat_interleave(r, 1), k, v, off, kv_offsets=kv, return_lse=True, **kw)
+    return out, lse, r
+
+
+def same_bits(a, b):
+    return torch.equal(torch.nan_to_num(a, nan=7.25), torch.nan_to_num(b, nan=7.25)) and torch.equal(a.isnan(), b.isnan())
+
+
+def check_repeated(q, k, v, off, kv=None, **kw):
+    out, lse = sage.prompt_attention(q, k, v, off, kv_offsets=kv, return_lse=True, **kw)
+    many, many_lse, r = repeated(q, k, v, off, kv, **kw)
+    assert same_bits(many, out.repeat_interleave(r, 1)) and same_bits(many_lse, lse.repeat_interleave(r, 0))
+    return out, lse
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_many_units(case):
+    rows, keys, H, Hkv, D, causal = CASES[case]
+    if sum(rows) > 2600:
+        rows, keys = [r // 3 for r in rows], [k // 3 for k in keys or rows] if keys else None
+    q, k, v = inputs(120 + case, rows, keys or rows, H, Hkv, D, spare=9)
+    off = ints(ends(rows))
+    out, lse = check_repeated(q, k, v, off, ints(ends(keys)) if keys else None, is_causal=causal)
+    n, m = sum(rows), sum(keys or rows)
+    close(out[:n], lse[:, :n], formula(q[:n], k[:m], v[:m], rows, keys or rows, causal, 1 / math.sqrt(D)))
+    assert (out[n:] == 0).all() and (lse[:, n:] == -math.inf).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("at", [0, 63, 64, 130, 299, 300, 301, 360, 599, 600, 655, 698])
+def test_many_units_with_values_that_are_not_finite(at, what, D):
+    """One value anywhere: in what a row sees, behind it, in the next sequence's tile, behind the last sequence."""
+    rows = [300, 0, 299, 56]
+    q, k, v = inputs(140, rows, rows, 4, 2, D, spare=44)
+    v[at, 1, 5] = what
+    out, lse = check_repeated(q, k, v, ints(ends(rows)))
+    bad = ~torch.isfinite(out)
+    seen = torch.zeros(out.shape[0], dtype=torch.bool, device="cuda")
+    for lo, hi in zip(ends(rows)[:-1], ends(rows)[1:]):
+        if lo <= at < hi:
+            seen[at:hi] = True
+    assert torch.equal(bad[:, 2, 5], seen) and torch.equal(bad[:, 3, 5], seen)
+    bad[:, 2:, 5] = False
+    assert not bad.any() and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_units_of_longer_keys_with_values_that_are_not_finite(D):
+    rows, keys = [60, 400], [261, 461]
+    q, k, v = inputs(141, rows, keys, 4, 2, D, spare=20)
+    for at in (0, 200, 201, 230, 260, 262, 320, 700, 721):
+        w = v.clone()
+        w[at, 0, 3] = math.nan
+        check_repeated(q[:460], k, w, ints(ends(rows)), ints(ends(keys)))
+
+
+@pytest.mark.parametrize("off,kv", [
+    ([0, 50, 40, 100], None), ([-1, 50, 100], None), ([0, 50, 101], None), ([0, 2 ** 31 - 1, 100], None),
+    ([0, 50, 100], [0, 60, 50]), ([0, 50, 100], [0, 50, 90]), ([0, 50, 100], [-5, 50, 80])])
+def test_many_units_bad_offsets_are_flagged(off, kv):
+    g = gen(142)
+    q, k, v = bf16(g, 100, 160, 64), bf16(g, 80 if kv else 100, 1, 64), bf16(g, 80 if kv else 100, 1, 64)
+    out, lse = sage.prompt_attention(q, k, v, ints(off), kv_offsets=ints(kv) if kv else None, return_lse=True)
+    torch.cuda.synchronize()
+    assert sage.device_error() == DEVICE_OFFSETS
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_units_leave_rest_rows(D):
+    rows = [70, 300]
+    q, k, v = inputs(143, rows, rows, 160, 4, D, spare=60)
+    off = ints([20, 90, 390])
+    out = torch.full_like(q, 7.0)
+    sage.prompt_attention(q, k, v, off, out=out)
+    assert (out[:20] == 7).all() and (out[390:] == 7).all() and not (out[20:390] == 7).all(-1).any()
+    fresh = sage.prompt_attention(q, k, v, off)
+    assert (fresh[:20] == 0).all() and (fresh[390:] == 0).all() and torch.equal(fresh[20:390], out[20:390])
+
+
+def test_units_around_the_number_of_sms():
+    """Calls with a unit fewer than SMs, as many, and one more (units: (N // 256 + B) H)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    q, k, v = inputs(144, [200], [200], sms + 1, 1, 64)
+    off = ints([0, 200])
+    outs = [sage.prompt_attention(q[:, :h], k, v, off) for h in (sms + 1, sms, sms - 1)]
+    assert torch.equal(outs[0][:, :sms], outs[1]) and torch.equal(outs[0][:, :sms - 1], outs[2])
+    close(outs[0], None, formula(q, k, v, [200], [200], True, 0.125))
+
+
+def test_expanded_heads_and_rows_are_refused():
+    g = gen(145)
+    q, k = bf16(g, 10, 4, 64), bf16(g, 10, 1, 64)
+    for change in (dict(k=k.expand(10, 4, 64)), dict(v=k.expand(10, 4, 64)), dict(q=q[:, :1].expand(10, 4, 64)),
+                   dict(q=q[:1].expand(10, 4, 64))):
+        with pytest.raises(SageError) as err:
+            sage.prompt_attention(**{**dict(q=q, k=q, v=q, offsets=ints([0, 10])), **change})
+        assert err.value.code == -6
+
+
+def test_graphs_replayed_at_once():
+    """Two captured graphs of calls with a list replay on two streams, each with its own workspace."""
+    data = [inputs(146 + i, r, r, 16, 2, 128) for i, r in enumerate(([3000, 500], [100] * 20))]
+    offs = [ints(ends(r)) for r in ([3000, 500], [100] * 20)]
+    want = [sage.prompt_attention(*d, o, return_lse=True) for d, o in zip(data, offs)]
+    streams, graphs, got = [torch.cuda.Stream() for _ in data], [], []
+    torch.cuda.synchronize()
+    for s, d, o in zip(streams, data, offs):
+        with torch.cuda.stream(s):
+            sage.prompt_attention(*d, o, return_lse=True)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                got.append(sage.prompt_attention(*d, o, return_lse=True))
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for out, lse in got:
+            out.zero_()
+            lse.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (out, lse), (o, l) in zip(got, want):
+            assert torch.equal(out, o) and torch.equal(lse, l)
