@@ -558,6 +558,38 @@ def cache_evict(cache: QuantizedCache, page_table, lengths, scores, keep: int, r
 
     workspace: a uint8 tensor of cache_evict_workspace_size bytes that no other call uses at the same time; None: the
     library's own, one for each thread and stream (a captured graph gets its own from its memory pool)."""
+    keep, recent = int(keep), int(recent)
+    kept = key = None
+    if workspace is None:
+        try:
+            key = ("evict", cache.signature, keep, recent, page_table.shape, page_table.stride(), page_table.dtype,
+                   page_table.get_device(), lengths.shape, lengths.stride(), lengths.dtype, lengths.get_device(),
+                   scores.shape, scores.stride(), scores.dtype, scores.get_device(), _meta(out_table))
+            kept = _kept.calls.get(key)
+        except (AttributeError, TypeError):
+            key = None
+    if kept is not None and kept[0] == _get_device():
+        index, fn, ref, args, shape, need = kept
+        device = scores.device
+        new_lengths = torch.empty_like(lengths)
+        ids = torch.empty(shape, dtype=torch.int32, device=device)
+        new_scores = torch.empty(scores.shape, dtype=torch.float32, device=device)
+        stream = _stream_handle(index)
+        args.cache = cache.address
+        args.table_dev = page_table.data_ptr()
+        args.out_table_dev = args.table_dev if out_table is None else out_table.data_ptr()
+        args.lengths_dev = lengths.data_ptr()
+        args.scores_dev = scores.data_ptr()
+        args.lengths_out_dev = new_lengths.data_ptr()
+        args.kept_dev = ids.data_ptr()
+        args.scores_out_dev = new_scores.data_ptr()
+        workspace = _call_workspace(device, stream, need)
+        args.workspace_dev = workspace.data_ptr()
+        args.cuda_stream = stream
+        rc = fn(ref)
+        if rc:
+            _check(rc)
+        return new_lengths, ids, new_scores
     _check_cache(cache)
     B = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else -1
     lens = _ints(lengths, B if lengths is not None else None, cache, "lengths")
@@ -566,7 +598,6 @@ def cache_evict(cache: QuantizedCache, page_table, lengths, scores, keep: int, r
     table = _table(page_table, B, cache)
     to = table if out_table is None else _table(out_table, B, cache)
     at, sb, sh, n = _scores(scores, B, cache)
-    keep, recent = int(keep), int(recent)
     need = cache_evict_workspace_size(B, cache.H, cache.D, keep, n)  # refuses sizes, too
     device = cache.k_codes.device
     most = min(keep, n)
@@ -582,7 +613,8 @@ def cache_evict(cache: QuantizedCache, page_table, lengths, scores, keep: int, r
             raise SageError(SAGE_ERR_LAYOUT, "workspace must be contiguous")
     args = _lib.CacheEvictArgs(cache.address, *table, *to, lens or 16, at, sb, sh, n, B, keep, recent,
                                new_lengths.data_ptr() or 16, kept.data_ptr() or 16, most, new_scores.data_ptr() or 16)
-    with _on(cache.k_codes.get_device()) as stream:
+    index = cache.k_codes.get_device()
+    with _on(index) as stream:
         if workspace is None and need:
             workspace = _call_workspace(device, stream, need)
         if workspace is not None:
@@ -590,4 +622,7 @@ def cache_evict(cache: QuantizedCache, page_table, lengths, scores, keep: int, r
             args.workspace_bytes = workspace.numel() * workspace.element_size()
         args.cuda_stream = stream
         _check(_lib.load().sage_cache_evict(ctypes.byref(args)))
+    if key is not None and need and table[2] and to[2] and kept.numel():
+        args.workspace_bytes = need
+        _keep(key, (index, _lib.load().sage_cache_evict, ctypes.byref(args), args, kept.shape, need))
     return new_lengths, kept, new_scores

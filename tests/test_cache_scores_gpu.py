@@ -606,3 +606,25 @@ def test_a_serving_run():
         total, bound = weights(c, f32(q), table, lens.tolist(), [1] * B, f32(lse), True, sm, T + new)
         x = (scores.double() - before.double()).cpu().numpy()
         assert (np.abs(x - total) <= bound + f32(scores).astype(np.float64) * 2.0 ** -24 + 1e-30).all()
+
+
+def test_evict_again_with_other_tensors():
+    """Calls of one signature, whose checks the first one made, take each call's own tensors and sizes."""
+    rng = np.random.default_rng(230)
+    B, Hkv, D, page, n = 2, 2, 64, 32, 200
+    for keep, recent in ((50, 5), (50, 6), (51, 5)):
+        for place in ("in place", "other pages"):
+            for seed in range(3):
+                table, P = make_table(rng, [n, n], page)
+                P += 20
+                c = random_cache(rng, P, Hkv, D, page)
+                gpu = upload(c)
+                to = table if place == "in place" else (np.arange(2 * 7).reshape(2, 7) + P - 14).astype(np.int32)
+                lengths = [int(x) for x in rng.integers(0, n + 1, B)]
+                scores = some_scores(rng, B, Hkv, n)
+                got = sage.cache_evict(gpu, ints(table), ints(lengths), dev(scores), keep, recent=recent,
+                                       out_table=None if place == "in place" else ints(to))
+                want = evict(c, table, lengths, scores, keep, recent, to)
+                for x, y in zip(got, want):
+                    assert np.array_equal(x.cpu().numpy(), y)
+                same_cache(gpu, c)
