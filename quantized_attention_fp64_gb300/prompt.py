@@ -77,9 +77,9 @@ def prompt_attention(q, k, v, offsets, kv_offsets=None, is_causal: bool = True, 
         except (AttributeError, TypeError):
             key = None
     if kept is not None and kept[0] == _get_device():
-        index, fn, ref, args, qi, ki, vi, oi, shape, lse_shape, need = kept
+        index, fn, ref, args, qi, ki, vi, oi, like, lse_shape, need = kept
         device = q.device
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty_like(q) if like else torch.empty(q.shape, dtype=torch.bfloat16, device=device)
         stream = _stream_handle(index)
         qi.ptr_dev, ki.ptr_dev, vi.ptr_dev, oi.ptr_dev = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
         args.offsets_dev = offsets.data_ptr()
