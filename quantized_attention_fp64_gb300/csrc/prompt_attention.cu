@@ -47,6 +47,7 @@ constexpr int kThreads = 512;
 constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
+constexpr uint32_t kRedoWords = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8
 
@@ -62,10 +63,7 @@ struct Header {
   int32_t blocks;            // entries of the list
   int32_t rest_lo, rest_hi;  // rows [0, rest_lo) and [rest_hi, N) belong to no sequence
 };
-// Behind it a word of each scanning block of the first kernel: whether it has met
-// an infinity or a NaN. Then the list.
-constexpr size_t kOddAt = 64, kHeaderBytes = 4096;
-constexpr int kMostScans = 960;
+constexpr size_t kHeaderBytes = 256;  // then the list
 
 __host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B; }
 
@@ -104,7 +102,6 @@ __device__ __forceinline__ Block row_block(const int32_t* offsets, const int32_t
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
-constexpr int kScanRows = 64;
 
 // acc stays (0, 0) as long as no BF16 of the pairs is an infinity or a NaN.
 __device__ __forceinline__ uint32_t collect(uint32_t pair, uint32_t acc) {
@@ -115,70 +112,11 @@ __device__ __forceinline__ uint32_t collect(uint32_t pair, uint32_t acc) {
 // Those are the sign bits of this.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
 
-struct Scan {
-  const uint16_t* v;
-  int64_t v_ss, v_sh;
-  int32_t heads, lanes;  // of a row: lanes = D / 8 chunks of 16 bytes
-  uint32_t* odd;
-};
-
-// Looks for infinities and NaN among the values that share a key tile with a key
-// that some row does not see: those of the sequences' own tokens (causal), and
-// the 127 rows behind a sequence's end.
-template <bool kCausal>
-__device__ __forceinline__ void scan_values(const int32_t* offsets, const int32_t* kv_offsets, int32_t B, int32_t M,
-                                            const Scan& sc) {
-  const int tid = static_cast<int>(threadIdx.x);
-  const int32_t lo = max(kv_offsets[0], 0), hi = static_cast<int32_t>(min(int64_t(M), int64_t(kv_offsets[B]) + kKeys - 1));
-  const bool all = kCausal && offsets == kv_offsets;
-  uint32_t acc[4] = {0u, 0u, 0u, 0u};
-  // a row's chunks of 16 bytes to as many threads, or all threads to a row
-  const int lane_bits = __ffs(sc.lanes) - 1;
-  const int32_t row_chunks = sc.heads * sc.lanes, row_threads = min(row_chunks, kPlanThreads);
-  const int32_t rows_at_once = kPlanThreads / row_threads;
-  for (int64_t r0 = lo + int64_t(blockIdx.x - 1) * kScanRows; r0 < hi; r0 += int64_t(gridDim.x - 1) * kScanRows) {
-    const int32_t r1 = static_cast<int32_t>(min(int64_t(hi), r0 + kScanRows));
-    if (!all) {
-      // the last sequence that begins at or before the rows' end; it and the one before may reach them
-      int32_t a = 0, z = B;
-      while (z - a > 1) {
-        const int32_t mid = (a + z) / 2;
-        if (kv_offsets[mid] < r1) a = mid;
-        else z = mid;
-      }
-      bool need = false;
-      for (int32_t b = a; b >= 0 && !need; --b) {
-        const int32_t end = kv_offsets[b + 1], own = kCausal ? offsets[b + 1] - offsets[b] : 0;
-        const int64_t first = int64_t(end) - own - kKeys;  // (the tile of the first own token begins at most so early)
-        need = r1 > first && r0 < int64_t(end) + kKeys;
-        if (int64_t(kv_offsets[b]) + kKeys < r0) break;    // sequences before end too early
-      }
-      if (!need) continue;
-    }
-    for (int32_t c = tid % row_threads; c < row_chunks; c += row_threads) {
-      const uint16_t* p = sc.v + (c >> lane_bits) * sc.v_sh + 8 * (c & (sc.lanes - 1));
-#pragma unroll 8
-      for (int64_t r = r0 + tid / row_threads; r < r1 && tid < rows_at_once * row_threads; r += rows_at_once) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p + r * sc.v_ss);
-        acc[0] = collect(v.x, acc[0]);
-        acc[1] = collect(v.y, acc[1]);
-        acc[2] = collect(v.z, acc[2]);
-        acc[3] = collect(v.w, acc[3]);
-      }
-    }
-  }
-  const bool odd = not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]);
-  const bool any = __syncthreads_or(odd);
-  if (tid == 0) sc.odd[blockIdx.x - 1] = any ? 1u : 0u;
-}
-
-// Block 0 lists the row blocks of all sequences by their key tiles, the most first
-// (in 1024 classes); the others look the values over. Offsets that decrease or
-// leave the tensors: no block, all rows are rest.
+// Lists the row blocks of all sequences by their key tiles, the most first (in 1024
+// classes). Offsets that decrease or leave the tensors: no block, all rows are rest.
 template <bool kCausal>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offsets, const int32_t* kv_offsets, int32_t B,
-                                                            int32_t N, int32_t M, Header* header, Block* list, const Scan sc,
-                                                            int* dev_err) {
+                                                            int32_t N, int32_t M, Header* header, Block* list, int* dev_err) {
   __shared__ int32_t count[kBins];
   __shared__ int32_t most;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
@@ -189,14 +127,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
   bool bad = false;
   for (int32_t b = tid; b <= B; b += kPlanThreads) bad |= bad_offsets(offsets, kv_offsets, b, N, M);
   if (__syncthreads_or(bad)) {
-    if (tid == 0 && blockIdx.x == 0) {
+    if (tid == 0) {
       *header = Header{0, 0, 0};
       atomicExch(dev_err, kDevErrOffsets);
     }
-    return;  // (without units nothing asks for the scan)
-  }
-  if (blockIdx.x > 0) {
-    scan_values<kCausal>(offsets, kv_offsets, B, M, sc);
     return;
   }
   const auto block_of = [&](int32_t b, int32_t p) { return row_block(offsets, kv_offsets, b, p); };
@@ -255,7 +189,8 @@ struct Smem {
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
   static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m
-  static constexpr uint32_t kOffBlock = (kOffStat + 2 * 128 * 8 + 15) / 16 * 16;  // the CTA's block, and the header, without a list
+  static constexpr uint32_t kOffRedo = kOffStat + 2 * 128 * 8;  // units to do again, and whether there are any
+  static constexpr uint32_t kOffBlock = (kOffRedo + 4 * (kRedoWords + 1) + 15) / 16 * 16;  // the CTA's block, and the header, without a list
   static constexpr uint32_t kBytes = kOffBlock + sizeof(Block) + 16;
 };
 static_assert(Smem<128>::kBytes <= 232448u && Smem<64>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
@@ -292,8 +227,6 @@ struct Divisor {
 struct Params {
   Divisor H, group;     // query heads, and those that share a key/value head
   const Header* header;
-  const uint32_t* odd;
-  int scans;            // words of it
   const Block* list;    // null: no list, a unit for each CTA
   const int32_t *offsets, *kv_offsets;
   int32_t B, M;
@@ -303,6 +236,7 @@ struct Params {
   float* lse;
   int64_t N;
   bool zero_rest;
+  bool wide_out;        // rows of out begin at whole sectors (32 bytes)
   float scale;          // c
   int* dev_err;
 };
@@ -328,12 +262,19 @@ struct Units {
   int32_t units, u, step, other;
   Block e;
   int32_t h;
-  __device__ __forceinline__ Units(const Params& p, const Block* l, int32_t n) : prm(p), list(l), units(n) {
+  uint32_t number;       // of the unit among the CTA's
+  const uint32_t* redo;  // the units to take (a bit for each number modulo 32 kRedoWords), or null: all
+  __device__ __forceinline__ Units(const Params& p, const Block* l, int32_t n, const uint32_t* r)
+      : prm(p), list(l), units(n), number(0), redo(r) {
     const int32_t g = static_cast<int32_t>(gridDim.x), c = static_cast<int32_t>(blockIdx.x);
     u = c;
     step = 2 * (g - 1 - c) + 1;
     other = 2 * c + 1;
-    load();
+    if (!taken()) advance();
+    else load();
+  }
+  __device__ __forceinline__ bool taken() const {
+    return redo == nullptr || (redo[number / 32u % kRedoWords] >> (number & 31u) & 1u) != 0;
   }
   __device__ __forceinline__ bool valid() const { return u < units; }
   __device__ __forceinline__ void load() {
@@ -345,10 +286,13 @@ struct Units {
     if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + prm.H.of(next)));
   }
   __device__ __forceinline__ void advance() {
-    u += step;
-    const int32_t s = step;
-    step = other;
-    other = s;
+    do {
+      u += step;
+      const int32_t s = step;
+      step = other;
+      other = s;
+      ++number;
+    } while (u < units && !taken());
     load();
   }
 };
@@ -455,8 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), prm.dev_err};
   volatile int32_t* bad_units = reinterpret_cast<volatile int32_t*>(smem + L::kOffBad);
+  uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kOffRedo);
   if (threadIdx.x == 0) {
     *w.abort_flag = 0;
+    for (uint32_t i = 0; i <= kRedoWords; ++i) redo[i] = 0;
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(w.bar(L::kQFull + i), 1);
       tc::mbar_init(w.bar(L::kQEmpty + i), 1);
@@ -492,12 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmem);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  // Few units: no list is made beforehand, each CTA looks its own up; value tiles
-  // with hidden keys then always pass through warp 3.
+  // Few units: no list is made beforehand, each CTA looks its own up.
   Block* own_block = reinterpret_cast<Block*>(smem + L::kOffBlock);
   Header* own_header = reinterpret_cast<Header*>(own_block + 1);
   const bool direct = prm.list == nullptr;
-  bool met = direct;
   if (direct) {
     if (warp == 0) {
       const int32_t N = static_cast<int32_t>(prm.N), B = prm.B;
@@ -525,23 +469,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         before += __shfl_sync(0xffffffffu, sum, 31);
       }
     }
-  } else {
-    for (int i = static_cast<int>(threadIdx.x); i < prm.scans; i += kThreads) met |= prm.odd[i] != 0;
+    __syncthreads();
   }
-  const bool odd = __syncthreads_or(met);  // value tiles with hidden keys pass through warp 3
   const Block* list = direct ? own_block - prm.H.of(static_cast<int32_t>(blockIdx.x)) : prm.list;
   const Header* header = direct ? own_header : prm.header;
   const int32_t units = direct ? (header->blocks != 0 ? static_cast<int32_t>(blockIdx.x) + 1 : 0) : header->blocks * prm.H.d;
 
+  // After the units: whether some have to be done again. All warps meet here once.
+  const auto again = [&]() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+    return reinterpret_cast<volatile uint32_t*>(redo)[kRedoWords] != 0;
+  };
   if (warp < 4) {
     tc::regs_dec<kCtlRegs>();
     if (warp == 0) {
       // -------------------------------------------------------------- copies --
-      if (lane == 0) {
-        uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
-        int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
-        bool ok = true;
-        for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
+      uint32_t at = 0, q_cnt[2] = {0, 0}, fixes = 0;  // ring position, queries loaded, tiles for warp 3
+      int32_t raw[L::kStages];                          // of the stage's tile: its number among those, or -1
+      bool ok = true;
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass > 0 && !again()) break;
+        for (Units it(prm, list, lane == 0 ? units : 0, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
           const Block& e = it.e;
           const int32_t h = it.h, hk = prm.group.of(h);
           const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
@@ -554,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, h, e.q0 + 128 * t,
                               w.bar(L::kQFull + t));
           };
-          const int32_t masked = odd ? sees<kCausal>(e, 0) >> 7 : n;  // value tiles from here on pass through warp 3
+          // in the second pass value tiles with hidden keys pass through warp 3
+          const int32_t masked = pass > 0 ? sees<kCausal>(e, 0) >> 7 : n;
           const auto tile = [&](const void* map, int32_t j, bool through) {
             const uint32_t st = at % L::kStages;
             if (!(ok = wait_bar(w, w.bar(L::kEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) return;
@@ -586,6 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      }
+      if (lane == 0) {
         if (!ok) {
           // every copy that this thread issued lands before the CTA exits
           const tc::Waits d = w.draining();
@@ -636,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) tc::mma_commit(w.bar(L::kQEmpty + t));
       };
       bool ok = true;
-      for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
+      int pass = 0;
+    units_of_tile:
+      for (Units it(prm, list, units, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
         const Block& e = it.e;
         const int32_t own = key_tiles<kCausal>(e, t), theirs = key_tiles<kCausal>(e, 1 - t), n = max(own, theirs);
         if (own > 0) {
@@ -699,19 +653,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) ++done;
         base += 2u * static_cast<uint32_t>(n);
       }
+      if (pass++ == 0 && again()) goto units_of_tile;
       // all products are done before TMEM is freed
       if (leader) tc::mma_commit(w.bar(L::kDrain + t));
       __syncwarp();
       wait_bar(w.draining(), w.bar(L::kDrain + t), 0);
     } else {
       // ---------------------------------------- value tiles with hidden keys --
+      // (in the second pass; the ring goes on from the first)
       uint32_t base = 0, fixes = 0, done = 0;
       bool ok = true;
-      for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
+      const int32_t second = again() ? units : 0;
+      for (Units it(prm, list, second, nullptr); it.valid(); it.advance())
+        base += 2u * static_cast<uint32_t>(max(key_tiles<kCausal>(it.e, 0), key_tiles<kCausal>(it.e, 1)));
+      for (Units it(prm, list, second, redo); ok && it.valid(); it.advance()) {
         const Block& e = it.e;
         const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
         bool bad = false;
-        for (int32_t j = odd ? sees<kCausal>(e, 0) >> 7 : n; j < n; ++j) {
+        for (int32_t j = sees<kCausal>(e, 0) >> 7; j < n; ++j) {
           const uint32_t p = base + 2u * static_cast<uint32_t>(j) + 1u;
           if (!(ok = wait_bar_warp(w, w.bar(L::kRaw + static_cast<int>(fixes % kFixes)), (fixes / kFixes) & 1u))) break;
           uint8_t* tile = smem + L::kOffRing + (p % L::kStages) * L::kTile;
@@ -770,7 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_cnt = 0, done = 0;
     float2* stat = reinterpret_cast<float2*>(smem + L::kOffStat) + 128 * t + row;
     bool ok = true;
-    for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
+    int pass = 0;
+  units_of_rows:
+    for (Units it(prm, list, units, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
       const int32_t mine = sees<kCausal>(e, 128 * t + row);
@@ -789,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n > 0) ++done;
     }
+    if (pass++ == 0 && again()) goto units_of_rows;
     tc::regs_dec<kCtlRegs>();
   } else {
     // ------------------------------------------------------------------ output --
@@ -808,19 +770,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
       }
     }
-    uint32_t fixes = 0, done = 0, stats[2] = {0, 0};
+    uint32_t fixes = 0, fixed = 0, done = 0, stats[2] = {0, 0};  // (fixed: units of the second pass with keys)
     bool ok = true;
-    for (Units it(prm, list, units); ok && it.valid(); it.advance()) {
+    int pass = 0;
+  units_of_output:
+    for (Units it(prm, list, units, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
       const int32_t masked = sees<kCausal>(e, 0) >> 7;
       bool bad = false;  // the unit has infinities or NaN that warp 3 has cleared
-      if (odd && n > masked) {
+      if (pass > 0 && n > masked) {
         fixes += static_cast<uint32_t>(n - masked);
         const uint32_t f = fixes - 1;
         if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(f % kFixes)), (f / kFixes) & 1u))) break;
-        bad = kCausal && bad_units[done % kFixes] != 0;
+        bad = kCausal && bad_units[fixed % kFixes] != 0;
       }
+      uint32_t met = 0;  // infinities and NaN among the outputs
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int32_t own = t == 0 ? n0 : n1, r = 128 * t + row;
@@ -836,49 +801,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = st.x == 0.0f ? 0.0f : 1.0f / st.x;
         if (prm.lse != nullptr && r < e.rows)
           prm.lse[static_cast<int64_t>(it.h) * prm.N + e.q0 + r] = st.x == 0.0f ? -INFINITY : (log2f(st.x) - st.y) * kLn2;
-        // Four lanes exchange their rows' chunks of 16 bytes, so that a store covers 64
-        // bytes of 8 rows instead of 16 of 32: chunk 4 x + q of row j of the four goes
-        // from lane j to lane q (two exchanges, with the neighbour and the next pair).
-        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r - (lane & 3)) * prm.out.ss + it.h * prm.out.sh;
+        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + it.h * prm.out.sh;
+        const bool there = r < e.rows;
+        // 16 channels at a time, a whole sector for each lane's store: little code
 #pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t o[32];
-          tc::tmem_ld32(tmem + lanes + col_o<D>(t) + 32u * static_cast<uint32_t>(x), o);
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t o[16], c[8], acc[2] = {0u, 0u};
+          tc::tmem_ld16(tmem + lanes + col_o<D>(t) + 16u * static_cast<uint32_t>(x), o);
           tc::tmem_wait_ld();
-          if (x == D / 32 - 1 && n > 0) {
+          if (x == D / 16 - 1 && n > 0) {
             tc::tc_fence_before();
             tc::mbar_arrive(w.bar(L::kOEmpty + t));
           }
-          uint32_t c[4][4];
+          const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              c[q][k] = tc::bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv, __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
-              if (own == 0) c[q][k] = 0u;  // (O is not this unit's)
-            }
-#pragma unroll
-          for (int s = 1; s <= 2; s *= 2) {
-            const bool upper = (lane & s) != 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if ((q & s) == 0) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? c[q][k] : c[q + s][k], s);
-                  if (upper) c[q][k] = got;
-                  else c[q + s][k] = got;
-                }
-              }
+          for (int k = 0; k < 8; ++k) {
+            const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), inv2);
+            c[k] = tc::bf16x2(y.x, y.y);
+            acc[k & 1] = collect(c[k], acc[k & 1]);
           }
+          if (own == 0) {  // (O is not this unit's)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (r - (lane & 3) + j < e.rows)
-              *reinterpret_cast<uint4*>(dst + j * prm.out.ss + 32 * x + 8 * (lane & 3)) = make_uint4(c[j][0], c[j][1], c[j][2], c[j][3]);
+            for (int k = 0; k < 8; ++k) c[k] = 0u;
+          }
+          if (there) {
+            if (own > 0) met |= not_finite(acc[0]) | not_finite(acc[1]);
+            if (prm.wide_out) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * x), "r"(c[0]), "r"(c[1]),
+                           "r"(c[2]), "r"(c[3]), "r"(c[4]), "r"(c[5]), "r"(c[6]), "r"(c[7])
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4*>(dst + 16 * x) = make_uint4(c[0], c[1], c[2], c[3]);
+              *reinterpret_cast<uint4*>(dst + 16 * x + 8) = make_uint4(c[4], c[5], c[6], c[7]);
+            }
+          }
         }
         if (kCausal && bad) {
-          __syncwarp();  // the row's values were stored by all four lanes
-          dst += (lane & 3) * prm.out.ss;
           const int32_t mine = r < e.rows ? sees<kCausal>(e, r) : 0;
 #pragma unroll 1
           for (int32_t k = masked * kKeys; k < mine; ++k) {
@@ -893,8 +851,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (n > 0) ++done;
+      if (pass == 0 && __any_sync(0xffffffffu, met != 0u)) {
+        if (lane == 0) {
+          atomicOr(redo + it.number / 32u % kRedoWords, 1u << (it.number & 31u));
+          reinterpret_cast<volatile uint32_t*>(redo)[kRedoWords] = 1u;
+        }
+        __syncwarp();
+      }
+      if (n > 0) {
+        ++done;
+        if (pass > 0) ++fixed;
+      }
     }
+    if (pass++ == 0 && again()) goto units_of_output;
     tc::regs_dec<kCtlRegs>();
   }
 
@@ -922,28 +891,19 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   if (!make_map(&tq, a.q, a.N, a.H, D) || !make_map(&tk, a.k, rows, a.Hkv, D) || !make_map(&tv, a.v, rows, a.Hkv, D))
     return cudaErrorInvalidValue;
   Header* header = static_cast<Header*>(a.workspace);
-  uint32_t* odd = reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + kOddAt);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
   const int64_t units = most_blocks(a.N, a.B) * a.H, sms = sm_count_current();
   // A unit for each CTA at most: no first kernel, which costs more than its list and
   // its look at the values save then. 100 tokens, 28 heads (28 units): 8.8 us instead
   // of 11.3; 1230 tokens (140 units): 24.4 us instead of 28.1.
   const bool direct = units <= sms;
-  int scans = 0;
   cudaError_t e;
-  if (!direct) {
-    const int64_t rows64 = div_up(a.M, kScanRows), fit = 2 * sms < kMostScans ? 2 * sms : kMostScans;
-    scans = static_cast<int>(rows64 < fit ? rows64 : fit);
-    const Scan sc{a.v.p, a.v.ss, a.v.sh, a.Hkv, D / 8, odd};
-    e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(static_cast<unsigned>(1 + scans)),
-                         kPlanThreads, 0, stream, a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
-                         static_cast<int32_t>(a.M), header, list, sc, a.dev_err);
-    if (e != cudaSuccess) return e;
-  }
+  if (!direct && (e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPlanThreads, 0, stream,
+                                       a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
+                                       static_cast<int32_t>(a.M), header, list, a.dev_err)) != cudaSuccess)
+    return e;
   Params p{Divisor(a.H), Divisor(a.H / a.Hkv)};
   p.header = header;
-  p.odd = odd;
-  p.scans = scans;
   p.list = direct ? nullptr : list;
   p.offsets = a.offsets;
   p.kv_offsets = a.kv_offsets;
@@ -956,6 +916,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.N = a.N;
   p.zero_rest = a.zero_rest;
+  p.wide_out = reinterpret_cast<uintptr_t>(a.out.p) % 32 == 0 && a.out.ss % 16 == 0 && a.out.sh % 16 == 0;
   p.scale = a.sm_log2;
   p.dev_err = a.dev_err;
   const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;

@@ -488,3 +488,19 @@ def test_graphs_replayed_at_once():
         torch.cuda.synchronize()
         for (out, lse), (o, l) in zip(got, want):
             assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [2, 160])
+def test_outputs_at_half_sectors(H, D):
+    """Rows of out that begin 16 bytes into a sector give the same, and nothing beside them is written."""
+    rows = [130, 7]
+    q, k, v = inputs(150, rows, rows, H, 2, D, spare=3)
+    off = ints(ends(rows))
+    want = sage.prompt_attention(q, k, v, off)
+    for at, width in ((8, D + 16), (0, D + 8), (16, D + 24)):
+        wide = torch.full((140, H, width), 3.0, dtype=torch.bfloat16, device="cuda")
+        sage.prompt_attention(q, k, v, off, out=wide[:, :, at:at + D])
+        assert torch.equal(wide[:137, :, at:at + D], want[:137])
+        wide[:137, :, at:at + D] = 3.0
+        assert (wide == 3).all()
