@@ -44,19 +44,20 @@ namespace sage {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRows = 256;      // query rows of a unit
+constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
 constexpr uint32_t kRedoWords = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8
 
-// A block of query rows, as the first kernel lists it.
+// One or two query tiles of a key/value head, the same for each of them.
 struct alignas(16) Block {
-  int32_t q0, rows;   // first row of the tensor, rows (1 .. 256)
+  int32_t q0, rows;   // first row of tile 0 in the tensor, rows of the sequence from there on
   int32_t kv0, keys;  // first key row, keys of the sequence
-  int32_t sees;       // keys that the block's row 0 sees with the causal mask, before it is cut to 0 .. keys
-  int32_t pad[3];
+  int32_t sees;       // keys that row 0 sees with the causal mask, before it is cut to 0 .. keys
+  int32_t g0, g1;     // query heads of tile 0 and 1 among those of the key/value head; g1 < 0: no tile 1
+  int32_t down;       // rows that tile 1 begins behind tile 0: 0 or kRows
 };
 
 struct Header {
@@ -65,8 +66,18 @@ struct Header {
 };
 constexpr size_t kHeaderBytes = 256;  // then the list
 
-__host__ __device__ inline int64_t most_blocks(int64_t N, int64_t B) { return N / kRows + B; }
+// Blocks of at most `pair` tiles that N rows in B sequences can make: of every
+// sequence (rows / 128, rounded up) times the heads of a key/value head, in twos.
+inline int64_t most_blocks(int64_t N, int64_t B, int64_t group, int pair) {
+  const int64_t tiles = (N / kRows + B) * group;
+  return pair == 1 ? tiles : (tiles + B) / 2;
+}
 
+// Tile i's first row and its rows, counted from the block's first.
+__device__ __forceinline__ int32_t begin_of(const Block& b, int i) { return i == 0 ? 0 : b.down; }
+__device__ __forceinline__ int32_t rows_of(const Block& b, int i) {
+  return i == 1 && b.g1 < 0 ? 0 : min(kRows, b.rows - begin_of(b, i));
+}
 // Keys that row r of a block sees.
 template <bool kCausal>
 __device__ __forceinline__ int32_t sees(const Block& b, int32_t r) {
@@ -77,8 +88,23 @@ static_assert(kKeys == 128, "key tiles are counted by shifts");
 // Key tiles of query tile i of a block.
 template <bool kCausal>
 __device__ __forceinline__ int32_t key_tiles(const Block& b, int i) {
-  return b.rows <= 128 * i ? 0 : tiles_of(sees<kCausal>(b, min(128 * i + 127, b.rows - 1)));
+  const int32_t rows = rows_of(b, i);
+  return rows <= 0 ? 0 : tiles_of(sees<kCausal>(b, begin_of(b, i) + rows - 1));
 }
+
+// u / d for u below 2^31, by a multiplication.
+struct Divisor {
+  int32_t d;
+  uint32_t mul;
+  int shift;
+  explicit Divisor(int32_t x) : d(x), mul(0), shift(0) {
+    while ((int64_t(1) << shift) < x) ++shift;  // 2^shift >= d
+    if (x > 1) mul = static_cast<uint32_t>((uint64_t(1) << (31 + shift)) / static_cast<uint64_t>(x) + 1), --shift;
+  }
+  __device__ __forceinline__ int32_t of(int32_t u) const {
+    return d == 1 ? u : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(u), mul) >> shift);
+  }
+};
 
 // ------------------------------------------------------------------ planning --
 
@@ -88,15 +114,27 @@ __device__ __forceinline__ bool bad_offsets(const int32_t* offsets, const int32_
   return o < 0 || o > N || k < 0 || k > M || (b > 0 && (offsets[b - 1] > o || kv_offsets[b - 1] > k));
 }
 
-// The p-th row block of sequence b.
-__device__ __forceinline__ Block row_block(const int32_t* offsets, const int32_t* kv_offsets, int32_t b, int32_t p) {
+// The p-th block of sequence b: its tiles are numbered head by head of a
+// key/value head, and then row tile by row tile, so that the two of a block have
+// the same key tiles, or the second has one more.
+__device__ __forceinline__ int32_t blocks_of(const int32_t* offsets, int32_t b, int32_t group, int pair) {
+  const int32_t tiles = (offsets[b + 1] - offsets[b] + kRows - 1) / kRows * group;
+  return (tiles + pair - 1) / pair;
+}
+__device__ __forceinline__ Block block_of(const int32_t* offsets, const int32_t* kv_offsets, int32_t b, int32_t p,
+                                          const Divisor& group, int pair) {
   const int32_t q0 = offsets[b], n = offsets[b + 1] - q0, kv0 = kv_offsets[b], m = kv_offsets[b + 1] - kv0;
-  Block e = {};
-  e.q0 = q0 + p * kRows;
-  e.rows = min(kRows, n - p * kRows);
+  const int32_t tile = p * pair, at = group.of(tile), g = tile - at * group.d;
+  const bool next = g + 1 == group.d;  // tile 1 is of the next rows
+  Block e;
+  e.q0 = q0 + at * kRows;
+  e.rows = n - at * kRows;
   e.kv0 = kv0;
   e.keys = m;
-  e.sees = m - n + p * kRows + 1;
+  e.sees = m - n + at * kRows + 1;
+  e.g0 = g;
+  e.g1 = pair == 1 || (next && e.rows <= kRows) ? -1 : next ? 0 : g + 1;
+  e.down = next ? kRows : 0;
   return e;
 }
 
@@ -112,11 +150,12 @@ __device__ __forceinline__ uint32_t collect(uint32_t pair, uint32_t acc) {
 // Those are the sign bits of this.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
 
-// Lists the row blocks of all sequences by their key tiles, the most first (in 1024
+// Lists the blocks of all sequences by their key tiles, the most first (in 1024
 // classes). Offsets that decrease or leave the tensors: no block, all rows are rest.
 template <bool kCausal>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offsets, const int32_t* kv_offsets, int32_t B,
-                                                            int32_t N, int32_t M, Header* header, Block* list, int* dev_err) {
+                                                            int32_t N, int32_t M, const Divisor group, Header* header,
+                                                            Block* list, int* dev_err) {
   __shared__ int32_t count[kBins];
   __shared__ int32_t most;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
@@ -133,18 +172,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
     }
     return;
   }
-  const auto block_of = [&](int32_t b, int32_t p) { return row_block(offsets, kv_offsets, b, p); };
-  const auto blocks_of = [&](int32_t b) { return (offsets[b + 1] - offsets[b] + kRows - 1) / kRows; };
+  const auto block = [&](int32_t b, int32_t p) { return block_of(offsets, kv_offsets, b, p, group, 2); };
+  const auto blocks = [&](int32_t b) { return blocks_of(offsets, b, group.d, 2); };
   const auto cost = [&](const Block& e) { return max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1)); };
   for (int32_t b = tid; b < B; b += kPlanThreads) {
-    const int32_t n = blocks_of(b);
-    if (n > 0) atomicMax(&most, cost(block_of(b, n - 1)));
+    const int32_t n = blocks(b);
+    if (n > 0) atomicMax(&most, cost(block(b, n - 1)));
   }
   __syncthreads();
   const int64_t top = max(most, 1);
   const auto bin = [&](const Block& e) { return kBins - 1 - static_cast<int>(cost(e) * int64_t(kBins - 1) / top); };
-  for (int32_t b = warp; b < B; b += kPlanThreads / 32)
-    for (int32_t p = lane, n = blocks_of(b); p < n; p += 32) atomicAdd(&count[bin(block_of(b, p))], 1);
+  // threads of a sequence: a power of two, at least a warp
+  const int shift = B <= 1 ? 10 : max(5, __clz(B - 1) - 22);
+  const int32_t own_b = tid >> shift, own_p = tid & ((1 << shift) - 1);
+  for (int32_t b = own_b; b < B; b += kPlanThreads >> shift)
+    for (int32_t p = own_p, n = blocks(b); p < n; p += 1 << shift) atomicAdd(&count[bin(block(b, p))], 1);
   __syncthreads();
   // where each class begins: a sum over the classes before it
   const int32_t own = count[tid];
@@ -162,9 +204,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t* offse
   count[tid] = before + sum - own;
   if (tid == kPlanThreads - 1) *header = Header{before + sum, offsets[0], offsets[B]};
   __syncthreads();
-  for (int32_t b = warp; b < B; b += kPlanThreads / 32)
-    for (int32_t p = lane, n = blocks_of(b); p < n; p += 32) {
-      const Block e = block_of(b, p);
+  for (int32_t b = own_b; b < B; b += kPlanThreads >> shift)
+    for (int32_t p = own_p, n = blocks(b); p < n; p += 1 << shift) {
+      const Block e = block(b, p);
       list[atomicAdd(&count[bin(e)], 1)] = e;
     }
 }
@@ -210,24 +252,11 @@ constexpr uint32_t kCtlRegs = 72, kSoftmaxRegs = 184, kOutRegs = 72;  // 512 thr
 static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 128, "registers of one CTA");
 static_assert(kOutRegs == kCtlRegs, "every warp runs the teardown with the control budget");
 
-// u / d for u below 2^31, by a multiplication.
-struct Divisor {
-  int32_t d;
-  uint32_t mul;
-  int shift;
-  explicit Divisor(int32_t x) : d(x), mul(0), shift(0) {
-    while ((int64_t(1) << shift) < x) ++shift;  // 2^shift >= d
-    if (x > 1) mul = static_cast<uint32_t>((uint64_t(1) << (31 + shift)) / static_cast<uint64_t>(x) + 1), --shift;
-  }
-  __device__ __forceinline__ int32_t of(int32_t u) const {
-    return d == 1 ? u : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(u), mul) >> shift);
-  }
-};
-
 struct Params {
-  Divisor H, group;     // query heads, and those that share a key/value head
+  Divisor Hkv, group;   // key/value heads, and the query heads of one
   const Header* header;
   const Block* list;    // null: no list, a unit for each CTA
+  int pair;             // tiles of a block
   const int32_t *offsets, *kv_offsets;
   int32_t B, M;
   Out out;
@@ -243,14 +272,8 @@ struct Params {
 
 __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
   const int4* p = reinterpret_cast<const int4*>(list + e);
-  const int4 a = p[0];
-  Block b;
-  b.q0 = a.x;
-  b.rows = a.y;
-  b.kv0 = a.z;
-  b.keys = a.w;
-  b.sees = list[e].sees;
-  return b;
+  const int4 x = p[0], y = p[1];
+  return Block{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 }
 
 // The CTA's units one after another; the next one's block is brought to L1 a unit ahead.
@@ -261,7 +284,7 @@ struct Units {
   const Block* list;
   int32_t units, u, step, other;
   Block e;
-  int32_t h;
+  int32_t hk;            // key/value head
   uint32_t number;       // of the unit among the CTA's
   const uint32_t* redo;  // the units to take (a bit for each number modulo 32 kRedoWords), or null: all
   __device__ __forceinline__ Units(const Params& p, const Block* l, int32_t n, const uint32_t* r)
@@ -277,13 +300,14 @@ struct Units {
     return redo == nullptr || (redo[number / 32u % kRedoWords] >> (number & 31u) & 1u) != 0;
   }
   __device__ __forceinline__ bool valid() const { return u < units; }
+  __device__ __forceinline__ int32_t head(int t) const { return hk * prm.group.d + (t == 0 ? e.g0 : e.g1); }
   __device__ __forceinline__ void load() {
     if (u >= units) return;
-    const int32_t b = prm.H.of(u);
+    const int32_t b = prm.Hkv.of(u);
     e = load_block(list, b);
-    h = u - b * prm.H.d;
+    hk = u - b * prm.Hkv.d;
     const int32_t next = u + step;
-    if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + prm.H.of(next)));
+    if (next < units) asm volatile("prefetch.global.L1 [%0];" ::"l"(list + prm.Hkv.of(next)));
   }
   __device__ __forceinline__ void advance() {
     do {
@@ -452,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) *own_header = bad ? Header{0, 0, 0} : Header{0, prm.offsets[0], prm.offsets[B]};
       __syncwarp();
       int32_t before = 0;
-      const int32_t mine = prm.H.of(static_cast<int32_t>(blockIdx.x));
+      const int32_t mine = prm.Hkv.of(static_cast<int32_t>(blockIdx.x));
       for (int32_t b0 = 0; !bad && b0 < B && before <= mine; b0 += 32) {
-        const int32_t b = b0 + lane, n = b < B ? (prm.offsets[b + 1] - prm.offsets[b] + kRows - 1) / kRows : 0;
+        const int32_t b = b0 + lane, n = b < B ? blocks_of(prm.offsets, b, prm.group.d, prm.pair) : 0;
         int32_t sum = n;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
@@ -463,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int32_t p = mine - (before + sum - n);
         if (p >= 0 && p < n) {
-          *own_block = row_block(prm.offsets, prm.kv_offsets, b, p);
+          *own_block = block_of(prm.offsets, prm.kv_offsets, b, p, prm.group, prm.pair);
           own_header->blocks = 1;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
@@ -471,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  const Block* list = direct ? own_block - prm.H.of(static_cast<int32_t>(blockIdx.x)) : prm.list;
+  const Block* list = direct ? own_block - prm.Hkv.of(static_cast<int32_t>(blockIdx.x)) : prm.list;
   const Header* header = direct ? own_header : prm.header;
-  const int32_t units = direct ? (header->blocks != 0 ? static_cast<int32_t>(blockIdx.x) + 1 : 0) : header->blocks * prm.H.d;
+  const int32_t units = direct ? (header->blocks != 0 ? static_cast<int32_t>(blockIdx.x) + 1 : 0) : header->blocks * prm.Hkv.d;
 
   // After the units: whether some have to be done again. All warps meet here once.
   const auto again = [&]() {
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pass > 0 && !again()) break;
         for (Units it(prm, list, lane == 0 ? units : 0, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
           const Block& e = it.e;
-          const int32_t h = it.h, hk = prm.group.of(h);
+          const int32_t hk = it.hk;
           const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
           const auto queries = [&](int t) {
             if (!(ok = wait_bar(w, w.bar(L::kQEmpty + t), (q_cnt[t] & 1u) ^ 1u))) return;
@@ -500,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive_expect_tx(w.bar(L::kQFull + t), L::kTile);
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
-              tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, h, e.q0 + 128 * t,
+              tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, it.head(t), e.q0 + begin_of(e, t),
                               w.bar(L::kQFull + t));
           };
           // in the second pass value tiles with hidden keys pass through warp 3
@@ -527,11 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               // the next unit's queries on their way to L2
               const int32_t next = it.u + it.step;
               if (next < units) {
-                const int32_t b = prm.H.of(next);
+                const int32_t b = prm.Hkv.of(next);
                 const Block f = load_block(list, b);
-                for (int t = 0; t < 2 && f.rows > 128 * t; ++t)
+                const int32_t h = (next - b * prm.Hkv.d) * prm.group.d;
+                for (int t = 0; t < 2 && rows_of(f, t) > 0; ++t)
 #pragma unroll
-                  for (int x = 0; x < D / 64; ++x) tc::tma_prefetch_3d(&tm_q, 64 * x, next - b * prm.H.d, f.q0 + 128 * t);
+                  for (int x = 0; x < D / 64; ++x)
+                    tc::tma_prefetch_3d(&tm_q, 64 * x, h + (t == 0 ? f.g0 : f.g1), f.q0 + begin_of(f, t));
               }
             }
           }
@@ -555,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The two query tiles' products take turns: issued side by side, they share the
       // tensor pipe and end together, and then both softmaxes run at once and the pipe
       // stands still. Tile 1's product with value tile j (and S of the next key tile)
-      // comes after tile 0's with j, and that with j + 1 after it. A tile says that a
-      // turn is over only where the other asks for it (tile 1 has as many key tiles as
-      // tile 0, or one more, or none at all), so no phase of the barriers is skipped.
+      // comes after tile 0's with j, and tile 0's next one, of this unit or the next with
+      // two tiles, after it. (Tile 1 has as many key tiles as tile 0, or one more, or
+      // none at all.) So each of the two barriers is never more than a phase ahead of
+      // who waits for it.
       const int t = warp - 1;
       const bool leader = tc::elect_one();
       const uint32_t d_s = tmem + col_s(t), d_p = tmem + col_p<D>(t), d_o = tmem + col_o<D>(t);
@@ -619,9 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dv = tc::desc_at(dv0, (pv % L::kStages) * L::kTile);
             if (!(ok = wait_bar_warp(w, w.bar(L::kPFull + t), p_cnt & 1u))) break;
             ++p_cnt;
-            if (theirs > 0 && (t == 0 ? j > 0 : j < theirs)) {
-              if (!(ok = wait_bar_warp(w, w.bar(L::kTurn + 1 - t), turns & 1u))) break;
-              ++turns;
+            const bool turn = j < theirs;
+            if (turn) {
+              const uint32_t before = turns++ + static_cast<uint32_t>(t);  // the other's turns that this one comes after
+              if (before > 0 && !(ok = wait_bar_warp(w, w.bar(L::kTurn + 1 - t), (before - 1) & 1u))) break;
             }
             tc::tc_fence_after();
             if (leader) {
@@ -633,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!kApart<D> && more) product_s(pk + 2u, j + 2 == own);
               tc::mma_commit(empty(pv));
               if (kApart<D>) tc::mma_commit(w.bar(L::kPFree + t));
-              if (t == 0 ? theirs > 0 : j + 1 < theirs) {
+              if (turn) {
                 if (kApart<D>) tc::mbar_arrive(w.bar(L::kTurn + t));  // issued
                 else tc::mma_commit(w.bar(L::kTurn + t));             // done
               }
@@ -734,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (Units it(prm, list, units, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
-      const int32_t mine = sees<kCausal>(e, 128 * t + row);
+      const int32_t mine = sees<kCausal>(e, begin_of(e, t) + row);
       float m = -INFINITY, neg = 0.0f, l = 0.0f;
       for (int32_t j = 0; j < own; ++j) {
         if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
@@ -742,13 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == 0, s_cnt, m, neg, l))) break;
         ++s_cnt;
       }
-      if (ok && own > 0) {
-        // the unit before has been stored
+      if (ok && n > 0) {
+        // the unit before has been stored (waited for in every unit: no phase is skipped)
         if (!(ok = wait_bar_warp(w, w.bar(L::kOEmpty + t), (done & 1u) ^ 1u))) break;
-        *stat = make_float2(l, neg);
-        tc::mbar_arrive(w.bar(L::kStat + t));
+        ++done;
+        if (own > 0) {
+          *stat = make_float2(l, neg);
+          tc::mbar_arrive(w.bar(L::kStat + t));
+        }
       }
-      if (n > 0) ++done;
     }
     if (pass++ == 0 && again()) goto units_of_rows;
     tc::regs_dec<kCtlRegs>();
@@ -763,9 +793,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t lo = header->rest_lo, hi = header->rest_hi;
       // a row's head at a time for D / 8 threads
       const int at = static_cast<int>(threadIdx.x) - 384, c = at % (D / 8);
-      const int64_t rest = lo + (prm.N - hi), items = rest * prm.H.d, step = static_cast<int64_t>(gridDim.x) * (128 / (D / 8));
+      const int64_t rest = lo + (prm.N - hi), heads = prm.Hkv.d * prm.group.d, items = rest * heads, step = static_cast<int64_t>(gridDim.x) * (128 / (D / 8));
       for (int64_t x = static_cast<int64_t>(blockIdx.x) * (128 / (D / 8)) + at / (D / 8); x < items; x += step) {
-        const int64_t i = x / prm.H.d, h = x - i * prm.H.d, r = i < lo ? i : hi + (i - lo);
+        const int64_t i = x / heads, h = x - i * heads, r = i < lo ? i : hi + (i - lo);
         *reinterpret_cast<uint4*>(prm.out.p + r * prm.out.ss + h * prm.out.sh + 8 * c) = make_uint4(0, 0, 0, 0);
         if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
       }
@@ -788,21 +818,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t met = 0;  // infinities and NaN among the outputs
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        const int32_t own = t == 0 ? n0 : n1, r = 128 * t + row;
+        const int32_t own = t == 0 ? n0 : n1, r = begin_of(e, t) + row, h = it.head(t);
         float2 st = make_float2(0.0f, 0.0f);
         if (own > 0) {
           uint32_t& c = stats[t];
           if (!(ok = wait_bar_warp(w, w.bar(L::kStat + t), c & 1u))) break;
           ++c;
-          st = reinterpret_cast<const float2*>(smem + L::kOffStat)[r];
+          st = reinterpret_cast<const float2*>(smem + L::kOffStat)[128 * t + row];
         }
         if (n > 0 && !(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
         tc::tc_fence_after();
+        if (rows_of(e, t) <= 0) {
+          if (n > 0) tc::mbar_arrive(w.bar(L::kOEmpty + t));
+          continue;
+        }
         const float inv = st.x == 0.0f ? 0.0f : 1.0f / st.x;
-        if (prm.lse != nullptr && r < e.rows)
-          prm.lse[static_cast<int64_t>(it.h) * prm.N + e.q0 + r] = st.x == 0.0f ? -INFINITY : (log2f(st.x) - st.y) * kLn2;
-        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + it.h * prm.out.sh;
-        const bool there = r < e.rows;
+        const bool there = row < rows_of(e, t);
+        if (prm.lse != nullptr && there)
+          prm.lse[static_cast<int64_t>(h) * prm.N + e.q0 + r] = st.x == 0.0f ? -INFINITY : (log2f(st.x) - st.y) * kLn2;
+        uint16_t* dst = prm.out.p + (static_cast<int64_t>(e.q0) + r) * prm.out.ss + h * prm.out.sh;
         // 16 channels at a time, a whole sector for each lane's store: little code
 #pragma unroll 1
         for (int x = 0; x < D / 16; ++x) {
@@ -837,10 +871,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (kCausal && bad) {
-          const int32_t mine = r < e.rows ? sees<kCausal>(e, r) : 0;
+          const int32_t mine = there ? sees<kCausal>(e, r) : 0;
 #pragma unroll 1
           for (int32_t k = masked * kKeys; k < mine; ++k) {
-            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + prm.group.of(it.h) * prm.v_sh;
+            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + it.hk * prm.v_sh;
 #pragma unroll 1
             for (int y = 0; y < D; ++y) {
               const uint32_t b = v[y];
@@ -892,7 +926,9 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   Header* header = static_cast<Header*>(a.workspace);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
-  const int64_t units = most_blocks(a.N, a.B) * a.H, sms = sm_count_current();
+  const int64_t group = a.H / a.Hkv, sms = sm_count_current();
+  const int pair = most_blocks(a.N, a.B, group, 1) * a.Hkv <= sms ? 1 : 2;
+  const int64_t units = most_blocks(a.N, a.B, group, pair) * a.Hkv;
   // A unit for each CTA at most: no first kernel, which costs more than its list and
   // its look at the values save then. 100 tokens, 28 heads (28 units): 8.8 us instead
   // of 11.3; 1230 tokens (140 units): 24.4 us instead of 28.1.
@@ -900,9 +936,10 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (!direct && (e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPlanThreads, 0, stream,
                                        a.offsets, a.kv_offsets, a.B, static_cast<int32_t>(a.N),
-                                       static_cast<int32_t>(a.M), header, list, a.dev_err)) != cudaSuccess)
+                                       static_cast<int32_t>(a.M), Divisor(static_cast<int32_t>(group)), header, list, a.dev_err)) != cudaSuccess)
     return e;
-  Params p{Divisor(a.H), Divisor(a.H / a.Hkv)};
+  Params p{Divisor(a.Hkv), Divisor(static_cast<int32_t>(group))};
+  p.pair = pair;
   p.header = header;
   p.list = direct ? nullptr : list;
   p.offsets = a.offsets;
@@ -929,8 +966,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t prompt_attention_workspace_bytes(int64_t N, int64_t, int64_t, int64_t, int64_t, int64_t B) {
-  return (kHeaderBytes + static_cast<size_t>(most_blocks(N, B)) * sizeof(Block) + 255) / 256 * 256;
+size_t prompt_attention_workspace_bytes(int64_t N, int64_t, int64_t H, int64_t Hkv, int64_t, int64_t B) {
+  return (kHeaderBytes + static_cast<size_t>(most_blocks(N, B, H / Hkv, 2)) * sizeof(Block) + 255) / 256 * 256;
 }
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int64_t D, cudaStream_t stream) {

@@ -443,7 +443,7 @@ def test_many_units_leave_rest_rows(D):
 
 
 def test_units_around_the_number_of_sms():
-    """Calls with a unit fewer than SMs, as many, and one more (units: (N // 256 + B) H)."""
+    """Calls with a unit fewer than SMs, as many, and one more (two tiles of 128 rows for each head)."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     q, k, v = inputs(144, [200], [200], sms + 1, 1, 64)
     off = ints([0, 200])
@@ -504,3 +504,22 @@ def test_outputs_at_half_sectors(H, D):
         assert torch.equal(wide[:137, :, at:at + D], want[:137])
         wide[:137, :, at:at + D] = 3.0
         assert (wide == 3).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,Hkv", [(3, 1), (7, 1), (10, 2), (9, 3)])
+def test_odd_heads_of_a_key_head(H, Hkv, causal, D):
+    """Pairs of query tiles that cross from one row tile to the next, and tiles without a partner, in calls with few
+    units and with many (whose heads come several times)."""
+    rows, past = [1, 127, 128, 129, 300, 513, 40], [0, 3, 0, 260, 0, 0, 400]
+    keys = [n + p for n, p in zip(rows, past)]
+    q, k, v = inputs(160, rows, keys, H, Hkv, D)
+    off, kv = ints(ends(rows)), ints(ends(keys))
+    out, lse = sage.prompt_attention(q, k, v, off, kv_offsets=kv, return_lse=True, is_causal=causal)
+    close(out, lse, formula(q, k, v, rows, keys, causal, 1 / math.sqrt(D)))
+    many_k, many_v = (x.repeat(1, 31, 1) for x in (k, v))
+    many, many_lse = sage.prompt_attention(q.repeat(1, 31, 1), many_k, many_v, off, kv_offsets=kv, return_lse=True, is_causal=causal)
+    assert torch.equal(many, out.repeat(1, 31, 1)) and torch.equal(many_lse, lse.repeat(31, 1))
+    one, one_lse = sage.prompt_attention(q[128:256], k[130:258], v[130:258], ints([0, 128]), return_lse=True, is_causal=causal)
+    close(one, one_lse, formula(q[128:256], k[130:258], v[130:258], [128], [128], causal, 1 / math.sqrt(D)))
