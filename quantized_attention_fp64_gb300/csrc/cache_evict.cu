@@ -13,7 +13,9 @@
 // reads only blocks that hold a kept token: keys row by row, values (channels by
 // tokens) a whole block at a time, a lane with all 32 bytes of a channel. What
 // bounds it is HBM, and the instructions that pick single bytes out of the values
-// and round the codes again.
+// and round the codes again. 16 sequences of 8 heads, D = 128, cut from up to 16001 to
+// 4096 tokens: selection 21 us (one CTA a head: a chain of three digits), moves 81 us,
+// of which 358 MB from and to HBM need 53 (4.4 TB/s); in place 86.
 // In place, kept tokens never move to a later place: block m is written by the
 // warp that has places 32 m .. 32 m + 31, and its old tokens are read by the
 // warps whose places they go to, which are m or before. So a warp reads first,
@@ -451,13 +453,17 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a, int64_t D, cudaStream_t 
   const Work work = work_of(a);
   const bool in_place = a.from.table == a.to.table && a.from.stride == a.to.stride;
   const dim3 grid(static_cast<unsigned>(a.c.H > 0 ? a.c.H : 1), static_cast<unsigned>(a.B));
-  // a sequence of some thousand tokens is too little for 1024 threads
-  const bool few = a.scores_n <= 8192, stage = a.scores_n <= kStaged;
-  const auto select = few ? select_kernel<256, true> : (stage ? select_kernel<1024, true> : select_kernel<1024, false>);
+  // A sequence of some thousand tokens is too little for 1024 threads (16 sequences of
+  // 8 heads, selection and moves: up to 1000 tokens 21.1 us with 512 threads, 25.0 with
+  // 1024; 2 of 4 heads up to 4000: 16.7 and 17.4; 16 of 8 up to 8000: 66 with 1024,
+  // 72 with 256). Scores that fit are read once and stay in shared memory (a
+  // sequence of 40000 tokens, 4 heads: 41.8 us, 51.3 read from L2 for each digit).
+  const bool few = a.scores_n <= 4096, stage = a.scores_n <= kStaged;
+  const auto select = few ? select_kernel<512, true> : (stage ? select_kernel<1024, true> : select_kernel<1024, false>);
   const int bytes = stage ? static_cast<int>(a.scores_n) * 4 : 0;
   cudaError_t e;
   if (bytes > 32768 && (e = set_smem_limit_once(reinterpret_cast<const void*>(select), kStaged * 4)) != cudaSuccess) return e;
-  if ((e = launch_dependent(select, grid, few ? 256 : 1024, static_cast<size_t>(bytes), stream, a, work, in_place)) != cudaSuccess)
+  if ((e = launch_dependent(select, grid, few ? 512 : 1024, static_cast<size_t>(bytes), stream, a, work, in_place)) != cudaSuccess)
     return e;
   const int64_t units = a.B * a.c.H * 2 * work.new_blocks;
   if (units == 0) return cudaSuccess;

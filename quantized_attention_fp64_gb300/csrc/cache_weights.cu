@@ -12,7 +12,9 @@
 // long as the queries are; queries are BF16 already and codes (8 bits with their
 // sign) are exact in it. The products' rows are keys, so a key's sum over the
 // query rows is one in a lane and two exchanges between four lanes, always in the
-// same order.
+// same order. 64 sequences of up to 8192 tokens, 8 key/value heads, D = 128, 4 rows
+// each: 51 us, 6.2 TB/s (93% of a copy's rate); 16 rows 64 us, 32 rows 82 us, bound by the
+// exponentials' and products' instructions.
 #include "cache.cuh"
 #include "launch.cuh"
 #include "tc_kernel.cuh"
@@ -250,6 +252,9 @@ cudaError_t launch_cache_weights(const CacheWeightsArgs& a, int64_t D, cudaStrea
   const int64_t tokens = a.scores_n < most ? a.scores_n : most;
   if (tokens == 0) return cudaSuccess;
   const int64_t rows = a.T * (a.H / a.c.H);
+  // Up to 32 rows here, more in cache_weights_tc.cu, which has the products of 128 rows
+  // whatever there are: one sequence of 16001 tokens, 8 heads, 32 rows: 12.3 us here,
+  // 21 there; 64 sequences up to 8192: 82 us here, 273 there.
   if (rows > 32) return launch_cache_weights_tc(a, D, stream);
   const int64_t blocks = div_up(tokens, kCacheBlock) * a.c.H * a.B;
   const int64_t ctas = div_up(blocks, kThreads / 32), fit = int64_t(sm_count_current()) * (rows > 16 ? 1 : 2);

@@ -8,16 +8,20 @@
 // BF16 once (exactly: 8 bits with their sign), and all query rows that see them
 // pass by in tiles that TMA brings (tokens x the heads of the group), each
 // multiplied with both key tiles. Tiles of 128 keys of all sequences and heads
-// form one list that is cut into equal ranges, one per CTA. Roles of the 16 warps:
+// form one list that is cut into equal ranges, one per CTA. Roles of the 24 warps:
 //   warp 0      TMA: query tiles
-//   warp 1      TMEM allocation; issues the products
+//   warps 1, 3  TMEM allocation; the products for two groups of sum warps each
 //   warp 2      log-sum-exps of the query tiles
-//   warps 4-7, 8-11  exponentials and sums of key tile 0, 1 (TMEM lane = key)
-//   warps 12-15 keys: codes to BF16, in the 128-byte-swizzled layout, one pair of
+//   warps 4-7   keys: codes to BF16, in the 128-byte-swizzled layout, one pair of
 //               tiles ahead
-// TMEM holds two S^T of 128 x 128 for each key tile: all 512 columns. The product
-// of a tile (512 cycles at D = 128) and its 16384 exponentials (512 cycles) bound
-// the kernel alike.
+//   warps 8-23  four groups: exponentials and sums of every other query tile of key
+//               tile 0 or 1 (TMEM lane = key); or, where there is one key tile, of
+//               every fourth
+// TMEM holds an S^T of 128 x 128 for each group: all 512 columns. The product of a
+// tile (512 cycles at D = 128) and its 16384 exponentials (512 cycles) bound the
+// kernel alike. A causal chunk of 2000 tokens over 16001, 32 heads on 8, D = 128: 215 us, 1140
+// TFLOP/s (276 with two groups, whose latencies lay open; 325 before the
+// log-sum-exps came in a ring of their own).
 //
 // Every wait on an mbarrier is bounded, as in prompt_attention.cu.
 #include <cuda.h>

@@ -5,15 +5,20 @@
 // the first m - n + t + 1 (n queries). Both products are BF16 with fp32 sums; P
 // is rounded to BF16, l_t = sum_j p_tj is taken in fp32 before that.
 //
-// A unit of work is one head of 256 consecutive query rows of a sequence: two
-// tiles of 128 rows that share the key tiles (128 keys) that pass through shared
-// memory. A first kernel lists the row blocks of all sequences, those with the
-// most key tiles first; the CTAs, one for each SM, take the units in that order
-// forth and back (0 1 .. 151, 151 .. 1 0, ...), so that each gets about the same
-// work whatever the lengths are. Roles of the 16 warps:
+// A unit of work is two query tiles of 128 rows that share the key tiles (128 keys)
+// which pass through shared memory: the same rows of two query heads of a key/value
+// head, or where the heads are odd, the last head's rows and the first one's next. So
+// both have the same key tiles, or the second one more. (Two row tiles of one
+// head, as it was, leave the first without work for the second's last key tile: 16
+// prompts up to 2000 tokens, 32 heads on 8, took 200 us, and now 192.) Where there are
+// fewer than SMs a unit is one tile.
+// A first kernel lists the units' blocks of all sequences, those with the most key
+// tiles first; the CTAs, one for each SM, take the units in that order forth and
+// back (0 1 .. 151, 151 .. 1 0, ...), so that each gets about the same work whatever
+// the lengths are. Calls of at most a unit for each SM do without. Roles of the 16 warps:
 //   warp 0      TMA: the unit's queries, and a ring of key and value tiles in turn
 //   warps 1, 2  TMEM allocation; the products of query tile 0, 1 (one thread issues)
-//   warp 3      makes value tiles ready that hold keys which some row does not see
+//   warp 3      in the second pass (below): clears value tiles
 //   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
 //   warps 12-15 output: O of either tile, scaled and stored
 // TMEM holds S0, S1, O0, O1: all 512 columns at D = 128. The softmax reads S of a
@@ -25,11 +30,26 @@
 // P and l stay within 2^8 of their usual range (no bit is lost in floating point).
 //
 // What a row does not see must not touch it, whatever stands there: its P is 0,
-// but 0 times an infinity or a NaN of V would be a NaN. In the tiles that hold
-// keys which some row of the unit does not see (the diagonal, the sequence's end)
-// warp 3 clears the rows behind the sequence's end and every infinity and NaN,
-// and tells the softmax warps, which then add those values to the rows that do
-// see them (a row's P of a key it sees is positive).
+// but 0 times an infinity or a NaN of V is a NaN. The output warps look for
+// infinities and NaN in what they store, and a unit that has one is done again in a
+// second pass. There warp 3 clears, in the tiles that hold keys which some row of the
+// unit does not see (the diagonal, the sequence's end), the rows behind the
+// sequence's end and every infinity and NaN, before the product takes them, and the
+// output warps add those values to the rows that do see them (a row's P of a key it
+// sees is positive). Calls with finite values pay for the look at the outputs
+// alone (2% of the prompts above); a look at all values beforehand took 23 us of
+// them, one at the value tiles as they pass by 32.
+//
+// What bounds it. D = 128: the tensor pipe; 16384 causal tokens, 28 heads on 4, run at 1590
+// to 1690 TFLOP/s (1200 to 1140 us, 81 to 86% of the measured peak of cuBLAS in a
+// burst, which no kernel keeps up under the power limit: 1752 TFLOP/s for seconds).
+// Prompts up to 2000 tokens, 1040 TFLOP/s: the masked halves of the diagonal tiles, ends of
+// sequences, and a microsecond to begin and end a unit of 6 key tiles. D = 64: the
+// softmax, whose exponentials are as many with half the products; 16384 tokens both
+// ways 1000 TFLOP/s, 1.28 us for a step of two tiles (with P double-buffered in TMEM
+// 1.33). Code that runs once in a unit is kept short: it is fetched anew each
+// time (the output warps' loop over 32 channels, three times as long, cost the
+// prompts above 20 us).
 //
 // Every wait on an mbarrier is bounded; when one runs out the kernel sets the
 // device error word, tells the other roles to stop, lets its copies and products

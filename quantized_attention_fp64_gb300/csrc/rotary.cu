@@ -11,7 +11,9 @@
 // The kernel moves bytes. A thread has 16 channels of a token, 8 pairs, in heads
 // hl, hl + lanes, ...: one set of sines and cosines for all of them, and four
 // heads' loads (two of 16 bytes each) in flight. A warp reads whole sectors, and
-// whole lines where the head is 128 channels wide.
+// whole lines where the head is 128 channels wide. HBM bounds it: 16001 tokens of
+// 40 heads, D = 128, take 50 us, 6.5 TB/s (98% of a copy's rate); a step's 64 tokens 2.8 us,
+// the latency of a launch, a load of the position, the sines and a store.
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
@@ -116,8 +118,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, ui
 cudaError_t launch_rotary(const RotaryArgs& a, int64_t D, cudaStream_t stream) {
   const uint32_t tokens = static_cast<uint32_t>(a.B * a.T);
   const int slots = kThreads / static_cast<int>(D / 16);
-  // one set of sines for many heads where there are tokens enough, else all
-  // heads at once
+  // One set of sines for many heads where there are tokens enough (16001 tokens, 40
+  // heads: 50 us, 55 with lanes for all heads), else all heads at once (64 tokens: 2.8
+  // us, 4.7 with four lanes; 500 tokens: 4.2 and 4.8).
   int lanes = 4;
   while (lanes < slots && lanes * kAtOnce < a.H + a.Hkv && div_up(tokens, slots / lanes) < 2 * sm_count_current())
     lanes *= 2;
