@@ -684,7 +684,8 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * tensors. With offsets that break this no row belongs to a sequence, and the
  * device error word is set.
  * q, k, v, out: BF16, stride_b is not used, the other strides of q, k and v must
- * be positive (LAYOUT); D = 128 or 64; out must not overlap the inputs. sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
+ * be positive (LAYOUT); D = 128 or 64; out must not overlap the inputs (ARG where
+ * it is one of them). sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16
  * (by 2^-9 of themselves) for the product with v, their sum is taken in fp32
  * before that.

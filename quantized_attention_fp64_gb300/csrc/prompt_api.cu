@@ -109,6 +109,8 @@ int sage_prompt_attention(const sage_prompt_attention_args* args) {
       (rc = check_ints(args->kv_offsets_dev, false)) != SAGE_OK || (rc = check_floats(args->lse_dev, false)) != SAGE_OK)
     return rc;
   if (!scale_ok(args->sm_scale)) return SAGE_ERR_ARG;
+  const void* out = args->out.ptr_dev;  // (a unit may be done twice: its queries have to be there still)
+  if (N > 0 && H > 0 && (out == args->q.ptr_dev || (M > 0 && (out == args->k.ptr_dev || out == args->v.ptr_dev)))) return SAGE_ERR_ARG;
   const size_t need = N == 0 || H == 0 ? 0 : prompt_attention_workspace_bytes(N, M, H, args->Hkv, D, B);
   if (need > 0) {
     if (args->workspace_dev == nullptr) return SAGE_ERR_NULLPTR;

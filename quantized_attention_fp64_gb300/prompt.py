@@ -63,6 +63,8 @@ def prompt_attention(q, k, v, offsets, kv_offsets=None, is_causal: bool = True, 
     fp32 [H, N], the natural-log log-sum-exp of each row's scaled logits. A row that sees no key gets 0 and -inf; rows
     behind the last sequence are the same, or left as they were in a given out (their lse is -inf all the same).
 
+    out: a tensor to write to, which must not overlap q, k or v.
+
     With offsets that decrease or leave the tensors no row belongs to a sequence, and ``device_error()`` then returns
     SAGE_ERR_DEVICE_OFFSETS (-17). workspace: a uint8 tensor of prompt_attention_workspace_size bytes that no other
     call uses at the same time; None: the library's own, one for each thread and stream (a captured graph gets its own

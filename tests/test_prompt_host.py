@@ -165,7 +165,7 @@ def test_rotary_refuses(lib):
 def _prompt(lib, q=None, k=None, v=None, out=None, N=100, M=100, H=4, Hkv=2, D=128, B=3, off=0x1000, kv=None, sm=0.1, lse=None,
             ws=0x90000, wsn=1 << 40):
     t = tensor()
-    return lib.sage_prompt_attention(_lib.PromptAttentionArgs(q or t, k or t, v or t, out or t, N, M, H, Hkv, D, B, off, kv,
+    return lib.sage_prompt_attention(_lib.PromptAttentionArgs(q or t, k or t, v or t, out or tensor(0x80000), N, M, H, Hkv, D, B, off, kv,
                                                               sm, 1, 1, lse, ws, wsn, None))
 
 
@@ -192,6 +192,7 @@ def test_prompt_attention_refuses(lib):
     for which in ("q", "k", "v"):  # expanded rows or heads, and backward ones
         for st in (dict(ss=0), dict(sh=0), dict(ss=-512), dict(sh=-128), dict(ss=1 << 39)):
             assert _prompt(lib, **{which: tensor(**st)}) == LAYOUT
+    assert _prompt(lib, out=tensor()) == ARG and _prompt(lib, q=tensor(0x80000)) == ARG and _prompt(lib, v=tensor(0x80000)) == ARG
     assert _prompt(lib, off=None) == NULLPTR and _prompt(lib, off=0x1002) == ALIGN and _prompt(lib, kv=0x1001) == ALIGN
     assert _prompt(lib, lse=0x1002) == ALIGN
     for sm in (0.0, -1.0, math.inf):
