@@ -586,7 +586,7 @@ SAGE_API int sage_cache_add_weights(const sage_cache_add_weights_args* args);
  *   kept[b][h][i]    = where token i came from, i < lengths_out[b]; -1 behind,
  *                      up to kept_size entries: int32 [B][H][kept_size],
  *                      kept_size >= min(keep, scores_size)
- *   scores_out[b][h][i] = its score; 0 behind, up to scores_size: fp32
+ *   scores_out[b][h][i] = its score (-0 as 0); 0 behind, up to scores_size: fp32
  *                      [B][H][scores_size]
  * A new block's scale is the largest of its tokens' old ones, and codes c become
  * rint(c * (s / scale)), fp32, correctly rounded, as when a block grows
@@ -596,7 +596,8 @@ SAGE_API int sage_cache_add_weights(const sage_cache_add_weights_args* args);
  * error word is set. A token on a page outside the cache is taken as 0 with
  * scale 0; what would go to a page outside the cache is lost.
  * out_table: int32 rows of out_max_pages entries; it may be the table itself
- * (the sequence is cut back in place), else its pages must not be among the
+ * (the sequence is cut back in place: one of at most keep tokens stays as it is, but
+ * for the slots behind its last token), else its pages must not be among the
  * ones read, nor be named twice. Pages behind a new length are not written.
  * Pages read may be shared by sequences unless they are written.
  * lengths_out, kept and scores_out must not overlap lengths and scores.
