@@ -600,11 +600,12 @@ SAGE_API int sage_cache_add_weights(const sage_cache_add_weights_args* args);
  * for the slots behind its last token), else its pages must not be among the
  * ones read, nor be named twice. Pages behind a new length are not written.
  * Pages read may be shared by sequences unless they are written.
- * lengths_out, kept and scores_out must not overlap lengths and scores.
+ * lengths_out, kept and scores_out must not overlap lengths and scores (ARG where
+ * one is the other).
  * workspace_dev: sage_cache_evict_workspace_size bytes, 256-byte aligned,
  * contents do not matter; not used by another call at the same time.
  * Errors: NULLPTR, SHAPE (also keep < 0, recent < 0, recent > keep, kept_size),
- * HEAD_DIM, ALIGN, WORKSPACE, TOO_LARGE, ARCH, CUDA; on the device DEVICE_PAGE. */
+ * HEAD_DIM, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH, CUDA; on the device DEVICE_PAGE. */
 typedef struct sage_cache_evict_args {
   const sage_cache* cache;
   const int32_t* table_dev;

@@ -628,3 +628,27 @@ def test_evict_again_with_other_tensors():
                 for x, y in zip(got, want):
                     assert np.array_equal(x.cpu().numpy(), y)
                 same_cache(gpu, c)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_scores_and_queries_past_32_bits(T):
+    rng = np.random.default_rng(231)
+    B, H, Hkv, D, page, n = 3, 4, 2, 64, 64, 150
+    table, P = make_table(rng, [n] * B, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    gpu, tab, lens = upload(c), ints(table), ints([n, 100, 77])
+    q, lse = bf16(rng, B, T, H, D), torch.full((B, H, T), 3.0, device="cuda")
+    apart = 1 << 30                                             # of sequences
+    room = torch.empty(2 * apart + (1 << 16), dtype=torch.float32, device="cuda")
+    scores = room.as_strided((B, Hkv, n), (apart, 1 << 12, 1))
+    scores.zero_()
+    wide = room.view(torch.bfloat16)[1 << 15:].as_strided((B, T, H, D), (apart, H * D, D, 1))
+    wide.copy_(q)
+    dense = torch.zeros((B, Hkv, n), device="cuda")
+    sage.cache_add_weights(dense, q, gpu, tab, lens, lse)
+    sage.cache_add_weights(scores, wide, gpu, tab, lens, lse)
+    assert torch.equal(scores, dense) and (dense > 0).any()
+    got = sage.cache_evict(gpu, tab, lens, scores, 60, recent=9)
+    for x, y in zip(got, evict(c, table, [n, 100, 77], dense.cpu().numpy(), 60, 9, table)):
+        assert np.array_equal(x.cpu().numpy(), y)
+    same_cache(gpu, c)

@@ -523,3 +523,29 @@ def test_odd_heads_of_a_key_head(H, Hkv, causal, D):
     assert torch.equal(many, out.repeat(1, 31, 1)) and torch.equal(many_lse, lse.repeat(31, 1))
     one, one_lse = sage.prompt_attention(q[128:256], k[130:258], v[130:258], ints([0, 128]), return_lse=True, is_causal=causal)
     close(one, one_lse, formula(q[128:256], k[130:258], v[130:258], [128], [128], causal, 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("H", [2, 160])
+def test_offsets_past_32_bits(H):
+    """Rows millions of elements apart: the tensors' last ones lie behind element 2^31."""
+    n, D, apart = 300, 128, 1 << 23
+    room = torch.empty(n * apart, dtype=torch.bfloat16, device="cuda")
+    assert room.numel() > 2 ** 31
+    q, k, v = inputs(170, [n], [n], H, 2, D)
+    wide = []
+    at = 0
+    for x in (q, k, v, q):
+        wide.append(room[at:].as_strided((n, x.shape[1], D), (apart, D, 1)))
+        at += x.shape[1] * D
+    for w, x in zip(wide, (q, k, v)):
+        w.copy_(x)
+    off = ints([0, 40, n])
+    want, lse = sage.prompt_attention(q, k, v, off, return_lse=True)
+    out, again = sage.prompt_attention(*wide[:3], off, out=wide[3], return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, again)
+    # turned in place, and from there to a dense tensor
+    table = sage.rotary_table(D, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    tq, tk = sage.rotary(q, k, pos, table)
+    sage.rotary(wide[0], wide[1], pos, table, out=(wide[0], wide[1]))
+    assert torch.equal(wide[0], tq) and torch.equal(wide[1], tk)

@@ -267,6 +267,7 @@ def test_eviction_refuses(lib):
     assert _evict(lib, kept_size=99) == SHAPE and _evict(lib, n=(1 << 30) + 1) == TOO_LARGE
     for name in ("lens", "kept", "moved"):
         assert _evict(lib, **{name: None}) == NULLPTR and _evict(lib, **{name: 0xb0002}) == ALIGN
+    assert _evict(lib, lens=0x60000) == ARG and _evict(lib, moved=0xa0000) == ARG
     assert _evict(lib, ws=None) == NULLPTR and _evict(lib, ws=0x90010) == ALIGN
     assert _evict(lib, wsn=need - 1) == WORKSPACE
 
