@@ -552,7 +552,7 @@ cudaError_t launch(const CacheWeightsArgs& a, cudaStream_t stream) {
   p.splits = static_cast<int32_t>(div_up(p.group, p.heads));
   CUtensorMap tq;
   const uint64_t dims[4] = {D, static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.T), static_cast<uint64_t>(a.B)};
-  // (strides of one head, token or sequence are not used; the driver wants valid ones)
+  // (strides of one head, token or sequence are not used; the tensor map wants valid ones)
   const uint64_t strides[3] = {static_cast<uint64_t>(a.H > 1 ? a.q.sh : D) * 2, static_cast<uint64_t>(a.T > 1 ? a.q.ss : D) * 2,
                                static_cast<uint64_t>(a.B > 1 ? a.q.sb : D) * 2};
   const uint32_t box[4] = {64, static_cast<uint32_t>(p.heads), static_cast<uint32_t>(p.tokens), 1};

@@ -272,7 +272,7 @@ __device__ __forceinline__ uint32_t col_p(int i) { return kApart<D> ? 384u + 64u
 
 constexpr uint32_t kCtlRegs = 72, kSoftmaxRegs = 184, kOutRegs = 72;  // 512 threads launched at 128
 static_assert(128 * kCtlRegs + 256 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 128, "registers of one CTA");
-static_assert(kOutRegs == kCtlRegs, "every warp runs the teardown with the control budget");
+static_assert(kOutRegs == kCtlRegs, "every warp runs the teardown with the control registers");
 
 struct Params {
   Divisor Hkv, group;   // key/value heads, and the query heads of one
@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Rows of one head of a packed tensor: boxes of 64 channels x 128 rows, 128-byte swizzle.
 bool make_map(CUtensorMap* map, const Bf16In& x, int64_t rows, int64_t heads, int64_t D) {
   const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows)};
-  // (strides of one head or row are not used; the driver wants valid ones)
+  // (strides of one head or row are not used; the tensor map wants valid ones)
   const uint64_t strides[2] = {static_cast<uint64_t>(heads > 1 ? x.sh : D) * 2, static_cast<uint64_t>(rows > 1 ? x.ss : D) * 2};
   const uint32_t box[3] = {64, 1, 128};
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -949,6 +949,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   Header* header = static_cast<Header*>(a.workspace);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
   const int64_t group = a.H / a.Hkv, sms = sm_count_current();
+  // (100 tokens, 28 heads: 7.8 us with a tile for each SM, 8.5 with two for 14 of them)
   const int pair = most_blocks(a.N, a.B, group, 1) * a.Hkv <= sms ? 1 : 2;
   const int64_t units = most_blocks(a.N, a.B, group, pair) * a.Hkv;
   // A unit for each CTA at most: no first kernel, which costs more than its list and

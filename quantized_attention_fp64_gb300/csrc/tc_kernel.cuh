@@ -1,5 +1,5 @@
 // What the warp-specialised tensor-core kernels of the prompt operators share:
-// bounded waits, register budgets, descriptors and products in BF16.
+// bounded waits, registers of warpgroups, descriptors and products in BF16.
 #pragma once
 
 #include <cstdint>
@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return r;
 }
 
-// Register budgets are those of a whole warpgroup.
+// Registers are those of a whole warpgroup.
 template <uint32_t N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
