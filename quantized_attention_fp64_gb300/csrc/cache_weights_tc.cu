@@ -19,7 +19,7 @@
 //               every fourth
 // TMEM holds an S^T of 128 x 128 for each group: all 512 columns. The product of a
 // tile (512 cycles at D = 128) and its 16384 exponentials (512 cycles) bound the
-// kernel alike. A causal chunk of 2000 tokens over 16001, 32 heads on 8, D = 128: 215 us, 1140
+// kernel alike. A causal chunk of 2000 tokens over 16001, 32 heads on 8, D = 128: 203 us, 1210
 // TFLOP/s (276 with two groups, whose latencies lay open; 325 before the
 // log-sum-exps came in a ring of their own).
 //
@@ -60,9 +60,10 @@ struct Smem {
 };
 static_assert(Smem<128>::kBytes <= 232448u, "shared memory of one CTA: at most 227 KB");
 
-// Registers: 768 threads launched at 80.
-constexpr uint32_t kCtlRegs = 56, kSumRegs = 80, kKeyRegs = 104;
-static_assert(kSumRegs == 80 && 128 * kCtlRegs + 512 * kSumRegs + 128 * kKeyRegs <= kThreads * 80, "registers of one CTA");
+// Registers: 768 threads launched at 80. The sums are the ones that want more (with
+// 80, 56 of the control warps and 104 of the keys' the chunk above takes 215 us).
+constexpr uint32_t kCtlRegs = 40, kSumRegs = 96, kKeyRegs = 56;
+static_assert(128 * kCtlRegs + 512 * kSumRegs + 128 * kKeyRegs <= kThreads * 80, "registers of one CTA");
 
 struct Params {
   CacheWeightsArgs a;
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 8) {
     // --------------------------------------------------------------------- sums --
+    tc::regs_inc<kSumRegs>();
     const int group = (warp - 8) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128u * static_cast<uint32_t>(group);
@@ -418,6 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t since = a.causal ? j - (k.len - k.rows) : 0;                    // the first row token that sees the key
       const int32_t all_since = a.causal ? j0 + kTile - 1 - (k.len - k.rows) : 0;   // and all keys of the tile
       const int32_t first = k.first(prm), n = k.end(prm), step = alone ? 4 : 2;
+      // who adds to a key's score first reads it now, not at the end
+      const float before = there && j < k.shown && group == 0
+                               ? *static_cast<volatile float*>(a.scores + k.b * a.scores_b + k.h * a.scores_h + j)
+                               : 0.0f;
       float sum = 0.0f;
       for (int32_t q = alone ? group : group & 1; q < n - first; q += step) {
         const uint32_t ls = (at + static_cast<uint32_t>(q)) % L::kLse, phase = (at + static_cast<uint32_t>(q)) / L::kLse;
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (group > 0 && !(ok = tc::wait_bar_warp(w, w.bar(L::kJoin + turn - 4), (unit >> 2) & 1u))) break;
       if (there && j < k.shown && !(sum == 0.0f)) {
         volatile float* p = a.scores + k.b * a.scores_b + k.h * a.scores_h + j;
-        *p = *p + sum;
+        *p = (group == 0 ? before : *p) + sum;
       }
       __syncwarp();
       if (lane == 0 && group < 3) tc::mbar_arrive(w.bar(L::kJoin + turn));
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::regs_dec<kCtlRegs>();
   } else {
     // --------------------------------------------------------------------- keys --
-    tc::regs_inc<kKeyRegs>();
+    tc::regs_dec<kKeyRegs>();
     const int g = lane >> 2, t4 = lane & 3;
     uint32_t unit = 0;
     bool bad = false;
@@ -498,23 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           there_ring[8 * buf + local] = slot < 0 ? 0 : 1;
         }
         // key 8 n + g of the block, channels 16 t4 .. 16 t4 + 15 of each half
-        uint4 c[4 * (D / 64)];
-#pragma unroll
-        for (int i = 0; i < 4 * (D / 64); ++i)
-          c[i] = slot < 0 ? make_uint4(0, 0, 0, 0)
-                          : *reinterpret_cast<const uint4*>(a.c.k + slot * (kCacheBlock * D) + i * 512 + lane * 16);
         uint8_t* tile = smem + L::kOffK + (2u * buf + static_cast<uint32_t>(local >> 2)) * L::kTileBytes;
+#pragma unroll 1
+        for (int x = 0; x < D / 64; ++x) {  // (half at a time, for few registers)
+          uint4 c[4];
 #pragma unroll
-        for (int i = 0; i < 4 * (D / 64); ++i) {
-          const int key = 32 * (local & 3) + 8 * (i & 3) + g;
-          uint32_t o[8];
-          codes_to_bf16(c[i].x, o[0], o[1]);
-          codes_to_bf16(c[i].y, o[2], o[3]);
-          codes_to_bf16(c[i].z, o[4], o[5]);
-          codes_to_bf16(c[i].w, o[6], o[7]);
-          uint8_t* p = tile + (i >> 2) * L::kSub + key * 128;
-          *reinterpret_cast<uint4*>(p + (((2 * t4) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(p + (((2 * t4 + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int i = 0; i < 4; ++i)
+            c[i] = slot < 0 ? make_uint4(0, 0, 0, 0)
+                            : *reinterpret_cast<const uint4*>(a.c.k + slot * (kCacheBlock * D) + (4 * x + i) * 512 + lane * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 32 * (local & 3) + 8 * i + g;
+            uint32_t o[8];
+            codes_to_bf16(c[i].x, o[0], o[1]);
+            codes_to_bf16(c[i].y, o[2], o[3]);
+            codes_to_bf16(c[i].z, o[4], o[5]);
+            codes_to_bf16(c[i].w, o[6], o[7]);
+            uint8_t* p = tile + x * L::kSub + key * 128;
+            *reinterpret_cast<uint4*>(p + (((2 * t4) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(p + (((2 * t4 + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
       tc::fence_proxy_async_smem();
