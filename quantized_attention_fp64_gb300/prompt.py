@@ -151,5 +151,5 @@ def prompt_attention(q, k, v, offsets, kv_offsets=None, is_causal: bool = True, 
         if need:
             args.workspace_bytes = need
         _keep(key, (index, _lib.load().sage_prompt_attention, ctypes.byref(args), args, args.q, args.k, args.v, args.out,
-                    q.shape, (H, N), need))
+                    q.is_contiguous(), (H, N), need))
     return (out, lse) if return_lse else out

@@ -1155,3 +1155,21 @@ def test_attention_nan_in_folded_parts(B, Hkv, n, D):
             assert torch.isnan(out[0, :, mine].float()).all()
             out[0, :, mine] = clean[0, :, mine]
             assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+def test_attention_repeated_calls_with_dense_views(layout, T):
+    """From its second call on a signature goes a shorter way: outputs of queries that are dense views of the other layout."""
+    lengths, H, Hkv, D, page = [300, 77, 50], 4, 2, 64, 64
+    for call in range(4):
+        rng = np.random.default_rng(300 + call)
+        table, P = make_table(rng, lengths, page)
+        c = random_cache(rng, P, Hkv, D, page)
+        poison_unused(c, table, lengths)
+        q = bf16(rng, 3, T, H, D)
+        ref = oc.attention(c, f32(q), table, lengths, [T] * 3, True, 1 / math.sqrt(D))
+        x = q.transpose(1, 2).contiguous().transpose(1, 2) if layout == "NHD" else q.transpose(1, 2)
+        out, lse = sage.cache_attention(x, upload(c), ints(table), ints(lengths), is_causal=True, return_lse=True, tensor_layout=layout)
+        assert out.shape == x.shape
+        close(out if layout == "NHD" else out.transpose(1, 2), lse, *ref)

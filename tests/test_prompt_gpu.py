@@ -549,3 +549,40 @@ def test_offsets_past_32_bits(H):
     tq, tk = sage.rotary(q, k, pos, table)
     sage.rotary(wide[0], wide[1], pos, table, out=(wide[0], wide[1]))
     assert torch.equal(wide[0], tq) and torch.equal(wide[1], tk)
+
+
+# ------------------------------------------------------------- repeated calls --
+# From its second call on a signature goes a shorter way, which has to give outputs laid out like the first one's.
+
+
+def views(g, N, heads, D, layout):
+    """Tensors [N, heads, D] in the layout that are dense views of the other one, without a copy."""
+    x = bf16(g, heads, N, D) if layout == "NHD" else bf16(g, N, heads, D)
+    return x.transpose(0, 1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+def test_repeated_calls_with_dense_views(layout, causal, D):
+    rows, H, Hkv = [140, 3, 260], 4, 2
+    off = ints(ends(rows))
+    for call in range(4):
+        g = gen(180 + call)
+        q, k, v = (views(g, sum(rows), h, D, layout) for h in (H, Hkv, Hkv))
+        assert not q.is_contiguous()
+        out, lse = sage.prompt_attention(q, k, v, off, is_causal=causal, return_lse=True, tensor_layout=layout)
+        assert out.shape == q.shape
+        x, o = ((q, k, v), out) if layout == "NHD" else ([t.transpose(0, 1) for t in (q, k, v)], out.transpose(0, 1))
+        close(o, lse, formula(*x, rows, rows, causal, 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_repeated_calls_with_queries_of_a_projection(D):
+    rows, H, Hkv = [140, 3, 260], 4, 2
+    for call in range(3):
+        g = gen(184 + call)
+        fused = bf16(g, sum(rows), H + 2 * Hkv, D)
+        q, k, v = fused[:, :H], fused[:, H:H + Hkv], fused[:, H + Hkv:]
+        out = sage.prompt_attention(q, k, v, ints(ends(rows)))
+        close(out, None, formula(q, k, v, rows, rows, True, 1 / math.sqrt(D)))

@@ -218,3 +218,22 @@ def test_graph_replay_with_moving_positions():
         torch.cuda.synchronize()
         close(qo, formula(q, pos, table, False))
         close(ko, formula(k, pos, table, False))
+
+
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_repeated_calls_with_dense_views(packed, layout):
+    """From the second call on a signature goes a shorter way."""
+    B, T, H, Hkv, D = 1 if packed else 3, 37, 4, 2, 64
+    table = sage.rotary_table(D, device="cuda")
+    for call in range(4):
+        g = gen(60 + call)
+        q, k = ((bf16(g, B, h, T, D) if layout == "NHD" else bf16(g, B, T, h, D)).transpose(1, 2) for h in (H, Hkv))
+        pos = torch.randint(0, 5000, (B, T), generator=g, device="cuda").to(torch.int32)
+        args = (q[0], k[0], pos[0]) if packed else (q, k, pos)
+        got = sage.rotary(*args, table, tensor_layout=layout)
+        for x, y in zip((q, k), got):
+            y = y[None] if packed else y
+            assert y.shape == x.shape
+            x, y = (x, y) if layout == "NHD" else (x.transpose(1, 2), y.transpose(1, 2))
+            close(y, formula(x, pos, table, False))
