@@ -49,8 +49,10 @@ struct Smem {
   static constexpr uint32_t kOffLse = kOffQ + kStages * kTileBytes;   // [stage][128] -log2(e) lse
   static constexpr uint32_t kOffScale = kOffLse + kLse * 512;         // [pair][8 blocks]
   static constexpr uint32_t kOffThere = kOffScale + 2 * 32;           // [pair][8 blocks]: on a page of the cache
-  static constexpr uint32_t kOffOdd = kOffThere + 2 * 32;             // [lse]: rows that are none
-  static constexpr uint32_t kOffBar = (kOffOdd + 4 * kLse + 7) / 8 * 8;
+  static constexpr uint32_t kOffOdd = kOffThere + 2 * 32;             // [stage]: whether a row is in one of these
+  static constexpr uint32_t kOffNone = kOffOdd + 4 * kLse;            // [stage][128 bits]: rows that add nothing
+  static constexpr uint32_t kOffNan = kOffNone + 16 * kLse;           // [stage][128 bits]: rows whose log-sum-exp is a NaN
+  static constexpr uint32_t kOffBar = (kOffNan + 16 * kLse + 7) / 8 * 8;
   static constexpr int kQFull = 0, kQEmpty = kQFull + kStages, kKFull = kQEmpty + kStages, kKEmpty = kKFull + 2;
   static constexpr int kSFull = kKEmpty + 2, kSFree = kSFull + 4, kDrain = kSFree + 4, kJoin = kDrain + 2;
   static constexpr int kLFull = kJoin + 12, kLEmpty = kLFull + kLse, kBars = kLEmpty + kLse;
@@ -172,32 +174,49 @@ __device__ __forceinline__ float sum_rows(const uint32_t (&s)[32], float scale, 
 }
 
 // S of rows that do not count becomes minus infinity in TMEM, so that their weights
-// are 0: those of tokens before `since` or from `rows` on, and those whose lse' is
-// that too (S may be a NaN). Rows of the tile: `heads` heads, token by token.
-__device__ __forceinline__ void hide_rows(uint32_t tS, const float* lse, int32_t since, int32_t t, int32_t heads,
-                                          int32_t rows) {
+// are 0: those of tokens before `since` or from `rows` on, and those of `none` (S may
+// be a NaN). That of the other rows of `nan` becomes a NaN: their lse' is finite, so
+// that keys which they do not see get nothing of it. Rows of the tile: `heads` heads,
+// token by token; a bit each in none and nan, which are there where `marked`.
+__device__ __forceinline__ void hide_rows(uint32_t tS, bool marked, const uint32_t* none, const uint32_t* nan, int32_t since,
+                                          int32_t t, int32_t heads, int32_t rows) {
   int32_t g = 0;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b) {
+    const uint32_t off = marked ? none[b] : 0u, odd = marked ? nan[b] : 0u;
     uint32_t s[32];
     tc::tmem_ld32(tS + 32u * static_cast<uint32_t>(b), s);
     tc::tmem_wait_ld();
+    if (odd != 0u) {
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const float4 l = *reinterpret_cast<const float4*>(lse + 32 * b + k);
-      const float ls[4] = {l.x, l.y, l.z, l.w};
+      for (int k = 0; k < 32; ++k)
+        if ((odd >> k & 1u) != 0) s[k] = 0x7FC00000u;
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool out = (t < since) | (t >= rows) | (ls[e] == -INFINITY);
-        s[k + e] = out ? 0xFF800000u : s[k + e];
-        const bool wrap = ++g == heads;
-        g = wrap ? 0 : g;
-        t += wrap ? 1 : 0;
-      }
+    for (int k = 0; k < 32; ++k) {
+      const bool out = (t < since) | (t >= rows) | ((off >> k & 1u) != 0);
+      s[k] = out ? 0xFF800000u : s[k];
+      const bool wrap = ++g == heads;
+      g = wrap ? 0 : g;
+      t += wrap ? 1 : 0;
     }
     tc::tmem_st32(tS + 32u * static_cast<uint32_t>(b), s);
   }
   tc::tmem_wait_st();
+}
+
+// The rows of a query tile that add nothing (log-sum-exp x of minus infinity), and those
+// where it is a NaN, whose lse' becomes 0. By a whole warp; row 32 e + lane.
+__device__ __forceinline__ void mark_rows(const float (&x)[4], float (&l)[4], uint32_t* none, uint32_t* nan) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t off = __ballot_sync(0xffffffffu, x[e] == -INFINITY), odd = __ballot_sync(0xffffffffu, x[e] != x[e]);
+    if ((threadIdx.x & 31u) == 0) {
+      none[e] = off;
+      nan[e] = odd;
+    }
+    if (x[e] != x[e]) l[e] = 0.0f;
+  }
 }
 
 // Which of the four groups of sum warps (and S) takes the q-th query tile of a unit
@@ -232,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* scale_ring = reinterpret_cast<float*>(smem + L::kOffScale);
   int32_t* there_ring = reinterpret_cast<int32_t*>(smem + L::kOffThere);
   int32_t* odd_ring = reinterpret_cast<int32_t*>(smem + L::kOffOdd);
+  uint32_t* none_ring = reinterpret_cast<uint32_t*>(smem + L::kOffNone);
+  uint32_t* nan_ring = reinterpret_cast<uint32_t*>(smem + L::kOffNan);
   if (threadIdx.x == 0) {
     *w.abort_flag = 0;
     for (int i = 0; i < L::kStages; ++i) {
@@ -381,12 +402,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool odd = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            odd |= x[e] == -INFINITY && !zero[e];
+            odd |= !(x[e] > -INFINITY) && !zero[e];
             l[e] = x[e] == -INFINITY ? -INFINITY : -x[e] * kLog2e;
           }
-          if (i + 1 < n) fetch(k, i + 1, x, zero);
           odd = __any_sync(0xffffffffu, odd);
-          if (!(ok = tc::wait_bar_warp(w, w.bar(L::kLEmpty + static_cast<int>(st)), ((at / L::kLse) & 1u) ^ 1u))) break;
+          const auto empty = [&]() {
+            return tc::wait_bar_warp(w, w.bar(L::kLEmpty + static_cast<int>(st)), ((at / L::kLse) & 1u) ^ 1u);
+          };
+          if (odd) {
+            if (!(ok = empty())) break;
+            mark_rows(x, l, none_ring + 4 * st, nan_ring + 4 * st);
+          }
+          if (i + 1 < n) fetch(k, i + 1, x, zero);
+          if (!(ok = empty())) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) lse_ring[st * kTile + 32 * e + lane] = l[e];
           if (lane == 0) odd_ring[st] = odd ? 1 : 0;
@@ -434,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         const float* lse = lse_ring + ls * kTile;
         const int32_t t0 = (prm.splits == 1 ? first + q : (first + q) / prm.splits) * prm.tokens;
-        if (t0 < all_since || odd_ring[ls] != 0) hide_rows(tS, lse, since, t0, prm.heads, k.rows);
+        const bool marked = odd_ring[ls] != 0;
+        if (t0 < all_since || marked)
+          hide_rows(tS, marked, none_ring + 4 * ls, nan_ring + 4 * ls, since, t0, prm.heads, k.rows);
         // S is read 32 columns at a time, the next ones under this one's exponentials
         uint32_t s0[32], s1[32];
         tc::tmem_ld32(tS, s0);

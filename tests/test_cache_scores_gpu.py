@@ -136,6 +136,36 @@ def test_weights_nan_stays_with_what_it_touches(T):
     assert torch.equal(odd, want)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,H", [(128, 4), (64, 10), (64, 2)])
+@pytest.mark.parametrize("T", [3, 7, 50, 140])
+def test_weights_log_sum_exps_that_are_nan(T, D, H, causal):
+    """Rows anywhere whose log-sum-exp is a NaN: the keys that they see become NaN, and all others are as without them."""
+    rng = np.random.default_rng(15)
+    lengths, q_lengths, Hkv, page = [400, 150, 290], [T, T - 1, T], 2, 64
+    table, P = make_table(rng, lengths, page)
+    gpu = upload(random_cache(rng, P, Hkv, D, page))
+    q = bf16(rng, 3, T, H, D)
+    args = dict(cache=gpu, page_table=ints(table), lengths=ints(lengths), q_lengths=ints(q_lengths), is_causal=causal)
+    _, lse = sage.cache_attention(q, return_lse=True, **args)
+    lse[2, 0, T - 1] = math.inf  # weighs nothing
+    start = torch.from_numpy(rng.random((3, Hkv, 400)).astype(np.float32)).cuda()
+    rows = [(0, 0, 0), (0, H - 1, T // 2), (1, H // 2, T // 3), (1, 0, T - 1), (2, H - 1, 0), (2, H - 1, T - 1)]  # (1, 0, T - 1) is none
+    for some in ([r] for r in rows), [rows]:
+        for marks in some:
+            without, odd = lse.clone(), lse.clone()
+            want_nan = torch.zeros_like(start, dtype=torch.bool)
+            for b, h, t in marks:
+                without[b, h, t], odd[b, h, t] = -math.inf, math.nan
+                if t < q_lengths[b]:
+                    want_nan[b, h // (H // Hkv), :lengths[b] - q_lengths[b] + t + 1 if causal else lengths[b]] = True
+            want = sage.cache_add_weights(start.clone(), q, lse=without, **args)
+            got = sage.cache_add_weights(start.clone(), q, lse=odd, **args)
+            assert not torch.isnan(want).any()
+            assert torch.equal(torch.isnan(got), want_nan)
+            assert torch.equal(got[~want_nan], want[~want_nan])
+
+
 @pytest.mark.parametrize("T", [1, 50])
 def test_weights_bad_pages_and_lengths_are_flagged(T):
     rng = np.random.default_rng(13)
