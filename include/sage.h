@@ -595,10 +595,11 @@ SAGE_API int sage_cache_add_weights(const sage_cache_add_weights_args* args);
  * lengths that reach past the table or past scores_size are cut, and the device
  * error word is set. A token on a page outside the cache is taken as 0 with
  * scale 0; what would go to a page outside the cache is lost.
- * out_table: int32 rows of out_max_pages entries; it may be the table itself
- * (the sequence is cut back in place: one of at most keep tokens stays as it is, but
- * for the slots behind its last token), else its pages must not be among the
- * ones read, nor be named twice. Pages behind a new length are not written.
+ * out_table: int32 rows of out_max_pages entries; it may be the table itself, or
+ * its first columns, at the same address (the sequence is cut back in place: one
+ * of at most keep tokens stays as it is, but for the slots behind its last token;
+ * with B > 1 rows as far apart as the table's, else ARG); otherwise its pages must
+ * not be among the ones read, nor be named twice. Pages behind a new length are not written.
  * Pages read may be shared by sequences unless they are written.
  * lengths_out, kept and scores_out must not overlap lengths and scores (ARG where
  * one is the other).

@@ -273,6 +273,9 @@ int sage_cache_evict(const sage_cache_evict_args* args) {
   if (args->B > 0 && (args->lengths_out_dev == args->lengths_dev ||
                       (a.c.H > 0 && S > 0 && args->scores_out_dev == args->scores_dev)))
     return SAGE_ERR_ARG;
+  // The table itself (in place): the rows have to be the same ones. The distance of a
+  // single row to the next does not matter.
+  if (a.from.table == a.to.table && a.from.stride != a.to.stride && args->B > 1) return SAGE_ERR_ARG;
   // blocks of all heads, keys and values, are numbered in 32 bits
   if (args->B > 0 && a.c.H > 0 && div_up(keep, kCacheBlock) > (int64_t(1) << 30) / (args->B * a.c.H)) return SAGE_ERR_TOO_LARGE;
   const size_t need = cache_evict_workspace_bytes(args->B, a.c.H, keep, S);

@@ -451,7 +451,7 @@ size_t cache_evict_workspace_bytes(int64_t B, int64_t H, int64_t keep, int64_t s
 
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, int64_t D, cudaStream_t stream) {
   const Work work = work_of(a);
-  const bool in_place = a.from.table == a.to.table && a.from.stride == a.to.stride;
+  const bool in_place = a.from.table == a.to.table;  // (one row, or rows equally far apart)
   const dim3 grid(static_cast<unsigned>(a.c.H > 0 ? a.c.H : 1), static_cast<unsigned>(a.B));
   // A sequence of some thousand tokens is too little for 1024 threads (16 sequences of
   // 8 heads, selection and moves: up to 1000 tokens 21.1 us with 512 threads, 25.0 with

@@ -327,6 +327,28 @@ def test_evict(case, place):
     same_cache(gpu, c)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_evict_one_sequence_in_place_by_another_view(D):
+    """A single row of the table may be passed as another view of it, whose distance to a next row is another one."""
+    H, page, n, keep, recent = 4, 64, 9000, 5000, 40
+    S = n + 3
+    for seed in range(3):
+        rng = np.random.default_rng(240 + seed)
+        table, P = make_table(rng, [n], page)
+        c = random_cache(rng, P, H, D, page)
+        scores = some_scores(rng, 1, H, S)
+        gpu = upload(c)
+        row = ints(table)
+        first = row[0][:-(-keep // page)][None]      # the columns that the result needs
+        assert first.data_ptr() == row.data_ptr() and first.stride(0) != row.stride(0)
+        wide = row.as_strided(row.shape, (row.stride(0) + 7, 1))
+        for out_table in ((first, wide) if seed % 2 else (wide, first)):
+            _, kept, moved = sage.cache_evict(gpu, row, ints([n]), dev(scores), keep, recent=recent, out_table=out_table)
+            want = evict(c, table, [n], scores, keep, recent, table)
+            assert np.array_equal(kept.cpu().numpy(), want[1]) and np.array_equal(moved.cpu().numpy(), want[2], equal_nan=True)
+            same_cache(gpu, c)
+
+
 def test_evict_scores_of_all_kinds():
     n, keep = 700, 200
     rng = np.random.default_rng(220)

@@ -272,6 +272,14 @@ def test_eviction_refuses(lib):
     assert _evict(lib, wsn=need - 1) == WORKSPACE
 
 
+def test_eviction_refuses_other_rows_at_the_table_s_address(lib):
+    """Cutting back in place has to be known as that: rows that begin where the table's do are the table's rows."""
+    far = lambda stride, n=4: _tab(stride=stride, n=n)  # noqa: E731
+    for stride in (0, 4, 6, 16):
+        assert _evict(lib, table=far(8), out=far(stride)) == ARG
+        assert _evict(lib, table=far(8), out=far(stride, n=2)) == ARG
+
+
 # ----------------------------------------------------------- Python binding --
 
 
