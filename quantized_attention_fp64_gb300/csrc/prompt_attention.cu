@@ -26,8 +26,9 @@
 // reads it; that product and the next S = Q K^T are issued together when P is
 // there, so the tensor pipe works on one query tile while the other's softmax runs.
 // The maximum m_t that the exponentials go by follows only when the true one has
-// grown by 2^8: O is rescaled then, a few times at the beginning of a row, and
-// P and l stay within 2^8 of their usual range (no bit is lost in floating point).
+// grown by 2^8: O is rescaled then, a few times at the beginning of a row. It is set
+// 2^8 above the true one, so that no weight is above 1 and O overflows no sooner than
+// the sum of a softmax by the true maximum (no bit is lost in floating point).
 //
 // What a row does not see must not touch it, whatever stands there: its P is 0,
 // but 0 times an infinity or a NaN of V is a NaN. The output warps look for
@@ -69,7 +70,7 @@ constexpr int kKeys = 128;      // keys of a tile
 constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
 constexpr uint32_t kRedoWords = 8;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8
+constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8, and is set that far above
 
 // One or two query tiles of a key/value head, the same for each of them.
 struct alignas(16) Block {
@@ -252,7 +253,7 @@ struct Smem {
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
-  static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m
+  static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m - 8
   static constexpr uint32_t kOffRedo = kOffStat + 2 * 128 * 8;  // units to do again, and whether there are any
   static constexpr uint32_t kOffBlock = (kOffRedo + 4 * (kRedoWords + 1) + 15) / 16 * 16;  // the CTA's block, and the header, without a list
   static constexpr uint32_t kBytes = kOffBlock + sizeof(Block) + 16;
@@ -380,10 +381,10 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
     if (!tc::wait_bar_warp(w, w.bar(L::kPFree + t), (pv - 1) & 1u)) return false;
     tc::tc_fence_after();
   }
-  // (up - m) c > 8; with m = -inf whenever the row has seen a key
-  if (__any_sync(0xffffffffu, fmaf(up, c, neg) > kGrowth || (m == -INFINITY && up != -INFINITY))) {
+  // neg = -m c - 8: a weight would be above 1; with m = -inf whenever the row has seen a key
+  if (__any_sync(0xffffffffu, fmaf(up, c, neg) > 0.0f || (m == -INFINITY && up != -INFINITY))) {
     const float m_new = fmaxf(m, up);
-    const float neg_new = m_new == -INFINITY ? 0.0f : -m_new * c;
+    const float neg_new = m_new == -INFINITY ? 0.0f : fmaf(-m_new, c, -kGrowth);
     if (!first) {
       // a row that had seen nothing has O = 0 and l = 0
       const float alpha = m == -INFINITY ? 0.0f : tc::exp2_approx(neg_new - neg);

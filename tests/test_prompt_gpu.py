@@ -252,6 +252,25 @@ def test_growing_and_falling_logits(D):
         assert ((lse.double() - l).abs() <= 2.0 ** -9).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("high", [5.375, 2.5])
+def test_large_values_whose_sum_is_in_range(high, causal, D):
+    """Values of 2^122: a key whose weight is 216 (or 12) times that of those before it leaves the sums finite."""
+    n, H = 400, 2
+    g = gen(74)
+    q = torch.ones((n, H, D), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    k[[150, 290, 399]] = high
+    v = (torch.rand((n, 1, D), generator=g, device="cuda") * 2.0 ** 122).to(torch.bfloat16)
+    ref = formula(q, k, v, [n], [n], causal, 1 / D)
+    assert torch.isfinite(ref[0]).all()
+    out, lse = sage.prompt_attention(q, k, v, ints([0, n]), is_causal=causal, sm_scale=1 / D, return_lse=True)
+    close(out, lse, ref)
+    out, lse, r = repeated(q, k, v, ints([0, n]), is_causal=causal, sm_scale=1 / D)
+    close(out[:, ::r], lse[::r], ref)
+
+
 def test_peaked_rows_take_one_value():
     n, D = 300, 128
     g = gen(73)
