@@ -691,7 +691,9 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * it is one of them). sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16
  * (by 2^-9 of themselves) for the product with v, their sum is taken in fp32
- * before that. Outputs are finite where the sums of p_j v_j stay within fp32.
+ * before that. Outputs are finite where the sums of p_j v_j stay within fp32. An
+ * infinity or NaN among the values of a key that a row sees is part of its sum
+ * however small the key's weight; other rows do not meet it.
  * workspace_dev: sage_prompt_attention_workspace_size bytes, 256-byte aligned,
  * contents do not matter; not used by another call at the same time.
  * Errors: NULLPTR, SHAPE, HEAD_DIM, LAYOUT, ALIGN, ARG, WORKSPACE, TOO_LARGE, ARCH,

@@ -18,7 +18,7 @@
 // the lengths are. Calls of at most a unit for each SM do without. Roles of the 16 warps:
 //   warp 0      TMA: the unit's queries, and a ring of key and value tiles in turn
 //   warps 1, 2  TMEM allocation; the products of query tile 0, 1 (one thread issues)
-//   warp 3      in the second pass (below): clears value tiles
+//   warp 3      in the second pass (below): clears infinities and NaN in value tiles
 //   warps 4-7, 8-11  softmax of query tile 0, 1 (TMEM lane = row)
 //   warps 12-15 output: O of either tile, scaled and stored
 // TMEM holds S0, S1, O0, O1: all 512 columns at D = 128. The softmax reads S of a
@@ -31,13 +31,14 @@
 // the sum of a softmax by the true maximum (no bit is lost in floating point).
 //
 // What a row does not see must not touch it, whatever stands there: its P is 0,
-// but 0 times an infinity or a NaN of V is a NaN. The output warps look for
-// infinities and NaN in what they store, and a unit that has one is done again in a
-// second pass. There warp 3 clears, in the tiles that hold keys which some row of the
-// unit does not see (the diagonal, the sequence's end), the rows behind the
-// sequence's end and every infinity and NaN, before the product takes them, and the
-// output warps add those values to the rows that do see them (a row's P of a key it
-// sees is positive). Calls with finite values pay for the look at the outputs
+// but 0 times an infinity or a NaN of V is a NaN. And what it does see has a weight
+// above 0, by the formula, though P may be 0 where the exponential leaves fp32. The
+// output warps look for infinities and NaN in what they store, and a unit that has
+// one is done again in a second pass. There warp 3 clears the rows of V behind the
+// sequence's end and every infinity and NaN, before the product takes them. Those of
+// tiles that all rows of the unit see are remembered by channel, and the output
+// warps add them to every row; in the other tiles (the diagonal) they look the
+// values up and add them to the rows that see them. Calls with finite values pay for the look at the outputs
 // alone (2% of the prompts above); a look at all values beforehand took 23 us of
 // them, one at the value tiles as they pass by 32.
 //
@@ -67,8 +68,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 128;      // keys of a tile
-constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring) that warp 3 may be ahead of a unit's end
+constexpr int kFixes = 8;       // more than the value tiles (at most 5 in the ring), and so the units, that warp 3 may be ahead
 constexpr uint32_t kRedoWords = 8;
+// What warp 3 has cleared in a unit: values that some of its rows see, and that all do.
+constexpr uint32_t kBadSome = 1, kBadAll = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8, and is set that far above
 
@@ -248,12 +251,13 @@ struct Smem {
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kDrain = 12;
   static constexpr int kSFree = 14, kPFree = 16;         // P apart from S
   static constexpr int kStat = 18;                       // a tile's sums and maxima are there
-  static constexpr int kRaw = 20, kFix = kRaw + kFixes;  // value tiles for warp 3, and done by it
+  static constexpr int kRaw = 20, kFix = kRaw + kFixes;  // value tiles for warp 3, and units done by it
   static constexpr int kFull = kFix + kFixes, kEmpty = kFull + kStages, kTurn = kEmpty + kStages, kBars = kTurn + 2;
   static constexpr uint32_t kOffTmem = kOffBar + 8 * kBars;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: the unit has infinities or NaN that were cleared
-  static constexpr uint32_t kOffStat = (kOffBad + 4 * kFixes + 7) / 8 * 8;  // [2][128]: l, -c m - 8
+  static constexpr uint32_t kOffBad = kOffAbort + 4;   // [kFixes]: kBadSome, kBadAll
+  static constexpr uint32_t kOffOdd = kOffBad + 4 * kFixes;  // [kFixes][2][D bits]: channels with +inf, -inf (NaN: both) of all rows
+  static constexpr uint32_t kOffStat = (kOffOdd + kFixes * 2 * D / 8 + 7) / 8 * 8;  // [2][128]: l, -c m - 8
   static constexpr uint32_t kOffRedo = kOffStat + 2 * 128 * 8;  // units to do again, and whether there are any
   static constexpr uint32_t kOffBlock = (kOffRedo + 4 * (kRedoWords + 1) + 15) / 16 * 16;  // the CTA's block, and the header, without a list
   static constexpr uint32_t kBytes = kOffBlock + sizeof(Block) + 16;
@@ -445,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = tc::smem_u32(smem);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), prm.dev_err};
-  volatile int32_t* bad_units = reinterpret_cast<volatile int32_t*>(smem + L::kOffBad);
+  volatile uint32_t* bad_units = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
+  uint32_t* odd_channels = reinterpret_cast<uint32_t*>(smem + L::kOffOdd);
   uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kOffRedo);
   if (threadIdx.x == 0) {
     *w.abort_flag = 0;
@@ -550,8 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tma_load_3d(sbase + L::kOffQ + t * L::kTile + x * L::kSub, &tm_q, 64 * x, it.head(t), e.q0 + begin_of(e, t),
                               w.bar(L::kQFull + t));
           };
-          // in the second pass value tiles with hidden keys pass through warp 3
-          const int32_t masked = pass > 0 ? sees<kCausal>(e, 0) >> 7 : n;
           const auto tile = [&](const void* map, int32_t j, bool through) {
             const uint32_t st = at % L::kStages;
             if (!(ok = wait_bar(w, w.bar(L::kEmpty + static_cast<int>(st)), ((at / L::kStages) & 1u) ^ 1u))) return;
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // before has to be through with its own
           for (int32_t j = 0; ok && j < n; ++j) {
             tile(&tm_k, j, false);
-            if (ok) tile(&tm_v, j, j >= masked);
+            if (ok) tile(&tm_v, j, pass > 0);  // (in the second pass through warp 3)
             if (j == 0) {
               if (ok && n0 > 0) queries(0);
               if (ok && n1 > 0) queries(1);
@@ -710,8 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       wait_bar(w.draining(), w.bar(L::kDrain + t), 0);
     } else {
-      // ---------------------------------------- value tiles with hidden keys --
-      // (in the second pass; the ring goes on from the first)
+      // ------------------------------------------ value tiles of the second pass --
+      // (the ring goes on from the first)
       uint32_t base = 0, fixes = 0, done = 0;
       bool ok = true;
       const int32_t second = again() ? units : 0;
@@ -720,36 +723,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Units it(prm, list, second, redo); ok && it.valid(); it.advance()) {
         const Block& e = it.e;
         const int32_t n = max(key_tiles<kCausal>(e, 0), key_tiles<kCausal>(e, 1));
-        bool bad = false;
-        for (int32_t j = sees<kCausal>(e, 0) >> 7; j < n; ++j) {
+        const int32_t whole = kCausal ? sees<kCausal>(e, 0) >> 7 : n;  // tiles whose keys all rows see
+        uint32_t* odd = odd_channels + done % kFixes * (2 * D / 32);
+        uint32_t bad = 0;
+        for (int32_t j = 0; j < n; ++j) {
           const uint32_t p = base + 2u * static_cast<uint32_t>(j) + 1u;
           if (!(ok = wait_bar_warp(w, w.bar(L::kRaw + static_cast<int>(fixes % kFixes)), (fixes / kFixes) & 1u))) break;
+          // (this tile is there, so the output warps are done with the unit eight before)
+          if (j == 0 && lane < 2 * D / 32) odd[lane] = 0;
+          __syncwarp();
           uint8_t* tile = smem + L::kOffRing + (p % L::kStages) * L::kTile;
           const int32_t there = min(kKeys, e.keys - j * kKeys);
           // rows of 128 bytes: row r of the 64 channels x at r * 128 + x * kSub
           for (int x = 0; x < D / 64; ++x) {
             uint4* chunk = reinterpret_cast<uint4*>(tile + x * L::kSub);
-            if (kCausal) {
-              uint32_t acc[4] = {0u, 0u, 0u, 0u};
+            uint32_t acc[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 8
+            for (int q = lane; q < there * 8; q += 32) {
+              const uint4 v = chunk[q];
+              acc[0] = collect(v.x, acc[0]);
+              acc[1] = collect(v.y, acc[1]);
+              acc[2] = collect(v.z, acc[2]);
+              acc[3] = collect(v.w, acc[3]);
+            }
+            if (__any_sync(0xffffffffu, not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]))) {
+              bad |= j < whole ? kBadAll : kBadSome;
+#pragma unroll 1
               for (int q = lane; q < there * 8; q += 32) {
-                const uint4 v = chunk[q];
-                acc[0] = collect(v.x, acc[0]);
-                acc[1] = collect(v.y, acc[1]);
-                acc[2] = collect(v.z, acc[2]);
-                acc[3] = collect(v.w, acc[3]);
-              }
-              if (__any_sync(0xffffffffu, not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]))) {
-                bad = true;
+                uint16_t* o = reinterpret_cast<uint16_t*>(chunk + q);
+                const int c0 = 64 * x + 8 * ((q & 7) ^ ((q >> 3) & 7));  // (swizzled)
 #pragma unroll 1
-                for (int q = lane; q < there * 8; q += 32) {
-                  uint32_t* o = reinterpret_cast<uint32_t*>(chunk + q);
-#pragma unroll 1
-                  for (int k = 0; k < 4; ++k) {
-                    const uint32_t f = not_finite(o[k]);
-                    if (f & 0x8000u) o[k] &= 0xFFFF0000u;
-                    if (f & 0x80000000u) o[k] &= 0x0000FFFFu;
-                  }
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t b = o[k];
+                  if ((b & 0x7F80u) != 0x7F80u) continue;
+                  o[k] = 0;
+                  if (j >= whole) continue;
+                  const uint32_t word = static_cast<uint32_t>(c0 + k) >> 5, bit = 1u << ((c0 + k) & 31);
+                  if (b != 0xFF80u) atomicOr(odd + word, bit);
+                  if (b != 0x7F80u) atomicOr(odd + D / 32 + word, bit);
                 }
               }
             }
@@ -757,16 +768,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            bad_units[done % kFixes] = bad ? 1 : 0;
-            tc::mbar_arrive(w.bar(L::kFix + static_cast<int>(fixes % kFixes)));
-            tc::mbar_arrive(w.bar(L::kFull + static_cast<int>(p % L::kStages)));
-          }
-          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(w.bar(L::kFull + static_cast<int>(p % L::kStages)));
           ++fixes;
         }
+        if (ok && n > 0) {
+          if (lane == 0) {
+            bad_units[done % kFixes] = bad;
+            tc::mbar_arrive(w.bar(L::kFix + static_cast<int>(done % kFixes)));
+          }
+          __syncwarp();
+          ++done;
+        }
         base += 2u * static_cast<uint32_t>(n);
-        if (n > 0) ++done;
       }
     }
     __syncwarp();
@@ -823,20 +836,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0 && prm.lse != nullptr) prm.lse[h * prm.N + r] = -INFINITY;
       }
     }
-    uint32_t fixes = 0, fixed = 0, done = 0, stats[2] = {0, 0};  // (fixed: units of the second pass with keys)
+    uint32_t fixed = 0, done = 0, stats[2] = {0, 0};  // (fixed: units of the second pass with keys)
     bool ok = true;
     int pass = 0;
   units_of_output:
     for (Units it(prm, list, units, pass > 0 ? redo : nullptr); ok && it.valid(); it.advance()) {
       const Block& e = it.e;
       const int32_t n0 = key_tiles<kCausal>(e, 0), n1 = key_tiles<kCausal>(e, 1), n = max(n0, n1);
-      const int32_t masked = sees<kCausal>(e, 0) >> 7;
-      bool bad = false;  // the unit has infinities or NaN that warp 3 has cleared
-      if (pass > 0 && n > masked) {
-        fixes += static_cast<uint32_t>(n - masked);
-        const uint32_t f = fixes - 1;
-        if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(f % kFixes)), (f / kFixes) & 1u))) break;
-        bad = kCausal && bad_units[fixed % kFixes] != 0;
+      uint32_t bad = 0;  // infinities and NaN that warp 3 has cleared
+      if (pass > 0 && n > 0) {
+        if (!(ok = wait_bar_warp(w, w.bar(L::kFix + static_cast<int>(fixed % kFixes)), (fixed / kFixes) & 1u))) break;
+        bad = bad_units[fixed % kFixes];
       }
       uint32_t met = 0;  // infinities and NaN among the outputs
 #pragma unroll 1
@@ -893,17 +903,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (kCausal && bad) {
-          const int32_t mine = there ? sees<kCausal>(e, r) : 0;
-#pragma unroll 1
-          for (int32_t k = masked * kKeys; k < mine; ++k) {
-            const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + it.hk * prm.v_sh;
+        if (bad != 0 && there) {
+          const auto add = [&](int y, float x) {
+            dst[y] = static_cast<uint16_t>(tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + x, 0.0f));
+          };
+          if (bad & kBadAll) {
+            const uint32_t* odd = odd_channels + fixed % kFixes * (2 * D / 32);
 #pragma unroll 1
             for (int y = 0; y < D; ++y) {
-              const uint32_t b = v[y];
-              if ((b & 0x7F80u) == 0x7F80u)
-                dst[y] = static_cast<uint16_t>(
-                    tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + __uint_as_float(b << 16), 0.0f));
+              const bool up = (odd[y >> 5] >> (y & 31) & 1u) != 0, down = (odd[D / 32 + (y >> 5)] >> (y & 31) & 1u) != 0;
+              if (up) add(y, INFINITY);
+              if (down) add(y, -INFINITY);
+            }
+          }
+          if (kCausal && (bad & kBadSome)) {
+            const int32_t mine = sees<kCausal>(e, r);
+#pragma unroll 1
+            for (int32_t k = (sees<kCausal>(e, 0) >> 7) * kKeys; k < mine; ++k) {
+              const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + it.hk * prm.v_sh;
+#pragma unroll 1
+              for (int x = 0; x < D / 8; ++x) {
+                const uint4 u = *reinterpret_cast<const uint4*>(v + 8 * x);
+                if ((not_finite(u.x) | not_finite(u.y) | not_finite(u.z) | not_finite(u.w)) == 0u) continue;
+#pragma unroll 1
+                for (int y = 8 * x; y < 8 * x + 8; ++y)
+                  if ((v[y] & 0x7F80u) == 0x7F80u) add(y, __uint_as_float(static_cast<uint32_t>(v[y]) << 16));
+              }
             }
           }
         }

@@ -234,6 +234,42 @@ def test_infinite_values_reach_the_rows_that_see_them(rows, past, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("units", ["few", "many"])
+def test_infinite_values_of_little_weight(units, causal, D):
+    """An infinity that a row sees is in its sum however small the weight, in whichever key tile: the weights here are
+    exp(-120) and below, which fp32 does not hold, of keys before and behind those that raise the maximum."""
+    rows, past, H, Hkv = [300, 77, 140], [0, 200, 390], 4, 2
+    keys = [n + p for n, p in zip(rows, past)]
+    q, k, v = inputs(75, rows, keys, H, Hkv, D)
+    q[..., 0] = 16.0
+    k[..., 0] = 0.0
+    start = ends(keys)
+    marks = [(0, 3, 0, math.inf), (0, 140, 9, -math.inf), (0, 255, D - 1, math.inf), (0, 290, 33, math.nan), (0, 5, 34, math.inf), (0, 270, 34, -math.inf),
+             (1, 2, 1, math.nan), (1, 150, 2, -math.inf), (1, 270, 2, -math.inf), (2, 0, 40, math.inf), (2, 200, 40, -math.inf), (2, 529, 41, math.inf)]
+    for b, j, c, x in marks:
+        k[start[b] + j, :, 0] = -10.0 * math.sqrt(D)
+        v[start[b] + j, :, c] = 0.0
+    ref = formula(q, k, v, rows, keys, causal, 1 / math.sqrt(D))
+    want = ref[0].clone()
+    for b, j, c, x in marks:
+        v[start[b] + j, :, c] = x
+        at = ends(rows)[b]
+        first = max(j - past[b], 0) if causal else 0
+        want[at + first:at + rows[b], :, c] += x
+    # rows that see none but such keys give them the whole weight
+    q = q if units == "few" else q.repeat_interleave(76, 1)
+    out = sage.prompt_attention(q, k, v, ints(ends(rows)), kv_offsets=ints(ends(keys)), is_causal=causal)
+    out = out if units == "few" else out[:, ::76]
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out[odd & ~torch.isnan(want)].double(), want[odd & ~torch.isnan(want)])
+    err = (out.double() - ref[0]).abs()
+    bound = (ref[0].abs() + ref[2] / 64) * 2.0 ** -8 + ref[2] * (2.0 ** -8 + 2.0 ** -10)
+    assert (err[~odd] <= bound[~odd]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_growing_and_falling_logits(D):
     # the running maximum has to follow, early and late, by little and by much
     n = 700
