@@ -555,8 +555,8 @@ SAGE_API int sage_cache_attention(const sage_cache_attention_args* args);
  * summed in one fixed order, so results repeat bit for bit. The rows of scores
  * must not overlap, and q's strides must be positive (LAYOUT).
  * Numbers: codes and queries enter exactly, sums are fp32.
- * A NaN in a key's scale makes that key's score NaN, a NaN in lse those of the
- * keys that its row sees.
+ * A NaN in a key's scale makes that key's score NaN if a row sees it, a NaN in lse
+ * those of the keys that its row sees.
  * Errors: NULLPTR, SHAPE, HEAD_DIM, LAYOUT, ALIGN, ARG, TOO_LARGE (limits of
  * sage_cache_attention), ARCH, CUDA; on the device DEVICE_PAGE. */
 typedef struct sage_cache_add_weights_args {

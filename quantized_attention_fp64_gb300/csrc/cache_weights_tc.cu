@@ -219,6 +219,17 @@ __device__ __forceinline__ void mark_rows(const float (&x)[4], float (&l)[4], ui
   }
 }
 
+// Whether a row of tokens [since, rows) of a key/value head adds to the keys it sees.
+__device__ __forceinline__ bool is_weighed(const CacheWeightsArgs& a, int32_t b, int32_t h, int32_t group, int32_t since,
+                                           int32_t rows) {
+  const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + h * group) * a.T;
+  for (int32_t t = since; t < rows; ++t)
+#pragma unroll 1
+    for (int32_t g = 0; g < group; ++g)
+      if (lse[static_cast<int64_t>(g) * a.T + t] != -INFINITY) return true;
+  return false;
+}
+
 // Which of the four groups of sum warps (and S) takes the q-th query tile of a unit
 // with n key tiles, key tile x: two of them share a key tile, or four the only one.
 __device__ __forceinline__ int group_of(int n, int x, uint32_t q) {
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool alone = k.n == 1;  // one key tile for all four groups
       const int tile = alone ? 0 : group >> 1, blk = 4 * tile + (row >> 5);
       // A scale of 0 or NaN counts as the smallest number, so that what is hidden
-      // (minus infinity) stays that; NaN comes back when the sum is there.
+      // (minus infinity) stays that; a NaN becomes the sum's if a row sees the key.
       float scale = scale_ring[8 * (unit & 1u) + blk];
       const bool odd_scale = scale != scale;
       if (odd_scale || scale == 0.0f) scale = 0x1p-126f;
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       at += static_cast<uint32_t>(max(n - first, 0));
-      if (odd_scale && sum != 0.0f) sum = __uint_as_float(0x7FC00000u);
+      if (odd_scale && j < k.shown && is_weighed(a, k.b, k.h, prm.group, max(since, 0), k.rows)) sum = __uint_as_float(0x7FC00000u);
       // The groups add their sums one after another, so that they always come in this
       // order. (Four barriers for each, unit by unit: a group may be three units ahead of
       // the next one, which has to begin a unit before the keys of the one after the

@@ -166,6 +166,30 @@ def test_weights_log_sum_exps_that_are_nan(T, D, H, causal):
             assert torch.equal(got[~want_nan], want[~want_nan])
 
 
+@pytest.mark.parametrize("lse", [3.0, 500.0, -math.inf])
+@pytest.mark.parametrize("T", [3, 50, 140])
+def test_weights_keys_whose_scale_is_a_nan(T, lse):
+    """A NaN in a key's scale makes its score a NaN if a row sees it, however small the weight, and not otherwise."""
+    rng = np.random.default_rng(16)
+    lengths, H, Hkv, D, page = [200, 260], 4, 2, 128, 64
+    table, P = make_table(rng, lengths, page)
+    c = random_cache(rng, P, Hkv, D, page)
+    c.k_scale[table[0][1], 1, 0] = np.nan   # tokens 64 .. 95 of sequence 0
+    c.k_scale[table[1][4], 0, 0] = np.nan   # the last four tokens of sequence 1
+    gpu = upload(c)
+    q = bf16(rng, 2, T, H, D)
+    l = torch.full((2, H, T), lse, device="cuda")
+    l[1, :2, T - 2:] = -math.inf            # the last two rows of head 0 add nothing: the last two keys have no row
+    start = torch.from_numpy(rng.random((2, Hkv, 260)).astype(np.float32)).cuda()
+    got = sage.cache_add_weights(start.clone(), q, gpu, ints(table), ints(lengths), l, is_causal=True)
+    want = torch.zeros_like(got, dtype=torch.bool)
+    if lse > 0:
+        want[0, 1, 64:96] = True
+        want[1, 0, 256:258] = True
+    assert torch.equal(torch.isnan(got), want)
+    assert torch.equal(got[1, 0, 258:], start[1, 0, 258:]) and torch.equal(got[0, :, 200:], start[0, :, 200:])
+
+
 @pytest.mark.parametrize("T", [1, 50])
 def test_weights_bad_pages_and_lengths_are_flagged(T):
     rng = np.random.default_rng(13)
