@@ -72,6 +72,7 @@ struct Params {
   int32_t group;          // query heads of a key/value head
   int32_t heads, tokens;  // of a query tile: heads of the group, and tokens
   int32_t splits;         // query tiles for all heads of the group
+  uint64_t wait_ns;       // limit of a wait
 };
 
 __device__ __forceinline__ int32_t tiles_of(int32_t keys) { return keys / kTile + (keys % kTile != 0 ? 1 : 0); }
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t sbase = tc::smem_u32(smem);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), a.dev_err};
+  const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), a.dev_err, prm.wait_ns};
   float* lse_ring = reinterpret_cast<float*>(smem + L::kOffLse);
   float* scale_ring = reinterpret_cast<float*>(smem + L::kOffScale);
   int32_t* there_ring = reinterpret_cast<int32_t*>(smem + L::kOffThere);
@@ -600,6 +601,7 @@ cudaError_t launch(const CacheWeightsArgs& a, cudaStream_t stream) {
   p.heads = p.group < kTile ? p.group : kTile;
   p.tokens = kTile / p.heads;
   p.splits = static_cast<int32_t>(div_up(p.group, p.heads));
+  p.wait_ns = tc::wait_limit_ns(div_up(a.T, p.tokens) * p.splits);
   CUtensorMap tq;
   const uint64_t dims[4] = {D, static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.T), static_cast<uint64_t>(a.B)};
   // (strides of one head, token or sequence are not used; the tensor map wants valid ones)

@@ -295,6 +295,7 @@ struct Params {
   bool wide_out;        // rows of out begin at whole sectors (32 bytes)
   float scale;          // c
   int* dev_err;
+  uint64_t wait_ns;     // limit of a wait
 };
 
 __device__ __forceinline__ Block load_block(const Block* list, int32_t e) {
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t sbase = tc::smem_u32(smem);
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), prm.dev_err};
+  const tc::Waits w{sbase + L::kOffBar, reinterpret_cast<volatile int*>(smem + L::kOffAbort), prm.dev_err, prm.wait_ns};
   volatile uint32_t* bad_units = reinterpret_cast<volatile uint32_t*>(smem + L::kOffBad);
   uint32_t* odd_channels = reinterpret_cast<uint32_t*>(smem + L::kOffOdd);
   uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kOffRedo);
@@ -1005,6 +1006,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.wide_out = reinterpret_cast<uintptr_t>(a.out.p) % 32 == 0 && a.out.ss % 16 == 0 && a.out.sh % 16 == 0;
   p.scale = a.sm_log2;
   p.dev_err = a.dev_err;
+  p.wait_ns = tc::wait_limit_ns(div_up(a.M, kKeys));
   const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;
   const int bytes = static_cast<int>(Smem<D>::kBytes);
   if ((e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes)) != cudaSuccess) return e;

@@ -11,6 +11,9 @@ namespace sage {
 namespace tc {
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
+// Some roles wait for all tiles of a unit of work, and a unit may have eight million: 2 s
+// and 20 us for each (a tile takes 0.3 to 1.5 us, a few where values are cleared).
+inline uint64_t wait_limit_ns(int64_t tiles) { return kWaitNs + static_cast<uint64_t>(tiles) * 20000u; }
 
 // Barriers and the abort word of a CTA, in shared memory. A wait that runs out
 // sets the device error word and the abort word, which ends every other wait.
@@ -18,8 +21,9 @@ struct Waits {
   uint32_t bar0;
   volatile int* abort_flag;  // null: a wait of the clean-up, which goes on after an abort
   int* dev_err;
+  uint64_t limit;            // of a wait, in ns
   __device__ uint32_t bar(int i) const { return bar0 + 8u * static_cast<uint32_t>(i); }
-  __device__ Waits draining() const { return Waits{bar0, nullptr, dev_err}; }
+  __device__ Waits draining() const { return Waits{bar0, nullptr, dev_err, limit}; }
 };
 
 __device__ __forceinline__ bool wait_bar(const Waits& w, uint32_t bar, uint32_t parity) {
@@ -32,7 +36,7 @@ __device__ __forceinline__ bool wait_bar(const Waits& w, uint32_t bar, uint32_t 
       const uint64_t now = global_timer_ns();
       if (t0 == 0) {
         t0 = now;
-      } else if (now - t0 > kWaitNs) {
+      } else if (now - t0 > w.limit) {
         if (w.abort_flag != nullptr) *w.abort_flag = 1;
         atomicExch(w.dev_err, kDevErrTimeout);
         return false;

@@ -641,3 +641,19 @@ def test_repeated_calls_with_queries_of_a_projection(D):
         q, k, v = fused[:, :H], fused[:, H:H + Hkv], fused[:, H + Hkv:]
         out = sage.prompt_attention(q, k, v, ints(ends(rows)))
         close(out, None, formula(q, k, v, rows, rows, True, 1 / math.sqrt(D)))
+
+
+def test_a_unit_of_some_seconds():
+    """2^28 keys of one sequence, 2.6 s for a unit: who waits for all of it waits longer than for a tile."""
+    M, D = 1 << 28, 128
+    if torch.cuda.mem_get_info()[0] < 2 * M * D + (8 << 30):
+        pytest.skip("not enough free memory")
+    ones = torch.ones((M, 1, D), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((3, 1, D), dtype=torch.bfloat16, device="cuda")
+    out, lse = sage.prompt_attention(q, ones, ones, ints([0, 3]), kv_offsets=ints([0, M]), is_causal=False, return_lse=True)
+    torch.cuda.synchronize()
+    assert sage.device_error() == 0
+    # all logits are 0: weights of 2^-8, and their sums, are exact
+    assert ((lse.double() - 28 * math.log(2)).abs() <= 2.0 ** -18).all()
+    del ones
+    torch.cuda.empty_cache()
