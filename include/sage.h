@@ -689,7 +689,9 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * q, k, v, out: BF16, stride_b is not used, the other strides of q, k and v must
  * be positive (LAYOUT); D = 128 or 64; out must not overlap the inputs (ARG where
  * it is one of them). sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
- * Numbers: products of BF16 with fp32 sums; the weights p_j are rounded to BF16
+ * Numbers: products of BF16 with fp32 sums on the tensor cores, in parts of at
+ * most 65536 keys (of m products of one sign such a sum may lose m 2^-26 of
+ * itself), which are added in fp32; the weights p_j are rounded to BF16
  * (by 2^-9 of themselves) for the product with v, their sum is taken in fp32
  * before that. Outputs are finite where the sums of p_j v_j stay within fp32. An
  * infinity or NaN among the values of a key that a row sees is part of its sum

@@ -30,6 +30,12 @@
 // 2^8 above the true one, so that no weight is above 1 and O overflows no sooner than
 // the sum of a softmax by the true maximum (no bit is lost in floating point).
 //
+// Long rows. The tensor core cuts a product off at 2^-25 of the sum that it is added to or
+// a little below, towards 0: one sum over 2^20 keys came out 0.5% too small, one over 2^24
+// 10%. So O and l begin anew every 65536 keys (2^-10 at most is lost, 2^-12 measured); what
+// they held goes to parts in the workspace, by fp32 additions, and comes back at the end
+// of the unit.
+//
 // What a row does not see must not touch it, whatever stands there: its P is 0,
 // but 0 times an infinity or a NaN of V is a NaN. And what it does see has a weight
 // above 0, by the formula, though P may be 0 where the exponential leaves fp32. The
@@ -73,6 +79,8 @@ constexpr uint32_t kRedoWords = 8;
 // What warp 3 has cleared in a unit: values that some of its rows see, and that all do.
 constexpr uint32_t kBadSome = 1, kBadAll = 2;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kFold = 512;      // key tiles that O holds at most, a power of two
+constexpr int kMostCtas = 160;  // for which the workspace has parts
 constexpr float kGrowth = 8.0f; // the maximum follows when it has grown by 2^8, and is set that far above
 
 // One or two query tiles of a key/value head, the same for each of them.
@@ -286,6 +294,7 @@ struct Params {
   int pair;             // tiles of a block
   const int32_t *offsets, *kv_offsets;
   int32_t B, M;
+  float* parts;         // [CTA][2][128][kPart], for units of more than kFold key tiles
   Out out;
   const uint16_t* v;
   int64_t v_ss, v_sh;
@@ -391,7 +400,7 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
     const float m_new = fmaxf(m, up);
     const float neg_new = m_new == -INFINITY ? 0.0f : fmaf(-m_new, c, -kGrowth);
     if (!first) {
-      // a row that had seen nothing has O = 0 and l = 0
+      // a row that had seen nothing has O = 0 and l = 0 (as they are in a new part)
       const float alpha = m == -INFINITY ? 0.0f : tc::exp2_approx(neg_new - neg);
       l *= alpha;
       const float2 a2 = make_float2(alpha, alpha);
@@ -437,7 +446,47 @@ __device__ __forceinline__ bool softmax_tile(const tc::Waits& w, int t, uint32_t
   return true;
 }
 
-template <int D, bool kCausal>
+// A row's parts in the workspace: sums of values [D], of weights, and what they are
+// taken to (neg of that time; inf: the row had seen nothing, the factor to any later one is 0).
+template <int D>
+constexpr int kPart = D + 4;
+// O goes to the parts (`none`: the unit's first time), and l.
+template <int D>
+__device__ __forceinline__ void fold(float* part, uint32_t tO, bool none, float m, float neg, float l) {
+  const float scale = none ? 0.0f : tc::exp2_approx(neg - part[D + 1]);
+  part[D] = none ? l : fmaf(part[D], scale, l);
+  part[D + 1] = m == -INFINITY ? INFINITY : neg;
+#pragma unroll 1
+  for (int x = 0; x < D / 16; ++x) {
+    uint32_t o[16];
+    tc::tmem_ld16(tO + 16u * x, o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float* at = part + 16 * x + k;
+      *at = none ? __uint_as_float(o[k]) : fmaf(*at, scale, __uint_as_float(o[k]));
+    }
+  }
+}
+// And back, on top of what O holds by now; returns l.
+template <int D>
+__device__ __forceinline__ float unfold(const float* part, uint32_t tO, float neg, float l) {
+  const float scale = tc::exp2_approx(neg - part[D + 1]);
+#pragma unroll 1
+  for (int x = 0; x < D / 16; ++x) {
+    uint32_t o[16];
+    tc::tmem_ld16(tO + 16u * x, o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(fmaf(part[16 * x + k], scale, __uint_as_float(o[k])));
+    tc::tmem_st16(tO + 16u * x, o);
+  }
+  tc::tmem_wait_st();
+  return fmaf(part[D], scale, l);
+}
+
+// kLong: units may have more than kFold key tiles.
+template <int D, bool kCausal, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const Params prm) {
@@ -684,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < kKeys / 16; ++ks)
                 if (ks < steps)
                   tc::mma_f16_ts(d_o, d_p + 8u * ks, tc::desc_at(dv, 2048u * ks), tc::IdescBf16<D, true>::value,
-                                 (j > 0 || ks > 0) ? 1u : 0u);
+                                 ((kLong ? j % kFold : j) > 0 || ks > 0) ? 1u : 0u);
               if (!kApart<D> && more) product_s(pk + 2u, j + 2 == own);
               tc::mma_commit(empty(pv));
               if (kApart<D>) tc::mma_commit(w.bar(L::kPFree + t));
@@ -793,6 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lanes + col_s(t), tP = tmem + lanes + col_p<D>(t), tO = tmem + lanes + col_o<D>(t);
     uint32_t s_cnt = 0, done = 0;
     float2* stat = reinterpret_cast<float2*>(smem + L::kOffStat) + 128 * t + row;
+    const auto part = [&]() { return prm.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + t) * kRows + row) * kPart<D>; };
     bool ok = true;
     int pass = 0;
   units_of_rows:
@@ -804,8 +854,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t j = 0; j < own; ++j) {
         if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
         tc::tc_fence_after();
-        if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == 0, s_cnt, m, neg, l))) break;
+        if (kLong && j > 0 && j % kFold == 0) {
+          // O begins anew, once the products with V so far are done (at D = 128 S comes after them)
+          if (kApart<D> && !(ok = wait_bar_warp(w, w.bar(L::kPFree + t), (s_cnt - 1) & 1u))) break;
+          tc::tc_fence_after();
+          fold<D>(part(), tO, j == kFold, m, neg, l);
+          l = 0.0f;
+        }
+        if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, (kLong ? j % kFold : j) == 0, s_cnt, m, neg, l)))
+          break;
         ++s_cnt;
+      }
+      if (kLong && ok && own > kFold) {
+        if (!(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
+        tc::tc_fence_after();
+        l = unfold<D>(part(), tO, neg, l);
+        tc::tc_fence_before();
       }
       if (ok && n > 0) {
         // the unit before has been stored (waited for in every unit: no phase is skipped)
@@ -967,6 +1031,17 @@ bool make_map(CUtensorMap* map, const Bf16In& x, int64_t rows, int64_t heads, in
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+size_t list_bytes(int64_t N, int64_t B, int64_t group) {
+  return (kHeaderBytes + static_cast<size_t>(most_blocks(N, B, group, 2)) * sizeof(Block) + 255) / 256 * 256;
+}
+// Whether a sequence may have more key tiles than O holds.
+bool has_parts(int64_t M) { return M > int64_t(kFold) * kKeys; }
+// CTAs of a call at most.
+int64_t most_ctas(int64_t N, int64_t H, int64_t Hkv, int64_t B) {
+  const int64_t units = most_blocks(N, B, H / Hkv, 1) * Hkv;
+  return units < kMostCtas ? units : kMostCtas;
+}
+
 template <int D>
 cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   const int64_t rows = a.M > 0 ? a.M : 1;  // a tensor without rows is not read
@@ -975,7 +1050,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   Header* header = static_cast<Header*>(a.workspace);
   Block* list = reinterpret_cast<Block*>(static_cast<char*>(a.workspace) + kHeaderBytes);
-  const int64_t group = a.H / a.Hkv, sms = sm_count_current();
+  const int64_t group = a.H / a.Hkv, sms = sm_count_current() < kMostCtas ? sm_count_current() : kMostCtas;
   // (100 tokens, 28 heads: 7.8 us with a tile for each SM, 8.5 with two for 14 of them)
   const int pair = most_blocks(a.N, a.B, group, 1) * a.Hkv <= sms ? 1 : 2;
   const int64_t units = most_blocks(a.N, a.B, group, pair) * a.Hkv;
@@ -996,6 +1071,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.kv_offsets = a.kv_offsets;
   p.B = a.B;
   p.M = static_cast<int32_t>(a.M);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + list_bytes(a.N, a.B, group));
   p.out = a.out;
   p.v = a.v.p;
   p.v_ss = a.v.ss;
@@ -1007,7 +1083,11 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.scale = a.sm_log2;
   p.dev_err = a.dev_err;
   p.wait_ns = tc::wait_limit_ns(div_up(a.M, kKeys));
-  const auto kernel = a.causal ? prompt_attention_kernel<D, true> : prompt_attention_kernel<D, false>;
+  // Parts cost calls that need none 0.5 to 5% (16 prompts of 1500 tokens 265 -> 270 us, at D = 64 48.6 -> 51), by the
+  // code that a unit's end grows by: a kernel of its own has them.
+  const bool parts = has_parts(a.M);
+  const auto kernel = parts ? (a.causal ? prompt_attention_kernel<D, true, true> : prompt_attention_kernel<D, false, true>)
+                            : (a.causal ? prompt_attention_kernel<D, true, false> : prompt_attention_kernel<D, false, false>);
   const int bytes = static_cast<int>(Smem<D>::kBytes);
   if ((e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), bytes)) != cudaSuccess) return e;
   const int64_t grid = units < 1 ? 1 : units < sms ? units : sms;
@@ -1017,8 +1097,9 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t prompt_attention_workspace_bytes(int64_t N, int64_t, int64_t H, int64_t Hkv, int64_t, int64_t B) {
-  return (kHeaderBytes + static_cast<size_t>(most_blocks(N, B, H / Hkv, 2)) * sizeof(Block) + 255) / 256 * 256;
+size_t prompt_attention_workspace_bytes(int64_t N, int64_t M, int64_t H, int64_t Hkv, int64_t D, int64_t B) {
+  const size_t parts = has_parts(M) ? static_cast<size_t>(most_ctas(N, H, Hkv, B) * 2 * kRows * (D + 4)) * sizeof(float) : 0;
+  return list_bytes(N, B, H / Hkv) + parts;
 }
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int64_t D, cudaStream_t stream) {

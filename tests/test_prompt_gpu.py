@@ -654,6 +654,94 @@ def test_a_unit_of_some_seconds():
     torch.cuda.synchronize()
     assert sage.device_error() == 0
     # all logits are 0: weights of 2^-8, and their sums, are exact
-    assert ((lse.double() - 28 * math.log(2)).abs() <= 2.0 ** -18).all()
+    assert (out == 1).all() and ((lse.double() - 28 * math.log(2)).abs() <= 2.0 ** -18).all()
     del ones
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------- long rows --
+# The tensor core cuts a product off at 2^-25 of the sum or below, so that a sum of m products of one sign loses up to
+# m 2^-26 of itself, 2^-10 for the 65536 keys after which it begins anew; the rest of the bound as above.
+
+
+def close_long(out, lse, ref):
+    o, l, a = ref
+    err = (out.double() - o).abs()
+    bound = (o.abs() + a / 64) * 2.0 ** -8 + a * (2.0 ** -8 + 2.0 ** -9)
+    assert not torch.isnan(out).any() and (err <= bound).all(), (err / bound).max().item()
+    assert ((lse.double() - l).abs() <= 2.0 ** -11).all()
+
+
+def formula_of_row(q, k, v, sm):
+    """formula() of one sequence's rows [n, H, D] that see all keys of one key/value head, key by key in parts."""
+    n, H, D = q.shape
+    x = q.double().permute(1, 0, 2).reshape(H * n, D)
+    z = torch.cat([x @ kk.double().T * sm for kk in k[:, 0].split(1 << 20)], 1)
+    lse = torch.logsumexp(z, 1)
+    o, a = 0.0, 0.0
+    for zz, vv in zip(z.split(1 << 20, 1), v[:, 0].split(1 << 20)):
+        p = torch.exp(zz - lse[:, None])
+        o, a = o + p @ vv.double(), a + p @ vv.double().abs()
+    o, a = (t.reshape(H, n, D).permute(1, 0, 2) for t in (o, a))
+    return o, lse.reshape(H, n), a
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("M", [(1 << 22) + 77, 65536, 65537, 3 * 65536])
+def test_sums_of_long_rows(M, D):
+    """Values of one sign, of which a sum in one piece loses 2.6% over 2^22 keys; beside a short sequence."""
+    g = gen(190)
+    rows, keys, H = [3, 200], [M, 300], 3
+    q, k = bf16(g, 203, H, D), bf16(g, M + 300, 1, D)
+    v = (1 + torch.rand((M + 300, 1, D), generator=g, device="cuda")).to(torch.bfloat16)
+    k[M - 5000:M] *= 1.5  # the maximum follows late, too
+    off, kv = ints(ends(rows)), ints(ends(keys))
+    for causal in (False, True):
+        out, lse = sage.prompt_attention(q, k, v, off, kv_offsets=kv, is_causal=causal, return_lse=True)
+        if causal:  # rows one by one, each with the keys that it sees
+            ref = [formula_of_row(q[t:t + 1], k[:M - 2 + t], v[:M - 2 + t], 1 / math.sqrt(D)) for t in range(3)]
+            ref = torch.cat([r[0] for r in ref]), torch.cat([r[1] for r in ref], 1), torch.cat([r[2] for r in ref])
+        else:
+            ref = formula_of_row(q[:3], k[:M], v[:M], 1 / math.sqrt(D))
+        close_long(out[:3], lse[:, :3], ref)
+        close(out[3:], lse[:, 3:], formula(q[3:], k[M:], v[M:], [200], [300], causal, 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [2, 200])
+def test_prompts_of_many_parts(heads, D):
+    """Whole tiles of rows over several parts, in calls with few units and with a list of them; all rows like the last."""
+    g = gen(191)
+    n, M = 300, 150000
+    q = bf16(g, 1, 2, D).expand(n, 2, D).contiguous()
+    k = bf16(g, M, 1, D)
+    v = (1 + torch.rand((M, 1, D), generator=g, device="cuda")).to(torch.bfloat16)
+    v[M - n:] = 0.0
+    k[M - n:, :] = -8.0 * q[0, :1].sign()  # what only some rows see has next to no weight with head 0
+    sm = 1 / math.sqrt(D)
+    x = q.repeat_interleave(heads // 2, 1)
+    out, lse = sage.prompt_attention(x, k, v, ints([0, n]), kv_offsets=ints([0, M]), return_lse=True)
+    ref = formula_of_row(q[:1], k[:M - n + 1], v[:M - n + 1], sm)
+    out, lse = out[:, :heads // 2], lse[:heads // 2]
+    close_long(out[:, :1], lse[:1], tuple(r[:, :1].expand(n, 1, D) if r.dim() == 3 else r[:1].expand(1, n) for r in ref))
+    assert torch.equal(out, out[:, :1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_rows_with_values_that_are_not_finite(D):
+    g = gen(192)
+    n, M = 200, 140000
+    q, k = bf16(g, n, 2, D), bf16(g, M, 1, D)
+    v = (1 + torch.rand((M, 1, D), generator=g, device="cuda")).to(torch.bfloat16)
+    off, kv = ints([0, n]), ints([0, M])
+    want, lse = sage.prompt_attention(q, k, v, off, kv_offsets=kv, return_lse=True)
+    w = v.clone()
+    w[[5, 70000, M - 100], 0, [1, 2, 3]] = torch.tensor([math.inf, -math.inf, math.nan], device="cuda").to(torch.bfloat16)
+    w[M - 1, 0, 4] = math.nan
+    got, again = sage.prompt_attention(q, k, w, off, kv_offsets=kv, return_lse=True)
+    assert torch.equal(again, lse)
+    assert (got[:, :, 1] == math.inf).all() and (got[:, :, 2] == -math.inf).all()
+    assert torch.isnan(got[100:, :, 3]).all() and torch.isnan(got[199:, :, 4]).all()
+    other = torch.ones(D, dtype=torch.bool, device="cuda")
+    other[1:4] = False
+    assert torch.equal(got[:100, :, 3], want[:100, :, 3]) and torch.equal(got[:199][:, :, other], want[:199][:, :, other])
