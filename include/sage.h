@@ -642,15 +642,17 @@ SAGE_API int sage_cache_evict_workspace_size(int64_t B, int64_t H, int64_t D, in
  * square: the gradient; and the way back). Channels from rotary_dim on are copied.
  * q, k (and their outputs): BF16 (B, T, H, D) and (B, T, Hkv, D), D = 64 or 128,
  * rotary_dim a positive multiple of 16 up to D; Hkv = 0: no k. An output may be
- * its input itself; otherwise they must not overlap. positions: int32, element
+ * its own input, with its strides (LAYOUT); otherwise they must not overlap (ARG
+ * where q_out is k or k_out, or k_out is q), nor may the rows of an output (LAYOUT,
+ * expanded ones above all). positions: int32, element
  * (b, t) at positions_dev + b * positions_stride_b + t * positions_stride_t
  * (strides of 0 and negative positions are taken).
  * turns_dev: rotary_dim / 2 frequencies as sage_rotary_turns makes them, in
  * device memory: the part of a full turn that a position adds, in 2^-64 turns, so
  * that the angle of any 32-bit position is reduced without error. Cosine and sine
  * err by up to 2^-20 before the rounding to BF16.
- * Errors: NULLPTR, SHAPE, HEAD_DIM, ALIGN, ARG (rotary_dim, magnitude not finite),
- * TOO_LARGE, ARCH, CUDA. */
+ * Errors: NULLPTR, SHAPE, HEAD_DIM, LAYOUT, ALIGN, ARG (also rotary_dim, magnitude not
+ * finite), TOO_LARGE, ARCH, CUDA. */
 typedef struct sage_rotary_args {
   sage_bf16_tensor q, k;           /* read */
   sage_bf16_tensor q_out, k_out;   /* written */
@@ -688,7 +690,7 @@ SAGE_API int sage_rotary_turns(const double* inv_freq, int64_t n, uint64_t* turn
  * device error word is set.
  * q, k, v, out: BF16, stride_b is not used, the other strides of q, k and v must
  * be positive (LAYOUT); D = 128 or 64; out must not overlap the inputs (ARG where
- * it is one of them). sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
+ * it is one of them), nor its rows each other (LAYOUT). sm_scale: NaN selects 1/sqrt(D), otherwise finite and > 0.
  * Numbers: products of BF16 with fp32 sums on the tensor cores, in parts of at
  * most 65536 keys (of m products of one sign such a sum may lose m 2^-26 of
  * itself), which are added in fp32; the weights p_j are rounded to BF16

@@ -60,6 +60,32 @@ inline bool rows_apart(int64_t B, int64_t stride_b, int64_t H, int64_t stride_h,
   return sh >= n && sb - n >= 0 && (sb - n) / sh >= H - 1;
 }
 
+// A tensor that is written: none of its rows of D channels may overlap another
+// (the dimensions nested in one another, in any order; an expanded one has stride 0).
+inline bool tensor_apart(const sage_bf16_tensor& t, int64_t B, int64_t S, int64_t H, int64_t D) {
+  int64_t n[3] = {B, S, H}, s[3] = {t.stride_b, t.stride_s, t.stride_h};
+  int64_t span = D;  // of what is nested so far
+  if (B <= 0 || S <= 0 || H <= 0) return true;
+  for (int done = 0; done < 3; ++done) {
+    int64_t least = INT64_MAX, entries = 1;
+    int at = -1;
+    for (int i = 0; i < 3; ++i) {
+      const int64_t x = s[i] == INT64_MIN ? INT64_MAX : s[i] < 0 ? -s[i] : s[i];
+      if (n[i] > 1 && (at < 0 || x < least)) at = i, least = x, entries = n[i];
+    }
+    if (at < 0) return true;
+    if (least < span) return false;
+    span = entries - 1 > (INT64_MAX - span) / least ? INT64_MAX : span + (entries - 1) * least;
+    n[at] = 1;
+  }
+  return true;
+}
+
+// Whether two tensors at one address have the same rows there.
+inline bool same_rows(const sage_bf16_tensor& x, const sage_bf16_tensor& y, int64_t B, int64_t S, int64_t H) {
+  return (B <= 1 || x.stride_b == y.stride_b) && (S <= 1 || x.stride_s == y.stride_s) && (H <= 1 || x.stride_h == y.stride_h);
+}
+
 inline Bf16In to_in(const sage_bf16_tensor& t) {
   return Bf16In{static_cast<const uint16_t*>(t.ptr_dev), t.stride_b, t.stride_s, t.stride_h};
 }

@@ -66,6 +66,14 @@ int sage_rotary(const sage_rotary_args* args) {
   if ((rc = check_ints(args->positions_dev, true)) != SAGE_OK) return rc;
   if (args->turns_dev == nullptr) return SAGE_ERR_NULLPTR;
   if (!aligned(args->turns_dev, 16)) return SAGE_ERR_ALIGN;
+  if (!tensor_apart(args->q_out, B, T, H, D) || !tensor_apart(args->k_out, B, T, Hkv, D)) return SAGE_ERR_LAYOUT;
+  if (B > 0 && T > 0) {
+    // in place a thread writes what it has read, if that is where it belongs
+    const void *q = args->q.ptr_dev, *k = args->k.ptr_dev, *q_out = args->q_out.ptr_dev, *k_out = args->k_out.ptr_dev;
+    if (H > 0 && q_out == q && !same_rows(args->q_out, args->q, B, T, H)) return SAGE_ERR_LAYOUT;
+    if (Hkv > 0 && k_out == k && !same_rows(args->k_out, args->k, B, T, Hkv)) return SAGE_ERR_LAYOUT;
+    if (H > 0 && Hkv > 0 && (q_out == k_out || q_out == k || k_out == q)) return SAGE_ERR_ARG;
+  }
   int* dev_err = nullptr;
   if ((rc = device_error_word(&dev_err)) != SAGE_OK) return rc;
   if (B == 0 || T == 0 || H + Hkv == 0) return SAGE_OK;
@@ -111,6 +119,7 @@ int sage_prompt_attention(const sage_prompt_attention_args* args) {
   if (!scale_ok(args->sm_scale)) return SAGE_ERR_ARG;
   const void* out = args->out.ptr_dev;  // (a unit may be done twice: its queries have to be there still)
   if (N > 0 && H > 0 && (out == args->q.ptr_dev || (M > 0 && (out == args->k.ptr_dev || out == args->v.ptr_dev)))) return SAGE_ERR_ARG;
+  if (!tensor_apart(args->out, 1, N, H, D)) return SAGE_ERR_LAYOUT;
   const size_t need = N == 0 || H == 0 ? 0 : prompt_attention_workspace_bytes(N, M, H, args->Hkv, D, B);
   if (need > 0) {
     if (args->workspace_dev == nullptr) return SAGE_ERR_NULLPTR;

@@ -517,6 +517,27 @@ def test_expanded_heads_and_rows_are_refused():
         assert err.value.code == -6
 
 
+def test_expanded_outputs_are_refused():
+    g = gen(149)
+    q, k = bf16(g, 10, 4, 64), bf16(g, 10, 1, 64)
+    for out in (q[:1].expand(10, 4, 64), q[:, :1].expand(10, 4, 64)):
+        with pytest.raises(SageError) as err:
+            sage.prompt_attention(k.expand(10, 4, 64).contiguous(), k, k, ints([0, 10]), out=out)
+        assert err.value.code == -6
+    x = torch.stack([q, q])
+    table, pos = sage.rotary_table(64, device="cuda"), torch.arange(10, dtype=torch.int32, device="cuda")
+    wide = q[None].expand(2, 10, 4, 64)
+    assert torch.equal(sage.rotary(wide, None, pos, table), sage.rotary(x, None, pos, table))  # read, they are fine
+    before = q.clone()
+    for args, out in (((x, None), wide), ((wide, None), wide), ((x, x[:, :, :1]), (x, wide[:, :, :1]))):
+        with pytest.raises(SageError) as err:
+            sage.rotary(*args, pos, table, out=out)
+        assert err.value.code == -6
+    with pytest.raises(SageError) as err:
+        sage.rotary(x, x, pos, table, out=(x, x))
+    assert err.value.code == -13 and torch.equal(q, before) and torch.equal(x[1], before)
+
+
 def test_graphs_replayed_at_once():
     """Two captured graphs of calls with a list replay on two streams, each with its own workspace."""
     data = [inputs(146 + i, r, r, 16, 2, 128) for i, r in enumerate(([3000, 500], [100] * 20))]

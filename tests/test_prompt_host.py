@@ -159,6 +159,33 @@ def test_rotary_refuses(lib):
     assert _rotary(lib, turns=0x1008) == ALIGN and _rotary(lib, pos=0x2002) == ALIGN
 
 
+def test_rotary_refuses_outputs_that_meet(lib):
+    """Rows of an output over each other, other rows at an input's address, one output for both."""
+    a, b, c = (lambda **kw: tensor(0x70000, **kw)), (lambda **kw: tensor(0x80000, **kw)), (lambda **kw: tensor(0x90000, **kw))  # noqa: E731
+    d = lambda **kw: tensor(0xa0000, **kw)  # noqa: E731
+    meet = [dict(ss=0), dict(sh=0), dict(sb=0), dict(sh=64), dict(ss=256), dict(sb=512), dict(sb=1024), dict(ss=-256), dict(sh=128, ss=384),
+            dict(sh=4096, ss=512, sb=1024), dict(sb=-(1 << 63))]
+    for st in meet[:-1]:
+        assert _rotary(lib, q=a(), k=b(), qo=c(**st), ko=d()) == LAYOUT, st
+    for st in (dict(ss=0), dict(sh=0), dict(sb=0), dict(sh=64), dict(ss=128)):
+        assert _rotary(lib, q=a(), k=b(), qo=c(), ko=d(**st)) == LAYOUT, st
+        assert _rotary(lib, q=a(**st), k=b(), qo=a(**st), ko=d()) == LAYOUT, st
+    for st in (dict(sb=1 << 21), dict(ss=1024), dict(sh=1 << 12)):
+        assert _rotary(lib, q=a(), k=b(), qo=a(**st), ko=d()) == LAYOUT, st
+        assert _rotary(lib, q=a(), k=b(), qo=c(), ko=b(**st)) == LAYOUT, st
+    assert _rotary(lib, q=a(), k=b(), qo=c(), ko=c()) == ARG
+    assert _rotary(lib, q=a(), k=b(), qo=b(), ko=d()) == ARG and _rotary(lib, q=a(), k=b(), qo=c(), ko=a()) == ARG
+    # what does not meet is taken: the next check that fails is that of the device, or none
+    fine = [dict(), dict(ss=1 << 12, sh=128), dict(sh=1 << 12, ss=128, sb=1 << 16), dict(ss=-512), dict(sh=-128, sb=-(1 << 20)), meet[-1]]
+    if not torch.cuda.is_available():
+        for st in fine:
+            assert _rotary(lib, q=a(), k=b(), qo=c(**st), ko=d()) not in (LAYOUT, ARG), st
+        assert _rotary(lib, q=a(), k=b(), qo=a(), ko=b()) not in (LAYOUT, ARG)
+        assert _rotary(lib, q=a(), k=a(), qo=c(), ko=d()) not in (LAYOUT, ARG)
+        assert _rotary(lib, q=a(), k=b(), qo=c(sb=0), ko=d(sb=0), B=1) not in (LAYOUT, ARG)
+        assert _rotary(lib, q=a(), k=b(), qo=a(sb=8, ss=0), ko=d(), B=1, T=1) not in (LAYOUT, ARG)
+
+
 # --------------------------------------------------------- prompt attention --
 
 
@@ -199,6 +226,16 @@ def test_prompt_attention_refuses(lib):
         assert _prompt(lib, sm=sm) == ARG
     assert _prompt(lib, ws=None) == NULLPTR and _prompt(lib, ws=0x90010) == ALIGN
     assert _prompt(lib, wsn=need - 1) == WORKSPACE
+
+
+def test_prompt_attention_refuses_outputs_over_each_other(lib):
+    for st in (dict(ss=0), dict(sh=0), dict(ss=384), dict(sh=64), dict(ss=64), dict(ss=-384), dict(sh=512, ss=1024)):
+        assert _prompt(lib, out=tensor(0x80000, **st)) == LAYOUT, st
+    if not torch.cuda.is_available():
+        for st in (dict(), dict(sb=0), dict(ss=-512), dict(ss=128, sh=1 << 14), dict(ss=520), dict(sh=136, ss=544)):
+            assert _prompt(lib, out=tensor(0x80000, **st)) not in (LAYOUT, ARG), st
+        assert _prompt(lib, out=tensor(0x80000, ss=0), N=1) not in (LAYOUT, ARG)
+        assert _prompt(lib, out=tensor(0x80000, sh=0), H=1, Hkv=1) not in (LAYOUT, ARG)
 
 
 # ------------------------------------------------------ weights and eviction --
