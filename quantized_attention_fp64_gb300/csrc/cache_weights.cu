@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, N == 4 ? 1 : 2) cache_weights_kernel
           sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
         }
         const float add = (t4 & 2) ? ((t4 & 1) ? sum[3] : sum[2]) : ((t4 & 1) ? sum[1] : sum[0]);
-        if (j0 + mine < len) scores[j0 + mine] = score + add;
+        if (j0 + mine < len && !(add == 0.0f)) scores[j0 + mine] = score + add;
       }
     }
     left -= run;

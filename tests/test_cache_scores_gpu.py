@@ -190,6 +190,29 @@ def test_weights_keys_whose_scale_is_a_nan(T, lse):
     assert torch.equal(got[1, 0, 258:], start[1, 0, 258:]) and torch.equal(got[0, :, 200:], start[0, :, 200:])
 
 
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_weights_leave_scores_of_unseen_tokens_as_they_were(T):
+    """To the bit: -0 and NaN with a payload, of tokens that no row sees, behind the sequence, and where a row's
+    log-sum-exp is minus infinity."""
+    rng = np.random.default_rng(17)
+    lengths, H, Hkv, D, page = [100, 64, 0], 4, 2, 64, 64
+    table, P = make_table(rng, lengths, page)
+    gpu = upload(random_cache(rng, P, Hkv, D, page))
+    q = bf16(rng, 3, T, H, D)
+    start = torch.full((3, Hkv, 130), -0.0, device="cuda")
+    start.view(torch.int32)[:, :, ::5] = 0x7FC12345
+    lse = torch.full((3, H, T), 3.0, device="cuda")
+    lse[1] = -math.inf
+    lse[0, :2] = -math.inf
+    q_lengths = ints([T, T, T])
+    got = sage.cache_add_weights(start.clone(), q, gpu, ints(table), ints(lengths), lse, q_lengths=q_lengths, is_causal=True)
+    a, b = start.view(torch.int32), got.view(torch.int32)
+    assert torch.equal(a[1:], b[1:]) and torch.equal(a[0, 0], b[0, 0]) and torch.equal(a[0, 1, 100:], b[0, 1, 100:])
+    seen = torch.ones(100, dtype=torch.bool, device="cuda")
+    seen[::5] = False
+    assert (got[0, 1, :100][seen] > 0).all() and torch.isnan(got[0, 1, :100][~seen]).all()
+
+
 @pytest.mark.parametrize("T", [1, 50])
 def test_weights_bad_pages_and_lengths_are_flagged(T):
     rng = np.random.default_rng(13)
