@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < kKeys / 16; ++ks)
                 if (ks < steps)
                   tc::mma_f16_ts(d_o, d_p + 8u * ks, tc::desc_at(dv, 2048u * ks), tc::IdescBf16<D, true>::value,
-                                 ((kLong ? j % kFold : j) > 0 || ks > 0) ? 1u : 0u);
+                                 ((kLong ? (j & (kFold - 1)) != 0 : j > 0) || ks > 0) ? 1u : 0u);
               if (!kApart<D> && more) product_s(pk + 2u, j + 2 == own);
               tc::mma_commit(empty(pv));
               if (kApart<D>) tc::mma_commit(w.bar(L::kPFree + t));
@@ -851,19 +851,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t own = key_tiles<kCausal>(e, t), n = max(own, key_tiles<kCausal>(e, 1 - t));
       const int32_t mine = sees<kCausal>(e, begin_of(e, t) + row);
       float m = -INFINITY, neg = 0.0f, l = 0.0f;
-      for (int32_t j = 0; j < own; ++j) {
-        if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
-        tc::tc_fence_after();
-        if (kLong && j > 0 && j % kFold == 0) {
-          // O begins anew, once the products with V so far are done (at D = 128 S comes after them)
-          if (kApart<D> && !(ok = wait_bar_warp(w, w.bar(L::kPFree + t), (s_cnt - 1) & 1u))) break;
+      for (int32_t j = 0, end = kLong ? min(own, kFold) : own;;) {
+        for (const int32_t first = j; j < end; ++j) {
+          if (!(ok = wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u))) break;
           tc::tc_fence_after();
-          fold<D>(part(), tO, j == kFold, m, neg, l);
-          l = 0.0f;
+          if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, j == first, s_cnt, m, neg, l))) break;
+          ++s_cnt;
         }
-        if (!(ok = softmax_tile<D>(w, t, tS, tP, tO, prm.scale, mine - j * kKeys, (kLong ? j % kFold : j) == 0, s_cnt, m, neg, l)))
+        if (!kLong || !ok || end == own) break;
+        // O begins anew, once the products with V so far are done (at D = 128 the next S comes after them)
+        if (!(ok = kApart<D> ? wait_bar_warp(w, w.bar(L::kPFree + t), (s_cnt - 1) & 1u)
+                             : wait_bar_warp(w, w.bar(L::kSFull + t), s_cnt & 1u)))
           break;
-        ++s_cnt;
+        tc::tc_fence_after();
+        fold<D>(part(), tO, j == kFold, m, neg, l);
+        l = 0.0f;
+        end = min(own, end + kFold);
       }
       if (kLong && ok && own > kFold) {
         if (!(ok = wait_bar_warp(w, w.bar(L::kOFull + t), done & 1u))) break;
@@ -1083,8 +1086,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.scale = a.sm_log2;
   p.dev_err = a.dev_err;
   p.wait_ns = tc::wait_limit_ns(div_up(a.M, kKeys));
-  // Parts cost calls that need none 0.5 to 5% (16 prompts of 1500 tokens 265 -> 270 us, at D = 64 48.6 -> 51), by the
-  // code that a unit's end grows by: a kernel of its own has them.
+  // The code for parts costs calls that need none 2 to 5% (16 prompts of 1500 tokens 265 -> 270 us, at D = 64 48.6 -> 51):
+  // calls with few rows have a kernel without. (48 such prompts, 72000 rows: 795 us with, 781 without.)
   const bool parts = has_parts(a.M);
   const auto kernel = parts ? (a.causal ? prompt_attention_kernel<D, true, true> : prompt_attention_kernel<D, false, true>)
                             : (a.causal ? prompt_attention_kernel<D, true, false> : prompt_attention_kernel<D, false, false>);
