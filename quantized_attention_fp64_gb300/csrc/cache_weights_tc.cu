@@ -18,8 +18,9 @@
 //               tile 0 or 1 (TMEM lane = key); or, where there is one key tile, of
 //               every fourth
 // TMEM holds an S^T of 128 x 128 for each group: all 512 columns. The product of a
-// tile (512 cycles at D = 128) and its 16384 exponentials (512 cycles) bound the
-// kernel alike. A causal chunk of 2000 tokens over 16001, 32 heads on 8, D = 128: 203 us, 1210
+// tile (512 cycles at D = 128) and its 16384 exponentials (512 cycles) weigh alike, and
+// either unit is busy 55 to 60% of the time; the operands of a product are 64 KB of shared
+// memory, 512 cycles of reading too, which was not measured. A causal chunk of 2000 tokens over 16001, 32 heads on 8, D = 128: 203 us, 1210
 // TFLOP/s (276 with two groups, whose latencies lay open; 325 before the
 // log-sum-exps came in a ring of their own).
 //

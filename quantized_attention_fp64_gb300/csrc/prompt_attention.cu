@@ -3,7 +3,10 @@
 //   out_t = sum_j p_tj v_j / sum_j p_tj,  p_tj = 2^(c (q_t . k_j - m_t)),  c = sm_scale log2 e
 // over the keys that row t sees: all m of its sequence, or with the causal mask
 // the first m - n + t + 1 (n queries). Both products are BF16 with fp32 sums; P
-// is rounded to BF16, l_t = sum_j p_tj is taken in fp32 before that.
+// is rounded to BF16, l_t = sum_j p_tj is taken in fp32 before that. (The tensor core
+// wants P in the type of V. Outputs are off by 0.19 to 0.23% of their norm so, and by 0.16%
+// with P in fp32, which is the outputs' own rounding; a second product for the rest of
+// P would bring that for half as much tensor work again.)
 //
 // A unit of work is two query tiles of 128 rows that share the key tiles (128 keys)
 // which pass through shared memory: the same rows of two query heads of a key/value
@@ -48,14 +51,13 @@
 // alone (2% of the prompts above); a look at all values beforehand took 23 us of
 // them, one at the value tiles as they pass by 32.
 //
-// What bounds it. D = 128: the tensor pipe; 16384 causal tokens, 28 heads on 4, run at 1590
-// to 1690 TFLOP/s (1200 to 1140 us, 81 to 86% of the measured peak of cuBLAS in a
-// burst, which no kernel keeps up under the power limit: 1752 TFLOP/s for seconds).
-// Prompts up to 2000 tokens, 1040 TFLOP/s: the masked halves of the diagonal tiles, ends of
+// What bounds it. D = 128: the tensor pipe; 16384 causal tokens, 28 heads on 4, run at 1540
+// to 1690 TFLOP/s (1250 to 1140 us, by what ran before; 79 to 86% of the measured peak of
+// cuBLAS in a burst, which no kernel keeps up under the power limit: 1752 TFLOP/s for seconds).
+// 16 prompts up to 2000 tokens, 1050 TFLOP/s (190 us): the masked halves of the diagonal tiles, ends of
 // sequences, and a microsecond to begin and end a unit of 6 key tiles. D = 64: the
 // softmax, whose exponentials are as many with half the products; 16384 tokens both
-// ways 1000 TFLOP/s, 1.28 us for a step of two tiles (with P double-buffered in TMEM
-// 1.33). Code that runs once in a unit is kept short: it is fetched anew each
+// ways 1060 TFLOP/s, 1.2 us for a step of two tiles. Code that runs once in a unit is kept short: it is fetched anew each
 // time (the output warps' loop over 32 channels, three times as long, cost the
 // prompts above 20 us).
 //
@@ -1057,9 +1059,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   // (100 tokens, 28 heads: 7.8 us with a tile for each SM, 8.5 with two for 14 of them)
   const int pair = most_blocks(a.N, a.B, group, 1) * a.Hkv <= sms ? 1 : 2;
   const int64_t units = most_blocks(a.N, a.B, group, pair) * a.Hkv;
-  // A unit for each CTA at most: no first kernel, which costs more than its list and
-  // its look at the values save then. 100 tokens, 28 heads (28 units): 8.8 us instead
-  // of 11.3; 1230 tokens (140 units): 24.4 us instead of 28.1.
+  // A unit for each CTA at most: no first kernel, which costs more than its list saves
+  // then. 100 tokens, 28 heads: 7.8 us, 11.1 with it; 1230 tokens (140 units): 22.6 us, 24.0 with it.
   const bool direct = units <= sms;
   cudaError_t e;
   if (!direct && (e = launch_dependent(a.causal ? plan_kernel<true> : plan_kernel<false>, dim3(1), kPlanThreads, 0, stream,

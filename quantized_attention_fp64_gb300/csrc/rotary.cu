@@ -6,7 +6,7 @@
 // without any rounding, however far the position and however fast the pair; its
 // upper 32 bits, as a signed number, are the angle within half a turn. So the
 // fast sine and cosine, whose error is absolute (2^-21 within that range),
-// are enough before a rounding to BF16 (2^-9).
+// are enough before a rounding to BF16 (2^-8).
 //
 // The kernel moves bytes. A thread has 16 channels of a token, 8 pairs, in heads
 // hl, hl + lanes, ...: one set of sines and cosines for all of them, and four
