@@ -183,6 +183,34 @@ __device__ __forceinline__ uint32_t collect(uint32_t pair, uint32_t acc) {
 }
 // Those are the sign bits of this.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t not_finite(const uint4& u) {
+  return not_finite(u.x) | not_finite(u.y) | not_finite(u.z) | not_finite(u.w);
+}
+// Eight channels with infinities or NaN: a bit for each that holds +inf goes to `up`, for
+// -inf to `down`, for a NaN to both, and those become 0.
+__device__ __forceinline__ void take_odd(uint4& u, uint32_t& up, uint32_t& down) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t odd = not_finite(w[k]), low = odd >> 15 & 1u, high = odd >> 31;
+    const uint32_t nan_low = (w[k] & 0x7Fu) != 0u, nan_high = (w[k] & 0x7F0000u) != 0u;
+    const uint32_t neg_low = w[k] >> 15 & 1u, neg_high = w[k] >> 31;
+    up |= ((low & (nan_low | (neg_low ^ 1u))) | (high & (nan_high | (neg_high ^ 1u))) << 1) << (2 * k);
+    down |= ((low & (nan_low | neg_low)) | (high & (nan_high | neg_high)) << 1) << (2 * k);
+    w[k] &= ~(odd | (odd - (odd >> 15)));
+  }
+}
+// And into the eight channels at p.
+__device__ __forceinline__ void add_odd(uint16_t* p, uint32_t up, uint32_t down) {
+  if ((up | down) == 0u) return;
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    float x = __uint_as_float(static_cast<uint32_t>(p[k]) << 16);
+    if (up >> k & 1u) x += INFINITY;
+    if (down >> k & 1u) x -= INFINITY;
+    p[k] = static_cast<uint16_t>(tc::bf16x2(x, 0.0f));
+  }
+}
 
 // Lists the blocks of all sequences by their key tiles, the most first (in 512
 // classes). Most of its time is a launch, barriers and code that is fetched: with
@@ -800,19 +828,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (__any_sync(0xffffffffu, not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]))) {
               bad |= j < whole ? kBadAll : kBadSome;
+              // (swizzled: the chunk q & 7 of a row has channels 8 ((q ^ row) & 7) on, which are two
+              // places for a lane, whose rows are 4 apart)
+              uint32_t up[2] = {0u, 0u}, down[2] = {0u, 0u};
 #pragma unroll 1
-              for (int q = lane; q < there * 8; q += 32) {
-                uint16_t* o = reinterpret_cast<uint16_t*>(chunk + q);
-                const int c0 = 64 * x + 8 * ((q & 7) ^ ((q >> 3) & 7));  // (swizzled)
-#pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t b = o[k];
-                  if ((b & 0x7F80u) != 0x7F80u) continue;
-                  o[k] = 0;
-                  if (j >= whole) continue;
-                  const uint32_t word = static_cast<uint32_t>(c0 + k) >> 5, bit = 1u << ((c0 + k) & 31);
-                  if (b != 0xFF80u) atomicOr(odd + word, bit);
-                  if (b != 0x7F80u) atomicOr(odd + D / 32 + word, bit);
+              for (int q = lane; q < there * 8; q += 64) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  if (q + 32 * y >= there * 8) continue;
+                  uint4 u = chunk[q + 32 * y];
+                  take_odd(u, up[y], down[y]);
+                  chunk[q + 32 * y] = u;
+                }
+              }
+              if (j < whole) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int c0 = 64 * x + 8 * ((lane ^ ((lane >> 3) + 4 * y)) & 7);
+                  if (up[y] != 0u) atomicOr(odd + c0 / 32, up[y] << (c0 & 31));
+                  if (down[y] != 0u) atomicOr(odd + D / 32 + c0 / 32, down[y] << (c0 & 31));
                 }
               }
             }
@@ -973,33 +1007,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (bad != 0 && there) {
-          const auto add = [&](int y, float x) {
-            dst[y] = static_cast<uint16_t>(tc::bf16x2(__uint_as_float(static_cast<uint32_t>(dst[y]) << 16) + x, 0.0f));
-          };
-          if (bad & kBadAll) {
-            const uint32_t* odd = odd_channels + fixed % kFixes * (2 * D / 32);
+        if (__builtin_expect(bad != 0 && there, 0)) {
+          const uint32_t* odd = odd_channels + fixed % kFixes * (2 * D / 32);
+          const uint16_t* v = prm.v + static_cast<int64_t>(e.kv0) * prm.v_ss + it.hk * prm.v_sh;
+          const int32_t from = (sees<kCausal>(e, 0) >> 7) * kKeys, mine = sees<kCausal>(e, r);
 #pragma unroll 1
-            for (int y = 0; y < D; ++y) {
-              const bool up = (odd[y >> 5] >> (y & 31) & 1u) != 0, down = (odd[D / 32 + (y >> 5)] >> (y & 31) & 1u) != 0;
-              if (up) add(y, INFINITY);
-              if (down) add(y, -INFINITY);
+          for (int c = 0; c < D; c += 8) {
+            uint32_t up = 0u, down = 0u;
+            if (bad & kBadAll) {
+              up = odd[c / 32] >> (c & 31) & 0xFFu;
+              down = odd[D / 32 + c / 32] >> (c & 31) & 0xFFu;
             }
-          }
-          if (kCausal && (bad & kBadSome)) {
-            const int32_t mine = sees<kCausal>(e, r);
+            if (kCausal && (bad & kBadSome)) {
 #pragma unroll 1
-            for (int32_t k = (sees<kCausal>(e, 0) >> 7) * kKeys; k < mine; ++k) {
-              const uint16_t* v = prm.v + (static_cast<int64_t>(e.kv0) + k) * prm.v_ss + it.hk * prm.v_sh;
-#pragma unroll 1
-              for (int x = 0; x < D / 8; ++x) {
-                const uint4 u = *reinterpret_cast<const uint4*>(v + 8 * x);
-                if ((not_finite(u.x) | not_finite(u.y) | not_finite(u.z) | not_finite(u.w)) == 0u) continue;
-#pragma unroll 1
-                for (int y = 8 * x; y < 8 * x + 8; ++y)
-                  if ((v[y] & 0x7F80u) == 0x7F80u) add(y, __uint_as_float(static_cast<uint32_t>(v[y]) << 16));
+              for (int32_t k = from; k < mine; ++k) {
+                uint4 u = *reinterpret_cast<const uint4*>(v + k * prm.v_ss + c);
+                if (not_finite(u) != 0u) take_odd(u, up, down);
               }
             }
+            add_odd(dst + c, up, down);
           }
         }
       }
@@ -1088,7 +1114,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   p.dev_err = a.dev_err;
   p.wait_ns = tc::wait_limit_ns(div_up(a.M, kKeys));
   // The code for parts costs calls that need none 2 to 5% (16 prompts of 1500 tokens 265 -> 270 us, at D = 64 48.6 -> 51):
-  // calls with few rows have a kernel without. (48 such prompts, 72000 rows: 795 us with, 781 without.)
+  // calls with few rows have a kernel without. (48 such prompts, 72000 rows: 811 us with, 782 without.)
   const bool parts = has_parts(a.M);
   const auto kernel = parts ? (a.causal ? prompt_attention_kernel<D, true, true> : prompt_attention_kernel<D, false, true>)
                             : (a.causal ? prompt_attention_kernel<D, true, false> : prompt_attention_kernel<D, false, false>);

@@ -270,6 +270,37 @@ def test_infinite_values_of_little_weight(units, causal, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("share", [0.002, 0.3, 1.0])
+def test_many_values_that_are_not_finite(share, causal, D):
+    """Any part of the values, in all channels, tiles and sequences: each output is what those that its row sees make of it."""
+    rows, past, H, Hkv = [300, 77, 513], [0, 200, 3], 4, 2
+    keys = [n + p for n, p in zip(rows, past)]
+    q, k, v = inputs(76, rows, keys, H, Hkv, D, spare=30)
+    n, m = sum(rows), sum(keys)
+    g = gen(77)
+    odd = torch.rand(v.shape, generator=g, device="cuda") < share
+    kind = torch.tensor([math.inf, -math.inf, math.nan], device="cuda").to(torch.bfloat16)
+    kind = kind[torch.randint(0, 3 if share < 1 else 2, v.shape, generator=g, device="cuda")]
+    ref = formula(q[:n], k[:m], torch.where(odd, 0.0, v)[:m], rows, keys, causal, 1 / math.sqrt(D))
+    v = torch.where(odd, kind, v)
+    out = sage.prompt_attention(q, k, v, ints(ends(rows)), kv_offsets=ints(ends(keys)), is_causal=causal)
+    x = v.double().repeat_interleave(H // Hkv, 1)
+    ups, downs = ((x == s) | x.isnan() for s in (math.inf, -math.inf))
+    for b in range(3):
+        o, r, a = (t[ends(rows)[b]:ends(rows)[b + 1]] for t in (out, ref[0], ref[2]))
+        up, down = (t[ends(keys)[b]:ends(keys)[b + 1]].to(torch.int32).cumsum(0) > 0 for t in (ups, downs))
+        at = torch.arange(rows[b], device="cuda") + past[b] if causal else torch.full((rows[b],), keys[b] - 1, device="cuda")
+        up, down = up[at], down[at]
+        assert torch.equal(torch.isnan(o), up & down)
+        assert torch.equal(o == math.inf, up & ~down) and torch.equal(o == -math.inf, down & ~up)
+        fine = ~(up | down)
+        bound = (r.abs() + a / 64) * 2.0 ** -8 + a * (2.0 ** -8 + 2.0 ** -10) + 1e-30
+        assert ((o.double() - r).abs() <= bound)[fine].all()
+    assert (out[n:] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_growing_and_falling_logits(D):
     # the running maximum has to follow, early and late, by little and by much
     n = 700
